@@ -733,6 +733,123 @@ cb_status cb_blend_layer(cb_model *m, int layer, float *h, int n_rows,
                          void *v_cache, void *ws, size_t ws_bytes,
                          cb_stream stream);
 
+/* ------------------------------------------------------------------------ */
+/* Generation: paged cache, attention over it, token sampling               */
+/* ------------------------------------------------------------------------ */
+
+/* Largest number of sequences one paged call accepts. */
+#define CB_MAX_SEQS 1024
+/* Largest vocabulary cb_sample_tokens accepts. */
+#define CB_MAX_SAMPLE_VOCAB 262144
+
+/* A paged K/V cache and the batch of sequences of one call.  Position p of
+ * sequence s lives in slot p % page_size of page
+ * block_table[s][p / page_size]; a slot is one cache row (n_kv_heads *
+ * head_dim elements).  Row r of the call's row tensors (q, k_new, v_new,
+ * out) belongs to the sequence s with row_offsets[s] <= r <
+ * row_offsets[s + 1]; the i-th of a sequence's n rows has position
+ * kv_lens[s] - n + i, so kv_lens counts the new rows.  A negative position
+ * (an idle slot of a padded batch: kv_lens[s] = 0) names no slot.  Rows
+ * outside every range (padding behind the last sequence) are left alone.
+ * All arrays are read on the device when the call runs, so a recorded call
+ * follows the lengths and tables of the moment it is replayed. */
+typedef struct {
+  void *k_pages, *v_pages;    /* device: slot t of page p at
+                                 p * page_stride + t * ld (elements)         */
+  int64_t page_stride, ld;
+  int n_pages;                /* pages of the pool                           */
+  int page_size;              /* slots per page: a power of two, 8 .. 1024   */
+  const int32_t *block_table; /* device [n_seq][ld_table], max_pages used    */
+  int64_t ld_table;
+  int max_pages;
+  const int32_t *row_offsets; /* device [n_seq + 1], ascending               */
+  const int32_t *kv_lens;     /* device [n_seq]                              */
+  int n_seq;                  /* 0 .. CB_MAX_SEQS                            */
+} cb_paged_kv;
+
+/* Appends the rows' keys and values to the cache and rotates keys and
+ * queries to their positions on the way ([CB] blend_layer step 2, with a
+ * page table in place of the fused cache's rows):
+ *   K[p] = R(p) k_new[r],  V[p] = v_new[r],  q_out[r] = R(p) q[r]
+ * with the rotation of cb_rope_reposition, in fp32 and rounded once.
+ * rope_table NULL: keys are copied as they are (already rotated rows, such
+ * as a blended prefill's fused cache), and q must be NULL.
+ * n_rows rows of n_layers layers are appended: layer l reads k_new + l *
+ * k_layer_stride (v alike) and writes k_pages + l * cache_layer_stride.
+ * q: device [n_rows][ld_q] or NULL (with n_layers 1); q_out may be q.  Rows
+ * without a position keep their q_out.  Sequences of one call must not share
+ * a page that the call writes.  k_new and v_new must not overlap the pools.
+ * Errors: CB_ERR_INVALID_ARG (NULL or misaligned pointers, strides below a
+ * row, head_dim not a multiple of 16), CB_ERR_UNSUPPORTED (page_size).  On
+ * the device, offsets that do not ascend inside [0, n_rows], a page outside
+ * the pool or the table, and a rotation at or past max_positions record
+ * CB_ERR_DEVICE_INDEX; those rows are skipped. */
+cb_status cb_paged_append(const cb_paged_kv *kv, const void *k_new, int64_t ld_k,
+                          int64_t k_layer_stride, const void *v_new, int64_t ld_v,
+                          int64_t v_layer_stride, int n_rows, int n_layers,
+                          int64_t cache_layer_stride, int n_kv_heads, int head_dim,
+                          const float *rope_table, int max_positions, const void *q,
+                          int64_t ld_q, int n_q_heads, void *q_out, int64_t ld_q_out,
+                          cb_dtype dtype, cb_stream stream);
+
+/* Causal attention of the new rows over the paged cache: for row r of
+ * sequence s at position p and q head h (kv head g = h / (n_q_heads /
+ * n_kv_heads)),
+ *   out[r][h] = sum_{j<=p} softmax_j(scale * q[r][h] . K[j][g]) V[j][g]
+ * over the sequence's pages: one row per sequence while tokens are
+ * generated, many for a chunk of a prompt, both in one call.  The rows' own
+ * keys are in the cache already (cb_paged_append).  A row with a negative
+ * position sees no key and gets zeros.  Slots past kv_lens are never used,
+ * whatever they hold; K and V up to kv_lens must be finite.
+ * q, out: device [n_rows][ld] (n_q_heads * head_dim columns); they must not
+ * overlap.  max_kv_len: an upper bound of every kv_lens[s], which sizes the
+ * split of long key ranges.  ws: device scratch of at least
+ * cb_paged_attention_workspace_size(...) bytes for the same sizes (16-byte
+ * aligned; contents need no initialisation; calls that share it must be
+ * ordered on one stream).
+ * Errors: CB_ERR_INVALID_ARG (NULL or misaligned pointers, strides, head
+ * counts not dividing or more than 128 q heads per kv head, head_dim not 64
+ * or 128), CB_ERR_UNSUPPORTED (page_size, or a row count whose tiles exceed a
+ * launch), CB_ERR_WORKSPACE.  On the device, offsets that do not ascend
+ * inside [0, n_rows], a length outside [0, max_kv_len] or past the table, and
+ * a page outside the pool record CB_ERR_DEVICE_INDEX; with a bad offset or
+ * length the sequence's rows are left unwritten, with a bad page they are
+ * unspecified. */
+size_t cb_paged_attention_workspace_size(int n_rows, int n_seq, int max_kv_len,
+                                         int n_q_heads, int n_kv_heads, int head_dim,
+                                         cb_dtype dtype);
+cb_status cb_paged_attention(const cb_paged_kv *kv, const void *q, int64_t ld_q,
+                             int n_rows, int max_kv_len, int n_q_heads,
+                             int n_kv_heads, int head_dim, float scale, void *out,
+                             int64_t ld_out, cb_dtype dtype, void *ws,
+                             size_t ws_bytes, cb_stream stream);
+
+/* Samples one token per row of logits from given uniform numbers.  With
+ * X = max x and w_i = exp((x_i - X) / temperature), of the tokens ordered by
+ * larger x, then lower index, keep the first top_k; of those the shortest
+ * prefix with at least top_p of their weight; of those w_i >= min_p.  The
+ * token is the lowest index i at which the kept weights of indices <= i
+ * exceed u times their total.
+ * logits: device [n_rows][ld_logits] of dtype, vocab columns, any element
+ * alignment.  Per row, device arrays: u (in [0, 1); below acts as 0, at or
+ * above 1 takes the last kept token); temperature (NULL: 1; not > 0: the
+ * arg-max, lowest index); top_k (NULL, <= 0 or >= vocab: off); top_p (NULL or
+ * >= 1: off; <= 0: the arg-max); min_p (NULL or <= 0: off; >= 1: the tokens
+ * equal to the largest).  NaN in top_p or min_p: off.
+ * A NaN logit counts as -inf, a token at -inf is never drawn; if several
+ * logits are +inf, one of those is.  tokens: device int32 [n_rows]; -1 for a
+ * row without a logit above -inf.
+ * Weights are 64-bit fixed point (exp to 2^-40), so sums are exact and the
+ * token does not depend on their order.
+ * Errors: CB_ERR_INVALID_ARG (NULL or misaligned pointers, ld_logits < vocab,
+ * n_rows outside [0, 2^20]), CB_ERR_UNSUPPORTED (vocab >
+ * CB_MAX_SAMPLE_VOCAB). */
+cb_status cb_sample_tokens(const void *logits, int64_t ld_logits, int n_rows,
+                           int vocab, cb_dtype dtype, const float *u,
+                           const float *temperature, const int32_t *top_k,
+                           const float *top_p, const float *min_p,
+                           int32_t *tokens, cb_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

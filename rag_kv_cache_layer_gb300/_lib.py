@@ -31,6 +31,8 @@ CB_PROBE_STITCH, CB_PROBE_SELECT, CB_PROBE_GATHER, CB_PROBE_LM_HEAD = 6, 7, 8, 9
 CB_PROBE_MLP = 10
 CB_MAX_BATCH = 64
 CB_MAX_SPANS = 1024
+CB_MAX_SEQS = 1024
+CB_MAX_SAMPLE_VOCAB = 262144
 
 
 class CBError(RuntimeError):
@@ -116,6 +118,13 @@ class Plan(C.Structure):
                 ("K_final", i64), ("R_final", i64)]
 
 
+class PagedKV(C.Structure):
+    _fields_ = [("k_pages", vp), ("v_pages", vp), ("page_stride", i64), ("ld", i64),
+                ("n_pages", i32), ("page_size", i32), ("block_table", vp),
+                ("ld_table", i64), ("max_pages", i32), ("row_offsets", vp),
+                ("kv_lens", vp), ("n_seq", i32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -181,6 +190,12 @@ def _load():
         "cb_anchor_count": (S, [C.POINTER(Segment), i32, i32, C.POINTER(i64)]),
         "cb_loading_ratio": (S, [C.c_double, C.POINTER(C.c_int32), C.POINTER(C.c_double), i32,
                                  C.c_int32, C.POINTER(C.c_int32)]),
+        "cb_paged_append": (S, [C.POINTER(PagedKV), vp, i64, i64, vp, i64, i64, i32, i32,
+                                i64, i32, i32, vp, i32, vp, i64, i32, vp, i64, i32, vp]),
+        "cb_paged_attention_workspace_size": (C.c_size_t, [i32, i32, i32, i32, i32, i32, i32]),
+        "cb_paged_attention": (S, [C.POINTER(PagedKV), vp, i64, i32, i32, i32, i32, i32,
+                                   C.c_float, vp, i64, i32, vp, C.c_size_t, vp]),
+        "cb_sample_tokens": (S, [vp, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp]),
         "cb_selection_stats": (S, [vp, vp, C.POINTER(SelectReq), i32, vp, vp, vp]),
     }
     for name, (res, args) in sigs.items():
@@ -211,6 +226,8 @@ EXPORTED = [
     "cb_layer_workspace_size", "cb_blend_layer",
     "cb_anchor_workspace_size", "cb_anchor_select", "cb_anchor_count",
     "cb_loading_ratio", "cb_selection_stats",
+    "cb_paged_append", "cb_paged_attention_workspace_size", "cb_paged_attention",
+    "cb_sample_tokens",
 ]
 
 

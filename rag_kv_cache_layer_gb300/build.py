@@ -30,6 +30,10 @@ SOURCES = [
     "k_attn_tc.cu",
     "k_qprobe.cu",
     "k_noalloc.cu",
+    "cb_paged_api.cu",
+    "k_paged_append.cu",
+    "k_paged_attn.cu",
+    "k_sample.cu",
 ]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
