@@ -33,6 +33,7 @@ SOURCES = [
     "cb_paged_api.cu",
     "k_paged_append.cu",
     "k_paged_attn.cu",
+    "k_paged_decode.cu",
     "k_sample.cu",
 ]
 

@@ -1,0 +1,28 @@
+// Parameters and variants of the paged attention, shared by its kernels.
+#pragma once
+
+#include "cb_common.cuh"
+#include "cb_internal.h"
+
+namespace cb {
+namespace paged {
+
+struct AttnParams {
+  PagedKV kv;
+  const void *q;
+  void *out;
+  int64_t ld_q, ld_out;
+  int n_rows, G, Hkv, max_kv;
+  int n_split;                            // parts of a tile's key range (fp32 kernel)
+  float scale_log2;                       // softmax scale times log2(e)
+  float *part_o;                          // unnormalised partial rows, HD floats each
+  float2 *part_ml;                        // (m, l) of each partial row
+};
+
+// bf16, few rows per sequence: R (16, 32 or 64) rows per tile.  The partials
+// take 2 * decode_grid() * R rows of the workspace.
+int decode_grid();
+cudaError_t launch_decode(const AttnParams &P, int R, int hd, int *status, cudaStream_t s);
+
+}  // namespace paged
+}  // namespace cb

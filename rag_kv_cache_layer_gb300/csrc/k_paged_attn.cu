@@ -14,6 +14,7 @@
 #include "cb_common.cuh"
 #include "cb_internal.h"
 #include "cb_paged.cuh"
+#include "cb_paged_attn.cuh"
 
 namespace cb {
 namespace paged {
@@ -21,25 +22,15 @@ namespace paged {
 constexpr int kSimtThreads = 256;
 constexpr int kBN = 64;                   // keys per block
 
-struct SimtParams {
-  PagedKV kv;
-  const void *q;
-  void *out;
-  int64_t ld_q, ld_out;
-  int n_rows, G, Hkv, max_kv, n_split;
-  float scale_log2;
-  float *part_o;                          // [tile * Hkv + g][split][R][HD]
-  float2 *part_ml;                        // (m, l) of each partial row
-};
-
 template <int R, int HD>
 constexpr size_t simt_smem() {
   return sizeof(float) * ((size_t)(R + kBN) * (HD + 4) + (size_t)kBN * HD + (size_t)R * kBN);
 }
 
-template <typename T, int R, int HD>
+template <int R, int HD>
 __global__ void __launch_bounds__(kSimtThreads)
-paged_simt_kernel(const __grid_constant__ SimtParams P, int *status) {
+paged_simt_kernel(const __grid_constant__ AttnParams P, int *status) {
+  typedef float T;
   constexpr int TM = R / 16, TD = HD / 64, VEC = 16 / sizeof(T), LD = HD + 4;
   extern __shared__ __align__(16) float sm[];
   float *sq = sm, *sk = sq + R * LD, *sv = sk + kBN * LD, *sp = sv + kBN * HD;
@@ -212,9 +203,10 @@ paged_simt_kernel(const __grid_constant__ SimtParams P, int *status) {
 // O = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c, in split order.  A warp
 // takes a row, each lane HD / 32 columns.
 constexpr int kMergeThreads = 256;
-template <typename T, int HD>
+template <int HD>
 __global__ void __launch_bounds__(kMergeThreads)
-paged_merge_kernel(const __grid_constant__ SimtParams P, int R, int *status) {
+paged_merge_kernel(const __grid_constant__ AttnParams P, int R, int *status) {
+  typedef float T;
   constexpr int PER = HD / 32;
   __shared__ PagedTile s_tile;
   __shared__ int s_sums[kMergeThreads / 32];
@@ -259,51 +251,60 @@ static int64_t tile_bound(int64_t n_rows, int S, int G, int R) {
   return a < b ? a : b;
 }
 
-struct Split {
-  int R;                                  // rows per tile
-  int64_t tiles;                          // tiles at most
+// How a call runs: rows per tile and, in fp32, the tiles at most and the
+// parts of their key ranges.
+struct Plan {
+  bool simt;                              // fp32 on the CUDA cores
+  int R;
+  int64_t tiles;
   int n_split;
+  int64_t partials;                       // partial rows the workspace holds
 };
 
-// Rows per tile: 16 where a sequence brings few rows (the wider tile would
-// mostly multiply zeros), else 64.  Key ranges are split until about two
-// waves of blocks run, in pieces of at least two blocks of keys.
-static Split plan(int64_t n_rows, int S, int max_kv, int G, int Hkv) {
-  Split p;
-  p.R = n_rows * G <= (int64_t)S * 16 ? 16 : 64;
+// fp32: 16-row tiles where a sequence brings few rows (the wider tile would
+// mostly multiply zeros), else 64; key ranges are split until about two waves
+// of blocks run, in parts of at least two 64-key blocks.
+// bf16: tiles of 16, 32 or 64 rows by the average sequence's rows.
+static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, cb_dtype dt) {
+  Plan p;
+  const int64_t per_seq = (n_rows * G + S - 1) / S;
+  p.simt = dt != CB_BF16;
+  p.tiles = p.n_split = 1;
+  if (!p.simt) {
+    p.R = per_seq <= 16 ? 16 : per_seq <= 32 ? 32 : 64;
+    p.partials = 2LL * decode_grid() * p.R;
+    return p;
+  }
+  p.R = per_seq <= 16 ? 16 : 64;
   p.tiles = tile_bound(n_rows, S, G, p.R);
-  const int64_t units = p.tiles * Hkv;
-  const int64_t want = (4LL * device_sm_count() + units - 1) / (units > 0 ? units : 1);
-  const int64_t most = (max_kv + 2 * kBN - 1) / (2 * kBN);
-  int64_t n = want < most ? want : most;
-  if (n > 64) n = 64;
-  p.n_split = n < 1 ? 1 : (int)n;
+  const int64_t units = p.tiles * Hkv > 0 ? p.tiles * Hkv : 1;
+  const int64_t want = (4LL * device_sm_count() + units - 1) / units, most = (max_kv + 127) / 128;
+  const int64_t n = want < most ? want : most;
+  p.n_split = n < 1 ? 1 : n > 64 ? 64 : (int)n;
+  p.partials = p.n_split == 1 ? 0 : p.tiles * Hkv * p.n_split * p.R;
   return p;
 }
 
-template <typename T, int R, int HD>
-static cudaError_t run_simt(const SimtParams &P, int64_t tiles, int *status, cudaStream_t s) {
+template <int R, int HD>
+static cudaError_t run_simt(const AttnParams &P, const Plan &p, int *status, cudaStream_t s) {
   static PerDeviceOnce attr;
   cudaError_t e = attr.run([](int) {
-    return cudaFuncSetAttribute(paged_simt_kernel<T, R, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(paged_simt_kernel<R, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)simt_smem<R, HD>());
   });
   if (e != cudaSuccess) return e;
-  e = launch_pdl(paged_simt_kernel<T, R, HD>, dim3((unsigned)(tiles * P.Hkv * P.n_split)),
+  e = launch_pdl(paged_simt_kernel<R, HD>, dim3((unsigned)(p.tiles * P.Hkv * P.n_split)),
                  dim3(kSimtThreads), simt_smem<R, HD>(), s, P, status);
   if (e != cudaSuccess) return e;
   if (P.n_split == 1) return launched(1);
-  e = launch_pdl(paged_merge_kernel<T, HD>, dim3((unsigned)(tiles * P.Hkv)), dim3(kMergeThreads), 0, s,
-                 P, R, status);
-  if (e != cudaSuccess) return e;
-  return launched(2);
+  e = launch_pdl(paged_merge_kernel<HD>, dim3((unsigned)(p.tiles * P.Hkv)), dim3(kMergeThreads), 0, s, P, R, status);
+  return e == cudaSuccess ? launched(2) : e;
 }
 
-template <typename T>
-static cudaError_t run_type(const SimtParams &P, const Split &sp, int hd, int *status, cudaStream_t s) {
-  if (hd == 128)
-    return sp.R == 16 ? run_simt<T, 16, 128>(P, sp.tiles, status, s) : run_simt<T, 64, 128>(P, sp.tiles, status, s);
-  return sp.R == 16 ? run_simt<T, 16, 64>(P, sp.tiles, status, s) : run_simt<T, 64, 64>(P, sp.tiles, status, s);
+template <int HD>
+static cudaError_t run_all(const AttnParams &P, const Plan &p, int *status, cudaStream_t s) {
+  if (!p.simt) return launch_decode(P, p.R, HD, status, s);
+  return p.R == 16 ? run_simt<16, HD>(P, p, status, s) : run_simt<64, HD>(P, p, status, s);
 }
 
 }  // namespace paged
@@ -311,9 +312,7 @@ static cudaError_t run_type(const SimtParams &P, const Split &sp, int hd, int *s
 size_t paged_attention_ws_bytes(int n_rows, int n_seq, int max_kv, int Hq, int Hkv, int hd, cb_dtype dt) {
   using namespace paged;
   if (n_rows <= 0 || n_seq <= 0) return 0;
-  const Split sp = plan(n_rows, n_seq, max_kv, Hq / Hkv, Hkv);
-  if (sp.n_split == 1) return 0;
-  return (size_t)sp.tiles * Hkv * sp.n_split * sp.R * (hd * sizeof(float) + sizeof(float2));
+  return (size_t)plan(n_rows, n_seq, max_kv, Hq / Hkv, Hkv, dt).partials * (hd * sizeof(float) + sizeof(float2));
 }
 
 cudaError_t launch_paged_attention(const PagedKV &kv, const void *q, int64_t ld_q, int n_rows, int max_kv,
@@ -321,9 +320,9 @@ cudaError_t launch_paged_attention(const PagedKV &kv, const void *q, int64_t ld_
                                    cb_dtype dt, void *ws, int *status, cudaStream_t s) {
   using namespace paged;
   if (n_rows == 0 || kv.n_seq == 0) return cudaSuccess;
-  const Split sp = plan(n_rows, kv.n_seq, max_kv, Hq / Hkv, Hkv);
-  if (sp.tiles * Hkv * sp.n_split > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  SimtParams P;
+  const Plan p = plan(n_rows, kv.n_seq, max_kv, Hq / Hkv, Hkv, dt);
+  if (p.tiles * Hkv * p.n_split > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  AttnParams P;
   P.kv = kv;
   P.q = q;
   P.out = out;
@@ -333,11 +332,11 @@ cudaError_t launch_paged_attention(const PagedKV &kv, const void *q, int64_t ld_
   P.G = Hq / Hkv;
   P.Hkv = Hkv;
   P.max_kv = max_kv;
-  P.n_split = sp.n_split;
+  P.n_split = p.n_split;
   P.scale_log2 = scale * 1.4426950408889634f;
   P.part_o = reinterpret_cast<float *>(ws);
-  P.part_ml = reinterpret_cast<float2 *>(P.part_o + (size_t)sp.tiles * Hkv * sp.n_split * sp.R * hd);
-  return dt == CB_BF16 ? run_type<bf16>(P, sp, hd, status, s) : run_type<float>(P, sp, hd, status, s);
+  P.part_ml = reinterpret_cast<float2 *>(P.part_o + (size_t)p.partials * hd);
+  return hd == 128 ? run_all<128>(P, p, status, s) : run_all<64>(P, p, status, s);
 }
 
 }  // namespace cb

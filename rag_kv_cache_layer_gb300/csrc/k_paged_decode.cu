@@ -1,0 +1,465 @@
+// bf16 paged attention of a few rows per sequence (generated tokens, short
+// drafts): keys and values stream through shared memory once, and the group's
+// q heads share them.
+//
+// Work.  A tile is R = 16 WM rows of one sequence and kv head (an item); its
+// keys come in blocks of BN.  All blocks of all items form one line of units,
+// which is cut into equal parts, one per block of the grid (two per SM): a
+// long sequence is shared by many blocks, short ones are taken whole, and the
+// lengths decide that on the device, so lengths of any mix keep every SM busy
+// until the end.  An item inside one part is written out directly; one that
+// crosses parts leaves its pieces' (O, m, l) in the workspace, at most two per
+// block, and decode_merge_kernel joins them.
+//
+// A block's four warps form WK = 4 / WM groups of WM warps; key block i goes
+// to group i mod WK.  A group fills a ring of its own by 16-byte cp.async,
+// two blocks ahead, with zeros for keys past the cached length (so nothing
+// unwritten in a page reaches the products), and meets nobody else inside the
+// loop.  TMA is not used here: a page's slice of one head is a box of 8 to 64
+// rows of 256 bytes, and a box costs about 140 ns of one SM's copy unit
+// whatever its height, which held the same loop to 12 - 27 GB/s per block.
+//
+// Each warp holds 16 rows: S = Q K^T and O += P V by mma.m16n8k16 on
+// fragments from ldmatrix, running maximum, sum and O in registers (base-2
+// exponentials, fp32; P rounds to bf16 as the second product's operand).  The
+// legacy tensor instruction is the right one: the work is bound by the pages'
+// bytes, 45 bytes per nanosecond and SM, and a 128-row tcgen05 tile with 4
+// rows in use would not read them faster.
+#include "cb_common.cuh"
+#include "cb_internal.h"
+#include "cb_paged.cuh"
+#include "cb_paged_attn.cuh"
+
+namespace cb {
+namespace paged {
+
+constexpr int kDecThreads = 128;
+constexpr int kDecBlocksPerSm = 2;
+
+template <int HD, int WM> struct DecCfg {
+  static constexpr int kBN = 2048 / HD;         // keys per stage: 8 KB of K and V
+  static constexpr int kTile = kBN * HD * 2;
+  static constexpr int kStage = 2 * kTile;      // K then V
+  static constexpr int kStages = 3 * WM;        // of each group: 96 KB per block
+  static constexpr int kSmem = (4 / WM) * kStages * kStage;
+};
+
+__device__ __forceinline__ void ldsm_x4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+// 16 bytes to shared memory, or 16 zero bytes when `there` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+// 2^x, relative error about 2^-22, far below the rounding of P to bf16.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Meets the WM warps of group `wk` (named barrier 1 + wk).
+template <int WM> __device__ __forceinline__ void group_sync(int wk) {
+  if (WM == 1) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(1 + wk), "r"(32 * WM) : "memory");
+}
+
+// ------------------------------------------------------------------ plan --
+// The line of units.  Sequence s has items(s) = tiles * Hkv items of blocks(s)
+// units each (every tile counts the sequence's whole length; the few keys a
+// tile's last row does not see are skipped when met).
+struct Line {
+  int64_t begin[CB_MAX_SEQS];     // first unit of each sequence
+  int blocks[CB_MAX_SEQS];        // units per item; 0: nothing to do
+  int64_t total;
+  int parts;                      // blocks of the grid that take part
+};
+
+__device__ __forceinline__ int64_t part_begin(const Line &L, int c) { return L.total * c / L.parts; }
+__device__ __forceinline__ int part_of(const Line &L, int64_t u) {
+  int c = (int)(u * L.parts / L.total);
+  while (c + 1 < L.parts && part_begin(L, c + 1) <= u) ++c;
+  while (c > 0 && part_begin(L, c) > u) --c;
+  return c;
+}
+
+// Every thread of the block calls it; one round of loads, one block scan.
+template <int NT>
+__device__ __forceinline__ void make_line(const AttnParams &P, int R, int BN, int grid, Line &L, int64_t *warp_sums,
+                                          int *status) {
+  constexpr int kPer = (CB_MAX_SEQS + NT - 1) / NT;
+  const int per = (P.kv.n_seq + NT - 1) / NT, i0 = threadIdx.x * per;
+  int64_t u[kPer], sum = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    u[k] = 0;
+    if (k < per && i0 + k < P.kv.n_seq) {
+      const int n = paged_rows(P.kv, i0 + k, P.n_rows, status), len = __ldg(P.kv.kv_lens + i0 + k);
+      int nb = 0;
+      if (n > 0) {
+        if (len < 0 || len > P.max_kv || len > (int64_t)P.kv.max_pages * P.kv.page_size)
+          report(status, CB_ERR_DEVICE_INDEX);
+        else
+          nb = len > 0 ? (len - 1) / BN + 1 : 1;        // an idle slot's rows get their zeros
+      }
+      L.blocks[i0 + k] = nb;
+      u[k] = ((int64_t)n * P.G + R - 1) / R * P.Hkv * nb;
+    }
+    sum += u[k];
+  }
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int64_t incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) warp_sums[w] = incl;
+  __syncthreads();
+  int64_t first = incl - sum;
+  for (int x = 0; x < w; ++x) first += warp_sums[x];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if (k < per && i0 + k < P.kv.n_seq) L.begin[i0 + k] = first;
+    first += u[k];
+  }
+  if (threadIdx.x == NT - 1) {
+    L.total = first;
+    // a part has at least one unit for each consumer group
+    const int64_t most = (first + 3) / 4;
+    L.parts = (int)(most < grid ? most : grid);
+  }
+  __syncthreads();
+}
+
+// The sequence that holds unit u.
+__device__ __forceinline__ int seq_of(const Line &L, int n_seq, int64_t u) {
+  int lo = 0, hi = n_seq - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (L.begin[mid] <= u) lo = mid; else hi = mid - 1;
+  }
+  return lo;                      // the last one that begins at or before u
+}
+
+template <int HD, int WM>
+__global__ void __launch_bounds__(kDecThreads, kDecBlocksPerSm)
+paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
+  typedef DecCfg<HD, WM> C;
+  constexpr int R = 16 * WM, WK = 4 / WM, ND = HD / 8, KS = HD / 16, BN = C::kBN, NS = C::kStages;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ Line line;
+  __shared__ int64_t s_sums[kDecThreads / 32];
+  __shared__ float2 s_ml[4 * 16];               // (m, l) of each warp's rows
+  grid_dep_wait();
+  grid_dep_launch();
+  make_line<kDecThreads>(P, R, BN, gridDim.x, line, s_sums, status);
+  if ((int)blockIdx.x >= line.parts) return;
+  const int64_t u0 = part_begin(line, blockIdx.x), u1 = part_begin(line, blockIdx.x + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wm = warp % WM, wk = warp / WM, gid = lane >> 2, q4 = lane & 3;
+  const uint32_t ring = smem_u32(smem) + wk * NS * C::kStage;
+  const int shift = __ffs(P.kv.page_size) - 1;
+  const bf16 *kp = reinterpret_cast<const bf16 *>(P.kv.k_pages), *vp = reinterpret_cast<const bf16 *>(P.kv.v_pages);
+  // rows and column that this lane copies: row i * kRows + crow of a stage
+  constexpr int kCols = HD / 8, kRows = 32 / kCols;
+  const int crow = lane / kCols, ccol = lane % kCols;
+  // ldmatrix row of this lane: K tiles as 8 keys x 4 8-dim columns, V tiles as
+  // 16 keys x 2 8-dim columns
+  const int krow = lane & 7, kcol = lane >> 3, vrow = lane & 15, vcol = lane >> 4;
+  const float sl2 = P.scale_log2;
+
+  int s = seq_of(line, P.kv.n_seq, u0);
+  for (int64_t u = u0; u < u1;) {
+    // this piece: item `item` of sequence s, its blocks [jb, je)
+    while (line.blocks[s] == 0 || (s + 1 < P.kv.n_seq && line.begin[s + 1] <= u)) ++s;
+    const int nbs = line.blocks[s];
+    const int item = (int)((u - line.begin[s]) / nbs), jb = (int)((u - line.begin[s]) % nbs);
+    const int take = (int)min((int64_t)(nbs - jb), u1 - u);
+    const bool whole = jb == 0 && take == nbs, first = u == u0;
+    u += take;
+    const int g = item % P.Hkv, l0 = item / P.Hkv * R;
+    const int row0 = __ldg(P.kv.row_offsets + s), n = __ldg(P.kv.row_offsets + s + 1) - row0;
+    const int kv = __ldg(P.kv.kv_lens + s), base = kv - n, rows = min(R, n * P.G - l0);
+    const int seen = base + (l0 + rows - 1) / P.G + 1;        // keys the tile's last row sees
+    const int je = min(jb + take, seen > 0 ? (seen - 1) / BN + 1 : 0);
+    const int32_t *table = P.kv.block_table + (int64_t)s * P.kv.ld_table;
+
+    auto fetch = [&](int j) -> int {            // page of key j * BN + lane
+      const int key = j * BN + lane;
+      return j < je && lane < BN && key < kv ? __ldg(table + (key >> shift)) : -1;
+    };
+    auto load = [&](int j, int st, int page) {
+      const uint32_t dst = ring + st * C::kStage;
+      if (page >= 0 && page >= P.kv.n_pages) {
+        report(status, CB_ERR_DEVICE_INDEX);
+        page = -1;
+      } else if (page < 0 && j < je && lane < BN && j * BN + lane < kv) {
+        report(status, CB_ERR_DEVICE_INDEX);
+      }
+#pragma unroll
+      for (int i = 0; i < BN / kRows / WM; ++i) {
+        const int r = (i * WM + wm) * kRows + crow;
+        const int pg = __shfl_sync(0xffffffffu, page, r);
+        const int slot = (j * BN + r) & (P.kv.page_size - 1);
+        const int64_t off = pg < 0 ? 0 : (int64_t)pg * P.kv.page_stride + (int64_t)slot * P.kv.ld + g * HD + ccol * 8;
+        const uint32_t d = dst + r * (HD * 2) + (((ccol & 8) | ((ccol ^ r) & 7)) << 4);
+        copy16(d, kp + off, pg >= 0);
+        copy16(d + C::kTile, vp + off, pg >= 0);
+      }
+    };
+    auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+
+    int pos[2];
+    uint32_t qf[KS][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = wm * 16 + gid + 8 * h;
+      const bool valid = r < rows;
+      const int qi = (l0 + r) / P.G;
+      pos[h] = valid ? base + qi : -1;
+      const bf16 *src = reinterpret_cast<const bf16 *>(P.q) + (int64_t)(row0 + qi) * P.ld_q +
+                        (int64_t)(g * P.G + (l0 + r) % P.G) * HD + q4 * 2;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          qf[k][h + 2 * c] = valid ? *reinterpret_cast<const uint32_t *>(src + k * 16 + c * 8) : 0u;
+    }
+    float o[ND][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
+
+    // group's blocks: jb + wk, jb + wk + WK, ..; the table is read one block
+    // further ahead than the pages
+    int page = fetch(jb + wk);
+    for (int i = 0; i < NS - 1; ++i) {
+      const int j = jb + wk + i * WK, next = fetch(j + WK);
+      if (j < je) load(j, i, page);
+      page = next;
+      commit();
+    }
+    int st = 0, fill = NS - 1;
+    for (int j = jb + wk; j < je; j += WK) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
+      group_sync<WM>(wk);                       // landed for every warp; the stage before is used up
+      {
+        const int jn = j + (NS - 1) * WK, next = fetch(jn + WK);
+        if (jn < je) load(jn, fill, page);
+        page = next;
+        commit();
+        fill = fill + 1 == NS ? 0 : fill + 1;
+      }
+      const uint32_t ks = ring + st * C::kStage, vs = ks + C::kTile;
+      st = st + 1 == NS ? 0 : st + 1;
+      float x[BN / 8][4];
+#pragma unroll
+      for (int t = 0; t < BN / 8; ++t) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[t][k] = 0.f;
+        const uint32_t row = ks + (t * 8 + krow) * (HD * 2);
+#pragma unroll
+        for (int k2 = 0; k2 < HD / 32; ++k2) {
+          uint32_t b[4];
+          const int ch = k2 * 4 + kcol;         // 16-byte column
+          ldsm_x4(row + (((ch & 8) | ((ch ^ krow) & 7)) << 4), b);
+          mma16816(x[t], qf[2 * k2], b[0], b[1]);
+          mma16816(x[t], qf[2 * k2 + 1], b[2], b[3]);
+        }
+      }
+      const int key0 = j * BN;
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int t = 0; t < BN / 8; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = key0 + t * 8 + q4 * 2 + (k & 1);
+          x[t][k] = key <= pos[k >> 1] ? x[t][k] * sl2 : -INFINITY;
+          mx[k >> 1] = fmaxf(mx[k >> 1], x[t][k]);
+        }
+      bool moved = false;
+      float corr[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+        const float mn = fmaxf(m[h], mx[h]);
+        corr[h] = mn == m[h] ? 1.f : ex2(m[h] - mn);        // also where both are -inf
+        moved |= mn != m[h];
+        m[h] = mn;
+        l[h] *= corr[h];
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[d][k] *= corr[k >> 1];
+      }
+#pragma unroll
+      for (int t = 0; t < BN / 8; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float p = x[t][k] == -INFINITY ? 0.f : ex2(x[t][k] - m[k >> 1]);
+          x[t][k] = p;
+          l[k >> 1] += p;
+        }
+#pragma unroll
+      for (int k2 = 0; k2 < BN / 16; ++k2) {
+        const uint32_t a[4] = {pack_bf16(x[2 * k2][0], x[2 * k2][1]), pack_bf16(x[2 * k2][2], x[2 * k2][3]),
+                               pack_bf16(x[2 * k2 + 1][0], x[2 * k2 + 1][1]),
+                               pack_bf16(x[2 * k2 + 1][2], x[2 * k2 + 1][3])};
+        const uint32_t row = vs + (k2 * 16 + vrow) * (HD * 2);
+#pragma unroll
+        for (int d2 = 0; d2 < ND / 2; ++d2) {
+          uint32_t b[4];
+          const int ch = d2 * 2 + vcol;
+          ldsm_x4_t(row + (((ch & 8) | ((ch ^ vrow) & 7)) << 4), b);
+          mma16816(o[2 * d2], a, b[0], b[1]);
+          mma16816(o[2 * d2 + 1], a, b[2], b[3]);
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      if (q4 == 0) s_ml[warp * 16 + gid + 8 * h] = make_float2(m[h], l[h]);
+    }
+    __syncthreads();                            // the rings are used up
+    // Every warp leaves its O in rows of HD + 4 floats (a quad's four rows
+    // fall into different banks), then the groups' states join.
+    constexpr int LD = HD + 4;
+    static_assert(4 * 16 * LD * 4 <= C::kSmem, "the warps' O fit the rings");
+    float *so = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float2 *>(so + (warp * 16 + gid + 8 * h) * LD + d * 8 + q4 * 2) =
+            make_float2(o[d][2 * h], o[d][2 * h + 1]);
+    __syncthreads();
+    const int64_t slot = (2 * (int64_t)blockIdx.x + (first ? 0 : 1)) * R;
+    for (int i = threadIdx.x; i < rows * (HD / 4); i += kDecThreads) {
+      const int r = i / (HD / 4), c = i % (HD / 4) * 4;
+      float M = -INFINITY, L = 0.f;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < WK; ++k) M = fmaxf(M, s_ml[(k * WM + r / 16) * 16 + r % 16].x);
+#pragma unroll
+      for (int k = 0; k < WK; ++k) {
+        const int row = (k * WM + r / 16) * 16 + r % 16;
+        const float2 ml = s_ml[row];
+        const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+        const float4 v = *reinterpret_cast<const float4 *>(so + row * LD + c);
+        L += w * ml.y;
+        a.x += w * v.x; a.y += w * v.y; a.z += w * v.z; a.w += w * v.w;
+      }
+      if (!whole) {
+        *reinterpret_cast<float4 *>(P.part_o + (slot + r) * HD + c) = a;
+        if (c == 0) P.part_ml[slot + r] = make_float2(M, L);
+      } else {
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        bf16 *dst = reinterpret_cast<bf16 *>(P.out) + (int64_t)(row0 + (l0 + r) / P.G) * P.ld_out +
+                    (int64_t)(g * P.G + (l0 + r) % P.G) * HD + c;
+        *reinterpret_cast<uint2 *>(dst) =
+            make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+      }
+    }
+    __syncthreads();                            // before the next piece fills the rings
+  }
+}
+
+// Joins the pieces of every item that crosses parts.  One block per item; a
+// warp takes a row, each lane HD / 32 columns.
+constexpr int kJoinThreads = 128;
+template <int HD>
+__global__ void __launch_bounds__(kJoinThreads)
+decode_merge_kernel(const __grid_constant__ AttnParams P, int R, int BN, int grid, int *status) {
+  constexpr int PER = HD / 32;
+  __shared__ Line line;
+  __shared__ int64_t s_sums[kJoinThreads / 32];
+  grid_dep_wait();
+  grid_dep_launch();
+  make_line<kJoinThreads>(P, R, BN, grid, line, s_sums, status);
+  // block i looks at the i-th part border, and joins the item that crosses it
+  // where this is the first border inside it
+  const int c1 = blockIdx.x + 1;
+  if (c1 >= line.parts) return;
+  const int64_t border = part_begin(line, c1);
+  const int s = seq_of(line, P.kv.n_seq, border);
+  const int nbs = line.blocks[s], item = (int)((border - line.begin[s]) / nbs);
+  const int64_t a = line.begin[s] + (int64_t)item * nbs, b = a + nbs;
+  if (border == a || part_begin(line, c1 - 1) > a) return;   // no item crosses it, or an earlier border is inside
+  const int row0 = __ldg(P.kv.row_offsets + s), n = __ldg(P.kv.row_offsets + s + 1) - row0;
+  const int g = item % P.Hkv, l0 = item / P.Hkv * R, rows = min(R, n * P.G - l0);
+  const int cl = c1 - 1, ch = part_of(line, b - 1);          // first and last part with a piece
+  auto slot = [&](int c) { return (2 * (int64_t)c + (c == cl && part_begin(line, cl) != a ? 1 : 0)) * R; };
+  const int lane = threadIdx.x & 31;
+  for (int r = threadIdx.x >> 5; r < rows; r += kJoinThreads / 32) {
+    float M = -INFINITY;
+    for (int c = cl + lane; c <= ch; c += 32) M = fmaxf(M, P.part_ml[slot(c) + r].x);
+    M = warp_max(M);
+    float l = 0.f, o[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int c = cl; c <= ch; ++c) {
+      const float2 ml = P.part_ml[slot(c) + r];
+      const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);   // no visible key in this piece
+      l += w * ml.y;
+      const float *src = P.part_o + (slot(c) + r) * HD + lane * PER;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) o[e] = fmaf(w, src[e], o[e]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    bf16 *dst = reinterpret_cast<bf16 *>(P.out) + (int64_t)(row0 + (l0 + r) / P.G) * P.ld_out +
+                (int64_t)(g * P.G + (l0 + r) % P.G) * HD + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER; e += 2)
+      *reinterpret_cast<uint32_t *>(dst + e) = pack_bf16(o[e] * inv, o[e + 1] * inv);
+  }
+}
+
+int decode_grid() { return kDecBlocksPerSm * device_sm_count(); }
+
+template <int HD, int WM>
+static cudaError_t run(const AttnParams &P, int *status, cudaStream_t s) {
+  typedef DecCfg<HD, WM> C;
+  static PerDeviceOnce attr;
+  cudaError_t e = attr.run([](int) {
+    return cudaFuncSetAttribute(paged_decode_kernel<HD, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  const int grid = decode_grid();
+  e = launch_pdl(paged_decode_kernel<HD, WM>, dim3(grid), dim3(kDecThreads), C::kSmem, s, P, status);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(decode_merge_kernel<HD>, dim3(grid), dim3(kJoinThreads), 0, s, P, 16 * WM, C::kBN, grid, status);
+  return e == cudaSuccess ? launched(2) : e;
+}
+
+cudaError_t launch_decode(const AttnParams &P, int R, int hd, int *status, cudaStream_t s) {
+  if (hd == 128)
+    return R == 16 ? run<128, 1>(P, status, s) : R == 32 ? run<128, 2>(P, status, s) : run<128, 4>(P, status, s);
+  return R == 16 ? run<64, 1>(P, status, s) : R == 32 ? run<64, 2>(P, status, s) : run<64, 4>(P, status, s);
+}
+
+}  // namespace paged
+}  // namespace cb

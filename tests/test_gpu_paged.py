@@ -284,6 +284,16 @@ def test_attention_split_over_long_keys(dt, heads, n, kv):
 
 
 @pytest.mark.parametrize("dt", list(HALF))
+@pytest.mark.parametrize("heads,page", [((8, 8, 128), 16), ((32, 16, 64), 64), ((32, 16, 64), 8)])
+@pytest.mark.parametrize("n", [1, 3, 20])
+def test_attention_long_loops(dt, heads, page, n):
+    """Enough tiles that no range is split far: every stage is used many times."""
+    rng = np.random.default_rng(n)
+    seqs = [(n, int(rng.integers(1500, 4500))) for _ in range(26)]
+    attention_case(rng, dt, heads, page, seqs if n < 20 else seqs[:8])
+
+
+@pytest.mark.parametrize("dt", list(HALF))
 def test_attention_many_sequences(dt):
     rng = np.random.default_rng(77)
     seqs = [(int(rng.integers(0, 4)), int(rng.integers(0, 60))) for _ in range(300)]

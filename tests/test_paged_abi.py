@@ -151,3 +151,61 @@ def test_oracle_sampling_by_hand():
     assert OP.sample_token([-np.inf, np.nan], 0.3) == -1
     assert OP.sample_token([np.inf, 1.0, np.inf], 0.7) == 2
     assert OP.sample_token([2.0, 2.0, 2.0], 0.5, top_k=2) == 1                       # ties: lowest indices kept
+
+
+# ----------------------------------------------------- the line of units --
+def _line(units, blocks, grid):
+    """The decode kernel's partition, restated: (part, item, first block, end
+    block, slot or None) of every piece, and (item, slots) of every join.
+    units: items per sequence; blocks: units per item (0: nothing)."""
+    begin = np.concatenate([[0], np.cumsum([u * b for u, b in zip(units, blocks)])])
+    total = int(begin[-1])
+    parts = min((total + 3) // 4, grid)
+    pb = lambda c: total * c // parts
+    seq = lambda u: max(s for s in range(len(units)) if begin[s] <= u)
+    pieces, joins = [], []
+    for c in range(parts):
+        u = pb(c)
+        s = seq(u)
+        while u < pb(c + 1):
+            while blocks[s] == 0 or (s + 1 < len(units) and begin[s + 1] <= u):
+                s += 1
+            item, jb = divmod(int(u - begin[s]), blocks[s])
+            take = min(blocks[s] - jb, pb(c + 1) - u)
+            whole = jb == 0 and take == blocks[s]
+            pieces.append((c, (s, item), jb, jb + take, None if whole else 2 * c + (u != pb(c))))
+            u += take
+    for c in range(1, parts):
+        s = seq(pb(c))
+        item = int(pb(c) - begin[s]) // blocks[s]
+        a = int(begin[s]) + item * blocks[s]
+        if pb(c) == a or pb(c - 1) > a:
+            continue
+        last = max(x for x in range(parts) if pb(x) <= a + blocks[s] - 1)
+        joins.append(((s, item), [2 * x + (x == c - 1 and pb(x) != a) for x in range(c - 1, last + 1)]))
+    return pieces, joins
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_every_unit_once_and_every_split_item_joined_once(seed):
+    rng = np.random.default_rng(seed)
+    n = int(rng.integers(1, 9))
+    units = [int(rng.integers(0, 9)) for _ in range(n)]
+    blocks = [int(rng.integers(1, [3, 30, 300][seed % 3])) if u else 0 for u in units]
+    if not any(units):
+        units[0], blocks[0] = 2, 5
+    pieces, joins = _line(units, blocks, int(rng.integers(1, 40)))
+    seen = {}
+    for c, item, jb, je, slot in pieces:
+        assert jb < je
+        seen.setdefault(item, []).append((jb, je, slot))
+    for s in range(n):
+        for k in range(units[s]):
+            got = sorted(seen.pop((s, k)))
+            assert [x[0] for x in got] == [0] + [x[1] for x in got[:-1]] and got[-1][1] == blocks[s]
+            slots = [x[2] for x in got]
+            found = [j for i, j in joins if i == (s, k)]
+            assert found == ([] if len(got) == 1 and slots == [None] else [slots])
+    assert not seen
+    used = [x[4] for x in pieces if x[4] is not None]
+    assert len(used) == len(set(used))
