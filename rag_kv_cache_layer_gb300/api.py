@@ -166,45 +166,50 @@ def cb_sparse_query_attention(q, q_pos, reqs, k_cache, v_cache, n_q_heads,
 
 
 # ------------------------------------------------------------ generation --
-def _same_device(*tensors):
-    """Kernels run on the current device: every tensor must live there."""
-    dev = torch.cuda.current_device()
+# These calls run once per layer and generated token, so their checks read
+# each tensor attribute once and build no intermediate objects.
+_cur_device = torch._C._cuda_getDevice
+_cur_stream = torch._C._cuda_getCurrentRawStream
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_CODES = {_BF16: L.CB_BF16, _F32: L.CB_F32}
+
+
+def _on_device(*tensors):
+    """Kernels run on the current device: every tensor must live there.
+    Returns that device's index."""
+    dev = _cur_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+    return dev
 
 
-def _rows(name, t, dtype, cols=None):
-    """Leading dimension of a row tensor [.., rows, cols] of `dtype`."""
-    if t.dtype != dtype:
-        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
-    if t.stride(-1) != 1 or (cols is not None and t.shape[-1] != cols):
-        raise ValueError(f"{name} must have contiguous rows" + ("" if cols is None else f" of {cols}"))
-    return t.stride(-2) if t.shape[-2] > 1 else t.shape[-1]
-
-
-def _ints(name, t, shape):
-    if t.dtype != torch.int32 or t.shape != shape or t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name} must be int32 of shape {tuple(shape)} with contiguous rows")
+def _ld(name, t, dtype, rows, cols):
+    """Leading dimension of a matrix t [rows, cols] of `dtype`."""
+    ld, one = t.stride()
+    if t.dtype != dtype or t.shape != (rows, cols) or (one != 1 and cols > 1):
+        raise ValueError(f"{name} must be {dtype} of shape ({rows}, {cols}) with contiguous rows")
+    return ld if rows > 1 else cols
 
 
 def _paged_kv(k_pages, v_pages, row_offsets, kv_lens, block_table):
-    n_seq = kv_lens.shape[0]
-    _ints("kv_lens", kv_lens, (n_seq,))
-    _ints("row_offsets", row_offsets, (n_seq + 1,))
-    _ints("block_table", block_table, (n_seq, block_table.shape[-1]))
-    if v_pages.shape != k_pages.shape or k_pages.dim() not in (3, 4):
-        raise ValueError("k_pages and v_pages must be [n_pages, page_size, row] (or with a "
-                         "leading layer dimension) of one shape")
-    n_pages, page, cols = k_pages.shape[-3:]
-    ld = _rows("k_pages", k_pages, k_pages.dtype)
-    stride = k_pages.stride(-3) if n_pages > 1 else page * ld
-    if _rows("v_pages", v_pages, k_pages.dtype) != ld or (n_pages > 1 and v_pages.stride(-3) != stride):
-        raise ValueError("k_pages and v_pages must have the same strides")
-    return L.PagedKV(k_pages.data_ptr(), v_pages.data_ptr(), stride, ld, n_pages, page,
-                     block_table.data_ptr(),
-                     block_table.stride(0) if n_seq > 1 else block_table.shape[1],
-                     block_table.shape[1], row_offsets.data_ptr(), kv_lens.data_ptr(), n_seq)
+    n_seq, = kv_lens.shape
+    seqs, width = block_table.shape
+    ld_table, one = block_table.stride()
+    if kv_lens.dtype != _I32 or row_offsets.dtype != _I32 or block_table.dtype != _I32 or \
+            row_offsets.shape != (n_seq + 1,) or seqs != n_seq or (one != 1 and width > 1) or \
+            (n_seq > 1 and kv_lens.stride(0) != 1) or row_offsets.stride(0) != 1:
+        raise ValueError("row_offsets [n_seq + 1], kv_lens [n_seq] and block_table [n_seq, max_pages] "
+                         "must be int32 with contiguous rows")
+    shape, strides = k_pages.shape, k_pages.stride()
+    if v_pages.shape != shape or v_pages.dtype != k_pages.dtype or v_pages.stride() != strides or \
+            strides[-1] != 1:
+        raise ValueError("k_pages and v_pages must have one shape, type and strides, with contiguous slots")
+    n_pages, page, cols = shape[-3:]
+    ld = strides[-2] if page > 1 else cols
+    return L.PagedKV(k_pages.data_ptr(), v_pages.data_ptr(), strides[-3] if n_pages > 1 else page * ld, ld,
+                     n_pages, page, block_table.data_ptr(), ld_table if n_seq > 1 else width, width,
+                     row_offsets.data_ptr(), kv_lens.data_ptr(), n_seq)
 
 
 def cb_paged_append(k_new, v_new, row_offsets, kv_lens, block_table, k_pages, v_pages,
@@ -216,39 +221,45 @@ def cb_paged_append(k_new, v_new, row_offsets, kv_lens, block_table, k_pages, v_
     block_table [n_seq, max_pages]: device int32.  rope_table: from
     cb_rope_table_init; None copies the keys as they are.  q: [rows,
     n_q_heads * head_dim], rotated into q_out (None: in place)."""
-    _same_device(k_new, v_new, row_offsets, kv_lens, block_table, k_pages, v_pages, rope_table,
-                 q, q_out)
+    dev = _on_device(k_new, v_new, row_offsets, kv_lens, block_table, k_pages, v_pages, rope_table, q, q_out)
     kv = _paged_kv(k_pages, v_pages, row_offsets, kv_lens, block_table)
-    dt, cols = k_pages.dtype, k_pages.shape[-1]
-    layers = k_pages.shape[0] if k_pages.dim() == 4 else 1
-    if k_new.dim() != k_pages.dim() - 1 or v_new.shape != k_new.shape or \
-            (k_new.dim() == 3 and k_new.shape[0] != layers):
-        raise ValueError("k_new and v_new must be [rows, row], with the pools' layer dimension if any")
+    dt, shape = k_pages.dtype, k_pages.shape
+    cols, layers, sk, sv, sc = shape[-1], 1, 0, 0, 0
+    k1, v1 = k_new, v_new
+    if len(shape) == 4:
+        layers = shape[0]
+        if k_new.dim() != 3 or v_new.shape != k_new.shape or k_new.shape[0] != layers:
+            raise ValueError("k_new and v_new must have the pools' layer dimension")
+        if layers == 0:
+            return
+        sk, sv, sc = k_new.stride(0), v_new.stride(0), k_pages.stride(0)
+        k1, v1 = k_new[0], v_new[0]
+    elif len(shape) != 3 or k_new.dim() != 2 or v_new.dim() != 2:
+        raise ValueError("k_new and v_new must be [rows, row], the pools [n_pages, page_size, row]")
     if cols % head_dim:
         raise ValueError("head_dim must divide the cache rows")
-    n_rows = k_new.shape[-2]
-    ls = (0, 0, 0)
-    if layers > 1:
-        ls = (k_new.stride(0), v_new.stride(0), k_pages.stride(0))
-        if v_pages.stride(0) != ls[2]:
-            raise ValueError("k_pages and v_pages must have the same strides")
-    max_pos = 0
+    n_rows = k1.shape[0]
+    rope = max_pos = 0
     if rope_table is not None:
-        if rope_table.dtype != torch.float32 or not rope_table.is_contiguous():
+        if rope_table.dtype != _F32 or not rope_table.is_contiguous():
             raise ValueError("rope_table must be contiguous float32")
-        max_pos = rope_table.numel() // head_dim
-    ld_q = ld_qo = n_q = 0
+        rope, max_pos = rope_table.data_ptr(), rope_table.numel() // head_dim
+    qp = qop = ld_q = ld_qo = n_q = 0
     if q is not None:
-        q_out = q if q_out is None else q_out
-        if q.dim() != 2 or q.shape[0] != n_rows or q.shape[1] % head_dim or q_out.shape != q.shape:
-            raise ValueError("q and q_out must be [rows, n_q_heads * head_dim]")
-        ld_q, ld_qo, n_q = _rows("q", q, dt), _rows("q_out", q_out, dt), q.shape[1] // head_dim
+        q_cols = q.shape[1]
+        n_q = q_cols // head_dim
+        if q_cols % head_dim:
+            raise ValueError("q must be [rows, n_q_heads * head_dim]")
+        qp, ld_q = q.data_ptr(), _ld("q", q, dt, n_rows, q_cols)
+        qop, ld_qo = (qp, ld_q) if q_out is None else (q_out.data_ptr(), _ld("q_out", q_out, dt, n_rows, q_cols))
     elif q_out is not None:
         raise ValueError("q_out without q")
-    check(lib.cb_paged_append(
-        C.byref(kv), k_new.data_ptr(), _rows("k_new", k_new, dt, cols), ls[0], v_new.data_ptr(),
-        _rows("v_new", v_new, dt, cols), ls[1], n_rows, layers, ls[2], cols // head_dim, head_dim,
-        _p(rope_table), max_pos, _p(q), ld_q, n_q, _p(q_out), ld_qo, dtype_code(dt), _s(stream)))
+    status = lib.cb_paged_append(
+        C.byref(kv), k1.data_ptr(), _ld("k_new", k1, dt, n_rows, cols), sk, v1.data_ptr(),
+        _ld("v_new", v1, dt, n_rows, cols), sv, n_rows, layers, sc, cols // head_dim, head_dim, rope, max_pos,
+        qp, ld_q, n_q, qop, ld_qo, _CODES.get(dt, -1), _cur_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        check(status)
 
 
 def cb_paged_attention_workspace(q, n_seq, max_kv_len, n_q_heads, n_kv_heads, head_dim):
@@ -267,24 +278,23 @@ def cb_paged_attention(q, row_offsets, kv_lens, block_table, k_pages, v_pages, n
     the rows, whose keys are already in the cache).  max_kv_len: an upper
     bound of kv_lens (default: what the table can hold).  ws: from
     cb_paged_attention_workspace (None: allocated here)."""
-    _same_device(q, row_offsets, kv_lens, block_table, k_pages, v_pages, out, ws)
-    if k_pages.dim() != 3:
-        raise ValueError("k_pages and v_pages must be one layer's [n_pages, page_size, row]")
+    dev = _on_device(q, row_offsets, kv_lens, block_table, k_pages, v_pages, out, ws)
     kv = _paged_kv(k_pages, v_pages, row_offsets, kv_lens, block_table)
-    dt, cols = k_pages.dtype, n_q_heads * head_dim
-    if k_pages.shape[2] != n_kv_heads * head_dim:
-        raise ValueError("cache rows must hold n_kv_heads * head_dim elements")
-    if q.dim() != 2 or out.shape != q.shape:
-        raise ValueError("q and out must be [rows, n_q_heads * head_dim]")
+    dt, cols, shape = k_pages.dtype, n_q_heads * head_dim, k_pages.shape
+    if len(shape) != 3 or shape[2] != n_kv_heads * head_dim:
+        raise ValueError("the pools must be one layer's [n_pages, page_size, n_kv_heads * head_dim]")
+    n_rows = q.shape[0]
     if max_kv_len is None:
-        max_kv_len = min(block_table.shape[1] * k_pages.shape[1], 2 ** 31 - 1)
-    scale = 1.0 / math.sqrt(head_dim) if scale is None else scale
+        max_kv_len = min(block_table.shape[1] * shape[1], 2 ** 31 - 1)
     if ws is None:
         ws = cb_paged_attention_workspace(q, kv.n_seq, max_kv_len, n_q_heads, n_kv_heads, head_dim)
-    check(lib.cb_paged_attention(
-        C.byref(kv), q.data_ptr(), _rows("q", q, dt, cols), q.shape[0], max_kv_len, n_q_heads,
-        n_kv_heads, head_dim, float(scale), out.data_ptr(), _rows("out", out, dt, cols),
-        dtype_code(dt), ws.data_ptr(), ws.numel() * ws.element_size(), _s(stream)))
+    status = lib.cb_paged_attention(
+        C.byref(kv), q.data_ptr(), _ld("q", q, dt, n_rows, cols), n_rows, max_kv_len, n_q_heads, n_kv_heads,
+        head_dim, 1.0 / math.sqrt(head_dim) if scale is None else scale, out.data_ptr(),
+        _ld("out", out, dt, n_rows, cols), _CODES.get(dt, -1), ws.data_ptr(), ws.numel() * ws.element_size(),
+        _cur_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        check(status)
 
 
 def cb_sample_tokens(logits, u, tokens, temperature=None, top_k=None, top_p=None, min_p=None,
@@ -292,18 +302,25 @@ def cb_sample_tokens(logits, u, tokens, temperature=None, top_k=None, top_p=None
     """Samples a token per row of logits [rows, vocab] into tokens (device
     int32 [rows]) from the uniform numbers u (float32 [rows]); temperature,
     top_p, min_p: float32 [rows] or None, top_k: int32 [rows] or None."""
-    _same_device(logits, u, tokens, temperature, top_k, top_p, min_p)
-    if logits.dim() != 2:
-        raise ValueError("logits must be [rows, vocab]")
-    n = logits.shape[0]
-    for name, t, dt in (("u", u, torch.float32), ("tokens", tokens, torch.int32),
-                        ("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
-                        ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
-        if t is not None and (t.dtype != dt or t.shape != (n,) or not t.is_contiguous()):
-            raise ValueError(f"{name} must be contiguous {dt} of shape ({n},)")
-    check(lib.cb_sample_tokens(_p(logits), _rows("logits", logits, logits.dtype), n, logits.shape[1],
-                               dtype_code(logits.dtype), _p(u), _p(temperature), _p(top_k),
-                               _p(top_p), _p(min_p), _p(tokens), _s(stream)))
+    dev = _on_device(logits, u, tokens, temperature, top_k, top_p, min_p)
+    n, vocab = logits.shape
+    dt = logits.dtype
+    if dt not in _CODES:
+        raise ValueError(f"unsupported dtype {dt}")
+
+    def per_row(name, t, dtype):
+        if t is None:
+            return 0
+        if t.dtype != dtype or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+            raise ValueError(f"{name} must be contiguous {dtype} of shape ({n},)")
+        return t.data_ptr()
+    status = lib.cb_sample_tokens(
+        logits.data_ptr(), _ld("logits", logits, dt, n, vocab), n, vocab, _CODES[dt], per_row("u", u, _F32),
+        per_row("temperature", temperature, _F32), per_row("top_k", top_k, _I32), per_row("top_p", top_p, _F32),
+        per_row("min_p", min_p, _F32), per_row("tokens", tokens, _I32),
+        _cur_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        check(status)
 
 
 def cb_debug_expire_wait(limit_us: int, stream=None):

@@ -7,6 +7,13 @@
 namespace cb {
 namespace paged {
 
+// An item of the few-rows kernel whose keys more than one block has: its rows
+// (0: nothing to join), the last block with a piece, and whether the first
+// block's piece is its second.
+struct Join {
+  int row0, l0, rows, g, last, second;
+};
+
 struct AttnParams {
   PagedKV kv;
   const void *q;
@@ -17,10 +24,11 @@ struct AttnParams {
   float scale_log2;                       // softmax scale times log2(e)
   float *part_o;                          // unnormalised partial rows, HD floats each
   float2 *part_ml;                        // (m, l) of each partial row
+  Join *joins;                            // one per block of the few-rows kernel
 };
 
-// bf16, few rows per sequence: R (16, 32 or 64) rows per tile.  The partials
-// take 2 * decode_grid() * R rows of the workspace.
+// bf16, few rows per sequence: R (16, 32 or 64) rows per tile.  The workspace
+// holds 2 * decode_grid() * R partial rows and decode_grid() joins.
 int decode_grid();
 cudaError_t launch_decode(const AttnParams &P, int R, int hd, int *status, cudaStream_t s);
 

@@ -312,7 +312,8 @@ static cudaError_t run_all(const AttnParams &P, const Plan &p, int *status, cuda
 size_t paged_attention_ws_bytes(int n_rows, int n_seq, int max_kv, int Hq, int Hkv, int hd, cb_dtype dt) {
   using namespace paged;
   if (n_rows <= 0 || n_seq <= 0) return 0;
-  return (size_t)plan(n_rows, n_seq, max_kv, Hq / Hkv, Hkv, dt).partials * (hd * sizeof(float) + sizeof(float2));
+  const Plan p = plan(n_rows, n_seq, max_kv, Hq / Hkv, Hkv, dt);
+  return (size_t)p.partials * (hd * sizeof(float) + sizeof(float2)) + (p.simt ? 0 : decode_grid() * sizeof(Join));
 }
 
 cudaError_t launch_paged_attention(const PagedKV &kv, const void *q, int64_t ld_q, int n_rows, int max_kv,
@@ -336,6 +337,7 @@ cudaError_t launch_paged_attention(const PagedKV &kv, const void *q, int64_t ld_
   P.scale_log2 = scale * 1.4426950408889634f;
   P.part_o = reinterpret_cast<float *>(ws);
   P.part_ml = reinterpret_cast<float2 *>(P.part_o + (size_t)p.partials * hd);
+  P.joins = reinterpret_cast<Join *>(P.part_ml + p.partials);
   return hd == 128 ? run_all<128>(P, p, status, s) : run_all<64>(P, p, status, s);
 }
 

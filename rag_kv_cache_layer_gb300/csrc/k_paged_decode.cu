@@ -9,7 +9,8 @@
 // lengths decide that on the device, so lengths of any mix keep every SM busy
 // until the end.  An item inside one part is written out directly; one that
 // crosses parts leaves its pieces' (O, m, l) in the workspace, at most two per
-// block, and decode_merge_kernel joins them.
+// block, and decode_merge_kernel joins them; the block with an item's first
+// piece also leaves the join's record, so the joining kernel searches nothing.
 //
 // A block's four warps form WK = 4 / WM groups of WM warps; key block i goes
 // to group i mod WK.  A group fills a ring of its own by 16-byte cp.async,
@@ -99,10 +100,9 @@ __device__ __forceinline__ int part_of(const Line &L, int64_t u) {
 }
 
 // Every thread of the block calls it; one round of loads, one block scan.
-template <int NT>
 __device__ __forceinline__ void make_line(const AttnParams &P, int R, int BN, int grid, Line &L, int64_t *warp_sums,
                                           int *status) {
-  constexpr int kPer = (CB_MAX_SEQS + NT - 1) / NT;
+  constexpr int NT = kDecThreads, kPer = (CB_MAX_SEQS + NT - 1) / NT;
   const int per = (P.kv.n_seq + NT - 1) / NT, i0 = threadIdx.x * per;
   int64_t u[kPer], sum = 0;
 #pragma unroll
@@ -168,8 +168,12 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
   __shared__ float2 s_ml[4 * 16];               // (m, l) of each warp's rows
   grid_dep_wait();
   grid_dep_launch();
-  make_line<kDecThreads>(P, R, BN, gridDim.x, line, s_sums, status);
-  if ((int)blockIdx.x >= line.parts) return;
+  make_line(P, R, BN, gridDim.x, line, s_sums, status);
+  Join *const join = P.joins + blockIdx.x;
+  if ((int)blockIdx.x >= line.parts) {
+    if (threadIdx.x == 0) join->rows = 0;
+    return;
+  }
   const int64_t u0 = part_begin(line, blockIdx.x), u1 = part_begin(line, blockIdx.x + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wm = warp % WM, wk = warp / WM, gid = lane >> 2, q4 = lane & 3;
@@ -192,6 +196,7 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
     const int item = (int)((u - line.begin[s]) / nbs), jb = (int)((u - line.begin[s]) % nbs);
     const int take = (int)min((int64_t)(nbs - jb), u1 - u);
     const bool whole = jb == 0 && take == nbs, first = u == u0;
+    const int64_t item_end = u - jb + nbs;
     u += take;
     const int g = item % P.Hkv, l0 = item / P.Hkv * R;
     const int row0 = __ldg(P.kv.row_offsets + s), n = __ldg(P.kv.row_offsets + s + 1) - row0;
@@ -199,6 +204,8 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
     const int seen = base + (l0 + rows - 1) / P.G + 1;        // keys the tile's last row sees
     const int je = min(jb + take, seen > 0 ? (seen - 1) / BN + 1 : 0);
     const int32_t *table = P.kv.block_table + (int64_t)s * P.kv.ld_table;
+    if (threadIdx.x == 0 && u == u1)            // the last piece: the one that may go on in the next part
+      *join = Join{row0, l0, jb == 0 && item_end > u1 ? rows : 0, g, part_of(line, item_end - 1), first ? 0 : 1};
 
     auto fetch = [&](int j) -> int {            // page of key j * BN + lane
       const int key = j * BN + lane;
@@ -387,54 +394,85 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
   }
 }
 
-// Joins the pieces of every item that crosses parts.  One block per item; a
-// warp takes a row, each lane HD / 32 columns.
-constexpr int kJoinThreads = 128;
+// Joins the pieces of the item whose first piece part blockIdx.x holds, four
+// rows at a time.  The weights are made once in shared memory, so the partial
+// rows' loads depend on nothing: warp w takes every eighth piece, a lane HD /
+// 32 columns, and the warps' sums meet in shared memory.
+constexpr int kJoinThreads = 256, kJoinRows = 4;
 template <int HD>
 __global__ void __launch_bounds__(kJoinThreads)
-decode_merge_kernel(const __grid_constant__ AttnParams P, int R, int BN, int grid, int *status) {
-  constexpr int PER = HD / 32;
-  __shared__ Line line;
-  __shared__ int64_t s_sums[kJoinThreads / 32];
+decode_merge_kernel(const __grid_constant__ AttnParams P, int R) {
+  constexpr int PER = HD / 32, NW = kJoinThreads / 32;
+  extern __shared__ float2 s_ml[];              // [pieces][kJoinRows]: (m, l), then the weight in x
+  __shared__ float s_o[NW][kJoinRows][HD];
+  __shared__ float s_inv[kJoinRows];
   grid_dep_wait();
   grid_dep_launch();
-  make_line<kJoinThreads>(P, R, BN, grid, line, s_sums, status);
-  // block i looks at the i-th part border, and joins the item that crosses it
-  // where this is the first border inside it
-  const int c1 = blockIdx.x + 1;
-  if (c1 >= line.parts) return;
-  const int64_t border = part_begin(line, c1);
-  const int s = seq_of(line, P.kv.n_seq, border);
-  const int nbs = line.blocks[s], item = (int)((border - line.begin[s]) / nbs);
-  const int64_t a = line.begin[s] + (int64_t)item * nbs, b = a + nbs;
-  if (border == a || part_begin(line, c1 - 1) > a) return;   // no item crosses it, or an earlier border is inside
-  const int row0 = __ldg(P.kv.row_offsets + s), n = __ldg(P.kv.row_offsets + s + 1) - row0;
-  const int g = item % P.Hkv, l0 = item / P.Hkv * R, rows = min(R, n * P.G - l0);
-  const int cl = c1 - 1, ch = part_of(line, b - 1);          // first and last part with a piece
-  auto slot = [&](int c) { return (2 * (int64_t)c + (c == cl && part_begin(line, cl) != a ? 1 : 0)) * R; };
-  const int lane = threadIdx.x & 31;
-  for (int r = threadIdx.x >> 5; r < rows; r += kJoinThreads / 32) {
-    float M = -INFINITY;
-    for (int c = cl + lane; c <= ch; c += 32) M = fmaxf(M, P.part_ml[slot(c) + r].x);
-    M = warp_max(M);
-    float l = 0.f, o[PER];
-#pragma unroll
-    for (int e = 0; e < PER; ++e) o[e] = 0.f;
-#pragma unroll 4
-    for (int c = cl; c <= ch; ++c) {
-      const float2 ml = P.part_ml[slot(c) + r];
-      const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);   // no visible key in this piece
-      l += w * ml.y;
-      const float *src = P.part_o + (slot(c) + r) * HD + lane * PER;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) o[e] = fmaf(w, src[e], o[e]);
+  const Join J = P.joins[blockIdx.x];
+  if (J.rows == 0) return;
+  const int first = blockIdx.x, count = J.last - first + 1;
+  // a later part's first slot; this part's first or second
+  auto slot = [&](int c) { return (2 * (int64_t)(first + c) + (c == 0 ? J.second : 0)) * R; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int r0 = 0; r0 < J.rows; r0 += kJoinRows) {
+    for (int i = threadIdx.x; i < count * kJoinRows; i += kJoinThreads) {
+      const int c = i / kJoinRows, r = r0 + i % kJoinRows;
+      s_ml[i] = r < J.rows ? P.part_ml[slot(c) + r] : make_float2(-INFINITY, 0.f);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    bf16 *dst = reinterpret_cast<bf16 *>(P.out) + (int64_t)(row0 + (l0 + r) / P.G) * P.ld_out +
-                (int64_t)(g * P.G + (l0 + r) % P.G) * HD + lane * PER;
+    __syncthreads();
+    if (warp < kJoinRows) {
+      float M = -INFINITY, l = 0.f;
+      for (int c = lane; c < count; c += 32) M = fmaxf(M, s_ml[c * kJoinRows + warp].x);
+      M = warp_max(M);
+      for (int c = lane; c < count; c += 32) {
+        const float2 ml = s_ml[c * kJoinRows + warp];
+        const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);   // no visible key in this piece
+        s_ml[c * kJoinRows + warp].x = w;
+        l += w * ml.y;
+      }
+      l = warp_sum(l);
+      if (lane == 0) s_inv[warp] = l == 0.f ? 0.f : 1.f / l;
+    }
+    __syncthreads();
+    float o[kJoinRows][PER];
 #pragma unroll
-    for (int e = 0; e < PER; e += 2)
-      *reinterpret_cast<uint32_t *>(dst + e) = pack_bf16(o[e] * inv, o[e + 1] * inv);
+    for (int k = 0; k < kJoinRows; ++k)
+#pragma unroll
+      for (int e = 0; e < PER; ++e) o[k][e] = 0.f;
+#pragma unroll 2
+    for (int c = warp; c < count; c += NW) {
+      const float *src = P.part_o + (slot(c) + r0) * HD + lane * PER;
+#pragma unroll
+      for (int k = 0; k < kJoinRows; ++k) {
+        const float w = s_ml[c * kJoinRows + k].x;
+        if (r0 + k < J.rows) {
+          float v[PER];
+          if constexpr (PER == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(src + k * HD);
+          else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(src + k * HD);
+#pragma unroll
+          for (int e = 0; e < PER; ++e) o[k][e] = fmaf(w, v[e], o[k][e]);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kJoinRows; ++k)
+#pragma unroll
+      for (int e = 0; e < PER; ++e) s_o[warp][k][lane * PER + e] = o[k][e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < kJoinRows * HD / 2; i += kJoinThreads) {
+      const int k = i / (HD / 2), c = i % (HD / 2) * 2, l = J.l0 + r0 + k;
+      float a = 0.f, b = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        a += s_o[w][k][c];
+        b += s_o[w][k][c + 1];
+      }
+      if (r0 + k < J.rows)
+        *reinterpret_cast<uint32_t *>(reinterpret_cast<bf16 *>(P.out) + (int64_t)(J.row0 + l / P.G) * P.ld_out +
+                                      (int64_t)(J.g * P.G + l % P.G) * HD + c) =
+            pack_bf16(a * s_inv[k], b * s_inv[k]);
+    }
+    __syncthreads();
   }
 }
 
@@ -448,10 +486,11 @@ static cudaError_t run(const AttnParams &P, int *status, cudaStream_t s) {
     return cudaFuncSetAttribute(paged_decode_kernel<HD, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   if (e != cudaSuccess) return e;
-  const int grid = decode_grid();
+  const int grid = decode_grid();               // 32 bytes of weights for each: within the default limit
   e = launch_pdl(paged_decode_kernel<HD, WM>, dim3(grid), dim3(kDecThreads), C::kSmem, s, P, status);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(decode_merge_kernel<HD>, dim3(grid), dim3(kJoinThreads), 0, s, P, 16 * WM, C::kBN, grid, status);
+  e = launch_pdl(decode_merge_kernel<HD>, dim3(grid), dim3(kJoinThreads), grid * kJoinRows * sizeof(float2), s, P,
+                 16 * WM);
   return e == cudaSuccess ? launched(2) : e;
 }
 
