@@ -809,7 +809,7 @@ cb_status cb_paged_append(const cb_paged_kv *kv, const void *k_new, int64_t ld_k
  * ordered on one stream).
  * Errors: CB_ERR_INVALID_ARG (NULL or misaligned pointers, strides, head
  * counts not dividing or more than 128 q heads per kv head, head_dim not 64
- * or 128), CB_ERR_UNSUPPORTED (page_size, or a row count whose tiles exceed a
+ * or 128, a negative or infinite scale), CB_ERR_UNSUPPORTED (page_size, or a row count whose tiles exceed a
  * launch), CB_ERR_WORKSPACE.  On the device, offsets that do not ascend
  * inside [0, n_rows], a length outside [0, max_kv_len] or past the table, and
  * a page outside the pool record CB_ERR_DEVICE_INDEX; with a bad offset or

@@ -34,6 +34,7 @@ SOURCES = [
     "k_paged_append.cu",
     "k_paged_attn.cu",
     "k_paged_decode.cu",
+    "k_paged_chunk.cu",
     "k_sample.cu",
 ]
 

@@ -46,7 +46,9 @@ __device__ __forceinline__ int paged_rows(const PagedKV &kv, int i, int n_rows, 
   return b - a;
 }
 
-// Finds the tile-th tile of R rows over all sequences.  Every thread of the
+// Finds the tile-th tile of R rows over the sequences with more than rows_lo
+// rows (queries x G); a sequence's last tile, which sees the most keys, comes
+// first.  Every thread of the
 // block calls it (NT threads, NT a multiple of 32); on return `out` (shared
 // memory) holds the tile, out->s = -1 when there are fewer tiles or the
 // sequence's length does not fit the table or max_kv (recorded; its rows are
@@ -54,7 +56,7 @@ __device__ __forceinline__ int paged_rows(const PagedKV &kv, int i, int n_rows, 
 template <int NT>
 __device__ __forceinline__ void paged_find_tile(const PagedKV &kv, int n_rows, int G, int R,
                                                 int max_kv, int tile, PagedTile *out,
-                                                int *warp_sums, int *status) {
+                                                int *warp_sums, int *status, int rows_lo = 0) {
   constexpr int kPer = (CB_MAX_SEQS + NT - 1) / NT;
   const int per = (kv.n_seq + NT - 1) / NT;
   const int i0 = threadIdx.x * per;
@@ -65,7 +67,7 @@ __device__ __forceinline__ void paged_find_tile(const PagedKV &kv, int n_rows, i
     cnt[k] = 0;
     if (k < per && i0 + k < kv.n_seq) {
       const int64_t rows = (int64_t)paged_rows(kv, i0 + k, n_rows, status) * G;
-      cnt[k] = (int)((rows + R - 1) / R);
+      cnt[k] = rows > rows_lo ? (int)((rows + R - 1) / R) : 0;
     }
     sum += cnt[k];
   }
@@ -90,7 +92,7 @@ __device__ __forceinline__ void paged_find_tile(const PagedKV &kv, int n_rows, i
           report(status, CB_ERR_DEVICE_INDEX);
         } else {
           const int a = __ldg(kv.row_offsets + s);
-          *out = PagedTile{s, tile - first, a, __ldg(kv.row_offsets + s + 1) - a, len};
+          *out = PagedTile{s, cnt[k] - 1 - (tile - first), a, __ldg(kv.row_offsets + s + 1) - a, len};
         }
       }
       first += cnt[k];

@@ -1,5 +1,6 @@
 // Entry points of the generation operators: argument checks of the paged
 // append, the paged attention and the token sampling.
+#include <math.h>
 #include <stdio.h>
 
 #include "cb_common.cuh"
@@ -107,6 +108,7 @@ extern "C" cb_status cb_paged_attention(const cb_paged_kv *kv, const void *q, in
     return bad("n_q_heads must be 1 to 128 times n_kv_heads, head_dim 64 or 128");
   if (const cb_status s = check_paged(kv, (int64_t)n_kv_heads * head_dim, dtype)) return s;
   if (n_rows < 0 || max_kv_len < 0) return bad("n_rows < 0 or max_kv_len < 0");
+  if (!(scale >= 0.f) || isinf(scale)) return bad("scale must be finite and >= 0");
   if (n_rows == 0 || kv->n_seq == 0) return CB_OK;
   const size_t eb = bytes_of(dtype);
   const int64_t cols = (int64_t)n_q_heads * head_dim;

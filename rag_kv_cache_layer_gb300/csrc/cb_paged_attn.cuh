@@ -20,7 +20,10 @@ struct AttnParams {
   void *out;
   int64_t ld_q, ld_out;
   int n_rows, G, Hkv, max_kv;
-  int n_split;                            // parts of a tile's key range (fp32 kernel)
+  int n_split;                            // parts of a tile's key range (chunk and fp32 kernels)
+  // Sequences by rows (queries x G): the few-rows kernel takes those up to
+  // few_hi, the chunk kernel those above rows_lo.
+  int few_hi, rows_lo;
   float scale_log2;                       // softmax scale times log2(e)
   float *part_o;                          // unnormalised partial rows, HD floats each
   float2 *part_ml;                        // (m, l) of each partial row
@@ -31,6 +34,11 @@ struct AttnParams {
 // holds 2 * decode_grid() * R partial rows and decode_grid() joins.
 int decode_grid();
 cudaError_t launch_decode(const AttnParams &P, int R, int hd, int *status, cudaStream_t s);
+
+// bf16, many rows: tiles of 128 rows, their keys in n_split parts; the
+// workspace holds tiles * Hkv * n_split * 128 partial rows if n_split > 1.
+int chunk_slots();
+cudaError_t launch_chunk(const AttnParams &P, int64_t tiles, int hd, int *status, cudaStream_t s);
 
 }  // namespace paged
 }  // namespace cb

@@ -203,17 +203,16 @@ paged_simt_kernel(const __grid_constant__ AttnParams P, int *status) {
 // O = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c, in split order.  A warp
 // takes a row, each lane HD / 32 columns.
 constexpr int kMergeThreads = 256;
-template <int HD>
+template <typename T, int HD>
 __global__ void __launch_bounds__(kMergeThreads)
 paged_merge_kernel(const __grid_constant__ AttnParams P, int R, int *status) {
-  typedef float T;
   constexpr int PER = HD / 32;
   __shared__ PagedTile s_tile;
   __shared__ int s_sums[kMergeThreads / 32];
   grid_dep_wait();
   grid_dep_launch();
   const int g = blockIdx.x % P.Hkv, tile = blockIdx.x / P.Hkv;
-  paged_find_tile<kMergeThreads>(P.kv, P.n_rows, P.G, R, P.max_kv, tile, &s_tile, s_sums, status);
+  paged_find_tile<kMergeThreads>(P.kv, P.n_rows, P.G, R, P.max_kv, tile, &s_tile, s_sums, status, P.rows_lo);
   const PagedTile tl = s_tile;
   if (tl.s < 0) return;
   const int lane = threadIdx.x & 31;
@@ -251,38 +250,61 @@ static int64_t tile_bound(int64_t n_rows, int S, int G, int R) {
   return a < b ? a : b;
 }
 
-// How a call runs: rows per tile and, in fp32, the tiles at most and the
-// parts of their key ranges.
+// How a call runs.
 struct Plan {
-  bool simt;                              // fp32 on the CUDA cores
-  int R;
-  int64_t tiles;
-  int n_split;
-  int64_t partials;                       // partial rows the workspace holds
+  int few_R;                              // bf16, few rows: rows per tile, 0: none
+  int R;                                  // chunk (128) or fp32 tiles (16, 64): rows, 0: none
+  int few_hi, rows_lo;                    // which sequences each takes
+  int64_t tiles;                          // R-row tiles at most
+  int n_split;                            // parts of their key ranges
+  int64_t few_partials, partials;         // partial rows in the workspace (reused)
 };
 
+// bf16: sequences of up to 64 rows (queries x G) go through the few-rows
+// kernel, longer ones through the chunk kernel.  Both are launched when the
+// sizes leave it open; a call whose rows do not exceed its sequences is taken
+// for one generated token each and runs the few-rows kernel alone (which
+// takes any number of rows), a single sequence runs the one its rows call
+// for.  The few-rows tile is 16, 32 or 64 rows by the average sequence.
 // fp32: 16-row tiles where a sequence brings few rows (the wider tile would
-// mostly multiply zeros), else 64; key ranges are split until about two waves
-// of blocks run, in parts of at least two 64-key blocks.
-// bf16: tiles of 16, 32 or 64 rows by the average sequence's rows.
+// mostly multiply zeros), else 64.
+// Key ranges of chunk and fp32 tiles are split while the tiles alone leave
+// SMs idle, in parts of at least 512 (chunk) or 128 keys: a part's fixed cost
+// is worth several blocks of its loop.
 static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, cb_dtype dt) {
-  Plan p;
-  const int64_t per_seq = (n_rows * G + S - 1) / S;
-  p.simt = dt != CB_BF16;
-  p.tiles = p.n_split = 1;
-  if (!p.simt) {
-    p.R = per_seq <= 16 ? 16 : per_seq <= 32 ? 32 : 64;
-    p.partials = 2LL * decode_grid() * p.R;
-    return p;
+  Plan p = {};
+  const int64_t all = n_rows * G, per_seq = (all + S - 1) / S;
+  int64_t slots, least;
+  p.few_hi = 0x7fffffff;
+  p.n_split = 1;
+  if (dt == CB_BF16) {
+    const bool few = all <= 64 || n_rows <= S;
+    if (few || S > 1) p.few_R = per_seq <= 16 || per_seq > 64 ? 16 : per_seq <= 32 ? 32 : 64;
+    p.few_partials = p.few_R ? 2LL * decode_grid() * p.few_R : 0;
+    if (few) return p;
+    p.R = 128;
+    if (S > 1) p.few_hi = p.rows_lo = 64;
+    slots = chunk_slots();
+    least = 512;
+  } else {
+    p.R = per_seq <= 16 ? 16 : 64;
+    slots = 4LL * device_sm_count();
+    least = 128;
   }
-  p.R = per_seq <= 16 ? 16 : 64;
   p.tiles = tile_bound(n_rows, S, G, p.R);
   const int64_t units = p.tiles * Hkv > 0 ? p.tiles * Hkv : 1;
-  const int64_t want = (4LL * device_sm_count() + units - 1) / units, most = (max_kv + 127) / 128;
+  const int64_t want = slots / units, most = (max_kv + least - 1) / least;
   const int64_t n = want < most ? want : most;
   p.n_split = n < 1 ? 1 : n > 64 ? 64 : (int)n;
   p.partials = p.n_split == 1 ? 0 : p.tiles * Hkv * p.n_split * p.R;
   return p;
+}
+
+static size_t plan_bytes(const Plan &p, int hd) {
+  const size_t row = hd * sizeof(float) + sizeof(float2);
+  const size_t few = (size_t)p.few_partials * row + (p.few_R ? decode_grid() * sizeof(Join) : 0);
+  const size_t rest = (size_t)p.partials * row;
+  return few > rest ? few : rest;
 }
 
 template <int R, int HD>
@@ -295,16 +317,34 @@ static cudaError_t run_simt(const AttnParams &P, const Plan &p, int *status, cud
   if (e != cudaSuccess) return e;
   e = launch_pdl(paged_simt_kernel<R, HD>, dim3((unsigned)(p.tiles * P.Hkv * P.n_split)),
                  dim3(kSimtThreads), simt_smem<R, HD>(), s, P, status);
-  if (e != cudaSuccess) return e;
-  if (P.n_split == 1) return launched(1);
-  e = launch_pdl(paged_merge_kernel<HD>, dim3((unsigned)(p.tiles * P.Hkv)), dim3(kMergeThreads), 0, s, P, R, status);
-  return e == cudaSuccess ? launched(2) : e;
+  return e == cudaSuccess ? launched(1) : e;
 }
 
+// The partials of a launch reuse the workspace of the launch before it: each
+// waits for its predecessor's end, and a merge has read them by then.
 template <int HD>
-static cudaError_t run_all(const AttnParams &P, const Plan &p, int *status, cudaStream_t s) {
-  if (!p.simt) return launch_decode(P, p.R, HD, status, s);
-  return p.R == 16 ? run_simt<16, HD>(P, p, status, s) : run_simt<64, HD>(P, p, status, s);
+static cudaError_t run_all(AttnParams P, const Plan &p, cb_dtype dt, void *ws, int *status, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  auto bind = [&](int64_t partials) {
+    P.part_o = reinterpret_cast<float *>(ws);
+    P.part_ml = reinterpret_cast<float2 *>(P.part_o + (size_t)partials * HD);
+    P.joins = reinterpret_cast<Join *>(P.part_ml + partials);
+  };
+  if (p.few_R) {
+    bind(p.few_partials);
+    e = launch_decode(P, p.few_R, HD, status, s);
+    if (e != cudaSuccess) return e;
+  }
+  if (!p.R) return e;
+  bind(p.partials);
+  e = p.R == 128  ? launch_chunk(P, p.tiles, HD, status, s)
+      : p.R == 16 ? run_simt<16, HD>(P, p, status, s)
+                  : run_simt<64, HD>(P, p, status, s);
+  if (e != cudaSuccess || p.n_split == 1) return e;
+  const dim3 grid((unsigned)(p.tiles * P.Hkv));
+  e = dt == CB_BF16 ? launch_pdl(paged_merge_kernel<bf16, HD>, grid, dim3(kMergeThreads), 0, s, P, p.R, status)
+                    : launch_pdl(paged_merge_kernel<float, HD>, grid, dim3(kMergeThreads), 0, s, P, p.R, status);
+  return e == cudaSuccess ? launched(1) : e;
 }
 
 }  // namespace paged
@@ -312,8 +352,7 @@ static cudaError_t run_all(const AttnParams &P, const Plan &p, int *status, cuda
 size_t paged_attention_ws_bytes(int n_rows, int n_seq, int max_kv, int Hq, int Hkv, int hd, cb_dtype dt) {
   using namespace paged;
   if (n_rows <= 0 || n_seq <= 0) return 0;
-  const Plan p = plan(n_rows, n_seq, max_kv, Hq / Hkv, Hkv, dt);
-  return (size_t)p.partials * (hd * sizeof(float) + sizeof(float2)) + (p.simt ? 0 : decode_grid() * sizeof(Join));
+  return plan_bytes(plan(n_rows, n_seq, max_kv, Hq / Hkv, Hkv, dt), hd);
 }
 
 cudaError_t launch_paged_attention(const PagedKV &kv, const void *q, int64_t ld_q, int n_rows, int max_kv,
@@ -334,11 +373,10 @@ cudaError_t launch_paged_attention(const PagedKV &kv, const void *q, int64_t ld_
   P.Hkv = Hkv;
   P.max_kv = max_kv;
   P.n_split = p.n_split;
+  P.few_hi = p.few_hi;
+  P.rows_lo = p.rows_lo;
   P.scale_log2 = scale * 1.4426950408889634f;
-  P.part_o = reinterpret_cast<float *>(ws);
-  P.part_ml = reinterpret_cast<float2 *>(P.part_o + (size_t)p.partials * hd);
-  P.joins = reinterpret_cast<Join *>(P.part_ml + p.partials);
-  return hd == 128 ? run_all<128>(P, p, status, s) : run_all<64>(P, p, status, s);
+  return hd == 128 ? run_all<128>(P, p, dt, ws, status, s) : run_all<64>(P, p, dt, ws, status, s);
 }
 
 }  // namespace cb

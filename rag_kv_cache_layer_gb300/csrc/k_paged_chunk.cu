@@ -1,0 +1,406 @@
+// bf16 paged attention of many rows per sequence on the tensor cores
+// (tcgen05): chunks of a prompt over what the cache holds.
+//
+// Work unit: 128 rows of one sequence and kv head (row l is query l / G, head
+// l % G of the group, so any group size fills the tile) and, where the tiles
+// alone do not fill the SMs, a part of their key range.  Tiles of a sequence
+// are taken last first: they see the most keys.
+//
+// Roles (224 threads, two CTAs per SM): warps 0 and 6 fill the double-buffered
+// 64-key K and V blocks; warp 1 owns 256 TMEM columns and issues tcgen05.mma:
+// S_j = Q K_j^T into slot j & 1 (columns 0..63 or 64..127) and O += P_j V_j
+// into columns 128.., P_j read from TMEM where it overwrites S_j; warps 2..5
+// load Q, then do the online softmax, one row per thread, in the log2 domain
+// and store P_j as packed bf16.  With two S slots S_{j+1} is computed while
+// the softmax works on S_j, and the SM's other CTA fills the remaining
+// tensor-core time.  The row's reference maximum m only moves when a block
+// raises it by more than 2^kRescale: then O (after P_{j-1} V_{j-1} has landed)
+// and l are scaled by 2^(m_old - m_new); O / l does not depend on m.
+//
+// Keys and values come by 16-byte cp.async to their swizzled places, each
+// eight rows of one page together, with zeros for keys past the cached length
+// (an unwritten slot may hold NaN, and 0 * NaN would reach O).  A TMA box
+// would be a page's rows: at 16 slots a page sixteen boxes per block, about
+// 90 ns each, twice what the block's arithmetic takes.
+//
+// Parts of a split key range leave (O, m, l) in fp32 for paged_merge_kernel.
+// All waits are bounded.
+#include "cb_attn_tc.cuh"
+#include "cb_common.cuh"
+#include "cb_internal.h"
+#include "cb_paged.cuh"
+#include "cb_paged_attn.cuh"
+
+namespace cb {
+namespace paged {
+
+using namespace attn;
+
+constexpr int kChThreads = 224;
+constexpr int kChRows = 128;
+constexpr int kChBN = 64;                 // keys per block
+constexpr float kChRescale = 8.f;         // log2 of the largest p between rescales
+constexpr int kChPerSm = 2;
+constexpr int kChTmem = 256;              // S/P slots 0..63, 64..127; O from 128
+
+template <int HD> struct ChCfg {
+  static constexpr int kAtom = kChRows * 128;        // [128 rows x 64 dims], 128-byte swizzle
+  static constexpr int kAtomKV = kChBN * 128;        // [64 keys x 64 dims]
+  static constexpr int kQ = kAtom * (HD / 64), kKV = kAtomKV * (HD / 64);
+  static constexpr int kOffK = kQ, kOffV = kOffK + 2 * kKV, kOffBar = kOffV + 2 * kKV;
+  static constexpr int kSmem = kOffBar + 256 + 1024;
+};
+
+// Fills one K or V stage: 64 keys of one head.  Lane = (row of 32 / cols,
+// 16-byte column); eight consecutive keys share a page (page_size >= 8).
+template <int HD>
+__device__ __forceinline__ void chunk_load(uint32_t dst, const bf16 *pool, const PagedKV &kv, int key0, int n_keys,
+                                           int page_lo, int page_hi, int lane) {
+  constexpr int kCols = HD / 8, kRows = 32 / kCols;
+  const int crow = lane / kCols, col = lane % kCols;
+  const uint32_t half = dst + (col >> 3) * (kChBN * 128);
+#pragma unroll
+  for (int g8 = 0; g8 < kChBN / 8; ++g8) {
+    const int page = __shfl_sync(0xffffffffu, g8 < 4 ? page_lo : page_hi, (g8 & 3) * 8);
+    const int slot = (key0 + g8 * 8) & (kv.page_size - 1);
+    const bf16 *src = pool + (page < 0 ? 0 : (int64_t)page * kv.page_stride + (int64_t)(slot + crow) * kv.ld) + col * 8;
+    const int64_t step = page < 0 ? 0 : (int64_t)kRows * kv.ld;
+#pragma unroll
+    for (int i = 0; i < 8 / kRows; ++i) {
+      const int r = g8 * 8 + i * kRows + crow;
+      const bool there = page >= 0 && r < n_keys;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(half + r * 128 + (((col ^ r) & 7) << 4)),
+                   "l"(src), "r"(there ? 16 : 0)
+                   : "memory");
+      src += step;
+    }
+  }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kChThreads, kChPerSm)
+paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
+  typedef ChCfg<HD> C;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
+  uint64_t *q_full = bar + 0;
+  uint64_t *k_full = bar + 1;      // [2] K_j landed
+  uint64_t *k_empty = bar + 3;     // [2] S_j = Q K_j^T done with K_j
+  uint64_t *v_full = bar + 5;      // [2] V_j landed
+  uint64_t *v_empty = bar + 7;     // [2] P_j V_j done with V_j
+  uint64_t *s_full = bar + 9;      // [2] S_j in its TMEM slot
+  uint64_t *p_full = bar + 11;     // [2] P_j in the slot (and O rescaled)
+  uint64_t *pv_done = bar + 13;    // [2] O += P_j V_j has landed
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 15);
+  volatile int *fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  __shared__ PagedTile s_tile;
+  __shared__ int s_sums[kChThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(q_full), 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&k_full[i]), 32);
+      mbar_init(smem_u32(&k_empty[i]), 1);
+      mbar_init(smem_u32(&v_full[i]), 32);
+      mbar_init(smem_u32(&v_empty[i]), 1);
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&p_full[i]), 128);
+      mbar_init(smem_u32(&pv_done[i]), 1);
+    }
+    *fail = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+  const int split = blockIdx.x % P.n_split, g = blockIdx.x / P.n_split % P.Hkv;
+  const int tile = blockIdx.x / P.n_split / P.Hkv;
+  paged_find_tile<kChThreads>(P.kv, P.n_rows, P.G, kChRows, P.max_kv, tile, &s_tile, s_sums, status, P.rows_lo);
+  const PagedTile tl = s_tile;
+  if (tl.s < 0) return;
+  const int l0 = tl.t * kChRows, rows = min(kChRows, tl.n * P.G - l0);
+  const int base = tl.kv - tl.n;
+  const int last = base + (l0 + rows - 1) / P.G;
+  const int nb_tile = last < 0 ? 0 : last / kChBN + 1;
+  const int jb = (int)((int64_t)nb_tile * split / P.n_split);
+  const int nb = (int)((int64_t)nb_tile * (split + 1) / P.n_split) - jb;
+  const int64_t slot0 = ((int64_t)(tile * P.Hkv + g) * P.n_split + split) * kChRows;
+  if (nb == 0) {
+    // no key of this part is seen: an empty partial, or rows of zeros
+    if ((int)threadIdx.x < rows) {
+      if (P.n_split > 1) {
+        P.part_ml[slot0 + threadIdx.x] = make_float2(-INFINITY, 0.f);
+      } else {
+        const int l = l0 + threadIdx.x;
+        uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<bf16 *>(P.out) +
+                                               (int64_t)(tl.row0 + l / P.G) * P.ld_out +
+                                               (int64_t)(g * P.G + l % P.G) * HD);
+        for (int c = 0; c < HD / 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
+      }
+    }
+    return;
+  }
+  if (warp == 1) tcx::tmem_alloc(smem_u32(tmem_slot), kChTmem);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto proxy_fence = [] { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); };
+
+  if (warp == 0 || warp == 6) {
+    // ------------------------------------- producers (K: warp 0, V: warp 6)
+    const bool is_v = warp == 6;
+    uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
+    const bf16 *pool = reinterpret_cast<const bf16 *>(is_v ? P.kv.v_pages : P.kv.k_pages) + (int64_t)g * HD;
+    const uint32_t dst = smem_u32(smem + (is_v ? C::kOffV : C::kOffK));
+    const int32_t *table = P.kv.block_table + (int64_t)tl.s * P.kv.ld_table;
+    const int shift = __ffs(P.kv.page_size) - 1;
+    auto fetch = [&](int key) -> int {           // the page of a key, -1: none
+      return key < tl.kv ? __ldg(table + (key >> shift)) : -1;
+    };
+    auto checked = [&](int page, int key) -> int {
+      if (page >= 0 && page < P.kv.n_pages) return page;
+      if (key < tl.kv) report(status, CB_ERR_DEVICE_INDEX);
+      return -1;
+    };
+    int lo = fetch(jb * kChBN + lane), hi = fetch(jb * kChBN + 32 + lane);
+    for (int j = 0; j < nb; ++j) {
+      const int sl = j & 1, key0 = (jb + j) * kChBN;
+      const bool ok = mbar_wait_bounded(smem_u32(&empty[sl]), ((j >> 1) & 1) ^ 1, kWaitLimitNs, status);
+      if (__any_sync(0xffffffffu, !ok || *fail)) {
+        *fail = 1;
+        break;
+      }
+      lo = checked(lo, key0 + lane);
+      hi = checked(hi, key0 + 32 + lane);
+      chunk_load<HD>(dst + sl * C::kKV, pool, P.kv, key0, tl.kv - key0, lo, hi, lane);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      lo = fetch(key0 + kChBN + lane);
+      hi = fetch(key0 + kChBN + 32 + lane);
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      proxy_fence();                             // this lane's bytes, to the tensor core
+      arrive(smem_u32(&full[sl]));
+    }
+  } else if (warp == 1) {
+    // ----------------------------------------------------------------- MMA
+    const uint32_t idS = idesc(false, kChBN), idPV = idesc(true, HD);
+    const uint32_t q_addr = smem_u32(smem);
+    auto wait_all = [&](uint64_t *b, uint32_t ph) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(b), ph, kWaitLimitNs, status));
+    };
+    bool ok = wait_all(q_full, 0);
+    // S_j into slot j & 1; the slot held P_{j-2}, so P_{j-2} V_{j-2} must be done
+    auto issue_s = [&](int j) -> bool {
+      const int sl = j & 1;
+      const uint32_t ph = (j >> 1) & 1;
+      if (!wait_all(&k_full[sl], ph)) return false;
+      if (j >= 2 && !wait_all(&pv_done[sl], ph ^ 1)) return false;
+      fence_after();
+      if (tcx::elect_one()) {
+        const uint32_t k_addr = smem_u32(smem + C::kOffK + sl * C::kKV);
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k) {
+          const uint32_t qo = (k >> 2) * C::kAtom + (k & 3) * 32;
+          const uint32_t ko = (k >> 2) * C::kAtomKV + (k & 3) * 32;
+          mma(tmem + sl * kChBN, desc_kmajor(q_addr + qo), desc_kmajor(k_addr + ko), idS, k > 0);
+        }
+        commit(smem_u32(&s_full[sl]));
+        commit(smem_u32(&k_empty[sl]));
+      }
+      __syncwarp();
+      return true;
+    };
+    if (ok) ok = issue_s(0);
+    for (int j = 0; j < nb && ok; ++j) {
+      if (__any_sync(0xffffffffu, *fail != 0)) break;
+      const int sl = j & 1;
+      const uint32_t ph = (j >> 1) & 1;
+      if (j + 1 < nb && !issue_s(j + 1)) { ok = false; break; }
+      if (!wait_all(&p_full[sl], ph) || !wait_all(&v_full[sl], ph)) {
+        ok = false;
+        break;
+      }
+      fence_after();
+      if (tcx::elect_one()) {
+        const uint32_t v_addr = smem_u32(smem + C::kOffV + sl * C::kKV);
+#pragma unroll
+        for (int k = 0; k < kChBN / 16; ++k)
+          mma_ts(tmem + 2 * kChBN, tmem + sl * kChBN + k * 8, desc_mnmajor(v_addr + k * 16 * 128, C::kAtomKV), idPV,
+                 (j > 0 || k > 0) ? 1u : 0u);
+        commit(smem_u32(&pv_done[sl]));
+        commit(smem_u32(&v_empty[sl]));
+      }
+      __syncwarp();
+    }
+    if (!ok && lane == 0) *fail = 1;
+  } else {
+    // ------------------------------------------------------ Q, then softmax
+    {
+      constexpr int kCols = HD / 8;
+      const bf16 *q = reinterpret_cast<const bf16 *>(P.q) + (int64_t)g * P.G * HD;
+      const int t = threadIdx.x - 64;
+#pragma unroll 4
+      for (int i = t; i < kChRows * kCols; i += 128) {
+        const int r = i / kCols, col = i % kCols, l = l0 + r;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < rows)
+          v = *reinterpret_cast<const uint4 *>(q + (int64_t)(tl.row0 + l / P.G) * P.ld_q + (int64_t)(l % P.G) * HD +
+                                               col * 8);
+        *reinterpret_cast<uint4 *>(smem + (col >> 3) * C::kAtom + r * 128 + (((col ^ r) & 7) << 4)) = v;
+      }
+      proxy_fence();
+      arrive(smem_u32(q_full));
+    }
+    const int quad = warp & 3;
+    const int row = quad * 32 + lane;            // MMA row
+    const bool valid = row < rows;
+    const int p = valid ? base + (l0 + row) / P.G : -1;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t obase = tmem + lane_off + 2 * kChBN;
+    float m = -INFINITY, l = 0.f;                // reference max (log2 domain), sum
+    const float sl2 = P.scale_log2;
+    bool failed = false;
+    auto pv_landed = [&](int j) -> bool {
+      const bool bad = !mbar_wait_bounded(smem_u32(&pv_done[j & 1]), (j >> 1) & 1, kWaitLimitNs, status) || *fail;
+      if (__any_sync(0xffffffffu, bad)) return false;
+      fence_after();
+      return true;
+    };
+    for (int j = 0; j < nb; ++j) {
+      const int sl = j & 1;
+      const uint32_t ph = (j >> 1) & 1;
+      const bool bad = !mbar_wait_bounded(smem_u32(&s_full[sl]), ph, kWaitLimitNs, status) || *fail;
+      if (__any_sync(0xffffffffu, bad)) { failed = true; break; }
+      fence_after();
+      const uint32_t sbase = tmem + lane_off + sl * kChBN;
+      const int key0 = (jb + j) * kChBN;
+      const int n_vis = p - key0 + 1;            // keys of the block this row sees; >= 64: no masking
+      float x[kChBN];
+      ld32_nw(sbase, x);
+      ld32_nw(sbase + 32, x + 32);
+      wait_ld();
+      float mx[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx[i] = -INFINITY;
+      if (n_vis >= kChBN) {
+#pragma unroll
+        for (int i = 0; i < kChBN; i += 8) {
+          mx[0] = max3(mx[0], x[i], x[i + 1]);
+          mx[1] = max3(mx[1], x[i + 2], x[i + 3]);
+          mx[2] = max3(mx[2], x[i + 4], x[i + 5]);
+          mx[3] = max3(mx[3], x[i + 6], x[i + 7]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kChBN; ++i)
+          if (i < n_vis) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
+      }
+      const float mloc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+      // move the reference only for a large rise; the first visible key
+      // always sets it (m = -inf before)
+      const bool move = mloc > m + kChRescale;
+      const bool rescale = move && m != -INFINITY;   // O and l hold earlier blocks
+      if (__any_sync(0xffffffffu, rescale) && j > 0) {
+        // O must hold P_{j-1} V_{j-1} first; rows that keep m scale by 1
+        if (!pv_landed(j - 1)) { failed = true; break; }
+        const float corr = rescale ? fast_exp2(m - mloc) : 1.f;
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 32) {
+          float y[32];
+          ld32(obase + c, y);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] *= corr;
+          st32(obase + c, y);
+        }
+        l *= corr;
+      }
+      if (move) m = mloc;
+      // P_j for keys c..c+31 -> slot columns c/2 .. c/2+15 (S_j is in
+      // registers); the scale-and-shift and the sums run on packed pairs
+      const unsigned long long s2 = pack2(sl2, sl2), nm2 = pack2(-m, -m);
+      unsigned long long ls2[2] = {0ull, 0ull};
+#pragma unroll
+      for (int c = 0; c < kChBN; c += 32) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const unsigned long long a = fma2(pack2(x[c + i], x[c + i + 1]), s2, nm2);
+          float p0 = fast_exp2(lo2(a));
+          float p1 = fast_exp2(hi2(a));
+          if (n_vis < kChBN) {
+            p0 = c + i < n_vis ? p0 : 0.f;
+            p1 = c + i + 1 < n_vis ? p1 : 0.f;
+          }
+          ls2[(i >> 1) & 1] = add2(ls2[(i >> 1) & 1], pack2(p0, p1));
+          __nv_bfloat162 v2 = __floats2bfloat162_rn(p0, p1);
+          pk[i / 2] = *reinterpret_cast<uint32_t *>(&v2);
+        }
+        st16(sbase + c / 2, pk);
+      }
+      wait_st();
+      l += (lo2(ls2[0]) + hi2(ls2[0])) + (lo2(ls2[1]) + hi2(ls2[1]));
+      fence_before();
+      arrive(smem_u32(&p_full[sl]));
+    }
+    // the whole key range is in O once the last P V has landed
+    if (!failed && !pv_landed(nb - 1)) failed = true;
+    if (failed) *fail = 1;
+    const bool ok = !failed && !*fail;
+    if (__any_sync(0xffffffffu, ok)) {
+      const int lr = l0 + row;
+      const float inv = l == 0.f ? 0.f : 1.f / l;    // no visible key: zeros
+      bf16 *out = reinterpret_cast<bf16 *>(P.out) + (int64_t)(tl.row0 + lr / P.G) * P.ld_out +
+                  (int64_t)(g * P.G + lr % P.G) * HD;
+      float *part = P.part_o + (slot0 + row) * HD;
+#pragma unroll 1
+      for (int c = 0; c < HD; c += 32) {
+        float o[32];
+        ld32(obase + c, o);
+        if (!(valid && ok)) continue;
+        if (P.n_split > 1) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4 *>(part + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          continue;
+        }
+#pragma unroll
+        for (int c8 = 0; c8 < 32; c8 += 8) {
+          uint4 pk;
+          __nv_bfloat162 *e = reinterpret_cast<__nv_bfloat162 *>(&pk);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            e[i] = __floats2bfloat162_rn(o[c8 + 2 * i] * inv, o[c8 + 2 * i + 1] * inv);
+          *reinterpret_cast<uint4 *>(out + c + c8) = pk;
+        }
+      }
+      if (valid && ok && P.n_split > 1) P.part_ml[slot0 + row] = make_float2(m, l);
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after();
+    tcx::tmem_dealloc(tmem, kChTmem);
+  }
+}
+
+int chunk_slots() { return kChPerSm * device_sm_count(); }
+
+template <int HD>
+static cudaError_t run(const AttnParams &P, int64_t tiles, int *status, cudaStream_t s) {
+  static PerDeviceOnce attr;
+  cudaError_t e = attr.run([](int) {
+    return cudaFuncSetAttribute(paged_chunk_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, ChCfg<HD>::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(paged_chunk_kernel<HD>, dim3((unsigned)(tiles * P.Hkv * P.n_split)), dim3(kChThreads),
+                 ChCfg<HD>::kSmem, s, P, status);
+  return e == cudaSuccess ? launched(1) : e;
+}
+
+cudaError_t launch_chunk(const AttnParams &P, int64_t tiles, int hd, int *status, cudaStream_t s) {
+  return hd == 128 ? run<128>(P, tiles, status, s) : run<64>(P, tiles, status, s);
+}
+
+}  // namespace paged
+}  // namespace cb

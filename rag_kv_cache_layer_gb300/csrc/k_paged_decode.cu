@@ -111,14 +111,14 @@ __device__ __forceinline__ void make_line(const AttnParams &P, int R, int BN, in
     if (k < per && i0 + k < P.kv.n_seq) {
       const int n = paged_rows(P.kv, i0 + k, P.n_rows, status), len = __ldg(P.kv.kv_lens + i0 + k);
       int nb = 0;
-      if (n > 0) {
+      if (n > 0 && (int64_t)n * P.G <= P.few_hi) {
         if (len < 0 || len > P.max_kv || len > (int64_t)P.kv.max_pages * P.kv.page_size)
           report(status, CB_ERR_DEVICE_INDEX);
         else
           nb = len > 0 ? (len - 1) / BN + 1 : 1;        // an idle slot's rows get their zeros
       }
       L.blocks[i0 + k] = nb;
-      u[k] = ((int64_t)n * P.G + R - 1) / R * P.Hkv * nb;
+      u[k] = nb ? ((int64_t)n * P.G + R - 1) / R * P.Hkv * nb : 0;
     }
     sum += u[k];
   }

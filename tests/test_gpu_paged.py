@@ -294,6 +294,15 @@ def test_attention_long_loops(dt, heads, page, n):
 
 
 @pytest.mark.parametrize("dt", list(HALF))
+@pytest.mark.parametrize("heads", [(8, 2, 128), (7, 1, 64), (5, 1, 128)])
+def test_attention_mixed_lengths_in_one_call(dt, heads):
+    """Generated tokens, drafts, idle slots and chunks in one batch."""
+    rng = np.random.default_rng(heads[0])
+    seqs = [(1, 900), (150, 700), (1, 0), (9, 10), (64, 64), (1, 1), (0, 5), (33, 2000), (16, 300), (1, 65)]
+    attention_case(rng, dt, heads, 16, seqs, tail=5)
+
+
+@pytest.mark.parametrize("dt", list(HALF))
 def test_attention_many_sequences(dt):
     rng = np.random.default_rng(77)
     seqs = [(int(rng.integers(0, 4)), int(rng.integers(0, 60))) for _ in range(300)]

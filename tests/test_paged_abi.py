@@ -71,15 +71,16 @@ def test_empty_calls_are_done():
 
 
 def _attn(kv=None, q=A, ld_q=512, rows=3, max_kv=64, hq=4, hkv=2, hd=128, out=A, ld_out=512, dt=L.CB_BF16,
-          ws=A, wsb=1 << 30):
+          ws=A, wsb=1 << 30, scale=0.1):
     kv = _kv() if kv is None else kv
-    return L.lib.cb_paged_attention(C.byref(kv) if kv else None, q, ld_q, rows, max_kv, hq, hkv, hd, 0.1, out,
+    return L.lib.cb_paged_attention(C.byref(kv) if kv else None, q, ld_q, rows, max_kv, hq, hkv, hd, scale, out,
                                     ld_out, dt, ws, wsb, None)
 
 
 @pytest.mark.parametrize("kw", [
     dict(q=None), dict(out=None), dict(q=P(4104)), dict(ld_q=504), dict(ld_out=508), dict(rows=-1), dict(max_kv=-1),
-    dict(hq=3), dict(hq=0), dict(hkv=0), dict(hq=258, hkv=2), dict(hd=96), dict(dt=2)])
+    dict(hq=3), dict(hq=0), dict(hkv=0), dict(hq=258, hkv=2), dict(hd=96), dict(dt=2),
+    dict(scale=-0.1), dict(scale=float("nan")), dict(scale=float("inf"))])
 def test_attention_refusals(kw):
     assert _attn(**kw) == L.CB_ERR_INVALID_ARG
 
