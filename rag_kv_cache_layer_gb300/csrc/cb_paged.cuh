@@ -60,13 +60,16 @@ __device__ __forceinline__ void paged_find_tile(const PagedKV &kv, int n_rows, i
   constexpr int kPer = (CB_MAX_SEQS + NT - 1) / NT;
   const int per = (kv.n_seq + NT - 1) / NT;
   const int i0 = threadIdx.x * per;
-  int cnt[kPer];
+  int cnt[kPer], len[kPer], row0[kPer], rows_of[kPer];
   int sum = 0;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     cnt[k] = 0;
     if (k < per && i0 + k < kv.n_seq) {
-      const int64_t rows = (int64_t)paged_rows(kv, i0 + k, n_rows, status) * G;
+      len[k] = __ldg(kv.kv_lens + i0 + k);
+      row0[k] = __ldg(kv.row_offsets + i0 + k);
+      rows_of[k] = paged_rows(kv, i0 + k, n_rows, status);
+      const int64_t rows = (int64_t)rows_of[k] * G;
       cnt[k] = rows > rows_lo ? (int)((rows + R - 1) / R) : 0;
     }
     sum += cnt[k];
@@ -87,13 +90,10 @@ __device__ __forceinline__ void paged_find_tile(const PagedKV &kv, int n_rows, i
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       if (tile >= first && tile < first + cnt[k]) {
-        const int s = i0 + k, len = __ldg(kv.kv_lens + s);
-        if (len < 0 || len > max_kv || len > (int64_t)kv.max_pages * kv.page_size) {
+        if (len[k] < 0 || len[k] > max_kv || len[k] > (int64_t)kv.max_pages * kv.page_size)
           report(status, CB_ERR_DEVICE_INDEX);
-        } else {
-          const int a = __ldg(kv.row_offsets + s);
-          *out = PagedTile{s, cnt[k] - 1 - (tile - first), a, __ldg(kv.row_offsets + s + 1) - a, len};
-        }
+        else
+          *out = PagedTile{i0 + k, cnt[k] - 1 - (tile - first), row0[k], rows_of[k], len[k]};
       }
       first += cnt[k];
     }

@@ -200,47 +200,57 @@ paged_simt_kernel(const __grid_constant__ AttnParams P, int *status) {
 }
 
 // Merges the partials of a tile's key ranges: with M = max m_c,
-// O = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c, in split order.  A warp
-// takes a row, each lane HD / 32 columns.
-constexpr int kMergeThreads = 256;
-template <typename T, int HD>
+// O = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c, in split order.  A block
+// takes eight rows of a tile, a warp a row, each lane HD / 32 columns: the
+// merge is a latency of three dependent reads, so it runs as wide as it can.
+constexpr int kMergeThreads = 256, kMergeRows = kMergeThreads / 32;
+template <int HD>
 __global__ void __launch_bounds__(kMergeThreads)
-paged_merge_kernel(const __grid_constant__ AttnParams P, int R, int *status) {
+paged_merge_kernel(const __grid_constant__ AttnParams P, int R) {
   constexpr int PER = HD / 32;
   __shared__ PagedTile s_tile;
   __shared__ int s_sums[kMergeThreads / 32];
-  grid_dep_wait();
+  const int slices = R / kMergeRows, slice = blockIdx.x % slices;
+  const int g = blockIdx.x / slices % P.Hkv, tile = blockIdx.x / slices / P.Hkv;
+  paged_find_tile<kMergeThreads>(P.kv, P.n_rows, P.G, R, P.max_kv, tile, &s_tile, s_sums, nullptr);
+  grid_dep_wait();                        // the tile's metadata was there before the partials' kernel began
   grid_dep_launch();
-  const int g = blockIdx.x % P.Hkv, tile = blockIdx.x / P.Hkv;
-  paged_find_tile<kMergeThreads>(P.kv, P.n_rows, P.G, R, P.max_kv, tile, &s_tile, s_sums, status, P.rows_lo);
   const PagedTile tl = s_tile;
   if (tl.s < 0) return;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, r = slice * kMergeRows + (threadIdx.x >> 5);
   const int l0 = tl.t * R, rows = min(R, tl.n * P.G - l0);
-  const int64_t slot0 = (int64_t)(tile * P.Hkv + g) * P.n_split * R;
-  for (int r = threadIdx.x >> 5; r < rows; r += kMergeThreads / 32) {
-    float M = -INFINITY;
-    for (int c = lane; c < P.n_split; c += 32) M = fmaxf(M, P.part_ml[slot0 + (int64_t)c * R + r].x);
-    M = warp_max(M);
-    float l = 0.f, o[PER];
+  if (r >= rows) return;
+  const int64_t row0 = (int64_t)(tile * P.Hkv + g) * P.n_split * R + r;
+  // lane c holds part c's (m, l); parts beyond 32 are met in further rounds
+  float M = -INFINITY;
+  for (int c = lane; c < P.n_split; c += 32) M = fmaxf(M, P.part_ml[row0 + (int64_t)c * R].x);
+  M = warp_max(M);
+  float l = 0.f, o[PER];
 #pragma unroll
-    for (int e = 0; e < PER; ++e) o[e] = 0.f;
-    for (int c = 0; c < P.n_split; ++c) {
-      const float2 ml = P.part_ml[slot0 + (int64_t)c * R + r];
-      if (ml.x == -INFINITY) continue;    // no visible key in this range
-      const float w = exp2f(ml.x - M);
+  for (int e = 0; e < PER; ++e) o[e] = 0.f;
+  for (int c0 = 0; c0 < P.n_split; c0 += 32) {
+    float w = 0.f;
+    if (c0 + lane < P.n_split) {
+      const float2 ml = P.part_ml[row0 + (int64_t)(c0 + lane) * R];
+      w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);      // no visible key in this range
       l += w * ml.y;
-      const float *src = P.part_o + (slot0 + (int64_t)c * R + r) * HD + lane * PER;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) o[e] = fmaf(w, src[e], o[e]);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int qi = (l0 + r) / P.G, h = (l0 + r) % P.G;
-    T *dst = reinterpret_cast<T *>(P.out) + (int64_t)(tl.row0 + qi) * P.ld_out +
-             (int64_t)(g * P.G + h) * HD + lane * PER;
+    const int n = min(32, P.n_split - c0);
+#pragma unroll 8
+    for (int c = 0; c < n; ++c) {
+      const float wc = __shfl_sync(0xffffffffu, w, c);
+      if (wc == 0.f) continue;                            // its row may not have been written
+      const float *src = P.part_o + (row0 + (int64_t)(c0 + c) * R) * HD + lane * PER;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) dst[e] = from_f<T>(o[e] * inv);
+      for (int e = 0; e < PER; ++e) o[e] = fmaf(wc, src[e], o[e]);
+    }
   }
+  l = warp_sum(l);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  float *dst = reinterpret_cast<float *>(P.out) + (int64_t)(tl.row0 + (l0 + r) / P.G) * P.ld_out +
+               (int64_t)(g * P.G + (l0 + r) % P.G) * HD + lane * PER;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) dst[e] = o[e] * inv;
 }
 
 // Tiles of R rows that n_rows rows over S sequences can make at most.
@@ -337,13 +347,11 @@ static cudaError_t run_all(AttnParams P, const Plan &p, cb_dtype dt, void *ws, i
   }
   if (!p.R) return e;
   bind(p.partials);
-  e = p.R == 128  ? launch_chunk(P, p.tiles, HD, status, s)
-      : p.R == 16 ? run_simt<16, HD>(P, p, status, s)
-                  : run_simt<64, HD>(P, p, status, s);
+  if (dt == CB_BF16) return launch_chunk(P, p.tiles, HD, status, s);
+  e = p.R == 16 ? run_simt<16, HD>(P, p, status, s) : run_simt<64, HD>(P, p, status, s);
   if (e != cudaSuccess || p.n_split == 1) return e;
-  const dim3 grid((unsigned)(p.tiles * P.Hkv));
-  e = dt == CB_BF16 ? launch_pdl(paged_merge_kernel<bf16, HD>, grid, dim3(kMergeThreads), 0, s, P, p.R, status)
-                    : launch_pdl(paged_merge_kernel<float, HD>, grid, dim3(kMergeThreads), 0, s, P, p.R, status);
+  const dim3 grid((unsigned)(p.tiles * P.Hkv * (p.R / kMergeRows)));
+  e = launch_pdl(paged_merge_kernel<HD>, grid, dim3(kMergeThreads), 0, s, P, p.R);
   return e == cudaSuccess ? launched(1) : e;
 }
 

@@ -23,7 +23,7 @@
 // would be a page's rows: at 16 slots a page sixteen boxes per block, about
 // 90 ns each, twice what the block's arithmetic takes.
 //
-// Parts of a split key range leave (O, m, l) in fp32 for paged_merge_kernel.
+// Parts of a split key range leave (O, m, l) in fp32 for chunk_merge_kernel.
 // All waits are bounded.
 #include "cb_attn_tc.cuh"
 #include "cb_common.cuh"
@@ -43,6 +43,14 @@ constexpr float kChRescale = 8.f;         // log2 of the largest p between resca
 constexpr int kChPerSm = 2;
 constexpr int kChTmem = 256;              // S/P slots 0..63, 64..127; O from 128
 
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+
 template <int HD> struct ChCfg {
   static constexpr int kAtom = kChRows * 128;        // [128 rows x 64 dims], 128-byte swizzle
   static constexpr int kAtomKV = kChBN * 128;        // [64 keys x 64 dims]
@@ -52,26 +60,38 @@ template <int HD> struct ChCfg {
 };
 
 // Fills one K or V stage: 64 keys of one head.  Lane = (row of 32 / cols,
-// 16-byte column); eight consecutive keys share a page (page_size >= 8).
-template <int HD>
+// 16-byte column); eight consecutive keys share a page (page_size >= 8), so a
+// group of eight rows is one page lookup and steps of a constant stride.
+// ALL: every key exists and every page is valid.
+template <int HD, bool ALL>
 __device__ __forceinline__ void chunk_load(uint32_t dst, const bf16 *pool, const PagedKV &kv, int key0, int n_keys,
                                            int page_lo, int page_hi, int lane) {
   constexpr int kCols = HD / 8, kRows = 32 / kCols;
   const int crow = lane / kCols, col = lane % kCols;
-  const uint32_t half = dst + (col >> 3) * (kChBN * 128);
+  const int64_t step = (int64_t)kRows * kv.ld;
+  pool += (int64_t)crow * kv.ld + col * 8;
+  uint32_t at[8 / kRows];
+#pragma unroll
+  for (int i = 0; i < 8 / kRows; ++i) {
+    const int r = i * kRows + crow;
+    at[i] = dst + (col >> 3) * (kChBN * 128) + r * 128 + (((col ^ r) & 7) << 4);
+  }
 #pragma unroll
   for (int g8 = 0; g8 < kChBN / 8; ++g8) {
     const int page = __shfl_sync(0xffffffffu, g8 < 4 ? page_lo : page_hi, (g8 & 3) * 8);
     const int slot = (key0 + g8 * 8) & (kv.page_size - 1);
-    const bf16 *src = pool + (page < 0 ? 0 : (int64_t)page * kv.page_stride + (int64_t)(slot + crow) * kv.ld) + col * 8;
-    const int64_t step = page < 0 ? 0 : (int64_t)kRows * kv.ld;
+    const bf16 *src = pool + (ALL || page >= 0 ? (int64_t)page * kv.page_stride + (int64_t)slot * kv.ld : 0);
 #pragma unroll
     for (int i = 0; i < 8 / kRows; ++i) {
-      const int r = g8 * 8 + i * kRows + crow;
-      const bool there = page >= 0 && r < n_keys;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(half + r * 128 + (((col ^ r) & 7) << 4)),
-                   "l"(src), "r"(there ? 16 : 0)
-                   : "memory");
+      if (ALL) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at[i] + g8 * 1024), "l"(src) : "memory");
+      } else {
+        // a row past the cached length, or of a bad page: zeros, nothing read
+        const bool there = page >= 0 && g8 * 8 + i * kRows + crow < n_keys;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at[i] + g8 * 1024),
+                     "l"(there ? src : pool), "r"(there ? 16 : 0)
+                     : "memory");
+      }
       src += step;
     }
   }
@@ -164,23 +184,44 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
       return -1;
     };
     int lo = fetch(jb * kChBN + lane), hi = fetch(jb * kChBN + 32 + lane);
+    // Two loads are in flight: a block is handed over (its bytes fenced for
+    // the tensor core) after the next one has been issued, or at once where
+    // the next one's stage is still in use.
+    int open = -1;                               // block issued but not handed over
+    auto hand_over = [&] {
+      proxy_fence();
+      arrive(smem_u32(&full[open & 1]));
+      open = -1;
+    };
     for (int j = 0; j < nb; ++j) {
       const int sl = j & 1, key0 = (jb + j) * kChBN;
-      const bool ok = mbar_wait_bounded(smem_u32(&empty[sl]), ((j >> 1) & 1) ^ 1, kWaitLimitNs, status);
+      const uint32_t eb = smem_u32(&empty[sl]), ph = ((j >> 1) & 1) ^ 1;
+      if (open >= 0 && !__all_sync(0xffffffffu, mbar_test(eb, ph))) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        hand_over();
+      }
+      const bool ok = mbar_wait_bounded(eb, ph, kWaitLimitNs, status);
       if (__any_sync(0xffffffffu, !ok || *fail)) {
         *fail = 1;
         break;
       }
       lo = checked(lo, key0 + lane);
       hi = checked(hi, key0 + 32 + lane);
-      chunk_load<HD>(dst + sl * C::kKV, pool, P.kv, key0, tl.kv - key0, lo, hi, lane);
+      if (__all_sync(0xffffffffu, lo >= 0 && hi >= 0))
+        chunk_load<HD, true>(dst + sl * C::kKV, pool, P.kv, key0, kChBN, lo, hi, lane);
+      else
+        chunk_load<HD, false>(dst + sl * C::kKV, pool, P.kv, key0, tl.kv - key0, lo, hi, lane);
       asm volatile("cp.async.commit_group;" ::: "memory");
       lo = fetch(key0 + kChBN + lane);
       hi = fetch(key0 + kChBN + 32 + lane);
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      proxy_fence();                             // this lane's bytes, to the tensor core
-      arrive(smem_u32(&full[sl]));
+      if (open >= 0) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        hand_over();
+      }
+      open = j;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (open >= 0) hand_over();
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA
     const uint32_t idS = idesc(false, kChBN), idPV = idesc(true, HD);
@@ -236,18 +277,18 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
   } else {
     // ------------------------------------------------------ Q, then softmax
     {
-      constexpr int kCols = HD / 8;
-      const bf16 *q = reinterpret_cast<const bf16 *>(P.q) + (int64_t)g * P.G * HD;
-      const int t = threadIdx.x - 64;
-#pragma unroll 4
-      for (int i = t; i < kChRows * kCols; i += 128) {
-        const int r = i / kCols, col = i % kCols, l = l0 + r;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < rows)
-          v = *reinterpret_cast<const uint4 *>(q + (int64_t)(tl.row0 + l / P.G) * P.ld_q + (int64_t)(l % P.G) * HD +
-                                               col * 8);
-        *reinterpret_cast<uint4 *>(smem + (col >> 3) * C::kAtom + r * 128 + (((col ^ r) & 7) << 4)) = v;
-      }
+      // thread t loads row t: all its loads are in flight at once, and eight
+      // neighbouring rows fall into different banks
+      const int r = threadIdx.x - 64, l = l0 + r;
+      const bf16 *q = reinterpret_cast<const bf16 *>(P.q) + (int64_t)(tl.row0 + l / P.G) * P.ld_q +
+                      (int64_t)(g * P.G + l % P.G) * HD;
+      uint4 v[HD / 8];
+#pragma unroll
+      for (int c = 0; c < HD / 8; ++c)
+        v[c] = r < rows ? *reinterpret_cast<const uint4 *>(q + c * 8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < HD / 8; ++c)
+        *reinterpret_cast<uint4 *>(smem + (c >> 3) * C::kAtom + r * 128 + (((c ^ r) & 7) << 4)) = v[c];
       proxy_fence();
       arrive(smem_u32(q_full));
     }
@@ -351,7 +392,9 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
       const float inv = l == 0.f ? 0.f : 1.f / l;    // no visible key: zeros
       bf16 *out = reinterpret_cast<bf16 *>(P.out) + (int64_t)(tl.row0 + lr / P.G) * P.ld_out +
                   (int64_t)(g * P.G + lr % P.G) * HD;
-      float *part = P.part_o + (slot0 + row) * HD;
+      // partials lie four columns of all 128 rows together, which a warp with
+      // a row per lane writes (and the merge reads) in whole lines
+      float4 *part = reinterpret_cast<float4 *>(P.part_o + slot0 * HD) + row;
 #pragma unroll 1
       for (int c = 0; c < HD; c += 32) {
         float o[32];
@@ -360,7 +403,7 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
         if (P.n_split > 1) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4 *>(part + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            part[(c + i) / 4 * kChRows] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           continue;
         }
 #pragma unroll
@@ -384,6 +427,64 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
   }
 }
 
+// Merges the parts of a tile: with M = max m_c, O = sum_c 2^(m_c - M) O_c /
+// sum_c 2^(m_c - M) l_c, in part order.  A block takes 32 rows (one per lane)
+// and 32 columns (four per warp).  The tile is found before the parts are
+// waited for: what it reads was there before the chunk kernel began.
+constexpr int kChMergeThreads = 256;
+template <int HD>
+__global__ void __launch_bounds__(kChMergeThreads)
+chunk_merge_kernel(const __grid_constant__ AttnParams P) {
+  constexpr int kQuads = kChRows / 32, kColBlocks = HD / 32;
+  __shared__ PagedTile s_tile;
+  __shared__ int s_sums[kChMergeThreads / 32];
+  __shared__ __align__(16) bf16 s_out[32][40];
+  const int sub = blockIdx.x % (kQuads * kColBlocks), quad = sub / kColBlocks, cb = sub % kColBlocks;
+  const int g = blockIdx.x / (kQuads * kColBlocks) % P.Hkv, tile = blockIdx.x / (kQuads * kColBlocks) / P.Hkv;
+  paged_find_tile<kChMergeThreads>(P.kv, P.n_rows, P.G, kChRows, P.max_kv, tile, &s_tile, s_sums, nullptr, P.rows_lo);
+  grid_dep_wait();
+  grid_dep_launch();
+  const PagedTile tl = s_tile;
+  const int l0 = tl.t * kChRows + quad * 32;
+  if (tl.s < 0 || l0 >= tl.n * P.G) return;
+  const int rows = min(32, tl.n * P.G - l0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t slot0 = (int64_t)(tile * P.Hkv + g) * P.n_split * kChRows;
+  const float2 *ml = P.part_ml + slot0 + quad * 32 + lane;
+  const float4 *po = reinterpret_cast<const float4 *>(P.part_o + slot0 * HD) + (cb * 8 + warp) * kChRows + quad * 32 + lane;
+  float M = -INFINITY, l = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (lane < rows) {
+#pragma unroll 8
+    for (int c = 0; c < P.n_split; ++c) M = fmaxf(M, ml[c * kChRows].x);
+#pragma unroll 4
+    for (int c = 0; c < P.n_split; ++c) {
+      const float2 x = ml[c * kChRows];
+      if (x.x == -INFINITY) continue;            // no visible key in this part; its O is not written
+      const float w = fast_exp2(x.x - M);
+      const float4 v = po[(int64_t)c * kChRows * HD / 4];
+      l = fmaf(w, x.y, l);
+      a.x = fmaf(w, v.x, a.x);
+      a.y = fmaf(w, v.y, a.y);
+      a.z = fmaf(w, v.z, a.z);
+      a.w = fmaf(w, v.w, a.w);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  __nv_bfloat162 *so = reinterpret_cast<__nv_bfloat162 *>(&s_out[lane][warp * 4]);
+  so[0] = __floats2bfloat162_rn(a.x * inv, a.y * inv);
+  so[1] = __floats2bfloat162_rn(a.z * inv, a.w * inv);
+  __syncthreads();
+  // 64 bytes of each row, four lanes a row
+  const int r = threadIdx.x / 4, c8 = threadIdx.x % 4 * 8;
+  if (r < rows) {
+    const int lr = l0 + r;
+    *reinterpret_cast<uint4 *>(reinterpret_cast<bf16 *>(P.out) + (int64_t)(tl.row0 + lr / P.G) * P.ld_out +
+                               (int64_t)(g * P.G + lr % P.G) * HD + cb * 32 + c8) =
+        *reinterpret_cast<const uint4 *>(&s_out[r][c8]);
+  }
+}
+
 int chunk_slots() { return kChPerSm * device_sm_count(); }
 
 template <int HD>
@@ -395,7 +496,11 @@ static cudaError_t run(const AttnParams &P, int64_t tiles, int *status, cudaStre
   if (e != cudaSuccess) return e;
   e = launch_pdl(paged_chunk_kernel<HD>, dim3((unsigned)(tiles * P.Hkv * P.n_split)), dim3(kChThreads),
                  ChCfg<HD>::kSmem, s, P, status);
-  return e == cudaSuccess ? launched(1) : e;
+  if (e != cudaSuccess) return e;
+  if (P.n_split == 1) return launched(1);
+  e = launch_pdl(chunk_merge_kernel<HD>, dim3((unsigned)(tiles * P.Hkv * (kChRows / 32) * (HD / 32))),
+                 dim3(kChMergeThreads), 0, s, P);
+  return e == cudaSuccess ? launched(2) : e;
 }
 
 cudaError_t launch_chunk(const AttnParams &P, int64_t tiles, int hd, int *status, cudaStream_t s) {
