@@ -17,9 +17,17 @@
 // 10^5 borders is a wrong token in every hundredth row.
 //
 // One cluster of C blocks holds a row in shared memory, C slices of it, so
-// the logits are read once from device memory; every further pass (the radix
-// levels of the two selections, the draw) reads shared memory, and the blocks
-// exchange histograms and sums through distributed shared memory.
+// the logits are read once from device memory.  The two selections share one
+// histogram over equal steps of x, from the maximum down to where weights
+// vanish: the step at which the count reaches top_k, or the weight top_p, is
+// found from its sums, and only the tokens that matter there are gathered and
+// sorted exactly by (x, index):
+//   small  all tokens down to that step (at most kCand): the cluster's first
+//          block sorts them and finishes the row alone;
+//   large  the step's own tokens: the exact cut goes back to the cluster,
+//          whose blocks then draw from everything above it;
+//   wide   more tokens in one step than kCand (long ties): a radix selection
+//          over the keys finds the cut instead.
 #include <math.h>
 
 #include "cb_common.cuh"
@@ -30,7 +38,8 @@ namespace cb {
 namespace smp {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kBins = 1024;                 // steps of the histogram
+constexpr int kCand = 2048;                 // tokens the sorter takes
 constexpr int kMaxCluster = 8;
 typedef unsigned long long u64;
 
@@ -127,39 +136,33 @@ __device__ __forceinline__ u64 scaled(u64 a, float f, bool *inexact) {
 
 // --------------------------------------------------------------- layout --
 struct Shared {
-  uint32_t cnt[kBins], m0[kBins], m1[kBins], m2[kBins];   // this block's histogram
-  u64 reduced[kBins];       // the bins this block reduces over the cluster
+  union {
+    struct {
+      uint32_t cnt[kBins], m0[kBins], m1[kBins], m2[kBins];   // this block's histogram
+    };
+    u64 cand[kCand];        // gathered tokens, sorted
+  };
+  u64 rmass[kBins];         // the bins this block reduces over the cluster
+  uint32_t rcnt[kBins];
   u64 table[65];
   u64 warp[kWarps];         // a pass's sum per warp
   u64 sum[3];               // this block's sums: weights to cut, ties, kept weights
   u64 best;                 // this block's largest (key, ~index)
-  u64 bin, left;            // a radix level's answer
-  u64 cut;                  // last index kept among the tokens at the cut
+  float least;              // and its smallest logit above -inf
+  uint32_t n_cand;
+  u64 left, total;          // a search's answer
+  int bin, count;
+  u64 cut;                  // the cut: key << 32 | last index kept with that key
 };
 
-template <typename T> struct Key;
-template <> struct Key<float> {
-  static constexpr int kLevels = 3;
-  __device__ static uint32_t of(float x) {
-    const uint32_t b = __float_as_uint(x);
-    return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
-  }
-  __device__ static float value(uint32_t k) {
-    return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
-  }
-  __device__ static int lo_bit(int level) { return level == 0 ? 21 : level == 1 ? 10 : 0; }
-  __device__ static int bits(int level) { return level == 2 ? 10 : 11; }
-};
-template <> struct Key<bf16> {
-  static constexpr int kLevels = 2;
-  __device__ static uint32_t of(float x) { return Key<float>::of(x) >> 16; }
-  __device__ static float value(uint32_t k) {
-    return Key<float>::value((k << 16) | ((k >> 15) ? 0u : 0xffffu));
-  }
-  __device__ static int lo_bit(int level) { return level == 0 ? 5 : 0; }
-  __device__ static int bits(int level) { return level == 0 ? 11 : 5; }
-};
-
+// Order-preserving integer of a float, and back.
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+}
 // NaN counts as -inf, -0 as 0: equal values have equal keys.
 __device__ __forceinline__ float clean(float x) { return x != x ? -INFINITY : x + 0.f; }
 
@@ -185,9 +188,53 @@ __device__ __forceinline__ uint32_t remote(const uint32_t *p, uint32_t rank) {
                : "=r"(v) : "r"(tcx::map_to_rank(smem_u32(p), rank)) : "memory");
   return v;
 }
+__device__ __forceinline__ float remote(const float *p, uint32_t rank) {
+  return __uint_as_float(remote(reinterpret_cast<const uint32_t *>(p), rank));
+}
 __device__ __forceinline__ void remote_store(u64 *p, uint32_t rank, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(tcx::map_to_rank(smem_u32(p), rank)), "l"(v)
                : "memory");
+}
+__device__ __forceinline__ uint32_t remote_add(uint32_t *p, uint32_t rank, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
+               : "=r"(old) : "r"(tcx::map_to_rank(smem_u32(p), rank)), "r"(v) : "memory");
+  return old;
+}
+
+// Exclusive prefix sum of v over the block, the block's sum in *total.
+__device__ __forceinline__ u64 block_scan(Shared &sh, u64 v, u64 *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  u64 incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  __syncthreads();
+  if (lane == 31) sh.warp[warp] = incl;
+  __syncthreads();
+  u64 before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const u64 t = sh.warp[w];
+    before += w < warp ? t : 0;
+    all += t;
+  }
+  *total = all;
+  return before + incl - v;
+}
+
+// Adds a weight to bin b of this block's histogram, in three 16-bit parts:
+// their sums over a slice of at most 2^16 tokens stay below 2^32.
+__device__ __forceinline__ void add_weight(Shared &sh, int b, u64 m) {
+  atomicAdd(&sh.m0[b], (uint32_t)m & 0xffffu);
+  const uint32_t hi = (uint32_t)(m >> 16) & 0xffffu, top = (uint32_t)(m >> 32);
+  if (hi) atomicAdd(&sh.m1[b], hi);
+  if (top) atomicAdd(&sh.m2[b], top);
+}
+__device__ __forceinline__ u64 remote_weight(const Shared &sh, int b, int rank) {
+  return (u64)remote(&sh.m0[b], rank) + ((u64)remote(&sh.m1[b], rank) << 16) + ((u64)remote(&sh.m2[b], rank) << 32);
 }
 
 // The consecutive range of a block's n tokens that warp w owns.
@@ -205,6 +252,7 @@ __device__ __forceinline__ u64 cluster_sum(Shared &sh, int slot, int n, int rank
   u64 s = 0;
   for (int i = warp_begin(n, warp) + lane; i < e; i += 32) s += f(i);
   s = warp_sum64(s);
+  __syncthreads();
   if (lane == 0) sh.warp[warp] = s;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -249,6 +297,35 @@ __device__ __forceinline__ void ordered_find(const Shared &sh, int n, u64 before
   }
 }
 
+// Sorts a[0 .. n) ascending (n a power of two); the block's threads all call.
+__device__ __forceinline__ void sort_block(u64 *a, int n) {
+  for (int k = 2; k <= n; k <<= 1)
+    for (int j = k >> 1; j; j >>= 1) {
+      for (int t = threadIdx.x; t < n / 2; t += kThreads) {
+        const int i = (t / j) * 2 * j + t % j, l = i + j;
+        const u64 x = a[i], y = a[l];
+        if ((x > y) == ((i & k) == 0)) {
+          a[i] = y;
+          a[l] = x;
+        }
+      }
+      __syncthreads();
+    }
+}
+// Sorts the first n gathered tokens (padded to a power of two); returns that
+// power.
+__device__ __forceinline__ int sort_cand(Shared &sh, int n) {
+  int m = 2;
+  while (m < n) m <<= 1;
+  for (int i = n + threadIdx.x; i < m; i += kThreads) sh.cand[i] = ~0ull;
+  __syncthreads();
+  sort_block(sh.cand, m);
+  return m;
+}
+// A gathered token: ascending order is larger x first, then lower index.
+__device__ __forceinline__ u64 pack(uint32_t key, uint32_t index) { return ((u64)~key << 32) | index; }
+__device__ __forceinline__ uint32_t packed_key(u64 v) { return ~(uint32_t)(v >> 32); }
+
 // Radix selection over the cluster's tokens, largest key first: the key at
 // which the running count (MASS false) or weight (MASS true) first reaches
 // `need` (>= 1 and at most the total), and in *left what of `need` falls to
@@ -258,29 +335,22 @@ template <typename T, bool MASS>
 __device__ __forceinline__ uint32_t radix_select(Shared &sh, const T *x, int n, int rank, int C, u64 need,
                                                  const Scale &sc, int64_t above, uint32_t extra_key,
                                                  u64 extra_mass, u64 *left) {
-  static_assert(kBins == 4 * kThreads, "four bins per thread");
+  constexpr int kDigit = 8, nb = 1 << kDigit;
+  static_assert(nb <= kThreads && nb <= kBins, "a bin per thread");
+  const int per = nb / C;
   uint32_t prefix = 0;
-  for (int level = 0; level < Key<T>::kLevels; ++level) {
-    const int lo = Key<T>::lo_bit(level), hi = lo + Key<T>::bits(level);
-    const int nb = 1 << Key<T>::bits(level), per = nb / C;
-    for (int i = threadIdx.x; i < nb; i += kThreads) {
-      sh.cnt[i] = 0;
-      if (MASS) sh.m0[i] = sh.m1[i] = sh.m2[i] = 0;
-    }
+  for (int lo = 32 - kDigit; lo >= 0; lo -= kDigit) {
+    const int hi = lo + kDigit;
+    for (int i = threadIdx.x; i < nb; i += kThreads) sh.cnt[i] = sh.m0[i] = sh.m1[i] = sh.m2[i] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += kThreads) {
       const float v = to_f(x[i]);
-      const uint32_t k = Key<T>::of(v);
-      if ((level && (k >> hi) != prefix) || (int64_t)k <= above) continue;
+      const uint32_t k = key_of(v);
+      if ((hi < 32 && (k >> hi) != prefix) || (int64_t)k <= above) continue;
       const uint32_t b = (k >> lo) & (nb - 1);
       if (MASS) {
-        // three 16-bit parts: sums over a slice stay below 2^32
         const u64 m = weight(v, sc, sh.table);
-        if (m) {
-          atomicAdd(&sh.m0[b], (uint32_t)m & 0xffffu);
-          atomicAdd(&sh.m1[b], (uint32_t)(m >> 16) & 0xffffu);
-          atomicAdd(&sh.m2[b], (uint32_t)(m >> 32));
-        }
+        if (m) add_weight(sh, b, m);
       } else {
         atomicAdd(&sh.cnt[b], 1u);
       }
@@ -288,48 +358,24 @@ __device__ __forceinline__ uint32_t radix_select(Shared &sh, const T *x, int n, 
     cluster_barrier();
     for (int b = rank * per + threadIdx.x; b < (rank + 1) * per; b += kThreads) {
       u64 s = 0;
-      for (int c = 0; c < C; ++c) {
-        if (MASS)
-          s += (u64)remote(&sh.m0[b], c) + ((u64)remote(&sh.m1[b], c) << 16) +
-               ((u64)remote(&sh.m2[b], c) << 32);
-        else
-          s += remote(&sh.cnt[b], c);
-      }
-      if (MASS && extra_mass && (level == 0 || (extra_key >> hi) == prefix) &&
+      for (int c = 0; c < C; ++c) s += MASS ? remote_weight(sh, b, c) : (u64)remote(&sh.cnt[b], c);
+      if (MASS && extra_mass && (hi == 32 || (extra_key >> hi) == prefix) &&
           ((extra_key >> lo) & (nb - 1)) == (uint32_t)b)
         s += extra_mass;
-      sh.reduced[b] = s;
+      sh.rmass[b] = s;
     }
     cluster_barrier();
     // every block scans all bins, largest first
-    u64 v[4], tot = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int b = nb - 1 - ((int)threadIdx.x * 4 + k);
-      v[k] = b >= 0 ? remote(&sh.reduced[b], b / per) : 0ull;
-      tot += v[k];
-    }
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    u64 incl = tot;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const u64 t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
-    }
-    if (lane == 31) sh.warp[warp] = incl;
-    __syncthreads();
-    u64 acc = incl - tot;
-    for (int w = 0; w < warp; ++w) acc += sh.warp[w];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (acc < need && need <= acc + v[k]) {
-        sh.bin = (u64)(nb - 1 - ((int)threadIdx.x * 4 + k));
-        sh.left = need - acc;
-      }
-      acc += v[k];
+    const int b = nb - 1 - (int)threadIdx.x;
+    const u64 v = b >= 0 ? remote(&sh.rmass[b], b / per) : 0ull;
+    u64 total;
+    const u64 acc = block_scan(sh, v, &total);
+    if (acc < need && need <= acc + v) {
+      sh.bin = b;
+      sh.left = need - acc;
     }
     __syncthreads();
-    prefix = (prefix << Key<T>::bits(level)) | (uint32_t)sh.bin;
+    prefix = (prefix << kDigit) | (uint32_t)sh.bin;
     need = sh.left;
     __syncthreads();
   }
@@ -337,116 +383,337 @@ __device__ __forceinline__ uint32_t radix_select(Shared &sh, const T *x, int n, 
   return prefix;
 }
 
+// Loads the block's slice, cleaned, and finds its largest logit (lowest
+// index first) and its smallest above -inf.
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__device__ __forceinline__ void load_slice(Shared &sh, T *x, const T *src, int n, int lo) {
+  constexpr int VEC = 16 / sizeof(T);
+  float mx = -INFINITY, mn = INFINITY;
+  int at = 0x7fffffff;
+  auto see = [&](float v, int i) {
+    if (v > mx) {                       // indices ascend within a thread
+      mx = v;
+      at = i;
+    }
+    if (v > -INFINITY) mn = fminf(mn, v);
+  };
+  const int nv = ((uintptr_t)src & 15) == 0 ? n / VEC : 0;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < nv; i += kThreads) {
+    uint4 raw = ldg16(src + i * VEC);
+    T *e = reinterpret_cast<T *>(&raw);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      const float v = clean(to_f(e[k]));
+      e[k] = from_f<T>(v);
+      see(v, i * VEC + k);
+    }
+    *reinterpret_cast<uint4 *>(x + i * VEC) = raw;
+  }
+#pragma unroll 4
+  for (int i = nv * VEC + threadIdx.x; i < n; i += kThreads) {
+    const float v = clean(to_f(src[i]));
+    x[i] = from_f<T>(v);
+    see(v, i);
+  }
+  u64 best = at == 0x7fffffff ? 0ull : ((u64)key_of(mx) << 32) | (uint32_t)~(uint32_t)(lo + at);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const u64 t = __shfl_xor_sync(0xffffffffu, best, o);
+    best = t > best ? t : best;
+    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float *wmin = reinterpret_cast<float *>(sh.rmass);
+  if (lane == 0) {
+    sh.warp[warp] = best;
+    wmin[warp] = mn;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kWarps; ++w) {
+      best = sh.warp[w] > best ? sh.warp[w] : best;
+      mn = fminf(mn, wmin[w]);
+    }
+    sh.best = best;
+    sh.least = mn;
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2)
 sample_kernel(const __grid_constant__ Params P) {
   extern __shared__ __align__(16) uint8_t raw[];
   Shared &sh = *reinterpret_cast<Shared *>(raw);
   T *x = reinterpret_cast<T *>(raw + (sizeof(Shared) + 15) / 16 * 16);
-  grid_dep_wait();
-  grid_dep_launch();
   const int rank = (int)tcx::cluster_rank();
   uint32_t csize;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
   const int C = (int)csize, row = blockIdx.x / C;
   const int lo = min(P.vocab, rank * P.slice), n = min(P.vocab, lo + P.slice) - lo;
-  const T *src = reinterpret_cast<const T *>(P.logits) + (int64_t)row * P.ld + lo;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-
   if (threadIdx.x < 65) sh.table[threadIdx.x] = kExp2Table[threadIdx.x];
-  u64 best = 0;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const float v = clean(to_f(src[i]));
-    x[i] = from_f<T>(v);
-    const u64 k = ((u64)Key<float>::of(v) << 32) | (uint32_t)~(uint32_t)(lo + i);
-    best = k > best ? k : best;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const u64 t = __shfl_xor_sync(0xffffffffu, best, o);
-    best = t > best ? t : best;
-  }
-  if (lane == 0) sh.warp[warp] = best;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 0; w < kWarps; ++w) best = sh.warp[w] > best ? sh.warp[w] : best;
-    sh.best = best;
-  }
-  cluster_barrier();
-  best = 0;
-  for (int c = 0; c < C; ++c) {
-    const u64 t = remote(&sh.best, c);
-    best = t > best ? t : best;
-  }
-  const int top_index = (int)~(uint32_t)best;
-  Scale sc;
-  sc.top = Key<float>::value((uint32_t)(best >> 32));
-  sc.shift = P.shift;
+  if (threadIdx.x == 0) sh.n_cand = 0;
+  for (int i = threadIdx.x; i < kBins; i += kThreads) sh.cnt[i] = sh.m0[i] = sh.m1[i] = sh.m2[i] = 0;
+  grid_dep_wait();
+  grid_dep_launch();
   const float temp = P.temperature ? P.temperature[row] : 1.f;
   const int k = P.top_k ? P.top_k[row] : 0;
   const float p = P.top_p ? P.top_p[row] : 1.f;
   const float mp = P.min_p ? P.min_p[row] : 0.f;
-  const bool empty = sc.top == -INFINITY;             // every logit is -inf or NaN
+  const float u = P.u[row];
+  load_slice(sh, x, reinterpret_cast<const T *>(P.logits) + (int64_t)row * P.ld + lo, n, lo);
+  cluster_barrier();
+  u64 best = 0;
+  float low = INFINITY;
+  for (int c = 0; c < C; ++c) {
+    const u64 t = remote(&sh.best, c);
+    best = t > best ? t : best;
+    low = fminf(low, remote(&sh.least, c));
+  }
+  const bool empty = best == 0;                       // every logit is -inf or NaN
   if (empty || !(temp > 0.f) || k == 1 || p <= 0.f) {
-    if (rank == 0 && threadIdx.x == 0) P.tokens[row] = empty ? -1 : top_index;
+    if (rank == 0 && threadIdx.x == 0) P.tokens[row] = empty ? -1 : (int)~(uint32_t)best;
     cluster_barrier();                                // its shared memory has been read
     return;
   }
+  Scale sc;
+  sc.top = value_of((uint32_t)(best >> 32));
+  sc.shift = P.shift;
   {
     // log2(e) / t as two floats; a temperature below 1e-30 acts as 1e-30
     const double c = 1.4426950408889634 / (double)fmaxf(temp, 1e-30f);
     sc.ch = (float)c;
     sc.cl = (float)(c - (double)sc.ch);
   }
-  const bool use_k = k > 0 && k < P.vocab, use_p = p < 1.f;
-  bool cut = false;
-  uint32_t cut_key = 0;
-  u64 cut_left = 0;                                   // tokens kept at cut_key
-  if (use_k) {
-    cut = true;
-    cut_key = radix_select<T, false>(sh, x, n, rank, C, (u64)k, sc, -1, 0, 0, &cut_left);
-  }
-  if (use_p) {
-    const int64_t above = use_k ? (int64_t)cut_key : -1;
-    const u64 tie = use_k ? cut_left * weight(Key<T>::value(cut_key), sc, sh.table) : 0ull;
-    u64 total;
-    cluster_sum(sh, 0, n, rank, C, [&](int i) {
-      const float v = to_f(x[i]);
-      return (int64_t)Key<T>::of(v) > above ? weight(v, sc, sh.table) : 0ull;
-    }, &total);
-    total += tie;
-    bool more;
-    u64 need = scaled(total, p, &more);
-    need += more;
-    u64 left;
-    cut_key = radix_select<T, true>(sh, x, n, rank, C, need ? need : 1, sc, above, cut_key, tie, &left);
-    const u64 one = weight(Key<T>::value(cut_key), sc, sh.table);
-    cut_left = (left + one - 1) / one;
-    cut = true;
-  }
-  int last = P.vocab;                                 // largest index kept at cut_key
-  if (cut) {
-    auto is_tie = [&](int i) { return Key<T>::of(to_f(x[i])) == cut_key ? 1ull : 0ull; };
-    u64 ties;
-    const u64 before = cluster_sum(sh, 1, n, rank, C, is_tie, &ties);
-    if (ties > cut_left) {                            // the same in every block
-      ordered_find(sh, n, before, cut_left - 1, is_tie, [&](int i) {
-        for (int c = 0; c < C; ++c) remote_store(&sh.cut, c, (u64)(lo + i));
-      });
-      cluster_barrier();
-      last = (int)sh.cut;
-    }
-  }
+  bool use_k = k > 0 && k < P.vocab;
+  const bool use_p = p < 1.f;
   u64 least = 1;                                      // min_p of the largest weight
   if (mp > 0.f) {
     bool more = false;
     least = mp >= 1.f ? 1ull << P.shift : scaled(1ull << P.shift, mp, &more);
     least += more;
   }
+  bool cut = false, wide = false;
+  uint32_t cut_key = 0;
+  int last = P.vocab;                                 // largest index kept at cut_key
+  if (use_k || use_p) {
+    // steps of x from the maximum down to where weights vanish (tokens beyond
+    // are in none: no cut can matter there)
+    const float range = fminf(sc.top - low, (float)(P.shift + 3) / sc.ch);
+    const float scale = (float)kBins / fmaxf(range * 1.0001f, 1e-35f);
+    auto bin_of = [&](float v) -> int {               // monotone in v
+      const float t = (sc.top - v) * scale;
+      return t < (float)kBins ? (int)t : kBins;
+    };
+    wide = sc.top == INFINITY;                        // no distance to measure by
+    if (!wide) {
+      for (int i = threadIdx.x; i < n; i += kThreads) {
+        const float v = to_f(x[i]);
+        const int b = bin_of(v);
+        if (b >= kBins) continue;
+        atomicAdd(&sh.cnt[b], 1u);
+        if (use_p) {
+          const u64 m = weight(v, sc, sh.table);
+          if (m) add_weight(sh, b, m);
+        }
+      }
+      cluster_barrier();
+      const int per = kBins / C;
+      for (int b = rank * per + threadIdx.x; b < (rank + 1) * per; b += kThreads) {
+        u64 s = 0;
+        uint32_t q = 0;
+        for (int c = 0; c < C; ++c) {
+          q += remote(&sh.cnt[b], c);
+          if (use_p) s += remote_weight(sh, b, c);
+        }
+        sh.rmass[b] = s;
+        sh.rcnt[b] = q;
+      }
+      cluster_barrier();
+      // every block scans all bins, two per thread, from the maximum down
+      static_assert(kBins == 2 * kThreads, "two bins per thread");
+      const int b = threadIdx.x * 2;
+      const uint32_t q0 = remote(&sh.rcnt[b], b / per), q1 = remote(&sh.rcnt[b + 1], b / per);
+      u64 count, total = 0, w0 = 0, w1 = 0, wacc = 0;
+      const u64 qacc = block_scan(sh, (u64)q0 + q1, &count);
+      if (use_p) {
+        w0 = remote(&sh.rmass[b], b / per);
+        w1 = remote(&sh.rmass[b + 1], b / per);
+        wacc = block_scan(sh, w0 + w1, &total);
+      }
+      use_k = use_k && (u64)k <= count;               // else only vanished weights fall to it
+      // the step that reaches top_k, or else top_p
+      bool more;
+      u64 need = (u64)k;
+      if (!use_k && use_p) {
+        need = scaled(total, p, &more);
+        need += more;
+        need = need ? need : 1;
+      }
+      if (use_k || use_p) {
+        const u64 a = use_k ? qacc : wacc, v0 = use_k ? q0 : w0, v1 = use_k ? q1 : w1;
+        if (a < need && need <= a + v0 + v1) {
+          const int second = need > a + v0;
+          sh.bin = b + second;
+          sh.left = need - a - (second ? v0 : 0);     // still needed inside the step
+          sh.count = (int)(qacc + q0 + (second ? q1 : 0));   // tokens down to and with it
+          sh.total = total;
+        }
+        __syncthreads();
+        const int step = sh.bin, in_step = (int)remote(&sh.rcnt[step], step / per), down = sh.count;
+        const bool small = down <= kCand;
+        // a step of its own serves one selection: large top_k with top_p goes wide
+        wide = !small && (in_step > kCand || (use_k && use_p));
+        if (!wide) {
+          for (int i0 = threadIdx.x & ~31; i0 < n; i0 += kThreads) {
+            const int i = i0 + (threadIdx.x & 31);
+            const float v = i < n ? to_f(x[i]) : -INFINITY;
+            const int bi = i < n ? bin_of(v) : kBins;
+            const bool take = small ? bi <= step : bi == step;
+            const uint32_t mask = __ballot_sync(0xffffffffu, take);
+            if (mask == 0) continue;
+            uint32_t base = 0;
+            const int leader = __ffs(mask) - 1, lane = threadIdx.x & 31;
+            if (lane == leader) base = remote_add(&sh.n_cand, 0, __popc(mask));
+            base = __shfl_sync(0xffffffffu, base, leader);
+            if (take)
+              remote_store(&sh.cand[base + __popc(mask & ((1u << lane) - 1))], 0, pack(key_of(v), lo + i));
+          }
+          cluster_barrier();
+          if (rank == 0) {
+            const int nc = small ? down : in_step;
+            const u64 in_left = sh.left, all = sh.total;
+            sort_cand(sh, nc);
+            // thread t holds sorted tokens 4t .. 4t + 3 and their weights
+            u64 w[4], s = 0, sum;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int i = threadIdx.x * 4 + e;
+              w[e] = i < nc && (small || use_p) ? weight(value_of(packed_key(sh.cand[i])), sc, sh.table) : 0ull;
+              s += w[e];
+            }
+            if (!small) {
+              // the cut: the in_left-th token of the step, or the one whose
+              // weight completes in_left
+              const u64 acc0 = block_scan(sh, s, &sum);
+              u64 acc = acc0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int i = threadIdx.x * 4 + e;
+                const bool hit = use_k ? (u64)i + 1 == in_left && i < nc : acc < in_left && in_left <= acc + w[e];
+                if (hit) {
+                  const u64 v = sh.cand[i];
+                  const u64 c64 = ((u64)packed_key(v) << 32) | (uint32_t)v;
+                  for (int c = 0; c < C; ++c) remote_store(&sh.cut, c, c64);
+                }
+                acc += w[e];
+              }
+            } else {
+              // the kept prefix: top_k of the tokens, top_p of their weight, min_p
+              const int nk = use_k ? k : nc;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if ((int)threadIdx.x * 4 + e >= nk) {
+                  s -= w[e];
+                  w[e] = 0;
+                }
+              const u64 acc0 = block_scan(sh, s, &sum);
+              u64 need_p = ~0ull;
+              if (use_p) {
+                need_p = scaled(use_k ? sum : all, p, &more);
+                need_p += more;
+                need_p = need_p ? need_p : 1;
+              }
+              // kept: what lies before it is short of need_p, and w >= least
+              u64 acc = acc0;
+              u64 kept_n = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const bool keep = w[e] >= least && acc < need_p;
+                acc += w[e];
+                kept_n += keep;
+              }
+              u64 nm;
+              block_scan(sh, kept_n, &nm);
+              __syncthreads();
+              // the kept tokens by index
+              u64 item[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int i = threadIdx.x * 4 + e;
+                const u64 v = i < (int)nm ? sh.cand[i] : 0ull;
+                item[e] = ((u64)(uint32_t)v << 32) | packed_key(v);
+              }
+              __syncthreads();
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if ((int)threadIdx.x * 4 + e < (int)nm) sh.cand[threadIdx.x * 4 + e] = item[e];
+              __syncthreads();
+              sort_cand(sh, (int)nm);
+              s = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int i = threadIdx.x * 4 + e;
+                w[e] = i < (int)nm ? weight(value_of((uint32_t)sh.cand[i]), sc, sh.table) : 0ull;
+                s += w[e];
+              }
+              acc = block_scan(sh, s, &sum);
+              const u64 target = u >= 1.f ? sum - 1 : u > 0.f ? scaled(sum, u, &more) : 0ull;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (acc <= target && target < acc + w[e])
+                  P.tokens[row] = (int)(sh.cand[threadIdx.x * 4 + e] >> 32);
+                acc += w[e];
+              }
+            }
+          }
+          if (small) return;                          // only the first block's memory is in use
+          cluster_barrier();
+          cut = true;
+          cut_key = (uint32_t)(sh.cut >> 32);
+          last = (int)(uint32_t)sh.cut;
+        }
+      }
+    }
+    if (wide) {
+      cluster_barrier();                              // the histograms have been read
+      u64 cut_left = 0;                               // tokens kept at cut_key
+      use_k = k > 0 && k < P.vocab;
+      if (use_k) cut_key = radix_select<T, false>(sh, x, n, rank, C, (u64)k, sc, -1, 0, 0, &cut_left);
+      if (use_p) {
+        const int64_t above = use_k ? (int64_t)cut_key : -1;
+        const u64 tie = use_k ? cut_left * weight(value_of(cut_key), sc, sh.table) : 0ull;
+        u64 total;
+        cluster_sum(sh, 0, n, rank, C, [&](int i) {
+          const float v = to_f(x[i]);
+          return (int64_t)key_of(v) > above ? weight(v, sc, sh.table) : 0ull;
+        }, &total);
+        total += tie;
+        bool more;
+        u64 need = scaled(total, p, &more);
+        need += more;
+        u64 left;
+        cut_key = radix_select<T, true>(sh, x, n, rank, C, need ? need : 1, sc, above, cut_key, tie, &left);
+        const u64 one = weight(value_of(cut_key), sc, sh.table);
+        cut_left = (left + one - 1) / one;
+      }
+      cut = true;
+      auto is_tie = [&](int i) { return key_of(to_f(x[i])) == cut_key ? 1ull : 0ull; };
+      u64 ties;
+      const u64 before = cluster_sum(sh, 1, n, rank, C, is_tie, &ties);
+      if (ties > cut_left) {                          // the same in every block
+        ordered_find(sh, n, before, cut_left - 1, is_tie, [&](int i) {
+          for (int c = 0; c < C; ++c) remote_store(&sh.cut, c, (u64)(lo + i));
+        });
+        cluster_barrier();
+        last = (int)sh.cut;
+      }
+    }
+  }
   auto kept = [&](int i) {
     const float v = to_f(x[i]);
     if (cut) {
-      const uint32_t key = Key<T>::of(v);
+      const uint32_t key = key_of(v);
       if (key < cut_key || (key == cut_key && lo + i > last)) return 0ull;
     }
     const u64 w = weight(v, sc, sh.table);
@@ -454,7 +721,6 @@ sample_kernel(const __grid_constant__ Params P) {
   };
   u64 total;
   const u64 before = cluster_sum(sh, 2, n, rank, C, kept, &total);
-  const float u = P.u[row];
   bool more;
   const u64 target = u >= 1.f ? total - 1 : u > 0.f ? scaled(total, u, &more) : 0ull;
   ordered_find(sh, n, before, target, kept, [&](int i) { P.tokens[row] = lo + i; });
