@@ -839,7 +839,7 @@ cb_status cb_paged_attention(const cb_paged_kv *kv, const void *q, int64_t ld_q,
  * A NaN logit counts as -inf, a token at -inf is never drawn; if several
  * logits are +inf, one of those is.  tokens: device int32 [n_rows]; -1 for a
  * row without a logit above -inf.
- * Weights are 64-bit fixed point (exp to 2^-40), so sums are exact and the
+ * Weights are 64-bit fixed point (exp to 2^-38), so sums are exact and the
  * token does not depend on their order.
  * Errors: CB_ERR_INVALID_ARG (NULL or misaligned pointers, ld_logits < vocab,
  * n_rows outside [0, 2^20]), CB_ERR_UNSUPPORTED (vocab >

@@ -395,7 +395,7 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
 }
 
 // Joins the pieces of the item whose first piece part blockIdx.x holds, four
-// rows at a time.  The weights are made once in shared memory, so the partial
+// rows per block (blockIdx.y).  The weights are made once in shared memory, so the partial
 // rows' loads depend on nothing: warp w takes every eighth piece, a lane HD /
 // 32 columns, and the warps' sums meet in shared memory.
 constexpr int kJoinThreads = 256, kJoinRows = 4;
@@ -409,70 +409,68 @@ decode_merge_kernel(const __grid_constant__ AttnParams P, int R) {
   grid_dep_wait();
   grid_dep_launch();
   const Join J = P.joins[blockIdx.x];
-  if (J.rows == 0) return;
+  if ((int)blockIdx.y * kJoinRows >= J.rows) return;
   const int first = blockIdx.x, count = J.last - first + 1;
   // a later part's first slot; this part's first or second
   auto slot = [&](int c) { return (2 * (int64_t)(first + c) + (c == 0 ? J.second : 0)) * R; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r0 = 0; r0 < J.rows; r0 += kJoinRows) {
-    for (int i = threadIdx.x; i < count * kJoinRows; i += kJoinThreads) {
-      const int c = i / kJoinRows, r = r0 + i % kJoinRows;
-      s_ml[i] = r < J.rows ? P.part_ml[slot(c) + r] : make_float2(-INFINITY, 0.f);
+  const int r0 = blockIdx.y * kJoinRows;
+  for (int i = threadIdx.x; i < count * kJoinRows; i += kJoinThreads) {
+    const int c = i / kJoinRows, r = r0 + i % kJoinRows;
+    s_ml[i] = r < J.rows ? P.part_ml[slot(c) + r] : make_float2(-INFINITY, 0.f);
+  }
+  __syncthreads();
+  if (warp < kJoinRows) {
+    float M = -INFINITY, l = 0.f;
+    for (int c = lane; c < count; c += 32) M = fmaxf(M, s_ml[c * kJoinRows + warp].x);
+    M = warp_max(M);
+    for (int c = lane; c < count; c += 32) {
+      const float2 ml = s_ml[c * kJoinRows + warp];
+      const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);   // no visible key in this piece
+      s_ml[c * kJoinRows + warp].x = w;
+      l += w * ml.y;
     }
-    __syncthreads();
-    if (warp < kJoinRows) {
-      float M = -INFINITY, l = 0.f;
-      for (int c = lane; c < count; c += 32) M = fmaxf(M, s_ml[c * kJoinRows + warp].x);
-      M = warp_max(M);
-      for (int c = lane; c < count; c += 32) {
-        const float2 ml = s_ml[c * kJoinRows + warp];
-        const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);   // no visible key in this piece
-        s_ml[c * kJoinRows + warp].x = w;
-        l += w * ml.y;
-      }
-      l = warp_sum(l);
-      if (lane == 0) s_inv[warp] = l == 0.f ? 0.f : 1.f / l;
-    }
-    __syncthreads();
-    float o[kJoinRows][PER];
+    l = warp_sum(l);
+    if (lane == 0) s_inv[warp] = l == 0.f ? 0.f : 1.f / l;
+  }
+  __syncthreads();
+  float o[kJoinRows][PER];
 #pragma unroll
-    for (int k = 0; k < kJoinRows; ++k)
+  for (int k = 0; k < kJoinRows; ++k)
 #pragma unroll
-      for (int e = 0; e < PER; ++e) o[k][e] = 0.f;
+    for (int e = 0; e < PER; ++e) o[k][e] = 0.f;
 #pragma unroll 2
-    for (int c = warp; c < count; c += NW) {
-      const float *src = P.part_o + (slot(c) + r0) * HD + lane * PER;
+  for (int c = warp; c < count; c += NW) {
+    const float *src = P.part_o + (slot(c) + r0) * HD + lane * PER;
 #pragma unroll
-      for (int k = 0; k < kJoinRows; ++k) {
-        const float w = s_ml[c * kJoinRows + k].x;
-        if (r0 + k < J.rows) {
-          float v[PER];
-          if constexpr (PER == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(src + k * HD);
-          else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(src + k * HD);
+    for (int k = 0; k < kJoinRows; ++k) {
+      const float w = s_ml[c * kJoinRows + k].x;
+      if (r0 + k < J.rows) {
+        float v[PER];
+        if constexpr (PER == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(src + k * HD);
+        else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(src + k * HD);
 #pragma unroll
-          for (int e = 0; e < PER; ++e) o[k][e] = fmaf(w, v[e], o[k][e]);
-        }
+        for (int e = 0; e < PER; ++e) o[k][e] = fmaf(w, v[e], o[k][e]);
       }
     }
+  }
 #pragma unroll
-    for (int k = 0; k < kJoinRows; ++k)
+  for (int k = 0; k < kJoinRows; ++k)
 #pragma unroll
-      for (int e = 0; e < PER; ++e) s_o[warp][k][lane * PER + e] = o[k][e];
-    __syncthreads();
-    for (int i = threadIdx.x; i < kJoinRows * HD / 2; i += kJoinThreads) {
-      const int k = i / (HD / 2), c = i % (HD / 2) * 2, l = J.l0 + r0 + k;
-      float a = 0.f, b = 0.f;
+    for (int e = 0; e < PER; ++e) s_o[warp][k][lane * PER + e] = o[k][e];
+  __syncthreads();
+  for (int i = threadIdx.x; i < kJoinRows * HD / 2; i += kJoinThreads) {
+    const int k = i / (HD / 2), c = i % (HD / 2) * 2, l = J.l0 + r0 + k;
+    float a = 0.f, b = 0.f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        a += s_o[w][k][c];
-        b += s_o[w][k][c + 1];
-      }
-      if (r0 + k < J.rows)
-        *reinterpret_cast<uint32_t *>(reinterpret_cast<bf16 *>(P.out) + (int64_t)(J.row0 + l / P.G) * P.ld_out +
-                                      (int64_t)(J.g * P.G + l % P.G) * HD + c) =
-            pack_bf16(a * s_inv[k], b * s_inv[k]);
+    for (int w = 0; w < NW; ++w) {
+      a += s_o[w][k][c];
+      b += s_o[w][k][c + 1];
     }
-    __syncthreads();
+    if (r0 + k < J.rows)
+      *reinterpret_cast<uint32_t *>(reinterpret_cast<bf16 *>(P.out) + (int64_t)(J.row0 + l / P.G) * P.ld_out +
+                                    (int64_t)(J.g * P.G + l % P.G) * HD + c) =
+          pack_bf16(a * s_inv[k], b * s_inv[k]);
   }
 }
 
@@ -489,7 +487,7 @@ static cudaError_t run(const AttnParams &P, int *status, cudaStream_t s) {
   const int grid = decode_grid();               // 32 bytes of weights for each: within the default limit
   e = launch_pdl(paged_decode_kernel<HD, WM>, dim3(grid), dim3(kDecThreads), C::kSmem, s, P, status);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(decode_merge_kernel<HD>, dim3(grid), dim3(kJoinThreads), grid * kJoinRows * sizeof(float2), s, P,
+  e = launch_pdl(decode_merge_kernel<HD>, dim3(grid, 16 * WM / kJoinRows), dim3(kJoinThreads), grid * kJoinRows * sizeof(float2), s, P,
                  16 * WM);
   return e == cudaSuccess ? launched(2) : e;
 }

@@ -10,7 +10,7 @@
 //
 // A token must not depend on the order of a sum, and a border is met to the
 // last bit only if both sides agree on the weights, so weights are 64-bit
-// fixed point numbers, w * 2^S rounded, with exp evaluated to about 2^-40:
+// fixed point numbers, w * 2^S rounded, with exp evaluated to about 2^-38:
 // every sum is then exact and the same whatever its order, and a token can
 // differ from the real-number definition only where u falls within about
 // 2^-36 of a border.  Sums of float weights would err by 2^-24, which over
@@ -30,9 +30,9 @@
 //          over the keys finds the cut instead.
 #include <math.h>
 
+#include "cb_attn_tc.cuh"
 #include "cb_common.cuh"
 #include "cb_internal.h"
-#include "cb_tc.cuh"
 
 namespace cb {
 namespace smp {
@@ -42,26 +42,46 @@ constexpr int kBins = 1024;                 // steps of the histogram
 constexpr int kCand = 2048;                 // tokens the sorter takes
 constexpr int kMaxCluster = 8;
 typedef unsigned long long u64;
+using attn::add2;
+using attn::fma2;
+using attn::hi2;
+using attn::lo2;
+using attn::pack2;
 
-// 2^(j / 64) * 2^62 for j = -32 .. 32, rounded.
-__device__ const u64 kExp2Table[65] = {
-    0x2d413cccfe779921ull, 0x2dbf6478ca345de4ull, 0x2e3eebd1d8bee7baull, 0x2ebfd6ac84cf917full,
-    0x2f4228e7d6030db0ull, 0x2fc5e66d9e9cc421ull, 0x304b1332999c2516ull, 0x30d1b3368925d902ull,
-    0x3159ca845541b6b7ull, 0x31e35d322aee6c57ull, 0x326e6f619b8bc9e9ull, 0x32fb053fbc9c9f17ull,
-    0x3389230547e12039ull, 0x3418ccf6bbcac965ull, 0x34aa07647c4ab917ull, 0x353cd6aaf3fb7e88ull,
-    0x35d13f32b5a75abdull, 0x366745709e2bf5edull, 0x36feede5f6bc8dd5ull, 0x37983d209783a449ull,
-    0x383337bb0aa53844ull, 0x38cfe25cafa29694ull, 0x396e41b9df20d22aull, 0x3a0e5a940f12f71aull,
-    0x3ab031b9f7490e4cull, 0x3b53cc07b6650ae1ull, 0x3bf92e66f736bd73ull, 0x3ca05dcf167fec4eull,
-    0x3d495f454921b30bull, 0x3df437dcc2b44eeeull, 0x3ea0ecb6dc8a80cfull, 0x3f4f83033d21b05dull,
-    0x4000000000000000ull, 0x40b268f9de0183baull, 0x4166c34c5615d0ecull, 0x421d1461d66f2023ull,
-    0x42d561b3e6243d8aull, 0x438fb0cb4f468808ull, 0x444c0740496d4294ull, 0x450a6abaa4b77ecdull,
-    0x45cae0f1f545eb73ull, 0x468d6fadbf2dd4f3ull, 0x47521cc5a2e6a9e0ull, 0x4818ee218a3358eeull,
-    0x48e1e9b9d588e19bull, 0x49ad159789f37496ull, 0x4a7a77d47f7b84b1ull, 0x4b4a169b900c2d00ull,
-    0x4c1bf828c6dc54b8ull, 0x4cf022c9905bfd32ull, 0x4dc69cdceaa72a9cull, 0x4e9f6cd3967fdba8ull,
-    0x4f7a993048d088d7ull, 0x50582887dcb8a7e1ull, 0x513821818624b40cull, 0x521a8ad704f3404full,
-    0x52ff6b54d8a89c75ull, 0x53e6c9da74b29ab5ull, 0x54d0ad5a753e077cull, 0x55bd1cdad49f699cull,
-    0x56ac1f752150a563ull, 0x579dbc56b48521baull, 0x5891fac0e95612c8ull, 0x5988e20954889245ull,
-    0x5a827999fcef3242ull,
+// 2^(j / 128) * 2^62 for j = 0 .. 127, rounded.
+__device__ const u64 kExp2Table[128] = {
+    0x4000000000000000ull, 0x4058f6a7ecccd5b6ull, 0x40b268f9de0183baull, 0x410c57a1b9fe12f6ull,
+    0x4166c34c5615d0ecull, 0x41c1aca777db771bull, 0x421d1461d66f2023ull, 0x4278fb2b1bce0d15ull,
+    0x42d561b3e6243d8aull, 0x433248adc91fdd02ull, 0x438fb0cb4f468808ull, 0x43ed9abffb4c6bc9ull,
+    0x444c0740496d4294ull, 0x44aaf701b0c72feeull, 0x450a6abaa4b77ecdull, 0x456a632296394492ull,
+    0x45cae0f1f545eb73ull, 0x462be4e23237a6efull, 0x468d6fadbf2dd4f3ull, 0x46ef821011734e6bull,
+    0x47521cc5a2e6a9e0ull, 0x47b5408bf36472e2ull, 0x4818ee218a3358eeull, 0x487d2645f7725895ull,
+    0x48e1e9b9d588e19bull, 0x4947393eca98fcd6ull, 0x49ad159789f37496ull, 0x4a137f87d58e025bull,
+    0x4a7a77d47f7b84b1ull, 0x4ae1ff436b663ff7ull, 0x4b4a169b900c2d00ull, 0x4bb2bea4f8bd5847ull,
+    0x4c1bf828c6dc54b8ull, 0x4c85c3f13360c4d5ull, 0x4cf022c9905bfd32ull, 0x4d5b157e4a7fc325ull,
+    0x4dc69cdceaa72a9cull, 0x4e32b9b417619617ull, 0x4e9f6cd3967fdba8ull, 0x4f0cb70c4ea39210ull,
+    0x4f7a993048d088d7ull, 0x4fe91412b2006e83ull, 0x50582887dcb8a7e1ull, 0x50c7d76542a25b72ull,
+    0x513821818624b40cull, 0x51a907b474015dc9ull, 0x521a8ad704f3404full, 0x528cabc35f4f799dull,
+    0x52ff6b54d8a89c75ull, 0x5372ca67f774358full, 0x53e6c9da74b29ab5ull, 0x545b6a8b3d990704ull,
+    0x54d0ad5a753e077cull, 0x5546932976483b15ull, 0x55bd1cdad49f699cull, 0x56344b525f1ff495ull,
+    0x56ac1f752150a563ull, 0x57249a29651adc07ull, 0x579dbc56b48521baull, 0x581786e5db7022c2ull,
+    0x5891fac0e95612c8ull, 0x590d18d3330c7f1eull, 0x5988e20954889245ull, 0x5a05575132a5cc20ull,
+    0x5a827999fcef3242ull, 0x5b0049d42f6afbb6ull, 0x5b7ec8f19468bbc9ull, 0x5bfdf7e546520f3eull,
+    0x5c7dd7a3b17dcf75ull, 0x5cfe69229605cef5ull, 0x5d7fad59099f22feull, 0x5e01a53f7974fd86ull,
+    0x5e8451cfac061b5full, 0x5f07b404c304c9f1ull, 0x5f8bccdb3d398841ull, 0x60109d50f86846d8ull,
+    0x6096266533384a2bull, 0x611c69188f1eb339ull, 0x61a3666d124bb204ull, 0x622b1f66299a6599ull,
+    0x62b39508aa836d6full, 0x633cc85ad5122fbdull, 0x63c6ba6455dcd8aeull, 0x64516c2e47ff1623ull,
+    0x64dcdec3371793d1ull, 0x6569132f21483ba7ull, 0x65f60a7f79393e2eull, 0x6683c5c3281ee6e9ull,
+    0x6712460a8fc24072ull, 0x67a18c678c8c8c61ull, 0x683199ed779592caull, 0x68c26fb128b4cd63ull,
+    0x69540ec8f895722dull, 0x69e6784cc2cd61bdull, 0x6a79ad55e7f6fd10ull, 0x6b0daeff4fcde703ull,
+    0x6ba27e656b4eb57aull, 0x6c381ca636d99642ull, 0x6cce8ae13c57ebdbull, 0x6d65ca379564e639ull,
+    0x6dfddbcbed791babull, 0x6e96c0c284192610ull, 0x6f307a412f074892ull, 0x6fcb096f5c782210ull,
+    0x70666f76154a7089ull, 0x7102ad7fff41e9b4ull, 0x719fc4b95f452d29ull, 0x723db6501b9ed447ull,
+    0x72dc8373be41a454ull, 0x737c2d55770fe711ull, 0x741cb5281e25ee34ull, 0x74be1c203627c62bull,
+    0x75606373ee921c97ull, 0x76038c5b260e5eeeull, 0x76a7980f6cca15c2ull, 0x774c87cc06d1812eull,
+    0x77f25ccdee6d7ae6ull, 0x78991853d684a285ull, 0x7940bb9e2cffd89dull, 0x79e947ef1d320d2dull,
+    0x7a92be8a92436616ull, 0x7b3d20b6399fc237ull, 0x7be86fb985689ddcull, 0x7c94acddaeea5d3aull,
+    0x7d41d96db915019dull, 0x7deff6b672f84e24ull, 0x7e9f06067a4360baull, 0x7f4f08ae3dc7c426ull,
 };
 
 struct Params {
@@ -81,39 +101,54 @@ struct Scale {
   int shift;
 };
 
-// w * 2^S of one logit.  (x - X) log2(e) / t is formed as an unevaluated sum
-// of two floats (the subtraction's and the product's errors are exact by
-// two-sum and fma); its integer part becomes a shift, the next six bits a
-// table entry, and the rest e (|e| <= 2^-7) enters 2^e - 1 = y + y^2/2 +
-// y^3/6 + y^4/24, y = e ln 2, whose first term is again a two-float product.
-__device__ __forceinline__ u64 weight(float x, const Scale &c, const u64 *table) {
-  if (x == c.top) return 1ull << c.shift;
-  const float dh = x - c.top;
-  const float ph = dh * c.ch;
-  if (!(ph > -(float)(c.shift + 2))) return 0ull;      // below half a unit; -inf
-  const float bb = dh - x;
-  const float dl = (x - (dh - bb)) + (-c.top - bb);
-  float pl = fmaf(dh, c.ch, -ph);
-  pl = fmaf(dh, c.cl, pl);
-  pl = fmaf(dl, c.ch, pl);
-  const float n = rintf(ph), f = ph - n;
-  const float jf = rintf(f * 64.f);
-  const float e = fmaf(jf, -1.f / 64.f, f);            // exact
+// w * 2^S of two logits, on packed pairs of floats.  (x - X) log2(e) / t is
+// formed as an unevaluated sum ph + pl of two floats: two-sum gives the
+// subtraction's error, fma the product's.  Adding and taking away a large
+// constant rounds ph to a multiple of 1/128, whose integer part becomes a
+// shift and whose rest picks a table entry; e = ph - that (|e| <= 2^-8) and
+// pl enter 2^(e + pl) - 1 = e ln 2 + pl ln 2 + (e + pl)^2 (c2 + e (c3 + e c4)),
+// the first product again as two floats.  The large part on a grid of 2^-30
+// and the rest on one of 2^-38 are read off as integers the same way, and one
+// 32 x 32 bit product scales the table entry.  Relative error about 2^-38.
+__device__ __forceinline__ void weight2(float x0, float x1, const Scale &c, const u64 *table, u64 &w0, u64 &w1) {
+  typedef unsigned long long P2;
+  constexpr float kM1 = 98304.f;                    // 1.5 * 2^16: steps of 2^-7
+  constexpr float kM2 = 0x1.8p-7f, kM3 = 0x1.8p-15f; // steps of 2^-30 (|.| < 2^-8) and 2^-38 (< 2^-16)
   constexpr float kLn2h = 0x1.62e430p-1f, kLn2l = -1.9046543e-9f;   // ln 2
-  const float yh = e * kLn2h;
-  float yl = fmaf(e, kLn2h, -yh);
-  yl = fmaf(e, kLn2l, yl);
-  yl = fmaf(pl, kLn2h, yl);
-  // yh on a grid of 2^-38, what is left of it to the small terms
-  const float gh = rintf(yh * 0x1p38f);
-  const float rest = fmaf(gh, -0x1p-38f, yh) + yl;
-  const float y = yh + yl;
-  const float q = fmaf(fmaf(y, 1.f / 24.f, 1.f / 6.f), y, 0.5f);
-  const float small = fmaf(y * y, q, rest);            // |.| < 2^-14
-  const long long m46 = (1ll << 46) + ((long long)(int)gh << 8) + (long long)(int)rintf(small * 0x1p46f);
-  const u64 w60 = __umul64hi((u64)m46 << 16, table[(int)jf + 32]);   // 2^(f) * 2^60
-  const int sh = 60 - c.shift - (int)n;
-  return sh > 63 ? 0ull : (w60 + (1ull << (sh - 1))) >> sh;
+  constexpr float kC2 = 2.402265070e-1f, kC3 = 5.550410866e-2f, kC4 = 9.618129108e-3f;   // ln2^k / k!
+  auto both = [](float v) { return pack2(v, v); };
+  const P2 neg = both(-1.f), X = pack2(x0, x1), T = both(-c.top), ch = both(c.ch);
+  const P2 D = add2(X, T), B = fma2(X, neg, D);
+  const P2 DL = add2(fma2(fma2(B, neg, D), neg, X), fma2(B, neg, T));
+  const P2 PH = fma2(D, ch, both(0.f));
+  P2 PL = fma2(D, ch, fma2(D, both(-c.ch), both(0.f)));
+  PL = fma2(DL, ch, fma2(D, both(c.cl), PL));
+  const P2 R = add2(PH, both(kM1)), E = fma2(add2(R, both(-kM1)), neg, PH), EP = add2(E, PL);
+  const P2 YH = fma2(E, both(kLn2h), both(0.f));
+  P2 YL = fma2(E, both(kLn2h), fma2(E, both(-kLn2h), both(0.f)));
+  YL = fma2(PL, both(kLn2h), fma2(E, both(kLn2l), YL));
+  YL = fma2(fma2(EP, EP, both(0.f)), fma2(EP, fma2(EP, both(kC4), both(kC3)), both(kC2)), YL);
+  const P2 R2 = add2(YH, both(kM2)), SM = add2(fma2(add2(R2, both(-kM2)), neg, YH), YL), R3 = add2(SM, both(kM3));
+  auto fixed = [&](float ph, float r, float r2, float r3) -> u64 {
+    const int k = __float_as_int(r) - __float_as_int(kM1);
+    const int q = ((__float_as_int(r2) - __float_as_int(kM2)) << 8) + (__float_as_int(r3) - __float_as_int(kM3));
+    const u64 t = table[k & 127];
+    const u64 w62 = t + (u64)(((long long)(int)(uint32_t)(t >> 32) * q) >> 6);
+    const int sh = min(62 - c.shift - (k >> 7), 64);
+    // below half a unit, or -inf (whose integers are meaningless)
+    return ph > -(float)(c.shift + 2) ? ((w62 >> (sh - 1)) + 1) >> 1 : 0ull;
+  };
+  w0 = fixed(lo2(PH), lo2(R), lo2(R2), lo2(R3));
+  w1 = fixed(hi2(PH), hi2(R), hi2(R2), hi2(R3));
+  if (c.top == INFINITY) {                          // tokens at +inf share the draw
+    w0 = x0 == c.top ? 1ull << c.shift : 0ull;
+    w1 = x1 == c.top ? 1ull << c.shift : 0ull;
+  }
+}
+__device__ __forceinline__ u64 weight(float x, const Scale &c, const u64 *table) {
+  u64 w, none;
+  weight2(x, -INFINITY, c, table, w, none);
+  return w;
 }
 
 // floor(a * f) for f in [0, 1], a < 2^63; `inexact`: the product has a
@@ -144,15 +179,15 @@ struct Shared {
   };
   u64 rmass[kBins];         // the bins this block reduces over the cluster
   uint32_t rcnt[kBins];
-  u64 table[65];
+  u64 table[128];
   u64 warp[kWarps];         // a pass's sum per warp
   u64 sum[3];               // this block's sums: weights to cut, ties, kept weights
   u64 best;                 // this block's largest (key, ~index)
   float least;              // and its smallest logit above -inf
-  uint32_t n_cand;
   u64 left, total;          // a search's answer
   int bin, count;
   u64 cut;                  // the cut: key << 32 | last index kept with that key
+  float ch, cl;             // log2(e) / temperature
 };
 
 // Order-preserving integer of a float, and back.
@@ -175,33 +210,35 @@ __device__ __forceinline__ void cluster_barrier() {
   __syncwarp();
   tcx::cluster_sync();
 }
-// The same shared variable in block `rank` of the cluster.
+// The same shared variable in block `rank` of the cluster.  What it reads was
+// written before the last cluster barrier, so several reads may be in flight.
 __device__ __forceinline__ u64 remote(const u64 *p, uint32_t rank) {
   u64 v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];"
-               : "=l"(v) : "r"(tcx::map_to_rank(smem_u32(p), rank)) : "memory");
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(tcx::map_to_rank(smem_u32(p), rank)));
   return v;
 }
 __device__ __forceinline__ uint32_t remote(const uint32_t *p, uint32_t rank) {
   uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];"
-               : "=r"(v) : "r"(tcx::map_to_rank(smem_u32(p), rank)) : "memory");
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(tcx::map_to_rank(smem_u32(p), rank)));
   return v;
 }
 __device__ __forceinline__ float remote(const float *p, uint32_t rank) {
   return __uint_as_float(remote(reinterpret_cast<const uint32_t *>(p), rank));
 }
+// Sum of the same variable over the cluster's C blocks.
+__device__ __forceinline__ u64 remote_sum(const uint32_t *p, int C) {
+  uint32_t v[kMaxCluster];
+#pragma unroll
+  for (int c = 0; c < kMaxCluster; ++c) v[c] = c < C ? remote(p, c) : 0u;
+  u64 s = 0;
+#pragma unroll
+  for (int c = 0; c < kMaxCluster; ++c) s += v[c];
+  return s;
+}
 __device__ __forceinline__ void remote_store(u64 *p, uint32_t rank, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(tcx::map_to_rank(smem_u32(p), rank)), "l"(v)
                : "memory");
 }
-__device__ __forceinline__ uint32_t remote_add(uint32_t *p, uint32_t rank, uint32_t v) {
-  uint32_t old;
-  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
-               : "=r"(old) : "r"(tcx::map_to_rank(smem_u32(p), rank)), "r"(v) : "memory");
-  return old;
-}
-
 // Exclusive prefix sum of v over the block, the block's sum in *total.
 __device__ __forceinline__ u64 block_scan(Shared &sh, u64 v, u64 *total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -214,15 +251,16 @@ __device__ __forceinline__ u64 block_scan(Shared &sh, u64 v, u64 *total) {
   __syncthreads();
   if (lane == 31) sh.warp[warp] = incl;
   __syncthreads();
-  u64 before = 0, all = 0;
+  // every warp scans the warps' sums
+  u64 w = lane < kWarps ? sh.warp[lane] : 0ull;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const u64 t = sh.warp[w];
-    before += w < warp ? t : 0;
-    all += t;
+  for (int o = 1; o < kWarps; o <<= 1) {
+    const u64 t = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += t;
   }
-  *total = all;
-  return before + incl - v;
+  *total = __shfl_sync(0xffffffffu, w, kWarps - 1);
+  const u64 before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  return (warp ? before : 0ull) + incl - v;
 }
 
 // Adds a weight to bin b of this block's histogram, in three 16-bit parts:
@@ -233,8 +271,10 @@ __device__ __forceinline__ void add_weight(Shared &sh, int b, u64 m) {
   if (hi) atomicAdd(&sh.m1[b], hi);
   if (top) atomicAdd(&sh.m2[b], top);
 }
-__device__ __forceinline__ u64 remote_weight(const Shared &sh, int b, int rank) {
-  return (u64)remote(&sh.m0[b], rank) + ((u64)remote(&sh.m1[b], rank) << 16) + ((u64)remote(&sh.m2[b], rank) << 32);
+// A bin's weight over the cluster.
+__device__ __forceinline__ u64 remote_weight(const Shared &sh, int b, int C) {
+  const u64 p0 = remote_sum(&sh.m0[b], C), p1 = remote_sum(&sh.m1[b], C), p2 = remote_sum(&sh.m2[b], C);
+  return p0 + (p1 << 16) + (p2 << 32);
 }
 
 // The consecutive range of a block's n tokens that warp w owns.
@@ -242,75 +282,96 @@ __device__ __forceinline__ int warp_begin(int n, int w) {
   return min(n, w * (((n + kWarps - 1) / kWarps + 31) / 32 * 32));
 }
 
-// This block's sum of f(i) over its tokens, left in sh.sum[slot] and, per
+// A pass weighs its tokens in pairs: f(xa, a, xb, b, wa, wb) gives the weights
+// of tokens a and b of the slice; a token past its end has index -1 and x
+// -inf and must get 0.
+
+// This block's sum of a pass over its tokens, left in sh.sum[slot] and, per
 // warp, in sh.warp; then meets the cluster.  Returns the sums of the blocks
 // before this one, and of all in *total.
-template <typename F>
-__device__ __forceinline__ u64 cluster_sum(Shared &sh, int slot, int n, int rank, int C, F f, u64 *total) {
+template <typename T, typename F>
+__device__ __forceinline__ u64 cluster_sum(Shared &sh, int slot, const T *x, int n, int rank, int C, F f,
+                                           u64 *total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int e = warp_begin(n, warp + 1);
   u64 s = 0;
-  for (int i = warp_begin(n, warp) + lane; i < e; i += 32) s += f(i);
+#pragma unroll 2
+  for (int i = warp_begin(n, warp) + lane; i < e; i += 64) {
+    const bool two = i + 32 < e;
+    u64 wa, wb;
+    f(to_f(x[i]), i, two ? to_f(x[i + 32]) : -INFINITY, two ? i + 32 : -1, wa, wb);
+    s += wa + wb;
+  }
   s = warp_sum64(s);
   __syncthreads();
   if (lane == 0) sh.warp[warp] = s;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    u64 t = 0;
-    for (int w = 0; w < kWarps; ++w) t += sh.warp[w];
-    sh.sum[slot] = t;
+  if (warp == 0) {
+    const u64 t = warp_sum64(lane < kWarps ? sh.warp[lane] : 0ull);
+    if (lane == 0) sh.sum[slot] = t;
   }
   cluster_barrier();
-  u64 before = 0, all = 0;
-  for (int c = 0; c < C; ++c) {
-    const u64 v = remote(&sh.sum[slot], c);
-    if (c < rank) before += v;
-    all += v;
+  u64 v[kMaxCluster], before = 0, all = 0;
+#pragma unroll
+  for (int c = 0; c < kMaxCluster; ++c) v[c] = c < C ? remote(&sh.sum[slot], c) : 0ull;
+#pragma unroll
+  for (int c = 0; c < kMaxCluster; ++c) {
+    if (c < rank) before += v[c];
+    all += v[c];
   }
   *total = all;
   return before;
 }
 
-// After cluster_sum over the same f: the token at which the running sum over
+// After cluster_sum of the same pass: the token at which the running sum over
 // the cluster, `before` at this block's first token, first exceeds `target`
-// is passed to found(i) by one thread of the block that holds it.
-template <typename F, typename G>
-__device__ __forceinline__ void ordered_find(const Shared &sh, int n, u64 before, u64 target, F f, G found) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  u64 acc = before;
-  for (int w = 0; w < warp; ++w) acc += sh.warp[w];
-  if (target < acc || target >= acc + sh.warp[warp]) return;
-  const int e = warp_begin(n, warp + 1);
-  for (int i0 = warp_begin(n, warp); i0 < e; i0 += 32) {
-    u64 v = i0 + lane < e ? f(i0 + lane) : 0ull;
+// is passed to found(i) by one thread of the block that holds it.  The block
+// scans the range of the warp that holds the token with all its threads.
+template <typename T, typename F, typename G>
+__device__ __forceinline__ void ordered_find(Shared &sh, int slot, const T *x, int n, u64 before, u64 target, F f,
+                                             G found) {
+  if (target < before || target >= before + sh.sum[slot]) return;   // the same in the whole block
+  int w = 0;
+  while (target >= before + sh.warp[w]) before += sh.warp[w++];
+  const int b = warp_begin(n, w), e = warp_begin(n, w + 1);
+  const int per = (e - b + kThreads - 1) / kThreads;
+  static_assert(CB_MAX_SAMPLE_VOCAB / kMaxCluster / kWarps <= 4 * kThreads, "four tokens per thread");
+  const int i0 = b + (int)threadIdx.x * per, i1 = min(e, i0 + per);
+  u64 v[4], s = 0, total;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const u64 t = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += t;
-    }
-    const uint32_t hit = __ballot_sync(0xffffffffu, acc + v > target);
-    if (hit) {
-      if (lane == __ffs(hit) - 1) found(i0 + lane);
-      return;
-    }
-    acc += __shfl_sync(0xffffffffu, v, 31);
+  for (int k = 0; k < 4; k += 2) {
+    const int i = i0 + k;
+    v[k] = v[k + 1] = 0;
+    if (i < i1) f(to_f(x[i]), i, i + 1 < i1 ? to_f(x[i + 1]) : -INFINITY, i + 1 < i1 ? i + 1 : -1, v[k], v[k + 1]);
+    s += v[k] + v[k + 1];
+  }
+  u64 acc = before + block_scan(sh, s, &total);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (acc <= target && target < acc + v[k]) found(i0 + k);
+    acc += v[k];
   }
 }
 
-// Sorts a[0 .. n) ascending (n a power of two); the block's threads all call.
+// Sorts a[0 .. n) ascending (n a power of two, bitonic); the block's threads
+// all call.  Exchanges over at most 32 places stay inside the 64 tokens of one
+// warp, so only the wider ones meet the block.
 __device__ __forceinline__ void sort_block(u64 *a, int n) {
   for (int k = 2; k <= n; k <<= 1)
     for (int j = k >> 1; j; j >>= 1) {
+      if (j >= 64) __syncthreads();
       for (int t = threadIdx.x; t < n / 2; t += kThreads) {
-        const int i = (t / j) * 2 * j + t % j, l = i + j;
+        const int i = ((t & ~(j - 1)) << 1) | (t & (j - 1)), l = i + j;
         const u64 x = a[i], y = a[l];
         if ((x > y) == ((i & k) == 0)) {
           a[i] = y;
           a[l] = x;
         }
       }
-      __syncthreads();
+      if (j >= 64) __syncthreads();
+      else __syncwarp();
     }
+  __syncthreads();
 }
 // Sorts the first n gathered tokens (padded to a power of two); returns that
 // power.
@@ -357,8 +418,7 @@ __device__ __forceinline__ uint32_t radix_select(Shared &sh, const T *x, int n, 
     }
     cluster_barrier();
     for (int b = rank * per + threadIdx.x; b < (rank + 1) * per; b += kThreads) {
-      u64 s = 0;
-      for (int c = 0; c < C; ++c) s += MASS ? remote_weight(sh, b, c) : (u64)remote(&sh.cnt[b], c);
+      u64 s = MASS ? remote_weight(sh, b, C) : remote_sum(&sh.cnt[b], C);
       if (MASS && extra_mass && (hi == 32 || (extra_key >> hi) == prefix) &&
           ((extra_key >> lo) & (nb - 1)) == (uint32_t)b)
         s += extra_mass;
@@ -451,8 +511,7 @@ sample_kernel(const __grid_constant__ Params P) {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
   const int C = (int)csize, row = blockIdx.x / C;
   const int lo = min(P.vocab, rank * P.slice), n = min(P.vocab, lo + P.slice) - lo;
-  if (threadIdx.x < 65) sh.table[threadIdx.x] = kExp2Table[threadIdx.x];
-  if (threadIdx.x == 0) sh.n_cand = 0;
+  if (threadIdx.x < 128) sh.table[threadIdx.x] = kExp2Table[threadIdx.x];
   for (int i = threadIdx.x; i < kBins; i += kThreads) sh.cnt[i] = sh.m0[i] = sh.m1[i] = sh.m2[i] = 0;
   grid_dep_wait();
   grid_dep_launch();
@@ -461,14 +520,26 @@ sample_kernel(const __grid_constant__ Params P) {
   const float p = P.top_p ? P.top_p[row] : 1.f;
   const float mp = P.min_p ? P.min_p[row] : 0.f;
   const float u = P.u[row];
+  if (threadIdx.x == kThreads - 1) {
+    // log2(e) / t as two floats, by one thread: double precision is scarce
+    // (a temperature below 1e-30 acts as 1e-30)
+    const double c = 1.4426950408889634 / (double)fmaxf(temp, 1e-30f);
+    sh.ch = (float)c;
+    sh.cl = (float)(c - (double)sh.ch);
+  }
   load_slice(sh, x, reinterpret_cast<const T *>(P.logits) + (int64_t)row * P.ld + lo, n, lo);
   cluster_barrier();
-  u64 best = 0;
-  float low = INFINITY;
-  for (int c = 0; c < C; ++c) {
-    const u64 t = remote(&sh.best, c);
-    best = t > best ? t : best;
-    low = fminf(low, remote(&sh.least, c));
+  u64 best = 0, bests[kMaxCluster];
+  float low = INFINITY, lows[kMaxCluster];
+#pragma unroll
+  for (int c = 0; c < kMaxCluster; ++c) {
+    bests[c] = c < C ? remote(&sh.best, c) : 0ull;
+    lows[c] = c < C ? remote(&sh.least, c) : INFINITY;
+  }
+#pragma unroll
+  for (int c = 0; c < kMaxCluster; ++c) {
+    best = bests[c] > best ? bests[c] : best;
+    low = fminf(low, lows[c]);
   }
   const bool empty = best == 0;                       // every logit is -inf or NaN
   if (empty || !(temp > 0.f) || k == 1 || p <= 0.f) {
@@ -479,12 +550,8 @@ sample_kernel(const __grid_constant__ Params P) {
   Scale sc;
   sc.top = value_of((uint32_t)(best >> 32));
   sc.shift = P.shift;
-  {
-    // log2(e) / t as two floats; a temperature below 1e-30 acts as 1e-30
-    const double c = 1.4426950408889634 / (double)fmaxf(temp, 1e-30f);
-    sc.ch = (float)c;
-    sc.cl = (float)(c - (double)sc.ch);
-  }
+  sc.ch = sh.ch;
+  sc.cl = sh.cl;
   bool use_k = k > 0 && k < P.vocab;
   const bool use_p = p < 1.f;
   u64 least = 1;                                      // min_p of the largest weight
@@ -507,27 +574,24 @@ sample_kernel(const __grid_constant__ Params P) {
     };
     wide = sc.top == INFINITY;                        // no distance to measure by
     if (!wide) {
-      for (int i = threadIdx.x; i < n; i += kThreads) {
-        const float v = to_f(x[i]);
-        const int b = bin_of(v);
-        if (b >= kBins) continue;
-        atomicAdd(&sh.cnt[b], 1u);
+#pragma unroll 2
+      for (int i = threadIdx.x; i < n; i += 2 * kThreads) {
+        const float xa = to_f(x[i]), xb = i + kThreads < n ? to_f(x[i + kThreads]) : -INFINITY;
+        const int ba = bin_of(xa), bb = bin_of(xb);
+        if (ba < kBins) atomicAdd(&sh.cnt[ba], 1u);
+        if (bb < kBins) atomicAdd(&sh.cnt[bb], 1u);
         if (use_p) {
-          const u64 m = weight(v, sc, sh.table);
-          if (m) add_weight(sh, b, m);
+          u64 wa, wb;
+          weight2(xa, xb, sc, sh.table, wa, wb);
+          if (wa) add_weight(sh, ba, wa);
+          if (wb) add_weight(sh, bb, wb);
         }
       }
       cluster_barrier();
       const int per = kBins / C;
       for (int b = rank * per + threadIdx.x; b < (rank + 1) * per; b += kThreads) {
-        u64 s = 0;
-        uint32_t q = 0;
-        for (int c = 0; c < C; ++c) {
-          q += remote(&sh.cnt[b], c);
-          if (use_p) s += remote_weight(sh, b, c);
-        }
-        sh.rmass[b] = s;
-        sh.rcnt[b] = q;
+        sh.rcnt[b] = (uint32_t)remote_sum(&sh.cnt[b], C);
+        if (use_p) sh.rmass[b] = remote_weight(sh, b, C);
       }
       cluster_barrier();
       // every block scans all bins, two per thread, from the maximum down
@@ -565,33 +629,62 @@ sample_kernel(const __grid_constant__ Params P) {
         // a step of its own serves one selection: large top_k with top_p goes wide
         wide = !small && (in_step > kCand || (use_k && use_p));
         if (!wide) {
-          for (int i0 = threadIdx.x & ~31; i0 < n; i0 += kThreads) {
-            const int i = i0 + (threadIdx.x & 31);
-            const float v = i < n ? to_f(x[i]) : -INFINITY;
-            const int bi = i < n ? bin_of(v) : kBins;
-            const bool take = small ? bi <= step : bi == step;
-            const uint32_t mask = __ballot_sync(0xffffffffu, take);
-            if (mask == 0) continue;
-            uint32_t base = 0;
-            const int leader = __ffs(mask) - 1, lane = threadIdx.x & 31;
-            if (lane == leader) base = remote_add(&sh.n_cand, 0, __popc(mask));
-            base = __shfl_sync(0xffffffffu, base, leader);
-            if (take)
-              remote_store(&sh.cand[base + __popc(mask & ((1u << lane) - 1))], 0, pack(key_of(v), lo + i));
-          }
+          // Every warp counts its tokens (its range is consecutive), then
+          // stores them at their places: the list comes in vocabulary order.
+          auto takes = [&](float v) -> bool {          // the same floats as bin_of
+            const float t = (sc.top - v) * scale;
+            return t < (float)(step + 1) && (small || t >= (float)step);
+          };
+          const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+          const int wb = warp_begin(n, warp), we = warp_begin(n, warp + 1);
+          u64 all_taken;
+          const u64 taken_before =
+              cluster_sum(sh, 0, x, n, rank, C, [&](float xa, int, float xb, int, u64 &wa, u64 &wb) {
+                wa = takes(xa);
+                wb = takes(xb);
+              }, &all_taken);
+          uint32_t at = (uint32_t)taken_before;
+          for (int w = 0; w < warp; ++w) at += (uint32_t)sh.warp[w];
+          if (sh.warp[warp])
+#pragma unroll 2
+            for (int i0 = wb; i0 < we; i0 += 32) {
+              const float v = i0 + lane < we ? to_f(x[i0 + lane]) : -INFINITY;
+              const bool take = takes(v);
+              const uint32_t mask = __ballot_sync(0xffffffffu, take);
+              if (take)
+                remote_store(&sh.cand[at + __popc(mask & ((1u << lane) - 1))], 0, pack(key_of(v), lo + i0 + lane));
+              at += __popc(mask);
+            }
           cluster_barrier();
           if (rank == 0) {
             const int nc = small ? down : in_step;
             const u64 in_left = sh.left, all = sh.total;
+            // weights of list entries 4t .. 4t + 3 (thread t), 0 past `n` and
+            // after `cut` in sorted order
+            auto weigh4 = [&](const u64 *list, int n, u64 cut, u64 (&w)[4]) {
+#pragma unroll
+              for (int e = 0; e < 4; e += 2) {
+                const int i = threadIdx.x * 4 + e;
+                w[e] = w[e + 1] = 0;
+                if (i >= n) continue;
+                const u64 a = list[i], b = i + 1 < n ? list[i + 1] : ~0ull;
+                weight2(value_of(packed_key(a)), i + 1 < n ? value_of(packed_key(b)) : -INFINITY, sc, sh.table, w[e],
+                        w[e + 1]);
+                if (a > cut) w[e] = 0;
+                if (b > cut) w[e + 1] = 0;
+              }
+            };
+            // a copy in vocabulary order stays in the slice's place, which the
+            // first block no longer needs if it finishes the row
+            u64 *listed = reinterpret_cast<u64 *>(x);
+            if (small)
+              for (int i = threadIdx.x; i < nc; i += kThreads) listed[i] = sh.cand[i];
             sort_cand(sh, nc);
             // thread t holds sorted tokens 4t .. 4t + 3 and their weights
             u64 w[4], s = 0, sum;
+            weigh4(sh.cand, small || use_p ? nc : 0, ~0ull, w);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int i = threadIdx.x * 4 + e;
-              w[e] = i < nc && (small || use_p) ? weight(value_of(packed_key(sh.cand[i])), sc, sh.table) : 0ull;
-              s += w[e];
-            }
+            for (int e = 0; e < 4; ++e) s += w[e];
             if (!small) {
               // the cut: the in_left-th token of the step, or the one whose
               // weight completes in_left
@@ -624,45 +717,29 @@ sample_kernel(const __grid_constant__ Params P) {
                 need_p += more;
                 need_p = need_p ? need_p : 1;
               }
-              // kept: what lies before it is short of need_p, and w >= least
+              // kept: what lies before it is short of need_p, and w >= least;
+              // the last kept token in sorted order is the cut
               u64 acc = acc0;
-              u64 kept_n = 0;
+              int kept_n = 0;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const bool keep = w[e] >= least && acc < need_p;
+                kept_n += w[e] >= least && acc < need_p;
                 acc += w[e];
-                kept_n += keep;
               }
-              u64 nm;
-              block_scan(sh, kept_n, &nm);
+              if (__syncthreads_count(kept_n > 0) == (int)threadIdx.x + 1)
+                sh.cut = sh.cand[threadIdx.x * 4 + kept_n - 1];
               __syncthreads();
-              // the kept tokens by index
-              u64 item[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int i = threadIdx.x * 4 + e;
-                const u64 v = i < (int)nm ? sh.cand[i] : 0ull;
-                item[e] = ((u64)(uint32_t)v << 32) | packed_key(v);
-              }
-              __syncthreads();
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if ((int)threadIdx.x * 4 + e < (int)nm) sh.cand[threadIdx.x * 4 + e] = item[e];
-              __syncthreads();
-              sort_cand(sh, (int)nm);
+              const u64 cut_at = sh.cut;
               s = 0;
+              weigh4(listed, nc, cut_at, w);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int i = threadIdx.x * 4 + e;
-                w[e] = i < (int)nm ? weight(value_of((uint32_t)sh.cand[i]), sc, sh.table) : 0ull;
-                s += w[e];
-              }
+              for (int e = 0; e < 4; ++e) s += w[e];
               acc = block_scan(sh, s, &sum);
               const u64 target = u >= 1.f ? sum - 1 : u > 0.f ? scaled(sum, u, &more) : 0ull;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 if (acc <= target && target < acc + w[e])
-                  P.tokens[row] = (int)(sh.cand[threadIdx.x * 4 + e] >> 32);
+                  P.tokens[row] = (int)(uint32_t)listed[threadIdx.x * 4 + e];
                 acc += w[e];
               }
             }
@@ -684,9 +761,10 @@ sample_kernel(const __grid_constant__ Params P) {
         const int64_t above = use_k ? (int64_t)cut_key : -1;
         const u64 tie = use_k ? cut_left * weight(value_of(cut_key), sc, sh.table) : 0ull;
         u64 total;
-        cluster_sum(sh, 0, n, rank, C, [&](int i) {
-          const float v = to_f(x[i]);
-          return (int64_t)key_of(v) > above ? weight(v, sc, sh.table) : 0ull;
+        cluster_sum(sh, 0, x, n, rank, C, [&](float xa, int, float xb, int, u64 &wa, u64 &wb) {
+          weight2(xa, xb, sc, sh.table, wa, wb);       // 0 at -inf
+          if ((int64_t)key_of(xa) <= above) wa = 0;
+          if ((int64_t)key_of(xb) <= above) wb = 0;
         }, &total);
         total += tie;
         bool more;
@@ -698,11 +776,14 @@ sample_kernel(const __grid_constant__ Params P) {
         cut_left = (left + one - 1) / one;
       }
       cut = true;
-      auto is_tie = [&](int i) { return key_of(to_f(x[i])) == cut_key ? 1ull : 0ull; };
+      auto is_tie = [&](float xa, int, float xb, int b, u64 &wa, u64 &wb) {
+        wa = key_of(xa) == cut_key;
+        wb = b >= 0 && key_of(xb) == cut_key;
+      };
       u64 ties;
-      const u64 before = cluster_sum(sh, 1, n, rank, C, is_tie, &ties);
+      const u64 before = cluster_sum(sh, 1, x, n, rank, C, is_tie, &ties);
       if (ties > cut_left) {                          // the same in every block
-        ordered_find(sh, n, before, cut_left - 1, is_tie, [&](int i) {
+        ordered_find(sh, 1, x, n, before, cut_left - 1, is_tie, [&](int i) {
           for (int c = 0; c < C; ++c) remote_store(&sh.cut, c, (u64)(lo + i));
         });
         cluster_barrier();
@@ -710,26 +791,30 @@ sample_kernel(const __grid_constant__ Params P) {
       }
     }
   }
-  auto kept = [&](int i) {
-    const float v = to_f(x[i]);
-    if (cut) {
-      const uint32_t key = key_of(v);
-      if (key < cut_key || (key == cut_key && lo + i > last)) return 0ull;
-    }
-    const u64 w = weight(v, sc, sh.table);
-    return w >= least ? w : 0ull;
+  auto keeps = [&](float v, int i) -> bool {
+    const uint32_t key = key_of(v);
+    return key > cut_key || (key == cut_key && lo + i <= last);
+  };
+  auto kept = [&](float xa, int a, float xb, int b, u64 &wa, u64 &wb) {
+    wa = wb = 0;
+    const bool ka = !cut || keeps(xa, a), kb = !cut || keeps(xb, b);   // -inf weighs 0 anyway
+    if (!ka && !kb) return;
+    weight2(xa, xb, sc, sh.table, wa, wb);
+    if (!ka || wa < least) wa = 0;
+    if (!kb || wb < least) wb = 0;
   };
   u64 total;
-  const u64 before = cluster_sum(sh, 2, n, rank, C, kept, &total);
+  const u64 before = cluster_sum(sh, 2, x, n, rank, C, kept, &total);
   bool more;
   const u64 target = u >= 1.f ? total - 1 : u > 0.f ? scaled(total, u, &more) : 0ull;
-  ordered_find(sh, n, before, target, kept, [&](int i) { P.tokens[row] = lo + i; });
+  ordered_find(sh, 2, x, n, before, target, kept, [&](int i) { P.tokens[row] = lo + i; });
   cluster_barrier();                                  // its shared memory has been read
 }
 
 template <typename T>
 static size_t smem_bytes(int slice) {
-  return (sizeof(Shared) + 15) / 16 * 16 + (size_t)slice * sizeof(T);
+  const size_t tokens = (size_t)slice * sizeof(T), list = kCand * sizeof(u64);   // the list takes the slice's place
+  return (sizeof(Shared) + 15) / 16 * 16 + (tokens > list ? tokens : list);
 }
 
 template <typename T>

@@ -1,5 +1,5 @@
 """Token sampling against its float64 definition.  The kernel's weights are
-exact to about 2^-40, so a token may differ from the definition only where u
+exact to about 2^-38, so a token may differ from the definition only where u
 meets a border that closely: the random cases below must agree everywhere, and
 the constructed ones meet borders exactly."""
 import numpy as np
