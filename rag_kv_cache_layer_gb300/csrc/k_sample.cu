@@ -188,6 +188,7 @@ struct Shared {
   int bin, count;
   u64 cut;                  // the cut: key << 32 | last index kept with that key
   float ch, cl;             // log2(e) / temperature
+  float border[2];          // smallest logits of a step and of the one above
 };
 
 // Order-preserving integer of a float, and back.
@@ -277,9 +278,10 @@ __device__ __forceinline__ u64 remote_weight(const Shared &sh, int b, int C) {
   return p0 + (p1 << 16) + (p2 << 32);
 }
 
-// The consecutive range of a block's n tokens that warp w owns.
+// The consecutive range of a block's n tokens that warp w owns: whole rounds of
+// 16 bytes per lane.
 __device__ __forceinline__ int warp_begin(int n, int w) {
-  return min(n, w * (((n + kWarps - 1) / kWarps + 31) / 32 * 32));
+  return min(n, w * (((n + kWarps - 1) / kWarps + 255) / 256 * 256));
 }
 
 // A pass weighs its tokens in pairs: f(xa, a, xb, b, wa, wb) gives the weights
@@ -335,7 +337,7 @@ __device__ __forceinline__ void ordered_find(Shared &sh, int slot, const T *x, i
   while (target >= before + sh.warp[w]) before += sh.warp[w++];
   const int b = warp_begin(n, w), e = warp_begin(n, w + 1);
   const int per = (e - b + kThreads - 1) / kThreads;
-  static_assert(CB_MAX_SAMPLE_VOCAB / kMaxCluster / kWarps <= 4 * kThreads, "four tokens per thread");
+  static_assert((CB_MAX_SAMPLE_VOCAB / kMaxCluster / kWarps + 255) / 256 * 256 <= 4 * kThreads, "four tokens each");
   const int i0 = b + (int)threadIdx.x * per, i1 = min(e, i0 + per);
   u64 v[4], s = 0, total;
 #pragma unroll
@@ -373,15 +375,13 @@ __device__ __forceinline__ void sort_block(u64 *a, int n) {
     }
   __syncthreads();
 }
-// Sorts the first n gathered tokens (padded to a power of two); returns that
-// power.
-__device__ __forceinline__ int sort_cand(Shared &sh, int n) {
+// Sorts the first n gathered tokens (padded to a power of two).
+__device__ __forceinline__ void sort_cand(Shared &sh, int n) {
   int m = 2;
   while (m < n) m <<= 1;
   for (int i = n + threadIdx.x; i < m; i += kThreads) sh.cand[i] = ~0ull;
   __syncthreads();
   sort_block(sh.cand, m);
-  return m;
 }
 // A gathered token: ascending order is larger x first, then lower index.
 __device__ __forceinline__ u64 pack(uint32_t key, uint32_t index) { return ((u64)~key << 32) | index; }
@@ -567,10 +567,10 @@ sample_kernel(const __grid_constant__ Params P) {
     // steps of x from the maximum down to where weights vanish (tokens beyond
     // are in none: no cut can matter there)
     const float range = fminf(sc.top - low, (float)(P.shift + 3) / sc.ch);
-    const float scale = (float)kBins / fmaxf(range * 1.0001f, 1e-35f);
-    auto bin_of = [&](float v) -> int {               // monotone in v
+    const float scale = ((float)kBins - 1.f) / fmaxf(range * 1.0001f, 1e-35f);
+    auto bin_of = [&](float v) -> int {               // monotone in v: the nearest step
       const float t = (sc.top - v) * scale;
-      return t < (float)kBins ? (int)t : kBins;
+      return t < (float)kBins - 1.f ? __float_as_int(t + 12582912.f) - 0x4b400000 : kBins;
     };
     wide = sc.top == INFINITY;                        // no distance to measure by
     if (!wide) {
@@ -631,29 +631,68 @@ sample_kernel(const __grid_constant__ Params P) {
         if (!wide) {
           // Every warp counts its tokens (its range is consecutive), then
           // stores them at their places: the list comes in vocabulary order.
-          auto takes = [&](float v) -> bool {          // the same floats as bin_of
-            const float t = (sc.top - v) * scale;
-            return t < (float)(step + 1) && (small || t >= (float)step);
-          };
+          // The step's borders as logits: the smallest float in a bin up to
+          // `want`, found over the ordered integers (bin_of is monotone), a
+          // warp narrowing the range to a 32nd each round.
           const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+          if (warp < 2) {
+            const int want = step - warp;              // and the step above it
+            u64 a = key_of(-INFINITY), b = key_of(sc.top);   // bin_of(b) = 0
+            while (want >= 0 && b - a > 1) {
+              const u64 by = (b - a + 31) / 32, at = a + by * (lane + 1);
+              const bool in = at >= b || bin_of(value_of((uint32_t)at)) <= want;
+              const int f = __ffs(__ballot_sync(0xffffffffu, in)) - 1;
+              b = min(b, a + by * (f + 1));
+              a += by * f;
+            }
+            if (lane == 0) sh.border[warp] = want < 0 ? INFINITY : value_of((uint32_t)b);
+          }
+          __syncthreads();
+          const float from = sh.border[0], below = small ? INFINITY : sh.border[1];
           const int wb = warp_begin(n, warp), we = warp_begin(n, warp + 1);
-          u64 all_taken;
-          const u64 taken_before =
-              cluster_sum(sh, 0, x, n, rank, C, [&](float xa, int, float xb, int, u64 &wa, u64 &wb) {
-                wa = takes(xa);
-                wb = takes(xb);
-              }, &all_taken);
-          uint32_t at = (uint32_t)taken_before;
-          for (int w = 0; w < warp; ++w) at += (uint32_t)sh.warp[w];
-          if (sh.warp[warp])
+          constexpr int VEC = 16 / sizeof(T);
+          // 16 bytes of tokens per lane: a mask of those taken
+          auto taken = [&](int i, float (&v)[VEC]) -> uint32_t {
+            uint32_t m = 0;
+            if (i < we) {
+              load16<T>(x + i, v);                     // past we: another warp's, or past n, unread below
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) m |= (uint32_t)(v[e] >= from && v[e] < below && i + e < we) << e;
+            }
+            return m;
+          };
+          uint32_t mine = 0;
+          float v[VEC];
 #pragma unroll 2
-            for (int i0 = wb; i0 < we; i0 += 32) {
-              const float v = i0 + lane < we ? to_f(x[i0 + lane]) : -INFINITY;
-              const bool take = takes(v);
-              const uint32_t mask = __ballot_sync(0xffffffffu, take);
-              if (take)
-                remote_store(&sh.cand[at + __popc(mask & ((1u << lane) - 1))], 0, pack(key_of(v), lo + i0 + lane));
-              at += __popc(mask);
+          for (int i0 = wb; i0 < we; i0 += 32 * VEC) mine += __popc(taken(i0 + lane * VEC, v));
+          mine = __reduce_add_sync(0xffffffffu, mine);
+          if (lane == 0) sh.warp[warp] = mine;
+          __syncthreads();
+          if (threadIdx.x == 0) {
+            u64 t = 0;
+            for (int w = 0; w < kWarps; ++w) t += sh.warp[w];
+            sh.sum[0] = t;
+          }
+          cluster_barrier();
+          uint32_t at = 0;
+          for (int c = 0; c < rank; ++c) at += (uint32_t)remote(&sh.sum[0], c);
+          for (int w = 0; w < warp; ++w) at += (uint32_t)sh.warp[w];
+          if (mine)
+            for (int i0 = wb; i0 < we; i0 += 32 * VEC) {
+              const int i = i0 + lane * VEC;
+              const uint32_t m = taken(i, v);
+              if (!__any_sync(0xffffffffu, m)) continue;
+              uint32_t incl = __popc(m);
+#pragma unroll
+              for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += t;
+              }
+              uint32_t place = at + incl - __popc(m);
+#pragma unroll
+              for (int e = 0; e < VEC; ++e)
+                if (m >> e & 1) remote_store(&sh.cand[place++], 0, pack(key_of(v[e]), lo + i + e));
+              at += __shfl_sync(0xffffffffu, incl, 31);
             }
           cluster_barrier();
           if (rank == 0) {
