@@ -196,9 +196,9 @@ def _paged_kv(k_pages, v_pages, row_offsets, kv_lens, block_table):
     n_seq, = kv_lens.shape
     seqs, width = block_table.shape
     ld_table, one = block_table.stride()
-    if kv_lens.dtype != _I32 or row_offsets.dtype != _I32 or block_table.dtype != _I32 or \
-            row_offsets.shape != (n_seq + 1,) or seqs != n_seq or (one != 1 and width > 1) or \
-            (n_seq > 1 and kv_lens.stride(0) != 1) or row_offsets.stride(0) != 1:
+    if not kv_lens.dtype == row_offsets.dtype == block_table.dtype == _I32 or seqs != n_seq or \
+            row_offsets.shape != (n_seq + 1,) or (one != 1 and width > 1) or \
+            not (kv_lens.is_contiguous() and row_offsets.is_contiguous()):
         raise ValueError("row_offsets [n_seq + 1], kv_lens [n_seq] and block_table [n_seq, max_pages] "
                          "must be int32 with contiguous rows")
     shape, strides = k_pages.shape, k_pages.stride()
@@ -207,9 +207,10 @@ def _paged_kv(k_pages, v_pages, row_offsets, kv_lens, block_table):
         raise ValueError("k_pages and v_pages must have one shape, type and strides, with contiguous slots")
     n_pages, page, cols = shape[-3:]
     ld = strides[-2] if page > 1 else cols
-    return L.PagedKV(k_pages.data_ptr(), v_pages.data_ptr(), strides[-3] if n_pages > 1 else page * ld, ld,
-                     n_pages, page, block_table.data_ptr(), ld_table if n_seq > 1 else width, width,
-                     row_offsets.data_ptr(), kv_lens.data_ptr(), n_seq)
+    kv = L.PagedKV(k_pages.data_ptr(), v_pages.data_ptr(), strides[-3] if n_pages > 1 else page * ld, ld,
+                   n_pages, page, block_table.data_ptr(), ld_table if n_seq > 1 else width, width,
+                   row_offsets.data_ptr(), kv_lens.data_ptr(), n_seq)
+    return kv, shape
 
 
 def cb_paged_append(k_new, v_new, row_offsets, kv_lens, block_table, k_pages, v_pages,
@@ -222,8 +223,8 @@ def cb_paged_append(k_new, v_new, row_offsets, kv_lens, block_table, k_pages, v_
     cb_rope_table_init; None copies the keys as they are.  q: [rows,
     n_q_heads * head_dim], rotated into q_out (None: in place)."""
     dev = _on_device(k_new, v_new, row_offsets, kv_lens, block_table, k_pages, v_pages, rope_table, q, q_out)
-    kv = _paged_kv(k_pages, v_pages, row_offsets, kv_lens, block_table)
-    dt, shape = k_pages.dtype, k_pages.shape
+    kv, shape = _paged_kv(k_pages, v_pages, row_offsets, kv_lens, block_table)
+    dt = k_pages.dtype
     cols, layers, sk, sv, sc = shape[-1], 1, 0, 0, 0
     k1, v1 = k_new, v_new
     if len(shape) == 4:
@@ -279,8 +280,8 @@ def cb_paged_attention(q, row_offsets, kv_lens, block_table, k_pages, v_pages, n
     bound of kv_lens (default: what the table can hold).  ws: from
     cb_paged_attention_workspace (None: allocated here)."""
     dev = _on_device(q, row_offsets, kv_lens, block_table, k_pages, v_pages, out, ws)
-    kv = _paged_kv(k_pages, v_pages, row_offsets, kv_lens, block_table)
-    dt, cols, shape = k_pages.dtype, n_q_heads * head_dim, k_pages.shape
+    kv, shape = _paged_kv(k_pages, v_pages, row_offsets, kv_lens, block_table)
+    dt, cols = k_pages.dtype, n_q_heads * head_dim
     if len(shape) != 3 or shape[2] != n_kv_heads * head_dim:
         raise ValueError("the pools must be one layer's [n_pages, page_size, n_kv_heads * head_dim]")
     n_rows = q.shape[0]
@@ -291,7 +292,7 @@ def cb_paged_attention(q, row_offsets, kv_lens, block_table, k_pages, v_pages, n
     status = lib.cb_paged_attention(
         C.byref(kv), q.data_ptr(), _ld("q", q, dt, n_rows, cols), n_rows, max_kv_len, n_q_heads, n_kv_heads,
         head_dim, 1.0 / math.sqrt(head_dim) if scale is None else scale, out.data_ptr(),
-        _ld("out", out, dt, n_rows, cols), _CODES.get(dt, -1), ws.data_ptr(), ws.numel() * ws.element_size(),
+        _ld("out", out, dt, n_rows, cols), _CODES.get(dt, -1), ws.data_ptr(), ws.nbytes,
         _cur_stream(dev) if stream is None else stream.cuda_stream)
     if status:
         check(status)

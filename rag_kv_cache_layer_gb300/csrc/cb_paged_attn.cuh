@@ -35,10 +35,9 @@ struct AttnParams {
 int decode_grid();
 cudaError_t launch_decode(const AttnParams &P, int R, int hd, int *status, cudaStream_t s);
 
-// bf16, many rows: tiles of 128 rows, their keys in n_split parts; the
-// workspace holds tiles * Hkv * n_split * 128 partial rows if n_split > 1.
-int chunk_slots();
-cudaError_t launch_chunk(const AttnParams &P, int64_t tiles, int hd, int *status, cudaStream_t s);
+// bf16, many rows: units of R (128 or 256) rows, their keys in n_split parts;
+// the workspace holds units * Hkv * n_split * R partial rows if n_split > 1.
+cudaError_t launch_chunk(const AttnParams &P, int R, int64_t units, int hd, int *status, cudaStream_t s);
 
 }  // namespace paged
 }  // namespace cb

@@ -263,7 +263,7 @@ static int64_t tile_bound(int64_t n_rows, int S, int G, int R) {
 // How a call runs.
 struct Plan {
   int few_R;                              // bf16, few rows: rows per tile, 0: none
-  int R;                                  // chunk (128) or fp32 tiles (16, 64): rows, 0: none
+  int R;                                  // chunk (128, 256) or fp32 tiles (16, 64): rows, 0: none
   int few_hi, rows_lo;                    // which sequences each takes
   int64_t tiles;                          // R-row tiles at most
   int n_split;                            // parts of their key ranges
@@ -275,7 +275,8 @@ struct Plan {
 // sizes leave it open; a call whose rows do not exceed its sequences is taken
 // for one generated token each and runs the few-rows kernel alone (which
 // takes any number of rows), a single sequence runs the one its rows call
-// for.  The few-rows tile is 16, 32 or 64 rows by the average sequence.
+// for.  The few-rows tile is 16, 32 or 64 rows, the chunk unit 128 or 256, by
+// the average sequence.
 // fp32: 16-row tiles where a sequence brings few rows (the wider tile would
 // mostly multiply zeros), else 64.
 // Key ranges of chunk and fp32 tiles are split while the tiles alone leave
@@ -292,9 +293,9 @@ static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, cb_dtype dt)
     if (few || S > 1) p.few_R = per_seq <= 16 || per_seq > 64 ? 16 : per_seq <= 32 ? 32 : 64;
     p.few_partials = p.few_R ? 2LL * decode_grid() * p.few_R : 0;
     if (few) return p;
-    p.R = 128;
+    p.R = per_seq <= 128 ? 128 : 256;
     if (S > 1) p.few_hi = p.rows_lo = 64;
-    slots = chunk_slots();
+    slots = (p.R == 128 ? 2LL : 1LL) * device_sm_count();
     least = 512;
   } else {
     p.R = per_seq <= 16 ? 16 : 64;
@@ -347,7 +348,7 @@ static cudaError_t run_all(AttnParams P, const Plan &p, cb_dtype dt, void *ws, i
   }
   if (!p.R) return e;
   bind(p.partials);
-  if (dt == CB_BF16) return launch_chunk(P, p.tiles, HD, status, s);
+  if (dt == CB_BF16) return launch_chunk(P, p.R, p.tiles, HD, status, s);
   e = p.R == 16 ? run_simt<16, HD>(P, p, status, s) : run_simt<64, HD>(P, p, status, s);
   if (e != cudaSuccess || p.n_split == 1) return e;
   const dim3 grid((unsigned)(p.tiles * P.Hkv * (p.R / kMergeRows)));

@@ -1,21 +1,26 @@
 // bf16 paged attention of many rows per sequence on the tensor cores
 // (tcgen05): chunks of a prompt over what the cache holds.
 //
-// Work unit: 128 rows of one sequence and kv head (row l is query l / G, head
-// l % G of the group, so any group size fills the tile) and, where the tiles
-// alone do not fill the SMs, a part of their key range.  Tiles of a sequence
-// are taken last first: they see the most keys.
+// Work unit: NT tiles of 128 rows of one sequence and kv head (row l is query
+// l / G, head l % G of the group, so any group size fills the tiles) and,
+// where the units alone do not fill the SMs, a part of their key range.  Units
+// of a sequence are taken last first: they see the most keys.
 //
-// Roles (224 threads, two CTAs per SM): warps 0 and 6 fill the double-buffered
-// 64-key K and V blocks; warp 1 owns 256 TMEM columns and issues tcgen05.mma:
-// S_j = Q K_j^T into slot j & 1 (columns 0..63 or 64..127) and O += P_j V_j
-// into columns 128.., P_j read from TMEM where it overwrites S_j; warps 2..5
-// load Q, then do the online softmax, one row per thread, in the log2 domain
-// and store P_j as packed bf16.  With two S slots S_{j+1} is computed while
-// the softmax works on S_j, and the SM's other CTA fills the remaining
-// tensor-core time.  The row's reference maximum m only moves when a block
-// raises it by more than 2^kRescale: then O (after P_{j-1} V_{j-1} has landed)
-// and l are scaled by 2^(m_old - m_new); O / l does not depend on m.
+// NT = 2, one CTA per SM: two tiles share every K and V block, so a block is
+// fetched once for 256 rows and four stages fit.  NT = 1, two CTAs per SM with
+// two stages each, serves sequences of up to 128 rows, whose second tile would
+// be empty.
+//
+// Roles: producer warps fill the 64-key K and V stages; one MMA warp per tile
+// owns 256 TMEM columns and issues tcgen05.mma: S_j = Q K_j^T into slot j & 1
+// (columns 0..63 or 64..127) and O += P_j V_j into columns 128.., P_j read
+// from TMEM where it overwrites S_j; four warps per tile load Q, then do the
+// online softmax, one row per thread, in the log2 domain and store P_j as
+// packed bf16.  With two S slots S_{j+1} is computed while the softmax works
+// on S_j, and the SM's other tile fills the remaining tensor-core time.  The
+// row's reference maximum m only moves when a block raises it by more than
+// 2^kChRescale: then O (after P_{j-1} V_{j-1} has landed) and l are scaled by
+// 2^(m_old - m_new); O / l does not depend on m.
 //
 // Keys and values come by 16-byte cp.async to their swizzled places, each
 // eight rows of one page together, with zeros for keys past the cached length
@@ -36,12 +41,9 @@ namespace paged {
 
 using namespace attn;
 
-constexpr int kChThreads = 224;
-constexpr int kChRows = 128;
 constexpr int kChBN = 64;                 // keys per block
 constexpr float kChRescale = 8.f;         // log2 of the largest p between rescales
-constexpr int kChPerSm = 2;
-constexpr int kChTmem = 256;              // S/P slots 0..63, 64..127; O from 128
+constexpr int kChTmem = 256;              // per tile: S/P slots 0..63, 64..127; O from 128
 
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -51,12 +53,16 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-template <int HD> struct ChCfg {
-  static constexpr int kAtom = kChRows * 128;        // [128 rows x 64 dims], 128-byte swizzle
+template <int HD, int NT> struct ChCfg {
+  static constexpr int kRows = 128 * NT, kPerSm = NT == 1 ? 2 : 1;
+  static constexpr int kStages = NT == 1 ? 2 : 4, kProd = NT;   // producer warps each for K and V
+  // warps: K producers, V producers, MMA, (idle), softmax from a multiple of 4
+  static constexpr int kMma = 2 * kProd, kSoft = (kMma + NT + 3) / 4 * 4, kThreads = 32 * (kSoft + 4 * NT);
+  static constexpr int kAtom = 128 * 128;            // [128 rows x 64 dims], 128-byte swizzle
   static constexpr int kAtomKV = kChBN * 128;        // [64 keys x 64 dims]
   static constexpr int kQ = kAtom * (HD / 64), kKV = kAtomKV * (HD / 64);
-  static constexpr int kOffK = kQ, kOffV = kOffK + 2 * kKV, kOffBar = kOffV + 2 * kKV;
-  static constexpr int kSmem = kOffBar + 256 + 1024;
+  static constexpr int kOffK = NT * kQ, kOffV = kOffK + kStages * kKV, kOffBar = kOffV + kStages * kKV;
+  static constexpr int kSmem = kOffBar + 512 + 1024;
 };
 
 // Fills one K or V stage: 64 keys of one head.  Lane = (row of 32 / cols,
@@ -97,54 +103,43 @@ __device__ __forceinline__ void chunk_load(uint32_t dst, const bf16 *pool, const
   }
 }
 
-template <int HD>
-__global__ void __launch_bounds__(kChThreads, kChPerSm)
+template <int HD, int NT>
+__global__ void __launch_bounds__(ChCfg<HD, NT>::kThreads, ChCfg<HD, NT>::kPerSm)
 paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
-  typedef ChCfg<HD> C;
+  typedef ChCfg<HD, NT> C;
+  constexpr int NS = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
-  uint64_t *q_full = bar + 0;
-  uint64_t *k_full = bar + 1;      // [2] K_j landed
-  uint64_t *k_empty = bar + 3;     // [2] S_j = Q K_j^T done with K_j
-  uint64_t *v_full = bar + 5;      // [2] V_j landed
-  uint64_t *v_empty = bar + 7;     // [2] P_j V_j done with V_j
-  uint64_t *s_full = bar + 9;      // [2] S_j in its TMEM slot
-  uint64_t *p_full = bar + 11;     // [2] P_j in the slot (and O rescaled)
-  uint64_t *pv_done = bar + 13;    // [2] O += P_j V_j has landed
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + 15);
+  uint64_t *k_full = bar;                      // [NS] K_j landed
+  uint64_t *k_empty = k_full + NS;             // [NS] every tile's S_j = Q K_j^T done with K_j
+  uint64_t *v_full = k_empty + NS;             // [NS] V_j landed
+  uint64_t *v_empty = v_full + NS;             // [NS] every tile's P_j V_j done with V_j
+  uint64_t *q_full = v_empty + NS;             // [NT]
+  uint64_t *s_full = q_full + NT;              // [NT][2] S_j in its TMEM slot
+  uint64_t *p_full = s_full + 2 * NT;          // [NT][2] P_j in the slot (and O rescaled)
+  uint64_t *pv_done = p_full + 2 * NT;         // [NT][2] O += P_j V_j has landed
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(pv_done + 2 * NT);
   volatile int *fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  static_assert(8 * (4 * NS + 7 * NT) + 8 <= 512, "barriers fit");
   __shared__ PagedTile s_tile;
-  __shared__ int s_sums[kChThreads / 32];
+  __shared__ int s_sums[C::kThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    mbar_init(smem_u32(q_full), 128);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&k_full[i]), 32);
-      mbar_init(smem_u32(&k_empty[i]), 1);
-      mbar_init(smem_u32(&v_full[i]), 32);
-      mbar_init(smem_u32(&v_empty[i]), 1);
-      mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&p_full[i]), 128);
-      mbar_init(smem_u32(&pv_done[i]), 1);
-    }
-    *fail = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
   grid_dep_wait();
   grid_dep_launch();
   const int split = blockIdx.x % P.n_split, g = blockIdx.x / P.n_split % P.Hkv;
   const int tile = blockIdx.x / P.n_split / P.Hkv;
-  paged_find_tile<kChThreads>(P.kv, P.n_rows, P.G, kChRows, P.max_kv, tile, &s_tile, s_sums, status, P.rows_lo);
+  paged_find_tile<C::kThreads>(P.kv, P.n_rows, P.G, C::kRows, P.max_kv, tile, &s_tile, s_sums, status, P.rows_lo);
   const PagedTile tl = s_tile;
   if (tl.s < 0) return;
-  const int l0 = tl.t * kChRows, rows = min(kChRows, tl.n * P.G - l0);
+  const int l0 = tl.t * C::kRows, rows = min(C::kRows, tl.n * P.G - l0);
+  const int active = NT == 1 || rows <= 128 ? 1 : 2;           // tiles with rows
   const int base = tl.kv - tl.n;
   const int last = base + (l0 + rows - 1) / P.G;
   const int nb_tile = last < 0 ? 0 : last / kChBN + 1;
   const int jb = (int)((int64_t)nb_tile * split / P.n_split);
   const int nb = (int)((int64_t)nb_tile * (split + 1) / P.n_split) - jb;
-  const int64_t slot0 = ((int64_t)(tile * P.Hkv + g) * P.n_split + split) * kChRows;
+  const int64_t slot0 = ((int64_t)(tile * P.Hkv + g) * P.n_split + split) * C::kRows;
   if (nb == 0) {
     // no key of this part is seen: an empty partial, or rows of zeros
     if ((int)threadIdx.x < rows) {
@@ -160,16 +155,33 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
     }
     return;
   }
-  if (warp == 1) tcx::tmem_alloc(smem_u32(tmem_slot), kChTmem);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(smem_u32(&k_full[i]), 32);
+      mbar_init(smem_u32(&k_empty[i]), active);
+      mbar_init(smem_u32(&v_full[i]), 32);
+      mbar_init(smem_u32(&v_empty[i]), active);
+    }
+    for (int i = 0; i < NT; ++i) mbar_init(smem_u32(&q_full[i]), 128);
+    for (int i = 0; i < 2 * NT; ++i) {
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&p_full[i]), 128);
+      mbar_init(smem_u32(&pv_done[i]), 1);
+    }
+    *fail = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == C::kMma) tcx::tmem_alloc(smem_u32(tmem_slot), NT * kChTmem);
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
   auto proxy_fence = [] { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); };
 
-  if (warp == 0 || warp == 6) {
-    // ------------------------------------- producers (K: warp 0, V: warp 6)
-    const bool is_v = warp == 6;
+  if (warp < 2 * C::kProd) {
+    // ------------------------------------------- producers (K, then V warps)
+    const bool is_v = warp >= C::kProd;
+    const int first = warp % C::kProd;           // this warp's blocks: first, first + kProd, ..
     uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
     const bf16 *pool = reinterpret_cast<const bf16 *>(is_v ? P.kv.v_pages : P.kv.k_pages) + (int64_t)g * HD;
     const uint32_t dst = smem_u32(smem + (is_v ? C::kOffV : C::kOffK));
@@ -183,19 +195,19 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
       if (key < tl.kv) report(status, CB_ERR_DEVICE_INDEX);
       return -1;
     };
-    int lo = fetch(jb * kChBN + lane), hi = fetch(jb * kChBN + 32 + lane);
+    int lo = fetch((jb + first) * kChBN + lane), hi = fetch((jb + first) * kChBN + 32 + lane);
     // Two loads are in flight: a block is handed over (its bytes fenced for
-    // the tensor core) after the next one has been issued, or at once where
-    // the next one's stage is still in use.
+    // the tensor core) after the warp's next one has been issued, or at once
+    // where the next one's stage is still in use.
     int open = -1;                               // block issued but not handed over
     auto hand_over = [&] {
       proxy_fence();
-      arrive(smem_u32(&full[open & 1]));
+      arrive(smem_u32(&full[open % NS]));
       open = -1;
     };
-    for (int j = 0; j < nb; ++j) {
-      const int sl = j & 1, key0 = (jb + j) * kChBN;
-      const uint32_t eb = smem_u32(&empty[sl]), ph = ((j >> 1) & 1) ^ 1;
+    for (int j = first; j < nb; j += C::kProd) {
+      const int sl = j % NS, key0 = (jb + j) * kChBN;
+      const uint32_t eb = smem_u32(&empty[sl]), ph = ((j / NS) & 1) ^ 1;
       if (open >= 0 && !__all_sync(0xffffffffu, mbar_test(eb, ph))) {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         hand_over();
@@ -212,8 +224,8 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
       else
         chunk_load<HD, false>(dst + sl * C::kKV, pool, P.kv, key0, tl.kv - key0, lo, hi, lane);
       asm volatile("cp.async.commit_group;" ::: "memory");
-      lo = fetch(key0 + kChBN + lane);
-      hi = fetch(key0 + kChBN + 32 + lane);
+      lo = fetch(key0 + C::kProd * kChBN + lane);
+      hi = fetch(key0 + C::kProd * kChBN + 32 + lane);
       if (open >= 0) {
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         hand_over();
@@ -222,31 +234,32 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (open >= 0) hand_over();
-  } else if (warp == 1) {
-    // ----------------------------------------------------------------- MMA
+  } else if (warp >= C::kMma && warp < C::kMma + active) {
+    // ----------------------------------------------------- MMA, one per tile
+    const int t = warp - C::kMma;
     const uint32_t idS = idesc(false, kChBN), idPV = idesc(true, HD);
-    const uint32_t q_addr = smem_u32(smem);
+    const uint32_t q_addr = smem_u32(smem + t * C::kQ), tm = tmem + t * kChTmem;
+    uint64_t *const sf = s_full + 2 * t, *const pf = p_full + 2 * t, *const pd = pv_done + 2 * t;
     auto wait_all = [&](uint64_t *b, uint32_t ph) -> bool {
       return __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(b), ph, kWaitLimitNs, status));
     };
-    bool ok = wait_all(q_full, 0);
+    bool ok = wait_all(q_full + t, 0);
     // S_j into slot j & 1; the slot held P_{j-2}, so P_{j-2} V_{j-2} must be done
     auto issue_s = [&](int j) -> bool {
-      const int sl = j & 1;
-      const uint32_t ph = (j >> 1) & 1;
-      if (!wait_all(&k_full[sl], ph)) return false;
-      if (j >= 2 && !wait_all(&pv_done[sl], ph ^ 1)) return false;
+      const int sl = j & 1, st = j % NS;
+      if (!wait_all(&k_full[st], (j / NS) & 1)) return false;
+      if (j >= 2 && !wait_all(&pd[sl], ((j >> 1) & 1) ^ 1)) return false;
       fence_after();
       if (tcx::elect_one()) {
-        const uint32_t k_addr = smem_u32(smem + C::kOffK + sl * C::kKV);
+        const uint32_t k_addr = smem_u32(smem + C::kOffK + st * C::kKV);
 #pragma unroll
         for (int k = 0; k < HD / 16; ++k) {
           const uint32_t qo = (k >> 2) * C::kAtom + (k & 3) * 32;
           const uint32_t ko = (k >> 2) * C::kAtomKV + (k & 3) * 32;
-          mma(tmem + sl * kChBN, desc_kmajor(q_addr + qo), desc_kmajor(k_addr + ko), idS, k > 0);
+          mma(tm + sl * kChBN, desc_kmajor(q_addr + qo), desc_kmajor(k_addr + ko), idS, k > 0);
         }
-        commit(smem_u32(&s_full[sl]));
-        commit(smem_u32(&k_empty[sl]));
+        commit(smem_u32(&sf[sl]));
+        commit(smem_u32(&k_empty[st]));
       }
       __syncwarp();
       return true;
@@ -254,32 +267,33 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
     if (ok) ok = issue_s(0);
     for (int j = 0; j < nb && ok; ++j) {
       if (__any_sync(0xffffffffu, *fail != 0)) break;
-      const int sl = j & 1;
-      const uint32_t ph = (j >> 1) & 1;
+      const int sl = j & 1, st = j % NS;
       if (j + 1 < nb && !issue_s(j + 1)) { ok = false; break; }
-      if (!wait_all(&p_full[sl], ph) || !wait_all(&v_full[sl], ph)) {
+      if (!wait_all(&pf[sl], (j >> 1) & 1) || !wait_all(&v_full[st], (j / NS) & 1)) {
         ok = false;
         break;
       }
       fence_after();
       if (tcx::elect_one()) {
-        const uint32_t v_addr = smem_u32(smem + C::kOffV + sl * C::kKV);
+        const uint32_t v_addr = smem_u32(smem + C::kOffV + st * C::kKV);
 #pragma unroll
         for (int k = 0; k < kChBN / 16; ++k)
-          mma_ts(tmem + 2 * kChBN, tmem + sl * kChBN + k * 8, desc_mnmajor(v_addr + k * 16 * 128, C::kAtomKV), idPV,
+          mma_ts(tm + 2 * kChBN, tm + sl * kChBN + k * 8, desc_mnmajor(v_addr + k * 16 * 128, C::kAtomKV), idPV,
                  (j > 0 || k > 0) ? 1u : 0u);
-        commit(smem_u32(&pv_done[sl]));
-        commit(smem_u32(&v_empty[sl]));
+        commit(smem_u32(&pd[sl]));
+        commit(smem_u32(&v_empty[st]));
       }
       __syncwarp();
     }
     if (!ok && lane == 0) *fail = 1;
-  } else {
+  } else if (warp >= C::kSoft && warp < C::kSoft + 4 * active) {
     // ------------------------------------------------------ Q, then softmax
+    const int t = (warp - C::kSoft) / 4;
+    uint64_t *const sf = s_full + 2 * t, *const pf = p_full + 2 * t, *const pd = pv_done + 2 * t;
     {
-      // thread t loads row t: all its loads are in flight at once, and eight
+      // a thread loads its row: all its loads are in flight at once, and eight
       // neighbouring rows fall into different banks
-      const int r = threadIdx.x - 64, l = l0 + r;
+      const int r = threadIdx.x - 32 * C::kSoft, l = l0 + r;
       const bf16 *q = reinterpret_cast<const bf16 *>(P.q) + (int64_t)(tl.row0 + l / P.G) * P.ld_q +
                       (int64_t)(g * P.G + l % P.G) * HD;
       uint4 v[HD / 8];
@@ -288,21 +302,22 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
         v[c] = r < rows ? *reinterpret_cast<const uint4 *>(q + c * 8) : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int c = 0; c < HD / 8; ++c)
-        *reinterpret_cast<uint4 *>(smem + (c >> 3) * C::kAtom + r * 128 + (((c ^ r) & 7) << 4)) = v[c];
+        *reinterpret_cast<uint4 *>(smem + t * C::kQ + (c >> 3) * C::kAtom + (r & 127) * 128 +
+                                   (((c ^ r) & 7) << 4)) = v[c];
       proxy_fence();
-      arrive(smem_u32(q_full));
+      arrive(smem_u32(q_full + t));
     }
     const int quad = warp & 3;
-    const int row = quad * 32 + lane;            // MMA row
+    const int row = t * 128 + quad * 32 + lane;  // row of the unit
     const bool valid = row < rows;
     const int p = valid ? base + (l0 + row) / P.G : -1;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t obase = tmem + lane_off + 2 * kChBN;
+    const uint32_t tm = tmem + t * kChTmem + lane_off, obase = tm + 2 * kChBN;
     float m = -INFINITY, l = 0.f;                // reference max (log2 domain), sum
     const float sl2 = P.scale_log2;
     bool failed = false;
     auto pv_landed = [&](int j) -> bool {
-      const bool bad = !mbar_wait_bounded(smem_u32(&pv_done[j & 1]), (j >> 1) & 1, kWaitLimitNs, status) || *fail;
+      const bool bad = !mbar_wait_bounded(smem_u32(&pd[j & 1]), (j >> 1) & 1, kWaitLimitNs, status) || *fail;
       if (__any_sync(0xffffffffu, bad)) return false;
       fence_after();
       return true;
@@ -310,10 +325,10 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
     for (int j = 0; j < nb; ++j) {
       const int sl = j & 1;
       const uint32_t ph = (j >> 1) & 1;
-      const bool bad = !mbar_wait_bounded(smem_u32(&s_full[sl]), ph, kWaitLimitNs, status) || *fail;
+      const bool bad = !mbar_wait_bounded(smem_u32(&sf[sl]), ph, kWaitLimitNs, status) || *fail;
       if (__any_sync(0xffffffffu, bad)) { failed = true; break; }
       fence_after();
-      const uint32_t sbase = tmem + lane_off + sl * kChBN;
+      const uint32_t sbase = tm + sl * kChBN;
       const int key0 = (jb + j) * kChBN;
       const int n_vis = p - key0 + 1;            // keys of the block this row sees; >= 64: no masking
       float x[kChBN];
@@ -381,7 +396,7 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
       wait_st();
       l += (lo2(ls2[0]) + hi2(ls2[0])) + (lo2(ls2[1]) + hi2(ls2[1]));
       fence_before();
-      arrive(smem_u32(&p_full[sl]));
+      arrive(smem_u32(&pf[sl]));
     }
     // the whole key range is in O once the last P V has landed
     if (!failed && !pv_landed(nb - 1)) failed = true;
@@ -392,7 +407,7 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
       const float inv = l == 0.f ? 0.f : 1.f / l;    // no visible key: zeros
       bf16 *out = reinterpret_cast<bf16 *>(P.out) + (int64_t)(tl.row0 + lr / P.G) * P.ld_out +
                   (int64_t)(g * P.G + lr % P.G) * HD;
-      // partials lie four columns of all 128 rows together, which a warp with
+      // partials lie four columns of all the unit's rows together, which a warp with
       // a row per lane writes (and the merge reads) in whole lines
       float4 *part = reinterpret_cast<float4 *>(P.part_o + slot0 * HD) + row;
 #pragma unroll 1
@@ -403,7 +418,7 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
         if (P.n_split > 1) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
-            part[(c + i) / 4 * kChRows] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            part[(c + i) / 4 * C::kRows] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           continue;
         }
 #pragma unroll
@@ -421,21 +436,21 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
   }
   fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == C::kMma) {
     fence_after();
-    tcx::tmem_dealloc(tmem, kChTmem);
+    tcx::tmem_dealloc(tmem, NT * kChTmem);
   }
 }
 
-// Merges the parts of a tile: with M = max m_c, O = sum_c 2^(m_c - M) O_c /
+// Merges the parts of a unit: with M = max m_c, O = sum_c 2^(m_c - M) O_c /
 // sum_c 2^(m_c - M) l_c, in part order.  A block takes 32 rows (one per lane)
-// and 32 columns (four per warp).  The tile is found before the parts are
+// and 32 columns (four per warp).  The unit is found before the parts are
 // waited for: what it reads was there before the chunk kernel began.
 constexpr int kChMergeThreads = 256;
-template <int HD>
+template <int HD, int NT>
 __global__ void __launch_bounds__(kChMergeThreads)
 chunk_merge_kernel(const __grid_constant__ AttnParams P) {
-  constexpr int kQuads = kChRows / 32, kColBlocks = HD / 32;
+  constexpr int kChRows = ChCfg<HD, NT>::kRows, kQuads = kChRows / 32, kColBlocks = HD / 32;
   __shared__ PagedTile s_tile;
   __shared__ int s_sums[kChMergeThreads / 32];
   __shared__ __align__(16) bf16 s_out[32][40];
@@ -485,26 +500,26 @@ chunk_merge_kernel(const __grid_constant__ AttnParams P) {
   }
 }
 
-int chunk_slots() { return kChPerSm * device_sm_count(); }
-
-template <int HD>
+template <int HD, int NT>
 static cudaError_t run(const AttnParams &P, int64_t tiles, int *status, cudaStream_t s) {
+  typedef ChCfg<HD, NT> C;
   static PerDeviceOnce attr;
   cudaError_t e = attr.run([](int) {
-    return cudaFuncSetAttribute(paged_chunk_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, ChCfg<HD>::kSmem);
+    return cudaFuncSetAttribute(paged_chunk_kernel<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   if (e != cudaSuccess) return e;
-  e = launch_pdl(paged_chunk_kernel<HD>, dim3((unsigned)(tiles * P.Hkv * P.n_split)), dim3(kChThreads),
-                 ChCfg<HD>::kSmem, s, P, status);
+  e = launch_pdl(paged_chunk_kernel<HD, NT>, dim3((unsigned)(tiles * P.Hkv * P.n_split)), dim3(C::kThreads), C::kSmem,
+                 s, P, status);
   if (e != cudaSuccess) return e;
   if (P.n_split == 1) return launched(1);
-  e = launch_pdl(chunk_merge_kernel<HD>, dim3((unsigned)(tiles * P.Hkv * (kChRows / 32) * (HD / 32))),
+  e = launch_pdl(chunk_merge_kernel<HD, NT>, dim3((unsigned)(tiles * P.Hkv * (C::kRows / 32) * (HD / 32))),
                  dim3(kChMergeThreads), 0, s, P);
   return e == cudaSuccess ? launched(2) : e;
 }
 
-cudaError_t launch_chunk(const AttnParams &P, int64_t tiles, int hd, int *status, cudaStream_t s) {
-  return hd == 128 ? run<128>(P, tiles, status, s) : run<64>(P, tiles, status, s);
+cudaError_t launch_chunk(const AttnParams &P, int R, int64_t tiles, int hd, int *status, cudaStream_t s) {
+  if (hd == 128) return R == 128 ? run<128, 1>(P, tiles, status, s) : run<128, 2>(P, tiles, status, s);
+  return R == 128 ? run<64, 1>(P, tiles, status, s) : run<64, 2>(P, tiles, status, s);
 }
 
 }  // namespace paged
