@@ -12,12 +12,15 @@
 // be empty.
 //
 // Roles: producer warps fill the 64-key K and V stages; one MMA warp per tile
-// owns 256 TMEM columns and issues tcgen05.mma: S_j = Q K_j^T into slot j & 1
-// (columns 0..63 or 64..127) and O += P_j V_j into columns 128.., P_j read
-// from TMEM where it overwrites S_j; four warps per tile load Q, then do the
+// owns 256 TMEM columns and issues tcgen05.mma: S_j = Q K_j^T into columns
+// 0..63 and O += P_j V_j into columns 128.., P_j read from TMEM (columns 64..95
+// or 96..127 by the parity of j); four warps per tile load Q, then do the
 // online softmax, one row per thread, in the log2 domain and store P_j as
-// packed bf16.  With two S slots S_{j+1} is computed while the softmax works
-// on S_j, and the SM's other tile fills the remaining tensor-core time.  The
+// packed bf16.  S_{j+1} is issued as soon as the softmax has taken S_j into
+// registers, so it is computed while the softmax works, and P V of block j
+// while the softmax is at block j + 1; with P in columns of its own neither
+// product waits for the other.  (With P_j over S_j and two S slots instead,
+// S_{j+1} had to wait for P_{j-1} V_{j-1}, and a block took 2100 cycles.)  The
 // row's reference maximum m only moves when a block raises it by more than
 // 2^kChRescale: then O (after P_{j-1} V_{j-1} has landed) and l are scaled by
 // 2^(m_old - m_new); O / l does not depend on m.
@@ -30,6 +33,8 @@
 //
 // Parts of a split key range leave (O, m, l) in fp32 for chunk_merge_kernel.
 // All waits are bounded.
+#include <type_traits>
+
 #include "cb_attn_tc.cuh"
 #include "cb_common.cuh"
 #include "cb_internal.h"
@@ -43,7 +48,7 @@ using namespace attn;
 
 constexpr int kChBN = 64;                 // keys per block
 constexpr float kChRescale = 8.f;         // log2 of the largest p between rescales
-constexpr int kChTmem = 256;              // per tile: S/P slots 0..63, 64..127; O from 128
+constexpr int kChTmem = 256, kChP = 64, kChO = 128;   // columns per tile: S from 0, P_0, P_1 (32 each), O
 
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -116,8 +121,9 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
   uint64_t *v_full = k_empty + NS;             // [NS] V_j landed
   uint64_t *v_empty = v_full + NS;             // [NS] every tile's P_j V_j done with V_j
   uint64_t *q_full = v_empty + NS;             // [NT]
-  uint64_t *s_full = q_full + NT;              // [NT][2] S_j in its TMEM slot
-  uint64_t *p_full = s_full + 2 * NT;          // [NT][2] P_j in the slot (and O rescaled)
+  uint64_t *s_full = q_full + NT;              // [NT] S_j in TMEM
+  uint64_t *s_read = s_full + NT;              // [NT] S_j in the softmax's registers
+  uint64_t *p_full = s_read + NT;              // [NT][2] P_j in its columns (and O rescaled)
   uint64_t *pv_done = p_full + 2 * NT;         // [NT][2] O += P_j V_j has landed
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(pv_done + 2 * NT);
   volatile int *fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -162,9 +168,12 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
       mbar_init(smem_u32(&v_full[i]), 32);
       mbar_init(smem_u32(&v_empty[i]), active);
     }
-    for (int i = 0; i < NT; ++i) mbar_init(smem_u32(&q_full[i]), 128);
-    for (int i = 0; i < 2 * NT; ++i) {
+    for (int i = 0; i < NT; ++i) {
+      mbar_init(smem_u32(&q_full[i]), 128);
       mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&s_read[i]), 128);
+    }
+    for (int i = 0; i < 2 * NT; ++i) {
       mbar_init(smem_u32(&p_full[i]), 128);
       mbar_init(smem_u32(&pv_done[i]), 1);
     }
@@ -239,16 +248,15 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
     const int t = warp - C::kMma;
     const uint32_t idS = idesc(false, kChBN), idPV = idesc(true, HD);
     const uint32_t q_addr = smem_u32(smem + t * C::kQ), tm = tmem + t * kChTmem;
-    uint64_t *const sf = s_full + 2 * t, *const pf = p_full + 2 * t, *const pd = pv_done + 2 * t;
+    uint64_t *const sf = s_full + t, *const sr = s_read + t, *const pf = p_full + 2 * t, *const pd = pv_done + 2 * t;
     auto wait_all = [&](uint64_t *b, uint32_t ph) -> bool {
       return __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(b), ph, kWaitLimitNs, status));
     };
     bool ok = wait_all(q_full + t, 0);
-    // S_j into slot j & 1; the slot held P_{j-2}, so P_{j-2} V_{j-2} must be done
     auto issue_s = [&](int j) -> bool {
-      const int sl = j & 1, st = j % NS;
+      const int st = j % NS;
       if (!wait_all(&k_full[st], (j / NS) & 1)) return false;
-      if (j >= 2 && !wait_all(&pd[sl], ((j >> 1) & 1) ^ 1)) return false;
+      if (j >= 1 && !wait_all(sr, (j & 1) ^ 1)) return false;   // S_{j-1} has been read
       fence_after();
       if (tcx::elect_one()) {
         const uint32_t k_addr = smem_u32(smem + C::kOffK + st * C::kKV);
@@ -256,9 +264,9 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
         for (int k = 0; k < HD / 16; ++k) {
           const uint32_t qo = (k >> 2) * C::kAtom + (k & 3) * 32;
           const uint32_t ko = (k >> 2) * C::kAtomKV + (k & 3) * 32;
-          mma(tm + sl * kChBN, desc_kmajor(q_addr + qo), desc_kmajor(k_addr + ko), idS, k > 0);
+          mma(tm, desc_kmajor(q_addr + qo), desc_kmajor(k_addr + ko), idS, k > 0);
         }
-        commit(smem_u32(&sf[sl]));
+        commit(smem_u32(sf));
         commit(smem_u32(&k_empty[st]));
       }
       __syncwarp();
@@ -278,7 +286,7 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
         const uint32_t v_addr = smem_u32(smem + C::kOffV + st * C::kKV);
 #pragma unroll
         for (int k = 0; k < kChBN / 16; ++k)
-          mma_ts(tm + 2 * kChBN, tm + sl * kChBN + k * 8, desc_mnmajor(v_addr + k * 16 * 128, C::kAtomKV), idPV,
+          mma_ts(tm + kChO, tm + kChP + sl * 32 + k * 8, desc_mnmajor(v_addr + k * 16 * 128, C::kAtomKV), idPV,
                  (j > 0 || k > 0) ? 1u : 0u);
         commit(smem_u32(&pd[sl]));
         commit(smem_u32(&v_empty[st]));
@@ -289,7 +297,7 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
   } else if (warp >= C::kSoft && warp < C::kSoft + 4 * active) {
     // ------------------------------------------------------ Q, then softmax
     const int t = (warp - C::kSoft) / 4;
-    uint64_t *const sf = s_full + 2 * t, *const pf = p_full + 2 * t, *const pd = pv_done + 2 * t;
+    uint64_t *const sf = s_full + t, *const sr = s_read + t, *const pf = p_full + 2 * t, *const pd = pv_done + 2 * t;
     {
       // a thread loads its row: all its loads are in flight at once, and eight
       // neighbouring rows fall into different banks
@@ -312,29 +320,31 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
     const bool valid = row < rows;
     const int p = valid ? base + (l0 + row) / P.G : -1;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t tm = tmem + t * kChTmem + lane_off, obase = tm + 2 * kChBN;
+    const uint32_t tm = tmem + t * kChTmem + lane_off, obase = tm + kChO;
     float m = -INFINITY, l = 0.f;                // reference max (log2 domain), sum
     const float sl2 = P.scale_log2;
     bool failed = false;
     auto pv_landed = [&](int j) -> bool {
-      const bool bad = !mbar_wait_bounded(smem_u32(&pd[j & 1]), (j >> 1) & 1, kWaitLimitNs, status) || *fail;
+      const bool bad = !mbar_wait_bounded(smem_u32(&pd[j & 1]), (j >> 1) & 1, kWaitLimitNs, status);
       if (__any_sync(0xffffffffu, bad)) return false;
       fence_after();
       return true;
     };
     for (int j = 0; j < nb; ++j) {
       const int sl = j & 1;
-      const uint32_t ph = (j >> 1) & 1;
-      const bool bad = !mbar_wait_bounded(smem_u32(&sf[sl]), ph, kWaitLimitNs, status) || *fail;
+      // (a failure elsewhere is met here as a wait that runs out: polling the
+      // flag would put another shared-memory read on every block's path)
+      const bool bad = !mbar_wait_bounded(smem_u32(sf), j & 1, kWaitLimitNs, status);
       if (__any_sync(0xffffffffu, bad)) { failed = true; break; }
       fence_after();
-      const uint32_t sbase = tm + sl * kChBN;
       const int key0 = (jb + j) * kChBN;
       const int n_vis = p - key0 + 1;            // keys of the block this row sees; >= 64: no masking
       float x[kChBN];
-      ld32_nw(sbase, x);
-      ld32_nw(sbase + 32, x + 32);
+      ld32_nw(tm, x);
+      ld32_nw(tm + 32, x + 32);
       wait_ld();
+      fence_before();
+      arrive(smem_u32(sr));
       float mx[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) mx[i] = -INFINITY;
@@ -371,28 +381,35 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
         l *= corr;
       }
       if (move) m = mloc;
-      // P_j for keys c..c+31 -> slot columns c/2 .. c/2+15 (S_j is in
-      // registers); the scale-and-shift and the sums run on packed pairs
+      // P_j for keys c..c+31 -> columns c/2 .. c/2+15; the scale-and-shift and
+      // the sums run on packed pairs.  The columns held P_{j-2}: S_j was
+      // issued after P_{j-2} V_{j-2} and its commit covers what came before,
+      // so that product is done.
       const unsigned long long s2 = pack2(sl2, sl2), nm2 = pack2(-m, -m);
       unsigned long long ls2[2] = {0ull, 0ull};
+      auto exps = [&](auto masked) {
 #pragma unroll
-      for (int c = 0; c < kChBN; c += 32) {
-        uint32_t pk[16];
+        for (int c = 0; c < kChBN; c += 32) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const unsigned long long a = fma2(pack2(x[c + i], x[c + i + 1]), s2, nm2);
-          float p0 = fast_exp2(lo2(a));
-          float p1 = fast_exp2(hi2(a));
-          if (n_vis < kChBN) {
-            p0 = c + i < n_vis ? p0 : 0.f;
-            p1 = c + i + 1 < n_vis ? p1 : 0.f;
+          for (int i = 0; i < 32; i += 2) {
+            const unsigned long long a = fma2(pack2(x[c + i], x[c + i + 1]), s2, nm2);
+            float p0 = fast_exp2(lo2(a));
+            float p1 = fast_exp2(hi2(a));
+            if (decltype(masked)::value) {
+              p0 = c + i < n_vis ? p0 : 0.f;
+              p1 = c + i + 1 < n_vis ? p1 : 0.f;
+            }
+            ls2[(i >> 1) & 1] = add2(ls2[(i >> 1) & 1], pack2(p0, p1));
+            __nv_bfloat162 v2 = __floats2bfloat162_rn(p0, p1);
+            pk[i / 2] = *reinterpret_cast<uint32_t *>(&v2);
           }
-          ls2[(i >> 1) & 1] = add2(ls2[(i >> 1) & 1], pack2(p0, p1));
-          __nv_bfloat162 v2 = __floats2bfloat162_rn(p0, p1);
-          pk[i / 2] = *reinterpret_cast<uint32_t *>(&v2);
+          st16(tm + kChP + sl * 32 + c / 2, pk);
         }
-        st16(sbase + c / 2, pk);
-      }
+      };
+      // most blocks lie wholly before every row of the warp: no selects there
+      if (__all_sync(0xffffffffu, n_vis >= kChBN)) exps(std::false_type{});
+      else exps(std::true_type{});
       wait_st();
       l += (lo2(ls2[0]) + hi2(ls2[0])) + (lo2(ls2[1]) + hi2(ls2[1]));
       fence_before();
