@@ -270,22 +270,49 @@ struct Plan {
   int64_t few_partials, partials;         // partial rows in the workspace (reused)
 };
 
+// Rows per unit and parts of the key ranges of the chunk kernel: the cheapest
+// by a model of its time, in microseconds, measured on four chunks of 2048
+// rows over 8192 keys, 512 rows over 4000 and 64 over 3200.  A part of 256
+// rows (one CTA per SM) costs 7.5 and each of its 64-key blocks 0.93, one of
+// 128 rows 5 and 1.04 (two CTAs on the SM) or 0.85 (alone on it); parts run in waves of CTA slots, and partials (written
+// and read once, about 8 MB per microsecond) and their merge come on top.
+// Large work takes 256 rows unsplit; a few tiles over many keys are split
+// until the SMs are full; and where the last of few waves would be nearly
+// empty, splitting evens it out (192 units of 30,000 keys, head_dim 64: 780
+// unsplit, 476 in three parts each).
+static void plan_chunk(Plan &p, int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd) {
+  const int sms = device_sm_count(), nb = (max_kv + 63) / 64 > 0 ? (max_kv + 63) / 64 : 1;
+  double best = 1e300;
+  for (int R = 128; R <= 256; R += 128) {
+    const int64_t tiles = tile_bound(n_rows, S, G, R), units = tiles * Hkv;
+    for (int n = 1; n <= 32 && (n == 1 || 2 * n <= nb); ++n) {
+      const bool alone = R == 256 || units * n <= sms;
+      const int64_t slots = alone ? sms : 2LL * sms;
+      const double block = R == 256 ? 0.93 : alone ? 0.85 : 1.04;
+      double t = (double)((units * n + slots - 1) / slots) * ((double)nb / n * block + (R == 256 ? 7.5 : 5.0));
+      if (n > 1) t += 5.0 + (double)units * n * R * hd * 8 / 8e6;
+      if (t < best) {
+        best = t;
+        p.R = R;
+        p.tiles = tiles;
+        p.n_split = n;
+      }
+    }
+  }
+}
+
 // bf16: sequences of up to 64 rows (queries x G) go through the few-rows
 // kernel, longer ones through the chunk kernel.  Both are launched when the
 // sizes leave it open; a call whose rows do not exceed its sequences is taken
 // for one generated token each and runs the few-rows kernel alone (which
 // takes any number of rows), a single sequence runs the one its rows call
-// for.  The few-rows tile is 16, 32 or 64 rows, the chunk unit 128 or 256, by
-// the average sequence.
+// for.  The few-rows tile is 16, 32 or 64 rows by the average sequence.
 // fp32: 16-row tiles where a sequence brings few rows (the wider tile would
-// mostly multiply zeros), else 64.
-// Key ranges of chunk and fp32 tiles are split while the tiles alone leave
-// SMs idle, in parts of at least 512 (chunk) or 128 keys: a part's fixed cost
-// is worth several blocks of its loop.
-static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, cb_dtype dt) {
+// mostly multiply zeros), else 64; key ranges are split while the tiles alone
+// leave SMs idle, in parts of at least 128 keys.
+static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd, cb_dtype dt) {
   Plan p = {};
   const int64_t all = n_rows * G, per_seq = (all + S - 1) / S;
-  int64_t slots, least;
   p.few_hi = 0x7fffffff;
   p.n_split = 1;
   if (dt == CB_BF16) {
@@ -293,20 +320,16 @@ static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, cb_dtype dt)
     if (few || S > 1) p.few_R = per_seq <= 16 || per_seq > 64 ? 16 : per_seq <= 32 ? 32 : 64;
     p.few_partials = p.few_R ? 2LL * decode_grid() * p.few_R : 0;
     if (few) return p;
-    p.R = per_seq <= 128 ? 128 : 256;
     if (S > 1) p.few_hi = p.rows_lo = 64;
-    slots = (p.R == 128 ? 2LL : 1LL) * device_sm_count();
-    least = 512;
+    plan_chunk(p, n_rows, S, max_kv, G, Hkv, hd);
   } else {
     p.R = per_seq <= 16 ? 16 : 64;
-    slots = 4LL * device_sm_count();
-    least = 128;
+    p.tiles = tile_bound(n_rows, S, G, p.R);
+    const int64_t units = p.tiles * Hkv > 0 ? p.tiles * Hkv : 1;
+    const int64_t want = 4LL * device_sm_count() / units, most = (max_kv + 127) / 128;
+    const int64_t n = want < most ? want : most;
+    p.n_split = n < 1 ? 1 : n > 64 ? 64 : (int)n;
   }
-  p.tiles = tile_bound(n_rows, S, G, p.R);
-  const int64_t units = p.tiles * Hkv > 0 ? p.tiles * Hkv : 1;
-  const int64_t want = slots / units, most = (max_kv + least - 1) / least;
-  const int64_t n = want < most ? want : most;
-  p.n_split = n < 1 ? 1 : n > 64 ? 64 : (int)n;
   p.partials = p.n_split == 1 ? 0 : p.tiles * Hkv * p.n_split * p.R;
   return p;
 }
@@ -361,7 +384,7 @@ static cudaError_t run_all(AttnParams P, const Plan &p, cb_dtype dt, void *ws, i
 size_t paged_attention_ws_bytes(int n_rows, int n_seq, int max_kv, int Hq, int Hkv, int hd, cb_dtype dt) {
   using namespace paged;
   if (n_rows <= 0 || n_seq <= 0) return 0;
-  return plan_bytes(plan(n_rows, n_seq, max_kv, Hq / Hkv, Hkv, dt), hd);
+  return plan_bytes(plan(n_rows, n_seq, max_kv, Hq / Hkv, Hkv, hd, dt), hd);
 }
 
 cudaError_t launch_paged_attention(const PagedKV &kv, const void *q, int64_t ld_q, int n_rows, int max_kv,
@@ -369,7 +392,7 @@ cudaError_t launch_paged_attention(const PagedKV &kv, const void *q, int64_t ld_
                                    cb_dtype dt, void *ws, int *status, cudaStream_t s) {
   using namespace paged;
   if (n_rows == 0 || kv.n_seq == 0) return cudaSuccess;
-  const Plan p = plan(n_rows, kv.n_seq, max_kv, Hq / Hkv, Hkv, dt);
+  const Plan p = plan(n_rows, kv.n_seq, max_kv, Hq / Hkv, Hkv, hd, dt);
   if (p.tiles * Hkv * p.n_split > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   AttnParams P;
   P.kv = kv;
