@@ -20,7 +20,7 @@ struct AttnParams {
   void *out;
   int64_t ld_q, ld_out;
   int n_rows, G, Hkv, max_kv;
-  int n_split;                            // parts of a tile's key range (chunk and fp32 kernels)
+  int n_split;                            // parts of a unit's key range (chunk kernel)
   // Sequences by rows (queries x G): the few-rows kernel takes those up to
   // few_hi, the chunk kernel those above rows_lo.
   int few_hi, rows_lo;
@@ -30,10 +30,10 @@ struct AttnParams {
   Join *joins;                            // one per block of the few-rows kernel
 };
 
-// bf16, few rows per sequence: R (16, 32 or 64) rows per tile.  The workspace
-// holds 2 * decode_grid() * R partial rows and decode_grid() joins.
+// Few rows per sequence, and all of fp32: R (16, 32 or 64) rows per tile.  The
+// workspace holds 2 * decode_grid() * R partial rows and decode_grid() joins.
 int decode_grid();
-cudaError_t launch_decode(const AttnParams &P, int R, int hd, int *status, cudaStream_t s);
+cudaError_t launch_decode(const AttnParams &P, int R, int hd, cb_dtype dt, int *status, cudaStream_t s);
 
 // bf16, many rows: units of R (128 or 256) rows, their keys in n_split parts;
 // the workspace holds units * Hkv * n_split * R partial rows if n_split > 1.

@@ -1,6 +1,6 @@
-// bf16 paged attention of a few rows per sequence (generated tokens, short
-// drafts): keys and values stream through shared memory once, and the group's
-// q heads share them.
+// Paged attention of a few rows per sequence (generated tokens, short drafts)
+// in bf16, and of any rows in fp32: keys and values stream through shared
+// memory once, and the group's q heads share them.
 //
 // Work.  A tile is R = 16 WM rows of one sequence and kv head (an item); its
 // keys come in blocks of BN.  All blocks of all items form one line of units,
@@ -20,12 +20,21 @@
 // rows of 256 bytes, and a box costs about 140 ns of one SM's copy unit
 // whatever its height, which held the same loop to 12 - 27 GB/s per block.
 //
-// Each warp holds 16 rows: S = Q K^T and O += P V by mma.m16n8k16 on
-// fragments from ldmatrix, running maximum, sum and O in registers (base-2
-// exponentials, fp32; P rounds to bf16 as the second product's operand).  The
-// legacy tensor instruction is the right one: the work is bound by the pages'
-// bytes, 45 bytes per nanosecond and SM, and a 128-row tcgen05 tile with 4
-// rows in use would not read them faster.
+// Each warp holds 16 rows, with the running maximum, sum and O in registers
+// (base-2 exponentials, fp32).  bf16: S = Q K^T and O += P V by mma.m16n8k16 on
+// fragments from ldmatrix; P rounds to bf16 as the second product's operand.
+// The legacy tensor instruction is the right one there: the work is bound by
+// the pages' bytes, 45 bytes per nanosecond and SM, and a 128-row tcgen05 tile
+// with 4 rows in use would not read them faster.
+// fp32: the same products by mma.m16n8k8 on TF32 halves, x = hi + lo with hi
+// the nearest TF32 value and lo = x - hi: hi hi + hi lo + lo hi drops 2^-22 of
+// a product, as much as an fp32 rounding or two.  The tensor core truncates
+// its sums, so every step of eight goes into a fresh accumulator that is added
+// in fp32 (one chain over 128 dimensions and thousands of keys would drift by
+// 1e-5 and more).  That is 2 to 5 times the CUDA cores' rate and keeps their
+// error.
+#include <type_traits>
+
 #include "cb_common.cuh"
 #include "cb_internal.h"
 #include "cb_paged.cuh"
@@ -37,9 +46,10 @@ namespace paged {
 constexpr int kDecThreads = 128;
 constexpr int kDecBlocksPerSm = 2;
 
-template <int HD, int WM> struct DecCfg {
-  static constexpr int kBN = 2048 / HD;         // keys per stage: 8 KB of K and V
-  static constexpr int kTile = kBN * HD * 2;
+template <typename T, int HD, int WM> struct DecCfg {
+  static constexpr int kBN = 4096 / (int)sizeof(T) / HD;   // keys per stage: 8 KB of K and V
+  static constexpr int kRow = HD * (int)sizeof(T);
+  static constexpr int kTile = kBN * kRow;
   static constexpr int kStage = 2 * kTile;      // K then V
   static constexpr int kStages = 3 * WM;        // of each group: 96 KB per block
   static constexpr int kSmem = (4 / WM) * kStages * kStage;
@@ -59,6 +69,32 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x = hi + lo, hi the nearest TF32 value.
+__device__ __forceinline__ void halves(float x, uint32_t &hi, uint32_t &lo) {
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+// c += A B of one m16n8k8 step in fp32: three TF32 products in a fresh
+// accumulator.
+__device__ __forceinline__ void step_f32(float (&c)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], float b0,
+                                         float b1) {
+  uint32_t h0, l0, h1, l1;
+  halves(b0, h0, l0);
+  halves(b1, h1, l1);
+  float t[4] = {0.f, 0.f, 0.f, 0.f};
+  mma1688(t, al, h0, h1);
+  mma1688(t, ah, l0, l1);
+  mma1688(t, ah, h0, h1);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] += t[i];
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -157,11 +193,13 @@ __device__ __forceinline__ int seq_of(const Line &L, int n_seq, int64_t u) {
   return lo;                      // the last one that begins at or before u
 }
 
-template <int HD, int WM>
+template <typename T, int HD, int WM>
 __global__ void __launch_bounds__(kDecThreads, kDecBlocksPerSm)
 paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
-  typedef DecCfg<HD, WM> C;
-  constexpr int R = 16 * WM, WK = 4 / WM, ND = HD / 8, KS = HD / 16, BN = C::kBN, NS = C::kStages;
+  typedef DecCfg<T, HD, WM> C;
+  constexpr bool F32 = std::is_same<T, float>::value;
+  // KS: k-steps of Q K^T (16 dims in bf16, 8 in fp32)
+  constexpr int R = 16 * WM, WK = 4 / WM, ND = HD / 8, KS = F32 ? HD / 8 : HD / 16, BN = C::kBN, NS = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Line line;
   __shared__ int64_t s_sums[kDecThreads / 32];
@@ -179,9 +217,9 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
   const int wm = warp % WM, wk = warp / WM, gid = lane >> 2, q4 = lane & 3;
   const uint32_t ring = smem_u32(smem) + wk * NS * C::kStage;
   const int shift = __ffs(P.kv.page_size) - 1;
-  const bf16 *kp = reinterpret_cast<const bf16 *>(P.kv.k_pages), *vp = reinterpret_cast<const bf16 *>(P.kv.v_pages);
+  const T *kp = reinterpret_cast<const T *>(P.kv.k_pages), *vp = reinterpret_cast<const T *>(P.kv.v_pages);
   // rows and column that this lane copies: row i * kRows + crow of a stage
-  constexpr int kCols = HD / 8, kRows = 32 / kCols;
+  constexpr int kVec = 16 / sizeof(T), kCols = HD / kVec, kRows = 32 / kCols;
   const int crow = lane / kCols, ccol = lane % kCols;
   // ldmatrix row of this lane: K tiles as 8 keys x 4 8-dim columns, V tiles as
   // 16 keys x 2 8-dim columns
@@ -198,8 +236,11 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
     const bool whole = jb == 0 && take == nbs, first = u == u0;
     const int64_t item_end = u - jb + nbs;
     u += take;
-    const int g = item % P.Hkv, l0 = item / P.Hkv * R;
     const int row0 = __ldg(P.kv.row_offsets + s), n = __ldg(P.kv.row_offsets + s + 1) - row0;
+    // tiles from both ends in turn: early ones see fewer keys than the line
+    // counts for them, so neighbours even out
+    const int g = item % P.Hkv, k = item / P.Hkv, tiles = (int)(((int64_t)n * P.G + R - 1) / R);
+    const int l0 = ((k & 1) ? tiles - 1 - k / 2 : k / 2) * R;
     const int kv = __ldg(P.kv.kv_lens + s), base = kv - n, rows = min(R, n * P.G - l0);
     const int seen = base + (l0 + rows - 1) / P.G + 1;        // keys the tile's last row sees
     const int je = min(jb + take, seen > 0 ? (seen - 1) / BN + 1 : 0);
@@ -224,29 +265,32 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
         const int r = (i * WM + wm) * kRows + crow;
         const int pg = __shfl_sync(0xffffffffu, page, r);
         const int slot = (j * BN + r) & (P.kv.page_size - 1);
-        const int64_t off = pg < 0 ? 0 : (int64_t)pg * P.kv.page_stride + (int64_t)slot * P.kv.ld + g * HD + ccol * 8;
-        const uint32_t d = dst + r * (HD * 2) + (((ccol & 8) | ((ccol ^ r) & 7)) << 4);
-        copy16(d, kp + off, pg >= 0);
-        copy16(d + C::kTile, vp + off, pg >= 0);
+        const int64_t off = pg < 0 ? 0 : (int64_t)pg * P.kv.page_stride + (int64_t)slot * P.kv.ld + g * HD + ccol * kVec;
+        // 16-byte columns are swizzled so that the fragments' reads meet all
+        // banks: by the row, or (V in fp32) by the pair of rows
+        const uint32_t d = dst + r * C::kRow, x = F32 ? ((r >> 1) & 3) << 1 : r & 7;
+        copy16(d + ((ccol ^ (r & 7)) << 4), kp + off, pg >= 0);
+        copy16(d + C::kTile + ((ccol ^ x) << 4), vp + off, pg >= 0);
       }
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
     int pos[2];
-    uint32_t qf[KS][4];
+    uint32_t qf[KS][4];                         // bf16 pairs, or fp32 values
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = wm * 16 + gid + 8 * h;
       const bool valid = r < rows;
       const int qi = (l0 + r) / P.G;
       pos[h] = valid ? base + qi : -1;
-      const bf16 *src = reinterpret_cast<const bf16 *>(P.q) + (int64_t)(row0 + qi) * P.ld_q +
-                        (int64_t)(g * P.G + (l0 + r) % P.G) * HD + q4 * 2;
+      const T *src = reinterpret_cast<const T *>(P.q) + (int64_t)(row0 + qi) * P.ld_q +
+                     (int64_t)(g * P.G + (l0 + r) % P.G) * HD + (F32 ? q4 : q4 * 2);
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          qf[k][h + 2 * c] = valid ? *reinterpret_cast<const uint32_t *>(src + k * 16 + c * 8) : 0u;
+          qf[k][h + 2 * c] =
+              valid ? *reinterpret_cast<const uint32_t *>(src + (F32 ? k * 8 + c * 4 : k * 16 + c * 8)) : 0u;
     }
     float o[ND][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
@@ -281,14 +325,23 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
       for (int t = 0; t < BN / 8; ++t) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[t][k] = 0.f;
-        const uint32_t row = ks + (t * 8 + krow) * (HD * 2);
+        const uint32_t row = ks + (t * 8 + krow) * C::kRow;
 #pragma unroll
-        for (int k2 = 0; k2 < HD / 32; ++k2) {
+        for (int k2 = 0; k2 < KS / 2; ++k2) {   // 64 bytes of 8 keys: two k-steps
           uint32_t b[4];
-          const int ch = k2 * 4 + kcol;         // 16-byte column
-          ldsm_x4(row + (((ch & 8) | ((ch ^ krow) & 7)) << 4), b);
-          mma16816(x[t], qf[2 * k2], b[0], b[1]);
-          mma16816(x[t], qf[2 * k2 + 1], b[2], b[3]);
+          ldsm_x4(row + (((k2 * 4 + kcol) ^ krow) << 4), b);
+          if constexpr (F32) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t ah[4], al[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) halves(__uint_as_float(qf[2 * k2 + c][e]), ah[e], al[e]);
+              step_f32(x[t], ah, al, __uint_as_float(b[2 * c]), __uint_as_float(b[2 * c + 1]));
+            }
+          } else {
+            mma16816(x[t], qf[2 * k2], b[0], b[1]);
+            mma16816(x[t], qf[2 * k2 + 1], b[2], b[3]);
+          }
         }
       }
       const int key0 = j * BN;
@@ -327,19 +380,41 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
           x[t][k] = p;
           l[k >> 1] += p;
         }
+      if constexpr (F32) {
+        // The product's step takes the keys of a tile in the order 0 2 4 6 1 3
+        // 5 7, in which the scores' registers already are its operand.
 #pragma unroll
-      for (int k2 = 0; k2 < BN / 16; ++k2) {
-        const uint32_t a[4] = {pack_bf16(x[2 * k2][0], x[2 * k2][1]), pack_bf16(x[2 * k2][2], x[2 * k2][3]),
-                               pack_bf16(x[2 * k2 + 1][0], x[2 * k2 + 1][1]),
-                               pack_bf16(x[2 * k2 + 1][2], x[2 * k2 + 1][3])};
-        const uint32_t row = vs + (k2 * 16 + vrow) * (HD * 2);
+        for (int t = 0; t < BN / 8; ++t) {
+          uint32_t ah[4], al[4];
+          halves(x[t][0], ah[0], al[0]);
+          halves(x[t][2], ah[1], al[1]);
+          halves(x[t][1], ah[2], al[2]);
+          halves(x[t][3], ah[3], al[3]);
+          const uint32_t row = vs + (t * 8 + 2 * q4) * C::kRow;
 #pragma unroll
-        for (int d2 = 0; d2 < ND / 2; ++d2) {
-          uint32_t b[4];
-          const int ch = d2 * 2 + vcol;
-          ldsm_x4_t(row + (((ch & 8) | ((ch ^ vrow) & 7)) << 4), b);
-          mma16816(o[2 * d2], a, b[0], b[1]);
-          mma16816(o[2 * d2 + 1], a, b[2], b[3]);
+          for (int d = 0; d < ND; ++d) {
+            // dims d * 8 + gid of keys 2 q4 and 2 q4 + 1
+            const uint32_t at = row + (((d * 2 + (gid >> 2)) ^ (q4 << 1)) << 4) + (gid & 3) * 4;
+            float b0, b1;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(b0) : "r"(at) : "memory");
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(b1) : "r"(at + C::kRow) : "memory");
+            step_f32(o[d], ah, al, b0, b1);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int k2 = 0; k2 < BN / 16; ++k2) {
+          const uint32_t a[4] = {pack_bf16(x[2 * k2][0], x[2 * k2][1]), pack_bf16(x[2 * k2][2], x[2 * k2][3]),
+                                 pack_bf16(x[2 * k2 + 1][0], x[2 * k2 + 1][1]),
+                                 pack_bf16(x[2 * k2 + 1][2], x[2 * k2 + 1][3])};
+          const uint32_t row = vs + (k2 * 16 + vrow) * C::kRow;
+#pragma unroll
+          for (int d2 = 0; d2 < ND / 2; ++d2) {
+            uint32_t b[4];
+            ldsm_x4_t(row + (((d2 * 2 + vcol) ^ (vrow & 7)) << 4), b);
+            mma16816(o[2 * d2], a, b[0], b[1]);
+            mma16816(o[2 * d2 + 1], a, b[2], b[3]);
+          }
         }
       }
     }
@@ -384,10 +459,13 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
         if (c == 0) P.part_ml[slot + r] = make_float2(M, L);
       } else {
         const float inv = L == 0.f ? 0.f : 1.f / L;
-        bf16 *dst = reinterpret_cast<bf16 *>(P.out) + (int64_t)(row0 + (l0 + r) / P.G) * P.ld_out +
-                    (int64_t)(g * P.G + (l0 + r) % P.G) * HD + c;
-        *reinterpret_cast<uint2 *>(dst) =
-            make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+        T *dst = reinterpret_cast<T *>(P.out) + (int64_t)(row0 + (l0 + r) / P.G) * P.ld_out +
+                 (int64_t)(g * P.G + (l0 + r) % P.G) * HD + c;
+        if constexpr (F32)
+          *reinterpret_cast<float4 *>(dst) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+        else
+          *reinterpret_cast<uint2 *>(dst) =
+              make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
       }
     }
     __syncthreads();                            // before the next piece fills the rings
@@ -399,7 +477,7 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
 // rows' loads depend on nothing: warp w takes every eighth piece, a lane HD /
 // 32 columns, and the warps' sums meet in shared memory.
 constexpr int kJoinThreads = 256, kJoinRows = 4;
-template <int HD>
+template <typename T, int HD>
 __global__ void __launch_bounds__(kJoinThreads)
 decode_merge_kernel(const __grid_constant__ AttnParams P, int R) {
   constexpr int PER = HD / 32, NW = kJoinThreads / 32;
@@ -467,35 +545,46 @@ decode_merge_kernel(const __grid_constant__ AttnParams P, int R) {
       a += s_o[w][k][c];
       b += s_o[w][k][c + 1];
     }
-    if (r0 + k < J.rows)
-      *reinterpret_cast<uint32_t *>(reinterpret_cast<bf16 *>(P.out) + (int64_t)(J.row0 + l / P.G) * P.ld_out +
-                                    (int64_t)(J.g * P.G + l % P.G) * HD + c) =
-          pack_bf16(a * s_inv[k], b * s_inv[k]);
+    if (r0 + k >= J.rows) continue;
+    T *dst = reinterpret_cast<T *>(P.out) + (int64_t)(J.row0 + l / P.G) * P.ld_out +
+             (int64_t)(J.g * P.G + l % P.G) * HD + c;
+    if constexpr (std::is_same<T, float>::value)
+      *reinterpret_cast<float2 *>(dst) = make_float2(a * s_inv[k], b * s_inv[k]);
+    else
+      *reinterpret_cast<uint32_t *>(dst) = pack_bf16(a * s_inv[k], b * s_inv[k]);
   }
 }
 
 int decode_grid() { return kDecBlocksPerSm * device_sm_count(); }
 
-template <int HD, int WM>
+template <typename T, int HD, int WM>
 static cudaError_t run(const AttnParams &P, int *status, cudaStream_t s) {
-  typedef DecCfg<HD, WM> C;
+  typedef DecCfg<T, HD, WM> C;
   static PerDeviceOnce attr;
   cudaError_t e = attr.run([](int) {
-    return cudaFuncSetAttribute(paged_decode_kernel<HD, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    return cudaFuncSetAttribute(paged_decode_kernel<T, HD, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                C::kSmem);
   });
   if (e != cudaSuccess) return e;
   const int grid = decode_grid();               // 32 bytes of weights for each: within the default limit
-  e = launch_pdl(paged_decode_kernel<HD, WM>, dim3(grid), dim3(kDecThreads), C::kSmem, s, P, status);
+  e = launch_pdl(paged_decode_kernel<T, HD, WM>, dim3(grid), dim3(kDecThreads), C::kSmem, s, P, status);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(decode_merge_kernel<HD>, dim3(grid, 16 * WM / kJoinRows), dim3(kJoinThreads), grid * kJoinRows * sizeof(float2), s, P,
-                 16 * WM);
+  e = launch_pdl(decode_merge_kernel<T, HD>, dim3(grid, 16 * WM / kJoinRows), dim3(kJoinThreads),
+                 grid * kJoinRows * sizeof(float2), s, P, 16 * WM);
   return e == cudaSuccess ? launched(2) : e;
 }
 
-cudaError_t launch_decode(const AttnParams &P, int R, int hd, int *status, cudaStream_t s) {
+template <typename T>
+static cudaError_t run_type(const AttnParams &P, int R, int hd, int *status, cudaStream_t s) {
   if (hd == 128)
-    return R == 16 ? run<128, 1>(P, status, s) : R == 32 ? run<128, 2>(P, status, s) : run<128, 4>(P, status, s);
-  return R == 16 ? run<64, 1>(P, status, s) : R == 32 ? run<64, 2>(P, status, s) : run<64, 4>(P, status, s);
+    return R == 16   ? run<T, 128, 1>(P, status, s)
+           : R == 32 ? run<T, 128, 2>(P, status, s)
+                     : run<T, 128, 4>(P, status, s);
+  return R == 16 ? run<T, 64, 1>(P, status, s) : R == 32 ? run<T, 64, 2>(P, status, s) : run<T, 64, 4>(P, status, s);
+}
+
+cudaError_t launch_decode(const AttnParams &P, int R, int hd, cb_dtype dt, int *status, cudaStream_t s) {
+  return dt == CB_BF16 ? run_type<bf16>(P, R, hd, status, s) : run_type<float>(P, R, hd, status, s);
 }
 
 }  // namespace paged
