@@ -745,7 +745,7 @@ cb_status cb_blend_layer(cb_model *m, int layer, float *h, int n_rows,
 /* A paged K/V cache and the batch of sequences of one call.  Position p of
  * sequence s lives in slot p % page_size of page
  * block_table[s][p / page_size]; a slot is one cache row (n_kv_heads *
- * head_dim elements).  Row r of the call's row tensors (q, k_new, v_new,
+ * head_dim elements).  Row r of the call's row tensors (q, k, v,
  * out) belongs to the sequence s with row_offsets[s] <= r <
  * row_offsets[s + 1]; the i-th of a sequence's n rows has position
  * kv_lens[s] - n + i, so kv_lens counts the new rows.  A negative position
@@ -770,26 +770,32 @@ typedef struct {
 /* Appends the rows' keys and values to the cache and rotates keys and
  * queries to their positions on the way ([CB] blend_layer step 2, with a
  * page table in place of the fused cache's rows):
- *   K[p] = R(p) k_new[r],  V[p] = v_new[r],  q_out[r] = R(p) q[r]
+ *   K[p] = R(p) k[r],  V[p] = v[r],  q_out[r] = R(p) q[r]
  * with the rotation of cb_rope_reposition, in fp32 and rounded once.
  * rope_table NULL: keys are copied as they are (already rotated rows, such
  * as a blended prefill's fused cache), and q must be NULL.
- * n_rows rows of n_layers layers are appended: layer l reads k_new + l *
+ * n_rows rows of n_layers layers are appended: layer l reads k + l *
  * k_layer_stride (v alike) and writes k_pages + l * cache_layer_stride.
- * q: device [n_rows][ld_q] or NULL (with n_layers 1); q_out may be q.  Rows
- * without a position keep their q_out.  Sequences of one call must not share
- * a page that the call writes.  k_new and v_new must not overlap the pools.
+ * Rows without a position keep their q_out.  Sequences of one call must not
+ * share a page that the call writes.  k and v must not overlap the pools.
  * Errors: CB_ERR_INVALID_ARG (NULL or misaligned pointers, strides below a
  * row, head_dim not a multiple of 16), CB_ERR_UNSUPPORTED (page_size).  On
  * the device, offsets that do not ascend inside [0, n_rows], a page outside
  * the pool or the table, and a rotation at or past max_positions record
  * CB_ERR_DEVICE_INDEX; those rows are skipped. */
-cb_status cb_paged_append(const cb_paged_kv *kv, const void *k_new, int64_t ld_k,
-                          int64_t k_layer_stride, const void *v_new, int64_t ld_v,
-                          int64_t v_layer_stride, int n_rows, int n_layers,
-                          int64_t cache_layer_stride, int n_kv_heads, int head_dim,
-                          const float *rope_table, int max_positions, const void *q,
-                          int64_t ld_q, int n_q_heads, void *q_out, int64_t ld_q_out,
+typedef struct {
+  const void *k, *v;          /* device [n_rows] rows of n_kv_heads * head_dim */
+  int64_t ld_k, ld_v;         /* elements between rows                       */
+  int64_t k_layer_stride, v_layer_stride, cache_layer_stride; /* n_layers > 1 */
+  int n_rows, n_layers, n_kv_heads, head_dim;
+  const float *rope_table;    /* device, from cb_rope_table_init, or NULL    */
+  const void *q;              /* device [n_rows][ld_q], n_q_heads * head_dim
+                                 columns, or NULL (with n_layers 1)          */
+  void *q_out;                /* may be q                                    */
+  int64_t ld_q, ld_q_out;
+  int n_q_heads, max_positions;
+} cb_paged_rows;
+cb_status cb_paged_append(const cb_paged_kv *kv, const cb_paged_rows *rows,
                           cb_dtype dtype, cb_stream stream);
 
 /* Causal attention of the new rows over the paged cache: for row r of
@@ -801,12 +807,8 @@ cb_status cb_paged_append(const cb_paged_kv *kv, const void *k_new, int64_t ld_k
  * keys are in the cache already (cb_paged_append).  A row with a negative
  * position sees no key and gets zeros.  Slots past kv_lens are never used,
  * whatever they hold; K and V up to kv_lens must be finite.
- * q, out: device [n_rows][ld] (n_q_heads * head_dim columns); they must not
- * overlap.  max_kv_len: an upper bound of every kv_lens[s], which sizes the
- * split of long key ranges.  ws: device scratch of at least
- * cb_paged_attention_workspace_size(...) bytes for the same sizes (16-byte
- * aligned; contents need no initialisation; calls that share it must be
- * ordered on one stream).
+ * The workspace needs no initialisation; calls that share it must be ordered
+ * on one stream.
  * Errors: CB_ERR_INVALID_ARG (NULL or misaligned pointers, strides, head
  * counts not dividing or more than 128 q heads per kv head, head_dim not 64
  * or 128, a negative or infinite scale), CB_ERR_UNSUPPORTED (page_size, or a row count whose tiles exceed a
@@ -818,11 +820,22 @@ cb_status cb_paged_append(const cb_paged_kv *kv, const void *k_new, int64_t ld_k
 size_t cb_paged_attention_workspace_size(int n_rows, int n_seq, int max_kv_len,
                                          int n_q_heads, int n_kv_heads, int head_dim,
                                          cb_dtype dtype);
-cb_status cb_paged_attention(const cb_paged_kv *kv, const void *q, int64_t ld_q,
-                             int n_rows, int max_kv_len, int n_q_heads,
-                             int n_kv_heads, int head_dim, float scale, void *out,
-                             int64_t ld_out, cb_dtype dtype, void *ws,
-                             size_t ws_bytes, cb_stream stream);
+typedef struct {
+  const void *q;              /* device [n_rows][ld_q], n_q_heads * head_dim */
+  void *out;                  /* the same shape; must not overlap q          */
+  int64_t ld_q, ld_out;       /* elements between rows                       */
+  void *ws;                   /* device scratch, 16-byte aligned, at least
+                                 cb_paged_attention_workspace_size(...) bytes
+                                 for these sizes                             */
+  size_t ws_bytes;
+  int n_rows;
+  int max_kv_len;             /* an upper bound of every kv_lens[s]: sizes the
+                                 split of long key ranges                    */
+  int n_q_heads, n_kv_heads, head_dim;
+  float scale;
+} cb_paged_query;
+cb_status cb_paged_attention(const cb_paged_kv *kv, const cb_paged_query *query,
+                             cb_dtype dtype, cb_stream stream);
 
 /* Samples one token per row of logits from given uniform numbers.  With
  * X = max x and w_i = exp((x_i - X) / temperature), of the tokens ordered by

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libcacheblend.so")
@@ -125,6 +126,30 @@ class PagedKV(C.Structure):
                 ("kv_lens", vp), ("n_seq", i32)]
 
 
+class PagedRows(C.Structure):
+    _fields_ = [("k", vp), ("v", vp), ("ld_k", i64), ("ld_v", i64),
+                ("k_layer_stride", i64), ("v_layer_stride", i64), ("cache_layer_stride", i64),
+                ("n_rows", i32), ("n_layers", i32), ("n_kv_heads", i32), ("head_dim", i32),
+                ("rope_table", vp), ("q", vp), ("q_out", vp), ("ld_q", i64), ("ld_q_out", i64),
+                ("n_q_heads", i32), ("max_positions", i32)]
+
+
+class PagedQuery(C.Structure):
+    _fields_ = [("q", vp), ("out", vp), ("ld_q", i64), ("ld_out", i64), ("ws", vp),
+                ("ws_bytes", C.c_size_t), ("n_rows", i32), ("max_kv_len", i32),
+                ("n_q_heads", i32), ("n_kv_heads", i32), ("head_dim", i32), ("scale", C.c_float)]
+
+
+def packer(cls):
+    """A function from field values to the structure's bytes: calls that run
+    once per layer and token pass those in place of a ctypes object, which
+    takes four times as long to fill."""
+    codes = {vp: "P", i32: "i", i64: "q", C.c_size_t: "N", C.c_float: "f"}
+    s = struct.Struct("@" + "".join(codes[t] for _, t in cls._fields_) + "0P")
+    assert s.size == C.sizeof(cls)
+    return s.pack
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -190,11 +215,10 @@ def _load():
         "cb_anchor_count": (S, [C.POINTER(Segment), i32, i32, C.POINTER(i64)]),
         "cb_loading_ratio": (S, [C.c_double, C.POINTER(C.c_int32), C.POINTER(C.c_double), i32,
                                  C.c_int32, C.POINTER(C.c_int32)]),
-        "cb_paged_append": (S, [C.POINTER(PagedKV), vp, i64, i64, vp, i64, i64, i32, i32,
-                                i64, i32, i32, vp, i32, vp, i64, i32, vp, i64, i32, vp]),
+        # structures as bytes (packer)
+        "cb_paged_append": (S, [C.c_char_p, C.c_char_p, i32, vp]),
+        "cb_paged_attention": (S, [C.c_char_p, C.c_char_p, i32, vp]),
         "cb_paged_attention_workspace_size": (C.c_size_t, [i32, i32, i32, i32, i32, i32, i32]),
-        "cb_paged_attention": (S, [C.POINTER(PagedKV), vp, i64, i32, i32, i32, i32, i32,
-                                   C.c_float, vp, i64, i32, vp, C.c_size_t, vp]),
         "cb_sample_tokens": (S, [vp, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp]),
         "cb_selection_stats": (S, [vp, vp, C.POINTER(SelectReq), i32, vp, vp, vp]),
     }

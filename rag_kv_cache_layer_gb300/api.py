@@ -172,6 +172,7 @@ _cur_device = torch._C._cuda_getDevice
 _cur_stream = torch._C._cuda_getCurrentRawStream
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _CODES = {_BF16: L.CB_BF16, _F32: L.CB_F32}
+_pack_kv, _pack_rows, _pack_query = L.packer(L.PagedKV), L.packer(L.PagedRows), L.packer(L.PagedQuery)
 
 
 def _on_device(*tensors):
@@ -207,9 +208,9 @@ def _paged_kv(k_pages, v_pages, row_offsets, kv_lens, block_table):
         raise ValueError("k_pages and v_pages must have one shape, type and strides, with contiguous slots")
     n_pages, page, cols = shape[-3:]
     ld = strides[-2] if page > 1 else cols
-    kv = L.PagedKV(k_pages.data_ptr(), v_pages.data_ptr(), strides[-3] if n_pages > 1 else page * ld, ld,
-                   n_pages, page, block_table.data_ptr(), ld_table if n_seq > 1 else width, width,
-                   row_offsets.data_ptr(), kv_lens.data_ptr(), n_seq)
+    kv = _pack_kv(k_pages.data_ptr(), v_pages.data_ptr(), strides[-3] if n_pages > 1 else page * ld, ld,
+                  n_pages, page, block_table.data_ptr(), ld_table if n_seq > 1 else width, width,
+                  row_offsets.data_ptr(), kv_lens.data_ptr(), n_seq)
     return kv, shape
 
 
@@ -255,10 +256,11 @@ def cb_paged_append(k_new, v_new, row_offsets, kv_lens, block_table, k_pages, v_
         qop, ld_qo = (qp, ld_q) if q_out is None else (q_out.data_ptr(), _ld("q_out", q_out, dt, n_rows, q_cols))
     elif q_out is not None:
         raise ValueError("q_out without q")
-    status = lib.cb_paged_append(
-        C.byref(kv), k1.data_ptr(), _ld("k_new", k1, dt, n_rows, cols), sk, v1.data_ptr(),
-        _ld("v_new", v1, dt, n_rows, cols), sv, n_rows, layers, sc, cols // head_dim, head_dim, rope, max_pos,
-        qp, ld_q, n_q, qop, ld_qo, _CODES.get(dt, -1), _cur_stream(dev) if stream is None else stream.cuda_stream)
+    rows = _pack_rows(k1.data_ptr(), v1.data_ptr(), _ld("k_new", k1, dt, n_rows, cols),
+                      _ld("v_new", v1, dt, n_rows, cols), sk, sv, sc, n_rows, layers, cols // head_dim, head_dim,
+                      rope, qp, qop, ld_q, ld_qo, n_q, max_pos)
+    status = lib.cb_paged_append(kv, rows, _CODES.get(dt, -1),
+                                 _cur_stream(dev) if stream is None else stream.cuda_stream)
     if status:
         check(status)
 
@@ -288,12 +290,12 @@ def cb_paged_attention(q, row_offsets, kv_lens, block_table, k_pages, v_pages, n
     if max_kv_len is None:
         max_kv_len = min(block_table.shape[1] * shape[1], 2 ** 31 - 1)
     if ws is None:
-        ws = cb_paged_attention_workspace(q, kv.n_seq, max_kv_len, n_q_heads, n_kv_heads, head_dim)
-    status = lib.cb_paged_attention(
-        C.byref(kv), q.data_ptr(), _ld("q", q, dt, n_rows, cols), n_rows, max_kv_len, n_q_heads, n_kv_heads,
-        head_dim, 1.0 / math.sqrt(head_dim) if scale is None else scale, out.data_ptr(),
-        _ld("out", out, dt, n_rows, cols), _CODES.get(dt, -1), ws.data_ptr(), ws.nbytes,
-        _cur_stream(dev) if stream is None else stream.cuda_stream)
+        ws = cb_paged_attention_workspace(q, kv_lens.shape[0], max_kv_len, n_q_heads, n_kv_heads, head_dim)
+    query = _pack_query(q.data_ptr(), out.data_ptr(), _ld("q", q, dt, n_rows, cols), _ld("out", out, dt, n_rows, cols),
+                        ws.data_ptr(), ws.nbytes, n_rows, max_kv_len, n_q_heads, n_kv_heads, head_dim,
+                        1.0 / math.sqrt(head_dim) if scale is None else scale)
+    status = lib.cb_paged_attention(kv, query, _CODES.get(dt, -1),
+                                    _cur_stream(dev) if stream is None else stream.cuda_stream)
     if status:
         check(status)
 

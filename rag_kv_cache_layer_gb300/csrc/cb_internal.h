@@ -385,19 +385,13 @@ cudaError_t launch_attention_mass(const void *q, int64_t ld_q, int u_off, int n_
 
 // ----------------------------------------------------------- paged cache --
 typedef cb_paged_kv PagedKV;
-// rope nullptr: keys are copied; q nullptr: none.  Strides in elements.
-cudaError_t launch_paged_append(const PagedKV &kv, const void *k, int64_t ld_k, int64_t stride_k,
-                                const void *v, int64_t ld_v, int64_t stride_v, int n_rows,
-                                int n_layers, int64_t cache_stride, int Hkv, int hd,
-                                const float *rope, int max_pos, const void *q, int64_t ld_q,
-                                int Hq, void *q_out, int64_t ld_qo, cb_dtype dt, int *status,
+// Arguments checked by the entry points.
+cudaError_t launch_paged_append(const PagedKV &kv, const cb_paged_rows &rows, cb_dtype dt, int *status,
                                 cudaStream_t s);
 size_t paged_attention_ws_bytes(int n_rows, int n_seq, int max_kv, int Hq, int Hkv, int hd,
                                 cb_dtype dt);
 // cudaErrorInvalidConfiguration: more tiles than one launch takes.
-cudaError_t launch_paged_attention(const PagedKV &kv, const void *q, int64_t ld_q, int n_rows,
-                                   int max_kv, int Hq, int Hkv, int hd, float scale, void *out,
-                                   int64_t ld_out, cb_dtype dt, void *ws, int *status,
+cudaError_t launch_paged_attention(const PagedKV &kv, const cb_paged_query &query, cb_dtype dt, int *status,
                                    cudaStream_t s);
 cudaError_t launch_sample(const void *logits, int64_t ld, int n_rows, int vocab, cb_dtype dt,
                           const float *u, const float *temperature, const int32_t *top_k,

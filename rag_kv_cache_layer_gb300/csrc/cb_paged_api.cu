@@ -50,40 +50,35 @@ cb_status status_word(int **st) {
 
 }  // namespace
 
-extern "C" cb_status cb_paged_append(const cb_paged_kv *kv, const void *k_new, int64_t ld_k,
-                                     int64_t k_layer_stride, const void *v_new, int64_t ld_v,
-                                     int64_t v_layer_stride, int n_rows, int n_layers,
-                                     int64_t cache_layer_stride, int n_kv_heads, int head_dim,
-                                     const float *rope_table, int max_positions, const void *q,
-                                     int64_t ld_q, int n_q_heads, void *q_out, int64_t ld_q_out,
-                                     cb_dtype dtype, cb_stream stream) {
-  if (n_kv_heads <= 0 || head_dim <= 0 || head_dim % 16 || head_dim > 1024 || n_kv_heads > 4096)
+extern "C" cb_status cb_paged_append(const cb_paged_kv *kv, const cb_paged_rows *rows, cb_dtype dtype,
+                                     cb_stream stream) {
+  if (!rows) return bad("rows is NULL");
+  const cb_paged_rows &r = *rows;
+  if (r.n_kv_heads <= 0 || r.head_dim <= 0 || r.head_dim % 16 || r.head_dim > 1024 || r.n_kv_heads > 4096)
     return bad("n_kv_heads must be in [1, 4096], head_dim a multiple of 16 up to 1024");
-  const int64_t cols = (int64_t)n_kv_heads * head_dim;
+  const int64_t cols = (int64_t)r.n_kv_heads * r.head_dim;
   if (const cb_status s = check_paged(kv, cols, dtype)) return s;
-  if (n_rows < 0 || n_layers < 0 || n_layers > 65535) return bad("n_rows < 0 or n_layers outside [0, 65535]");
-  if (n_rows == 0 || n_layers == 0 || kv->n_seq == 0) return CB_OK;
+  if (r.n_rows < 0 || r.n_layers < 0 || r.n_layers > 65535)
+    return bad("n_rows < 0 or n_layers outside [0, 65535]");
+  if (r.n_rows == 0 || r.n_layers == 0 || kv->n_seq == 0) return CB_OK;
   const size_t eb = bytes_of(dtype);
-  if (!rows_ok(k_new, ld_k, cols, eb) || !rows_ok(v_new, ld_v, cols, eb))
-    return bad("k_new / v_new: NULL, misaligned, or a leading dimension below a row");
-  if (n_layers > 1 && (k_layer_stride * (int64_t)eb % 16 || v_layer_stride * (int64_t)eb % 16 ||
-                       cache_layer_stride * (int64_t)eb % 16))
+  if (!rows_ok(r.k, r.ld_k, cols, eb) || !rows_ok(r.v, r.ld_v, cols, eb))
+    return bad("k / v: NULL, misaligned, or a leading dimension below a row");
+  if (r.n_layers > 1 && (r.k_layer_stride * (int64_t)eb % 16 || r.v_layer_stride * (int64_t)eb % 16 ||
+                         r.cache_layer_stride * (int64_t)eb % 16))
     return bad("layer strides must be multiples of 16 bytes");
-  if (rope_table && (!aligned(rope_table, 16) || max_positions <= 0))
+  if (r.rope_table && (!aligned(r.rope_table, 16) || r.max_positions <= 0))
     return bad("rope_table misaligned or max_positions <= 0");
-  if (q || q_out) {
-    if (!rope_table || n_layers != 1) return bad("q is rotated: it needs rope_table and one layer");
-    if (n_q_heads <= 0 || n_q_heads > 4096) return bad("n_q_heads must be in [1, 4096]");
-    const int64_t qc = (int64_t)n_q_heads * head_dim;
-    if (!rows_ok(q, ld_q, qc, eb) || !rows_ok(q_out, ld_q_out, qc, eb))
+  if (r.q || r.q_out) {
+    if (!r.rope_table || r.n_layers != 1) return bad("q is rotated: it needs rope_table and one layer");
+    if (r.n_q_heads <= 0 || r.n_q_heads > 4096) return bad("n_q_heads must be in [1, 4096]");
+    const int64_t qc = (int64_t)r.n_q_heads * r.head_dim;
+    if (!rows_ok(r.q, r.ld_q, qc, eb) || !rows_ok(r.q_out, r.ld_q_out, qc, eb))
       return bad("q / q_out: NULL, misaligned, or a leading dimension below a row");
   }
   int *st;
   if (const cb_status s = status_word(&st)) return s;
-  return cuda(launch_paged_append(*kv, k_new, ld_k, k_layer_stride, v_new, ld_v, v_layer_stride,
-                                  n_rows, n_layers, cache_layer_stride, n_kv_heads, head_dim,
-                                  rope_table, max_positions, q, ld_q, n_q_heads, q_out, ld_q_out,
-                                  dtype, st, stream));
+  return cuda(launch_paged_append(*kv, r, dtype, st, stream));
 }
 
 static bool paged_heads_ok(int Hq, int Hkv, int hd) {
@@ -100,30 +95,30 @@ extern "C" size_t cb_paged_attention_workspace_size(int n_rows, int n_seq, int m
   return n > 256 ? n : 256;
 }
 
-extern "C" cb_status cb_paged_attention(const cb_paged_kv *kv, const void *q, int64_t ld_q,
-                                        int n_rows, int max_kv_len, int n_q_heads, int n_kv_heads,
-                                        int head_dim, float scale, void *out, int64_t ld_out,
-                                        cb_dtype dtype, void *ws, size_t ws_bytes, cb_stream stream) {
-  if (!paged_heads_ok(n_q_heads, n_kv_heads, head_dim))
+extern "C" cb_status cb_paged_attention(const cb_paged_kv *kv, const cb_paged_query *query, cb_dtype dtype,
+                                        cb_stream stream) {
+  if (!query) return bad("query is NULL");
+  const cb_paged_query &a = *query;
+  if (!paged_heads_ok(a.n_q_heads, a.n_kv_heads, a.head_dim))
     return bad("n_q_heads must be 1 to 128 times n_kv_heads, head_dim 64 or 128");
-  if (const cb_status s = check_paged(kv, (int64_t)n_kv_heads * head_dim, dtype)) return s;
-  if (n_rows < 0 || max_kv_len < 0) return bad("n_rows < 0 or max_kv_len < 0");
-  if (!(scale >= 0.f) || isinf(scale)) return bad("scale must be finite and >= 0");
-  if (n_rows == 0 || kv->n_seq == 0) return CB_OK;
+  if (const cb_status s = check_paged(kv, (int64_t)a.n_kv_heads * a.head_dim, dtype)) return s;
+  if (a.n_rows < 0 || a.max_kv_len < 0) return bad("n_rows < 0 or max_kv_len < 0");
+  if (!(a.scale >= 0.f) || isinf(a.scale)) return bad("scale must be finite and >= 0");
+  if (a.n_rows == 0 || kv->n_seq == 0) return CB_OK;
   const size_t eb = bytes_of(dtype);
-  const int64_t cols = (int64_t)n_q_heads * head_dim;
-  if (!rows_ok(q, ld_q, cols, eb) || !rows_ok(out, ld_out, cols, eb))
+  const int64_t cols = (int64_t)a.n_q_heads * a.head_dim;
+  if (!rows_ok(a.q, a.ld_q, cols, eb) || !rows_ok(a.out, a.ld_out, cols, eb))
     return bad("q / out: NULL, misaligned, or a leading dimension below a row");
-  const size_t need = paged_attention_ws_bytes(n_rows, kv->n_seq, max_kv_len, n_q_heads, n_kv_heads, head_dim, dtype);
-  if (need > 0 && (!ws || ws_bytes < need || !aligned(ws, 16))) {
+  const size_t need = paged_attention_ws_bytes(a.n_rows, kv->n_seq, a.max_kv_len, a.n_q_heads, a.n_kv_heads,
+                                               a.head_dim, dtype);
+  if (need > 0 && (!a.ws || a.ws_bytes < need || !aligned(a.ws, 16))) {
     char msg[96];
-    snprintf(msg, sizeof msg, "paged attention workspace too small or misaligned (%zu < %zu)", ws_bytes, need);
+    snprintf(msg, sizeof msg, "paged attention workspace too small or misaligned (%zu < %zu)", a.ws_bytes, need);
     return record_error(CB_ERR_WORKSPACE, msg);
   }
   int *st;
   if (const cb_status s = status_word(&st)) return s;
-  const cudaError_t e = launch_paged_attention(*kv, q, ld_q, n_rows, max_kv_len, n_q_heads, n_kv_heads, head_dim,
-                                               scale, out, ld_out, dtype, ws, st, stream);
+  const cudaError_t e = launch_paged_attention(*kv, a, dtype, st, stream);
   if (e == cudaErrorInvalidConfiguration)
     return record_error(CB_ERR_UNSUPPORTED, "more query tiles than one launch takes: split the call");
   return cuda(e);

@@ -129,30 +129,26 @@ paged_append_kernel(const __grid_constant__ AppendParams P, int *status) {
   }
 }
 
-cudaError_t launch_paged_append(const PagedKV &kv, const void *k, int64_t ld_k, int64_t stride_k,
-                                const void *v, int64_t ld_v, int64_t stride_v, int n_rows,
-                                int n_layers, int64_t cache_stride, int Hkv, int hd,
-                                const float *rope, int max_pos, const void *q, int64_t ld_q,
-                                int Hq, void *q_out, int64_t ld_qo, cb_dtype dt, int *status,
+cudaError_t launch_paged_append(const PagedKV &kv, const cb_paged_rows &r, cb_dtype dt, int *status,
                                 cudaStream_t s) {
-  if (n_rows == 0 || n_layers == 0) return cudaSuccess;
   AppendParams P;
   P.kv = kv;
-  P.k = k; P.v = v; P.q = q; P.q_out = q_out;
-  P.ld_k = ld_k; P.ld_v = ld_v; P.ld_q = ld_q; P.ld_qo = ld_qo;
-  P.new_stride_k = stride_k; P.new_stride_v = stride_v;
-  P.cache_stride = cache_stride;
-  P.n_rows = n_rows;
-  P.max_pos = max_pos;
-  P.half = hd / 2;
-  P.rope = reinterpret_cast<const float2 *>(rope);
+  P.k = r.k; P.v = r.v; P.q = r.q; P.q_out = r.q_out;
+  P.ld_k = r.ld_k; P.ld_v = r.ld_v; P.ld_q = r.ld_q; P.ld_qo = r.ld_q_out;
+  P.new_stride_k = r.k_layer_stride; P.new_stride_v = r.v_layer_stride;
+  P.cache_stride = r.cache_layer_stride;
+  P.n_rows = r.n_rows;
+  P.max_pos = r.max_positions;
+  P.half = r.head_dim / 2;
+  P.rope = reinterpret_cast<const float2 *>(r.rope_table);
+  const float2 *rope = P.rope;
   const int vec = dt == CB_BF16 ? 8 : 4;
-  P.v_units = Hkv * hd / vec;
+  P.v_units = r.n_kv_heads * r.head_dim / vec;
   P.k_units = rope ? P.v_units / 2 : P.v_units;
-  P.q_units = q ? Hq * hd / vec / 2 : 0;
+  P.q_units = r.q ? r.n_q_heads * r.head_dim / vec / 2 : 0;
   const int per_row = P.v_units + P.k_units + P.q_units;
   P.rows_per_block = max(1, min(kAppendRows, 4 * kAppendThreads / per_row));
-  const dim3 grid((n_rows + P.rows_per_block - 1) / P.rows_per_block, n_layers);
+  const dim3 grid((r.n_rows + P.rows_per_block - 1) / P.rows_per_block, r.n_layers);
   cudaError_t e;
   if (dt == CB_BF16)
     e = rope ? launch_pdl(paged_append_kernel<bf16, true>, grid, dim3(kAppendThreads), 0, s, P, status)

@@ -111,28 +111,27 @@ size_t paged_attention_ws_bytes(int n_rows, int n_seq, int max_kv, int Hq, int H
   return plan_bytes(plan(n_rows, n_seq, max_kv, Hq / Hkv, Hkv, hd, dt), hd);
 }
 
-cudaError_t launch_paged_attention(const PagedKV &kv, const void *q, int64_t ld_q, int n_rows, int max_kv,
-                                   int Hq, int Hkv, int hd, float scale, void *out, int64_t ld_out,
-                                   cb_dtype dt, void *ws, int *status, cudaStream_t s) {
+cudaError_t launch_paged_attention(const PagedKV &kv, const cb_paged_query &a, cb_dtype dt, int *status,
+                                   cudaStream_t s) {
   using namespace paged;
-  if (n_rows == 0 || kv.n_seq == 0) return cudaSuccess;
-  const Plan p = plan(n_rows, kv.n_seq, max_kv, Hq / Hkv, Hkv, hd, dt);
-  if (p.tiles * Hkv * p.n_split > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const int G = a.n_q_heads / a.n_kv_heads;
+  const Plan p = plan(a.n_rows, kv.n_seq, a.max_kv_len, G, a.n_kv_heads, a.head_dim, dt);
+  if (p.tiles * a.n_kv_heads * p.n_split > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   AttnParams P;
   P.kv = kv;
-  P.q = q;
-  P.out = out;
-  P.ld_q = ld_q;
-  P.ld_out = ld_out;
-  P.n_rows = n_rows;
-  P.G = Hq / Hkv;
-  P.Hkv = Hkv;
-  P.max_kv = max_kv;
+  P.q = a.q;
+  P.out = a.out;
+  P.ld_q = a.ld_q;
+  P.ld_out = a.ld_out;
+  P.n_rows = a.n_rows;
+  P.G = G;
+  P.Hkv = a.n_kv_heads;
+  P.max_kv = a.max_kv_len;
   P.n_split = p.n_split;
   P.few_hi = p.few_hi;
   P.rows_lo = p.rows_lo;
-  P.scale_log2 = scale * 1.4426950408889634f;
-  return run_plan(P, p, hd, dt, ws, status, s);
+  P.scale_log2 = a.scale * 1.4426950408889634f;
+  return run_plan(P, p, a.head_dim, dt, a.ws, status, s);
 }
 
 }  // namespace cb

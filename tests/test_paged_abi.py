@@ -1,6 +1,8 @@
 """Host-side refusals of the generation operators (no device needed) and hand
 values of their float64 oracle."""
 import ctypes as C
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -10,22 +12,23 @@ import rag_kv_cache_layer_gb300 as R
 from oracle import paged as OP
 from rag_kv_cache_layer_gb300 import _lib as L
 
-P = C.c_void_p
-A = P(4096)          # an aligned address that validation never follows
+A = 4096             # an aligned address that validation never follows
 
 
 def _kv(**kw):
     d = dict(k_pages=4096, v_pages=4096, page_stride=16 * 256, ld=256, n_pages=4, page_size=16,
              block_table=4096, ld_table=8, max_pages=8, row_offsets=4096, kv_lens=4096, n_seq=2)
     d.update(kw)
-    return L.PagedKV(*[d[f] for f, _ in L.PagedKV._fields_])
+    return L.packer(L.PagedKV)(*[d[f] for f, _ in L.PagedKV._fields_])
 
 
-def _append(kv=None, k=A, ld_k=256, ks=0, v=A, ld_v=256, vs=0, rows=3, layers=1, cs=0, heads=2, hd=128,
-            rope=A, maxp=64, q=None, ld_q=0, nq=0, qo=None, ld_qo=0, dt=L.CB_BF16):
-    kv = _kv() if kv is None else kv
-    return L.lib.cb_paged_append(C.byref(kv) if kv else None, k, ld_k, ks, v, ld_v, vs, rows, layers, cs, heads,
-                                 hd, rope, maxp, q, ld_q, nq, qo, ld_qo, dt, None)
+def _append(kv=None, dt=L.CB_BF16, **kw):
+    d = dict(k=A, v=A, ld_k=256, ld_v=256, k_layer_stride=0, v_layer_stride=0, cache_layer_stride=0, n_rows=3,
+             n_layers=1, n_kv_heads=2, head_dim=128, rope_table=A, q=0, q_out=0, ld_q=0, ld_q_out=0, n_q_heads=0,
+             max_positions=64)
+    d.update(kw)
+    rows = L.packer(L.PagedRows)(*[d[f] for f, _ in L.PagedRows._fields_])
+    return L.lib.cb_paged_append(_kv() if kv is None else kv, rows, dt, None)
 
 
 BAD_KV = [dict(k_pages=0), dict(v_pages=4098), dict(ld=248), dict(ld=260), dict(page_stride=256),
@@ -49,38 +52,73 @@ def test_page_size_is_refused(kw):
 
 
 @pytest.mark.parametrize("kw", [
-    dict(k=None), dict(v=None), dict(k=P(4098)), dict(ld_k=255), dict(ld_v=128), dict(rows=-1),
-    dict(layers=-1), dict(layers=65536), dict(layers=2, ks=4, cs=8), dict(layers=2, ks=8, cs=4), dict(heads=0),
-    dict(hd=120), dict(hd=0), dict(dt=7), dict(rope=P(4100)), dict(maxp=0),
-    dict(q=A, ld_q=512, nq=4), dict(qo=A, ld_qo=512, nq=4),            # only one of the two
-    dict(q=A, ld_q=512, qo=A, ld_qo=512, nq=0), dict(q=A, ld_q=504, qo=A, ld_qo=512, nq=4),
-    dict(q=A, ld_q=512, qo=A, ld_qo=512, nq=4, rope=None),             # nothing to rotate by
-    dict(q=A, ld_q=512, qo=A, ld_qo=512, nq=4, layers=2)])
+    dict(k=0), dict(v=0), dict(k=4098), dict(ld_k=255), dict(ld_v=128), dict(n_rows=-1), dict(n_layers=-1),
+    dict(n_layers=65536), dict(n_layers=2, k_layer_stride=4), dict(n_layers=2, v_layer_stride=4),
+    dict(n_layers=2, cache_layer_stride=4), dict(n_kv_heads=0), dict(head_dim=120), dict(head_dim=0), dict(dt=7),
+    dict(rope_table=4100), dict(max_positions=0),
+    dict(q=A, ld_q=512, n_q_heads=4), dict(q_out=A, ld_q_out=512, n_q_heads=4),     # only one of the two
+    dict(q=A, ld_q=512, q_out=A, ld_q_out=512, n_q_heads=0), dict(q=A, ld_q=504, q_out=A, ld_q_out=512, n_q_heads=4),
+    dict(q=A, ld_q=512, q_out=A, ld_q_out=512, n_q_heads=4, rope_table=0),          # nothing to rotate by
+    dict(q=A, ld_q=512, q_out=A, ld_q_out=512, n_q_heads=4, n_layers=2)])
 def test_append_refusals(kw):
     assert _append(**kw) == L.CB_ERR_INVALID_ARG
     assert L.lib.cb_last_error_message()
 
 
 def test_empty_calls_are_done():
-    assert _append(rows=0, k=None, v=None) == L.CB_OK
-    assert _append(layers=0, k=None) == L.CB_OK
+    assert _append(n_rows=0, k=0, v=0) == L.CB_OK
+    assert _append(n_layers=0, k=0) == L.CB_OK
     assert _append(_kv(n_seq=0, row_offsets=0, kv_lens=0, block_table=0)) == L.CB_OK
-    assert _attn(rows=0, q=None) == L.CB_OK
+    assert _attn(n_rows=0, q=0) == L.CB_OK
     assert _attn(_kv(n_seq=0, row_offsets=0, kv_lens=0, block_table=0)) == L.CB_OK
     assert L.lib.cb_sample_tokens(None, 8, 0, 8, 0, None, None, None, None, None, None, None) == L.CB_OK
 
 
-def _attn(kv=None, q=A, ld_q=512, rows=3, max_kv=64, hq=4, hkv=2, hd=128, out=A, ld_out=512, dt=L.CB_BF16,
-          ws=A, wsb=1 << 30, scale=0.1):
-    kv = _kv() if kv is None else kv
-    return L.lib.cb_paged_attention(C.byref(kv) if kv else None, q, ld_q, rows, max_kv, hq, hkv, hd, scale, out,
-                                    ld_out, dt, ws, wsb, None)
+def test_null_structures():
+    kv = _kv()
+    rows, query = bytes(C.sizeof(L.PagedRows)), bytes(C.sizeof(L.PagedQuery))
+    for call, arg in ((L.lib.cb_paged_append, rows), (L.lib.cb_paged_attention, query)):
+        assert call(None, arg, L.CB_BF16, None) == L.CB_ERR_INVALID_ARG
+        assert call(kv, None, L.CB_BF16, None) == L.CB_ERR_INVALID_ARG
+        assert call(kv, arg, L.CB_BF16, None) == L.CB_ERR_INVALID_ARG          # zeros in every field
+
+
+STRUCTS = {"cb_paged_kv": L.PagedKV, "cb_paged_rows": L.PagedRows, "cb_paged_query": L.PagedQuery}
+
+
+def test_ctypes_mirrors_match_c_layout(tmp_path):
+    """Sizes and offsets as the C compiler sees them, and as packed."""
+    src = ["#include <stdio.h>", "#include <stddef.h>", '#include "cacheblend.h"', "int main(void) {"]
+    for name, cls in STRUCTS.items():
+        src.append(f'printf("{name} %zu\\n", sizeof({name}));')
+        src += [f'printf("{name}.{f} %zu\\n", offsetof({name}, {f}));' for f, _ in cls._fields_]
+    (tmp_path / "l.c").write_text("\n".join(src + ["return 0; }"]))
+    inc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    subprocess.run(["gcc", "-std=c99", "-I", inc, str(tmp_path / "l.c"), "-o", str(tmp_path / "l")], check=True)
+    got = dict(x.rsplit(" ", 1) for x in subprocess.run([str(tmp_path / "l")], capture_output=True, text=True,
+                                                        check=True).stdout.strip().splitlines())
+    for name, cls in STRUCTS.items():
+        assert int(got[name]) == C.sizeof(cls)
+        values = []
+        for i, (f, t) in enumerate(cls._fields_):
+            assert int(got[f"{name}.{f}"]) == getattr(cls, f).offset, (name, f)
+            values.append(i + 1)
+        back = cls.from_buffer_copy(L.packer(cls)(*values))
+        assert [getattr(back, f) for f, _ in cls._fields_] == values
+
+
+def _attn(kv=None, dt=L.CB_BF16, **kw):
+    d = dict(q=A, out=A, ld_q=512, ld_out=512, ws=A, ws_bytes=1 << 30, n_rows=3, max_kv_len=64, n_q_heads=4,
+             n_kv_heads=2, head_dim=128, scale=0.1)
+    d.update(kw)
+    query = L.packer(L.PagedQuery)(*[d[f] for f, _ in L.PagedQuery._fields_])
+    return L.lib.cb_paged_attention(_kv() if kv is None else kv, query, dt, None)
 
 
 @pytest.mark.parametrize("kw", [
-    dict(q=None), dict(out=None), dict(q=P(4104)), dict(ld_q=504), dict(ld_out=508), dict(rows=-1), dict(max_kv=-1),
-    dict(hq=3), dict(hq=0), dict(hkv=0), dict(hq=258, hkv=2), dict(hd=96), dict(dt=2),
-    dict(scale=-0.1), dict(scale=float("nan")), dict(scale=float("inf"))])
+    dict(q=0), dict(out=0), dict(q=4104), dict(ld_q=504), dict(ld_out=508), dict(n_rows=-1), dict(max_kv_len=-1),
+    dict(n_q_heads=3), dict(n_q_heads=0), dict(n_kv_heads=0), dict(n_q_heads=258, n_kv_heads=2), dict(head_dim=96),
+    dict(dt=2), dict(scale=-0.1), dict(scale=float("nan")), dict(scale=float("inf"))])
 def test_attention_refusals(kw):
     assert _attn(**kw) == L.CB_ERR_INVALID_ARG
 
@@ -89,18 +127,18 @@ def test_attention_workspace():
     size = L.lib.cb_paged_attention_workspace_size
     need = size(1, 1, 100000, 32, 8, 128, L.CB_BF16)
     assert need > 256                       # one row over many keys: the range is split
-    kv = _kv(ld=1024, page_stride=16 * 1024, n_seq=1)
-    kw = dict(kv=kv, rows=1, max_kv=100000, hq=32, hkv=8, ld_q=4096, ld_out=4096)
-    assert _attn(ws=None, **kw) == L.CB_ERR_WORKSPACE
-    assert _attn(wsb=need - 1, **kw) == L.CB_ERR_WORKSPACE
-    assert _attn(ws=P(4100), **kw) == L.CB_ERR_WORKSPACE
+    kw = dict(kv=_kv(ld=1024, page_stride=16 * 1024, n_seq=1), n_rows=1, max_kv_len=100000, n_q_heads=32,
+              n_kv_heads=8, ld_q=4096, ld_out=4096)
+    assert _attn(ws=0, **kw) == L.CB_ERR_WORKSPACE
+    assert _attn(ws_bytes=need - 1, **kw) == L.CB_ERR_WORKSPACE
+    assert _attn(ws=4100, **kw) == L.CB_ERR_WORKSPACE
     for bad in [(-1, 1, 8, 4, 2, 128, 1), (1, 1025, 8, 4, 2, 128, 1), (1, 1, 8, 3, 2, 128, 1), (1, 1, 8, 4, 2, 80, 1)]:
         assert size(*bad) == 256
 
 
 @pytest.mark.parametrize("kw", [
     dict(logits=None), dict(u=None), dict(tokens=None), dict(ld=999), dict(rows=-1), dict(rows=(1 << 20) + 1),
-    dict(vocab=0), dict(dt=2), dict(logits=P(4098)), dict(u=P(4097)), dict(topk=P(4098))])
+    dict(vocab=0), dict(dt=2), dict(logits=4098), dict(u=4097), dict(topk=4098)])
 def test_sample_refusals(kw):
     a = dict(logits=A, ld=1000, rows=2, vocab=1000, dt=L.CB_F32, u=A, t=None, topk=None, topp=None, minp=None,
              tokens=A)
