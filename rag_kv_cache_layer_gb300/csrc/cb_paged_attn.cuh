@@ -8,7 +8,7 @@ namespace cb {
 namespace paged {
 
 // An item of the few-rows kernel whose keys more than one block has: its rows
-// (0: nothing to join), the last block with a piece, and whether the first
+// (0: nothing to join), its first kv head, the last block with a piece, and whether the first
 // block's piece is its second.
 struct Join {
   int row0, l0, rows, g, last, second;
@@ -24,6 +24,7 @@ struct AttnParams {
   // Sequences by rows (queries x G): the few-rows kernel takes those up to
   // few_hi, the chunk kernel those above rows_lo.
   int few_hi, rows_lo;
+  int hc;                                 // kv heads per item of the few-rows kernel
   float scale_log2;                       // softmax scale times log2(e)
   float *part_o;                          // unnormalised partial rows, HD floats each
   float2 *part_ml;                        // (m, l) of each partial row
@@ -31,8 +32,10 @@ struct AttnParams {
 };
 
 // Few rows per sequence, and all of fp32: R (16, 32 or 64) rows per tile.  The
-// workspace holds 2 * decode_grid() * R partial rows and decode_grid() joins.
+// workspace holds 2 * decode_grid() * R * hc partial rows and decode_grid()
+// joins.
 int decode_grid();
+int decode_heads(int R, int64_t tiles, int Hkv);   // hc, for that many tiles
 cudaError_t launch_decode(const AttnParams &P, int R, int hd, cb_dtype dt, int *status, cudaStream_t s);
 
 // bf16, many rows: units of R (128 or 256) rows, their keys in n_split parts;

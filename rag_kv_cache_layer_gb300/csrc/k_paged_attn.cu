@@ -16,7 +16,7 @@ static int64_t tile_bound(int64_t n_rows, int S, int G, int R) {
 
 // How a call runs.
 struct Plan {
-  int few_R;                              // few-rows kernel: rows per tile, 0: not launched
+  int few_R, hc;                          // few-rows kernel: rows per tile (0: not launched), heads per item
   int R;                                  // chunk kernel: rows per unit, 0: not launched
   int few_hi, rows_lo;                    // which sequences each takes
   int64_t tiles;                          // chunk units at most
@@ -69,7 +69,8 @@ static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd, cb_d
   p.few_hi = 0x7fffffff;
   p.n_split = 1;
   if (few || S > 1) p.few_R = per_seq <= 16 ? 16 : per_seq <= 32 ? 32 : few || per_seq <= 64 ? 64 : 16;
-  p.few_partials = p.few_R ? 2LL * decode_grid() * p.few_R : 0;
+  p.hc = p.few_R ? decode_heads(p.few_R, tile_bound(n_rows, S, G, p.few_R), Hkv) : 1;
+  p.few_partials = p.few_R ? 2LL * decode_grid() * p.few_R * p.hc : 0;
   if (few) return p;
   if (S > 1) p.few_hi = p.rows_lo = 64;
   plan_chunk(p, n_rows, S, max_kv, G, Hkv, hd);
@@ -130,6 +131,7 @@ cudaError_t launch_paged_attention(const PagedKV &kv, const cb_paged_query &a, c
   P.n_split = p.n_split;
   P.few_hi = p.few_hi;
   P.rows_lo = p.rows_lo;
+  P.hc = p.hc;
   P.scale_log2 = a.scale * 1.4426950408889634f;
   return run_plan(P, p, a.head_dim, dt, a.ws, status, s);
 }

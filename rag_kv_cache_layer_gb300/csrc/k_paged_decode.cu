@@ -12,8 +12,13 @@
 // block, and decode_merge_kernel joins them; the block with an item's first
 // piece also leaves the join's record, so the joining kernel searches nothing.
 //
-// A block's four warps form WK = 4 / WM groups of WM warps; key block i goes
-// to group i mod WK.  A group fills a ring of its own by 16-byte cp.async,
+// A block's four warps form WK = 4 / WM groups of WM warps.  With many items
+// (hc = WK, decode_heads) an item is WK neighbouring heads, one per group, all
+// groups walking the same keys: their slices of a cache row lie side by side
+// and are read together, which the memory's pages like (64 ragged requests:
+// 148 us with a head per item, 128 so), and the groups' states need no join.
+// Else (hc = 1) an item is one head, and key block i goes to group i mod WK.
+// A group fills a ring of its own by 16-byte cp.async,
 // two blocks ahead, with zeros for keys past the cached length (so nothing
 // unwritten in a page reaches the products), and meets nobody else inside the
 // loop.  TMA is not used here: a page's slice of one head is a box of 8 to 64
@@ -117,8 +122,8 @@ template <int WM> __device__ __forceinline__ void group_sync(int wk) {
 }
 
 // ------------------------------------------------------------------ plan --
-// The line of units.  Sequence s has items(s) = tiles * Hkv items of blocks(s)
-// units each (every tile counts the sequence's whole length; the few keys a
+// The line of units.  Sequence s has items(s) = tiles * Hkv / hc items of
+// blocks(s) units each (every tile counts the sequence's whole length; the few keys a
 // tile's last row does not see are skipped when met).
 struct Line {
   int64_t begin[CB_MAX_SEQS];     // first unit of each sequence
@@ -154,7 +159,7 @@ __device__ __forceinline__ void make_line(const AttnParams &P, int R, int BN, in
           nb = len > 0 ? (len - 1) / BN + 1 : 1;        // an idle slot's rows get their zeros
       }
       L.blocks[i0 + k] = nb;
-      u[k] = nb ? ((int64_t)n * P.G + R - 1) / R * P.Hkv * nb : 0;
+      u[k] = nb ? ((int64_t)n * P.G + R - 1) / R * (P.Hkv / P.hc) * nb : 0;
     }
     sum += u[k];
   }
@@ -176,8 +181,8 @@ __device__ __forceinline__ void make_line(const AttnParams &P, int R, int BN, in
   }
   if (threadIdx.x == NT - 1) {
     L.total = first;
-    // a part has at least one unit for each consumer group
-    const int64_t most = (first + 3) / 4;
+    // a part has at least one unit, or one for each group that shares its head
+    const int64_t most = P.hc > 1 ? first : (first + 3) / 4;
     L.parts = (int)(most < grid ? most : grid);
   }
   __syncthreads();
@@ -193,7 +198,8 @@ __device__ __forceinline__ int seq_of(const Line &L, int n_seq, int64_t u) {
   return lo;                      // the last one that begins at or before u
 }
 
-template <typename T, int HD, int WM>
+// HEADS: an item is WK heads, one per group (P.hc = WK); else one head.
+template <typename T, int HD, int WM, bool HEADS>
 __global__ void __launch_bounds__(kDecThreads, kDecBlocksPerSm)
 paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
   typedef DecCfg<T, HD, WM> C;
@@ -216,6 +222,9 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wm = warp % WM, wk = warp / WM, gid = lane >> 2, q4 = lane & 3;
   const uint32_t ring = smem_u32(smem) + wk * NS * C::kStage;
+  // heads per item; this group's head among them, its first key block, its step
+  constexpr int hc = HEADS ? WK : 1, step = HEADS ? 1 : WK;
+  const int sub = HEADS ? wk : 0, first_block = HEADS ? 0 : wk;
   const int shift = __ffs(P.kv.page_size) - 1;
   const T *kp = reinterpret_cast<const T *>(P.kv.k_pages), *vp = reinterpret_cast<const T *>(P.kv.v_pages);
   // rows and column that this lane copies: row i * kRows + crow of a stage
@@ -239,14 +248,14 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
     const int row0 = __ldg(P.kv.row_offsets + s), n = __ldg(P.kv.row_offsets + s + 1) - row0;
     // tiles from both ends in turn: early ones see fewer keys than the line
     // counts for them, so neighbours even out
-    const int g = item % P.Hkv, k = item / P.Hkv, tiles = (int)(((int64_t)n * P.G + R - 1) / R);
+    const int quads = P.Hkv / hc, g0 = item % quads * hc, g = g0 + sub, k = item / quads, tiles = (int)(((int64_t)n * P.G + R - 1) / R);
     const int l0 = ((k & 1) ? tiles - 1 - k / 2 : k / 2) * R;
     const int kv = __ldg(P.kv.kv_lens + s), base = kv - n, rows = min(R, n * P.G - l0);
     const int seen = base + (l0 + rows - 1) / P.G + 1;        // keys the tile's last row sees
     const int je = min(jb + take, seen > 0 ? (seen - 1) / BN + 1 : 0);
     const int32_t *table = P.kv.block_table + (int64_t)s * P.kv.ld_table;
     if (threadIdx.x == 0 && u == u1)            // the last piece: the one that may go on in the next part
-      *join = Join{row0, l0, jb == 0 && item_end > u1 ? rows : 0, g, part_of(line, item_end - 1), first ? 0 : 1};
+      *join = Join{row0, l0, jb == 0 && item_end > u1 ? rows : 0, g0, part_of(line, item_end - 1), first ? 0 : 1};
 
     auto fetch = [&](int j) -> int {            // page of key j * BN + lane
       const int key = j * BN + lane;
@@ -298,21 +307,20 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
 
-    // group's blocks: jb + wk, jb + wk + WK, ..; the table is read one block
-    // further ahead than the pages
-    int page = fetch(jb + wk);
+    // the table is read one block further ahead than the pages
+    int page = fetch(jb + first_block);
     for (int i = 0; i < NS - 1; ++i) {
-      const int j = jb + wk + i * WK, next = fetch(j + WK);
+      const int j = jb + first_block + i * step, next = fetch(j + step);
       if (j < je) load(j, i, page);
       page = next;
       commit();
     }
     int st = 0, fill = NS - 1;
-    for (int j = jb + wk; j < je; j += WK) {
+    for (int j = jb + first_block; j < je; j += step) {
       asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
       group_sync<WM>(wk);                       // landed for every warp; the stage before is used up
       {
-        const int jn = j + (NS - 1) * WK, next = fetch(jn + WK);
+        const int jn = j + (NS - 1) * step, next = fetch(jn + step);
         if (jn < je) load(jn, fill, page);
         page = next;
         commit();
@@ -438,16 +446,19 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
         *reinterpret_cast<float2 *>(so + (warp * 16 + gid + 8 * h) * LD + d * 8 + q4 * 2) =
             make_float2(o[d][2 * h], o[d][2 * h + 1]);
     __syncthreads();
-    const int64_t slot = (2 * (int64_t)blockIdx.x + (first ? 0 : 1)) * R;
-    for (int i = threadIdx.x; i < rows * (HD / 4); i += kDecThreads) {
-      const int r = i / (HD / 4), c = i % (HD / 4) * 4;
+    const int64_t slot = (2 * (int64_t)blockIdx.x + (first ? 0 : 1)) * R * hc;
+    const int per_head = rows * (HD / 4);
+    for (int i = threadIdx.x; i < hc * per_head; i += kDecThreads) {
+      const int hs = HEADS ? i / per_head : 0, e = i - hs * per_head;
+      const int r = e / (HD / 4), c = e % (HD / 4) * 4;
       float M = -INFINITY, L = 0.f;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      // the states of the head's groups: all, or its own
 #pragma unroll
-      for (int k = 0; k < WK; ++k) M = fmaxf(M, s_ml[(k * WM + r / 16) * 16 + r % 16].x);
+      for (int k = 0; k < WK / hc; ++k) M = fmaxf(M, s_ml[((hs + k) * WM + r / 16) * 16 + r % 16].x);
 #pragma unroll
-      for (int k = 0; k < WK; ++k) {
-        const int row = (k * WM + r / 16) * 16 + r % 16;
+      for (int k = 0; k < WK / hc; ++k) {
+        const int row = ((hs + k) * WM + r / 16) * 16 + r % 16;
         const float2 ml = s_ml[row];
         const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
         const float4 v = *reinterpret_cast<const float4 *>(so + row * LD + c);
@@ -455,12 +466,13 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
         a.x += w * v.x; a.y += w * v.y; a.z += w * v.z; a.w += w * v.w;
       }
       if (!whole) {
-        *reinterpret_cast<float4 *>(P.part_o + (slot + r) * HD + c) = a;
-        if (c == 0) P.part_ml[slot + r] = make_float2(M, L);
+        const int64_t at = slot + hs * R + r;
+        *reinterpret_cast<float4 *>(P.part_o + at * HD + c) = a;
+        if (c == 0) P.part_ml[at] = make_float2(M, L);
       } else {
         const float inv = L == 0.f ? 0.f : 1.f / L;
         T *dst = reinterpret_cast<T *>(P.out) + (int64_t)(row0 + (l0 + r) / P.G) * P.ld_out +
-                 (int64_t)(g * P.G + (l0 + r) % P.G) * HD + c;
+                 (int64_t)((g0 + hs) * P.G + (l0 + r) % P.G) * HD + c;
         if constexpr (F32)
           *reinterpret_cast<float4 *>(dst) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
         else
@@ -487,12 +499,13 @@ decode_merge_kernel(const __grid_constant__ AttnParams P, int R) {
   grid_dep_wait();
   grid_dep_launch();
   const Join J = P.joins[blockIdx.x];
-  if ((int)blockIdx.y * kJoinRows >= J.rows) return;
+  // rows r0 .. r0 + 3 of one of the item's heads
+  const int hs = blockIdx.y * kJoinRows / R, r0 = blockIdx.y * kJoinRows % R;
+  if (r0 >= J.rows) return;
   const int first = blockIdx.x, count = J.last - first + 1;
   // a later part's first slot; this part's first or second
-  auto slot = [&](int c) { return (2 * (int64_t)(first + c) + (c == 0 ? J.second : 0)) * R; };
+  auto slot = [&](int c) { return ((2 * (int64_t)(first + c) + (c == 0 ? J.second : 0)) * P.hc + hs) * R; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r0 = blockIdx.y * kJoinRows;
   for (int i = threadIdx.x; i < count * kJoinRows; i += kJoinThreads) {
     const int c = i / kJoinRows, r = r0 + i % kJoinRows;
     s_ml[i] = r < J.rows ? P.part_ml[slot(c) + r] : make_float2(-INFINITY, 0.f);
@@ -547,7 +560,7 @@ decode_merge_kernel(const __grid_constant__ AttnParams P, int R) {
     }
     if (r0 + k >= J.rows) continue;
     T *dst = reinterpret_cast<T *>(P.out) + (int64_t)(J.row0 + l / P.G) * P.ld_out +
-             (int64_t)(J.g * P.G + l % P.G) * HD + c;
+             (int64_t)((J.g + hs) * P.G + l % P.G) * HD + c;
     if constexpr (std::is_same<T, float>::value)
       *reinterpret_cast<float2 *>(dst) = make_float2(a * s_inv[k], b * s_inv[k]);
     else
@@ -556,35 +569,42 @@ decode_merge_kernel(const __grid_constant__ AttnParams P, int R) {
 }
 
 int decode_grid() { return kDecBlocksPerSm * device_sm_count(); }
+// Heads per item: as many as the block has groups where that leaves at least
+// one item for every eight parts, else one (an item in many pieces is joined
+// slowly: one row over 3137 keys took 23 us with four heads per item, 11 with
+// one; 64 ragged sequences 128 and 148).
+int decode_heads(int R, int64_t tiles, int Hkv) {
+  const int groups = 64 / R;
+  return Hkv % groups == 0 && 8 * tiles * (Hkv / groups) >= decode_grid() ? groups : 1;
+}
 
-template <typename T, int HD, int WM>
+template <typename T, int HD, int WM, bool HEADS>
 static cudaError_t run(const AttnParams &P, int *status, cudaStream_t s) {
   typedef DecCfg<T, HD, WM> C;
   static PerDeviceOnce attr;
   cudaError_t e = attr.run([](int) {
-    return cudaFuncSetAttribute(paged_decode_kernel<T, HD, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(paged_decode_kernel<T, HD, WM, HEADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 C::kSmem);
   });
   if (e != cudaSuccess) return e;
   const int grid = decode_grid();               // 32 bytes of weights for each: within the default limit
-  e = launch_pdl(paged_decode_kernel<T, HD, WM>, dim3(grid), dim3(kDecThreads), C::kSmem, s, P, status);
+  e = launch_pdl(paged_decode_kernel<T, HD, WM, HEADS>, dim3(grid), dim3(kDecThreads), C::kSmem, s, P, status);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(decode_merge_kernel<T, HD>, dim3(grid, 16 * WM / kJoinRows), dim3(kJoinThreads),
+  e = launch_pdl(decode_merge_kernel<T, HD>, dim3(grid, 16 * WM * P.hc / kJoinRows), dim3(kJoinThreads),
                  grid * kJoinRows * sizeof(float2), s, P, 16 * WM);
   return e == cudaSuccess ? launched(2) : e;
 }
 
-template <typename T>
-static cudaError_t run_type(const AttnParams &P, int R, int hd, int *status, cudaStream_t s) {
-  if (hd == 128)
-    return R == 16   ? run<T, 128, 1>(P, status, s)
-           : R == 32 ? run<T, 128, 2>(P, status, s)
-                     : run<T, 128, 4>(P, status, s);
-  return R == 16 ? run<T, 64, 1>(P, status, s) : R == 32 ? run<T, 64, 2>(P, status, s) : run<T, 64, 4>(P, status, s);
+template <typename T, int HD>
+static cudaError_t run_rows(const AttnParams &P, int R, int *status, cudaStream_t s) {
+  if (R == 64) return run<T, HD, 4, false>(P, status, s);
+  if (R == 32) return P.hc > 1 ? run<T, HD, 2, true>(P, status, s) : run<T, HD, 2, false>(P, status, s);
+  return P.hc > 1 ? run<T, HD, 1, true>(P, status, s) : run<T, HD, 1, false>(P, status, s);
 }
 
 cudaError_t launch_decode(const AttnParams &P, int R, int hd, cb_dtype dt, int *status, cudaStream_t s) {
-  return dt == CB_BF16 ? run_type<bf16>(P, R, hd, status, s) : run_type<float>(P, R, hd, status, s);
+  if (dt == CB_BF16) return hd == 128 ? run_rows<bf16, 128>(P, R, status, s) : run_rows<bf16, 64>(P, R, status, s);
+  return hd == 128 ? run_rows<float, 128>(P, R, status, s) : run_rows<float, 64>(P, R, status, s);
 }
 
 }  // namespace paged

@@ -193,13 +193,14 @@ def test_oracle_sampling_by_hand():
 
 
 # ----------------------------------------------------- the line of units --
-def _line(units, blocks, grid):
+def _line(units, blocks, grid, per):
     """The decode kernel's partition, restated: (part, item, first block, end
     block, slot or None) of every piece, and (item, slots) of every join.
-    units: items per sequence; blocks: units per item (0: nothing)."""
+    units: items per sequence; blocks: units per item (0: nothing); per: units
+    a part has at least (4 where the block's groups share a head, else 1)."""
     begin = np.concatenate([[0], np.cumsum([u * b for u, b in zip(units, blocks)])])
     total = int(begin[-1])
-    parts = min((total + 3) // 4, grid)
+    parts = min((total + per - 1) // per, grid)
     pb = lambda c: total * c // parts
     seq = lambda u: max(s for s in range(len(units)) if begin[s] <= u)
     pieces, joins = [], []
@@ -233,7 +234,7 @@ def test_every_unit_once_and_every_split_item_joined_once(seed):
     blocks = [int(rng.integers(1, [3, 30, 300][seed % 3])) if u else 0 for u in units]
     if not any(units):
         units[0], blocks[0] = 2, 5
-    pieces, joins = _line(units, blocks, int(rng.integers(1, 40)))
+    pieces, joins = _line(units, blocks, int(rng.integers(1, 40)), [1, 4][seed % 2])
     seen = {}
     for c, item, jb, je, slot in pieces:
         assert jb < je
