@@ -9,11 +9,10 @@
 // rounded once to the cache's type; values are copied.
 //
 // A pure stream: every byte of K, V (and Q) is read once and written once.
-// A block owns a few rows of one layer.  Its threads first issue their data
-// loads -- these need no metadata -- and meanwhile the rows' sequences are
-// found in shared memory from one coalesced read of the offsets and lengths,
-// so a row waits for two dependent loads (offsets, then the page entry and
-// the table row), not for a search in global memory.
+// A block owns a few rows of one layer.  It reads all offsets and lengths in
+// one coalesced round, finds its rows' sequences in shared memory, reads their
+// page entries, and then streams the rows: three dependent rounds of loads in
+// a call of any size, not a search in global memory per row.
 #include "cb_common.cuh"
 #include "cb_internal.h"
 #include "cb_paged.cuh"

@@ -128,16 +128,25 @@ template <int WM> __device__ __forceinline__ void group_sync(int wk) {
 struct Line {
   int64_t begin[CB_MAX_SEQS];     // first unit of each sequence
   int blocks[CB_MAX_SEQS];        // units per item; 0: nothing to do
-  int64_t total;
-  int parts;                      // blocks of the grid that take part
+  int64_t total, each;            // units; units per part (the first `extra` parts: one more)
+  int parts, extra;               // blocks of the grid that take part
 };
 
-__device__ __forceinline__ int64_t part_begin(const Line &L, int c) { return L.total * c / L.parts; }
+__device__ __forceinline__ int64_t part_begin(const Line &L, int c) { return L.each * c + min(c, L.extra); }
 __device__ __forceinline__ int part_of(const Line &L, int64_t u) {
-  int c = (int)(u * L.parts / L.total);
-  while (c + 1 < L.parts && part_begin(L, c + 1) <= u) ++c;
-  while (c > 0 && part_begin(L, c) > u) --c;
-  return c;
+  const int64_t long_parts = (L.each + 1) * L.extra;
+  return (int)(u < long_parts ? u / (L.each + 1) : L.extra + (u - long_parts) / L.each);
+}
+// a / b and a % b, in 32 bits where a fits (64-bit division is several times
+// slower and on every piece's path).
+__device__ __forceinline__ void divide(int64_t a, int b, int &quot, int &rem) {
+  if (a >> 32 == 0) {
+    quot = (int)((uint32_t)a / (uint32_t)b);
+    rem = (int)((uint32_t)a % (uint32_t)b);
+  } else {
+    quot = (int)(a / b);
+    rem = (int)(a % b);
+  }
 }
 
 // Every thread of the block calls it; one round of loads, one block scan.
@@ -184,6 +193,14 @@ __device__ __forceinline__ void make_line(const AttnParams &P, int R, int BN, in
     // a part has at least one unit, or one for each group that shares its head
     const int64_t most = P.hc > 1 ? first : (first + 3) / 4;
     L.parts = (int)(most < grid ? most : grid);
+    if (L.parts > 0) {
+      if (first >> 32 == 0) {
+        L.each = (uint32_t)first / (uint32_t)L.parts;
+      } else {
+        L.each = first / L.parts;
+      }
+      L.extra = (int)(first - L.each * L.parts);
+    }
   }
   __syncthreads();
 }
@@ -240,7 +257,8 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
     // this piece: item `item` of sequence s, its blocks [jb, je)
     while (line.blocks[s] == 0 || (s + 1 < P.kv.n_seq && line.begin[s + 1] <= u)) ++s;
     const int nbs = line.blocks[s];
-    const int item = (int)((u - line.begin[s]) / nbs), jb = (int)((u - line.begin[s]) % nbs);
+    int item, jb;
+    divide(u - line.begin[s], nbs, item, jb);
     const int take = (int)min((int64_t)(nbs - jb), u1 - u);
     const bool whole = jb == 0 && take == nbs, first = u == u0;
     const int64_t item_end = u - jb + nbs;
@@ -530,7 +548,7 @@ decode_merge_kernel(const __grid_constant__ AttnParams P, int R) {
   for (int k = 0; k < kJoinRows; ++k)
 #pragma unroll
     for (int e = 0; e < PER; ++e) o[k][e] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
   for (int c = warp; c < count; c += NW) {
     const float *src = P.part_o + (slot(c) + r0) * HD + lane * PER;
 #pragma unroll

@@ -201,7 +201,10 @@ def _line(units, blocks, grid, per):
     begin = np.concatenate([[0], np.cumsum([u * b for u, b in zip(units, blocks)])])
     total = int(begin[-1])
     parts = min((total + per - 1) // per, grid)
-    pb = lambda c: total * c // parts
+    each, extra = divmod(total, parts)
+    pb = lambda c: each * c + min(c, extra)
+    long_parts = (each + 1) * extra
+    part_of = lambda u: u // (each + 1) if u < long_parts else extra + (u - long_parts) // each
     seq = lambda u: max(s for s in range(len(units)) if begin[s] <= u)
     pieces, joins = [], []
     for c in range(parts):
@@ -221,7 +224,8 @@ def _line(units, blocks, grid, per):
         a = int(begin[s]) + item * blocks[s]
         if pb(c) == a or pb(c - 1) > a:
             continue
-        last = max(x for x in range(parts) if pb(x) <= a + blocks[s] - 1)
+        last = part_of(a + blocks[s] - 1)
+        assert pb(last) <= a + blocks[s] - 1 < pb(last + 1)
         joins.append(((s, item), [2 * x + (x == c - 1 and pb(x) != a) for x in range(c - 1, last + 1)]))
     return pieces, joins
 
