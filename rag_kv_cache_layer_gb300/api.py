@@ -290,7 +290,9 @@ def cb_paged_attention(q, row_offsets, kv_lens, block_table, k_pages, v_pages, n
     if max_kv_len is None:
         max_kv_len = min(block_table.shape[1] * shape[1], 2 ** 31 - 1)
     if ws is None:
-        ws = cb_paged_attention_workspace(q, kv_lens.shape[0], max_kv_len, n_q_heads, n_kv_heads, head_dim)
+        # belongs to the stream that uses it: it may be handed out again there only
+        with torch.cuda.stream(stream):
+            ws = cb_paged_attention_workspace(q, kv_lens.shape[0], max_kv_len, n_q_heads, n_kv_heads, head_dim)
     query = _pack_query(q.data_ptr(), out.data_ptr(), _ld("q", q, dt, n_rows, cols), _ld("out", out, dt, n_rows, cols),
                         ws.data_ptr(), ws.nbytes, n_rows, max_kv_len, n_q_heads, n_kv_heads, head_dim,
                         1.0 / math.sqrt(head_dim) if scale is None else scale)

@@ -445,6 +445,36 @@ def test_repeatable_streams_and_graphs(dt, n):
     assert R.device_status() == 0
 
 
+def test_own_workspace_belongs_to_the_calls_stream(monkeypatch):
+    """The scratch a call allocates itself is not handed to the current
+    stream's tensors while the call runs on another stream."""
+    from rag_kv_cache_layer_gb300 import api
+    plain, where = api.cb_paged_attention_workspace, []
+
+    def noted(*args):
+        w = plain(*args)
+        where.append(w.data_ptr())
+        return w
+    monkeypatch.setattr(api, "cb_paged_attention_workspace", noted)
+    rng = np.random.default_rng(12)
+    heads, dt = (8, 2, 128), torch.bfloat16
+    hq, hkv, hd = heads
+    b = Batch(rng, [(1, 2000), (1, 700)], 16, dt, hkv, hd)
+    k, v, dk, dv = b.pools(rng)
+    q = vals(rng, (2, hq * hd), dt)
+    dq = torch.from_numpy(q).cuda().to(dt)
+    off, lens, table = b.dev()
+    out = torch.full_like(dq, 9.0)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    R.cb_paged_attention(dq, off, lens, table, dk, dv, hq, hkv, hd, out, max_kv_len=2000, stream=s)
+    need = plain(dq, 2, 2000, hq, hkv, hd).numel()
+    others = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert all(o.data_ptr() != where[0] for o in others)
+    torch.cuda.synchronize()
+    check_attention(out, q, k, v, b, heads, hd ** -0.5, dt)
+
+
 def test_wrappers_refuse_shapes_and_types():
     dt = torch.bfloat16
     kp = torch.zeros(4, 16, 128, dtype=dt, device="cuda")
