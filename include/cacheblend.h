@@ -739,6 +739,8 @@ cb_status cb_blend_layer(cb_model *m, int layer, float *h, int n_rows,
 
 /* Largest number of sequences one paged call accepts. */
 #define CB_MAX_SEQS 1024
+/* Largest max_kv_len of a paged attention call. */
+#define CB_MAX_KV_LEN (1 << 30)
 /* Largest vocabulary cb_sample_tokens accepts. */
 #define CB_MAX_SAMPLE_VOCAB 262144
 
@@ -779,7 +781,8 @@ typedef struct {
  * Rows without a position keep their q_out.  Sequences of one call must not
  * share a page that the call writes.  k and v must not overlap the pools.
  * Errors: CB_ERR_INVALID_ARG (NULL or misaligned pointers, strides below a
- * row, head_dim not a multiple of 16), CB_ERR_UNSUPPORTED (page_size).  On
+ * row, head_dim not a multiple of 16, several layers with a cache_layer_stride
+ * of 0), CB_ERR_UNSUPPORTED (page_size).  On
  * the device, offsets that do not ascend inside [0, n_rows], a page outside
  * the pool or the table, and a rotation at or past max_positions record
  * CB_ERR_DEVICE_INDEX; those rows are skipped. */
@@ -811,8 +814,9 @@ cb_status cb_paged_append(const cb_paged_kv *kv, const cb_paged_rows *rows,
  * on one stream.
  * Errors: CB_ERR_INVALID_ARG (NULL or misaligned pointers, strides, head
  * counts not dividing or more than 128 q heads per kv head, head_dim not 64
- * or 128, a negative or infinite scale), CB_ERR_UNSUPPORTED (page_size, or a row count whose tiles exceed a
- * launch), CB_ERR_WORKSPACE.  On the device, offsets that do not ascend
+ * or 128, a scale outside [0, 2^127)), CB_ERR_UNSUPPORTED (page_size,
+ * max_kv_len > CB_MAX_KV_LEN, or a row count whose tiles exceed a launch),
+ * CB_ERR_WORKSPACE.  On the device, offsets that do not ascend
  * inside [0, n_rows], a length outside [0, max_kv_len] or past the table, and
  * a page outside the pool record CB_ERR_DEVICE_INDEX; with a bad offset or
  * length the sequence's rows are left unwritten, with a bad page they are

@@ -33,6 +33,7 @@ CB_PROBE_MLP = 10
 CB_MAX_BATCH = 64
 CB_MAX_SPANS = 1024
 CB_MAX_SEQS = 1024
+CB_MAX_KV_LEN = 1 << 30
 CB_MAX_SAMPLE_VOCAB = 262144
 
 

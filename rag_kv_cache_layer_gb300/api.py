@@ -288,7 +288,7 @@ def cb_paged_attention(q, row_offsets, kv_lens, block_table, k_pages, v_pages, n
         raise ValueError("the pools must be one layer's [n_pages, page_size, n_kv_heads * head_dim]")
     n_rows = q.shape[0]
     if max_kv_len is None:
-        max_kv_len = min(block_table.shape[1] * shape[1], 2 ** 31 - 1)
+        max_kv_len = min(block_table.shape[1] * shape[1], L.CB_MAX_KV_LEN)
     if ws is None:
         # belongs to the stream that uses it: it may be handed out again there only
         with torch.cuda.stream(stream):

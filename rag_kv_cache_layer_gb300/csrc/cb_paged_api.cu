@@ -64,6 +64,7 @@ extern "C" cb_status cb_paged_append(const cb_paged_kv *kv, const cb_paged_rows 
   const size_t eb = bytes_of(dtype);
   if (!rows_ok(r.k, r.ld_k, cols, eb) || !rows_ok(r.v, r.ld_v, cols, eb))
     return bad("k / v: NULL, misaligned, or a leading dimension below a row");
+  if (r.n_layers > 1 && r.cache_layer_stride == 0) return bad("layers need a cache of their own each");
   if (r.n_layers > 1 && (r.k_layer_stride * (int64_t)eb % 16 || r.v_layer_stride * (int64_t)eb % 16 ||
                          r.cache_layer_stride * (int64_t)eb % 16))
     return bad("layer strides must be multiples of 16 bytes");
@@ -103,7 +104,9 @@ extern "C" cb_status cb_paged_attention(const cb_paged_kv *kv, const cb_paged_qu
     return bad("n_q_heads must be 1 to 128 times n_kv_heads, head_dim 64 or 128");
   if (const cb_status s = check_paged(kv, (int64_t)a.n_kv_heads * a.head_dim, dtype)) return s;
   if (a.n_rows < 0 || a.max_kv_len < 0) return bad("n_rows < 0 or max_kv_len < 0");
-  if (!(a.scale >= 0.f) || isinf(a.scale)) return bad("scale must be finite and >= 0");
+  if (a.max_kv_len > CB_MAX_KV_LEN) return record_error(CB_ERR_UNSUPPORTED, "max_kv_len > CB_MAX_KV_LEN");
+  // (the kernels work with scale * log2(e))
+  if (!(a.scale >= 0.f) || isinf(2.f * a.scale)) return bad("scale must be >= 0 and below 2^127");
   if (a.n_rows == 0 || kv->n_seq == 0) return CB_OK;
   const size_t eb = bytes_of(dtype);
   const int64_t cols = (int64_t)a.n_q_heads * a.head_dim;

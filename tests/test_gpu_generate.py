@@ -4,6 +4,10 @@ layers with cb_paged_append and cb_paged_attention, and cb_sample_tokens draws
 from the tied output projection's logits.  The reference is the library's own
 full prefill of the longer sequence, at the bounds its caches and hidden states
 are held to (max-abs 1e-4 in fp32, 2e-2 RMS-relative in bf16)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -218,3 +222,39 @@ def test_recorded_generation_step():
         assert torch.equal(o, outs[1]) and torch.equal(tok, outs[2])
         assert all(torch.equal(state[a], other[a]) for a in state)
         assert not o[3].any()                                                   # the idle slot attends to nothing
+
+
+FIRST_CALLS = """
+import torch, rag_kv_cache_layer_gb300 as R
+g = torch.Generator(device="cuda").manual_seed(3)
+ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+kn, vn, q = (torch.randn(70, w, device="cuda", generator=g).bfloat16() for w in (256, 256, 1024))
+kp, vp = torch.zeros(8, 16, 256, device="cuda").bfloat16(), torch.zeros(8, 16, 256, device="cuda").bfloat16()
+off, lens, table = ints([0, 1, 70]), ints([1, 69]), ints([[7, 0, 0, 0, 0], [3, 1, 4, 0, 6]])
+rope = R.cb_rope_table_init(128, 128, 10000.0)
+logits, u = torch.randn(2, 5000, device="cuda", generator=g), torch.rand(2, device="cuda", generator=g)
+outs = [(torch.zeros_like(q), torch.zeros_like(q), torch.zeros(2, dtype=torch.int32, device="cuda")) for _ in range(2)]
+ws = R.cb_paged_attention_workspace(q, 2, 80, 8, 2, 128)
+top_p = torch.full((2,), 0.9, device="cuda")
+def step(qr, out, tokens):
+    R.cb_paged_append(kn, vn, off, lens, table, kp, vp, 128, rope_table=rope, q=q, q_out=qr)
+    R.cb_paged_attention(qr, off, lens, table, kp, vp, 8, 2, 128, out, max_kv_len=80, ws=ws)
+    R.cb_sample_tokens(logits, u, tokens, top_p=top_p)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step(*outs[0])
+graph.replay()
+step(*outs[1])
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(*outs)) and R.device_status() == 0
+assert float(outs[0][1].float().abs().sum()) > 0
+print("recorded first")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_recorded():
+    """Nothing is set up at a first call that a recording would refuse."""
+    run = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=300,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert run.returncode == 0 and "recorded first" in run.stdout, run.stderr[-2000:]

@@ -310,6 +310,26 @@ def test_attention_many_sequences(dt):
 
 
 @pytest.mark.parametrize("dt", list(HALF))
+def test_full_batch_of_padded_slots(dt):
+    """The most sequences of a call, two thirds of them idle or without rows."""
+    rng = np.random.default_rng(5)
+    seqs = [[(1, int(rng.integers(1, 90))), (1, 0), (0, 0)][i % 3] for i in range(L.CB_MAX_SEQS)]
+    attention_case(rng, dt, (4, 2, 64), 16, seqs, tail=3)
+
+
+@pytest.mark.parametrize("dt", list(HALF))
+@pytest.mark.parametrize("n", [1, 20, 200])
+def test_table_without_pages(dt, n):
+    """A batch of idle slots may come with a table of no columns: zeros."""
+    kp = torch.full((1, 16, 128), float("nan"), dtype=dt, device="cuda")
+    q = torch.randn(2 * n, 256, device="cuda").to(dt)
+    out = torch.full_like(q, 9.0)
+    table = torch.zeros(2, 0, dtype=torch.int32, device="cuda")
+    R.cb_paged_attention(q, ints([0, n, 2 * n]), ints([0, 0]), table, kp, kp, 4, 2, 64, out)
+    assert torch.all(out == 0) and R.device_status() == 0
+
+
+@pytest.mark.parametrize("dt", list(HALF))
 @pytest.mark.parametrize("n", [1, 6, 70])
 def test_attention_steep_scores(dt, n):
     """Scores far apart: the running maximum moves, most weights vanish."""

@@ -123,6 +123,16 @@ def test_attention_refusals(kw):
     assert _attn(**kw) == L.CB_ERR_INVALID_ARG
 
 
+def test_limits_of_lengths_scales_and_layers():
+    """Key indices stay below 2^31 with a block's reach to spare, the scale in
+    the log2 domain is finite, and no two layers append to one place."""
+    assert _attn(max_kv_len=L.CB_MAX_KV_LEN + 1) == L.CB_ERR_UNSUPPORTED
+    assert _attn(max_kv_len=2 ** 31 - 1) == L.CB_ERR_UNSUPPORTED
+    assert _attn(scale=3e38) == L.CB_ERR_INVALID_ARG
+    assert _append(n_layers=2, cache_layer_stride=0) == L.CB_ERR_INVALID_ARG
+    assert L.CB_MAX_KV_LEN == 1 << 30
+
+
 def test_attention_workspace():
     size = L.lib.cb_paged_attention_workspace_size
     need = size(1, 1, 100000, 32, 8, 128, L.CB_BF16)
