@@ -175,35 +175,33 @@ _CODES = {_BF16: L.CB_BF16, _F32: L.CB_F32}
 _pack_kv, _pack_rows, _pack_query = L.packer(L.PagedKV), L.packer(L.PagedRows), L.packer(L.PagedQuery)
 
 
-def _on_device(*tensors):
-    """Kernels run on the current device: every tensor must live there.
-    Returns that device's index."""
-    dev = _cur_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
-    return dev
+def _device_error(dev, *tensors):
+    """Kernels run on the current device: every tensor must live there."""
+    t = next(t for t in tensors if t is not None and t.get_device() != dev)
+    raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
 
 
 def _ld(name, t, dtype, rows, cols):
     """Leading dimension of a matrix t [rows, cols] of `dtype`."""
     ld, one = t.stride()
-    if t.dtype != dtype or t.shape != (rows, cols) or (one != 1 and cols > 1):
+    if t.dtype is not dtype or t.shape != (rows, cols) or (one != 1 and cols > 1):
         raise ValueError(f"{name} must be {dtype} of shape ({rows}, {cols}) with contiguous rows")
     return ld if rows > 1 else cols
 
 
-def _paged_kv(k_pages, v_pages, row_offsets, kv_lens, block_table):
-    n_seq, = kv_lens.shape
-    seqs, width = block_table.shape
+def _paged_kv(dev, k_pages, v_pages, row_offsets, kv_lens, block_table):
+    if not k_pages.get_device() == v_pages.get_device() == row_offsets.get_device() == \
+            kv_lens.get_device() == block_table.get_device() == dev:
+        _device_error(dev, k_pages, v_pages, row_offsets, kv_lens, block_table)
+    n_seq, width = block_table.shape
     ld_table, one = block_table.stride()
-    if not kv_lens.dtype == row_offsets.dtype == block_table.dtype == _I32 or seqs != n_seq or \
-            row_offsets.shape != (n_seq + 1,) or (one != 1 and width > 1) or \
+    if not kv_lens.dtype is row_offsets.dtype is block_table.dtype is _I32 or (one != 1 and width > 1) or \
+            kv_lens.shape != (n_seq,) or row_offsets.shape != (n_seq + 1,) or \
             not (kv_lens.is_contiguous() and row_offsets.is_contiguous()):
         raise ValueError("row_offsets [n_seq + 1], kv_lens [n_seq] and block_table [n_seq, max_pages] "
                          "must be int32 with contiguous rows")
     shape, strides = k_pages.shape, k_pages.stride()
-    if v_pages.shape != shape or v_pages.dtype != k_pages.dtype or v_pages.stride() != strides or \
+    if v_pages.stride() != strides or v_pages.shape != shape or v_pages.dtype is not k_pages.dtype or \
             strides[-1] != 1:
         raise ValueError("k_pages and v_pages must have one shape, type and strides, with contiguous slots")
     n_pages, page, cols = shape[-3:]
@@ -223,8 +221,10 @@ def cb_paged_append(k_new, v_new, row_offsets, kv_lens, block_table, k_pages, v_
     block_table [n_seq, max_pages]: device int32.  rope_table: from
     cb_rope_table_init; None copies the keys as they are.  q: [rows,
     n_q_heads * head_dim], rotated into q_out (None: in place)."""
-    dev = _on_device(k_new, v_new, row_offsets, kv_lens, block_table, k_pages, v_pages, rope_table, q, q_out)
-    kv, shape = _paged_kv(k_pages, v_pages, row_offsets, kv_lens, block_table)
+    dev = _cur_device()
+    kv, shape = _paged_kv(dev, k_pages, v_pages, row_offsets, kv_lens, block_table)
+    if not k_new.get_device() == v_new.get_device() == dev:
+        _device_error(dev, k_new, v_new)
     dt = k_pages.dtype
     cols, layers, sk, sv, sc = shape[-1], 1, 0, 0, 0
     k1, v1 = k_new, v_new
@@ -243,11 +243,16 @@ def cb_paged_append(k_new, v_new, row_offsets, kv_lens, block_table, k_pages, v_
     n_rows = k1.shape[0]
     rope = max_pos = 0
     if rope_table is not None:
-        if rope_table.dtype != _F32 or not rope_table.is_contiguous():
+        if rope_table.get_device() != dev:
+            _device_error(dev, rope_table)
+        if rope_table.dtype is not _F32 or not rope_table.is_contiguous():
             raise ValueError("rope_table must be contiguous float32")
         rope, max_pos = rope_table.data_ptr(), rope_table.numel() // head_dim
     qp = qop = ld_q = ld_qo = n_q = 0
     if q is not None:
+        q_to = q if q_out is None else q_out
+        if not q.get_device() == q_to.get_device() == dev:
+            _device_error(dev, q, q_to)
         q_cols = q.shape[1]
         n_q = q_cols // head_dim
         if q_cols % head_dim:
@@ -281,8 +286,10 @@ def cb_paged_attention(q, row_offsets, kv_lens, block_table, k_pages, v_pages, n
     the rows, whose keys are already in the cache).  max_kv_len: an upper
     bound of kv_lens (default: what the table can hold).  ws: from
     cb_paged_attention_workspace (None: allocated here)."""
-    dev = _on_device(q, row_offsets, kv_lens, block_table, k_pages, v_pages, out, ws)
-    kv, shape = _paged_kv(k_pages, v_pages, row_offsets, kv_lens, block_table)
+    dev = _cur_device()
+    kv, shape = _paged_kv(dev, k_pages, v_pages, row_offsets, kv_lens, block_table)
+    if not q.get_device() == out.get_device() == dev or (ws is not None and ws.get_device() != dev):
+        _device_error(dev, q, out, ws)
     dt, cols = k_pages.dtype, n_q_heads * head_dim
     if len(shape) != 3 or shape[2] != n_kv_heads * head_dim:
         raise ValueError("the pools must be one layer's [n_pages, page_size, n_kv_heads * head_dim]")
@@ -307,16 +314,20 @@ def cb_sample_tokens(logits, u, tokens, temperature=None, top_k=None, top_p=None
     """Samples a token per row of logits [rows, vocab] into tokens (device
     int32 [rows]) from the uniform numbers u (float32 [rows]); temperature,
     top_p, min_p: float32 [rows] or None, top_k: int32 [rows] or None."""
-    dev = _on_device(logits, u, tokens, temperature, top_k, top_p, min_p)
+    dev = _cur_device()
     n, vocab = logits.shape
     dt = logits.dtype
     if dt not in _CODES:
         raise ValueError(f"unsupported dtype {dt}")
+    if logits.get_device() != dev:
+        _device_error(dev, logits)
 
     def per_row(name, t, dtype):
         if t is None:
             return 0
-        if t.dtype != dtype or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        if t.get_device() != dev:
+            _device_error(dev, t)
+        if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous {dtype} of shape ({n},)")
         return t.data_ptr()
     status = lib.cb_sample_tokens(
