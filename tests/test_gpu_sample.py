@@ -115,6 +115,40 @@ def test_ties_at_the_cut():
                 assert sample(x, u, dt, **kw) == reference(x, u, **kw)
 
 
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("v", [3000, 60000])
+@pytest.mark.parametrize("levels", [3, 40, 5000])
+def test_lists_of_any_length_and_crowding(dt, v, levels):
+    """Border lists from a few tokens to more than the first block takes, with
+    few equal logits and with hundreds of them."""
+    rng = np.random.default_rng(v + levels)
+    k = np.array([2, 31, 63, 64, 65, 127, 200, 511, 512, 513, 700, 1000, 1023, 1500, 2047, 2048, 2049, 2600])
+    x = rng.standard_normal((len(k), v)).astype(np.float32)
+    x = (np.round(x * levels / 8) * (8 / levels)).astype(np.float32)
+    x = bf16_values(x) if dt == torch.bfloat16 else x
+    u, t = rng.random(len(k)).astype(np.float32), rng.uniform(0.5, 2, len(k)).astype(np.float32)
+    for kw in (dict(), dict(top_p=0.5), dict(top_p=0.95, min_p=0.1)):
+        assert sample(x, u, dt, temperature=t, top_k=k, **kw) == reference(x, u, t, k, **kw), kw
+    p = np.linspace(0.01, 0.999, len(k)).astype(np.float32)
+    assert sample(x, u, dt, temperature=t, top_p=p) == reference(x, u, t, top_p=p)
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("temperature", [0.02, 1.0])
+def test_top_k_past_the_tokens_that_weigh(dt, temperature):
+    """More asked for than lie within the weights' range (all others are at
+    -inf, or so far below that they weigh nothing): top_k keeps them all, and
+    top_p is of their whole weight."""
+    rng = np.random.default_rng(9)
+    x = np.full((6, 20000), -np.inf, np.float32)
+    for r in x:
+        r[rng.permutation(20000)[:800]] = bf16_values(rng.standard_normal(800).astype(np.float32) * 2)
+    u = rng.random(6).astype(np.float32)
+    for kw in (dict(top_k=5000), dict(top_k=5000, top_p=0.9), dict(top_k=801, top_p=0.5), dict(top_k=800, top_p=0.5),
+               dict(top_k=19999, top_p=0.99, min_p=0.01)):
+        assert sample(x, u, dt, temperature=temperature, **kw) == reference(x, u, np.float32(temperature), **kw), kw
+
+
 def test_greedy_and_degenerate_settings():
     x = np.array([[1.0, 5.0, 5.0, -2.0], [-0.0, 0.0, -1.0, 0.0], [3.0, np.nan, 2.0, np.inf]], np.float32)
     top = [1, 0, 3]
