@@ -14,6 +14,20 @@ struct Join {
   int row0, l0, rows, g, last, second;
 };
 
+// x / d for 0 <= x < 2^31 by one product: m = ceil(2^s / d) with s = 31 +
+// ceil(log2 d) is off by less than 2^(s - 31) / d.  The kernels' index
+// arithmetic lies on every piece's path, where a division costs 20 dependent
+// instructions.
+struct Divisor {
+  uint32_t d, m;
+  int s;
+  explicit Divisor(int by = 1) : d(by), s(31) {
+    while ((1u << (s - 31)) < d) ++s;
+    m = (uint32_t)(((1ull << s) + d - 1) / d);
+  }
+  __device__ __forceinline__ int div(int x) const { return (int)(((uint64_t)(uint32_t)x * m) >> s); }
+};
+
 struct AttnParams {
   PagedKV kv;
   const void *q;
@@ -25,6 +39,7 @@ struct AttnParams {
   // few_hi, the chunk kernel those above rows_lo.
   int few_hi, rows_lo;
   int hc;                                 // kv heads per item of the few-rows kernel
+  Divisor by_G, by_quads;                 // G; Hkv / hc
   float scale_log2;                       // softmax scale times log2(e)
   float *part_o;                          // unnormalised partial rows, HD floats each
   float2 *part_ml;                        // (m, l) of each partial row

@@ -132,6 +132,8 @@ cudaError_t launch_paged_attention(const PagedKV &kv, const cb_paged_query &a, c
   P.few_hi = p.few_hi;
   P.rows_lo = p.rows_lo;
   P.hc = p.hc;
+  P.by_G = Divisor(G);
+  P.by_quads = Divisor(a.n_kv_heads / p.hc);
   P.scale_log2 = a.scale * 1.4426950408889634f;
   return run_plan(P, p, a.head_dim, dt, a.ws, status, s);
 }

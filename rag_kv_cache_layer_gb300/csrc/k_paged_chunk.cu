@@ -141,7 +141,7 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
   const int l0 = tl.t * C::kRows, rows = min(C::kRows, tl.n * P.G - l0);
   const int active = NT == 1 || rows <= 128 ? 1 : 2;           // tiles with rows
   const int base = tl.kv - tl.n;
-  const int last = base + (l0 + rows - 1) / P.G;
+  const int last = base + P.by_G.div(l0 + rows - 1);
   const int nb_tile = last < 0 ? 0 : last / kChBN + 1;
   const int jb = (int)((int64_t)nb_tile * split / P.n_split);
   const int nb = (int)((int64_t)nb_tile * (split + 1) / P.n_split) - jb;
@@ -152,10 +152,10 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
       if (P.n_split > 1) {
         P.part_ml[slot0 + threadIdx.x] = make_float2(-INFINITY, 0.f);
       } else {
-        const int l = l0 + threadIdx.x;
+        const int l = l0 + threadIdx.x, qi = P.by_G.div(l);
         uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<bf16 *>(P.out) +
-                                               (int64_t)(tl.row0 + l / P.G) * P.ld_out +
-                                               (int64_t)(g * P.G + l % P.G) * HD);
+                                               (int64_t)(tl.row0 + qi) * P.ld_out +
+                                               (int64_t)(g * P.G + l - qi * P.G) * HD);
         for (int c = 0; c < HD / 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
       }
     }
@@ -301,9 +301,9 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
     {
       // a thread loads its row: all its loads are in flight at once, and eight
       // neighbouring rows fall into different banks
-      const int r = threadIdx.x - 32 * C::kSoft, l = l0 + r;
-      const bf16 *q = reinterpret_cast<const bf16 *>(P.q) + (int64_t)(tl.row0 + l / P.G) * P.ld_q +
-                      (int64_t)(g * P.G + l % P.G) * HD;
+      const int r = threadIdx.x - 32 * C::kSoft, l = l0 + r, qi = P.by_G.div(l);
+      const bf16 *q = reinterpret_cast<const bf16 *>(P.q) + (int64_t)(tl.row0 + qi) * P.ld_q +
+                      (int64_t)(g * P.G + l - qi * P.G) * HD;
       uint4 v[HD / 8];
 #pragma unroll
       for (int c = 0; c < HD / 8; ++c)
@@ -318,7 +318,7 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
     const int quad = warp & 3;
     const int row = t * 128 + quad * 32 + lane;  // row of the unit
     const bool valid = row < rows;
-    const int p = valid ? base + (l0 + row) / P.G : -1;
+    const int p = valid ? base + P.by_G.div(l0 + row) : -1;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const uint32_t tm = tmem + t * kChTmem + lane_off, obase = tm + kChO;
     float m = -INFINITY, l = 0.f;                // reference max (log2 domain), sum
@@ -420,10 +420,10 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
     if (failed) *fail = 1;
     const bool ok = !failed && !*fail;
     if (__any_sync(0xffffffffu, ok)) {
-      const int lr = l0 + row;
+      const int lr = l0 + row, qi = P.by_G.div(lr);
       const float inv = l == 0.f ? 0.f : 1.f / l;    // no visible key: zeros
-      bf16 *out = reinterpret_cast<bf16 *>(P.out) + (int64_t)(tl.row0 + lr / P.G) * P.ld_out +
-                  (int64_t)(g * P.G + lr % P.G) * HD;
+      bf16 *out = reinterpret_cast<bf16 *>(P.out) + (int64_t)(tl.row0 + qi) * P.ld_out +
+                  (int64_t)(g * P.G + lr - qi * P.G) * HD;
       // partials lie four columns of all the unit's rows together, which a warp with
       // a row per lane writes (and the merge reads) in whole lines
       float4 *part = reinterpret_cast<float4 *>(P.part_o + slot0 * HD) + row;
@@ -510,9 +510,9 @@ chunk_merge_kernel(const __grid_constant__ AttnParams P) {
   // 64 bytes of each row, four lanes a row
   const int r = threadIdx.x / 4, c8 = threadIdx.x % 4 * 8;
   if (r < rows) {
-    const int lr = l0 + r;
-    *reinterpret_cast<uint4 *>(reinterpret_cast<bf16 *>(P.out) + (int64_t)(tl.row0 + lr / P.G) * P.ld_out +
-                               (int64_t)(g * P.G + lr % P.G) * HD + cb * 32 + c8) =
+    const int lr = l0 + r, qi = P.by_G.div(lr);
+    *reinterpret_cast<uint4 *>(reinterpret_cast<bf16 *>(P.out) + (int64_t)(tl.row0 + qi) * P.ld_out +
+                               (int64_t)(g * P.G + lr - qi * P.G) * HD + cb * 32 + c8) =
         *reinterpret_cast<const uint4 *>(&s_out[r][c8]);
   }
 }

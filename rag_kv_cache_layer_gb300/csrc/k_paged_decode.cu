@@ -128,14 +128,20 @@ template <int WM> __device__ __forceinline__ void group_sync(int wk) {
 struct Line {
   int64_t begin[CB_MAX_SEQS];     // first unit of each sequence
   int blocks[CB_MAX_SEQS];        // units per item; 0: nothing to do
-  int64_t total, each;            // units; units per part (the first `extra` parts: one more)
-  int parts, extra;               // blocks of the grid that take part
+  int64_t total;                  // units
+  int parts;                      // blocks of the grid that take part
 };
 
-__device__ __forceinline__ int64_t part_begin(const Line &L, int c) { return L.each * c + min(c, L.extra); }
+// Part c is [c total / parts, (c + 1) total / parts), each rounded down.  The
+// products fit 32 bits in all but the longest calls, and 64-bit division is
+// several times slower.
+__device__ __forceinline__ int64_t part_begin(const Line &L, int c) {
+  const int64_t x = L.total * c;
+  return x >> 32 == 0 ? (uint32_t)x / (uint32_t)L.parts : x / L.parts;
+}
 __device__ __forceinline__ int part_of(const Line &L, int64_t u) {
-  const int64_t long_parts = (L.each + 1) * L.extra;
-  return (int)(u < long_parts ? u / (L.each + 1) : L.extra + (u - long_parts) / L.each);
+  const int64_t x = (u + 1) * L.parts - 1;
+  return x >> 32 == 0 ? (int)((uint32_t)x / (uint32_t)L.total) : (int)(x / L.total);
 }
 // a / b and a % b, in 32 bits where a fits (64-bit division is several times
 // slower and on every piece's path).
@@ -152,25 +158,22 @@ __device__ __forceinline__ void divide(int64_t a, int b, int &quot, int &rem) {
 // Every thread of the block calls it; one round of loads, one block scan.
 __device__ __forceinline__ void make_line(const AttnParams &P, int R, int BN, int grid, Line &L, int64_t *warp_sums,
                                           int *status) {
-  constexpr int NT = kDecThreads, kPer = (CB_MAX_SEQS + NT - 1) / NT;
-  const int per = (P.kv.n_seq + NT - 1) / NT, i0 = threadIdx.x * per;
-  int64_t u[kPer], sum = 0;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    u[k] = 0;
-    if (k < per && i0 + k < P.kv.n_seq) {
-      const int n = paged_rows(P.kv, i0 + k, P.n_rows, status), len = __ldg(P.kv.kv_lens + i0 + k);
-      int nb = 0;
-      if (n > 0 && (int64_t)n * P.G <= P.few_hi) {
-        if (len < 0 || len > P.max_kv || len > (int64_t)P.kv.max_pages * P.kv.page_size)
-          report(status, CB_ERR_DEVICE_INDEX);
-        else
-          nb = len > 0 ? (len - 1) / BN + 1 : 1;        // an idle slot's rows get their zeros
-      }
-      L.blocks[i0 + k] = nb;
-      u[k] = nb ? ((int64_t)n * P.G + R - 1) / R * (P.Hkv / P.hc) * nb : 0;
+  constexpr int NT = kDecThreads;
+  const int per = (P.kv.n_seq + NT - 1) / NT, i0 = threadIdx.x * per, i1 = min(i0 + per, P.kv.n_seq);
+  int64_t sum = 0;
+#pragma unroll 1
+  for (int i = i0; i < i1; ++i) {
+    const int n = paged_rows(P.kv, i, P.n_rows, status), len = __ldg(P.kv.kv_lens + i);
+    int nb = 0;
+    if (n > 0 && (int64_t)n * P.G <= P.few_hi) {
+      if (len < 0 || len > P.max_kv || len > (int64_t)P.kv.max_pages * P.kv.page_size)
+        report(status, CB_ERR_DEVICE_INDEX);
+      else
+        nb = len > 0 ? (len - 1) / BN + 1 : 1;          // an idle slot's rows get their zeros
     }
-    sum += u[k];
+    L.blocks[i] = nb;
+    L.begin[i] = sum;
+    sum += ((int64_t)n * P.G + R - 1) / R * P.by_quads.d * nb;
   }
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int64_t incl = sum;
@@ -183,23 +186,21 @@ __device__ __forceinline__ void make_line(const AttnParams &P, int R, int BN, in
   __syncthreads();
   int64_t first = incl - sum;
   for (int x = 0; x < w; ++x) first += warp_sums[x];
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    if (k < per && i0 + k < P.kv.n_seq) L.begin[i0 + k] = first;
-    first += u[k];
-  }
+#pragma unroll 1
+  for (int i = i0; i < i1; ++i) L.begin[i] += first;
+  first += sum;
   if (threadIdx.x == NT - 1) {
     L.total = first;
     // a part has at least one unit, or one for each group that shares its head
     const int64_t most = P.hc > 1 ? first : (first + 3) / 4;
     L.parts = (int)(most < grid ? most : grid);
-    if (L.parts > 0) {
-      if (first >> 32 == 0) {
-        L.each = (uint32_t)first / (uint32_t)L.parts;
-      } else {
-        L.each = first / L.parts;
-      }
-      L.extra = (int)(first - L.each * L.parts);
+    // Items of one length that are fewer than the parts take the same number
+    // of parts each, so that no part has two pieces, which costs it a second
+    // prologue and join (one row over 3137 keys: 13.1 us, 11.8 so).
+    if (P.kv.n_seq == 1 && L.parts > 0) {
+      int items, none;
+      divide(first, L.blocks[0], items, none);
+      if (items < L.parts) L.parts -= L.parts % items;
     }
   }
   __syncthreads();
@@ -266,10 +267,11 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
     const int row0 = __ldg(P.kv.row_offsets + s), n = __ldg(P.kv.row_offsets + s + 1) - row0;
     // tiles from both ends in turn: early ones see fewer keys than the line
     // counts for them, so neighbours even out
-    const int quads = P.Hkv / hc, g0 = item % quads * hc, g = g0 + sub, k = item / quads, tiles = (int)(((int64_t)n * P.G + R - 1) / R);
+    const int k = P.by_quads.div(item), g0 = (item - k * (int)P.by_quads.d) * hc, g = g0 + sub;
+    const int tiles = (int)(((int64_t)n * P.G + R - 1) / R);
     const int l0 = ((k & 1) ? tiles - 1 - k / 2 : k / 2) * R;
     const int kv = __ldg(P.kv.kv_lens + s), base = kv - n, rows = min(R, n * P.G - l0);
-    const int seen = base + (l0 + rows - 1) / P.G + 1;        // keys the tile's last row sees
+    const int seen = base + P.by_G.div(l0 + rows - 1) + 1;        // keys the tile's last row sees
     const int je = min(jb + take, seen > 0 ? (seen - 1) / BN + 1 : 0);
     const int32_t *table = P.kv.block_table + (int64_t)s * P.kv.ld_table;
     if (threadIdx.x == 0 && u == u1)            // the last piece: the one that may go on in the next part
@@ -279,6 +281,7 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
       const int key = j * BN + lane;
       return j < je && lane < BN && key < kv ? __ldg(table + (key >> shift)) : -1;
     };
+    const int64_t lane_off = g * HD + ccol * kVec, down = (int64_t)(WM * kRows) * P.kv.ld;
     auto load = [&](int j, int st, int page) {
       const uint32_t dst = ring + st * C::kStage;
       if (page >= 0 && page >= P.kv.n_pages) {
@@ -287,31 +290,53 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
       } else if (page < 0 && j < je && lane < BN && j * BN + lane < kv) {
         report(status, CB_ERR_DEVICE_INDEX);
       }
+      // eight rows lie in one page (page_size >= 8): one lookup, then a stride
+      int pg = 0;
+      int64_t off = 0;
 #pragma unroll
       for (int i = 0; i < BN / kRows / WM; ++i) {
         const int r = (i * WM + wm) * kRows + crow;
-        const int pg = __shfl_sync(0xffffffffu, page, r);
-        const int slot = (j * BN + r) & (P.kv.page_size - 1);
-        const int64_t off = pg < 0 ? 0 : (int64_t)pg * P.kv.page_stride + (int64_t)slot * P.kv.ld + g * HD + ccol * kVec;
+        pg = __shfl_sync(0xffffffffu, page, r);
+        if (i * WM * kRows % 8 == 0) {
+          const int slot = (j * BN + r) & (P.kv.page_size - 1);
+          off = (int64_t)pg * P.kv.page_stride + (int64_t)slot * P.kv.ld + lane_off;
+        } else {
+          off += down;
+        }
+        const int64_t from = pg < 0 ? 0 : off;
         // 16-byte columns are swizzled so that the fragments' reads meet all
         // banks: by the row, or (V in fp32) by the pair of rows
         const uint32_t d = dst + r * C::kRow, x = F32 ? ((r >> 1) & 3) << 1 : r & 7;
-        copy16(d + ((ccol ^ (r & 7)) << 4), kp + off, pg >= 0);
-        copy16(d + C::kTile + ((ccol ^ x) << 4), vp + off, pg >= 0);
+        copy16(d + ((ccol ^ (r & 7)) << 4), kp + from, pg >= 0);
+        copy16(d + C::kTile + ((ccol ^ x) << 4), vp + from, pg >= 0);
       }
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
+    // the table is read kAhead blocks further ahead than the pages: the first
+    // stages' entries one after the other would cost a memory latency each
+    constexpr int kAhead = 3;
+    int ahead[kAhead], from = jb + first_block;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) ahead[i] = fetch(from + i * step);
+    auto next_page = [&]() -> int {
+      const int page = ahead[0];
+#pragma unroll
+      for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
+      ahead[kAhead - 1] = fetch(from + kAhead * step);
+      from += step;
+      return page;
+    };
     int pos[2];
     uint32_t qf[KS][4];                         // bf16 pairs, or fp32 values
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = wm * 16 + gid + 8 * h;
       const bool valid = r < rows;
-      const int qi = (l0 + r) / P.G;
+      const int qi = P.by_G.div(l0 + r);
       pos[h] = valid ? base + qi : -1;
       const T *src = reinterpret_cast<const T *>(P.q) + (int64_t)(row0 + qi) * P.ld_q +
-                     (int64_t)(g * P.G + (l0 + r) % P.G) * HD + (F32 ? q4 : q4 * 2);
+                     (int64_t)(g * P.G + l0 + r - qi * P.G) * HD + (F32 ? q4 : q4 * 2);
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -325,12 +350,10 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
 
-    // the table is read one block further ahead than the pages
-    int page = fetch(jb + first_block);
+#pragma unroll 1
     for (int i = 0; i < NS - 1; ++i) {
-      const int j = jb + first_block + i * step, next = fetch(j + step);
+      const int j = from, page = next_page();
       if (j < je) load(j, i, page);
-      page = next;
       commit();
     }
     int st = 0, fill = NS - 1;
@@ -338,9 +361,8 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
       asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
       group_sync<WM>(wk);                       // landed for every warp; the stage before is used up
       {
-        const int jn = j + (NS - 1) * step, next = fetch(jn + step);
+        const int jn = from, page = next_page();
         if (jn < je) load(jn, fill, page);
-        page = next;
         commit();
         fill = fill + 1 == NS ? 0 : fill + 1;
       }
@@ -489,8 +511,9 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
         if (c == 0) P.part_ml[at] = make_float2(M, L);
       } else {
         const float inv = L == 0.f ? 0.f : 1.f / L;
-        T *dst = reinterpret_cast<T *>(P.out) + (int64_t)(row0 + (l0 + r) / P.G) * P.ld_out +
-                 (int64_t)((g0 + hs) * P.G + (l0 + r) % P.G) * HD + c;
+        const int qi = P.by_G.div(l0 + r);
+        T *dst = reinterpret_cast<T *>(P.out) + (int64_t)(row0 + qi) * P.ld_out +
+                 (int64_t)((g0 + hs) * P.G + l0 + r - qi * P.G) * HD + c;
         if constexpr (F32)
           *reinterpret_cast<float4 *>(dst) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
         else
@@ -577,8 +600,9 @@ decode_merge_kernel(const __grid_constant__ AttnParams P, int R) {
       b += s_o[w][k][c + 1];
     }
     if (r0 + k >= J.rows) continue;
-    T *dst = reinterpret_cast<T *>(P.out) + (int64_t)(J.row0 + l / P.G) * P.ld_out +
-             (int64_t)((J.g + hs) * P.G + l % P.G) * HD + c;
+    const int qi = P.by_G.div(l);
+    T *dst = reinterpret_cast<T *>(P.out) + (int64_t)(J.row0 + qi) * P.ld_out +
+             (int64_t)((J.g + hs) * P.G + l - qi * P.G) * HD + c;
     if constexpr (std::is_same<T, float>::value)
       *reinterpret_cast<float2 *>(dst) = make_float2(a * s_inv[k], b * s_inv[k]);
     else

@@ -211,10 +211,10 @@ def _line(units, blocks, grid, per):
     begin = np.concatenate([[0], np.cumsum([u * b for u, b in zip(units, blocks)])])
     total = int(begin[-1])
     parts = min((total + per - 1) // per, grid)
-    each, extra = divmod(total, parts)
-    pb = lambda c: each * c + min(c, extra)
-    long_parts = (each + 1) * extra
-    part_of = lambda u: u // (each + 1) if u < long_parts else extra + (u - long_parts) // each
+    if len(units) == 1 and units[0] < parts:
+        parts -= parts % units[0]
+    pb = lambda c: c * total // parts
+    part_of = lambda u: ((u + 1) * parts - 1) // total
     seq = lambda u: max(s for s in range(len(units)) if begin[s] <= u)
     pieces, joins = [], []
     for c in range(parts):
@@ -261,5 +261,8 @@ def test_every_unit_once_and_every_split_item_joined_once(seed):
             found = [j for i, j in joins if i == (s, k)]
             assert found == ([] if len(got) == 1 and slots == [None] else [slots])
     assert not seen
+    if len(units) == 1:                       # items of one length: no part has pieces of two
+        owners = [p[0] for p in pieces]
+        assert units[0] > len(set(owners)) or len(owners) == len(set(owners))
     used = [x[4] for x in pieces if x[4] is not None]
     assert len(used) == len(set(used))
