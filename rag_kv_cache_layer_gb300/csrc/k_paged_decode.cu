@@ -82,9 +82,10 @@ __device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], u
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x = hi + lo, hi the nearest TF32 value.
+// x = hi + lo, hi the nearest TF32 value (10 bits after the point; ties away
+// from zero).
 __device__ __forceinline__ void halves(float x, uint32_t &hi, uint32_t &lo) {
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
   lo = __float_as_uint(x - __uint_as_float(hi));
 }
 // c += A B of one m16n8k8 step in fp32: three TF32 products in a fresh
@@ -370,27 +371,38 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
       st = st + 1 == NS ? 0 : st + 1;
       float x[BN / 8][4];
 #pragma unroll
-      for (int t = 0; t < BN / 8; ++t) {
+      for (int t = 0; t < BN / 8; ++t)
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[t][k] = 0.f;
-        const uint32_t row = ks + (t * 8 + krow) * C::kRow;
+      const uint32_t krows = ks + krow * C::kRow;
+      // 64 bytes of 8 keys: two k-steps
+      if constexpr (F32) {
 #pragma unroll
-        for (int k2 = 0; k2 < KS / 2; ++k2) {   // 64 bytes of 8 keys: two k-steps
-          uint32_t b[4];
-          ldsm_x4(row + (((k2 * 4 + kcol) ^ krow) << 4), b);
-          if constexpr (F32) {
+        for (int k2 = 0; k2 < KS / 2; ++k2) {
+          uint32_t ah[2][4], al[2][4];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t ah[4], al[4];
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) halves(__uint_as_float(qf[2 * k2 + c][e]), ah[e], al[e]);
-              step_f32(x[t], ah, al, __uint_as_float(b[2 * c]), __uint_as_float(b[2 * c + 1]));
-            }
-          } else {
+            for (int e = 0; e < 4; ++e) halves(__uint_as_float(qf[2 * k2 + c][e]), ah[c][e], al[c][e]);
+#pragma unroll
+          for (int t = 0; t < BN / 8; ++t) {
+            uint32_t b[4];
+            ldsm_x4(krows + t * 8 * C::kRow + (((k2 * 4 + kcol) ^ krow) << 4), b);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              step_f32(x[t], ah[c], al[c], __uint_as_float(b[2 * c]), __uint_as_float(b[2 * c + 1]));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < BN / 8; ++t)
+#pragma unroll
+          for (int k2 = 0; k2 < KS / 2; ++k2) {
+            uint32_t b[4];
+            ldsm_x4(krows + t * 8 * C::kRow + (((k2 * 4 + kcol) ^ krow) << 4), b);
             mma16816(x[t], qf[2 * k2], b[0], b[1]);
             mma16816(x[t], qf[2 * k2 + 1], b[2], b[3]);
           }
-        }
       }
       const int key0 = j * BN;
       float mx[2] = {-INFINITY, -INFINITY};
