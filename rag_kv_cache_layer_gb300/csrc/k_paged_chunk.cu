@@ -33,6 +33,13 @@
 //
 // Parts of a split key range leave (O, m, l) in fp32 for chunk_merge_kernel.
 // All waits are bounded.
+//
+// Measured: four chunks of 2048 rows over 8192 keys, 32/8 heads of 128: 760 us,
+// 1266 TFLOP/s.  A 64-key block of 256 rows takes 1668 cycles: the tensor pipe's
+// two S (about 500 each; N = 64 reads Q again for every 64 keys) and two P V (256)
+// are 1512 of them, the softmax alone takes 1500.  S of 128 keys would halve its
+// cost, but two tiles of 128 score and 128 output columns leave P no place of its
+// own, and with P over S the chain through P V is longer than what it saves (804 us).
 #include <type_traits>
 
 #include "cb_attn_tc.cuh"
