@@ -42,7 +42,7 @@
 // Measured (32/8 heads of 128): 64 ragged requests of 200 to 16,384 keys 122
 // us, 6.0 TB/s; two of 120 to 131 thousand 164 us, 6.3 TB/s: memory.  One row over
 // 3137 keys 10.8 us: a block's 12,000 cycles of mostly dependent instructions
-// and the join.  fp32: 31 TFLOP/s on many rows (4.2 TB/s on single ones), bound
+// and the join.  fp32: 37 TFLOP/s on many rows (4.2 TB/s on single ones), bound
 // by instructions, about 25 for each step's three products.
 #include <type_traits>
 
@@ -58,11 +58,16 @@ constexpr int kDecThreads = 128;
 constexpr int kDecBlocksPerSm = 2;
 
 template <typename T, int HD, int WM> struct DecCfg {
-  static constexpr int kBN = 4096 / (int)sizeof(T) / HD;   // keys per stage: 8 KB of K and V
+  // keys per stage: 8 KB of K and V together; fp32 tiles of 64 rows take at least 16
+  // keys, since a block of 8 costs them as much in its meeting and its softmax as in
+  // products (256 rows over 8192 keys, 32/8 heads of 128: 1089 us, 918 so; 16 keys
+  // are enough at head_dim 64: 27.8 us for ragged chunks, 28.6 with 32)
+  static constexpr int kMul = sizeof(T) == 4 && WM == 4 && HD == 128 ? 2 : 1;
+  static constexpr int kBN = kMul * 4096 / (int)sizeof(T) / HD;
   static constexpr int kRow = HD * (int)sizeof(T);
   static constexpr int kTile = kBN * kRow;
   static constexpr int kStage = 2 * kTile;      // K then V
-  static constexpr int kStages = 3 * WM;        // of each group: 96 KB per block
+  static constexpr int kStages = 3 * WM / kMul; // of each group: 96 KB per block
   static constexpr int kSmem = (4 / WM) * kStages * kStage;
 };
 
@@ -385,18 +390,18 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
       if constexpr (F32) {
 #pragma unroll
         for (int k2 = 0; k2 < KS / 2; ++k2) {
-          uint32_t ah[2][4], al[2][4];
+          uint32_t b[BN / 8][4];
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int t = 0; t < BN / 8; ++t)
+            ldsm_x4(krows + t * 8 * C::kRow + (((k2 * 4 + kcol) ^ krow) << 4), b[t]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) halves(__uint_as_float(qf[2 * k2 + c][e]), ah[c][e], al[c][e]);
+          for (int c = 0; c < 2; ++c) {
+            uint32_t ah[4], al[4];
 #pragma unroll
-          for (int t = 0; t < BN / 8; ++t) {
-            uint32_t b[4];
-            ldsm_x4(krows + t * 8 * C::kRow + (((k2 * 4 + kcol) ^ krow) << 4), b);
+            for (int e = 0; e < 4; ++e) halves(__uint_as_float(qf[2 * k2 + c][e]), ah[e], al[e]);
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-              step_f32(x[t], ah[c], al[c], __uint_as_float(b[2 * c]), __uint_as_float(b[2 * c + 1]));
+            for (int t = 0; t < BN / 8; ++t)
+              step_f32(x[t], ah, al, __uint_as_float(b[t][2 * c]), __uint_as_float(b[t][2 * c + 1]));
           }
         }
       } else {
