@@ -134,12 +134,17 @@ template <int WM> __device__ __forceinline__ void group_sync(int wk) {
 }
 
 // ------------------------------------------------------------------ plan --
-// The line of units.  Sequence s has items(s) = tiles * Hkv / hc items of
-// blocks(s) units each (every tile counts the sequence's whole length; the few keys a
-// tile's last row does not see are skipped when met).
+// The line of units.  A sequence's tiles are taken in pairs, one from its end
+// and one from its start: a late tile sees many keys, an early one few, and
+// the two together about the same in every pair, C units at most.  Pair q of a
+// group of heads is C units: the late tile's blocks, then the early one's (the
+// few units behind its last block are empty); behind the pairs comes an odd
+// middle tile.  Counted one by one at the sequence's length, early tiles leave
+// half of the parts idle (2000 rows from nothing in fp32, 4/2 heads of 64: 108
+// us, 65 so).
 struct Line {
   int64_t begin[CB_MAX_SEQS];     // first unit of each sequence
-  int blocks[CB_MAX_SEQS];        // units per item; 0: nothing to do
+  int blocks[CB_MAX_SEQS];        // units per pair (C), or of the only tile; 0: nothing to do
   int64_t total;                  // units
   int parts;                      // blocks of the grid that take part
 };
@@ -167,6 +172,13 @@ __device__ __forceinline__ void divide(int64_t a, int b, int &quot, int &rem) {
   }
 }
 
+// Key blocks that row l of a sequence's tile sees, at least one (rows without
+// keys get their zeros).
+__device__ __forceinline__ int blocks_seen(const AttnParams &P, int base, int l, int BN) {
+  const int seen = base + P.by_G.div(l) + 1;
+  return seen > 0 ? (seen - 1) / BN + 1 : 1;
+}
+
 // Every thread of the block calls it; one round of loads, one block scan.
 __device__ __forceinline__ void make_line(const AttnParams &P, int R, int BN, int grid, Line &L, int64_t *warp_sums,
                                           int *status) {
@@ -176,16 +188,23 @@ __device__ __forceinline__ void make_line(const AttnParams &P, int R, int BN, in
 #pragma unroll 1
   for (int i = i0; i < i1; ++i) {
     const int n = paged_rows(P.kv, i, P.n_rows, status), len = __ldg(P.kv.kv_lens + i);
-    int nb = 0;
+    int pair = 0, units = 0;                            // per group of heads
+    const int tiles = (int)(((int64_t)n * P.G + R - 1) / R);
     if (n > 0 && (int64_t)n * P.G <= P.few_hi) {
       if (len < 0 || len > P.max_kv || len > (int64_t)P.kv.max_pages * P.kv.page_size)
         report(status, CB_ERR_DEVICE_INDEX);
-      else
-        nb = len > 0 ? (len - 1) / BN + 1 : 1;          // an idle slot's rows get their zeros
+      else if (tiles == 1)
+        units = pair = blocks_seen(P, len - n, n * P.G - 1, BN);
+      else {
+        // each of a pair's two counts is within one of a linear function of
+        // the tile, and those add up to the same in every pair
+        pair = blocks_seen(P, len - n, R - 1, BN) + blocks_seen(P, len - n, tiles * R - 1, BN) + 2;
+        units = tiles & 1 ? blocks_seen(P, len - n, (tiles / 2 + 1) * R - 1, BN) : 0;
+      }
     }
-    L.blocks[i] = nb;
+    L.blocks[i] = pair;
     L.begin[i] = sum;
-    sum += ((int64_t)n * P.G + R - 1) / R * P.by_quads.d * nb;
+    sum += ((int64_t)(tiles / 2) * pair + units) * P.by_quads.d;
   }
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int64_t incl = sum;
@@ -206,9 +225,9 @@ __device__ __forceinline__ void make_line(const AttnParams &P, int R, int BN, in
     // a part has at least one unit, or one for each group that shares its head
     const int64_t most = P.hc > 1 ? first : (first + 3) / 4;
     L.parts = (int)(most < grid ? most : grid);
-    // Items of one length that are fewer than the parts take the same number
-    // of parts each, so that no part has two pieces, which costs it a second
-    // prologue and join (one row over 3137 keys: 13.1 us, 11.8 so).
+    // One sequence's pairs, where they are fewer than the parts, take the same
+    // number of parts each, so that no part has two pieces of single tiles, which
+    // costs it a second prologue and join (one row over 3137 keys: 13.1 us, 11.8 so).
     if (P.kv.n_seq == 1 && L.parts > 0) {
       int items, none;
       divide(first, L.blocks[0], items, none);
@@ -267,23 +286,38 @@ paged_decode_kernel(const __grid_constant__ AttnParams P, int *status) {
 
   int s = seq_of(line, P.kv.n_seq, u0);
   for (int64_t u = u0; u < u1;) {
-    // this piece: item `item` of sequence s, its blocks [jb, je)
+    // this piece: a tile of sequence s for a group of heads (an item), its blocks [jb, je)
     while (line.blocks[s] == 0 || (s + 1 < P.kv.n_seq && line.begin[s + 1] <= u)) ++s;
-    const int nbs = line.blocks[s];
-    int item, jb;
-    divide(u - line.begin[s], nbs, item, jb);
+    const int row0 = __ldg(P.kv.row_offsets + s), n = __ldg(P.kv.row_offsets + s + 1) - row0;
+    const int kv = __ldg(P.kv.kv_lens + s), base = kv - n, all = n * P.G, tiles = (all - 1) / R + 1;
+    int64_t local = u - line.begin[s];
+    int nbs = line.blocks[s], ph, jb, l0 = 0;    // the item's units; its pair and heads, its unit, its first row
+    const int64_t pairs = (int64_t)(tiles / 2) * P.by_quads.d * nbs;
+    if (local >= pairs) {                       // the only tile, or an odd middle one
+      if (tiles > 1) {
+        l0 = tiles / 2 * R;
+        nbs = blocks_seen(P, base, l0 + R - 1, BN);
+      }
+      divide(local - pairs, nbs, ph, jb);
+    } else {
+      divide(local, nbs, ph, jb);
+      const int q = P.by_quads.div(ph), late = blocks_seen(P, base, min((tiles - q) * R, all) - 1, BN);
+      ph -= q * (int)P.by_quads.d;
+      if (jb < late) {
+        nbs = late;
+        l0 = (tiles - 1 - q) * R;
+      } else {
+        nbs -= late;
+        jb -= late;
+        l0 = q * R;
+      }
+    }
+    const int g0 = ph * hc, g = g0 + sub, rows = min(R, all - l0);
     const int take = (int)min((int64_t)(nbs - jb), u1 - u);
     const bool whole = jb == 0 && take == nbs, first = u == u0;
     const int64_t item_end = u - jb + nbs;
     u += take;
-    const int row0 = __ldg(P.kv.row_offsets + s), n = __ldg(P.kv.row_offsets + s + 1) - row0;
-    // tiles from both ends in turn: early ones see fewer keys than the line
-    // counts for them, so neighbours even out
-    const int k = P.by_quads.div(item), g0 = (item - k * (int)P.by_quads.d) * hc, g = g0 + sub;
-    const int tiles = (int)(((int64_t)n * P.G + R - 1) / R);
-    const int l0 = ((k & 1) ? tiles - 1 - k / 2 : k / 2) * R;
-    const int kv = __ldg(P.kv.kv_lens + s), base = kv - n, rows = min(R, n * P.G - l0);
-    const int seen = base + P.by_G.div(l0 + rows - 1) + 1;        // keys the tile's last row sees
+    const int seen = base + P.by_G.div(l0 + rows - 1) + 1;    // keys the tile's last row sees
     const int je = min(jb + take, seen > 0 ? (seen - 1) / BN + 1 : 0);
     const int32_t *table = P.kv.block_table + (int64_t)s * P.kv.ld_table;
     if (threadIdx.x == 0 && u == u1)            // the last piece: the one that may go on in the next part

@@ -203,66 +203,90 @@ def test_oracle_sampling_by_hand():
 
 
 # ----------------------------------------------------- the line of units --
-def _line(units, blocks, grid, per):
-    """The decode kernel's partition, restated: (part, item, first block, end
-    block, slot or None) of every piece, and (item, slots) of every join.
-    units: items per sequence; blocks: units per item (0: nothing); per: units
-    a part has at least (4 where the block's groups share a head, else 1)."""
-    begin = np.concatenate([[0], np.cumsum([u * b for u, b in zip(units, blocks)])])
+def _blocks(base, row, G, BN):
+    """Key blocks that row `row` (query x G + head) of a sequence sees, at least one."""
+    seen = base + row // G + 1
+    return (seen - 1) // BN + 1 if seen > 0 else 1
+
+
+def _line(seqs, heads, G, R, BN, grid, per):
+    """The few-rows kernel's partition, restated: (part, item, first block, end
+    block, slot or None) of every piece, and (item, slots) of every join.  seqs:
+    (new rows, length); an item is a tile for one group of heads; per: units a
+    part has at least (4 where the block's groups share a head, else 1)."""
+    tiles = [-(-n * G // R) for n, _ in seqs]
+    pair, units = [], []
+    for (n, kv), t in zip(seqs, tiles):
+        b = lambda row: _blocks(kv - n, row, G, BN)
+        pair.append(0 if t == 0 else b(n * G - 1) if t == 1 else b(R - 1) + b(t * R - 1) + 2)
+        mid = 0 if t % 2 == 0 else pair[-1] if t == 1 else b((t // 2 + 1) * R - 1)
+        units.append(heads * (t // 2 * pair[-1] + mid))
+    begin = np.concatenate([[0], np.cumsum(units)])
     total = int(begin[-1])
     parts = min((total + per - 1) // per, grid)
-    if len(units) == 1 and units[0] < parts:
-        parts -= parts % units[0]
+    if len(seqs) == 1 and total // pair[0] < parts:
+        parts -= parts % (total // pair[0])
     pb = lambda c: c * total // parts
     part_of = lambda u: ((u + 1) * parts - 1) // total
-    seq = lambda u: max(s for s in range(len(units)) if begin[s] <= u)
+    seq = lambda u: max(s for s in range(len(seqs)) if begin[s] <= u)
     pieces, joins = [], []
     for c in range(parts):
-        u = pb(c)
+        u, u1 = pb(c), pb(c + 1)
         s = seq(u)
-        while u < pb(c + 1):
-            while blocks[s] == 0 or (s + 1 < len(units) and begin[s + 1] <= u):
+        while u < u1:
+            while pair[s] == 0 or (s + 1 < len(seqs) and begin[s + 1] <= u):
                 s += 1
-            item, jb = divmod(int(u - begin[s]), blocks[s])
-            take = min(blocks[s] - jb, pb(c + 1) - u)
-            whole = jb == 0 and take == blocks[s]
-            pieces.append((c, (s, item), jb, jb + take, None if whole else 2 * c + (u != pb(c))))
+            n, kv = seqs[s]
+            t, local, size = tiles[s], int(u - begin[s]), pair[s]
+            pairs = t // 2 * heads * size
+            if local >= pairs:
+                k = t // 2
+                size = size if t == 1 else _blocks(kv - n, (k + 1) * R - 1, G, BN)
+                g, jb = divmod(local - pairs, size)
+            else:
+                ph, jb = divmod(local, size)
+                q, g = divmod(ph, heads)
+                late = _blocks(kv - n, min((t - q) * R, n * G) - 1, G, BN)
+                k, size, jb = (t - 1 - q, late, jb) if jb < late else (q, size - late, jb - late)
+            item = (s, k, g)
+            take, first, end = min(size - jb, u1 - u), u == pb(c), u - jb + size
             u += take
-    for c in range(1, parts):
-        s = seq(pb(c))
-        item = int(pb(c) - begin[s]) // blocks[s]
-        a = int(begin[s]) + item * blocks[s]
-        if pb(c) == a or pb(c - 1) > a:
-            continue
-        last = part_of(a + blocks[s] - 1)
-        assert pb(last) <= a + blocks[s] - 1 < pb(last + 1)
-        joins.append(((s, item), [2 * x + (x == c - 1 and pb(x) != a) for x in range(c - 1, last + 1)]))
-    return pieces, joins
+            whole = jb == 0 and take == size
+            pieces.append((c, item, jb, jb + take, size, None if whole else 2 * c + (not first)))
+            if u == u1 and jb == 0 and end > u1:
+                last = part_of(end - 1)
+                assert pb(last) <= end - 1 < pb(last + 1)
+                joins.append((item, [2 * c + (not first)] + [2 * x for x in range(c + 1, last + 1)]))
+    return tiles, pieces, joins
 
 
-@pytest.mark.parametrize("seed", range(60))
+@pytest.mark.parametrize("seed", range(120))
 def test_every_unit_once_and_every_split_item_joined_once(seed):
     rng = np.random.default_rng(seed)
-    n = int(rng.integers(1, 9))
-    units = [int(rng.integers(0, 9)) for _ in range(n)]
-    blocks = [int(rng.integers(1, [3, 30, 300][seed % 3])) if u else 0 for u in units]
-    if not any(units):
-        units[0], blocks[0] = 2, 5
-    pieces, joins = _line(units, blocks, int(rng.integers(1, 40)), [1, 4][seed % 2])
+    G, R, BN, heads = (int(rng.choice(x)) for x in ([1, 2, 4, 7, 128], [16, 32, 64], [8, 16, 32], [1, 2, 5]))
+    seqs = []
+    for _ in range(int(rng.integers(1, 9)) if seed % 3 else 1):
+        n = int(rng.choice([0, 1, 1, 2, 5, rng.integers(1, [40, 300][seed % 2])]))
+        seqs.append((n, int(rng.choice([0, n, n // 2, n + rng.integers(0, 900)]))))
+    if not any(n for n, _ in seqs):
+        seqs[0] = (2, 40)
+    tiles, pieces, joins = _line(seqs, heads, G, R, BN, int(rng.integers(1, 60)), [1, 4][seed % 2])
     seen = {}
-    for c, item, jb, je, slot in pieces:
-        assert jb < je
-        seen.setdefault(item, []).append((jb, je, slot))
-    for s in range(n):
-        for k in range(units[s]):
-            got = sorted(seen.pop((s, k)))
-            assert [x[0] for x in got] == [0] + [x[1] for x in got[:-1]] and got[-1][1] == blocks[s]
-            slots = [x[2] for x in got]
-            found = [j for i, j in joins if i == (s, k)]
-            assert found == ([] if len(got) == 1 and slots == [None] else [slots])
+    for c, item, jb, je, size, slot in pieces:
+        assert jb < je <= size
+        seen.setdefault(item, []).append((jb, je, slot, size))
+    for s, (n, kv) in enumerate(seqs):
+        for k in range(tiles[s]):
+            need = _blocks(kv - n, min((k + 1) * R, n * G) - 1, G, BN)
+            for g in range(heads):
+                got = sorted(seen.pop((s, k, g)), key=lambda x: x[0])
+                assert [x[0] for x in got] == [0] + [x[1] for x in got[:-1]] and got[-1][1] == got[0][3] >= need
+                slots = [x[2] for x in got]
+                found = [j for i, j in joins if i == (s, k, g)]
+                assert found == ([] if slots == [None] else [slots])
     assert not seen
-    if len(units) == 1:                       # items of one length: no part has pieces of two
-        owners = [p[0] for p in pieces]
-        assert units[0] > len(set(owners)) or len(owners) == len(set(owners))
-    used = [x[4] for x in pieces if x[4] is not None]
+    used = [x[5] for x in pieces if x[5] is not None]
     assert len(used) == len(set(used))
+    if len(seqs) == 1 and tiles[0] == 1:      # items of one length: no part has pieces of two
+        owners = [p[0] for p in pieces]
+        assert heads > len(set(owners)) or len(owners) == len(set(owners))
