@@ -128,6 +128,10 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 // its writes are visible; it then calls grid_dep_launch() so that the next
 // kernel may start its own setup.  The next grid is scheduled only after
 // every CTA of this grid has called grid_dep_launch() or exited.
+// A kernel that uses TMEM calls grid_dep_launch() after its allocation.  The
+// next kernel may take all 512 columns of an SM in its setup and then wait for
+// this grid; a CTA of this grid that still had to allocate there would wait for
+// those columns, and neither wait would end.
 __device__ __forceinline__ void grid_dep_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

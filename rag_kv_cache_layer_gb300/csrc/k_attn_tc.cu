@@ -259,7 +259,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mapQ,
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();      // q, the cache and q_pos come from earlier kernels
-  grid_dep_launch();
   if (threadIdx.x == 0) {
     // this CTA's unit: a tile and a range of its key blocks
     int tile, jb, jcap, split;
@@ -336,6 +335,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mapQ,
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_dep_launch();    // after the allocation (see cb_common.cuh)
 
   if (warp == 0 && lane < 2) {
     // ----------------------------------------------- producers (K: lane 0, V: lane 1)

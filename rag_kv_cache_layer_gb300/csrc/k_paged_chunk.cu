@@ -139,7 +139,6 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
   __shared__ int s_sums[C::kThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
-  grid_dep_launch();
   const int split = blockIdx.x % P.n_split, g = blockIdx.x / P.n_split % P.Hkv;
   const int tile = blockIdx.x / P.n_split / P.Hkv;
   paged_find_tile<C::kThreads>(P.kv, P.n_rows, P.G, C::kRows, P.max_kv, tile, &s_tile, s_sums, status, P.rows_lo);
@@ -192,6 +191,7 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_dep_launch();                           // after the allocation (see cb_common.cuh)
   auto proxy_fence = [] { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); };
 
   if (warp < 2 * C::kProd) {
