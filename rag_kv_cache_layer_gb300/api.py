@@ -290,6 +290,8 @@ def cb_paged_attention(q, row_offsets, kv_lens, block_table, k_pages, v_pages, n
     kv, shape = _paged_kv(dev, k_pages, v_pages, row_offsets, kv_lens, block_table)
     if not q.get_device() == out.get_device() == dev or (ws is not None and ws.get_device() != dev):
         _device_error(dev, q, out, ws)
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")      # else its bytes are not the ones behind its address
     dt, cols = k_pages.dtype, n_q_heads * head_dim
     if len(shape) != 3 or shape[2] != n_kv_heads * head_dim:
         raise ValueError("the pools must be one layer's [n_pages, page_size, n_kv_heads * head_dim]")

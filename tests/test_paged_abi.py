@@ -169,6 +169,33 @@ def test_python_wrappers_refuse_host_tensors():
         R.cb_sample_tokens(z, torch.zeros(2), torch.zeros(2, dtype=torch.int32))
 
 
+def test_a_workspace_with_gaps_or_repeats_is_refused(monkeypatch):
+    """Its byte count would not be that of the memory behind its address.  Host
+    tensors stand for device ones: the wrapper compares device indices, and the
+    library is not reached."""
+    from rag_kv_cache_layer_gb300 import api
+    calls = []
+
+    class Lib:
+        def cb_paged_attention(self, *args):
+            calls.append(args)
+            return L.CB_OK
+    monkeypatch.setattr(api, "_cur_device", lambda: -1)
+    monkeypatch.setattr(api, "_cur_stream", lambda dev: 0)
+    monkeypatch.setattr(api, "lib", Lib())
+    ints = lambda x: torch.tensor(x, dtype=torch.int32)
+    kp, q = torch.zeros(4, 16, 128), torch.zeros(1, 256)
+    run = lambda ws: api.cb_paged_attention(q, ints([0, 1]), ints([1]), ints([[0]]), kp, kp, 4, 2, 64,
+                                            torch.zeros_like(q), ws=ws)
+    run(torch.empty(1 << 16, dtype=torch.uint8))
+    assert len(calls) == 1
+    for ws in (torch.empty(1, dtype=torch.uint8).expand(1 << 24), torch.empty(1 << 16, dtype=torch.uint8)[::2],
+               torch.empty(64, 64).t()):
+        with pytest.raises(ValueError, match="contiguous"):
+            run(ws)
+    assert len(calls) == 1
+
+
 # ------------------------------------------------------------------ oracle --
 def test_oracle_attention_by_hand():
     # two keys, one query at position 1 and one at position 0; head_dim 2
