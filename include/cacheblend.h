@@ -843,6 +843,19 @@ typedef struct {
 cb_status cb_paged_attention(const cb_paged_kv *kv, const cb_paged_query *query,
                              cb_dtype dtype, cb_stream stream);
 
+/* How a cb_paged_attention call of these sizes runs on the current device
+ * (148 SMs are assumed where there is none): plan[0] rows per tile of the
+ * few-rows kernel (0: not launched), plan[1] kv heads per item of it, plan[2]
+ * its blocks, plan[3] rows per unit of the chunk kernel (0: not launched),
+ * plan[4] parts of a unit's key range, plan[5] units per kv head at most, plan[6]
+ * the most rows (queries times heads per kv head) of a sequence that the few-rows
+ * kernel takes.  Host arithmetic only: tests see from it which variant a call
+ * covers.  Errors: CB_ERR_INVALID_ARG (plan NULL, or sizes that
+ * cb_paged_attention refuses or that leave it nothing to do). */
+cb_status cb_debug_paged_plan(int n_rows, int n_seq, int max_kv_len, int n_q_heads,
+                              int n_kv_heads, int head_dim, cb_dtype dtype,
+                              int64_t plan[7]);
+
 /* Samples one token per row of logits from given uniform numbers.  With
  * X = max x and w_i = exp((x_i - X) / temperature), of the tokens ordered by
  * larger x, then lower index, keep the first top_k; of those the shortest

@@ -220,6 +220,7 @@ def _load():
         "cb_paged_append": (S, [C.c_char_p, C.c_char_p, i32, vp]),
         "cb_paged_attention": (S, [C.c_char_p, C.c_char_p, i32, vp]),
         "cb_paged_attention_workspace_size": (C.c_size_t, [i32, i32, i32, i32, i32, i32, i32]),
+        "cb_debug_paged_plan": (S, [i32, i32, i32, i32, i32, i32, i32, C.POINTER(i64)]),
         "cb_sample_tokens": (S, [vp, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp]),
         "cb_selection_stats": (S, [vp, vp, C.POINTER(SelectReq), i32, vp, vp, vp]),
     }
@@ -252,7 +253,7 @@ EXPORTED = [
     "cb_anchor_workspace_size", "cb_anchor_select", "cb_anchor_count",
     "cb_loading_ratio", "cb_selection_stats",
     "cb_paged_append", "cb_paged_attention_workspace_size", "cb_paged_attention",
-    "cb_sample_tokens",
+    "cb_debug_paged_plan", "cb_sample_tokens",
 ]
 
 

@@ -390,6 +390,8 @@ cudaError_t launch_paged_append(const PagedKV &kv, const cb_paged_rows &rows, cb
                                 cudaStream_t s);
 size_t paged_attention_ws_bytes(int n_rows, int n_seq, int max_kv, int Hq, int Hkv, int hd,
                                 cb_dtype dt);
+// out: see cb_debug_paged_plan.
+void paged_attention_plan(int n_rows, int n_seq, int max_kv, int Hq, int Hkv, int hd, cb_dtype dt, int64_t out[7]);
 // cudaErrorInvalidConfiguration: more tiles than one launch takes.
 cudaError_t launch_paged_attention(const PagedKV &kv, const cb_paged_query &query, cb_dtype dt, int *status,
                                    cudaStream_t s);

@@ -86,14 +86,27 @@ static bool paged_heads_ok(int Hq, int Hkv, int hd) {
   return Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && Hq / Hkv <= 128 && Hkv <= 4096 && (hd == 64 || hd == 128);
 }
 
+// Sizes of a call that has something to do.
+static bool paged_sizes_ok(int n_rows, int n_seq, int max_kv_len, int Hq, int Hkv, int hd, cb_dtype dtype) {
+  return n_rows > 0 && n_seq > 0 && n_seq <= CB_MAX_SEQS && max_kv_len >= 0 && paged_heads_ok(Hq, Hkv, hd) &&
+         (dtype == CB_F32 || dtype == CB_BF16);
+}
+
 extern "C" size_t cb_paged_attention_workspace_size(int n_rows, int n_seq, int max_kv_len,
                                                     int n_q_heads, int n_kv_heads, int head_dim,
                                                     cb_dtype dtype) {
-  if (n_rows <= 0 || n_seq <= 0 || n_seq > CB_MAX_SEQS || max_kv_len < 0 ||
-      !paged_heads_ok(n_q_heads, n_kv_heads, head_dim) || (dtype != CB_F32 && dtype != CB_BF16))
-    return 256;
+  if (!paged_sizes_ok(n_rows, n_seq, max_kv_len, n_q_heads, n_kv_heads, head_dim, dtype)) return 256;
   const size_t n = paged_attention_ws_bytes(n_rows, n_seq, max_kv_len, n_q_heads, n_kv_heads, head_dim, dtype);
   return n > 256 ? n : 256;
+}
+
+extern "C" cb_status cb_debug_paged_plan(int n_rows, int n_seq, int max_kv_len, int n_q_heads, int n_kv_heads,
+                                         int head_dim, cb_dtype dtype, int64_t plan[7]) {
+  if (!plan || max_kv_len > CB_MAX_KV_LEN ||
+      !paged_sizes_ok(n_rows, n_seq, max_kv_len, n_q_heads, n_kv_heads, head_dim, dtype))
+    return bad("plan is NULL, or sizes that cb_paged_attention refuses");
+  paged_attention_plan(n_rows, n_seq, max_kv_len, n_q_heads, n_kv_heads, head_dim, dtype, plan);
+  return CB_OK;
 }
 
 extern "C" cb_status cb_paged_attention(const cb_paged_kv *kv, const cb_paged_query *query, cb_dtype dtype,

@@ -112,6 +112,13 @@ size_t paged_attention_ws_bytes(int n_rows, int n_seq, int max_kv, int Hq, int H
   return plan_bytes(plan(n_rows, n_seq, max_kv, Hq / Hkv, Hkv, hd, dt), hd);
 }
 
+void paged_attention_plan(int n_rows, int n_seq, int max_kv, int Hq, int Hkv, int hd, cb_dtype dt, int64_t out[7]) {
+  using namespace paged;
+  const Plan p = plan(n_rows, n_seq, max_kv, Hq / Hkv, Hkv, hd, dt);
+  const int64_t v[7] = {p.few_R, p.hc, decode_grid(), p.R, p.n_split, p.tiles, p.few_R ? p.few_hi : 0};
+  for (int i = 0; i < 7; ++i) out[i] = v[i];
+}
+
 cudaError_t launch_paged_attention(const PagedKV &kv, const cb_paged_query &a, cb_dtype dt, int *status,
                                    cudaStream_t s) {
   using namespace paged;

@@ -169,6 +169,31 @@ def test_python_wrappers_refuse_host_tensors():
         R.cb_sample_tokens(z, torch.zeros(2), torch.zeros(2, dtype=torch.int32))
 
 
+def test_plan_query():
+    """What a call of given sizes runs, and its workspace from that."""
+    def plan(*a):
+        out = (C.c_int64 * 7)(*[-5] * 7)
+        st = L.lib.cb_debug_paged_plan(*a, out)
+        return list(out) if st == L.CB_OK else st
+    size = L.lib.cb_paged_attention_workspace_size
+    for a in [(1, 1, 100000, 32, 8, 128), (64, 1, 3200, 32, 8, 128), (8192, 4, 8192, 32, 8, 128), (127, 64, 16384, 32, 8, 128),
+              (2000, 1, 30000, 24, 8, 64), (300, 1, 9000, 32, 16, 64), (60, 300, 60, 4, 2, 64)]:
+        for dt in (L.CB_BF16, L.CB_F32):
+            tile, hc, grid, unit, parts, units, limit = plan(*a, dt)
+            hkv, hd = a[4], a[5]
+            assert tile in (0, 16, 32, 64) and unit in (0, 128, 256) and (tile or unit) and grid > 0 and parts >= 1
+            assert not (unit and dt == L.CB_F32) and hc in (1, 64 // tile if tile else 1)
+            assert limit == (0 if not tile else 64 if unit else 0x7fffffff)
+            few = 2 * grid * tile * hc * (4 * hd + 8) + 24 * grid if tile else 0
+            chunk = units * hkv * parts * unit * (4 * hd + 8) if parts > 1 else 0
+            assert size(*a, dt) == max(256, few, chunk)
+    assert plan(64, 1, 3200, 32, 8, 128, L.CB_BF16)[3] == 128 and plan(1, 1, 3200, 32, 8, 128, L.CB_BF16)[:1] == [16]
+    for bad in [(0, 1, 8, 4, 2, 128, 1), (1, 0, 8, 4, 2, 128, 1), (1, 1025, 8, 4, 2, 128, 1), (1, 1, -1, 4, 2, 128, 1),
+                (1, 1, L.CB_MAX_KV_LEN + 1, 4, 2, 128, 1), (1, 1, 8, 3, 2, 128, 1), (1, 1, 8, 4, 2, 80, 1), (1, 1, 8, 4, 2, 128, 2)]:
+        assert plan(*bad) == L.CB_ERR_INVALID_ARG
+    assert L.lib.cb_debug_paged_plan(1, 1, 8, 4, 2, 128, L.CB_BF16, None) == L.CB_ERR_INVALID_ARG
+
+
 def test_a_workspace_with_gaps_or_repeats_is_refused(monkeypatch):
     """Its byte count would not be that of the memory behind its address.  Host
     tensors stand for device ones: the wrapper compares device indices, and the
