@@ -15,7 +15,7 @@ import torch
 
 import rag_kv_cache_layer_gb300 as R
 from rag_kv_cache_layer_gb300 import _lib as L
-from test_gpu_paged import F, HALF, Batch, ints, vals
+from test_gpu_paged import F, HALF, Batch, attention_case, ints, vals
 from test_paged_abi import _line
 
 pytestmark = pytest.mark.gpu
@@ -171,6 +171,14 @@ def test_chunk_variants_report_bad_pages(heads, seqs, parts):
         out = c.launch(table=t)
         assert R.device_status() == L.CB_ERR_DEVICE_INDEX
         assert torch.equal(out[:r0], good[:r0]) and torch.equal(out[r1:], good[r1:])
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 128), (4, 4, 64)])
+@pytest.mark.parametrize("dt", list(HALF))
+@pytest.mark.parametrize("seqs", [[(1, 300)], [(3, 2), (1, 0), (2, 700)], [(150, 130)], [(90, 4000)], [(70, 70), (1, 500), (200, 260)]])
+def test_a_scale_of_zero_averages_the_values(dt, heads, seqs):
+    """Every visible key weighs the same, in blocks without a visible key too."""
+    attention_case(np.random.default_rng(3), dt, heads, 16, seqs, scale=0.0)
 
 
 # ------------------------------------------------------- the line of units --
