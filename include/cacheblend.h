@@ -811,7 +811,11 @@ cb_status cb_paged_append(const cb_paged_kv *kv, const cb_paged_rows *rows,
  * generated, many for a chunk of a prompt, both in one call.  The rows' own
  * keys are in the cache already (cb_paged_append).  A row with a negative
  * position sees no key and gets zeros.  Slots past kv_lens are never used,
- * whatever they hold; K and V up to kv_lens must be finite.
+ * whatever they hold; q, and K and V up to kv_lens, must be finite (in fp32 below
+ * 2^128 - 2^116 in magnitude: larger values have no TF32 neighbour), and so must
+ * scale * q . K * log2(e) be in fp32.
+ * One call may mix single rows, drafts and chunks; a chunk beside many single rows
+ * over long caches is faster as a call of its own.
  * The workspace needs no initialisation; calls that share it must be ordered
  * on one stream.
  * Errors: CB_ERR_INVALID_ARG (NULL or misaligned pointers, strides, head

@@ -8,8 +8,8 @@
 
 namespace cb {
 
-// Sequences of one block's tile search: with kTileSearch threads per block,
-// each looks at CB_MAX_SEQS / kTileSearch consecutive sequences at most.
+// Sequences of one block's tile search: with NT threads per block (a template
+// parameter below), each looks at CB_MAX_SEQS / NT consecutive sequences at most.
 static_assert(CB_MAX_SEQS == 1024, "the searches below cover 1024 sequences");
 
 // Physical page of logical page `j` of sequence s; -1 when the table names a

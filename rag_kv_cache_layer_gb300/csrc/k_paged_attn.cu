@@ -34,6 +34,12 @@ struct Plan {
 // until the SMs are full; and where the last of few waves would be nearly
 // empty, splitting evens it out (192 units of 30,000 keys, head_dim 64: 780
 // unsplit, 476 in three parts each).
+// The model sees bounds: max_kv for every length, and up to a unit for every
+// sequence.  A loose max_kv costs little (64 rows over 3200 keys: 15.6 us, 20.1 with
+// a bound of 131,072; large chunks the same).  Single rows beside a chunk cost more:
+// they count as units, so the chunk is split less or not at all, and the call lasts
+// as long as its few CTAs (64 rows + 63 single rows, all over 16,384 keys: 894 us; as
+// two calls 35 + 610).
 static void plan_chunk(Plan &p, int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd) {
   const int sms = device_sm_count(), nb = (max_kv + 63) / 64 > 0 ? (max_kv + 63) / 64 : 1;
   double best = 1e300;
@@ -60,7 +66,17 @@ static void plan_chunk(Plan &p, int64_t n_rows, int S, int max_kv, int G, int Hk
 // sizes leave it open; a call whose rows do not exceed its sequences is taken
 // for one generated token each and runs the few-rows kernel alone (which
 // takes any number of rows), a single sequence runs the one its rows call
-// for.  The few-rows tile is 16, 32 or 64 rows by the average sequence.
+// for.  Taken for single rows, one sequence's many rows are slower than through
+// both kernels (128 over 8192 keys in 128 slots: 106 us and 88), and single rows
+// are faster (64 over 2000 keys: 89 us and 94).
+// The few-rows tile is 16, 32 or 64 rows by the average sequence, 16 where that
+// exceeds 64.  The average is right for drafts alone and misleads in mixed calls,
+// whose long sequences the chunk kernel takes (32/8 heads over 8192 keys unless
+// stated; us with tiles of 16 / 32 / 64 rows, the rule's in brackets):
+//   512 + 63 single rows                         435 / 442 / [701]
+//   2048 + 63 single rows                      [618] / 624 / 877
+//   512 + 32 drafts of 4, 16,384 keys          [484] / 490 / 752
+//   512 + 16 drafts of 5 to 8, 64/8, 16,384    [712] / 644 / 618
 // fp32 runs the few-rows kernel alone, whatever its rows.
 static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd, cb_dtype dt) {
   Plan p = {};

@@ -7,9 +7,10 @@
 // of a sequence are taken last first: they see the most keys.
 //
 // NT = 2, one CTA per SM: two tiles share every K and V block, so a block is
-// fetched once for 256 rows and four stages fit.  NT = 1, two CTAs per SM with
-// two stages each, serves sequences of up to 128 rows, whose second tile would
-// be empty.
+// fetched once for 256 rows and four stages fit; a unit of up to 128 rows runs
+// its first tile alone.  NT = 1: two CTAs per SM with two stages each, for calls
+// whose units of 256 rows would leave SMs empty or tiles without rows.  The cost
+// model in plan_chunk picks NT for a call.
 //
 // Roles: producer warps fill the 64-key K and V stages; one MMA warp per tile
 // owns 256 TMEM columns and issues tcgen05.mma: S_j = Q K_j^T into columns
@@ -34,12 +35,13 @@
 // Parts of a split key range leave (O, m, l) in fp32 for chunk_merge_kernel.
 // All waits are bounded.
 //
-// Measured: four chunks of 2048 rows over 8192 keys, 32/8 heads of 128: 760 us,
-// 1266 TFLOP/s.  A 64-key block of 256 rows takes 1668 cycles: the tensor pipe's
+// Measured: four chunks of 2048 rows over 8192 keys, 32/8 heads of 128: 760 to 785
+// us on several GPUs, 1225 to 1266 TFLOP/s.  A 64-key block of 256 rows takes 1668 cycles: the tensor pipe's
 // two S (about 500 each; N = 64 reads Q again for every 64 keys) and two P V (256)
 // are 1512 of them, the softmax alone takes 1500.  S of 128 keys would halve its
 // cost, but two tiles of 128 score and 128 output columns leave P no place of its
-// own, and with P over S the chain through P V is longer than what it saves (804 us).
+// own, and with P over S the chain through P V is longer than what it saves (804 us
+// where this form took 762).
 #include <type_traits>
 
 #include "cb_attn_tc.cuh"

@@ -16,12 +16,12 @@
 // (hc = WK, decode_heads) an item is WK neighbouring heads, one per group, all
 // groups walking the same keys: their slices of a cache row lie side by side
 // and are read together, which the memory's pages like (64 ragged requests:
-// 148 us with a head per item, 128 so), and the groups' states need no join.
+// 142 us with a head per item, 123 so), and the groups' states need no join.
 // Else (hc = 1) an item is one head, and key block i goes to group i mod WK.
-// A group fills a ring of its own by 16-byte cp.async,
-// two blocks ahead, with zeros for keys past the cached length (so nothing
-// unwritten in a page reaches the products), and meets nobody else inside the
-// loop.  TMA is not used here: a page's slice of one head is a box of 8 to 64
+// A group fills a ring of its own by 16-byte cp.async, kStages - 1 blocks ahead
+// (2 for 16-row tiles, 5 for 32, 11 or 5 for 64), with zeros for keys past the
+// cached length (so nothing unwritten in a page reaches the products), and meets
+// nobody else inside the loop.  TMA is not used here: a page's slice of one head is a box of 8 to 64
 // rows of 256 bytes, and a box costs about 140 ns of one SM's copy unit
 // whatever its height, which held the same loop to 12 - 27 GB/s per block.
 //
@@ -39,9 +39,9 @@
 // 1e-5 and more).  That is 2 to 5 times the CUDA cores' rate and keeps their
 // error.
 //
-// Measured (32/8 heads of 128): 64 ragged requests of 200 to 16,384 keys 122
-// us, 6.0 TB/s; two of 120 to 131 thousand 164 us, 6.3 TB/s: memory.  One row over
-// 3137 keys 10.8 us: a block's 12,000 cycles of mostly dependent instructions
+// Measured (32/8 heads of 128): 64 ragged requests of 200 to 16,384 keys 122 to
+// 125 us, 6.0 TB/s; two of 120 to 131 thousand 164 to 166 us, 6.3 TB/s: memory.  One
+// row over 3137 keys 10.8 us: a block's 12,000 cycles of mostly dependent instructions
 // and the join.  fp32: 37 TFLOP/s on many rows (4.2 TB/s on single ones), bound
 // by instructions, about 25 for each step's three products.
 #include <type_traits>
@@ -227,7 +227,8 @@ __device__ __forceinline__ void make_line(const AttnParams &P, int R, int BN, in
     L.parts = (int)(most < grid ? most : grid);
     // One sequence's pairs, where they are fewer than the parts, take the same
     // number of parts each, so that no part has two pieces of single tiles, which
-    // costs it a second prologue and join (one row over 3137 keys: 13.1 us, 11.8 so).
+    // costs it a second prologue and join (one row, 28/4 heads of 128: 10.0 us over
+    // 1000 keys, 8.4 so; where no part had two anyway, the arithmetic costs 0.2 us).
     if (P.kv.n_seq == 1 && L.parts > 0) {
       int items, none;
       divide(first, L.blocks[0], items, none);
@@ -670,8 +671,8 @@ decode_merge_kernel(const __grid_constant__ AttnParams P, int R) {
 int decode_grid() { return kDecBlocksPerSm * device_sm_count(); }
 // Heads per item: as many as the block has groups where that leaves at least
 // one item for every eight parts, else one (an item in many pieces is joined
-// slowly: one row over 3137 keys took 23 us with four heads per item, 11 with
-// one; 64 ragged sequences 128 and 148).
+// slowly: one row over 3137 keys takes 20.8 us with four heads per item, 10.9 with
+// one; 64 ragged sequences 123 and 142).
 int decode_heads(int R, int64_t tiles, int Hkv) {
   const int groups = 64 / R;
   return Hkv % groups == 0 && 8 * tiles * (Hkv / groups) >= decode_grid() ? groups : 1;

@@ -20,8 +20,8 @@
 // the logits are read once from device memory.  The two selections share one
 // histogram over equal steps of x, from the maximum down to where weights
 // vanish.  Under top_k it counts tokens only: top_p is then of the kept
-// tokens' weight, and they are few (one row of 128,256, top_k 50 and top_p: 26
-// us with every token weighed, 14.5 without).  The step at which the count
+// tokens' weight, and they are few (when that was brought in, one row of 128,256
+// with top_k 50 and top_p went from 26 us to 14.5; it takes 11.7 now).  The step at which the count
 // reaches top_k, or the weight top_p, is found from its sums, and only the
 // tokens that matter there are gathered, in vocabulary order:
 //   small  all tokens down to that step (at most kCand): the cluster's first
@@ -35,7 +35,7 @@
 //
 // What it measures: one row of 128,256 in bf16 4.2 us when greedy, 11 to 17 us
 // with top_k 5 to 1000 and top_p; 96 rows of 151,936 in fp32 with mixed
-// settings 87 us.  One row is a chain of a dozen dependent phases of 0.3 to 2 us
+// settings 76 to 88 us, by the settings drawn.  One row is a chain of a dozen dependent phases of 0.3 to 2 us
 // (load, maximum, histogram, its sums over the cluster, search, gather, order,
 // draw), with a cluster barrier between most; many rows are bound by the
 // arithmetic, about 90 instructions per token where weights are exact.
