@@ -39,7 +39,7 @@ struct Plan {
 // a bound of 131,072; large chunks the same).  Single rows beside a chunk cost more:
 // they count as units, so the chunk is split less or not at all, and the call lasts
 // as long as its few CTAs (64 rows + 63 single rows, all over 16,384 keys: 894 us; as
-// two calls 35 + 610).
+// two calls 35 + 610).  The costs are those of head_dim 128; 64 is planned by them too.
 static void plan_chunk(Plan &p, int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd) {
   const int sms = device_sm_count(), nb = (max_kv + 63) / 64 > 0 ? (max_kv + 63) / 64 : 1;
   double best = 1e300;

@@ -40,7 +40,7 @@
 // error.
 //
 // Measured (32/8 heads of 128): 64 ragged requests of 200 to 16,384 keys 122 to
-// 125 us, 6.0 TB/s; two of 120 to 131 thousand 164 to 166 us, 6.3 TB/s: memory.  One
+// 125 us, 6.0 TB/s; two of 120 to 131 thousand 162 to 166 us, 6.3 TB/s: memory.  One
 // row over 3137 keys 10.8 us: a block's 12,000 cycles of mostly dependent instructions
 // and the join.  fp32: 37 TFLOP/s on many rows (4.2 TB/s on single ones), bound
 // by instructions, about 25 for each step's three products.
