@@ -886,6 +886,157 @@ cb_status cb_sample_tokens(const void *logits, int64_t ld_logits, int n_rows,
                            const float *top_p, const float *min_p,
                            int32_t *tokens, cb_stream stream);
 
+/* ------------------------------------------------------------------------ */
+/* Long contexts: a paged cache in 4 bits                                   */
+/* ------------------------------------------------------------------------ */
+
+/* A paged cache whose values are 4-bit floats (sign, 2 exponent and 1 mantissa
+ * bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6) with one 8-bit float scale (4 exponent and 3
+ * mantissa bits, no infinities) for each group of 16 consecutive dimensions of a
+ * head: 4.5 bits a value.  A value stands for code * scale * 2^k_exp (keys) or
+ * 2^v_exp (values).
+ * A page holds its kv heads one after the other; a head's block is
+ *   keys' codes [slot][head_dim / 2] | values' codes [slot][head_dim / 2] |
+ *   keys' scales [slot][head_dim / 16] | values' scales [slot][head_dim / 16],
+ * a byte of codes an even dimension (low four bits) and the next one.
+ * head_dim is 64 or 128.  Sequences, rows and tables as for cb_paged_kv. */
+typedef struct {
+  void *pages;                /* device: page p at p * page_stride bytes,
+                                 16-byte aligned                             */
+  int64_t page_stride;        /* bytes, a multiple of 16, at least
+                                 cb_paged4_page_bytes(...)                   */
+  int n_pages;                /* pages of the pool                           */
+  int page_size;              /* slots per page: a power of two, 8 .. 1024   */
+  const int32_t *block_table; /* device [n_seq][ld_table], max_pages used    */
+  int64_t ld_table;
+  int max_pages;
+  const int32_t *row_offsets; /* device [n_seq + 1], ascending               */
+  const int32_t *kv_lens;     /* device [n_seq]                              */
+  int n_seq;                  /* 0 .. CB_MAX_SEQS                            */
+  int k_exp, v_exp;           /* -64 .. 64                                   */
+} cb_paged4_kv;
+
+/* Bytes of a page of such a cache, 0 for sizes that it does not take
+ * (page_size, head_dim, n_kv_heads outside [1, 4096]). */
+size_t cb_paged4_page_bytes(int page_size, int n_kv_heads, int head_dim);
+
+/* Appends rows to a 4-bit cache: cb_paged_append with its arguments, rotation and
+ * errors (cache_layer_stride in bytes), and with the stored rows quantised.  A key
+ * is rotated and rounded to the rows' type, as a cache of that type would hold it
+ * (the rounding is exact: q_out and the keys may differ from cb_paged_append's in
+ * the last bit).  Of y = 2^-exp times a group's 16 values, a the largest magnitude:
+ *   scale = the 8-bit float nearest to a / 6 (ties to even), within [2^-9, 448],
+ *   code  = the 4-bit float nearest to y / scale (ties to the even code), 6 where
+ *           it is larger.
+ * Rows should be finite: an infinity is stored as 6 times its scale, a NaN as
+ * some finite value.  Slots of other rows keep their codes. */
+cb_status cb_paged4_append(const cb_paged4_kv *kv, const cb_paged_rows *rows,
+                           cb_dtype dtype, cb_stream stream);
+
+/* Reads rows back: row r gets the values that its position's codes stand for,
+ * rounded to dtype where 2^exp takes them out of its range.  With the append's
+ * offsets and lengths these are the rows that it stored (keys rotated).
+ * Rows without a position, or whose page is outside the pool or the table
+ * (CB_ERR_DEVICE_INDEX), keep their content.  Errors as for cb_paged4_append. */
+typedef struct {
+  void *k, *v;                /* device [n_rows] rows of n_kv_heads * head_dim */
+  int64_t ld_k, ld_v;         /* elements between rows                       */
+  int64_t k_layer_stride, v_layer_stride; /* elements, n_layers > 1          */
+  int64_t cache_layer_stride; /* bytes, n_layers > 1                         */
+  int n_rows, n_layers, n_kv_heads, head_dim;
+} cb_paged_rows_out;
+cb_status cb_paged4_gather(const cb_paged4_kv *kv, const cb_paged_rows_out *rows,
+                           cb_dtype dtype, cb_stream stream);
+
+/* cb_paged_attention over a 4-bit cache, with its arguments and errors: q and out
+ * are of dtype, the keys and values what their codes stand for, without a further
+ * rounding.  Codes past kv_lens are never used; scales up to it must not be NaN
+ * (cb_paged4_append writes none).  q, and scale * q . K * log2(e), must be finite. */
+size_t cb_paged4_attention_workspace_size(int n_rows, int n_seq, int max_kv_len,
+                                          int n_q_heads, int n_kv_heads, int head_dim,
+                                          cb_dtype dtype);
+cb_status cb_paged4_attention(const cb_paged4_kv *kv, const cb_paged_query *query,
+                              cb_dtype dtype, cb_stream stream);
+
+/* ------------------------------------------------------------------------ */
+/* Long contexts: attention over the pages that a row needs                 */
+/* ------------------------------------------------------------------------ */
+
+/* Largest n_picks of cb_paged_select and cb_paged_attention_picked. */
+#define CB_MAX_PICKS 1024
+
+/* Bounds of the keys of every page: the smallest and the largest key, dimension
+ * by dimension, over the page's slots that a sequence's length covers. */
+typedef struct {
+  void *bounds;               /* device: of page p, the minima at p *
+                                 page_stride, the maxima ld after them
+                                 (elements; rows of n_kv_heads * head_dim)   */
+  int64_t page_stride, ld;    /* rows 16-byte aligned                        */
+  int64_t bounds_layer_stride, cache_layer_stride; /* n_layers > 1           */
+  int n_rows, n_layers, n_kv_heads, head_dim;
+} cb_page_bounds;
+
+/* Brings the bounds of every page up to date that holds one of the call's rows
+ * (their keys are in the cache already), from all of its slots up to kv_lens: a
+ * page that is used again needs no clearing.  kv->v_pages is not read (may be
+ * NULL).  Keys must not be NaN.
+ * Errors: CB_ERR_INVALID_ARG (NULL or misaligned pointers, strides below a row,
+ * head_dim not a multiple of 16, several layers with a layer stride of 0),
+ * CB_ERR_UNSUPPORTED (page_size).  On the device, bad offsets, and pages outside
+ * the pool or the table record CB_ERR_DEVICE_INDEX and are skipped. */
+cb_status cb_paged_bounds(const cb_paged_kv *kv, const cb_page_bounds *bounds,
+                          cb_dtype dtype, cb_stream stream);
+
+/* Picks pages for every row and kv head.  A row at position p has the pages
+ * 0 .. p / page_size.  A page's score is the largest dot product that its bounds
+ * allow a key of it, over the q heads h of the kv head's group:
+ *   score(j) = max_h sum_d max(q[h][d] min[j][d], q[h][d] max[j][d]).
+ * Where the row has more than n_picks pages: the first n_first, the last n_last
+ * and of the others those of the largest scores (ties: the lower page), n_picks
+ * in all; else all of them.  Where the choice hangs on it, scores are summed in
+ * 64 bits.
+ * picks: device int32 [n_rows][n_kv_heads][n_picks] contiguous, a sequence's page
+ * numbers (indices into its table row) ascending, -1 behind the last one; all -1
+ * for a row with a negative position.  Rows of no sequence, or of one with wrong
+ * offsets or length, keep theirs.
+ * kv's k_pages and v_pages are not read (may be NULL).  q, the bounds and the scores
+ * (in fp32) must be finite.  The workspace as for cb_paged_attention.
+ * Errors: CB_ERR_INVALID_ARG (NULL or misaligned pointers, strides, n_picks outside
+ * [1, CB_MAX_PICKS], n_first or n_last negative or their sum above n_picks, head
+ * counts not dividing or more than 128 q heads per kv head, head_dim not 64 or
+ * 128), CB_ERR_UNSUPPORTED (page_size, max_kv_len > CB_MAX_KV_LEN, more pages than
+ * one launch takes), CB_ERR_WORKSPACE.  On the device as for cb_paged_attention; a
+ * page outside the pool counts as one of the smallest score. */
+typedef struct {
+  const void *q;              /* device [n_rows][ld_q], n_q_heads * head_dim */
+  int64_t ld_q;
+  int32_t *picks;             /* device [n_rows][n_kv_heads][n_picks]        */
+  void *ws;                   /* 16-byte aligned device scratch              */
+  size_t ws_bytes;
+  int max_kv_len;             /* an upper bound of every kv_lens[s]          */
+  int n_q_heads, n_picks, n_first, n_last;
+} cb_page_select;
+size_t cb_paged_select_workspace_size(int n_rows, int max_kv_len, int page_size,
+                                      int n_kv_heads);
+cb_status cb_paged_select(const cb_paged_kv *kv, const cb_page_bounds *bounds,
+                          const cb_page_select *select, cb_dtype dtype,
+                          cb_stream stream);
+
+/* cb_paged_attention over picked pages: row r sees, for kv head g, the keys at
+ * positions <= its own in the pages picks[r][g][0 .. n_picks) of its sequence, in
+ * any order; an entry of -1 names none, a page named twice counts twice.  A row
+ * that sees no key gets zeros.  picks: device int32 [n_rows][n_kv_heads][n_picks]
+ * contiguous, 4-byte aligned.  query->max_kv_len is not used.  Errors: as for
+ * cb_paged_attention, and CB_ERR_INVALID_ARG for n_picks outside [1, CB_MAX_PICKS].
+ * On the device, a pick below -1 or outside the table, and a page outside the pool
+ * record CB_ERR_DEVICE_INDEX and count as no page. */
+size_t cb_paged_attention_picked_workspace_size(int n_rows, int n_picks, int page_size,
+                                                int n_q_heads, int n_kv_heads,
+                                                int head_dim, cb_dtype dtype);
+cb_status cb_paged_attention_picked(const cb_paged_kv *kv, const cb_paged_query *query,
+                                    const int32_t *picks, int n_picks, cb_dtype dtype,
+                                    cb_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -141,6 +141,30 @@ class PagedQuery(C.Structure):
                 ("n_q_heads", i32), ("n_kv_heads", i32), ("head_dim", i32), ("scale", C.c_float)]
 
 
+class Paged4KV(C.Structure):
+    _fields_ = [("pages", vp), ("page_stride", i64), ("n_pages", i32), ("page_size", i32),
+                ("block_table", vp), ("ld_table", i64), ("max_pages", i32), ("row_offsets", vp),
+                ("kv_lens", vp), ("n_seq", i32), ("k_exp", i32), ("v_exp", i32)]
+
+
+class PagedRowsOut(C.Structure):
+    _fields_ = [("k", vp), ("v", vp), ("ld_k", i64), ("ld_v", i64),
+                ("k_layer_stride", i64), ("v_layer_stride", i64), ("cache_layer_stride", i64),
+                ("n_rows", i32), ("n_layers", i32), ("n_kv_heads", i32), ("head_dim", i32)]
+
+
+class PageBounds(C.Structure):
+    _fields_ = [("bounds", vp), ("page_stride", i64), ("ld", i64), ("bounds_layer_stride", i64),
+                ("cache_layer_stride", i64), ("n_rows", i32), ("n_layers", i32),
+                ("n_kv_heads", i32), ("head_dim", i32)]
+
+
+class PageSelect(C.Structure):
+    _fields_ = [("q", vp), ("ld_q", i64), ("picks", vp), ("ws", vp), ("ws_bytes", C.c_size_t),
+                ("max_kv_len", i32), ("n_q_heads", i32), ("n_picks", i32), ("n_first", i32),
+                ("n_last", i32)]
+
+
 def packer(cls):
     """A function from field values to the structure's bytes: calls that run
     once per layer and token pass those in place of a ctypes object, which
@@ -222,6 +246,16 @@ def _load():
         "cb_paged_attention_workspace_size": (C.c_size_t, [i32, i32, i32, i32, i32, i32, i32]),
         "cb_debug_paged_plan": (S, [i32, i32, i32, i32, i32, i32, i32, C.POINTER(i64)]),
         "cb_sample_tokens": (S, [vp, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp]),
+        "cb_paged4_page_bytes": (C.c_size_t, [i32, i32, i32]),
+        "cb_paged4_append": (S, [C.c_char_p, C.c_char_p, i32, vp]),
+        "cb_paged4_gather": (S, [C.c_char_p, C.c_char_p, i32, vp]),
+        "cb_paged4_attention_workspace_size": (C.c_size_t, [i32, i32, i32, i32, i32, i32, i32]),
+        "cb_paged4_attention": (S, [C.c_char_p, C.c_char_p, i32, vp]),
+        "cb_paged_bounds": (S, [C.c_char_p, C.c_char_p, i32, vp]),
+        "cb_paged_select_workspace_size": (C.c_size_t, [i32, i32, i32, i32]),
+        "cb_paged_select": (S, [C.c_char_p, C.c_char_p, C.c_char_p, i32, vp]),
+        "cb_paged_attention_picked_workspace_size": (C.c_size_t, [i32, i32, i32, i32, i32, i32, i32]),
+        "cb_paged_attention_picked": (S, [C.c_char_p, C.c_char_p, vp, i32, i32, vp]),
         "cb_selection_stats": (S, [vp, vp, C.POINTER(SelectReq), i32, vp, vp, vp]),
     }
     for name, (res, args) in sigs.items():
@@ -254,6 +288,10 @@ EXPORTED = [
     "cb_loading_ratio", "cb_selection_stats",
     "cb_paged_append", "cb_paged_attention_workspace_size", "cb_paged_attention",
     "cb_debug_paged_plan", "cb_sample_tokens",
+    "cb_paged4_page_bytes", "cb_paged4_append", "cb_paged4_gather",
+    "cb_paged4_attention_workspace_size", "cb_paged4_attention",
+    "cb_paged_bounds", "cb_paged_select_workspace_size", "cb_paged_select",
+    "cb_paged_attention_picked_workspace_size", "cb_paged_attention_picked",
 ]
 
 

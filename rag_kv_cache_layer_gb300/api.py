@@ -24,6 +24,10 @@ __all__ = [
     "device_status",
     "cb_paged_append", "cb_paged_attention", "cb_paged_attention_workspace",
     "cb_sample_tokens",
+    "cb_paged4_page_bytes", "cb_paged4_append", "cb_paged4_gather", "cb_paged4_attention",
+    "cb_paged4_attention_workspace", "cb_paged_bounds", "cb_paged_select",
+    "cb_paged_select_workspace", "cb_paged_attention_picked",
+    "cb_paged_attention_picked_workspace",
 ]
 
 device_status = L.device_status
@@ -172,7 +176,10 @@ _cur_device = torch._C._cuda_getDevice
 _cur_stream = torch._C._cuda_getCurrentRawStream
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _CODES = {_BF16: L.CB_BF16, _F32: L.CB_F32}
+_U8 = torch.uint8
 _pack_kv, _pack_rows, _pack_query = L.packer(L.PagedKV), L.packer(L.PagedRows), L.packer(L.PagedQuery)
+_pack_kv4, _pack_rows_out = L.packer(L.Paged4KV), L.packer(L.PagedRowsOut)
+_pack_bounds, _pack_select = L.packer(L.PageBounds), L.packer(L.PageSelect)
 
 
 def _device_error(dev, *tensors):
@@ -189,10 +196,8 @@ def _ld(name, t, dtype, rows, cols):
     return ld if rows > 1 else cols
 
 
-def _paged_kv(dev, k_pages, v_pages, row_offsets, kv_lens, block_table):
-    if not k_pages.get_device() == v_pages.get_device() == row_offsets.get_device() == \
-            kv_lens.get_device() == block_table.get_device() == dev:
-        _device_error(dev, k_pages, v_pages, row_offsets, kv_lens, block_table)
+def _table(row_offsets, kv_lens, block_table):
+    """Number of sequences and table width and leading dimension."""
     n_seq, width = block_table.shape
     ld_table, one = block_table.stride()
     if not kv_lens.dtype is row_offsets.dtype is block_table.dtype is _I32 or (one != 1 and width > 1) or \
@@ -200,6 +205,14 @@ def _paged_kv(dev, k_pages, v_pages, row_offsets, kv_lens, block_table):
             not (kv_lens.is_contiguous() and row_offsets.is_contiguous()):
         raise ValueError("row_offsets [n_seq + 1], kv_lens [n_seq] and block_table [n_seq, max_pages] "
                          "must be int32 with contiguous rows")
+    return n_seq, width, ld_table if n_seq > 1 else width
+
+
+def _paged_kv(dev, k_pages, v_pages, row_offsets, kv_lens, block_table):
+    if not k_pages.get_device() == v_pages.get_device() == row_offsets.get_device() == \
+            kv_lens.get_device() == block_table.get_device() == dev:
+        _device_error(dev, k_pages, v_pages, row_offsets, kv_lens, block_table)
+    n_seq, width, ld_table = _table(row_offsets, kv_lens, block_table)
     shape, strides = k_pages.shape, k_pages.stride()
     if v_pages.stride() != strides or v_pages.shape != shape or v_pages.dtype is not k_pages.dtype or \
             strides[-1] != 1:
@@ -207,7 +220,7 @@ def _paged_kv(dev, k_pages, v_pages, row_offsets, kv_lens, block_table):
     n_pages, page, cols = shape[-3:]
     ld = strides[-2] if page > 1 else cols
     kv = _pack_kv(k_pages.data_ptr(), v_pages.data_ptr(), strides[-3] if n_pages > 1 else page * ld, ld,
-                  n_pages, page, block_table.data_ptr(), ld_table if n_seq > 1 else width, width,
+                  n_pages, page, block_table.data_ptr(), ld_table, width,
                   row_offsets.data_ptr(), kv_lens.data_ptr(), n_seq)
     return kv, shape
 
@@ -270,6 +283,11 @@ def cb_paged_append(k_new, v_new, row_offsets, kv_lens, block_table, k_pages, v_
         check(status)
 
 
+def _check_ws(ws):
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")      # else its bytes are not the ones behind its address
+
+
 def cb_paged_attention_workspace(q, n_seq, max_kv_len, n_q_heads, n_kv_heads, head_dim):
     """Scratch for cb_paged_attention calls of these sizes (rows and dtype of
     q), to be kept from call to call."""
@@ -290,8 +308,7 @@ def cb_paged_attention(q, row_offsets, kv_lens, block_table, k_pages, v_pages, n
     kv, shape = _paged_kv(dev, k_pages, v_pages, row_offsets, kv_lens, block_table)
     if not q.get_device() == out.get_device() == dev or (ws is not None and ws.get_device() != dev):
         _device_error(dev, q, out, ws)
-    if ws is not None and not ws.is_contiguous():
-        raise ValueError("ws must be contiguous")      # else its bytes are not the ones behind its address
+    _check_ws(ws)
     dt, cols = k_pages.dtype, n_q_heads * head_dim
     if len(shape) != 3 or shape[2] != n_kv_heads * head_dim:
         raise ValueError("the pools must be one layer's [n_pages, page_size, n_kv_heads * head_dim]")
@@ -307,6 +324,263 @@ def cb_paged_attention(q, row_offsets, kv_lens, block_table, k_pages, v_pages, n
                         1.0 / math.sqrt(head_dim) if scale is None else scale)
     status = lib.cb_paged_attention(kv, query, _CODES.get(dt, -1),
                                     _cur_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        check(status)
+
+
+# ----------------------------------------------- generation: 4-bit cache --
+def cb_paged4_page_bytes(page_size, n_kv_heads, head_dim):
+    """Bytes of a page of a 4-bit cache: a pool is uint8 [n_pages, that many]."""
+    n = lib.cb_paged4_page_bytes(page_size, n_kv_heads, head_dim)
+    if n == 0:
+        raise ValueError("page_size must be a power of two from 8 to 1024, head_dim 64 or 128, "
+                         "n_kv_heads from 1 to 4096")
+    return n
+
+
+def _paged4_kv(dev, pages, page_size, row_offsets, kv_lens, block_table, k_exp, v_exp):
+    if not pages.get_device() == row_offsets.get_device() == kv_lens.get_device() == \
+            block_table.get_device() == dev:
+        _device_error(dev, pages, row_offsets, kv_lens, block_table)
+    n_seq, width, ld_table = _table(row_offsets, kv_lens, block_table)
+    shape, strides = pages.shape, pages.stride()
+    if pages.dtype is not _U8 or len(shape) not in (2, 3) or strides[-1] != 1:
+        raise ValueError("pages must be uint8 [n_pages, page bytes] (or with a layer dimension before), "
+                         "each page contiguous")
+    n_pages, size = shape[-2:]
+    return _pack_kv4(pages.data_ptr(), strides[-2] if n_pages > 1 else size, n_pages, page_size,
+                     block_table.data_ptr(), ld_table, width, row_offsets.data_ptr(), kv_lens.data_ptr(), n_seq,
+                     k_exp, v_exp), shape
+
+
+def _paged4_rows(dev, k, v, pages, page_size, head_dim):
+    """First layer's rows, number of layers and strides of k and v [(layers,) rows, row] and the pool."""
+    if not k.get_device() == v.get_device() == dev:
+        _device_error(dev, k, v)
+    layers, sk, sv, sc = 1, 0, 0, 0
+    if pages.dim() == 3:
+        layers = pages.shape[0]
+        if k.dim() != 3 or v.shape != k.shape or k.shape[0] != layers:
+            raise ValueError("the rows must have the pool's layer dimension")
+        sk, sv, sc = k.stride(0), v.stride(0), pages.stride(0)
+        if layers:
+            k, v = k[0], v[0]
+    elif k.dim() != 2 or v.dim() != 2:
+        raise ValueError("the rows must be [rows, row], the pool [n_pages, page bytes]")
+    cols = k.shape[-1]
+    if cols % head_dim:
+        raise ValueError("head_dim must divide the rows")
+    if pages.shape[-1] < cb_paged4_page_bytes(page_size, cols // head_dim, head_dim):
+        raise ValueError("the pool's pages are smaller than these rows need")
+    return k, v, layers, sk, sv, sc, cols
+
+
+def cb_paged4_append(k_new, v_new, row_offsets, kv_lens, block_table, pages, page_size, head_dim,
+                     rope_table=None, q=None, q_out=None, k_exp=0, v_exp=0, stream=None):
+    """Appends rows to a paged cache in 4 bits, rotating keys and queries to
+    their positions: cb_paged_append with a pool of bytes, pages [n_pages,
+    cb_paged4_page_bytes(...)] (with a layer dimension where k_new and v_new
+    have one).  Values are stored divided by 2^k_exp and 2^v_exp: the format
+    reaches from 2^-10 to 2688."""
+    dev = _cur_device()
+    kv, _ = _paged4_kv(dev, pages, page_size, row_offsets, kv_lens, block_table, k_exp, v_exp)
+    k1, v1, layers, sk, sv, sc, cols = _paged4_rows(dev, k_new, v_new, pages, page_size, head_dim)
+    if layers == 0:
+        return
+    dt, n_rows = k_new.dtype, k1.shape[0]
+    rope = max_pos = 0
+    if rope_table is not None:
+        if rope_table.get_device() != dev:
+            _device_error(dev, rope_table)
+        if rope_table.dtype is not _F32 or not rope_table.is_contiguous():
+            raise ValueError("rope_table must be contiguous float32")
+        rope, max_pos = rope_table.data_ptr(), rope_table.numel() // head_dim
+    qp = qop = ld_q = ld_qo = n_q = 0
+    if q is not None:
+        q_to = q if q_out is None else q_out
+        if not q.get_device() == q_to.get_device() == dev:
+            _device_error(dev, q, q_to)
+        q_cols = q.shape[1]
+        n_q = q_cols // head_dim
+        if q_cols % head_dim:
+            raise ValueError("q must be [rows, n_q_heads * head_dim]")
+        qp, ld_q = q.data_ptr(), _ld("q", q, dt, n_rows, q_cols)
+        qop, ld_qo = (qp, ld_q) if q_out is None else (q_out.data_ptr(), _ld("q_out", q_out, dt, n_rows, q_cols))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rows = _pack_rows(k1.data_ptr(), v1.data_ptr(), _ld("k_new", k1, dt, n_rows, cols),
+                      _ld("v_new", v1, dt, n_rows, cols), sk, sv, sc, n_rows, layers, cols // head_dim, head_dim,
+                      rope, qp, qop, ld_q, ld_qo, n_q, max_pos)
+    status = lib.cb_paged4_append(kv, rows, _CODES.get(dt, -1),
+                                  _cur_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        check(status)
+
+
+def cb_paged4_gather(row_offsets, kv_lens, block_table, pages, page_size, head_dim, k_out, v_out,
+                     k_exp=0, v_exp=0, stream=None):
+    """Reads rows back from a 4-bit cache: row r of k_out and v_out ([rows,
+    row], or with the pool's layer dimension; bf16 or float32) gets what its
+    position holds; arguments as for cb_paged4_append."""
+    dev = _cur_device()
+    kv, _ = _paged4_kv(dev, pages, page_size, row_offsets, kv_lens, block_table, k_exp, v_exp)
+    k1, v1, layers, sk, sv, sc, cols = _paged4_rows(dev, k_out, v_out, pages, page_size, head_dim)
+    if layers == 0:
+        return
+    dt, n_rows = k_out.dtype, k1.shape[0]
+    rows = _pack_rows_out(k1.data_ptr(), v1.data_ptr(), _ld("k_out", k1, dt, n_rows, cols),
+                          _ld("v_out", v1, dt, n_rows, cols), sk, sv, sc, n_rows, layers, cols // head_dim, head_dim)
+    status = lib.cb_paged4_gather(kv, rows, _CODES.get(dt, -1),
+                                  _cur_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        check(status)
+
+
+def cb_paged4_attention_workspace(q, n_seq, max_kv_len, n_q_heads, n_kv_heads, head_dim):
+    """Scratch for cb_paged4_attention calls of these sizes (rows and dtype of
+    q), to be kept from call to call."""
+    need = lib.cb_paged4_attention_workspace_size(q.shape[0], n_seq, max_kv_len, n_q_heads,
+                                                  n_kv_heads, head_dim, dtype_code(q.dtype))
+    return torch.empty(need, dtype=torch.uint8, device=q.device)
+
+
+def cb_paged4_attention(q, row_offsets, kv_lens, block_table, pages, page_size, n_q_heads,
+                        n_kv_heads, head_dim, out, max_kv_len=None, scale=None, k_exp=0, v_exp=0,
+                        ws=None, stream=None):
+    """cb_paged_attention over a 4-bit cache (pages as for cb_paged4_append,
+    one layer's).  ws: from cb_paged4_attention_workspace (None: allocated
+    here)."""
+    dev = _cur_device()
+    kv, shape = _paged4_kv(dev, pages, page_size, row_offsets, kv_lens, block_table, k_exp, v_exp)
+    if not q.get_device() == out.get_device() == dev or (ws is not None and ws.get_device() != dev):
+        _device_error(dev, q, out, ws)
+    _check_ws(ws)
+    dt, cols, n_rows = q.dtype, n_q_heads * head_dim, q.shape[0]
+    if len(shape) != 2 or shape[1] < cb_paged4_page_bytes(page_size, n_kv_heads, head_dim):
+        raise ValueError("the pool must be one layer's, its pages cb_paged4_page_bytes(...) or more")
+    if max_kv_len is None:
+        max_kv_len = min(block_table.shape[1] * page_size, L.CB_MAX_KV_LEN)
+    if ws is None:
+        with torch.cuda.stream(stream):        # belongs to the stream that uses it
+            ws = cb_paged4_attention_workspace(q, kv_lens.shape[0], max_kv_len, n_q_heads, n_kv_heads, head_dim)
+    query = _pack_query(q.data_ptr(), out.data_ptr(), _ld("q", q, dt, n_rows, cols), _ld("out", out, dt, n_rows, cols),
+                        ws.data_ptr(), ws.nbytes, n_rows, max_kv_len, n_q_heads, n_kv_heads, head_dim,
+                        1.0 / math.sqrt(head_dim) if scale is None else scale)
+    status = lib.cb_paged4_attention(kv, query, _CODES.get(dt, -1),
+                                     _cur_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        check(status)
+
+
+# ---------------------------------------------- generation: picked pages --
+def _bounds(bounds, dt, n_pages, cols):
+    """Address and strides of the bounds [(layers,) n_pages, 2, row]."""
+    shape, strides = bounds.shape, bounds.stride()
+    if bounds.dtype is not dt or shape[-3:] != (n_pages, 2, cols) or strides[-1] != 1:
+        raise ValueError(f"bounds must be {dt} [n_pages, 2, row] with contiguous rows")
+    return bounds.data_ptr(), strides[-3] if n_pages > 1 else strides[-2] + cols, strides[-2]
+
+
+def cb_paged_bounds(row_offsets, kv_lens, block_table, k_pages, bounds, n_rows, stream=None):
+    """Brings the bounds of every page up to date that holds one of the call's
+    n_rows new rows: bounds [n_pages, 2, row], the smallest and the largest
+    key of a page by dimension, of the type of k_pages [n_pages, page_size,
+    row]; both may have a leading layer dimension."""
+    dev = _cur_device()
+    kv, shape = _paged_kv(dev, k_pages, k_pages, row_offsets, kv_lens, block_table)
+    if bounds.get_device() != dev:
+        _device_error(dev, bounds)
+    if len(shape) not in (3, 4) or bounds.dim() != len(shape) or bounds.shape[:-3] != shape[:-3]:
+        raise ValueError("k_pages must be [n_pages, page_size, row], bounds [n_pages, 2, row], both with "
+                         "a leading layer dimension or without")
+    layers, sb, sc = (shape[0], bounds.stride(0), k_pages.stride(0)) if len(shape) == 4 else (1, 0, 0)
+    if layers == 0:
+        return
+    dt, cols = k_pages.dtype, shape[-1]
+    # rows need no heads here: any split of the row into multiples of 16 will do
+    unit = next((u for u in (128, 64, 32, 16) if cols % u == 0), cols)
+    b = _pack_bounds(*_bounds(bounds, dt, shape[-3], cols), sb, sc, n_rows, layers, cols // unit, unit)
+    status = lib.cb_paged_bounds(kv, b, _CODES.get(dt, -1),
+                                 _cur_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        check(status)
+
+
+def cb_paged_select_workspace(q, max_kv_len, page_size, n_kv_heads):
+    """Scratch for cb_paged_select calls of these sizes (rows of q), to be
+    kept from call to call."""
+    need = lib.cb_paged_select_workspace_size(q.shape[0], max_kv_len, page_size, n_kv_heads)
+    return torch.empty(need, dtype=torch.uint8, device=q.device)
+
+
+def cb_paged_select(q, row_offsets, kv_lens, block_table, bounds, page_size, n_q_heads, n_kv_heads,
+                    head_dim, picks, n_first=1, n_last=1, max_kv_len=None, ws=None, stream=None):
+    """Picks pages for every row of q and kv head by the largest dot product
+    that the pages' bounds [n_pages, 2, n_kv_heads * head_dim] allow; picks:
+    int32 [rows, n_kv_heads, n_picks], ascending, -1 behind the last.  The
+    first n_first and the newest n_last pages are always among them."""
+    dev = _cur_device()
+    if not q.get_device() == bounds.get_device() == picks.get_device() == row_offsets.get_device() == \
+            kv_lens.get_device() == block_table.get_device() == dev or (ws is not None and ws.get_device() != dev):
+        _device_error(dev, q, bounds, picks, row_offsets, kv_lens, block_table, ws)
+    _check_ws(ws)
+    n_seq, width, ld_table = _table(row_offsets, kv_lens, block_table)
+    if bounds.dim() != 3:
+        raise ValueError("bounds must be one layer's [n_pages, 2, row]")
+    dt, n_pages, n_rows = q.dtype, bounds.shape[0], q.shape[0]
+    if picks.dtype is not _I32 or picks.dim() != 3 or picks.shape[:2] != (n_rows, n_kv_heads) or \
+            not picks.is_contiguous():
+        raise ValueError(f"picks must be contiguous int32 of shape ({n_rows}, {n_kv_heads}, n_picks)")
+    if max_kv_len is None:
+        max_kv_len = min(width * page_size, L.CB_MAX_KV_LEN)
+    if ws is None:
+        with torch.cuda.stream(stream):        # belongs to the stream that uses it
+            ws = cb_paged_select_workspace(q, max_kv_len, page_size, n_kv_heads)
+    kv = _pack_kv(0, 0, 0, 0, n_pages, page_size, block_table.data_ptr(), ld_table, width, row_offsets.data_ptr(),
+                  kv_lens.data_ptr(), n_seq)
+    b = _pack_bounds(*_bounds(bounds, dt, n_pages, n_kv_heads * head_dim), 0, 0, n_rows, 1, n_kv_heads, head_dim)
+    a = _pack_select(q.data_ptr(), _ld("q", q, dt, n_rows, n_q_heads * head_dim), picks.data_ptr(), ws.data_ptr(),
+                     ws.nbytes, max_kv_len, n_q_heads, picks.shape[2], n_first, n_last)
+    status = lib.cb_paged_select(kv, b, a, _CODES.get(dt, -1),
+                                 _cur_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        check(status)
+
+
+def cb_paged_attention_picked_workspace(q, n_picks, page_size, n_q_heads, n_kv_heads, head_dim):
+    """Scratch for cb_paged_attention_picked calls of these sizes (rows and
+    dtype of q), to be kept from call to call."""
+    need = lib.cb_paged_attention_picked_workspace_size(q.shape[0], n_picks, page_size, n_q_heads, n_kv_heads,
+                                                        head_dim, dtype_code(q.dtype))
+    return torch.empty(need, dtype=torch.uint8, device=q.device)
+
+
+def cb_paged_attention_picked(q, row_offsets, kv_lens, block_table, k_pages, v_pages, picks, n_q_heads,
+                              n_kv_heads, head_dim, out, scale=None, ws=None, stream=None):
+    """cb_paged_attention where each row and kv head sees only the pages of
+    its list: picks int32 [rows, n_kv_heads, n_picks], a sequence's page
+    numbers, -1 for none (from cb_paged_select, or any other choice)."""
+    dev = _cur_device()
+    kv, shape = _paged_kv(dev, k_pages, v_pages, row_offsets, kv_lens, block_table)
+    if not q.get_device() == out.get_device() == picks.get_device() == dev or \
+            (ws is not None and ws.get_device() != dev):
+        _device_error(dev, q, out, picks, ws)
+    _check_ws(ws)
+    dt, cols, n_rows = k_pages.dtype, n_q_heads * head_dim, q.shape[0]
+    if len(shape) != 3 or shape[2] != n_kv_heads * head_dim:
+        raise ValueError("the pools must be one layer's [n_pages, page_size, n_kv_heads * head_dim]")
+    if picks.dtype is not _I32 or picks.dim() != 3 or picks.shape[:2] != (n_rows, n_kv_heads) or \
+            not picks.is_contiguous():
+        raise ValueError(f"picks must be contiguous int32 of shape ({n_rows}, {n_kv_heads}, n_picks)")
+    n_picks = picks.shape[2]
+    if ws is None:
+        with torch.cuda.stream(stream):        # belongs to the stream that uses it
+            ws = cb_paged_attention_picked_workspace(q, n_picks, shape[1], n_q_heads, n_kv_heads, head_dim)
+    query = _pack_query(q.data_ptr(), out.data_ptr(), _ld("q", q, dt, n_rows, cols), _ld("out", out, dt, n_rows, cols),
+                        ws.data_ptr(), ws.nbytes, n_rows, 0, n_q_heads, n_kv_heads, head_dim,
+                        1.0 / math.sqrt(head_dim) if scale is None else scale)
+    status = lib.cb_paged_attention_picked(kv, query, picks.data_ptr(), n_picks, _CODES.get(dt, -1),
+                                           _cur_stream(dev) if stream is None else stream.cuda_stream)
     if status:
         check(status)
 

@@ -35,6 +35,10 @@ SOURCES = [
     "k_paged_attn.cu",
     "k_paged_decode.cu",
     "k_paged_chunk.cu",
+    "k_paged4_rows.cu",
+    "k_paged4_attn.cu",
+    "k_paged_pages.cu",
+    "k_paged_picked.cu",
     "k_sample.cu",
 ]
 

@@ -395,6 +395,25 @@ void paged_attention_plan(int n_rows, int n_seq, int max_kv, int Hq, int Hkv, in
 // cudaErrorInvalidConfiguration: more tiles than one launch takes.
 cudaError_t launch_paged_attention(const PagedKV &kv, const cb_paged_query &query, cb_dtype dt, int *status,
                                    cudaStream_t s);
+
+// 4-bit cache; the geometry as a cb_paged_kv with byte strides.
+PagedKV paged4_plain_kv(const cb_paged4_kv &kv);
+cudaError_t launch_paged4_append(const cb_paged4_kv &kv, const cb_paged_rows &rows, cb_dtype dt, int *status,
+                                 cudaStream_t s);
+cudaError_t launch_paged4_gather(const cb_paged4_kv &kv, const cb_paged_rows_out &rows, cb_dtype dt, int *status,
+                                 cudaStream_t s);
+size_t paged4_attention_ws_bytes(int n_rows, int n_seq, int max_kv, int Hq, int Hkv, int hd, cb_dtype dt);
+cudaError_t launch_paged4_attention(const cb_paged4_kv &kv, const cb_paged_query &query, cb_dtype dt, int *status,
+                                    cudaStream_t s);
+
+// Page bounds, selection, attention over picked pages.
+cudaError_t launch_paged_bounds(const PagedKV &kv, const cb_page_bounds &b, cb_dtype dt, int *status, cudaStream_t s);
+size_t paged_select_ws_bytes(int n_rows, int max_kv, int page_size, int Hkv);
+cudaError_t launch_paged_select(const PagedKV &kv, const cb_page_bounds &b, const cb_page_select &a, cb_dtype dt,
+                                int *status, cudaStream_t s);
+size_t paged_picked_ws_bytes(int n_rows, int n_picks, int page_size, int Hq, int Hkv, int hd, cb_dtype dt);
+cudaError_t launch_paged_picked(const PagedKV &kv, const cb_paged_query &query, const int32_t *picks, int n_picks,
+                                cb_dtype dt, int *status, cudaStream_t s);
 cudaError_t launch_sample(const void *logits, int64_t ld, int n_rows, int vocab, cb_dtype dt,
                           const float *u, const float *temperature, const int32_t *top_k,
                           const float *top_p, const float *min_p, int32_t *tokens,

@@ -101,4 +101,48 @@ __device__ __forceinline__ void paged_find_tile(const PagedKV &kv, int n_rows, i
   __syncthreads();
 }
 
+// Calls place(x, n, i) in the first `rows` threads of the block, once or, where the
+// offsets are wrong, twice: thread t's row row0 + t is the i-th of the n rows of
+// sequence x (of none where i is not in [0, n)).  s_off: the call's offsets in
+// shared memory, *s_bad 0; every thread of the block calls it after a barrier, and
+// another one ends it.
+template <int NT, int ROWS, typename F>
+__device__ __forceinline__ void paged_find_rows(int S, int n_rows, int row0, int rows, const int *s_off, int *s_bad,
+                                                int *status, const F &place) {
+  // The first warp looks up the rows, the others look at every sequence: one
+  // whose offsets do not ascend may hold no row that a search ends in.
+  const int r = row0 + threadIdx.x;
+  if ((int)threadIdx.x < rows) {
+    // the last sequence that starts at or before r
+    int lo = 0, hi = S - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_off[mid] <= r) lo = mid; else hi = mid - 1;
+    }
+    place(lo, s_off[lo + 1] - s_off[lo], r - s_off[lo]);
+  }
+  for (int x = (int)threadIdx.x - ROWS; x < S; x += NT - ROWS)
+    if (x >= 0 && (s_off[x] < 0 || s_off[x + 1] < s_off[x] || s_off[x + 1] > n_rows)) *s_bad = 1;
+  __syncthreads();
+  if (*s_bad) {
+    // Once more: of the sequences whose offsets ascend from all before them,
+    // the one that holds r; rows of the others belong to none.
+    if (threadIdx.x == 0) report(status, CB_ERR_DEVICE_INDEX);
+    if ((int)threadIdx.x < rows) {
+      int seq = 0, n = 0, i = 0;
+      for (int x = 0, top = 0; x < S; ++x) {
+        const int a = s_off[x], b = s_off[x + 1];
+        if (a >= top && a <= r && r < b && b <= n_rows) {
+          seq = x;
+          n = b - a;
+          i = r - a;
+        }
+        top = max(top, max(a, b));
+      }
+      place(seq, n, i);
+    }
+    __syncthreads();
+  }
+}
+
 }  // namespace cb

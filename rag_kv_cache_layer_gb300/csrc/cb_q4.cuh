@@ -1,0 +1,141 @@
+// The 4-bit cache's format: 4-bit floats (sign, 2 exponent bits, 1 mantissa bit:
+// 0, 0.5, 1, 1.5, 2, 3, 4, 6) with one 8-bit float scale (4 exponent bits, 3
+// mantissa bits) for 16 consecutive dimensions of a head: 4.5 bits a value.
+//
+// A page holds its kv heads one after the other; a head's block is
+//   keys' codes [slot][hd / 2] | values' codes | keys' scales [slot][hd / 16] |
+//   values' scales,
+// so one head's part of a page is contiguous: the attention, which works head
+// by head, reads whole lines whatever the page size is.
+//
+// A product code * scale has at most 2 + 4 significant bits and lies between
+// 2^-10 and 2688: it is exact in fp16 (and in bf16).
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "cb_common.cuh"
+
+namespace cb {
+namespace q4 {
+
+constexpr int kGroup = 16;
+constexpr float kMinScale = 0x1p-9f;        // the smallest scale: never zero
+
+// Bytes of one head's block, and the places of its parts.
+__host__ __device__ constexpr int head_bytes(int page, int hd) { return page * (hd + hd / 8); }
+__host__ __device__ constexpr int codes_at(int page, int hd, bool v) { return v ? page * (hd / 2) : 0; }
+__host__ __device__ constexpr int scales_at(int page, int hd, bool v) { return page * hd + (v ? page * (hd / 16) : 0); }
+
+// Two codes of a byte, the low one first.
+__device__ __forceinline__ void decode8(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+// Two scales of 16 bits, the low one first, as fp16.
+__device__ __forceinline__ uint32_t decode_scales(uint32_t two) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 s;\n\tcvt.u16.u32 s, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, s;\n\t}" : "=r"(h) : "r"(two));
+  return h;
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t both(uint32_t h2, bool high) {
+  return high ? __byte_perm(h2, h2, 0x3232) : __byte_perm(h2, h2, 0x1010);
+}
+
+// x / s toward zero with a sticky last bit (x, s finite, s > 0, q = 0 or
+// normal): a further rounding to fewer bits then rounds the quotient itself.
+__device__ __forceinline__ float divide_odd(float x, float s, float inv) {
+  float q = x * inv;
+  q = fmaf(fmaf(-q, s, x), inv, q);                   // within one step of x / s
+  const float rest = fmaf(-q, s, x);                  // exact
+  if (rest == 0.f) return q;
+  uint32_t b = __float_as_uint(q);
+  if ((rest < 0.f) != (x < 0.f)) --b;                 // |q| was too large
+  return __uint_as_float(b | 1u);
+}
+
+// The scale of a group whose largest magnitude is a (as an 8-bit float): a / 6 to
+// the nearest, ties to even, within [2^-9, 448]; and its value.
+template <typename T>
+__device__ __forceinline__ uint32_t scale_of(float a, float &value) {
+  // bf16: a has 8 bits, so a / 6 is a border between two scales (5 bits) or at least
+  // 2^-9 of itself away from one, and its rounding to fp32 does not matter
+  const float r = sizeof(T) == 2 || !(a < 3e4f) || a < 1e-6f ? __fdiv_rn(a, 6.f) : divide_odd(a, 6.f, 1.f / 6.f);
+  uint32_t code;
+  asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n\tcvt.u32.u16 %0, t;\n\t}"
+      : "=r"(code) : "f"(0.f), "f"(r));
+  code = max(code & 0xffu, 1u);
+  value = __half2float(__ushort_as_half((unsigned short)(decode_scales(code) & 0xffffu)));
+  return code;
+}
+
+// Codes of 16 values x and their scale's code: codes[0] holds dimensions 0..7, the
+// lowest four bits the first.  Each value is the 4-bit float nearest to x / scale
+// (the quotient itself: ties go to the even code).
+template <typename T>
+__device__ __forceinline__ uint32_t quantise(float (&x)[kGroup], uint2 &codes) {
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < kGroup; ++i) a = fmaxf(a, fabsf(x[i]));
+  float s;
+  const uint32_t scale = scale_of<T>(a, s);
+  const float inv = 1.f / s;
+  if (a > 4096.f) {
+    // far above 6 * 448, where every value saturates: keeps infinities out of the
+    // quotient (NaN becomes a number too)
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) x[i] = fminf(fmaxf(x[i], -4096.f), 4096.f);
+  }
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < kGroup; i += 2) {
+    float q[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float v = x[i + k];
+      if (sizeof(T) == 2) {
+        // a border is met exactly (a quotient of 3 bits) or missed by 2^-9 of it
+        const float q0 = v * inv;
+        q[k] = fmaf(fmaf(-q0, s, v), inv, q0);
+      } else {
+        q[k] = fabsf(v) < 0.125f * s ? 0.f * v : divide_odd(v, s, inv);
+      }
+    }
+    uint32_t two;
+    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
+        : "=r"(two) : "f"(q[1]), "f"(q[0]));
+    w[i / 8] |= two << (4 * (i % 8));
+  }
+  codes = make_uint2(w[0], w[1]);
+  return scale;
+}
+
+// x a - y b (a, b fp32), correctly rounded to T up to 2^-46 of the larger product:
+// products and sum in pairs of floats, and an odd last bit in place of the rest where
+// T has fewer.
+template <typename T>
+__device__ __forceinline__ float turned(float x, float a, float y, float b) {
+  // (__fmul_rn: a product that a sum took into an fma would not be the rounded one)
+  const float h1 = __fmul_rn(x, a), l1 = fmaf(x, a, -h1), h2 = -__fmul_rn(y, b), l2 = fmaf(-y, b, -h2);
+  const float s = h1 + h2, t = s - h1;
+  const float e = (h1 - (s - t)) + (h2 - t) + (l1 + l2);
+  const float hi = s + e, lo = e - (hi - s);
+  if (sizeof(T) == 4) return hi;
+  uint32_t bits = __float_as_uint(hi);
+  if (lo != 0.f && hi != 0.f) {
+    if ((lo < 0.f) != (hi < 0.f)) --bits;
+    bits |= 1u;
+  }
+  return to_f(from_f<bf16>(__uint_as_float(bits)));
+}
+
+}  // namespace q4
+}  // namespace cb

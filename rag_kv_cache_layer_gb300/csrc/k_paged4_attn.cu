@@ -1,0 +1,581 @@
+// Attention over a paged cache of 4-bit floats, few rows per sequence.
+//
+// Work is cut as in the few-rows kernel of the 16-bit cache (cb_paged_line.cuh): a
+// tile is R = 8 NT rows of one sequence and kv head, its keys come in blocks of 32,
+// all blocks of all tiles form one line that the grid's blocks share in equal parts,
+// and decode_merge_kernel joins tiles that several parts hold.  The block's four
+// warps take a tile's key blocks in turn, each with a cp.async ring of its own.
+//
+// Mathematics.  A code times its scale is exact in fp16 (cb_q4.cuh), so keys and
+// values meet the tensor cores as fp16 without a rounding.  q is put into fp16 after
+// a power of two per row that brings its largest magnitude to [2^13, 2^14): a bf16 q
+// is then exact down to 2^-27 of that magnitude and off by at most 2^-39 of it
+// below.  P = 2^(x - m + 14) rounds to fp16 (2^-12 of itself, 2^-39 of the largest
+// weight at the bottom); both powers of two leave with the softmax scale and the
+// division by the sum.  fp32 rows take q and P as two fp16 halves (hi, lo with
+// 2^-22 and less dropped) and every step of 16 in a fresh accumulator that is added
+// in fp32, since the tensor core truncates its sums.
+//
+// Both products put the cache on the 16-row side of mma.m16n8k16 and the query rows
+// on the 8-column side: S^T = K Q^T, O^T = V^T P^T.  A group of up to 8 heads then
+// fills the instruction, and a lane's operand is made of neighbouring dimensions of
+// one key (K: 32, one 16-byte load and two scales) or of 16 dimensions of four keys
+// (V: four 8-byte loads), so that codes go from shared memory to fp16 pairs by one
+// conversion and one product with the scale for two values; V's pairs are two keys'
+// codes of one dimension, put into a byte by a shift and a select first.  S^T comes
+// out as P^T's operand up to a transposition of 8x8 blocks (movmatrix).
+#include "cb_common.cuh"
+#include "cb_internal.h"
+#include "cb_paged.cuh"
+#include "cb_paged_attn.cuh"
+#include "cb_paged_line.cuh"
+#include "cb_q4.cuh"
+
+namespace cb {
+namespace paged4 {
+
+using namespace paged;
+
+struct Params : AttnParams {
+  int head_bytes;                       // of one head's block of a page
+  float v_mul;                          // 2^v_exp
+};
+
+constexpr int kBN = 32;                 // keys per block
+constexpr float kPShift = 14.f;         // log2 of P at the running maximum
+
+template <int HD, int NT> struct Cfg {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kPerSm = NT == 4 ? 2 : 3, kStages = NT == 4 ? 4 : 3;
+  static constexpr int kCodes = kBN * HD / 2, kScales = kBN * HD / 16;
+  static constexpr int kOffV = kCodes, kOffKs = 2 * kCodes, kOffVs = kOffKs + kScales;
+  static constexpr int kStage = kOffVs + kScales;
+  static constexpr int kSmem = 4 * kStages * kStage;
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+// hi: the halves of (x, y) nearest in fp16; the result: what they leave.
+__device__ __forceinline__ uint32_t pack_rest(float x, float y, uint32_t hi) {
+  const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+  return pack_f16(x - h.x, y - h.y);
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+// W words from shared memory.
+template <int W> __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[W]) {
+  if constexpr (W == 4)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a) : "memory");
+  else if constexpr (W == 2)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a) : "memory");
+  else
+    w[0] = lds32(a);
+}
+// `bytes` bytes to shared memory and zeros up to 16.
+__device__ __forceinline__ void copy_part(uint32_t dst, const void *src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+template <typename T, int HD, int NT>
+__global__ void __launch_bounds__(kDecThreads, Cfg<HD, NT>::kPerSm)
+paged4_few_kernel(const __grid_constant__ Params P, int *status) {
+  typedef Cfg<HD, NT> C;
+  constexpr bool F32 = std::is_same<T, float>::value;
+  constexpr int R = C::kRows, NS = C::kStages, KS = HD / 16, MT = HD / 16;
+  // words of codes that a lane takes of a key (K: HD / 4 dimensions; V: HD / 8)
+  constexpr int KW = HD / 32, VW = HD / 64;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ Line line;
+  __shared__ int64_t s_sums[kDecThreads / 32];
+  __shared__ float2 s_ml[4 * R];                // (m, l) of each warp's rows
+  grid_dep_wait();
+  grid_dep_launch();
+  make_line(P, R, kBN, gridDim.x, line, s_sums, status);
+  Join *const join = P.joins + blockIdx.x;
+  if ((int)blockIdx.x >= line.parts) {
+    if (threadIdx.x == 0) join->rows = 0;
+    return;
+  }
+  const int64_t u0 = part_begin(line, blockIdx.x), u1 = part_begin(line, blockIdx.x + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, q4 = lane & 3;
+  const uint32_t ring = smem_u32(smem) + warp * NS * C::kStage;
+  const int page_size = P.kv.page_size, shift = __ffs(page_size) - 1;
+  const uint8_t *const pool = reinterpret_cast<const uint8_t *>(P.kv.k_pages);
+
+  int s = seq_of(line, P.kv.n_seq, u0);
+  for (int64_t u = u0; u < u1;) {
+    // this piece: a tile of sequence s and kv head g, its blocks [jb, je) (as in paged_decode_kernel)
+    while (line.blocks[s] == 0 || (s + 1 < P.kv.n_seq && line.begin[s + 1] <= u)) ++s;
+    const int row0 = __ldg(P.kv.row_offsets + s), n = __ldg(P.kv.row_offsets + s + 1) - row0;
+    const int kv = __ldg(P.kv.kv_lens + s), base = kv - n, all = n * P.G, tiles = (all - 1) / R + 1;
+    int64_t local = u - line.begin[s];
+    int nbs = line.blocks[s], g, jb, l0 = 0;
+    const int64_t pairs = (int64_t)(tiles / 2) * P.by_quads.d * nbs;
+    if (local >= pairs) {                       // the only tile, or an odd middle one
+      if (tiles > 1) {
+        l0 = tiles / 2 * R;
+        nbs = blocks_seen(P, base, l0 + R - 1, kBN);
+      }
+      divide(local - pairs, nbs, g, jb);
+    } else {
+      divide(local, nbs, g, jb);
+      const int q = P.by_quads.div(g), late = blocks_seen(P, base, min((tiles - q) * R, all) - 1, kBN);
+      g -= q * (int)P.by_quads.d;
+      if (jb < late) {
+        nbs = late;
+        l0 = (tiles - 1 - q) * R;
+      } else {
+        nbs -= late;
+        jb -= late;
+        l0 = q * R;
+      }
+    }
+    const int rows = min(R, all - l0);
+    const int take = (int)min((int64_t)(nbs - jb), u1 - u);
+    const bool whole = jb == 0 && take == nbs, first = u == u0;
+    const int64_t item_end = u - jb + nbs;
+    u += take;
+    const int seen = base + P.by_G.div(l0 + rows - 1) + 1;    // keys the tile's last row sees
+    const int je = min(jb + take, seen > 0 ? (seen - 1) / kBN + 1 : 0);
+    const int sure = base + P.by_G.div(l0);                   // every row sees the keys up to this one
+    const int32_t *table = P.kv.block_table + (int64_t)s * P.kv.ld_table;
+    if (threadIdx.x == 0 && u == u1)            // the last piece: the one that may go on in the next part
+      *join = Join{row0, l0, jb == 0 && item_end > u1 ? rows : 0, g, part_of(line, item_end - 1), first ? 0 : 1};
+
+    auto fetch = [&](int j) -> int {            // page of key j * 32 + lane
+      const int key = j * kBN + lane;
+      return j < je && key < kv ? __ldg(table + (key >> shift)) : -1;
+    };
+    const uint8_t *const head = pool + (int64_t)g * P.head_bytes;
+    auto load = [&](int j, int st, int page) {
+      const uint32_t dst = ring + st * C::kStage;
+      const int key0 = j * kBN, left = kv - key0;             // keys from key0 on
+      if (lane < left && (page < 0 || page >= P.kv.n_pages)) {
+        report(status, CB_ERR_DEVICE_INDEX);
+        page = -1;
+      }
+      // Codes: a warp copies 512 bytes at once, 1024 / HD keys: a group of eight
+      // keys lies in one page (page_size >= 8).  The values' 16-byte columns are
+      // swizzled by the key (bit 1) so that the fragments' loads meet all banks.
+      constexpr int kCols = HD / 32, kKeys = 32 / kCols;
+      const int crow = lane / kCols, ccol = lane % kCols;
+#pragma unroll
+      for (int i = 0; i < kBN / kKeys; ++i) {
+        const int r = i * kKeys + crow, pg = __shfl_sync(0xffffffffu, page, kKeys == 8 ? i * 8 : r);
+        const int slot = (key0 + r) & (page_size - 1);
+        const bool there = pg >= 0 && r < left;
+        const uint8_t *src = head + (there ? pg * P.kv.page_stride + slot * (HD / 2) + ccol * 16 : 0);
+        const uint32_t d = dst + r * (HD / 2);
+        copy16(d + ccol * 16, src, there);
+        const int vcol = HD == 128 ? ccol ^ (r & 2) : ccol;
+        copy16(d + C::kOffV + vcol * 16, src + (there ? q4::codes_at(page_size, HD, true) : 0), there);
+      }
+      // Scales: 16 bytes are 256 / HD keys'; lanes 0..15 the keys', 16..31 the values'.
+      constexpr int kPer = 256 / HD, kChunks = kBN / kPer;    // keys a chunk; chunks
+      const int c = lane & 15, r = min(c, kChunks - 1) * kPer, pg = __shfl_sync(0xffffffffu, page, r);
+      if (c < kChunks) {
+        const bool v = lane >= 16;
+        const int slot = (key0 + r) & (page_size - 1);
+        const int bytes = pg < 0 ? 0 : max(0, min(16, (left - r) * (HD / 16)));
+        copy_part(dst + (v ? C::kOffVs : C::kOffKs) + c * 16,
+                  head + (bytes ? pg * P.kv.page_stride + q4::scales_at(page_size, HD, v) + slot * (HD / 16) : 0), bytes);
+      }
+    };
+    auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+
+    // the table is read kAhead blocks further ahead than the pages
+    constexpr int kAhead = 3;
+    int ahead[kAhead], from = jb + warp;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) ahead[i] = fetch(from + i * 4);
+    auto next_page = [&]() -> int {
+      const int page = ahead[0];
+#pragma unroll
+      for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
+      ahead[kAhead - 1] = fetch(from + kAhead * 4);
+      from += 4;
+      return page;
+    };
+#pragma unroll 1
+    for (int i = 0; i < NS - 1; ++i) {
+      const int j = from, page = next_page();
+      if (j < je) load(j, i, page);
+      commit();
+    }
+    // q: column gid of tile nt is row nt * 8 + gid; k-step k takes dimensions
+    // HD / 4 * q4 + 4 k .. + 3 of it
+    uint32_t qh[NT][KS][2], ql[F32 ? NT : 1][F32 ? KS : 1][2];
+    float sl[NT][2];                            // log2 scale of this lane's two score columns
+    int pos[NT][2];                             // their positions, -1: no row
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + gid, qi = P.by_G.div(l0 + r);
+      const T *src = reinterpret_cast<const T *>(P.q) + (int64_t)(row0 + qi) * P.ld_q +
+                     (int64_t)(g * P.G + l0 + r - qi * P.G) * HD + q4 * (HD / 4);
+      float x[HD / 4];
+      constexpr int VEC = 16 / sizeof(T);
+#pragma unroll
+      for (int i = 0; i < HD / 4; i += VEC) {
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (r < rows) raw = ldg16(src + i);
+        const T *e = reinterpret_cast<const T *>(&raw);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) x[i + k] = to_f(e[k]);
+      }
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < HD / 4; ++i) top = fmaxf(top, fabsf(x[i]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^up brings top to [2^13, 2^14); in two factors, since 2^up may exceed fp32
+      const int up = top > 0.f ? 13 - ilogbf(top) : 0;
+      const float f1 = ldexpf(1.f, up / 2), f2 = ldexpf(1.f, up - up / 2);
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float y0 = x[4 * k + 2 * c] * f1 * f2, y1 = x[4 * k + 2 * c + 1] * f1 * f2;
+          qh[nt][k][c] = pack_f16(y0, y1);
+          if constexpr (F32) ql[nt][k][c] = pack_rest(y0, y1, qh[nt][k][c]);
+        }
+      // scores of this lane are of rows nt * 8 + 2 q4 and + 1, whose q lanes 8 q4 and 8 q4 + 4 have
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int rc = nt * 8 + 2 * q4 + e, down = -__shfl_sync(0xffffffffu, up, 8 * q4 + 4 * e);
+        sl[nt][e] = P.scale_log2 * ldexpf(1.f, down / 2) * ldexpf(1.f, down - down / 2);
+        pos[nt][e] = rc < rows ? base + P.by_G.div(l0 + rc) : -1;
+      }
+    }
+    float o[MT][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[nt][e] = -INFINITY;
+        l[nt][e] = 0.f;
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[t][nt][k] = 0.f;
+    }
+    // Row i of a score tile of 16 keys is key (i & 8) + (i & 7) / 2 + 4 (i & 1): the
+    // four keys whose values a lane needs then are q4, q4 + 4, q4 + 8, q4 + 12.
+    const int krow = (gid >> 1) + 4 * (gid & 1);
+    int st = 0, fill = NS - 1;
+    for (int j = jb + warp; j < je; j += 4) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
+      __syncwarp();                             // landed for every lane; the stage before is used up
+      {
+        const int jn = from, page = next_page();
+        if (jn < je) load(jn, fill, page);
+        commit();
+        fill = fill + 1 == NS ? 0 : fill + 1;
+      }
+      const uint32_t stage = ring + st * C::kStage;
+      st = st + 1 == NS ? 0 : st + 1;
+      float x[2][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[mt][nt][k] = 0.f;
+        uint32_t w[2][KW], sc[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int key = mt * 16 + 8 * h + krow;
+          lds_words<KW>(stage + key * (HD / 2) + q4 * (HD / 8), w[h]);
+          const uint32_t at = stage + C::kOffKs + key * (HD / 16) + q4 * (HD / 64);
+          sc[h] = q4::decode_scales(HD == 128 ? lds16(at) : lds8(at));
+        }
+#pragma unroll
+        for (int i = 0; i < KW; ++i) {
+          uint32_t a[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            q4::decode8(w[h][i], a[h]);
+            const uint32_t scale = q4::both(sc[h], i >= 2);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) a[h][b] = q4::mul2(a[h][b], scale);
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t f[4] = {a[0][2 * c], a[1][2 * c], a[0][2 * c + 1], a[1][2 * c + 1]};
+            const int k = 2 * i + c;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (F32) {
+                float t[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16(t, f, ql[nt][k][0], ql[nt][k][1]);
+                mma_f16(t, f, qh[nt][k][0], qh[nt][k][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[mt][nt][e] += t[e];
+              } else {
+                mma_f16(x[mt][nt], f, qh[nt][k][0], qh[nt][k][1]);
+              }
+            }
+          }
+        }
+      }
+      const int key0 = j * kBN;
+      float mx[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
+      const bool clear = key0 + kBN - 1 <= sure;              // no masking (columns without a row do not matter)
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int key = key0 + mt * 16 + (k >> 1) * 8 + krow;
+            x[mt][nt][k] = clear || key <= pos[nt][k & 1] ? x[mt][nt][k] * sl[nt][k & 1] : -INFINITY;
+            mx[nt][k & 1] = fmaxf(mx[nt][k & 1], x[mt][nt][k]);
+          }
+      bool moved = false;
+      float corr[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], d));
+          const float mn = fmaxf(m[nt][e], mx[nt][e]);
+          corr[nt][e] = mn == m[nt][e] ? 1.f : ex2(m[nt][e] - mn);      // also where both are -inf
+          moved |= mn != m[nt][e];
+          m[nt][e] = mn;
+          l[nt][e] *= corr[nt][e];
+        }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[t][nt][k] *= corr[nt][k & 1];
+      }
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t ph[NT][2], pl[F32 ? NT : 1][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float p[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float v = x[mt][nt][2 * h + e];
+              p[e] = v == -INFINITY ? 0.f : ex2(v - (m[nt][e] - kPShift));
+              l[nt][e] += p[e];
+            }
+            const uint32_t hi = pack_f16(p[0], p[1]);
+            ph[nt][h] = transposed(hi);
+            if constexpr (F32) pl[nt][h] = transposed(pack_rest(p[0], p[1], hi));
+          }
+        // values of keys q4 + 4 i; pairs (i = 0, 1) and (2, 3)
+        uint32_t w[4][VW], sc[2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = mt * 16 + q4 + 4 * i;
+          const int col = HD == 128 ? ((gid >> 1) ^ (key & 2)) * 16 + (gid & 1) * 8 : gid * 4;
+          lds_words<VW>(stage + C::kOffV + key * (HD / 2) + col, w[i]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t at = stage + C::kOffVs + (mt * 16 + q4 + 8 * h) * (HD / 16) + gid * HD / 128;
+          sc[h] = q4::decode_scales(lds8(at) | lds8(at + 4 * (HD / 16)) << 8);
+        }
+#pragma unroll
+        for (int i = 0; i < VW; ++i) {
+          uint32_t even[2][4], odd[2][4];       // (key, key + 4) of dimensions 2 t and 2 t + 1
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a = w[2 * h][i], b = w[2 * h + 1][i];
+            q4::decode8((a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u), even[h]);
+            q4::decode8(((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u), odd[h]);
+          }
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t f[4] = {q4::mul2(even[0][t], sc[0]), q4::mul2(odd[0][t], sc[0]),
+                                   q4::mul2(even[1][t], sc[1]), q4::mul2(odd[1][t], sc[1])};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float (&acc)[4] = o[i * 4 + t][nt];
+              if constexpr (F32) {
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16(c, f, pl[nt][0], pl[nt][1]);
+                mma_f16(c, f, ph[nt][0], ph[nt][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[e] += c[e];
+              } else {
+                mma_f16(acc, f, ph[nt][0], ph[nt][1]);
+              }
+            }
+          }
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
+        if (gid == 0) s_ml[warp * R + nt * 8 + 2 * q4 + e] = make_float2(m[nt][e], l[nt][e]);
+      }
+    __syncthreads();                            // the rings are used up
+    // Every warp leaves its O in rows of HD + 4 floats, then the four states join.
+    constexpr int LD = HD + 4;
+    static_assert(4 * R * LD * 4 <= C::kSmem, "the warps' O fit the rings");
+    float *so = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float2 *>(so + (warp * R + nt * 8 + 2 * q4 + e) * LD + gid * (HD / 8) + 2 * t) =
+              make_float2(o[t][nt][e], o[t][nt][2 + e]);
+    __syncthreads();
+    const int64_t slot = (2 * (int64_t)blockIdx.x + (first ? 0 : 1)) * R;
+    for (int i = threadIdx.x; i < rows * (HD / 4); i += kDecThreads) {
+      const int r = i / (HD / 4), c = i % (HD / 4) * 4;
+      float M = -INFINITY, L = 0.f;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) M = fmaxf(M, s_ml[k * R + r].x);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 ml = s_ml[k * R + r];
+        const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+        const float4 v = *reinterpret_cast<const float4 *>(so + (k * R + r) * LD + c);
+        L += w * ml.y;
+        a.x += w * v.x; a.y += w * v.y; a.z += w * v.z; a.w += w * v.w;
+      }
+      a.x *= P.v_mul; a.y *= P.v_mul; a.z *= P.v_mul; a.w *= P.v_mul;
+      if (!whole) {
+        *reinterpret_cast<float4 *>(P.part_o + (slot + r) * HD + c) = a;
+        if (c == 0) P.part_ml[slot + r] = make_float2(M, L);
+      } else {
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const int qi = P.by_G.div(l0 + r);
+        T *dst = reinterpret_cast<T *>(P.out) + (int64_t)(row0 + qi) * P.ld_out +
+                 (int64_t)(g * P.G + l0 + r - qi * P.G) * HD + c;
+        if constexpr (F32)
+          *reinterpret_cast<float4 *>(dst) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+        else
+          *reinterpret_cast<uint2 *>(dst) =
+              make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+      }
+    }
+    __syncthreads();                            // before the next piece fills the rings
+  }
+}
+
+// ------------------------------------------------------------------ plan --
+struct Plan {
+  int nt, grid;                         // score columns / 8 per tile; blocks
+};
+
+static Plan plan(int64_t n_rows, int S, int G) {
+  const int64_t per_seq = (n_rows * G + S - 1) / S;
+  Plan p;
+  p.nt = per_seq <= 8 ? 1 : per_seq <= 16 ? 2 : 4;
+  p.grid = device_sm_count() * (p.nt == 4 ? 2 : 3);
+  return p;
+}
+static size_t plan_bytes(const Plan &p, int hd) {
+  return 2ull * p.grid * 8 * p.nt * (hd * sizeof(float) + sizeof(float2)) + p.grid * sizeof(Join);
+}
+
+template <typename T, int HD, int NT>
+static cudaError_t run(const Params &P, int grid, int *status, cudaStream_t s) {
+  typedef Cfg<HD, NT> C;
+  static PerDeviceOnce attr;
+  cudaError_t e = attr.run([](int) {
+    return cudaFuncSetAttribute(paged4_few_kernel<T, HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(paged4_few_kernel<T, HD, NT>, dim3(grid), dim3(kDecThreads), C::kSmem, s, P, status);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(decode_merge_kernel<T, HD>, dim3(grid, C::kRows / kJoinRows), dim3(kJoinThreads),
+                 grid * kJoinRows * sizeof(float2), s, static_cast<const AttnParams &>(P), C::kRows);
+  return e == cudaSuccess ? launched(2) : e;
+}
+
+template <typename T, int HD>
+static cudaError_t run_rows(const Params &P, const Plan &p, int *status, cudaStream_t s) {
+  return p.nt == 1 ? run<T, HD, 1>(P, p.grid, status, s)
+         : p.nt == 2 ? run<T, HD, 2>(P, p.grid, status, s) : run<T, HD, 4>(P, p.grid, status, s);
+}
+
+}  // namespace paged4
+
+size_t paged4_attention_ws_bytes(int n_rows, int n_seq, int max_kv, int Hq, int Hkv, int hd, cb_dtype) {
+  if (n_rows <= 0 || n_seq <= 0) return 0;
+  return paged4::plan_bytes(paged4::plan(n_rows, n_seq, Hq / Hkv), hd);
+}
+
+cudaError_t launch_paged4_attention(const cb_paged4_kv &kv, const cb_paged_query &a, cb_dtype dt, int *status,
+                                    cudaStream_t s) {
+  using namespace paged4;
+  const int G = a.n_q_heads / a.n_kv_heads;
+  const Plan p = plan(a.n_rows, kv.n_seq, G);
+  Params P;
+  P.kv = paged4_plain_kv(kv);
+  P.q = a.q;
+  P.out = a.out;
+  P.ld_q = a.ld_q;
+  P.ld_out = a.ld_out;
+  P.n_rows = a.n_rows;
+  P.G = G;
+  P.Hkv = a.n_kv_heads;
+  P.max_kv = a.max_kv_len;
+  P.n_split = 1;
+  P.few_hi = 0x7fffffff;
+  P.rows_lo = 0;
+  P.hc = 1;
+  P.by_G = Divisor(G);
+  P.by_quads = Divisor(a.n_kv_heads);
+  P.scale_log2 = a.scale * 1.4426950408889634f * ldexpf(1.f, kv.k_exp);
+  P.head_bytes = q4::head_bytes(kv.page_size, a.head_dim);
+  P.v_mul = ldexpf(1.f, kv.v_exp);
+  const int64_t partials = 2LL * p.grid * 8 * p.nt;
+  P.part_o = reinterpret_cast<float *>(a.ws);
+  P.part_ml = reinterpret_cast<float2 *>(P.part_o + partials * a.head_dim);
+  P.joins = reinterpret_cast<Join *>(P.part_ml + partials);
+  if (dt == CB_BF16)
+    return a.head_dim == 128 ? run_rows<bf16, 128>(P, p, status, s) : run_rows<bf16, 64>(P, p, status, s);
+  return a.head_dim == 128 ? run_rows<float, 128>(P, p, status, s) : run_rows<float, 64>(P, p, status, s);
+}
+
+}  // namespace cb

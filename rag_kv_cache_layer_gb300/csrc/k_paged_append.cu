@@ -78,40 +78,7 @@ paged_append_kernel(const __grid_constant__ AppendParams P, int *status) {
     s_pos[threadIdx.x] = pos;
     s_dst[threadIdx.x] = dst;
   };
-  // The first warp looks up the rows, the others look at every sequence: one
-  // whose offsets do not ascend may hold no row that a search ends in.
-  const int r = row0 + threadIdx.x;
-  if ((int)threadIdx.x < rows) {
-    // the last sequence that starts at or before r
-    int lo = 0, hi = S - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s_off[mid] <= r) lo = mid; else hi = mid - 1;
-    }
-    place(lo, s_off[lo + 1] - s_off[lo], r - s_off[lo]);
-  }
-  for (int x = (int)threadIdx.x - kAppendRows; x < S; x += kAppendThreads - kAppendRows)
-    if (x >= 0 && (s_off[x] < 0 || s_off[x + 1] < s_off[x] || s_off[x + 1] > P.n_rows)) s_bad = 1;
-  __syncthreads();
-  if (s_bad) {
-    // Once more: of the sequences whose offsets ascend from all before them,
-    // the one that holds r; rows of the others belong to none.
-    if (threadIdx.x == 0) report(status, CB_ERR_DEVICE_INDEX);
-    if ((int)threadIdx.x < rows) {
-      int seq = 0, n = 0, i = 0;
-      for (int x = 0, top = 0; x < S; ++x) {
-        const int a = s_off[x], b = s_off[x + 1];
-        if (a >= top && a <= r && r < b && b <= P.n_rows) {
-          seq = x;
-          n = b - a;
-          i = r - a;
-        }
-        top = max(top, max(a, b));
-      }
-      place(seq, n, i);
-    }
-    __syncthreads();
-  }
+  paged_find_rows<kAppendThreads, kAppendRows>(S, P.n_rows, row0, rows, s_off, &s_bad, status, place);
   const int layer = blockIdx.y;
   const T *kn = reinterpret_cast<const T *>(P.k) + layer * P.new_stride_k;
   const T *vn = reinterpret_cast<const T *>(P.v) + layer * P.new_stride_v;
