@@ -75,8 +75,9 @@ __device__ __forceinline__ int blocks_seen(const AttnParams &P, int base, int l,
 }
 
 // Every thread of the block calls it; one round of loads, one block scan.
+// pad: empty units behind each tile's blocks, for what a tile costs beyond them.
 __device__ __forceinline__ void make_line(const AttnParams &P, int R, int BN, int grid, Line &L, int64_t *warp_sums,
-                                          int *status) {
+                                          int *status, int pad = 0) {
   constexpr int NT = kDecThreads;
   const int per = (P.kv.n_seq + NT - 1) / NT, i0 = threadIdx.x * per, i1 = min(i0 + per, P.kv.n_seq);
   int64_t sum = 0;
@@ -89,12 +90,12 @@ __device__ __forceinline__ void make_line(const AttnParams &P, int R, int BN, in
       if (len < 0 || len > P.max_kv || len > (int64_t)P.kv.max_pages * P.kv.page_size)
         report(status, CB_ERR_DEVICE_INDEX);
       else if (tiles == 1)
-        units = pair = blocks_seen(P, len - n, n * P.G - 1, BN);
+        units = pair = blocks_seen(P, len - n, n * P.G - 1, BN) + pad;
       else {
         // each of a pair's two counts is within one of a linear function of
         // the tile, and those add up to the same in every pair
-        pair = blocks_seen(P, len - n, R - 1, BN) + blocks_seen(P, len - n, tiles * R - 1, BN) + 2;
-        units = tiles & 1 ? blocks_seen(P, len - n, (tiles / 2 + 1) * R - 1, BN) : 0;
+        pair = blocks_seen(P, len - n, R - 1, BN) + blocks_seen(P, len - n, tiles * R - 1, BN) + 2 + 2 * pad;
+        units = tiles & 1 ? blocks_seen(P, len - n, (tiles / 2 + 1) * R - 1, BN) + pad : 0;
       }
     }
     L.blocks[i] = pair;

@@ -46,8 +46,12 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
   return *reinterpret_cast<const uint32_t *>(&r);
 }
+// (v, v) of a pair's low or high half.
 __device__ __forceinline__ uint32_t both(uint32_t h2, bool high) {
-  return high ? __byte_perm(h2, h2, 0x3232) : __byte_perm(h2, h2, 0x1010);
+  uint32_t r;
+  if (high) asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {h, h};\n\t}" : "=r"(r) : "r"(h2));
+  else asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(r) : "r"(h2));
+  return r;
 }
 
 // x / s toward zero with a sticky last bit (x, s finite, s > 0, q = 0 or

@@ -39,14 +39,16 @@ using namespace paged;
 struct Params : AttnParams {
   int head_bytes;                       // of one head's block of a page
   float v_mul;                          // 2^v_exp
+  int pad;                              // units that a tile counts beyond its blocks
 };
 
 constexpr int kBN = 32;                 // keys per block
+constexpr int kPad = 12;
 constexpr float kPShift = 14.f;         // log2 of P at the running maximum
 
-template <int HD, int NT> struct Cfg {
+template <int HD, int NT, bool F32> struct Cfg {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kPerSm = NT == 4 ? 2 : 3, kStages = NT == 4 ? 4 : 3;
+  static constexpr int kPerSm = NT == 4 || F32 ? 2 : NT == 2 ? 3 : 4, kStages = NT == 4 || F32 ? 4 : NT == 2 ? 3 : 2;
   static constexpr int kCodes = kBN * HD / 2, kScales = kBN * HD / 16;
   static constexpr int kOffV = kCodes, kOffKs = 2 * kCodes, kOffVs = kOffKs + kScales;
   static constexpr int kStage = kOffVs + kScales;
@@ -54,15 +56,22 @@ template <int HD, int NT> struct Cfg {
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// the same from c = 0
+__device__ __forceinline__ void mma_f16_new(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -98,16 +107,24 @@ template <int W> __device__ __forceinline__ void lds_words(uint32_t a, uint32_t 
   else
     w[0] = lds32(a);
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ void copy_all(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 // `bytes` bytes to shared memory and zeros up to 16.
 __device__ __forceinline__ void copy_part(uint32_t dst, const void *src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
 template <typename T, int HD, int NT>
-__global__ void __launch_bounds__(kDecThreads, Cfg<HD, NT>::kPerSm)
+__global__ void __launch_bounds__(kDecThreads, (Cfg<HD, NT, std::is_same<T, float>::value>::kPerSm))
 paged4_few_kernel(const __grid_constant__ Params P, int *status) {
-  typedef Cfg<HD, NT> C;
   constexpr bool F32 = std::is_same<T, float>::value;
+  typedef Cfg<HD, NT, F32> C;
   constexpr int R = C::kRows, NS = C::kStages, KS = HD / 16, MT = HD / 16;
   // words of codes that a lane takes of a key (K: HD / 4 dimensions; V: HD / 8)
   constexpr int KW = HD / 32, VW = HD / 64;
@@ -117,12 +134,10 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
   __shared__ float2 s_ml[4 * R];                // (m, l) of each warp's rows
   grid_dep_wait();
   grid_dep_launch();
-  make_line(P, R, kBN, gridDim.x, line, s_sums, status);
+  make_line(P, R, kBN, gridDim.x, line, s_sums, status, P.pad);
   Join *const join = P.joins + blockIdx.x;
-  if ((int)blockIdx.x >= line.parts) {
-    if (threadIdx.x == 0) join->rows = 0;
-    return;
-  }
+  if (threadIdx.x == 0) join->rows = 0;
+  if ((int)blockIdx.x >= line.parts) return;
   const int64_t u0 = part_begin(line, blockIdx.x), u1 = part_begin(line, blockIdx.x + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, q4 = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * NS * C::kStage;
@@ -141,12 +156,12 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
     if (local >= pairs) {                       // the only tile, or an odd middle one
       if (tiles > 1) {
         l0 = tiles / 2 * R;
-        nbs = blocks_seen(P, base, l0 + R - 1, kBN);
+        nbs = blocks_seen(P, base, l0 + R - 1, kBN) + P.pad;
       }
       divide(local - pairs, nbs, g, jb);
     } else {
       divide(local, nbs, g, jb);
-      const int q = P.by_quads.div(g), late = blocks_seen(P, base, min((tiles - q) * R, all) - 1, kBN);
+      const int q = P.by_quads.div(g), late = blocks_seen(P, base, min((tiles - q) * R, all) - 1, kBN) + P.pad;
       g -= q * (int)P.by_quads.d;
       if (jb < late) {
         nbs = late;
@@ -159,27 +174,52 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
     }
     const int rows = min(R, all - l0);
     const int take = (int)min((int64_t)(nbs - jb), u1 - u);
-    const bool whole = jb == 0 && take == nbs, first = u == u0;
-    const int64_t item_end = u - jb + nbs;
+    const int real = blocks_seen(P, base, l0 + rows - 1, kBN);   // of the tile's units, the others are padding
+    const int64_t item_end = u - jb + real;
+    const bool whole = jb == 0 && item_end <= u1, first = u == u0;
     u += take;
+    if (jb >= real) continue;                   // nothing but padding
     const int seen = base + P.by_G.div(l0 + rows - 1) + 1;    // keys the tile's last row sees
-    const int je = min(jb + take, seen > 0 ? (seen - 1) / kBN + 1 : 0);
+    const int je = min(jb + take, seen > 0 ? real : 0);
     const int sure = base + P.by_G.div(l0);                   // every row sees the keys up to this one
     const int32_t *table = P.kv.block_table + (int64_t)s * P.kv.ld_table;
-    if (threadIdx.x == 0 && u == u1)            // the last piece: the one that may go on in the next part
-      *join = Join{row0, l0, jb == 0 && item_end > u1 ? rows : 0, g, part_of(line, item_end - 1), first ? 0 : 1};
+    if (threadIdx.x == 0 && jb == 0 && item_end > u1)   // goes on in the next part (no more pieces here)
+      *join = Join{row0, l0, rows, g, part_of(line, item_end - 1), first ? 0 : 1};
 
     auto fetch = [&](int j) -> int {            // page of key j * 32 + lane
       const int key = j * kBN + lane;
       return j < je && key < kv ? __ldg(table + (key >> shift)) : -1;
     };
     const uint8_t *const head = pool + (int64_t)g * P.head_bytes;
+    // places of this lane's 16 bytes of a stage's values and scales; a 16-byte column of
+    // the values is swizzled by the key's bit 1 (see below)
+    const bool one_page = page_size >= kBN;
+    const uint32_t vdst = C::kOffV + (HD == 128 ? (lane & ~3) * 16 + ((lane & 3) ^ ((lane >> 2) & 2)) * 16 : lane * 16);
+    constexpr int kHalf = C::kScales / 16;      // lanes that copy the keys' scales
+    const uint32_t sdst = C::kOffKs + lane * 16;
+    const int ssrc = lane < kHalf ? q4::scales_at(page_size, HD, false) + lane * 16
+                                  : q4::scales_at(page_size, HD, true) + (lane - kHalf) * 16;
     auto load = [&](int j, int st, int page) {
       const uint32_t dst = ring + st * C::kStage;
       const int key0 = j * kBN, left = kv - key0;             // keys from key0 on
       if (lane < left && (page < 0 || page >= P.kv.n_pages)) {
         report(status, CB_ERR_DEVICE_INDEX);
         page = -1;
+      }
+      // A whole block inside one page: everything lies at fixed distances.
+      if (one_page && left >= kBN) {
+        const int pg = __shfl_sync(0xffffffffu, page, 0), slot = key0 & (page_size - 1);
+        if (pg >= 0) {
+          const uint8_t *src = head + pg * P.kv.page_stride + slot * (HD / 2) + lane * 16;
+          const uint8_t *vsrc = src + q4::codes_at(page_size, HD, true);
+#pragma unroll
+          for (int i = 0; i < C::kCodes / 512; ++i) {
+            copy_all(dst + lane * 16 + i * 512, src + i * 512);
+            copy_all(dst + vdst + i * 512, vsrc + i * 512);
+          }
+          if (HD == 128 || lane < 16) copy_all(dst + sdst, head + pg * P.kv.page_stride + ssrc + slot * (HD / 16));
+          return;
+        }
       }
       // Codes: a warp copies 512 bytes at once, 1024 / HD keys: a group of eight
       // keys lies in one page (page_size >= 8).  The values' 16-byte columns are
@@ -269,7 +309,8 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int rc = nt * 8 + 2 * q4 + e, down = -__shfl_sync(0xffffffffu, up, 8 * q4 + 4 * e);
-        sl[nt][e] = P.scale_log2 * ldexpf(1.f, down / 2) * ldexpf(1.f, down - down / 2);
+        // above 0, so that a masked -inf stays one; a smaller scale leaves every weight at 1 too
+        sl[nt][e] = fmaxf(P.scale_log2 * ldexpf(1.f, down / 2) * ldexpf(1.f, down - down / 2), 0x1p-126f);
         pos[nt][e] = rc < rows ? base + P.by_G.div(l0 + rc) : -1;
       }
     }
@@ -304,10 +345,6 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
       float x[2][NT][4];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[mt][nt][k] = 0.f;
         uint32_t w[2][KW], sc[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -333,11 +370,13 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               if constexpr (F32) {
-                float t[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_f16(t, f, ql[nt][k][0], ql[nt][k][1]);
+                float t[4];
+                mma_f16_new(t, f, ql[nt][k][0], ql[nt][k][1]);
                 mma_f16(t, f, qh[nt][k][0], qh[nt][k][1]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[mt][nt][e] += t[e];
+                for (int e = 0; e < 4; ++e) x[mt][nt][e] = k == 0 ? t[e] : x[mt][nt][e] + t[e];
+              } else if (k == 0) {
+                mma_f16_new(x[mt][nt], f, qh[nt][k][0], qh[nt][k][1]);
               } else {
                 mma_f16(x[mt][nt], f, qh[nt][k][0], qh[nt][k][1]);
               }
@@ -347,19 +386,22 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
       }
       const int key0 = j * kBN;
       float mx[NT][2];
+      // no masking where every row sees the block (columns without a row do not matter)
+      const bool clear = key0 + kBN - 1 <= sure;
+      if (!clear) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
-      const bool clear = key0 + kBN - 1 <= sure;              // no masking (columns without a row do not matter)
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int k = 0; k < 4; ++k)
+              if (key0 + mt * 16 + (k >> 1) * 8 + krow > pos[nt][k & 1]) x[mt][nt][k] = -INFINITY;
+      }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int key = key0 + mt * 16 + (k >> 1) * 8 + krow;
-            x[mt][nt][k] = clear || key <= pos[nt][k & 1] ? x[mt][nt][k] * sl[nt][k & 1] : -INFINITY;
-            mx[nt][k & 1] = fmaxf(mx[nt][k & 1], x[mt][nt][k]);
-          }
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          mx[nt][e] = fmaxf(max3(x[0][nt][e], x[0][nt][2 + e], x[1][nt][e]), x[1][nt][2 + e]);
       bool moved = false;
       float corr[NT][2];
 #pragma unroll
@@ -368,12 +410,18 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], d));
-          const float mn = fmaxf(m[nt][e], mx[nt][e]);
+          // (the scale is positive: the largest score is the largest product)
+          const float mn = fmaxf(m[nt][e], mx[nt][e] * sl[nt][e]);
           corr[nt][e] = mn == m[nt][e] ? 1.f : ex2(m[nt][e] - mn);      // also where both are -inf
           moved |= mn != m[nt][e];
           m[nt][e] = mn;
           l[nt][e] *= corr[nt][e];
         }
+      float shift2[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) shift2[nt][e] = m[nt][e] == -INFINITY ? 0.f : kPShift - m[nt][e];
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
         for (int t = 0; t < MT; ++t)
@@ -392,8 +440,7 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
             float p[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float v = x[mt][nt][2 * h + e];
-              p[e] = v == -INFINITY ? 0.f : ex2(v - (m[nt][e] - kPShift));
+              p[e] = ex2(fmaf(x[mt][nt][2 * h + e], sl[nt][e], shift2[nt][e]));   // 0 where masked
               l[nt][e] += p[e];
             }
             const uint32_t hi = pack_f16(p[0], p[1]);
@@ -411,7 +458,7 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t at = stage + C::kOffVs + (mt * 16 + q4 + 8 * h) * (HD / 16) + gid * HD / 128;
-          sc[h] = q4::decode_scales(lds8(at) | lds8(at + 4 * (HD / 16)) << 8);
+          sc[h] = q4::decode_scales(__byte_perm(lds8(at), lds8(at + 4 * (HD / 16)), 0x0040));
         }
 #pragma unroll
         for (int i = 0; i < VW; ++i) {
@@ -430,8 +477,8 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
             for (int nt = 0; nt < NT; ++nt) {
               float (&acc)[4] = o[i * 4 + t][nt];
               if constexpr (F32) {
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_f16(c, f, pl[nt][0], pl[nt][1]);
+                float c[4];
+                mma_f16_new(c, f, pl[nt][0], pl[nt][1]);
                 mma_f16(c, f, ph[nt][0], ph[nt][1]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[e] += c[e];
@@ -506,11 +553,11 @@ struct Plan {
   int nt, grid;                         // score columns / 8 per tile; blocks
 };
 
-static Plan plan(int64_t n_rows, int S, int G) {
+static Plan plan(int64_t n_rows, int S, int G, cb_dtype dt) {
   const int64_t per_seq = (n_rows * G + S - 1) / S;
   Plan p;
   p.nt = per_seq <= 8 ? 1 : per_seq <= 16 ? 2 : 4;
-  p.grid = device_sm_count() * (p.nt == 4 ? 2 : 3);
+  p.grid = device_sm_count() * (p.nt == 4 || dt == CB_F32 ? 2 : p.nt == 2 ? 3 : 4);
   return p;
 }
 static size_t plan_bytes(const Plan &p, int hd) {
@@ -519,7 +566,7 @@ static size_t plan_bytes(const Plan &p, int hd) {
 
 template <typename T, int HD, int NT>
 static cudaError_t run(const Params &P, int grid, int *status, cudaStream_t s) {
-  typedef Cfg<HD, NT> C;
+  typedef Cfg<HD, NT, std::is_same<T, float>::value> C;
   static PerDeviceOnce attr;
   cudaError_t e = attr.run([](int) {
     return cudaFuncSetAttribute(paged4_few_kernel<T, HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
@@ -540,16 +587,16 @@ static cudaError_t run_rows(const Params &P, const Plan &p, int *status, cudaStr
 
 }  // namespace paged4
 
-size_t paged4_attention_ws_bytes(int n_rows, int n_seq, int max_kv, int Hq, int Hkv, int hd, cb_dtype) {
+size_t paged4_attention_ws_bytes(int n_rows, int n_seq, int max_kv, int Hq, int Hkv, int hd, cb_dtype dt) {
   if (n_rows <= 0 || n_seq <= 0) return 0;
-  return paged4::plan_bytes(paged4::plan(n_rows, n_seq, Hq / Hkv), hd);
+  return paged4::plan_bytes(paged4::plan(n_rows, n_seq, Hq / Hkv, dt), hd);
 }
 
 cudaError_t launch_paged4_attention(const cb_paged4_kv &kv, const cb_paged_query &a, cb_dtype dt, int *status,
                                     cudaStream_t s) {
   using namespace paged4;
   const int G = a.n_q_heads / a.n_kv_heads;
-  const Plan p = plan(a.n_rows, kv.n_seq, G);
+  const Plan p = plan(a.n_rows, kv.n_seq, G, dt);
   Params P;
   P.kv = paged4_plain_kv(kv);
   P.q = a.q;
@@ -560,6 +607,7 @@ cudaError_t launch_paged4_attention(const cb_paged4_kv &kv, const cb_paged_query
   P.G = G;
   P.Hkv = a.n_kv_heads;
   P.max_kv = a.max_kv_len;
+  P.pad = 2 * kv.n_seq * a.n_kv_heads >= p.grid ? kPad : 0;
   P.n_split = 1;
   P.few_hi = 0x7fffffff;
   P.rows_lo = 0;
