@@ -32,6 +32,9 @@ constexpr uint32_t idesc(bool b_mn_major, int n) {
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
+// the same for fp16 operands
+constexpr uint32_t idesc_f16(bool b_mn_major, int n) { return idesc(b_mn_major, n) & ~((1u << 7) | (1u << 10)); }
+
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map,
                                             uint32_t bar, int x, int y) {
   asm volatile(

@@ -44,6 +44,10 @@ struct AttnParams {
   float *part_o;                          // unnormalised partial rows, HD floats each
   float2 *part_ml;                        // (m, l) of each partial row
   Join *joins;                            // one per block of the few-rows kernel
+  // 4-bit cache (kv.k_pages: the pool, kv.page_stride in bytes)
+  int head_bytes = 0;                     // of one head's block of a page
+  float v_mul = 1.f;                      // 2^v_exp
+  int pad = 0;                            // units that a tile counts beyond its blocks
 };
 
 // Few rows per sequence, and all of fp32: R (16, 32 or 64) rows per tile.  The
@@ -55,7 +59,21 @@ cudaError_t launch_decode(const AttnParams &P, int R, int hd, cb_dtype dt, int *
 
 // bf16, many rows: units of R (128 or 256) rows, their keys in n_split parts;
 // the workspace holds units * Hkv * n_split * R partial rows if n_split > 1.
-cudaError_t launch_chunk(const AttnParams &P, int R, int64_t units, int hd, int *status, cudaStream_t s);
+// q4: over a 4-bit cache.
+struct ChunkPlan {
+  int R, n_split;
+  int64_t units;
+};
+ChunkPlan plan_chunk(int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd);
+cudaError_t launch_chunk(const AttnParams &P, int R, int64_t units, int hd, int *status, cudaStream_t s,
+                         bool q4 = false);
+
+// Tiles of R rows that n_rows rows over S sequences can make at most.
+inline int64_t tile_bound(int64_t n_rows, int S, int G, int R) {
+  const int64_t a = (n_rows * G + (int64_t)S * (R - 1)) / R;
+  const int64_t b = n_rows * ((G + R - 1) / R);
+  return a < b ? a : b;
+}
 
 }  // namespace paged
 }  // namespace cb

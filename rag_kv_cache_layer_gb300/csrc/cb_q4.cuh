@@ -141,5 +141,31 @@ __device__ __forceinline__ float turned(float x, float a, float y, float b) {
   return to_f(from_f<bf16>(__uint_as_float(bits)));
 }
 
+// The power of two that brings a row's largest magnitude to [2^13, 2^14), as an exponent.
+__device__ __forceinline__ int exponent_up(float top) { return top > 0.f ? 13 - ilogbf(top) : 0; }
+// ... and what is left of the softmax's log2 scale: above 0, so that a masked -inf stays
+// one (with a smaller scale every weight is 1 too).
+__device__ __forceinline__ float scale_down(float scale_log2, int up) {
+  const int down = -up;                     // in two factors: 2^down may leave fp32
+  return fmaxf(scale_log2 * ldexpf(1.f, down / 2) * ldexpf(1.f, down - down / 2), 0x1p-126f);
+}
+// A bf16 row (8 values each) to fp16 behind its power of two; the softmax's log2 scale of
+// the row.
+template <int N> __device__ __forceinline__ float scaled_row(uint4 (&v)[N], float scale_log2) {
+  __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);
+  __nv_bfloat162 *e = reinterpret_cast<__nv_bfloat162 *>(v);
+#pragma unroll
+  for (int i = 0; i < 4 * N; ++i) top2 = __hmax2(top2, __habs2(e[i]));
+  const int up = exponent_up(fmaxf(__low2float(top2), __high2float(top2)));
+  const float f1 = ldexpf(1.f, up / 2), f2 = ldexpf(1.f, up - up / 2);
+#pragma unroll
+  for (int i = 0; i < 4 * N; ++i) {
+    const float2 x = __bfloat1622float2(e[i]);
+    const __half2 h = __floats2half2_rn(x.x * f1 * f2, x.y * f1 * f2);
+    e[i] = *reinterpret_cast<const __nv_bfloat162 *>(&h);
+  }
+  return scale_down(scale_log2, up);
+}
+
 }  // namespace q4
 }  // namespace cb

@@ -36,11 +36,7 @@ namespace paged4 {
 
 using namespace paged;
 
-struct Params : AttnParams {
-  int head_bytes;                       // of one head's block of a page
-  float v_mul;                          // 2^v_exp
-  int pad;                              // units that a tile counts beyond its blocks
-};
+typedef AttnParams Params;
 
 constexpr int kBN = 32;                 // keys per block
 constexpr int kPad = 12;
@@ -294,8 +290,7 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
       for (int i = 0; i < HD / 4; ++i) top = fmaxf(top, fabsf(x[i]));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // 2^up brings top to [2^13, 2^14); in two factors, since 2^up may exceed fp32
-      const int up = top > 0.f ? 13 - ilogbf(top) : 0;
+      const int up = q4::exponent_up(top);
       const float f1 = ldexpf(1.f, up / 2), f2 = ldexpf(1.f, up - up / 2);
 #pragma unroll
       for (int k = 0; k < KS; ++k)
@@ -308,9 +303,8 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
       // scores of this lane are of rows nt * 8 + 2 q4 and + 1, whose q lanes 8 q4 and 8 q4 + 4 have
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int rc = nt * 8 + 2 * q4 + e, down = -__shfl_sync(0xffffffffu, up, 8 * q4 + 4 * e);
-        // above 0, so that a masked -inf stays one; a smaller scale leaves every weight at 1 too
-        sl[nt][e] = fmaxf(P.scale_log2 * ldexpf(1.f, down / 2) * ldexpf(1.f, down - down / 2), 0x1p-126f);
+        const int rc = nt * 8 + 2 * q4 + e;
+        sl[nt][e] = q4::scale_down(P.scale_log2, __shfl_sync(0xffffffffu, up, 8 * q4 + 4 * e));
         pos[nt][e] = rc < rows ? base + P.by_G.div(l0 + rc) : -1;
       }
     }
@@ -550,18 +544,36 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
 
 // ------------------------------------------------------------------ plan --
 struct Plan {
-  int nt, grid;                         // score columns / 8 per tile; blocks
+  int nt, grid;                         // few-rows kernel: score columns / 8 per tile (0: not launched), blocks
+  int few_hi, rows_lo;                  // which sequences each kernel takes
+  ChunkPlan chunk;                      // R 0: not launched
 };
 
-static Plan plan(int64_t n_rows, int S, int G, cb_dtype dt) {
-  const int64_t per_seq = (n_rows * G + S - 1) / S;
-  Plan p;
-  p.nt = per_seq <= 8 ? 1 : per_seq <= 16 ? 2 : 4;
+// bf16: as for the 16-bit cache, sequences of up to kFewRows rows (queries x G) go
+// through the few-rows kernel, longer ones through the chunk kernel; fp32 runs the
+// few-rows kernel alone.
+constexpr int kFewRows = 32;
+static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd, cb_dtype dt) {
+  Plan p = {};
+  const int64_t all = n_rows * G, per_seq = (all + S - 1) / S;
+  const bool few = dt == CB_F32 || all <= kFewRows || n_rows <= S;
+  p.few_hi = 0x7fffffff;
+  if (few || S > 1) p.nt = per_seq <= 8 ? 1 : per_seq <= 16 ? 2 : few || per_seq <= kFewRows ? 4 : 1;
   p.grid = device_sm_count() * (p.nt == 4 || dt == CB_F32 ? 2 : p.nt == 2 ? 3 : 4);
+  if (few) return p;
+  if (S > 1) p.few_hi = p.rows_lo = kFewRows;
+  p.chunk = plan_chunk(n_rows, S, max_kv, G, Hkv, hd);
   return p;
 }
-static size_t plan_bytes(const Plan &p, int hd) {
-  return 2ull * p.grid * 8 * p.nt * (hd * sizeof(float) + sizeof(float2)) + p.grid * sizeof(Join);
+static int64_t few_partials(const Plan &p) { return p.nt ? 2LL * p.grid * 8 * p.nt : 0; }
+static int64_t chunk_partials(const Plan &p, int Hkv) {
+  return p.chunk.R && p.chunk.n_split > 1 ? p.chunk.units * Hkv * p.chunk.n_split * p.chunk.R : 0;
+}
+static size_t plan_bytes(const Plan &p, int Hkv, int hd) {
+  const size_t row = hd * sizeof(float) + sizeof(float2);
+  const size_t few = (size_t)few_partials(p) * row + (p.nt ? p.grid * sizeof(Join) : 0);
+  const size_t chunk = (size_t)chunk_partials(p, Hkv) * row;
+  return few > chunk ? few : chunk;
 }
 
 template <typename T, int HD, int NT>
@@ -589,14 +601,15 @@ static cudaError_t run_rows(const Params &P, const Plan &p, int *status, cudaStr
 
 size_t paged4_attention_ws_bytes(int n_rows, int n_seq, int max_kv, int Hq, int Hkv, int hd, cb_dtype dt) {
   if (n_rows <= 0 || n_seq <= 0) return 0;
-  return paged4::plan_bytes(paged4::plan(n_rows, n_seq, Hq / Hkv, dt), hd);
+  return paged4::plan_bytes(paged4::plan(n_rows, n_seq, max_kv, Hq / Hkv, Hkv, hd, dt), Hkv, hd);
 }
 
 cudaError_t launch_paged4_attention(const cb_paged4_kv &kv, const cb_paged_query &a, cb_dtype dt, int *status,
                                     cudaStream_t s) {
   using namespace paged4;
   const int G = a.n_q_heads / a.n_kv_heads;
-  const Plan p = plan(a.n_rows, kv.n_seq, G, dt);
+  const Plan p = plan(a.n_rows, kv.n_seq, a.max_kv_len, G, a.n_kv_heads, a.head_dim, dt);
+  if (p.chunk.units * a.n_kv_heads * p.chunk.n_split > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   Params P;
   P.kv = paged4_plain_kv(kv);
   P.q = a.q;
@@ -608,22 +621,34 @@ cudaError_t launch_paged4_attention(const cb_paged4_kv &kv, const cb_paged_query
   P.Hkv = a.n_kv_heads;
   P.max_kv = a.max_kv_len;
   P.pad = 2 * kv.n_seq * a.n_kv_heads >= p.grid ? kPad : 0;
-  P.n_split = 1;
-  P.few_hi = 0x7fffffff;
-  P.rows_lo = 0;
+  P.n_split = p.chunk.n_split;
+  P.few_hi = p.few_hi;
+  P.rows_lo = p.rows_lo;
   P.hc = 1;
   P.by_G = Divisor(G);
   P.by_quads = Divisor(a.n_kv_heads);
   P.scale_log2 = a.scale * 1.4426950408889634f * ldexpf(1.f, kv.k_exp);
   P.head_bytes = q4::head_bytes(kv.page_size, a.head_dim);
   P.v_mul = ldexpf(1.f, kv.v_exp);
-  const int64_t partials = 2LL * p.grid * 8 * p.nt;
-  P.part_o = reinterpret_cast<float *>(a.ws);
-  P.part_ml = reinterpret_cast<float2 *>(P.part_o + partials * a.head_dim);
-  P.joins = reinterpret_cast<Join *>(P.part_ml + partials);
-  if (dt == CB_BF16)
-    return a.head_dim == 128 ? run_rows<bf16, 128>(P, p, status, s) : run_rows<bf16, 64>(P, p, status, s);
-  return a.head_dim == 128 ? run_rows<float, 128>(P, p, status, s) : run_rows<float, 64>(P, p, status, s);
+  // the partials of a launch reuse the workspace of the one before it: each waits for its
+  // predecessor's end
+  auto bind = [&](int64_t partials) {
+    P.part_o = reinterpret_cast<float *>(a.ws);
+    P.part_ml = reinterpret_cast<float2 *>(P.part_o + partials * a.head_dim);
+    P.joins = reinterpret_cast<Join *>(P.part_ml + partials);
+  };
+  if (p.nt) {
+    bind(few_partials(p));
+    cudaError_t e;
+    if (dt == CB_BF16)
+      e = a.head_dim == 128 ? run_rows<bf16, 128>(P, p, status, s) : run_rows<bf16, 64>(P, p, status, s);
+    else
+      e = a.head_dim == 128 ? run_rows<float, 128>(P, p, status, s) : run_rows<float, 64>(P, p, status, s);
+    if (e != cudaSuccess) return e;
+  }
+  if (!p.chunk.R) return cudaSuccess;
+  bind(chunk_partials(p, a.n_kv_heads));
+  return launch_chunk(P, p.chunk.R, p.chunk.units, a.head_dim, status, s, true);
 }
 
 }  // namespace cb

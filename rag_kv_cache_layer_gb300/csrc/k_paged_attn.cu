@@ -7,13 +7,6 @@
 namespace cb {
 namespace paged {
 
-// Tiles of R rows that n_rows rows over S sequences can make at most.
-static int64_t tile_bound(int64_t n_rows, int S, int G, int R) {
-  const int64_t a = (n_rows * G + (int64_t)S * (R - 1)) / R;
-  const int64_t b = n_rows * ((G + R - 1) / R);
-  return a < b ? a : b;
-}
-
 // How a call runs.
 struct Plan {
   int few_R, hc;                          // few-rows kernel: rows per tile (0: not launched), heads per item
@@ -40,7 +33,8 @@ struct Plan {
 // they count as units, so the chunk is split less or not at all, and the call lasts
 // as long as its few CTAs (64 rows + 63 single rows, all over 16,384 keys: 894 us; as
 // two calls 35 + 610).  The costs are those of head_dim 128; 64 is planned by them too.
-static void plan_chunk(Plan &p, int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd) {
+ChunkPlan plan_chunk(int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd) {
+  ChunkPlan p = {};
   const int sms = device_sm_count(), nb = (max_kv + 63) / 64 > 0 ? (max_kv + 63) / 64 : 1;
   double best = 1e300;
   for (int R = 128; R <= 256; R += 128) {
@@ -54,11 +48,12 @@ static void plan_chunk(Plan &p, int64_t n_rows, int S, int max_kv, int G, int Hk
       if (t < best) {
         best = t;
         p.R = R;
-        p.tiles = tiles;
+        p.units = tiles;
         p.n_split = n;
       }
     }
   }
+  return p;
 }
 
 // bf16: sequences of up to 64 rows (queries x G) go through the few-rows
@@ -89,7 +84,10 @@ static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd, cb_d
   p.few_partials = p.few_R ? 2LL * decode_grid() * p.few_R * p.hc : 0;
   if (few) return p;
   if (S > 1) p.few_hi = p.rows_lo = 64;
-  plan_chunk(p, n_rows, S, max_kv, G, Hkv, hd);
+  const ChunkPlan c = plan_chunk(n_rows, S, max_kv, G, Hkv, hd);
+  p.R = c.R;
+  p.tiles = c.units;
+  p.n_split = c.n_split;
   p.partials = p.n_split == 1 ? 0 : p.tiles * Hkv * p.n_split * p.R;
   return p;
 }

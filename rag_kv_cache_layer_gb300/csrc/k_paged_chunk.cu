@@ -49,6 +49,7 @@
 #include "cb_internal.h"
 #include "cb_paged.cuh"
 #include "cb_paged_attn.cuh"
+#include "cb_q4.cuh"
 
 namespace cb {
 namespace paged {
@@ -117,7 +118,64 @@ __device__ __forceinline__ void chunk_load(uint32_t dst, const bf16 *pool, const
   }
 }
 
-template <int HD, int NT>
+// 4-bit cache: a lane's 16 bytes of codes (32 dimensions of a key) of every group of
+// keys of a block, and their two scales.  Eight neighbouring lanes have eight keys and
+// the same dimensions, so that their 16-byte stores fall into different banks.
+template <int HD> struct ChCodes {
+  static constexpr int kCols = HD / 32, kKeys = 32 / kCols, kLoads = kChBN / kKeys;
+  uint4 codes[kLoads];
+  uint32_t scales[kLoads];
+};
+template <int HD>
+__device__ __forceinline__ void chunk_load4(ChCodes<HD> &c, const uint8_t *head, const PagedKV &kv, bool is_v, int key0,
+                                            int n_keys, int page_lo, int page_hi, int lane) {
+  typedef ChCodes<HD> C;
+  const int part = lane / C::kKeys, page_size = kv.page_size;
+  const uint8_t *codes = head + q4::codes_at(page_size, HD, is_v) + part * 16;
+  const uint8_t *scales = head + q4::scales_at(page_size, HD, is_v) + part * 2;
+#pragma unroll
+  for (int i = 0; i < C::kLoads; ++i) {
+    const int r = i * C::kKeys + lane % C::kKeys;
+    const int page = __shfl_sync(0xffffffffu, i * C::kKeys < 32 ? page_lo : page_hi, r & 31);
+    const int slot = (key0 + r) & (page_size - 1);
+    c.codes[i] = make_uint4(0, 0, 0, 0);      // a key past the cached length, or of a bad page: zeros
+    c.scales[i] = 0;
+    if (page >= 0 && r < n_keys) {
+      const int64_t at = (int64_t)page * kv.page_stride;
+      c.codes[i] = ldg16(codes + at + slot * (HD / 2));
+      c.scales[i] = __ldg(reinterpret_cast<const unsigned short *>(scales + at + slot * (HD / 16)));
+    }
+  }
+}
+// ... and their values in fp16, exact, to a stage.
+template <int HD> __device__ __forceinline__ void chunk_store4(const ChCodes<HD> &c, uint32_t dst, int lane) {
+  typedef ChCodes<HD> C;
+  const int part = lane / C::kKeys;
+#pragma unroll
+  for (int i = 0; i < C::kLoads; ++i) {
+    const int r = i * C::kKeys + lane % C::kKeys;
+    const uint32_t two = q4::decode_scales(c.scales[i]);
+    const uint32_t w[4] = {c.codes[i].x, c.codes[i].y, c.codes[i].z, c.codes[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t h[4];
+      q4::decode8(w[k], h);
+      const uint32_t s = q4::both(two, k >= 2);
+      const int col = part * 4 + k;
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (col >> 3) * (kChBN * 128) + r * 128 +
+                                                                    (((col ^ r) & 7) << 4)),
+                   "r"(q4::mul2(h[0], s)), "r"(q4::mul2(h[1], s)), "r"(q4::mul2(h[2], s)), "r"(q4::mul2(h[3], s))
+                   : "memory");
+    }
+  }
+}
+
+// Q4: over a 4-bit cache.  Keys and values come as codes and scales into registers and go
+// to their stage as fp16; q is fp16 behind a power of two per row, P fp16 with 2^6 at
+// the running reference (2^14 at the largest p), and the row's sum carries the same factor.
+constexpr float kCh4Shift = 6.f;
+
+template <int HD, int NT, bool Q4>
 __global__ void __launch_bounds__(ChCfg<HD, NT>::kThreads, ChCfg<HD, NT>::kPerSm)
 paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
   typedef ChCfg<HD, NT> C;
@@ -214,6 +272,32 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
       return -1;
     };
     int lo = fetch((jb + first) * kChBN + lane), hi = fetch((jb + first) * kChBN + 32 + lane);
+    if constexpr (Q4) {
+      // The next block's codes are on their way while this one's become values.
+      const uint8_t *head = reinterpret_cast<const uint8_t *>(P.kv.k_pages) + (int64_t)g * P.head_bytes;
+      ChCodes<HD> now, next;
+      auto load = [&](ChCodes<HD> &c, int j) {
+        const int key0 = (jb + j) * kChBN;
+        chunk_load4<HD>(c, head, P.kv, is_v, key0, tl.kv - key0, checked(lo, key0 + lane), checked(hi, key0 + 32 + lane),
+                        lane);
+        lo = fetch(key0 + C::kProd * kChBN + lane);
+        hi = fetch(key0 + C::kProd * kChBN + 32 + lane);
+      };
+      if (first < nb) load(now, first);
+      for (int j = first; j < nb; j += C::kProd) {
+        if (j + C::kProd < nb) load(next, j + C::kProd);
+        const int sl = j % NS;
+        const bool ok = mbar_wait_bounded(smem_u32(&empty[sl]), ((j / NS) & 1) ^ 1, kWaitLimitNs, status);
+        if (__any_sync(0xffffffffu, !ok || *fail)) {
+          *fail = 1;
+          break;
+        }
+        chunk_store4<HD>(now, dst + sl * C::kKV, lane);
+        proxy_fence();
+        arrive(smem_u32(&full[sl]));
+        now = next;
+      }
+    } else {
     // Two loads are in flight: a block is handed over (its bytes fenced for
     // the tensor core) after the warp's next one has been issued, or at once
     // where the next one's stage is still in use.
@@ -252,10 +336,12 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (open >= 0) hand_over();
+    }
   } else if (warp >= C::kMma && warp < C::kMma + active) {
     // ----------------------------------------------------- MMA, one per tile
     const int t = warp - C::kMma;
-    const uint32_t idS = idesc(false, kChBN), idPV = idesc(true, HD);
+    const uint32_t idS = Q4 ? idesc_f16(false, kChBN) : idesc(false, kChBN);
+    const uint32_t idPV = Q4 ? idesc_f16(true, HD) : idesc(true, HD);
     const uint32_t q_addr = smem_u32(smem + t * C::kQ), tm = tmem + t * kChTmem;
     uint64_t *const sf = s_full + t, *const sr = s_read + t, *const pf = p_full + 2 * t, *const pd = pv_done + 2 * t;
     auto wait_all = [&](uint64_t *b, uint32_t ph) -> bool {
@@ -307,6 +393,7 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
     // ------------------------------------------------------ Q, then softmax
     const int t = (warp - C::kSoft) / 4;
     uint64_t *const sf = s_full + t, *const sr = s_read + t, *const pf = p_full + 2 * t, *const pd = pv_done + 2 * t;
+    float sl2 = P.scale_log2;
     {
       // a thread loads its row: all its loads are in flight at once, and eight
       // neighbouring rows fall into different banks
@@ -317,6 +404,7 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
 #pragma unroll
       for (int c = 0; c < HD / 8; ++c)
         v[c] = r < rows ? *reinterpret_cast<const uint4 *>(q + c * 8) : make_uint4(0, 0, 0, 0);
+      if constexpr (Q4) sl2 = q4::scaled_row(v, sl2);
 #pragma unroll
       for (int c = 0; c < HD / 8; ++c)
         *reinterpret_cast<uint4 *>(smem + t * C::kQ + (c >> 3) * C::kAtom + (r & 127) * 128 +
@@ -331,7 +419,6 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const uint32_t tm = tmem + t * kChTmem + lane_off, obase = tm + kChO;
     float m = -INFINITY, l = 0.f;                // reference max (log2 domain), sum
-    const float sl2 = P.scale_log2;
     bool failed = false;
     auto pv_landed = [&](int j) -> bool {
       const bool bad = !mbar_wait_bounded(smem_u32(&pd[j & 1]), (j >> 1) & 1, kWaitLimitNs, status);
@@ -394,7 +481,7 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
       // the sums run on packed pairs.  The columns held P_{j-2}: S_j was
       // issued after P_{j-2} V_{j-2} and its commit covers what came before,
       // so that product is done.
-      const unsigned long long s2 = pack2(sl2, sl2), nm2 = pack2(-m, -m);
+      const unsigned long long s2 = pack2(sl2, sl2), nm2 = Q4 ? pack2(kCh4Shift - m, kCh4Shift - m) : pack2(-m, -m);
       unsigned long long ls2[2] = {0ull, 0ull};
       auto exps = [&](auto masked) {
 #pragma unroll
@@ -410,8 +497,13 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
               p1 = c + i + 1 < n_vis ? p1 : 0.f;
             }
             ls2[(i >> 1) & 1] = add2(ls2[(i >> 1) & 1], pack2(p0, p1));
-            __nv_bfloat162 v2 = __floats2bfloat162_rn(p0, p1);
-            pk[i / 2] = *reinterpret_cast<uint32_t *>(&v2);
+            if constexpr (Q4) {
+              __half2 v2 = __floats2half2_rn(p0, p1);
+              pk[i / 2] = *reinterpret_cast<uint32_t *>(&v2);
+            } else {
+              __nv_bfloat162 v2 = __floats2bfloat162_rn(p0, p1);
+              pk[i / 2] = *reinterpret_cast<uint32_t *>(&v2);
+            }
           }
           st16(tm + kChP + sl * 32 + c / 2, pk);
         }
@@ -430,7 +522,7 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
     const bool ok = !failed && !*fail;
     if (__any_sync(0xffffffffu, ok)) {
       const int lr = l0 + row, qi = P.by_G.div(lr);
-      const float inv = l == 0.f ? 0.f : 1.f / l;    // no visible key: zeros
+      const float inv = l == 0.f ? 0.f : Q4 ? P.v_mul / l : 1.f / l;    // no visible key: zeros
       bf16 *out = reinterpret_cast<bf16 *>(P.out) + (int64_t)(tl.row0 + qi) * P.ld_out +
                   (int64_t)(g * P.G + lr - qi * P.G) * HD;
       // partials lie four columns of all the unit's rows together, which a warp with
@@ -473,7 +565,7 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
 // and 32 columns (four per warp).  The unit is found before the parts are
 // waited for: what it reads was there before the chunk kernel began.
 constexpr int kChMergeThreads = 256;
-template <int HD, int NT>
+template <int HD, int NT, bool Q4>
 __global__ void __launch_bounds__(kChMergeThreads)
 chunk_merge_kernel(const __grid_constant__ AttnParams P) {
   constexpr int kChRows = ChCfg<HD, NT>::kRows, kQuads = kChRows / 32, kColBlocks = HD / 32;
@@ -511,7 +603,7 @@ chunk_merge_kernel(const __grid_constant__ AttnParams P) {
       a.w = fmaf(w, v.w, a.w);
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = l == 0.f ? 0.f : Q4 ? P.v_mul / l : 1.f / l;
   __nv_bfloat162 *so = reinterpret_cast<__nv_bfloat162 *>(&s_out[lane][warp * 4]);
   so[0] = __floats2bfloat162_rn(a.x * inv, a.y * inv);
   so[1] = __floats2bfloat162_rn(a.z * inv, a.w * inv);
@@ -526,26 +618,31 @@ chunk_merge_kernel(const __grid_constant__ AttnParams P) {
   }
 }
 
-template <int HD, int NT>
+template <int HD, int NT, bool Q4>
 static cudaError_t run(const AttnParams &P, int64_t tiles, int *status, cudaStream_t s) {
   typedef ChCfg<HD, NT> C;
   static PerDeviceOnce attr;
   cudaError_t e = attr.run([](int) {
-    return cudaFuncSetAttribute(paged_chunk_kernel<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    return cudaFuncSetAttribute(paged_chunk_kernel<HD, NT, Q4>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   if (e != cudaSuccess) return e;
-  e = launch_pdl(paged_chunk_kernel<HD, NT>, dim3((unsigned)(tiles * P.Hkv * P.n_split)), dim3(C::kThreads), C::kSmem,
+  e = launch_pdl(paged_chunk_kernel<HD, NT, Q4>, dim3((unsigned)(tiles * P.Hkv * P.n_split)), dim3(C::kThreads), C::kSmem,
                  s, P, status);
   if (e != cudaSuccess) return e;
   if (P.n_split == 1) return launched(1);
-  e = launch_pdl(chunk_merge_kernel<HD, NT>, dim3((unsigned)(tiles * P.Hkv * (C::kRows / 32) * (HD / 32))),
+  e = launch_pdl(chunk_merge_kernel<HD, NT, Q4>, dim3((unsigned)(tiles * P.Hkv * (C::kRows / 32) * (HD / 32))),
                  dim3(kChMergeThreads), 0, s, P);
   return e == cudaSuccess ? launched(2) : e;
 }
 
-cudaError_t launch_chunk(const AttnParams &P, int R, int64_t tiles, int hd, int *status, cudaStream_t s) {
-  if (hd == 128) return R == 128 ? run<128, 1>(P, tiles, status, s) : run<128, 2>(P, tiles, status, s);
-  return R == 128 ? run<64, 1>(P, tiles, status, s) : run<64, 2>(P, tiles, status, s);
+template <bool Q4>
+static cudaError_t run_units(const AttnParams &P, int R, int64_t tiles, int hd, int *status, cudaStream_t s) {
+  if (hd == 128) return R == 128 ? run<128, 1, Q4>(P, tiles, status, s) : run<128, 2, Q4>(P, tiles, status, s);
+  return R == 128 ? run<64, 1, Q4>(P, tiles, status, s) : run<64, 2, Q4>(P, tiles, status, s);
+}
+
+cudaError_t launch_chunk(const AttnParams &P, int R, int64_t tiles, int hd, int *status, cudaStream_t s, bool q4) {
+  return q4 ? run_units<true>(P, R, tiles, hd, status, s) : run_units<false>(P, R, tiles, hd, status, s);
 }
 
 }  // namespace paged
