@@ -10,17 +10,20 @@
 //     = max_h (q_h^+ . max + q_h^- . min),   q^+ = max(q, 0), q^- = min(q, 0),
 // is computed in fp32 first, off by at most
 //   eps = 2^-15 max_h |q_h|_1 max |bounds|
-// (256 products of one sum, each rounded, summed in fp32: 2 * 256 * 2^-24).  With t
-// the fp32 score in the place of the last one that fits, pages above t + 2 eps are in,
-// pages below t - 2 eps are not, and the few between are scored again in fp64, where
-// the products are exact, and ranked (ties: the lower page): the picks are those of
-// the exact scores.
+// (256 products of one sum, each rounded, summed in fp32 with truncated sums: 2 * 256 *
+// 2^-24).  The fp32 score in the place of the last one that fits lies in some range
+// [from, to]; pages above to + 2 eps are in, pages below from - 2 eps are not, and the
+// few between are scored again in fp64, where the products are exact, and ranked
+// (ties: the lower page): the picks are those of the exact scores.
 //
 // A generated token reads two bounds for a page in place of its keys: the scores are
 // a stream over the bounds.
 #include "cb_common.cuh"
 #include "cb_internal.h"
+#include <type_traits>
+
 #include "cb_paged.cuh"
+#include "cb_paged_few.cuh"
 
 namespace cb {
 namespace pages {
@@ -205,17 +208,102 @@ paged_score_kernel(const __grid_constant__ SelectParams P, int *status) {
   }
 }
 
+// bf16: a warp takes 16 pages and one kv head at a time, 8 q heads per instruction: the
+// bounds are the 16-row side of mma.m16n8k16, (q^+, q^-) the 8-column side.  Every 16
+// bytes of a bound are eight dimensions of one lane and two of the instruction's steps,
+// so the bounds go from memory to the tensor cores as they are.  The block's warps take
+// neighbouring heads of the same pages, whose bounds lie side by side.
+constexpr int kTPages = 64;             // pages of a block
+
+template <int HD>
+__global__ void __launch_bounds__(kSThreads)
+paged_score_tc_kernel(const __grid_constant__ SelectParams P, int *status) {
+  constexpr int NL = HD / 32;           // 16-byte loads of a lane per bound
+  __shared__ RowPlace s_row;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int part = blockIdx.x % P.parts, r = blockIdx.x / P.parts;
+  const RowPlace at = find_row<kSThreads>(P.kv, P.n_rows, r, &s_row, status);
+  const int pages = pages_of(P, at, status);
+  if (pages <= P.n_picks) return;
+  const int j0 = max(P.n_first, part * kTPages), j1 = min(pages - P.n_last, (part + 1) * kTPages);
+  if (j0 >= j1) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, q4 = lane & 3;
+  const bf16 *q = reinterpret_cast<const bf16 *>(P.q) + r * P.ld_q + q4 * 8;
+  const int tiles = (j1 - j0 + 15) / 16 * P.Hkv;
+  for (int t = warp; t < tiles; t += kSThreads / 32) {
+    const int g = t % P.Hkv, j = j0 + t / P.Hkv * 16;
+    // pages of this lane's rows gid and gid + 8; -1: none
+    const bf16 *b[2];
+    bool there[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int jj = j + gid + 8 * h;
+      const int page = jj < j1 ? paged_page(P.kv, at.s, jj, status) : -1;
+      there[h] = page >= 0;
+      b[h] = reinterpret_cast<const bf16 *>(P.bounds) + max(page, 0) * P.page_stride + g * HD + q4 * 8;
+    }
+    uint4 lo[2][NL], hi[2][NL];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        lo[h][i] = there[h] ? ldg16(b[h] + i * 32) : make_uint4(0, 0, 0, 0);
+        hi[h][i] = there[h] ? ldg16(b[h] + P.ld + i * 32) : make_uint4(0, 0, 0, 0);
+      }
+    float best[2] = {-INFINITY, -INFINITY};
+    for (int h0 = 0; h0 < P.G; h0 += 8) {
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const uint4 raw = h0 + gid < P.G ? ldg16(q + (int64_t)(g * P.G + h0 + gid) * HD + i * 32) : make_uint4(0, 0, 0, 0);
+        const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+        uint32_t up[4], down[4];
+        const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162 *>(&x[k]);
+          const __nv_bfloat162 p = __hmax2(v, zero), n = __hmin2(v, zero);
+          up[k] = *reinterpret_cast<const uint32_t *>(&p);
+          down[k] = *reinterpret_cast<const uint32_t *>(&n);
+        }
+        const uint32_t a0[4] = {hi[0][i].x, hi[1][i].x, hi[0][i].y, hi[1][i].y};
+        const uint32_t a1[4] = {hi[0][i].z, hi[1][i].z, hi[0][i].w, hi[1][i].w};
+        const uint32_t d0[4] = {lo[0][i].x, lo[1][i].x, lo[0][i].y, lo[1][i].y};
+        const uint32_t d1[4] = {lo[0][i].z, lo[1][i].z, lo[0][i].w, lo[1][i].w};
+        paged::mma16816(c, a0, up[0], up[1]);
+        paged::mma16816(c, a1, up[2], up[3]);
+        paged::mma16816(c, d0, down[0], down[1]);
+        paged::mma16816(c, d1, down[2], down[3]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (h0 + 2 * q4 + (k & 1) < P.G) best[k >> 1] = fmaxf(best[k >> 1], c[k]);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const uint32_t x[8] = {lo[h][i].x, lo[h][i].y, lo[h][i].z, lo[h][i].w, hi[h][i].x, hi[h][i].y, hi[h][i].z, hi[h][i].w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&x[k])));
+      }
+      float top = fmaxf(__low2float(top2), __high2float(top2));
+#pragma unroll
+      for (int d = 1; d < 4; d <<= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        best[h] = fmaxf(best[h], __shfl_xor_sync(0xffffffffu, best[h], d));
+      }
+      const int jj = j + gid + 8 * h;
+      if (q4 == 0 && jj < j1)
+        P.approx[((int64_t)r * P.Hkv + g) * P.held + jj] = there[h] ? make_float2(best[h], top) : make_float2(-INFINITY, 0.f);
+    }
+  }
+}
+
 // ---------------------------------------------------------------- choice --
 constexpr int kCThreads = 512;
-
-// A float's order as an unsigned number.
-__device__ __forceinline__ uint32_t ordered(float x) {
-  const uint32_t b = __float_as_uint(x);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float unordered(uint32_t u) {
-  return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
-}
 
 // Sum of v over the block's threads before this one, and the whole.
 __device__ __forceinline__ int block_scan(int v, int *s_warp, int &total) {
@@ -239,12 +327,16 @@ __device__ __forceinline__ int block_scan(int v, int *s_warp, int &total) {
   return before;
 }
 
+constexpr int kBins = 2048, kHeld = 16;  // bins of a histogram; scores a thread keeps in registers
+constexpr int kFew = 32;                // candidates that need no narrower bins
+
 template <typename T, int HD>
 __global__ void __launch_bounds__(kCThreads)
 paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
+  constexpr int NW = kCThreads / 32;
   __shared__ RowPlace s_row;
-  __shared__ int s_hist[256], s_warp[kCThreads / 32], s_bin, s_rest, s_count;
-  __shared__ float s_f[kCThreads / 32];
+  __shared__ int s_hist[kBins], s_warp[NW], s_bin, s_in, s_count;
+  __shared__ float s_f[4][NW];
   grid_dep_wait();
   grid_dep_launch();
   const int g = blockIdx.x % P.Hkv, r = blockIdx.x / P.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -262,81 +354,118 @@ paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
   int *list = P.list + base;
   const int lo = P.n_first, hi = pages - P.n_last;          // scored pages
   const int want = P.n_picks - P.n_first - P.n_last;        // of them are picked, fewer than there are
-  float t = INFINITY, eps = 0.f;
+  float sure = INFINITY, none = INFINITY;                   // above: in; below: out; between: scored exactly
+  // scores lo + tid + i * kCThreads, the first kHeld of them in registers
+  float held[kHeld];
+  auto each = [&](auto &&f) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (lo + tid + i * kCThreads < hi) f(lo + tid + i * kCThreads, held[i]);
+    for (int j = lo + tid + kHeld * kCThreads; j < hi; j += kCThreads) f(j, a[j].x);
+  };
   if (want > 0) {
-    // eps: |q|_1 of the heads, the largest bound
     const T *q = reinterpret_cast<const T *>(P.q) + r * P.ld_q + (int64_t)g * P.G * HD;
-    float norm = 0.f, top = 0.f;
-    for (int h = warp; h < P.G; h += kCThreads / 32) {
-      float s = 0.f;
-      for (int i = lane; i < HD; i += 32) s += fabsf(to_f(q[h * HD + i]));
-      norm = fmaxf(norm, warp_sum(s));
-    }
-    for (int j = lo + tid; j < hi; j += kCThreads) top = fmaxf(top, a[j].y);
-    auto block_max = [&](float v) {
-      v = warp_max(v);
-      __syncthreads();
-      if (lane == 0) s_f[warp] = v;
-      __syncthreads();
-      float x = s_f[0];
-      for (int w = 1; w < kCThreads / 32; ++w) x = fmaxf(x, s_f[w]);
-      return x;
+    float v[4] = {-INFINITY, -INFINITY, 0.f, 0.f};          // largest score, largest negative, |bound|, |q|_1
+    int finite = 0, in_pool;
+    auto take = [&](float2 x) {
+      if (x.x > -INFINITY) {                                // (a page outside the pool has -inf)
+        v[1] = fmaxf(v[1], -x.x);
+        ++finite;
+      }
+      v[0] = fmaxf(v[0], x.x);
+      v[2] = fmaxf(v[2], x.y);
     };
-    norm = block_max(norm);
-    top = block_max(top);
-    eps = 0x1p-15f * norm * top;
-    // the want-th largest fp32 score, eight bits at a time
-    uint32_t prefix = 0;
-    int rest = want;
-    for (int sh = 24; sh >= 0; sh -= 8) {
-      for (int i = tid; i < 256; i += kCThreads) s_hist[i] = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int j = lo + tid + i * kCThreads;
+      const float2 x = j < hi ? a[j] : make_float2(-INFINITY, 0.f);
+      held[i] = x.x;
+      take(x);
+    }
+    for (int j = lo + tid + kHeld * kCThreads; j < hi; j += kCThreads) take(a[j]);
+    for (int h = warp; h < P.G; h += NW) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = lane; i < HD; i += 32) s += fabsf(to_f(q[h * HD + i]));
+      v[3] = fmaxf(v[3], warp_sum(s));
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = warp_max(v[k]);
+      if (lane == 0) s_f[k][warp] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      for (int w = 0; w < NW; ++w) v[k] = fmaxf(v[k], s_f[k][w]);
+    const float eps = 0x1p-15f * v[3] * v[2];
+    block_scan(finite, s_warp, in_pool);
+    // [from, to] holds the score in the last place that fits: bins over it, the one with
+    // that place in turn, until few scores (or nothing to tell apart) are left
+    float from = -v[1], to = v[0];
+    int above = 0;                                          // scores above `to`
+    for (int round = 0; round < 8 && in_pool >= want; ++round) {
+      for (int i = tid; i < kBins; i += kCThreads) s_hist[i] = 0;
       __syncthreads();
-      for (int j = lo + tid; j < hi; j += kCThreads) {
-        const uint32_t u = ordered(a[j].x);
-        if (sh == 24 || u >> (sh + 8) == prefix >> (sh + 8)) atomicAdd(&s_hist[u >> sh & 255], 1);
+      const float width = to - from, inv = kBins / width;
+      if (!(width > 2.f * eps) || !(inv < INFINITY)) break;
+      auto bin = [&](float x) { return min(kBins - 1, (int)((x - from) * inv)); };
+      each([&](int, float x) {
+        if (x >= from && x <= to) atomicAdd(&s_hist[bin(x)], 1);
+      });
+      __syncthreads();
+      // thread t: bins from the largest down, kBins / kCThreads of them
+      constexpr int PER = kBins / kCThreads;
+      int n[PER], sum = 0, all;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) sum += n[i] = s_hist[kBins - 1 - tid * PER - i];
+      int before = above + block_scan(sum, s_warp, all);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (before < want && before + n[i] >= want) {
+          s_bin = kBins - 1 - tid * PER - i;
+          s_in = n[i];
+        }
+        before += n[i];
       }
       __syncthreads();
-      if (warp == 0) {
-        // lane: bins 255 - 8 lane .. 248 - 8 lane, from the largest down
-        int n = 0;
-        for (int i = 0; i < 8; ++i) n += s_hist[255 - 8 * lane - i];
-        int incl = n;
-        for (int o = 1; o < 32; o <<= 1) {
-          const int x = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += x;
-        }
-        int above = incl - n;
-        if (above < rest && incl >= rest) {
-          int b = 255 - 8 * lane;
-          while (above + s_hist[b] < rest) above += s_hist[b--];
-          s_bin = b;
-          s_rest = rest - above;
-        }
-      }
+      // the bin's scores lie between its edges; a rounding of the edges moves them by
+      // less than 2^-20 of the range, which the margins cover
+      const float b0 = from + s_bin * (width / kBins), b1 = from + (s_bin + 1) * (width / kBins), slack = 0x1p-20f * (fabsf(from) + fabsf(to));
+      const bool few = s_in <= kFew;
+      to = fminf(to, b1 + slack);
+      from = fmaxf(from, b0 - slack);
       __syncthreads();
-      prefix |= (uint32_t)s_bin << sh;
-      rest = s_rest;
+      if (few || !(to - from < width)) break;
+      // (with the slack the range may hold scores of the neighbouring bins: count anew)
+      int over = 0;
+      each([&](int, float x) { over += x > to; });
+      block_scan(over, s_warp, above);
       __syncthreads();
     }
-    t = unordered(prefix);
+    // (all pages of the pool, and some outside, where those do not suffice)
+    sure = in_pool >= want ? to + 2.f * eps : -3.402823466e38f;
+    none = in_pool >= want ? from - 2.f * eps : -INFINITY;
   }
-  // how many are in for certain; exact scores of those at the border
-  const float sure = t + 2.f * eps, none = t - 2.f * eps;
+  // how many are in for certain; exact scores of those between
   if (tid == 0) s_count = 0;
   __syncthreads();
   int in = 0, total;
-  for (int j0 = lo + warp * 32; j0 < hi && want > 0; j0 += kCThreads) {
-    const float x = j0 + lane < hi ? a[j0 + lane].x : -INFINITY;
-    if (j0 + lane < hi) in += x > sure;
-    unsigned border = __ballot_sync(0xffffffffu, j0 + lane < hi && !(x > sure) && x >= none);
-    while (border) {
-      const int j = j0 + __ffs(border) - 1;
-      border &= border - 1;
-      const int page = paged_page(P.kv, at.s, j, nullptr);
+  if (want > 0)
+    each([&](int j, float x) {
+      if (x > sure) ++in;
+      else if (x >= none) list[atomicAdd(&s_count, 1)] = j;
+    });
+  block_scan(in, s_warp, total);
+  const int need = want - total;                            // of the pages between
+  __syncthreads();
+  if (s_count > need) {
+    const T *q = reinterpret_cast<const T *>(P.q) + r * P.ld_q + (int64_t)g * P.G * HD;
+    for (int c = warp; c < s_count; c += NW) {
+      const int page = paged_page(P.kv, at.s, list[c], nullptr);
       double best = -INFINITY;
       if (page >= 0) {
         const T *b = reinterpret_cast<const T *>(P.bounds) + page * P.page_stride + g * HD;
-        const T *q = reinterpret_cast<const T *>(P.q) + r * P.ld_q + (int64_t)g * P.G * HD;
         for (int h = 0; h < P.G; ++h) {
           double sum = 0.0;
 #pragma unroll
@@ -347,24 +476,20 @@ paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
           best = fmax(best, warp_sum_d(sum));
         }
       }
-      if (lane == 0) {
-        const int c = atomicAdd(&s_count, 1);
-        exact[c] = best;
-        list[c] = j;
-      }
+      if (lane == 0) exact[c] = best;
     }
+    __syncthreads();
   }
-  block_scan(in, s_warp, total);
-  const int need = want - total;                            // of the pages at the border
-  __syncthreads();
   // their ranks: -1 in place of the bound of a page that is picked, -2 of one that is not
   for (int c = tid; c < s_count; c += kCThreads) {
-    const double e = exact[c];
     const int j = list[c];
     int better = 0;
-    for (int k = 0; k < s_count && better < need; ++k) {
-      const double f = exact[k];
-      better += f > e || (f == e && list[k] < j);
+    if (s_count > need) {
+      const double e = exact[c];
+      for (int k = 0; k < s_count && better < need; ++k) {
+        const double f = exact[k];
+        better += f > e || (f == e && list[k] < j);
+      }
     }
     a[j].y = better < need ? -1.f : -2.f;
   }
@@ -415,7 +540,11 @@ static cudaError_t run_select(const pages::SelectParams &P, int *status, cudaStr
   using namespace pages;
   int n = 0;
   if (P.held > P.n_picks) {
-    const cudaError_t e = launch_pdl(paged_score_kernel<T, HD>, dim3(P.parts * P.Hkv * P.n_rows), dim3(kSThreads), 0, s, P, status);
+    cudaError_t e;
+    if constexpr (std::is_same<T, bf16>::value)
+      e = launch_pdl(paged_score_tc_kernel<HD>, dim3(P.parts * P.n_rows), dim3(kSThreads), 0, s, P, status);
+    else
+      e = launch_pdl(paged_score_kernel<T, HD>, dim3(P.parts * P.Hkv * P.n_rows), dim3(kSThreads), 0, s, P, status);
     if (e != cudaSuccess) return e;
     ++n;
   }
@@ -446,6 +575,7 @@ cudaError_t launch_paged_select(const PagedKV &kv, const cb_page_bounds &b, cons
   const size_t all = (size_t)b.n_rows * P.Hkv * P.held;
   P.exact = reinterpret_cast<double *>(P.approx + all);
   P.list = reinterpret_cast<int *>(P.exact + all);
+  static_assert(pages::kSPages == pages::kTPages, "pages of a block");
   P.parts = (P.held + pages::kSPages - 1) / pages::kSPages;
   if ((int64_t)P.parts * P.Hkv * b.n_rows > 0x7fffffffLL || (int64_t)P.Hkv * b.n_rows > 0x7fffffffLL)
     return cudaErrorInvalidConfiguration;

@@ -119,6 +119,29 @@ def test_select_equal_and_extreme_scores():
     assert np.array_equal(picks.cpu().numpy(), want) and R.device_status() == 0
 
 
+@pytest.mark.parametrize("dt", list(HALF))
+@pytest.mark.parametrize("kind", ["outlier", "two values", "many equal", "wide"])
+def test_select_scores_of_any_distribution(dt, kind):
+    """Scores that a histogram of their range does not tell apart, more pages than a
+    block holds in registers, borders between equal scores."""
+    rng = np.random.default_rng(31)
+    b = Batch(rng, [(1, 8 * 9000), (2, 8 * 700)], 8, dt, 2, 64)
+    x = vals(rng, (b.n_pages, 1, 128), dt)
+    if kind == "outlier":
+        x[b.table[0][5]] *= 2.0 ** 40
+    elif kind == "two values":
+        x[:] = np.where(rng.random((b.n_pages, 1, 1)) < 0.01, 1.0, 0.5)
+    elif kind == "many equal":
+        x[rng.random(b.n_pages) < 0.7] = x[0]
+    else:
+        x *= np.exp2(rng.integers(-30, 30, (b.n_pages, 1, 1))).astype(np.float32)
+    bounds, q = np.repeat(x, 2, 1), vals(rng, (b.rows, 4 * 64), dt)
+    picks = torch.zeros(b.rows, 2, 100, dtype=torch.int32, device="cuda")
+    R.cb_paged_select(dev(q, dt), *b.dev(), dev(bounds, dt), 8, 4, 2, 64, picks, n_first=1, n_last=1)
+    want = O4.select(q, bounds, b.table, b.offsets, b.lens, 8, 4, 2, 64, np.zeros(picks.shape), 1, 1)
+    assert np.array_equal(picks.cpu().numpy(), want) and R.device_status() == 0
+
+
 def test_select_errors_on_the_device():
     dt, page = torch.bfloat16, 8
     bounds, q = torch.zeros(20, 2, 64, dtype=dt, device="cuda"), torch.ones(3, 64, dtype=dt, device="cuda")
@@ -135,7 +158,9 @@ def test_select_errors_on_the_device():
     assert run([0, 1, 2], [80, -1], t) == (bad, [ok, old, old])
     assert run([0, 1, 2], [80, 80], t, max_kv_len=79) == (bad, [old, old, old])
     assert run([0, 1, 9], [80, 80], t) == (bad, [ok, old, old])
-    # a page outside the pool has the smallest score
+    # pages outside the pool have the smallest score
+    assert run([0, 1, 2], [80, 80], [[0] + [-1] * 8 + [1], t[1]]) == (bad, [[0, 1, 2, 9], ok, old])
+    assert run([0, 1, 2], [80, 80], [[0, 5, 77, 77, 77, 77, 77, 77, 77, 9], t[1]], n_first=0, n_last=0) == (bad, [[0, 1, 2, 9], [0, 1, 2, 3], old])
     assert run([0, 1, 2], [80, 80], [[0, 20, 2, 3, 4, 5, 6, 7, 8, 9], t[1]]) == (bad, [[0, 2, 3, 9], ok, old])
 
 
