@@ -8,6 +8,7 @@
 #include "cb_internal.h"
 #include "cb_paged.cuh"
 #include "cb_paged_attn.cuh"
+#include "cb_paged_few.cuh"
 
 namespace cb {
 namespace paged {
@@ -17,10 +18,6 @@ constexpr int kDecThreads = 128;
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&v);
-}
-// 16 bytes to shared memory, or 16 zero bytes when `there` is false.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 // 2^x, relative error about 2^-22, far below the rounding of P to bf16.
 __device__ __forceinline__ float ex2(float x) {

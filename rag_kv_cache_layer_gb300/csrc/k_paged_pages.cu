@@ -13,8 +13,9 @@
 // (256 products of one sum, each rounded, summed in fp32 with truncated sums: 2 * 256 *
 // 2^-24).  The fp32 score in the place of the last one that fits lies in some range
 // [from, to]; pages above to + 2 eps are in, pages below from - 2 eps are not, and the
-// few between are scored again in fp64, where the products are exact, and ranked
-// (ties: the lower page): the picks are those of the exact scores.
+// few between are scored again with exact products in pairs of floats (2^-44 of the
+// terms; an fp64 sum costs twenty times as much here) and ranked (ties: the lower
+// page): the picks are those of the exact scores.
 //
 // A generated token reads two bounds for a page in place of its keys: the scores are
 // a stream over the bounds.
@@ -23,6 +24,7 @@
 #include <type_traits>
 
 #include "cb_paged.cuh"
+#include "cb_paged_attn.cuh"
 #include "cb_paged_few.cuh"
 
 namespace cb {
@@ -66,21 +68,24 @@ template <typename T>
 __global__ void __launch_bounds__(kBThreads)
 paged_bounds_kernel(const __grid_constant__ BoundsParams P, int *status) {
   constexpr int VEC = 16 / sizeof(T), kSlots = kBThreads / kBCols;
-  __shared__ int s_off[CB_MAX_SEQS + 1];
+  __shared__ int s_off[CB_MAX_SEQS + 1], s_len[CB_MAX_SEQS];
   __shared__ int s_page[kBRows], s_n[kBRows], s_bad;   // page (-1: none) and covered slots of an owning row
   __shared__ float s_lo[kSlots][kBCols][VEC + 1], s_hi[kSlots][kBCols][VEC + 1];
   grid_dep_wait();
   grid_dep_launch();
   const int S = P.kv.n_seq, row0 = blockIdx.x * P.rows_per_block;
   const int rows = min(P.rows_per_block, P.n_rows - row0);
-  for (int i = threadIdx.x; i <= S; i += kBThreads) s_off[i] = __ldg(P.kv.row_offsets + i);
+  for (int i = threadIdx.x; i <= S; i += kBThreads) {
+    s_off[i] = __ldg(P.kv.row_offsets + i);
+    if (i < S) s_len[i] = __ldg(P.kv.kv_lens + i);
+  }
   if (threadIdx.x == 0) s_bad = 0;
   __syncthreads();
   const int page = P.kv.page_size, shift = __ffs(page) - 1;
   auto place = [&](int x, int n, int i) {
     int pg = -1, slots = 0;
     if (i >= 0 && i < n) {
-      const int kv = __ldg(P.kv.kv_lens + x);
+      const int kv = s_len[x];
       const int64_t p = (int64_t)kv - n + i;
       // the sequence's first new row in this page
       if (p >= 0 && (i == 0 || p == 0 || (p & (page - 1)) == 0)) {
@@ -144,11 +149,13 @@ struct SelectParams {
   int64_t page_stride, ld, ld_q;        // elements
   int32_t *picks;
   float2 *approx;                       // [rows][Hkv][max_pages]: fp32 score, largest |bound|
-  double *exact;                        // the same shape: exact scores of the pages at the border, one after another
+  float2 *exact;                        // the same shape: exact scores of the pages at the border, one after another
   int *list;                            // the same shape: those pages
   int n_rows, G, Hkv, hd, max_kv;
   int held, parts;                      // pages of max_kv; blocks that score them
   int n_picks, n_first, n_last;
+  paged::Divisor by_heads;              // Hkv
+  bool scored;                          // the launch before the choice is the scores'
 };
 
 constexpr int kSThreads = 256, kSPages = 64;   // pages of a block
@@ -209,104 +216,229 @@ paged_score_kernel(const __grid_constant__ SelectParams P, int *status) {
 }
 
 // bf16: a warp takes 16 pages and one kv head at a time, 8 q heads per instruction: the
-// bounds are the 16-row side of mma.m16n8k16, (q^+, q^-) the 8-column side.  Every 16
-// bytes of a bound are eight dimensions of one lane and two of the instruction's steps,
-// so the bounds go from memory to the tensor cores as they are.  The block's warps take
-// neighbouring heads of the same pages, whose bounds lie side by side.
-constexpr int kTPages = 64;             // pages of a block
+// bounds are the 16-row side of mma.m16n8k16, (q^+, q^-) the 8-column side; each warp
+// keeps two tiles of bounds on their way by cp.async.  All rows' tiles of 16
+// pages form one line that the grid shares in equal parts (long and short requests in
+// one batch keep every SM busy); neighbouring warps take neighbouring heads of the same
+// pages, whose bounds lie side by side.
+constexpr int kTStages = 3;              // of each warp
 
+// The line: tiles of a sequence, each of its rows as many as its last one.
+struct ScoreLine {
+  int64_t begin[CB_MAX_SEQS + 1];       // first tile of each sequence
+  int tiles[CB_MAX_SEQS];               // tiles of one of its rows
+};
+
+// (the bound of 384 threads leaves registers for a block of the choice beside this one's)
 template <int HD>
-__global__ void __launch_bounds__(kSThreads)
+__global__ void __launch_bounds__(384, 1)
 paged_score_tc_kernel(const __grid_constant__ SelectParams P, int *status) {
-  constexpr int NL = HD / 32;           // 16-byte loads of a lane per bound
-  __shared__ RowPlace s_row;
+  constexpr int kBytes = HD * 2, kStage = 16 * 2 * kBytes;   // of a bound; 16 pages' minima and maxima
+  constexpr int PER = (CB_MAX_SEQS + kSThreads - 1) / kSThreads;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ ScoreLine line;
+  __shared__ int64_t s_sums[kSThreads / 32];
   grid_dep_wait();
   grid_dep_launch();
-  const int part = blockIdx.x % P.parts, r = blockIdx.x / P.parts;
-  const RowPlace at = find_row<kSThreads>(P.kv, P.n_rows, r, &s_row, status);
-  const int pages = pages_of(P, at, status);
-  if (pages <= P.n_picks) return;
-  const int j0 = max(P.n_first, part * kTPages), j1 = min(pages - P.n_last, (part + 1) * kTPages);
-  if (j0 >= j1) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, q4 = lane & 3;
-  const bf16 *q = reinterpret_cast<const bf16 *>(P.q) + r * P.ld_q + q4 * 8;
-  const int tiles = (j1 - j0 + 15) / 16 * P.Hkv;
-  for (int t = warp; t < tiles; t += kSThreads / 32) {
-    const int g = t % P.Hkv, j = j0 + t / P.Hkv * 16;
-    // pages of this lane's rows gid and gid + 8; -1: none
-    const bf16 *b[2];
-    bool there[2];
+  const int S = P.kv.n_seq, page_size = P.kv.page_size, shift = __ffs(page_size) - 1;
+  {
+    const int per = (S + kSThreads - 1) / kSThreads, i0 = threadIdx.x * per;
+    int64_t n[PER], sum = 0;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int jj = j + gid + 8 * h;
-      const int page = jj < j1 ? paged_page(P.kv, at.s, jj, status) : -1;
-      there[h] = page >= 0;
-      b[h] = reinterpret_cast<const bf16 *>(P.bounds) + max(page, 0) * P.page_stride + g * HD + q4 * 8;
-    }
-    uint4 lo[2][NL], hi[2][NL];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        lo[h][i] = there[h] ? ldg16(b[h] + i * 32) : make_uint4(0, 0, 0, 0);
-        hi[h][i] = there[h] ? ldg16(b[h] + P.ld + i * 32) : make_uint4(0, 0, 0, 0);
-      }
-    float best[2] = {-INFINITY, -INFINITY};
-    for (int h0 = 0; h0 < P.G; h0 += 8) {
-      float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const uint4 raw = h0 + gid < P.G ? ldg16(q + (int64_t)(g * P.G + h0 + gid) * HD + i * 32) : make_uint4(0, 0, 0, 0);
-        const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
-        uint32_t up[4], down[4];
-        const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162 *>(&x[k]);
-          const __nv_bfloat162 p = __hmax2(v, zero), n = __hmin2(v, zero);
-          up[k] = *reinterpret_cast<const uint32_t *>(&p);
-          down[k] = *reinterpret_cast<const uint32_t *>(&n);
+    for (int k = 0; k < PER; ++k) {
+      n[k] = 0;
+      const int i = i0 + k;
+      if (k < per && i < S) {
+        const int rows = paged_rows(P.kv, i, P.n_rows, status), kv = __ldg(P.kv.kv_lens + i);
+        int tiles = 0;
+        if (rows > 0) {
+          if (kv < 0 || kv > P.max_kv || kv > (int64_t)P.kv.max_pages * page_size) {
+            report(status, CB_ERR_DEVICE_INDEX);
+          } else {
+            const int pages = kv > 0 ? ((kv - 1) >> shift) + 1 : 0;
+            if (pages > P.n_picks) tiles = (pages - P.n_first - P.n_last + 15) / 16;
+          }
         }
-        const uint32_t a0[4] = {hi[0][i].x, hi[1][i].x, hi[0][i].y, hi[1][i].y};
-        const uint32_t a1[4] = {hi[0][i].z, hi[1][i].z, hi[0][i].w, hi[1][i].w};
-        const uint32_t d0[4] = {lo[0][i].x, lo[1][i].x, lo[0][i].y, lo[1][i].y};
-        const uint32_t d1[4] = {lo[0][i].z, lo[1][i].z, lo[0][i].w, lo[1][i].w};
-        paged::mma16816(c, a0, up[0], up[1]);
-        paged::mma16816(c, a1, up[2], up[3]);
-        paged::mma16816(c, d0, down[0], down[1]);
-        paged::mma16816(c, d1, down[2], down[3]);
+        line.tiles[i] = tiles;
+        n[k] = (int64_t)rows * tiles;
+        sum += n[k];
+      }
+    }
+    int64_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) s_sums[warp] = incl;
+    __syncthreads();
+    int64_t first = incl - sum;
+    for (int w = 0; w < warp; ++w) first += s_sums[w];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      if (k < per && i0 + k < S) line.begin[i0 + k] = first;
+      first += n[k];
+    }
+    if (threadIdx.x == kSThreads - 1) line.begin[S] = first;
+    __syncthreads();
+  }
+  const int64_t units = line.begin[S] * P.Hkv;
+  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+  const uint32_t ring = smem_u32(smem) + warp * kTStages * kStage;
+  // A unit's tile: row r, head g, pages j .. j + count - 1 (0: nothing), and in lanes 0..15
+  // their places in the pool (-1: none).
+  struct Tile { int r, g, j, count, page; };
+  int s = -1, row0 = 0, n = 0, kv = 0;
+  auto describe = [&](int64_t u) -> Tile {
+    Tile t = {0, 0, 0, 0, -1};
+    if (u >= u1) return t;
+    int64_t tile;
+    if (units >> 31 == 0) {             // (a 64-bit division is several times slower)
+      tile = P.by_heads.div((int)u);
+      t.g = (int)u - (int)tile * P.Hkv;
+    } else {
+      tile = u / P.Hkv;
+      t.g = (int)(u - tile * P.Hkv);
+    }
+    if (s < 0 || line.begin[s + 1] <= tile) {
+      int lo = max(s, 0), hi = S - 1;   // the last sequence that begins at or before the tile
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (line.begin[mid] <= tile) lo = mid; else hi = mid - 1;
+      }
+      s = lo;
+      row0 = __ldg(P.kv.row_offsets + s);
+      n = __ldg(P.kv.row_offsets + s + 1) - row0;
+      kv = __ldg(P.kv.kv_lens + s);
+    }
+    const int64_t local = tile - line.begin[s];
+    const int per = line.tiles[s], i = n == 1 ? 0 : (int)(local / per);
+    const int pos = kv - n + i, pages = pos < 0 ? 0 : (pos >> shift) + 1;
+    t.r = row0 + i;
+    t.j = P.n_first + (int)(local - (int64_t)i * per) * 16;
+    // 0: the row has fewer pages than the sequence's last, or takes all
+    t.count = pages > P.n_picks ? max(0, min(16, pages - P.n_last - t.j)) : 0;
+    if (lane < t.count) t.page = paged_page(P.kv, s, t.j + lane, status);
+    return t;
+  };
+  // Its bounds to a stage: a warp copies a page's two at once.  16-byte columns are swizzled
+  // by the page so that ldmatrix meets all banks.
+  auto load = [&](const Tile &t, int st) {
+    constexpr int kCols = kBytes / 16, kPages = 16 / kCols;      // pages of one copy (1 or 2)
+    const int x = lane / (2 * kCols), half = lane / kCols & 1, col = lane % kCols;
+    const bf16 *src = reinterpret_cast<const bf16 *>(P.bounds) + half * P.ld + t.g * HD + col * 8;
+    uint32_t dst = ring + st * kStage + half * kBytes;
+    if (__all_sync(0xffffffffu, t.page >= 0 || lane >= 16)) {
+#pragma unroll
+      for (int i = 0; i < 16 / kPages; ++i) {
+        const int p = i * kPages + x, page = __shfl_sync(0xffffffffu, t.page, p);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + p * 2 * kBytes + ((col ^ (p & 7)) << 4)),
+                     "l"(src + page * P.page_stride) : "memory");
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16 / kPages; ++i) {
+        const int p = i * kPages + x, page = __shfl_sync(0xffffffffu, t.page, p);
+        paged::copy16(dst + p * 2 * kBytes + ((col ^ (p & 7)) << 4), src + (page < 0 ? 0 : page * P.page_stride), page >= 0);
+      }
+    }
+  };
+  auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+  // tiles in flight, the first of them to be scored next; places are looked up one tile
+  // ahead of the bounds
+  Tile wait[kTStages];
+  const int64_t first = u0 + warp;
+  constexpr int kStep = kSThreads / 32;
+#pragma unroll
+  for (int i = 0; i < kTStages; ++i) wait[i] = describe(first + i * kStep);
+#pragma unroll
+  for (int i = 0; i < kTStages - 1; ++i) {
+    if (wait[i].count) load(wait[i], i);
+    commit();
+  }
+  uint32_t up[HD / 8], down[HD / 8];
+  int q_row = -1, q_head = -1, q_first = -1;
+  int st = 0, fill = kTStages - 1;
+  for (int64_t u = first; u < u1; u += kStep) {
+    const Tile t = wait[0];
+    asm volatile("cp.async.wait_group %0;" ::"n"(kTStages - 2) : "memory");
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i + 1 < kTStages; ++i) wait[i] = wait[i + 1];
+    if (wait[kTStages - 2].count) load(wait[kTStages - 2], fill);
+    commit();
+    wait[kTStages - 1] = describe(u + kTStages * kStep);
+    const uint32_t stage = ring + st * kStage;
+    st = st + 1 == kTStages ? 0 : st + 1;
+    fill = fill + 1 == kTStages ? 0 : fill + 1;
+    if (!t.count) continue;
+    const int g = t.g, r = t.r, j = t.j, j1 = t.j + t.count;
+    const bf16 *q = reinterpret_cast<const bf16 *>(P.q) + r * P.ld_q + (int64_t)g * P.G * HD + q4 * 2;
+    // ldmatrix: lanes 0..7 the first eight pages' eight dimensions, 8..15 the other pages',
+    // 16..31 the next dimensions
+    const int page = lane & 15;
+    const uint32_t rows = stage + page * 2 * kBytes;
+    float best[2] = {-INFINITY, -INFINITY};
+    const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+    __nv_bfloat162 least[2] = {zero, zero}, most[2] = {zero, zero};     // of pages gid and gid + 8
+    for (int h0 = 0; h0 < P.G; h0 += 8) {
+      // q^+ and q^- of this lane's head: kept while the row and the heads stay
+      if (r != q_row || g != q_head || h0 != q_first) {
+        q_row = r;
+        q_head = g;
+        q_first = h0;
+#pragma unroll
+        for (int k = 0; k < HD / 8; ++k) {
+          uint32_t x = 0;
+          if (h0 + gid < P.G) x = __ldg(reinterpret_cast<const uint32_t *>(q + (int64_t)(h0 + gid) * HD + k * 8));
+          const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162 *>(&x);
+          const __nv_bfloat162 p = __hmax2(v, zero), m = __hmin2(v, zero);
+          up[k] = *reinterpret_cast<const uint32_t *>(&p);
+          down[k] = *reinterpret_cast<const uint32_t *>(&m);
+        }
+      }
+      float c[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < HD / 16; ++k) {
+        uint32_t lo[4], hi[4];
+        const uint32_t at = rows + (((2 * k + (lane >> 4)) ^ (page & 7)) << 4);
+        paged::ldsm_x4(at, lo);
+        paged::ldsm_x4(at + kBytes, hi);
+        paged::mma16816(c, hi, up[2 * k], up[2 * k + 1]);
+        paged::mma16816(d, lo, down[2 * k], down[2 * k + 1]);
+        if (h0 == 0) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            least[e & 1] = __hmin2(least[e & 1], *reinterpret_cast<const __nv_bfloat162 *>(&lo[e]));
+            most[e & 1] = __hmax2(most[e & 1], *reinterpret_cast<const __nv_bfloat162 *>(&hi[e]));
+          }
+        }
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (h0 + 2 * q4 + (k & 1) < P.G) best[k >> 1] = fmaxf(best[k >> 1], c[k]);
+      for (int e = 0; e < 4; ++e)
+        if (h0 + 2 * q4 + (e & 1) < P.G) best[e >> 1] = fmaxf(best[e >> 1], c[e] + d[e]);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);
+      // the largest |bound|: of the maxima, or of the minima's opposites
+      float top = fmaxf(fmaxf(__low2float(most[h]), __high2float(most[h])), -fminf(__low2float(least[h]), __high2float(least[h])));
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const uint32_t x[8] = {lo[h][i].x, lo[h][i].y, lo[h][i].z, lo[h][i].w, hi[h][i].x, hi[h][i].y, hi[h][i].z, hi[h][i].w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&x[k])));
-      }
-      float top = fmaxf(__low2float(top2), __high2float(top2));
-#pragma unroll
-      for (int d = 1; d < 4; d <<= 1) {
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        best[h] = fmaxf(best[h], __shfl_xor_sync(0xffffffffu, best[h], d));
+      for (int o = 1; o < 4; o <<= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        best[h] = fmaxf(best[h], __shfl_xor_sync(0xffffffffu, best[h], o));
       }
       const int jj = j + gid + 8 * h;
+      const bool there = __shfl_sync(0xffffffffu, t.page, gid + 8 * h) >= 0;
       if (q4 == 0 && jj < j1)
-        P.approx[((int64_t)r * P.Hkv + g) * P.held + jj] = there[h] ? make_float2(best[h], top) : make_float2(-INFINITY, 0.f);
+        P.approx[((int64_t)r * P.Hkv + g) * P.held + jj] = there ? make_float2(best[h], top) : make_float2(-INFINITY, 0.f);
     }
   }
 }
 
 // ---------------------------------------------------------------- choice --
-constexpr int kCThreads = 512;
-
-// Sum of v over the block's threads before this one, and the whole.
-__device__ __forceinline__ int block_scan(int v, int *s_warp, int &total) {
+// Sum of v over the block's NT threads before this one, and the whole.
+template <int NT> __device__ __forceinline__ int block_scan(int v, int *s_warp, int &total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int incl = v;
 #pragma unroll
@@ -317,32 +449,62 @@ __device__ __forceinline__ int block_scan(int v, int *s_warp, int &total) {
   __syncthreads();
   if (lane == 31) s_warp[warp] = incl;
   __syncthreads();
-  int before = incl - v;
-  total = 0;
+  const int sum = lane < NT / 32 ? s_warp[lane] : 0;
+  int upto = sum;
 #pragma unroll
-  for (int w = 0; w < kCThreads / 32; ++w) {
-    if (w < warp) before += s_warp[w];
-    total += s_warp[w];
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
   }
+  total = __shfl_sync(0xffffffffu, upto, 31);
+  const int before = __shfl_sync(0xffffffffu, upto - sum, warp) + incl - v;
   return before;
 }
 
-constexpr int kBins = 2048, kHeld = 16;  // bins of a histogram; scores a thread keeps in registers
+constexpr int kBins = 2048, kHeld = 8;  // bins of a histogram; scores a thread keeps in registers
 constexpr int kFew = 32;                // candidates that need no narrower bins
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(kCThreads)
+// Sums in pairs of floats: (hi, lo) + x, with the sum's rounding kept in lo.
+__device__ __forceinline__ void add_exact(float &hi, float &lo, float x) {
+  const float s = hi + x, t = s - hi;
+  lo += (hi - (s - t)) + (x - t);
+  hi = s;
+}
+// x y as a pair (__fmul_rn: the rounded product, whatever it is added to).
+__device__ __forceinline__ void add_product(float &hi, float &lo, float x, float y) {
+  const float p = __fmul_rn(x, y);
+  lo += fmaf(x, y, -p);
+  add_exact(hi, lo, p);
+}
+
+// kCThreads: 256 for up to 2048 pages, all in registers, 1024 for more.
+template <typename T, int HD, int kCThreads>
+__global__ void __launch_bounds__(kCThreads, 1024 / kCThreads)
 paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
   constexpr int NW = kCThreads / 32;
   __shared__ RowPlace s_row;
   __shared__ int s_hist[kBins], s_warp[NW], s_bin, s_in, s_count;
   __shared__ float s_f[4][NW];
-  grid_dep_wait();
-  grid_dep_launch();
+  __shared__ unsigned s_mask[kCThreads];
+  static_assert(kCThreads <= kBins, "the masks' places reuse the bins");
+  if (!P.scored) grid_dep_wait();
   const int g = blockIdx.x % P.Hkv, r = blockIdx.x / P.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const RowPlace at = find_row<kCThreads>(P.kv, P.n_rows, r, &s_row, nullptr);
   const int pages = pages_of(P, at, nullptr);
   int32_t *out = P.picks + ((int64_t)r * P.Hkv + g) * P.n_picks;
+  const int want = P.n_picks - P.n_first - P.n_last;        // of the scored pages are picked, fewer than there are
+  const T *q = reinterpret_cast<const T *>(P.q) + r * P.ld_q + (int64_t)g * P.G * HD;
+  float norm = 0.f;                                         // |q|_1 of this warp's heads
+  if (pages > P.n_picks && want > 0)
+    for (int h = warp; h < P.G; h += NW) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = lane; i < HD; i += 32) s += fabsf(to_f(q[h * HD + i]));
+      norm = fmaxf(norm, warp_sum(s));
+    }
+  // what was read so far was there before the scores' kernel began, which waited for it
+  if (P.scored) grid_dep_wait();
+  grid_dep_launch();
   if (pages < 0) return;
   if (pages <= P.n_picks) {
     for (int i = tid; i < P.n_picks; i += kCThreads) out[i] = i < pages ? i : -1;
@@ -350,10 +512,9 @@ paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
   }
   const int64_t base = ((int64_t)r * P.Hkv + g) * P.held;
   float2 *a = P.approx + base;
-  double *exact = P.exact + base;
+  float2 *exact = P.exact + base;
   int *list = P.list + base;
   const int lo = P.n_first, hi = pages - P.n_last;          // scored pages
-  const int want = P.n_picks - P.n_first - P.n_last;        // of them are picked, fewer than there are
   float sure = INFINITY, none = INFINITY;                   // above: in; below: out; between: scored exactly
   // scores lo + tid + i * kCThreads, the first kHeld of them in registers
   float held[kHeld];
@@ -364,8 +525,7 @@ paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
     for (int j = lo + tid + kHeld * kCThreads; j < hi; j += kCThreads) f(j, a[j].x);
   };
   if (want > 0) {
-    const T *q = reinterpret_cast<const T *>(P.q) + r * P.ld_q + (int64_t)g * P.G * HD;
-    float v[4] = {-INFINITY, -INFINITY, 0.f, 0.f};          // largest score, largest negative, |bound|, |q|_1
+    float v[4] = {-INFINITY, -INFINITY, 0.f, norm};          // largest score, largest negative, |bound|, |q|_1
     int finite = 0, in_pool;
     auto take = [&](float2 x) {
       if (x.x > -INFINITY) {                                // (a page outside the pool has -inf)
@@ -383,12 +543,6 @@ paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
       take(x);
     }
     for (int j = lo + tid + kHeld * kCThreads; j < hi; j += kCThreads) take(a[j]);
-    for (int h = warp; h < P.G; h += NW) {
-      float s = 0.f;
-#pragma unroll
-      for (int i = lane; i < HD; i += 32) s += fabsf(to_f(q[h * HD + i]));
-      v[3] = fmaxf(v[3], warp_sum(s));
-    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       v[k] = warp_max(v[k]);
@@ -396,10 +550,9 @@ paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      for (int w = 0; w < NW; ++w) v[k] = fmaxf(v[k], s_f[k][w]);
+    for (int k = 0; k < 4; ++k) v[k] = warp_max(lane < NW ? s_f[k][lane] : v[k]);
     const float eps = 0x1p-15f * v[3] * v[2];
-    block_scan(finite, s_warp, in_pool);
+    block_scan<kCThreads>(finite, s_warp, in_pool);
     // [from, to] holds the score in the last place that fits: bins over it, the one with
     // that place in turn, until few scores (or nothing to tell apart) are left
     float from = -v[1], to = v[0];
@@ -419,7 +572,7 @@ paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
       int n[PER], sum = 0, all;
 #pragma unroll
       for (int i = 0; i < PER; ++i) sum += n[i] = s_hist[kBins - 1 - tid * PER - i];
-      int before = above + block_scan(sum, s_warp, all);
+      int before = above + block_scan<kCThreads>(sum, s_warp, all);
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         if (before < want && before + n[i] >= want) {
@@ -440,7 +593,7 @@ paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
       // (with the slack the range may hold scores of the neighbouring bins: count anew)
       int over = 0;
       each([&](int, float x) { over += x > to; });
-      block_scan(over, s_warp, above);
+      block_scan<kCThreads>(over, s_warp, above);
       __syncthreads();
     }
     // (all pages of the pool, and some outside, where those do not suffice)
@@ -456,24 +609,32 @@ paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
       if (x > sure) ++in;
       else if (x >= none) list[atomicAdd(&s_count, 1)] = j;
     });
-  block_scan(in, s_warp, total);
+  block_scan<kCThreads>(in, s_warp, total);
   const int need = want - total;                            // of the pages between
   __syncthreads();
   if (s_count > need) {
-    const T *q = reinterpret_cast<const T *>(P.q) + r * P.ld_q + (int64_t)g * P.G * HD;
     for (int c = warp; c < s_count; c += NW) {
       const int page = paged_page(P.kv, at.s, list[c], nullptr);
-      double best = -INFINITY;
+      float2 best = make_float2(-INFINITY, 0.f);
       if (page >= 0) {
         const T *b = reinterpret_cast<const T *>(P.bounds) + page * P.page_stride + g * HD;
         for (int h = 0; h < P.G; ++h) {
-          double sum = 0.0;
+          float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int i = lane; i < HD; i += 32) {
             const float y = to_f(q[h * HD + i]);
-            sum += (double)y * (double)to_f(y > 0.f ? b[P.ld + i] : b[i]);
+            add_product(sum.x, sum.y, y, to_f(y > 0.f ? b[P.ld + i] : b[i]));
           }
-          best = fmax(best, warp_sum_d(sum));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            const float x = __shfl_xor_sync(0xffffffffu, sum.x, o), y = __shfl_xor_sync(0xffffffffu, sum.y, o);
+            // (both lanes of a pair add the same two numbers in the same order)
+            float hi = lane & o ? x : sum.x, lo = sum.y + y;
+            add_exact(hi, lo, lane & o ? sum.x : x);
+            sum = make_float2(hi, lo);
+          }
+          const float hi = sum.x + sum.y, lo = sum.y - (hi - sum.x);   // one pair for one sum
+          if (hi > best.x || (hi == best.x && lo > best.y)) best = make_float2(hi, lo);
         }
       }
       if (lane == 0) exact[c] = best;
@@ -485,27 +646,40 @@ paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
     const int j = list[c];
     int better = 0;
     if (s_count > need) {
-      const double e = exact[c];
+      const float2 e = exact[c];
       for (int k = 0; k < s_count && better < need; ++k) {
-        const double f = exact[k];
-        better += f > e || (f == e && list[k] < j);
+        const float2 f = exact[k];
+        better += f.x > e.x || (f.x == e.x && (f.y > e.y || (f.y == e.y && list[k] < j)));
       }
     }
     a[j].y = better < need ? -1.f : -2.f;
   }
   __syncthreads();
+  // ascending: a mask for every 32 pages, one scan over the masks of 32 kCThreads pages
   int written = 0;
-  for (int j0 = 0; j0 < pages; j0 += kCThreads) {
-    const int j = j0 + tid;
-    bool pick = j < pages && (j < lo || j >= hi);
-    if (j >= lo && j < hi && want > 0) {
-      const float2 x = a[j];
-      pick = x.y < 0.f ? x.y == -1.f : x.x > sure;
+  for (int j0 = 0; j0 < pages; j0 += 32 * kCThreads) {
+    const int groups = min(kCThreads, (pages - j0 + 31) / 32);
+    for (int k = warp; k < groups; k += NW) {
+      const int j = j0 + k * 32 + lane;
+      bool pick = j < pages && (j < lo || j >= hi);
+      if (j >= lo && j < hi && want > 0) {
+        const float2 x = a[j];
+        pick = x.y < 0.f ? x.y == -1.f : x.x > sure;
+      }
+      const unsigned mask = __ballot_sync(0xffffffffu, pick);
+      if (lane == 0) s_mask[k] = mask;
     }
+    __syncthreads();
     int n;
-    const int before = block_scan(pick, s_warp, n);
-    if (pick) out[written + before] = j;
+    const int before = block_scan<kCThreads>(tid < groups ? __popc(s_mask[tid]) : 0, s_warp, n);
+    s_hist[tid] = written + before;
+    __syncthreads();
+    for (int k = warp; k < groups; k += NW) {
+      const unsigned mask = s_mask[k];
+      if (mask >> lane & 1) out[s_hist[k] + __popc(mask & ((1u << lane) - 1))] = j0 + k * 32 + lane;
+    }
     written += n;
+    __syncthreads();
   }
 }
 
@@ -532,23 +706,33 @@ cudaError_t launch_paged_bounds(const PagedKV &kv, const cb_page_bounds &b, cb_d
 static int64_t held_pages(int max_kv, int page_size) { return ((int64_t)max_kv + page_size - 1) / page_size; }
 
 size_t paged_select_ws_bytes(int n_rows, int max_kv, int page_size, int Hkv) {
-  return (size_t)n_rows * Hkv * held_pages(max_kv, page_size) * (sizeof(float2) + sizeof(double) + sizeof(int));
+  return (size_t)n_rows * Hkv * held_pages(max_kv, page_size) * (sizeof(float2) + sizeof(float2) + sizeof(int));
 }
 
 template <typename T, int HD>
 static cudaError_t run_select(const pages::SelectParams &P, int *status, cudaStream_t s) {
   using namespace pages;
   int n = 0;
-  if (P.held > P.n_picks) {
+  if (P.scored) {
     cudaError_t e;
-    if constexpr (std::is_same<T, bf16>::value)
-      e = launch_pdl(paged_score_tc_kernel<HD>, dim3(P.parts * P.n_rows), dim3(kSThreads), 0, s, P, status);
-    else
+    if constexpr (std::is_same<T, bf16>::value) {
+      constexpr int kSmem = kSThreads / 32 * kTStages * 16 * 2 * HD * 2;
+      static PerDeviceOnce attr;
+      e = attr.run([](int) {
+        return cudaFuncSetAttribute(paged_score_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      });
+      if (e == cudaSuccess)
+        e = launch_pdl(paged_score_tc_kernel<HD>, dim3(device_sm_count()), dim3(kSThreads), kSmem, s, P, status);
+    } else {
       e = launch_pdl(paged_score_kernel<T, HD>, dim3(P.parts * P.Hkv * P.n_rows), dim3(kSThreads), 0, s, P, status);
+    }
     if (e != cudaSuccess) return e;
     ++n;
   }
-  const cudaError_t e = launch_pdl(paged_choose_kernel<T, HD>, dim3(P.Hkv * P.n_rows), dim3(kCThreads), 0, s, P, status);
+  const dim3 grid(P.Hkv * P.n_rows);
+  const cudaError_t e = P.held <= 256 * kHeld
+      ? launch_pdl(paged_choose_kernel<T, HD, 256>, grid, dim3(256), 0, s, P, status)
+      : launch_pdl(paged_choose_kernel<T, HD, 1024>, grid, dim3(1024), 0, s, P, status);
   return e == cudaSuccess ? launched(n + 1) : e;
 }
 
@@ -571,11 +755,12 @@ cudaError_t launch_paged_select(const PagedKV &kv, const cb_page_bounds &b, cons
   P.n_picks = a.n_picks;
   P.n_first = a.n_first;
   P.n_last = a.n_last;
+  P.by_heads = paged::Divisor(P.Hkv);
+  P.scored = P.held > P.n_picks;
   P.approx = reinterpret_cast<float2 *>(a.ws);
   const size_t all = (size_t)b.n_rows * P.Hkv * P.held;
-  P.exact = reinterpret_cast<double *>(P.approx + all);
+  P.exact = P.approx + all;
   P.list = reinterpret_cast<int *>(P.exact + all);
-  static_assert(pages::kSPages == pages::kTPages, "pages of a block");
   P.parts = (P.held + pages::kSPages - 1) / pages::kSPages;
   if ((int64_t)P.parts * P.Hkv * b.n_rows > 0x7fffffffLL || (int64_t)P.Hkv * b.n_rows > 0x7fffffffLL)
     return cudaErrorInvalidConfiguration;
