@@ -437,6 +437,13 @@ paged_score_tc_kernel(const __grid_constant__ SelectParams P, int *status) {
 }
 
 // ---------------------------------------------------------------- choice --
+// The largest v of the warp (redux.sync of floats: one instruction in place of ten).
+__device__ __forceinline__ float warp_top(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // Sum of v over the block's NT threads before this one, and the whole.
 template <int NT> __device__ __forceinline__ int block_scan(int v, int *s_warp, int &total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -463,6 +470,7 @@ template <int NT> __device__ __forceinline__ int block_scan(int v, int *s_warp, 
 
 constexpr int kBins = 2048, kHeld = 8;  // bins of a histogram; scores a thread keeps in registers
 constexpr int kFew = 32;                // candidates that need no narrower bins
+constexpr int kPairs = 8;               // pages, and heads, scored exactly at a time
 
 // Sums in pairs of floats: (hi, lo) + x, with the sum's rounding kept in lo.
 __device__ __forceinline__ void add_exact(float &hi, float &lo, float x) {
@@ -483,9 +491,10 @@ __global__ void __launch_bounds__(kCThreads, 1024 / kCThreads)
 paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
   constexpr int NW = kCThreads / 32;
   __shared__ RowPlace s_row;
-  __shared__ int s_hist[kBins], s_warp[NW], s_bin, s_in, s_count;
+  __shared__ int s_hist[kBins + kBins / 32], s_warp[NW], s_bin, s_in, s_count;
   __shared__ float s_f[4][NW];
   __shared__ unsigned s_mask[kCThreads];
+  __shared__ float2 s_pair[kPairs * kPairs];
   static_assert(kCThreads <= kBins, "the masks' places reuse the bins");
   if (!P.scored) grid_dep_wait();
   const int g = blockIdx.x % P.Hkv, r = blockIdx.x / P.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -543,35 +552,38 @@ paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
       take(x);
     }
     for (int j = lo + tid + kHeld * kCThreads; j < hi; j += kCThreads) take(a[j]);
+    finite = __reduce_add_sync(0xffffffffu, finite);
+    if (lane == 0) s_warp[warp] = finite;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      v[k] = warp_max(v[k]);
+      v[k] = warp_top(v[k]);
       if (lane == 0) s_f[k][warp] = v[k];
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = warp_max(lane < NW ? s_f[k][lane] : v[k]);
+    for (int k = 0; k < 4; ++k) v[k] = warp_top(lane < NW ? s_f[k][lane] : v[k]);
     const float eps = 0x1p-15f * v[3] * v[2];
-    block_scan<kCThreads>(finite, s_warp, in_pool);
+    in_pool = __reduce_add_sync(0xffffffffu, lane < NW ? s_warp[lane] : 0);
     // [from, to] holds the score in the last place that fits: bins over it, the one with
     // that place in turn, until few scores (or nothing to tell apart) are left
     float from = -v[1], to = v[0];
     int above = 0;                                          // scores above `to`
     for (int round = 0; round < 8 && in_pool >= want; ++round) {
-      for (int i = tid; i < kBins; i += kCThreads) s_hist[i] = 0;
+      for (int i = tid; i < kBins + kBins / 32; i += kCThreads) s_hist[i] = 0;
       __syncthreads();
       const float width = to - from, inv = kBins / width;
       if (!(width > 2.f * eps) || !(inv < INFINITY)) break;
+      auto place = [](int b) { return b + (b >> 5); };       // so that a scan's threads meet all banks
       auto bin = [&](float x) { return min(kBins - 1, (int)((x - from) * inv)); };
       each([&](int, float x) {
-        if (x >= from && x <= to) atomicAdd(&s_hist[bin(x)], 1);
+        if (x >= from && x <= to) atomicAdd(&s_hist[place(bin(x))], 1);
       });
       __syncthreads();
       // thread t: bins from the largest down, kBins / kCThreads of them
       constexpr int PER = kBins / kCThreads;
       int n[PER], sum = 0, all;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) sum += n[i] = s_hist[kBins - 1 - tid * PER - i];
+      for (int i = 0; i < PER; ++i) sum += n[i] = s_hist[place(kBins - 1 - tid * PER - i)];
       int before = above + block_scan<kCThreads>(sum, s_warp, all);
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
@@ -613,33 +625,48 @@ paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
   const int need = want - total;                            // of the pages between
   __syncthreads();
   if (s_count > need) {
-    for (int c = warp; c < s_count; c += NW) {
-      const int page = paged_page(P.kv, at.s, list[c], nullptr);
-      float2 best = make_float2(-INFINITY, 0.f);
-      if (page >= 0) {
-        const T *b = reinterpret_cast<const T *>(P.bounds) + page * P.page_stride + g * HD;
-        for (int h = 0; h < P.G; ++h) {
-          float2 sum = make_float2(0.f, 0.f);
+    // a warp takes a page and, of up to eight heads, one; the largest of a page's heads
+    // afterwards
+    const int heads = min(P.G, kPairs);
+    for (int c0 = 0; c0 < s_count; c0 += kPairs) {
+      const int pairs = min(kPairs, s_count - c0) * heads;
+      for (int k = warp; k < pairs; k += NW) {
+        const int page = paged_page(P.kv, at.s, list[c0 + k / heads], nullptr);
+        float2 best = make_float2(-INFINITY, 0.f);
+        if (page >= 0) {
+          const T *b = reinterpret_cast<const T *>(P.bounds) + page * P.page_stride + g * HD;
+          for (int h = k % heads; h < P.G; h += heads) {
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int i = lane; i < HD; i += 32) {
-            const float y = to_f(q[h * HD + i]);
-            add_product(sum.x, sum.y, y, to_f(y > 0.f ? b[P.ld + i] : b[i]));
-          }
+            for (int i = lane; i < HD; i += 32) {
+              const float y = to_f(q[h * HD + i]);
+              add_product(sum.x, sum.y, y, to_f(y > 0.f ? b[P.ld + i] : b[i]));
+            }
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) {
-            const float x = __shfl_xor_sync(0xffffffffu, sum.x, o), y = __shfl_xor_sync(0xffffffffu, sum.y, o);
-            // (both lanes of a pair add the same two numbers in the same order)
-            float hi = lane & o ? x : sum.x, lo = sum.y + y;
-            add_exact(hi, lo, lane & o ? sum.x : x);
-            sum = make_float2(hi, lo);
+            for (int o = 16; o > 0; o >>= 1) {
+              const float x = __shfl_xor_sync(0xffffffffu, sum.x, o), y = __shfl_xor_sync(0xffffffffu, sum.y, o);
+              // (both lanes of a pair add the same two numbers in the same order)
+              float hi = lane & o ? x : sum.x, lo = sum.y + y;
+              add_exact(hi, lo, lane & o ? sum.x : x);
+              sum = make_float2(hi, lo);
+            }
+            const float hi = sum.x + sum.y, lo = sum.y - (hi - sum.x);   // one pair for one sum
+            if (hi > best.x || (hi == best.x && lo > best.y)) best = make_float2(hi, lo);
           }
-          const float hi = sum.x + sum.y, lo = sum.y - (hi - sum.x);   // one pair for one sum
-          if (hi > best.x || (hi == best.x && lo > best.y)) best = make_float2(hi, lo);
         }
+        if (lane == 0) s_pair[k] = best;
       }
-      if (lane == 0) exact[c] = best;
+      __syncthreads();
+      if (tid < kPairs && c0 + tid < s_count) {
+        float2 best = s_pair[tid * heads];
+        for (int h = 1; h < heads; ++h) {
+          const float2 x = s_pair[tid * heads + h];
+          if (x.x > best.x || (x.x == best.x && x.y > best.y)) best = x;
+        }
+        exact[c0 + tid] = best;
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
   // their ranks: -1 in place of the bound of a page that is picked, -2 of one that is not
   for (int c = tid; c < s_count; c += kCThreads) {
