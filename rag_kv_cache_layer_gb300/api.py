@@ -5,6 +5,7 @@ library.  PyTorch is used only to own device memory and streams.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import math
 from dataclasses import dataclass, field
 
@@ -201,8 +202,8 @@ def _table(row_offsets, kv_lens, block_table):
     n_seq, width = block_table.shape
     ld_table, one = block_table.stride()
     if not kv_lens.dtype is row_offsets.dtype is block_table.dtype is _I32 or (one != 1 and width > 1) or \
-            kv_lens.shape != (n_seq,) or row_offsets.shape != (n_seq + 1,) or \
-            not (kv_lens.is_contiguous() and row_offsets.is_contiguous()):
+            not kv_lens.dim() == row_offsets.dim() == 1 or kv_lens.numel() != n_seq or \
+            row_offsets.numel() != n_seq + 1 or not (kv_lens.is_contiguous() and row_offsets.is_contiguous()):
         raise ValueError("row_offsets [n_seq + 1], kv_lens [n_seq] and block_table [n_seq, max_pages] "
                          "must be int32 with contiguous rows")
     return n_seq, width, ld_table if n_seq > 1 else width
@@ -329,6 +330,7 @@ def cb_paged_attention(q, row_offsets, kv_lens, block_table, k_pages, v_pages, n
 
 
 # ----------------------------------------------- generation: 4-bit cache --
+@functools.lru_cache(maxsize=None)      # asked for by every call
 def cb_paged4_page_bytes(page_size, n_kv_heads, head_dim):
     """Bytes of a page of a 4-bit cache: a pool is uint8 [n_pages, that many]."""
     n = lib.cb_paged4_page_bytes(page_size, n_kv_heads, head_dim)
@@ -353,13 +355,13 @@ def _paged4_kv(dev, pages, page_size, row_offsets, kv_lens, block_table, k_exp, 
                      k_exp, v_exp), shape
 
 
-def _paged4_rows(dev, k, v, pages, page_size, head_dim):
+def _paged4_rows(dev, k, v, pages, shape, page_size, head_dim):
     """First layer's rows, number of layers and strides of k and v [(layers,) rows, row] and the pool."""
     if not k.get_device() == v.get_device() == dev:
         _device_error(dev, k, v)
     layers, sk, sv, sc = 1, 0, 0, 0
-    if pages.dim() == 3:
-        layers = pages.shape[0]
+    if len(shape) == 3:
+        layers = shape[0]
         if k.dim() != 3 or v.shape != k.shape or k.shape[0] != layers:
             raise ValueError("the rows must have the pool's layer dimension")
         sk, sv, sc = k.stride(0), v.stride(0), pages.stride(0)
@@ -370,7 +372,7 @@ def _paged4_rows(dev, k, v, pages, page_size, head_dim):
     cols = k.shape[-1]
     if cols % head_dim:
         raise ValueError("head_dim must divide the rows")
-    if pages.shape[-1] < cb_paged4_page_bytes(page_size, cols // head_dim, head_dim):
+    if shape[-1] < cb_paged4_page_bytes(page_size, cols // head_dim, head_dim):
         raise ValueError("the pool's pages are smaller than these rows need")
     return k, v, layers, sk, sv, sc, cols
 
@@ -383,8 +385,8 @@ def cb_paged4_append(k_new, v_new, row_offsets, kv_lens, block_table, pages, pag
     have one).  Values are stored divided by 2^k_exp and 2^v_exp: the format
     reaches from 2^-10 to 2688."""
     dev = _cur_device()
-    kv, _ = _paged4_kv(dev, pages, page_size, row_offsets, kv_lens, block_table, k_exp, v_exp)
-    k1, v1, layers, sk, sv, sc, cols = _paged4_rows(dev, k_new, v_new, pages, page_size, head_dim)
+    kv, shape = _paged4_kv(dev, pages, page_size, row_offsets, kv_lens, block_table, k_exp, v_exp)
+    k1, v1, layers, sk, sv, sc, cols = _paged4_rows(dev, k_new, v_new, pages, shape, page_size, head_dim)
     if layers == 0:
         return
     dt, n_rows = k_new.dtype, k1.shape[0]
@@ -423,8 +425,8 @@ def cb_paged4_gather(row_offsets, kv_lens, block_table, pages, page_size, head_d
     row], or with the pool's layer dimension; bf16 or float32) gets what its
     position holds; arguments as for cb_paged4_append."""
     dev = _cur_device()
-    kv, _ = _paged4_kv(dev, pages, page_size, row_offsets, kv_lens, block_table, k_exp, v_exp)
-    k1, v1, layers, sk, sv, sc, cols = _paged4_rows(dev, k_out, v_out, pages, page_size, head_dim)
+    kv, shape = _paged4_kv(dev, pages, page_size, row_offsets, kv_lens, block_table, k_exp, v_exp)
+    k1, v1, layers, sk, sv, sc, cols = _paged4_rows(dev, k_out, v_out, pages, shape, page_size, head_dim)
     if layers == 0:
         return
     dt, n_rows = k_out.dtype, k1.shape[0]

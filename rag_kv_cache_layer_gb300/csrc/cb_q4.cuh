@@ -66,19 +66,60 @@ __device__ __forceinline__ float divide_odd(float x, float s, float inv) {
   return __uint_as_float(b | 1u);
 }
 
+__device__ __forceinline__ float reciprocal(float x) {      // to a step or two
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // The scale of a group whose largest magnitude is a (as an 8-bit float): a / 6 to
 // the nearest, ties to even, within [2^-9, 448]; and its value.
 template <typename T>
 __device__ __forceinline__ uint32_t scale_of(float a, float &value) {
-  // bf16: a has 8 bits, so a / 6 is a border between two scales (5 bits) or at least
-  // 2^-9 of itself away from one, and its rounding to fp32 does not matter
-  const float r = sizeof(T) == 2 || !(a < 3e4f) || a < 1e-6f ? __fdiv_rn(a, 6.f) : divide_odd(a, 6.f, 1.f / 6.f);
+  float r;
+  if (sizeof(T) == 4 && a < 3e4f && a > 1e-6f) {
+    r = divide_odd(a, 6.f, 1.f / 6.f);
+  } else {
+    // bf16: a has 8 bits, so a / 6 is a border between two scales (5 bits) or at least
+    // 2^-9 of itself away from one: one correction makes a border exact, and the others'
+    // rounding to fp32 does not matter (an infinity stays one by the choice of the larger)
+    r = a * (1.f / 6.f);
+    r = fmaxf(fmaf(fmaf(-r, 6.f, a), 1.f / 6.f, r), a > 1e30f ? a : 0.f);
+  }
   uint32_t code;
   asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n\tcvt.u32.u16 %0, t;\n\t}"
       : "=r"(code) : "f"(0.f), "f"(r));
   code = max(code & 0xffu, 1u);
   value = __half2float(__ushort_as_half((unsigned short)(decode_scales(code) & 0xffffu)));
   return code;
+}
+
+// (x0, x1) in one register pair, and arithmetic on such pairs.
+typedef unsigned long long Pair;
+__device__ __forceinline__ Pair pair(float x, float y) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+  return p;
+}
+__device__ __forceinline__ Pair fma_pair(Pair a, Pair b, Pair c) {
+  Pair p;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(a), "l"(b), "l"(c));
+  return p;
+}
+__device__ __forceinline__ Pair add_pair(Pair a, Pair b) {
+  Pair p;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
+  return p;
+}
+// Two 4-bit floats of a byte, x the low one.
+__device__ __forceinline__ uint32_t encode2(float x, float y) {
+  uint32_t two;
+  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
+      : "=r"(two) : "f"(y), "f"(x));
+  return two;
+}
+__device__ __forceinline__ uint32_t join4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
 // Codes of 16 values x and their scale's code: codes[0] holds dimensions 0..7, the
@@ -91,34 +132,38 @@ __device__ __forceinline__ uint32_t quantise(float (&x)[kGroup], uint2 &codes) {
   for (int i = 0; i < kGroup; ++i) a = fmaxf(a, fabsf(x[i]));
   float s;
   const uint32_t scale = scale_of<T>(a, s);
-  const float inv = 1.f / s;
   if (a > 4096.f) {
     // far above 6 * 448, where every value saturates: keeps infinities out of the
     // quotient (NaN becomes a number too)
 #pragma unroll
     for (int i = 0; i < kGroup; ++i) x[i] = fminf(fmaxf(x[i], -4096.f), 4096.f);
   }
-  uint32_t w[2] = {0u, 0u};
+  uint32_t two[8];
+  if constexpr (sizeof(T) == 2) {
+    // A value has 8 bits, border * scale at most 7: their quotient is a border (a multiple
+    // of 1/4) or at least 2^-10 away from it.  Rounding to multiples of 2^-11, by adding
+    // and taking off 1.5 * 2^12, restores met borders and keeps the others on their side.
+    const float inv = reciprocal(s), big = 6144.f;
+    const Pair inv2 = pair(inv, inv), up = pair(big, big), down = pair(-big, -big);
 #pragma unroll
-  for (int i = 0; i < kGroup; i += 2) {
-    float q[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float v = x[i + k];
-      if (sizeof(T) == 2) {
-        // a border is met exactly (a quotient of 3 bits) or missed by 2^-9 of it
-        const float q0 = v * inv;
-        q[k] = fmaf(fmaf(-q0, s, v), inv, q0);
-      } else {
-        q[k] = fabsf(v) < 0.125f * s ? 0.f * v : divide_odd(v, s, inv);
-      }
+    for (int i = 0; i < kGroup; i += 2) {
+      const Pair q = add_pair(fma_pair(pair(x[i], x[i + 1]), inv2, up), down);
+      float q0, q1;
+      asm("mov.b64 {%0, %1}, %2;" : "=f"(q0), "=f"(q1) : "l"(q));
+      two[i / 2] = encode2(q0, q1);
     }
-    uint32_t two;
-    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
-        : "=r"(two) : "f"(q[1]), "f"(q[0]));
-    w[i / 8] |= two << (4 * (i % 8));
+  } else {
+    const float inv = 1.f / s;
+#pragma unroll
+    for (int i = 0; i < kGroup; i += 2) {
+      float q[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        q[k] = fabsf(x[i + k]) < 0.125f * s ? 0.f : divide_odd(x[i + k], s, inv);
+      two[i / 2] = encode2(q[0], q[1]);
+    }
   }
-  codes = make_uint2(w[0], w[1]);
+  codes = make_uint2(join4(two[0], two[1], two[2], two[3]), join4(two[4], two[5], two[6], two[7]));
   return scale;
 }
 

@@ -10,13 +10,14 @@
 // Gather: the same rows back, code * scale * 2^exp.
 //
 // Both are streams: rows are read once and written once, 4.5 bits a value on the
-// cache's side.  A thread has 16 values (a scale's group, or the two groups that a
+// cache's side.  Appending, a thread has 16 values (a scale's group, or the two groups that a
 // rotation mixes), whose codes are one 8-byte store; eight neighbours make a head's
 // line.  The rows' places come as in paged_append_kernel: three dependent rounds of
 // loads in a call of any size.
 #include "cb_common.cuh"
 #include "cb_internal.h"
 #include "cb_paged.cuh"
+#include "cb_paged_attn.cuh"
 #include "cb_q4.cuh"
 
 namespace cb {
@@ -31,6 +32,7 @@ struct Rows4Params {
   int n_rows, max_pos, hd;
   int k_units, v_units, q_units;        // threads' shares of a row
   int rows_per_block;
+  paged::Divisor by_row;                // units of a row
   float k_mul, v_mul;                   // 2^-exp (append), 2^exp (gather)
   const float2 *rope;                   // nullptr: keys are taken as they are
 };
@@ -63,7 +65,11 @@ template <typename T> __device__ __forceinline__ void store_group(T *p, const fl
 struct Places4 {
   int off[CB_MAX_SEQS + 1], len[CB_MAX_SEQS];
   int pos[kR4Rows], page[kR4Rows], bad;
+  // byte offsets of the row's page in the pool (-1: none) and of its key and value rows, so
+  // that a unit's addresses take no 64-bit products
+  int64_t base[kR4Rows], k[kR4Rows], v[kR4Rows];
 };
+template <typename T>
 __device__ __forceinline__ void find_places(const Rows4Params &P, int row0, int rows, bool rotate, Places4 &s,
                                             int *status) {
   const int S = P.kv.n_seq;
@@ -89,61 +95,70 @@ __device__ __forceinline__ void find_places(const Rows4Params &P, int row0, int 
     }
     s.pos[threadIdx.x] = pos;
     s.page[threadIdx.x] = page;
+    s.base[threadIdx.x] = page < 0 ? -1 : page * P.kv.page_stride;
+    s.k[threadIdx.x] = (row0 + (int64_t)threadIdx.x) * P.ld_k * (int)sizeof(T);
+    s.v[threadIdx.x] = (row0 + (int64_t)threadIdx.x) * P.ld_v * (int)sizeof(T);
   };
   paged_find_rows<kR4Threads, kR4Rows>(S, P.n_rows, row0, rows, s.off, &s.bad, status, place);
 }
 
-template <typename T, bool ROT>
+template <typename T, int HD, bool ROT>
 __global__ void __launch_bounds__(kR4Threads)
 paged4_append_kernel(const __grid_constant__ Rows4Params P, int *status) {
   __shared__ Places4 s_at;
+  constexpr int kGroups = HD / 16;
   grid_dep_wait();
   grid_dep_launch();
   const int row0 = blockIdx.x * P.rows_per_block;
   const int rows = min(P.rows_per_block, P.n_rows - row0);
-  find_places(P, row0, rows, ROT, s_at, status);
-  const int layer = blockIdx.y, hd = P.hd, groups = hd / 16, page = P.kv.page_size;
+  find_places<T>(P, row0, rows, ROT, s_at, status);
+  const int layer = blockIdx.y, page = P.kv.page_size, head_bytes = q4::head_bytes(page, HD);
   uint8_t *pool = reinterpret_cast<uint8_t *>(P.kv.k_pages) + layer * P.cache_stride;
-  const T *kn = reinterpret_cast<const T *>(P.k) + layer * P.k_layer_stride;
-  const T *vn = reinterpret_cast<const T *>(P.v) + layer * P.v_layer_stride;
+  const uint8_t *kn = reinterpret_cast<const uint8_t *>(reinterpret_cast<const T *>(P.k) + layer * P.k_layer_stride);
+  const uint8_t *vn = reinterpret_cast<const uint8_t *>(reinterpret_cast<const T *>(P.v) + layer * P.v_layer_stride);
   const int per_row = P.k_units + P.v_units + P.q_units;
   for (int t = threadIdx.x; t < rows * per_row; t += kR4Threads) {
-    const int lr = t / per_row;
+    const int lr = P.by_row.div(t);
     int u = t - lr * per_row;
-    if (s_at.page[lr] < 0) continue;
-    const int64_t r = row0 + lr;
+    const int64_t base = s_at.base[lr];
+    if (base < 0) continue;
     const int slot = s_at.pos[lr] & (page - 1);
-    uint8_t *at = pool + s_at.page[lr] * P.kv.page_stride;
+    uint8_t *at = pool + base;
     // codes and scale of group e of head h
     auto put = [&](float (&x)[16], int h, int e, bool v, float mul) {
+      if (mul != 1.f) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] *= mul;
+        for (int i = 0; i < 16; ++i) x[i] *= mul;
+      }
       uint2 codes;
       const uint32_t scale = q4::quantise<T>(x, codes);
-      uint8_t *head = at + (int64_t)h * q4::head_bytes(page, hd);
-      *reinterpret_cast<uint2 *>(head + q4::codes_at(page, hd, v) + slot * (hd / 2) + e * 8) = codes;
-      head[q4::scales_at(page, hd, v) + slot * groups + e] = (uint8_t)scale;
+      uint8_t *head = at + h * head_bytes;
+      *reinterpret_cast<uint2 *>(head + q4::codes_at(page, HD, v) + slot * (HD / 2) + e * 8) = codes;
+      head[q4::scales_at(page, HD, v) + slot * kGroups + e] = (uint8_t)scale;
     };
     if (u < P.v_units) {
       float x[16];
-      load_group(vn + r * P.ld_v + u * 16, x);
-      put(x, u / groups, u % groups, true, P.v_mul);
+      load_group(reinterpret_cast<const T *>(vn + s_at.v[lr]) + u * 16, x);
+      put(x, u / kGroups, u % kGroups, true, P.v_mul);
       continue;
     }
     u -= P.v_units;
     if constexpr (!ROT) {
       float x[16];
-      load_group(kn + r * P.ld_k + u * 16, x);
-      put(x, u / groups, u % groups, false, P.k_mul);
+      load_group(reinterpret_cast<const T *>(kn + s_at.k[lr]) + u * 16, x);
+      put(x, u / kGroups, u % kGroups, false, P.k_mul);
     } else {
       const bool is_q = u >= P.k_units;
       if (is_q) u -= P.k_units;
-      const int per_head = groups / 2, h = u / per_head, e = u % per_head, half = hd / 2;
-      const T *src = (is_q ? reinterpret_cast<const T *>(P.q) + r * P.ld_q : kn + r * P.ld_k) + h * hd + e * 16;
+      constexpr int kPairs = kGroups / 2, kHalf = HD / 2;
+      const int h = u / kPairs, e = u % kPairs;
+      const int64_t r = row0 + lr;
+      const T *src = (is_q ? reinterpret_cast<const T *>(P.q) + r * P.ld_q : reinterpret_cast<const T *>(kn + s_at.k[lr])) +
+                     h * HD + e * 16;
       float x1[16], x2[16];
       load_group(src, x1);
-      load_group(src + half, x2);
-      const float4 *cs = reinterpret_cast<const float4 *>(P.rope + (int64_t)s_at.pos[lr] * half + e * 16);
+      load_group(src + kHalf, x2);
+      const float4 *cs = reinterpret_cast<const float4 *>(P.rope + (int64_t)s_at.pos[lr] * kHalf + e * 16);
 #pragma unroll
       for (int i = 0; i < 16; i += 2) {
         const float4 w = __ldg(cs + i / 2);
@@ -154,18 +169,18 @@ paged4_append_kernel(const __grid_constant__ Rows4Params P, int *status) {
         x2[i + 1] = q4::turned<T>(b1, w.z, -a1, w.w);
       }
       if (is_q) {
-        T *dst = reinterpret_cast<T *>(P.q_out) + r * P.ld_qo + h * hd + e * 16;
+        T *dst = reinterpret_cast<T *>(P.q_out) + r * P.ld_qo + h * HD + e * 16;
         store_group(dst, x1);
-        store_group(dst + half, x2);
+        store_group(dst + kHalf, x2);
       } else {
         put(x1, h, e, false, P.k_mul);
-        put(x2, h, e + per_head, false, P.k_mul);
+        put(x2, h, e + kPairs, false, P.k_mul);
       }
     }
   }
 }
 
-template <typename T>
+template <typename T, int HD>
 __global__ void __launch_bounds__(kR4Threads)
 paged4_gather_kernel(const __grid_constant__ Rows4Params P, int *status) {
   __shared__ Places4 s_at;
@@ -173,38 +188,68 @@ paged4_gather_kernel(const __grid_constant__ Rows4Params P, int *status) {
   grid_dep_launch();
   const int row0 = blockIdx.x * P.rows_per_block;
   const int rows = min(P.rows_per_block, P.n_rows - row0);
-  find_places(P, row0, rows, false, s_at, status);
-  const int layer = blockIdx.y, hd = P.hd, groups = hd / 16, page = P.kv.page_size;
-  const uint8_t *pool = reinterpret_cast<const uint8_t *>(P.kv.k_pages) + layer * P.cache_stride;
-  T *ko = reinterpret_cast<T *>(P.k_out) + layer * P.k_layer_stride;
-  T *vo = reinterpret_cast<T *>(P.v_out) + layer * P.v_layer_stride;
-  const int per_row = 2 * P.k_units;
-  for (int t = threadIdx.x; t < rows * per_row; t += kR4Threads) {
-    const int lr = t / per_row;
-    int u = t - lr * per_row;
-    if (s_at.page[lr] < 0) continue;
-    const bool v = u >= P.k_units;
-    if (v) u -= P.k_units;
-    const int h = u / groups, e = u % groups, slot = s_at.pos[lr] & (page - 1);
-    const uint8_t *head = pool + s_at.page[lr] * P.kv.page_stride + (int64_t)h * q4::head_bytes(page, hd);
-    const uint2 codes = __ldg(reinterpret_cast<const uint2 *>(head + q4::codes_at(page, hd, v) + slot * (hd / 2) + e * 8));
-    const uint32_t s = q4::both(q4::decode_scales(__ldg(head + q4::scales_at(page, hd, v) + slot * groups + e)), false);
-    const float mul = v ? P.v_mul : P.k_mul;
-    float x[16];
+  find_places<T>(P, row0, rows, false, s_at, status);
+  const int page = P.kv.page_size, head_bytes = q4::head_bytes(page, HD);
+  const bool v = blockIdx.z != 0;         // a block reads keys or values
+  const uint8_t *pool = reinterpret_cast<const uint8_t *>(P.kv.k_pages) + blockIdx.y * P.cache_stride;
+  const uint8_t *codes_of = pool + q4::codes_at(page, HD, v), *scales_of = pool + q4::scales_at(page, HD, v);
+  uint8_t *out = v ? reinterpret_cast<uint8_t *>(reinterpret_cast<T *>(P.v_out) + blockIdx.y * P.v_layer_stride)
+                   : reinterpret_cast<uint8_t *>(reinterpret_cast<T *>(P.k_out) + blockIdx.y * P.k_layer_stride);
+  const int64_t *row_at = v ? s_at.v : s_at.k;
+  const float mul = v ? P.v_mul : P.k_mul;
+  // a unit is 8 values (4 bytes of codes), so that neighbours write neighbouring 16 bytes;
+  // a thread's kUnits are under way together
+  constexpr int kUnits = 4, kHead = HD / 8;     // units of a thread, of a head
+  const int per_row = P.k_units, step_row = kR4Threads / per_row, step_unit = kR4Threads % per_row;
+  int lr = P.by_row.div(threadIdx.x), u = threadIdx.x - lr * per_row;
+  while (lr < rows) {
+    uint32_t codes[kUnits], scale[kUnits];
+    uint8_t *dst[kUnits];
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      uint32_t h2[4];
-      q4::decode8(w ? codes.y : codes.x, h2);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t p = q4::mul2(h2[i], s);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&p));
-        x[w * 8 + 2 * i] = f.x * mul;
-        x[w * 8 + 2 * i + 1] = f.y * mul;
+    for (int k = 0; k < kUnits; ++k) {
+      const int64_t base = lr < rows ? s_at.base[lr] : -1;
+      dst[k] = nullptr;
+      if (base >= 0) {
+        const int h = u / kHead, e = u % kHead, slot = s_at.pos[lr] & (page - 1), at = h * head_bytes;
+        codes[k] = __ldg(reinterpret_cast<const uint32_t *>(codes_of + base + (at + slot * (HD / 2) + e * 4)));
+        scale[k] = __ldg(scales_of + base + (at + slot * (HD / 16) + e / 2));
+        dst[k] = out + row_at[lr] + u * (8 * (int)sizeof(T));
+      }
+      lr += step_row;
+      u += step_unit;
+      if (u >= per_row) {
+        u -= per_row;
+        ++lr;
       }
     }
-    const int64_t r = row0 + lr;
-    store_group((v ? vo + r * P.ld_v : ko + r * P.ld_k) + u * 16, x);
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      if (!dst[k]) continue;
+      const uint32_t s = q4::both(q4::decode_scales(scale[k]), false);
+      uint32_t h2[4];
+      q4::decode8(codes[k], h2);
+      float2 x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t p = q4::mul2(h2[e], s);
+        x[e] = __half22float2(*reinterpret_cast<const __half2 *>(&p));
+      }
+      if (mul != 1.f) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = make_float2(x[e].x * mul, x[e].y * mul);
+      }
+      if constexpr (sizeof(T) == 4) {
+        float4 *to = reinterpret_cast<float4 *>(dst[k]);
+        to[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+        to[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+      } else {
+        uint4 y;
+        __nv_bfloat162 *to = reinterpret_cast<__nv_bfloat162 *>(&y);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) to[e] = __floats2bfloat162_rn(x[e].x, x[e].y);
+        *reinterpret_cast<uint4 *>(dst[k]) = y;
+      }
+    }
   }
 }
 
@@ -223,9 +268,12 @@ PagedKV paged4_plain_kv(const cb_paged4_kv &kv) {
   return p;
 }
 
+// As many rows a block as leave every SM its eight blocks once: a block's three rounds of
+// lookups are paid for a row where rows are few, and for 32 where they are many (32 layers
+// of 3136 rows: 237 us with 4 and 8 rows, 202 with 16 and 16).
 static dim3 plan_rows(Rows4Params &P, int n_layers) {
-  const int per_row = P.k_units + P.v_units + P.q_units;
-  P.rows_per_block = max(1, min(kR4Rows, 4 * kR4Threads / per_row));
+  P.rows_per_block = (int)max((int64_t)1, min((int64_t)kR4Rows, (int64_t)P.n_rows * n_layers / (8 * device_sm_count())));
+  P.by_row = paged::Divisor(P.k_units + P.v_units + P.q_units);
   return dim3((P.n_rows + P.rows_per_block - 1) / P.rows_per_block, n_layers);
 }
 
@@ -248,13 +296,17 @@ cudaError_t launch_paged4_append(const cb_paged4_kv &kv, const cb_paged_rows &r,
   P.k_mul = ldexpf(1.f, -kv.k_exp);
   P.v_mul = ldexpf(1.f, -kv.v_exp);
   const dim3 grid = plan_rows(P, r.n_layers);
+  const bool rot = P.rope != nullptr;
+  auto go = [&](auto *kernel) { return launch_pdl(kernel, grid, dim3(kR4Threads), 0, s, P, status); };
   cudaError_t e;
-  if (dt == CB_BF16)
-    e = P.rope ? launch_pdl(paged4_append_kernel<bf16, true>, grid, dim3(kR4Threads), 0, s, P, status)
-               : launch_pdl(paged4_append_kernel<bf16, false>, grid, dim3(kR4Threads), 0, s, P, status);
+  if (dt == CB_BF16 && P.hd == 128)
+    e = rot ? go(paged4_append_kernel<bf16, 128, true>) : go(paged4_append_kernel<bf16, 128, false>);
+  else if (dt == CB_BF16)
+    e = rot ? go(paged4_append_kernel<bf16, 64, true>) : go(paged4_append_kernel<bf16, 64, false>);
+  else if (P.hd == 128)
+    e = rot ? go(paged4_append_kernel<float, 128, true>) : go(paged4_append_kernel<float, 128, false>);
   else
-    e = P.rope ? launch_pdl(paged4_append_kernel<float, true>, grid, dim3(kR4Threads), 0, s, P, status)
-               : launch_pdl(paged4_append_kernel<float, false>, grid, dim3(kR4Threads), 0, s, P, status);
+    e = rot ? go(paged4_append_kernel<float, 64, true>) : go(paged4_append_kernel<float, 64, false>);
   return e == cudaSuccess ? launched(1) : e;
 }
 
@@ -269,13 +321,15 @@ cudaError_t launch_paged4_gather(const cb_paged4_kv &kv, const cb_paged_rows_out
   P.cache_stride = r.cache_layer_stride;
   P.n_rows = r.n_rows;
   P.hd = r.head_dim;
-  P.k_units = P.v_units = r.n_kv_heads * r.head_dim / 16;
+  P.k_units = r.n_kv_heads * r.head_dim / 8;
   P.k_mul = ldexpf(1.f, kv.k_exp);
   P.v_mul = ldexpf(1.f, kv.v_exp);
-  const dim3 grid = plan_rows(P, r.n_layers);
-  const cudaError_t e = dt == CB_BF16
-      ? launch_pdl(paged4_gather_kernel<bf16>, grid, dim3(kR4Threads), 0, s, P, status)
-      : launch_pdl(paged4_gather_kernel<float>, grid, dim3(kR4Threads), 0, s, P, status);
+  dim3 grid = plan_rows(P, r.n_layers);
+  grid.z = 2;                             // keys, values
+  auto go = [&](auto *kernel) { return launch_pdl(kernel, grid, dim3(kR4Threads), 0, s, P, status); };
+  cudaError_t e;
+  if (dt == CB_BF16) e = P.hd == 128 ? go(paged4_gather_kernel<bf16, 128>) : go(paged4_gather_kernel<bf16, 64>);
+  else e = P.hd == 128 ? go(paged4_gather_kernel<float, 128>) : go(paged4_gather_kernel<float, 64>);
   return e == cudaSuccess ? launched(1) : e;
 }
 
