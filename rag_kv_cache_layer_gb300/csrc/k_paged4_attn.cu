@@ -10,8 +10,8 @@
 // values meet the tensor cores as fp16 without a rounding.  q is put into fp16 after
 // a power of two per row that brings its largest magnitude to [2^13, 2^14): a bf16 q
 // is then exact down to 2^-27 of that magnitude and off by at most 2^-39 of it
-// below.  P = 2^(x - m + 14) rounds to fp16 (2^-12 of itself, 2^-39 of the largest
-// weight at the bottom); both powers of two leave with the softmax scale and the
+// below.  P = 2^(x - m + 8), m a reference that scores exceed by 2^7 at most, rounds to
+// fp16 (2^-12 of itself, 2^-33 of the reference's weight at the bottom); both powers of two leave with the softmax scale and the
 // division by the sum.  fp32 rows take q and P as two fp16 halves (hi, lo with
 // 2^-22 and less dropped) and every step of 16 in a fresh accumulator that is added
 // in fp32, since the tensor core truncates its sums.
@@ -40,7 +40,8 @@ typedef AttnParams Params;
 
 constexpr int kBN = 32;                 // keys per block
 constexpr int kPad = 12;
-constexpr float kPShift = 14.f;         // log2 of P at the running maximum
+constexpr float kPShift = 8.f;          // log2 of P at the reference
+constexpr float kRise = 7.f;            // log2 of what a score may exceed it by: P stays below 2^15
 
 template <int HD, int NT, bool F32> struct Cfg {
   static constexpr int kRows = 8 * NT;
@@ -308,13 +309,13 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
         pos[nt][e] = rc < rows ? base + P.by_G.div(l0 + rc) : -1;
       }
     }
-    float o[MT][NT][4], m[NT][2], l[NT][2];
+    float o[MT][NT][4], m[NT][2], l[NT][2], shift[NT][2];     // shift: kPShift - m
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         m[nt][e] = -INFINITY;
-        l[nt][e] = 0.f;
+        l[nt][e] = shift[nt][e] = 0.f;
       }
 #pragma unroll
       for (int t = 0; t < MT; ++t)
@@ -396,33 +397,32 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           mx[nt][e] = fmaxf(max3(x[0][nt][e], x[0][nt][2 + e], x[1][nt][e]), x[1][nt][2 + e]);
-      bool moved = false;
-      float corr[NT][2];
+      // The reference m stays until a score of some lane exceeds it by more than 2^kRise:
+      // most blocks need no exchange between lanes (the scale is positive: the largest
+      // score is the largest product).
+      bool over = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < 2; ++e) over |= mx[nt][e] * sl[nt][e] > m[nt][e] + kRise;
+      if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-          for (int d = 4; d < 32; d <<= 1) mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], d));
-          // (the scale is positive: the largest score is the largest product)
-          const float mn = fmaxf(m[nt][e], mx[nt][e] * sl[nt][e]);
-          corr[nt][e] = mn == m[nt][e] ? 1.f : ex2(m[nt][e] - mn);      // also where both are -inf
-          moved |= mn != m[nt][e];
-          m[nt][e] = mn;
-          l[nt][e] *= corr[nt][e];
-        }
-      float shift2[NT][2];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+          for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) shift2[nt][e] = m[nt][e] == -INFINITY ? 0.f : kPShift - m[nt][e];
-      if (__any_sync(0xffffffffu, moved)) {
+            for (int d = 4; d < 32; d <<= 1) mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], d));
+            const float mn = fmaxf(m[nt][e], mx[nt][e] * sl[nt][e]);
+            const float corr = mn == m[nt][e] ? 1.f : ex2(m[nt][e] - mn);      // also where both are -inf
+            m[nt][e] = mn;
+            shift[nt][e] = mn == -INFINITY ? 0.f : kPShift - mn;
+            l[nt][e] *= corr;
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[t][nt][k] *= corr[nt][k & 1];
+            for (int t = 0; t < MT; ++t) {
+              o[t][nt][e] *= corr;
+              o[t][nt][2 + e] *= corr;
+            }
+          }
       }
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
@@ -434,7 +434,7 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
             float p[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              p[e] = ex2(fmaf(x[mt][nt][2 * h + e], sl[nt][e], shift2[nt][e]));   // 0 where masked
+              p[e] = ex2(fmaf(x[mt][nt][2 * h + e], sl[nt][e], shift[nt][e]));   // 0 where masked
               l[nt][e] += p[e];
             }
             const uint32_t hi = pack_f16(p[0], p[1]);
