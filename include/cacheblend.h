@@ -958,6 +958,17 @@ size_t cb_paged4_attention_workspace_size(int n_rows, int n_seq, int max_kv_len,
 cb_status cb_paged4_attention(const cb_paged4_kv *kv, const cb_paged_query *query,
                               cb_dtype dtype, cb_stream stream);
 
+/* How a cb_paged4_attention call of these sizes runs on the current device (148 SMs
+ * are assumed where there is none): plan[0] rows per tile of the few-rows kernel (0:
+ * not launched), plan[1] blocks of a tile's cluster (0: tiles lie on one line that
+ * plan[2] blocks share), plan[3] rows per unit of the chunk kernel (0: not launched),
+ * plan[4] parts of a unit's key range, plan[5] the most rows (queries times heads per
+ * kv head) of a sequence that the few-rows kernel takes.  Host arithmetic only.
+ * Errors: as for cb_debug_paged_plan. */
+cb_status cb_debug_paged4_plan(int n_rows, int n_seq, int max_kv_len, int n_q_heads,
+                               int n_kv_heads, int head_dim, cb_dtype dtype,
+                               int64_t plan[6]);
+
 /* ------------------------------------------------------------------------ */
 /* Long contexts: attention over the pages that a row needs                 */
 /* ------------------------------------------------------------------------ */
@@ -1036,6 +1047,13 @@ size_t cb_paged_attention_picked_workspace_size(int n_rows, int n_picks, int pag
 cb_status cb_paged_attention_picked(const cb_paged_kv *kv, const cb_paged_query *query,
                                     const int32_t *picks, int n_picks, cb_dtype dtype,
                                     cb_stream stream);
+
+/* How such a call runs: plan[0] blocks of an item's cluster (an item: up to 16 q heads
+ * of one row and kv head; 0: items lie on one line), plan[1] items, plan[2] key blocks
+ * of an item.  Host arithmetic only.  Errors: CB_ERR_INVALID_ARG. */
+cb_status cb_debug_picked_plan(int n_rows, int n_picks, int page_size, int n_q_heads,
+                               int n_kv_heads, int head_dim, cb_dtype dtype,
+                               int64_t plan[3]);
 
 #ifdef __cplusplus
 }

@@ -251,6 +251,8 @@ def _load():
         "cb_paged4_gather": (S, [C.c_char_p, C.c_char_p, i32, vp]),
         "cb_paged4_attention_workspace_size": (C.c_size_t, [i32, i32, i32, i32, i32, i32, i32]),
         "cb_paged4_attention": (S, [C.c_char_p, C.c_char_p, i32, vp]),
+        "cb_debug_paged4_plan": (S, [i32, i32, i32, i32, i32, i32, i32, C.POINTER(i64)]),
+        "cb_debug_picked_plan": (S, [i32, i32, i32, i32, i32, i32, i32, C.POINTER(i64)]),
         "cb_paged_bounds": (S, [C.c_char_p, C.c_char_p, i32, vp]),
         "cb_paged_select_workspace_size": (C.c_size_t, [i32, i32, i32, i32]),
         "cb_paged_select": (S, [C.c_char_p, C.c_char_p, C.c_char_p, i32, vp]),
@@ -289,7 +291,8 @@ EXPORTED = [
     "cb_paged_append", "cb_paged_attention_workspace_size", "cb_paged_attention",
     "cb_debug_paged_plan", "cb_sample_tokens",
     "cb_paged4_page_bytes", "cb_paged4_append", "cb_paged4_gather",
-    "cb_paged4_attention_workspace_size", "cb_paged4_attention",
+    "cb_paged4_attention_workspace_size", "cb_paged4_attention", "cb_debug_paged4_plan",
+    "cb_debug_picked_plan",
     "cb_paged_bounds", "cb_paged_select_workspace_size", "cb_paged_select",
     "cb_paged_attention_picked_workspace_size", "cb_paged_attention_picked",
 ]

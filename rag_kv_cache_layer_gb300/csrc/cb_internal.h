@@ -91,6 +91,26 @@ cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t 
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// The same in clusters of `cluster` blocks.
+template <typename... Params, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(Params...), dim3 grid, dim3 block, int cluster, size_t smem,
+                            cudaStream_t s, Args &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 // ----------------------------------------------------------------- RoPE --
 cudaError_t launch_rope_table(float *table, int max_pos, int head_dim,
                               float base, cudaStream_t s);
@@ -403,6 +423,8 @@ cudaError_t launch_paged4_append(const cb_paged4_kv &kv, const cb_paged_rows &ro
 cudaError_t launch_paged4_gather(const cb_paged4_kv &kv, const cb_paged_rows_out &rows, cb_dtype dt, int *status,
                                  cudaStream_t s);
 size_t paged4_attention_ws_bytes(int n_rows, int n_seq, int max_kv, int Hq, int Hkv, int hd, cb_dtype dt);
+// out: see cb_debug_paged4_plan.
+void paged4_attention_plan(int n_rows, int n_seq, int max_kv, int Hq, int Hkv, int hd, cb_dtype dt, int64_t out[6]);
 cudaError_t launch_paged4_attention(const cb_paged4_kv &kv, const cb_paged_query &query, cb_dtype dt, int *status,
                                     cudaStream_t s);
 
@@ -412,6 +434,8 @@ size_t paged_select_ws_bytes(int n_rows, int max_kv, int page_size, int Hkv);
 cudaError_t launch_paged_select(const PagedKV &kv, const cb_page_bounds &b, const cb_page_select &a, cb_dtype dt,
                                 int *status, cudaStream_t s);
 size_t paged_picked_ws_bytes(int n_rows, int n_picks, int page_size, int Hq, int Hkv, int hd, cb_dtype dt);
+// out: see cb_debug_picked_plan.
+void paged_picked_plan(int n_rows, int n_picks, int page_size, int Hq, int Hkv, int hd, cb_dtype dt, int64_t out[3]);
 cudaError_t launch_paged_picked(const PagedKV &kv, const cb_paged_query &query, const int32_t *picks, int n_picks,
                                 cb_dtype dt, int *status, cudaStream_t s);
 cudaError_t launch_sample(const void *logits, int64_t ld, int n_rows, int vocab, cb_dtype dt,

@@ -240,6 +240,15 @@ extern "C" size_t cb_paged4_attention_workspace_size(int n_rows, int n_seq, int 
   return n > 256 ? n : 256;
 }
 
+extern "C" cb_status cb_debug_paged4_plan(int n_rows, int n_seq, int max_kv_len, int n_q_heads, int n_kv_heads,
+                                          int head_dim, cb_dtype dtype, int64_t plan[6]) {
+  if (!plan || max_kv_len > CB_MAX_KV_LEN ||
+      !paged_sizes_ok(n_rows, n_seq, max_kv_len, n_q_heads, n_kv_heads, head_dim, dtype))
+    return bad("plan is NULL, or sizes that cb_paged4_attention refuses");
+  paged4_attention_plan(n_rows, n_seq, max_kv_len, n_q_heads, n_kv_heads, head_dim, dtype, plan);
+  return CB_OK;
+}
+
 extern "C" cb_status cb_paged4_attention(const cb_paged4_kv *kv, const cb_paged_query *query, cb_dtype dtype,
                                          cb_stream stream) {
   if (!query) return bad("query is NULL");
@@ -357,6 +366,16 @@ extern "C" cb_status cb_paged_attention_picked(const cb_paged_kv *kv, const cb_p
   int *st;
   if (const cb_status s = status_word(&st)) return s;
   return cuda(launch_paged_picked(*kv, a, picks, n_picks, dtype, st, stream));
+}
+
+extern "C" cb_status cb_debug_picked_plan(int n_rows, int n_picks, int page_size, int n_q_heads, int n_kv_heads,
+                                          int head_dim, cb_dtype dtype, int64_t plan[3]) {
+  if (!plan || n_rows <= 0 || n_picks < 1 || n_picks > CB_MAX_PICKS || page_size < 8 || page_size > 1024 ||
+      (page_size & (page_size - 1)) || !paged_heads_ok(n_q_heads, n_kv_heads, head_dim) ||
+      (dtype != CB_F32 && dtype != CB_BF16))
+    return bad("plan is NULL, or sizes that cb_paged_attention_picked refuses");
+  paged_picked_plan(n_rows, n_picks, page_size, n_q_heads, n_kv_heads, head_dim, dtype, plan);
+  return CB_OK;
 }
 
 extern "C" cb_status cb_sample_tokens(const void *logits, int64_t ld_logits, int n_rows, int vocab,

@@ -9,6 +9,7 @@
 #include "cb_paged.cuh"
 #include "cb_paged_attn.cuh"
 #include "cb_paged_few.cuh"
+#include "cb_tc.cuh"
 
 namespace cb {
 namespace paged {
@@ -224,6 +225,44 @@ decode_merge_kernel(const __grid_constant__ AttnParams P, int R) {
     else
       *reinterpret_cast<uint32_t *>(dst) = pack_bf16(a * s_inv[k], b * s_inv[k]);
   }
+}
+
+// Joins the parts (unnormalised O in `part` [rows][HD], (m, l) in `ml`, in shared memory) of
+// the `ranks` blocks of a cluster, a power of two up to 16: block `rank` writes a share of
+// the rows' columns, four at a time, by write(row, column, O, l).  A lane has one block's
+// part of them, and neighbouring lanes add up in the order of a tree.  Every thread of the
+// cluster's blocks (of NTH) calls it.
+template <int NTH, int HD, typename F>
+__device__ __forceinline__ void cluster_join(const float *part, const float2 *ml, int rows, int rank, int ranks,
+                                             const F &write) {
+  tcx::cluster_sync();
+  const int all = rows * (HD / 4), per = (all + ranks - 1) / ranks, groups = NTH / ranks;
+  const int from = threadIdx.x & (ranks - 1), k0 = threadIdx.x / ranks;
+  for (int k = 0; k < per; k += groups) {
+    const int i = rank * per + k + k0;
+    const bool valid = k + k0 < per && i < all;
+    const int r = valid ? i / (HD / 4) : 0, c = valid ? i % (HD / 4) * 4 : 0;
+    float2 x;
+    float4 a;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y)
+                 : "r"(tcx::map_to_rank(smem_u32(ml + r), from)) : "memory");
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(a.x), "=f"(a.y), "=f"(a.z), "=f"(a.w)
+                 : "r"(tcx::map_to_rank(smem_u32(part + r * HD + c), from)) : "memory");
+    float M = x.x;
+    for (int o = 1; o < ranks; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float w = x.x == -INFINITY ? 0.f : ex2(x.x - M);
+    float L = w * x.y;
+    a = make_float4(w * a.x, w * a.y, w * a.z, w * a.w);
+    for (int o = 1; o < ranks; o <<= 1) {
+      L += __shfl_xor_sync(0xffffffffu, L, o);
+      a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
+      a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
+      a.z += __shfl_xor_sync(0xffffffffu, a.z, o);
+      a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
+    }
+    if (valid && from == 0) write(r, c, a, L);
+  }
+  tcx::cluster_sync();                          // no block leaves while its parts are read
 }
 
 }  // namespace paged

@@ -30,6 +30,7 @@
 #include "cb_paged_attn.cuh"
 #include "cb_paged_line.cuh"
 #include "cb_q4.cuh"
+#include "cb_tc.cuh"
 
 namespace cb {
 namespace paged4 {
@@ -43,13 +44,15 @@ constexpr int kPad = 12;
 constexpr float kPShift = 8.f;          // log2 of P at the reference
 constexpr float kRise = 7.f;            // log2 of what a score may exceed it by: P stays below 2^15
 
-template <int HD, int NT, bool F32> struct Cfg {
-  static constexpr int kRows = 8 * NT;
-  static constexpr int kPerSm = NT == 4 || F32 ? 2 : NT == 2 ? 3 : 4, kStages = NT == 4 || F32 ? 4 : NT == 2 ? 3 : 2;
+// CL: a tile's keys in one cluster, eight warps a block.
+template <int HD, int NT, bool F32, bool CL> struct Cfg {
+  static constexpr int kRows = 8 * NT, kWarps = CL ? 8 : 4, kThreads = 32 * kWarps;
+  static constexpr int kPerSm = CL ? (NT == 1 && !F32 ? 2 : 1) : NT == 4 || F32 ? 2 : NT == 2 ? 3 : 4;
+  static constexpr int kStages = CL ? (NT == 1 ? 2 : NT == 2 ? 3 : 4) : NT == 4 || F32 ? 4 : NT == 2 ? 3 : 2;
   static constexpr int kCodes = kBN * HD / 2, kScales = kBN * HD / 16;
   static constexpr int kOffV = kCodes, kOffKs = 2 * kCodes, kOffVs = kOffKs + kScales;
   static constexpr int kStage = kOffVs + kScales;
-  static constexpr int kSmem = 4 * kStages * kStage;
+  static constexpr int kSmem = kWarps * kStages * kStage;
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -117,71 +120,114 @@ __device__ __forceinline__ void copy_part(uint32_t dst, const void *src, int byt
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-template <typename T, int HD, int NT>
-__global__ void __launch_bounds__(kDecThreads, (Cfg<HD, NT, std::is_same<T, float>::value>::kPerSm))
+struct None {};
+
+template <typename T, int HD, int NT, bool CL>
+__global__ void __launch_bounds__((Cfg<HD, NT, std::is_same<T, float>::value, CL>::kThreads),
+                                  (Cfg<HD, NT, std::is_same<T, float>::value, CL>::kPerSm))
 paged4_few_kernel(const __grid_constant__ Params P, int *status) {
   constexpr bool F32 = std::is_same<T, float>::value;
-  typedef Cfg<HD, NT, F32> C;
+  typedef Cfg<HD, NT, F32, CL> C;
+  constexpr int NW = C::kWarps;
   constexpr int R = C::kRows, NS = C::kStages, KS = HD / 16, MT = HD / 16;
   // words of codes that a lane takes of a key (K: HD / 4 dimensions; V: HD / 8)
   constexpr int KW = HD / 32, VW = HD / 64;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ Line line;
-  __shared__ int64_t s_sums[kDecThreads / 32];
-  __shared__ float2 s_ml[4 * R];                // (m, l) of each warp's rows
-  grid_dep_wait();
-  grid_dep_launch();
-  make_line(P, R, kBN, gridDim.x, line, s_sums, status, P.pad);
-  Join *const join = P.joins + blockIdx.x;
-  if (threadIdx.x == 0) join->rows = 0;
-  if ((int)blockIdx.x >= line.parts) return;
-  const int64_t u0 = part_begin(line, blockIdx.x), u1 = part_begin(line, blockIdx.x + 1);
+  __shared__ typename std::conditional<CL, None, Line>::type s_line;
+  __shared__ int64_t s_sums[NW];
+  __shared__ float2 s_ml[NW * R];               // (m, l) of each warp's rows
+  __shared__ PagedTile s_tile;
+  // CL: the block's joined rows, read by the cluster's others
+  __shared__ __align__(16) float s_part[CL ? R * HD : 4];
+  __shared__ float2 s_pml[CL ? R : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, q4 = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * NS * C::kStage;
   const int page_size = P.kv.page_size, shift = __ffs(page_size) - 1;
   const uint8_t *const pool = reinterpret_cast<const uint8_t *>(P.kv.k_pages);
-
-  int s = seq_of(line, P.kv.n_seq, u0);
+  grid_dep_wait();
+  grid_dep_launch();
+  int64_t u0 = 0, u1 = 1;
+  int s = 0, rank = 0, ranks = 1;
+  if constexpr (CL) {
+    ranks = tcx::cluster_size();
+    rank = blockIdx.x % ranks;
+    paged_find_tile<C::kThreads>(P.kv, P.n_rows, P.G, R, P.max_kv, (int)P.by_quads.div(blockIdx.x / ranks), &s_tile,
+                                 reinterpret_cast<int *>(s_sums), status);
+    if (s_tile.s < 0) return;                   // (as in the cluster's other blocks)
+  } else {
+    make_line(P, R, kBN, gridDim.x, s_line, s_sums, status, P.pad);
+    Join *const join = P.joins + blockIdx.x;
+    if (threadIdx.x == 0) join->rows = 0;
+    if ((int)blockIdx.x >= s_line.parts) return;
+    u0 = part_begin(s_line, blockIdx.x);
+    u1 = part_begin(s_line, blockIdx.x + 1);
+    s = seq_of(s_line, P.kv.n_seq, u0);
+  }
   for (int64_t u = u0; u < u1;) {
-    // this piece: a tile of sequence s and kv head g, its blocks [jb, je) (as in paged_decode_kernel)
-    while (line.blocks[s] == 0 || (s + 1 < P.kv.n_seq && line.begin[s + 1] <= u)) ++s;
-    const int row0 = __ldg(P.kv.row_offsets + s), n = __ldg(P.kv.row_offsets + s + 1) - row0;
-    const int kv = __ldg(P.kv.kv_lens + s), base = kv - n, all = n * P.G, tiles = (all - 1) / R + 1;
-    int64_t local = u - line.begin[s];
-    int nbs = line.blocks[s], g, jb, l0 = 0;
-    const int64_t pairs = (int64_t)(tiles / 2) * P.by_quads.d * nbs;
-    if (local >= pairs) {                       // the only tile, or an odd middle one
-      if (tiles > 1) {
-        l0 = tiles / 2 * R;
-        nbs = blocks_seen(P, base, l0 + R - 1, kBN) + P.pad;
-      }
-      divide(local - pairs, nbs, g, jb);
+    // this piece: rows [l0, l0 + rows) of sequence s and kv head g, key blocks [jb, je)
+    int row0, kv, base, g, l0 = 0, rows, jb, je, seen;
+    bool whole = true, first = true;
+    if constexpr (CL) {
+      const PagedTile t = s_tile;
+      u = u1;
+      s = t.s;
+      row0 = t.row0;
+      kv = t.kv;
+      base = kv - t.n;
+      const int item = blockIdx.x / ranks;
+      g = item - P.by_quads.div(item) * (int)P.by_quads.d;
+      l0 = t.t * R;
+      rows = min(R, t.n * P.G - l0);
+      seen = base + P.by_G.div(l0 + rows - 1) + 1;            // keys the tile's last row sees
+      const int nb = seen > 0 ? (seen - 1) / kBN + 1 : 0;
+      jb = (int)((int64_t)nb * rank / ranks);
+      je = (int)((int64_t)nb * (rank + 1) / ranks);
     } else {
-      divide(local, nbs, g, jb);
-      const int q = P.by_quads.div(g), late = blocks_seen(P, base, min((tiles - q) * R, all) - 1, kBN) + P.pad;
-      g -= q * (int)P.by_quads.d;
-      if (jb < late) {
-        nbs = late;
-        l0 = (tiles - 1 - q) * R;
+      // (as in paged_decode_kernel)
+      const Line &line = s_line;
+      while (line.blocks[s] == 0 || (s + 1 < P.kv.n_seq && line.begin[s + 1] <= u)) ++s;
+      row0 = __ldg(P.kv.row_offsets + s);
+      const int n = __ldg(P.kv.row_offsets + s + 1) - row0;
+      kv = __ldg(P.kv.kv_lens + s);
+      base = kv - n;
+      const int all = n * P.G, tiles = (all - 1) / R + 1;
+      int64_t local = u - line.begin[s];
+      int nbs = line.blocks[s];
+      const int64_t pairs = (int64_t)(tiles / 2) * P.by_quads.d * nbs;
+      if (local >= pairs) {                     // the only tile, or an odd middle one
+        if (tiles > 1) {
+          l0 = tiles / 2 * R;
+          nbs = blocks_seen(P, base, l0 + R - 1, kBN) + P.pad;
+        }
+        divide(local - pairs, nbs, g, jb);
       } else {
-        nbs -= late;
-        jb -= late;
-        l0 = q * R;
+        divide(local, nbs, g, jb);
+        const int q = P.by_quads.div(g), late = blocks_seen(P, base, min((tiles - q) * R, all) - 1, kBN) + P.pad;
+        g -= q * (int)P.by_quads.d;
+        if (jb < late) {
+          nbs = late;
+          l0 = (tiles - 1 - q) * R;
+        } else {
+          nbs -= late;
+          jb -= late;
+          l0 = q * R;
+        }
       }
+      rows = min(R, all - l0);
+      const int take = (int)min((int64_t)(nbs - jb), u1 - u);
+      const int real = blocks_seen(P, base, l0 + rows - 1, kBN);   // of the tile's units, the others are padding
+      const int64_t item_end = u - jb + real;
+      whole = jb == 0 && item_end <= u1;
+      first = u == u0;
+      u += take;
+      if (jb >= real) continue;                 // nothing but padding
+      seen = base + P.by_G.div(l0 + rows - 1) + 1;
+      je = min(jb + take, seen > 0 ? real : 0);
+      if (threadIdx.x == 0 && jb == 0 && item_end > u1)   // goes on in the next part (no more pieces here)
+        P.joins[blockIdx.x] = Join{row0, l0, rows, g, part_of(line, item_end - 1), first ? 0 : 1};
     }
-    const int rows = min(R, all - l0);
-    const int take = (int)min((int64_t)(nbs - jb), u1 - u);
-    const int real = blocks_seen(P, base, l0 + rows - 1, kBN);   // of the tile's units, the others are padding
-    const int64_t item_end = u - jb + real;
-    const bool whole = jb == 0 && item_end <= u1, first = u == u0;
-    u += take;
-    if (jb >= real) continue;                   // nothing but padding
-    const int seen = base + P.by_G.div(l0 + rows - 1) + 1;    // keys the tile's last row sees
-    const int je = min(jb + take, seen > 0 ? real : 0);
     const int sure = base + P.by_G.div(l0);                   // every row sees the keys up to this one
     const int32_t *table = P.kv.block_table + (int64_t)s * P.kv.ld_table;
-    if (threadIdx.x == 0 && jb == 0 && item_end > u1)   // goes on in the next part (no more pieces here)
-      *join = Join{row0, l0, rows, g, part_of(line, item_end - 1), first ? 0 : 1};
 
     auto fetch = [&](int j) -> int {            // page of key j * 32 + lane
       const int key = j * kBN + lane;
@@ -251,13 +297,13 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
     constexpr int kAhead = 3;
     int ahead[kAhead], from = jb + warp;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) ahead[i] = fetch(from + i * 4);
+    for (int i = 0; i < kAhead; ++i) ahead[i] = fetch(from + i * NW);
     auto next_page = [&]() -> int {
       const int page = ahead[0];
 #pragma unroll
       for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
-      ahead[kAhead - 1] = fetch(from + kAhead * 4);
-      from += 4;
+      ahead[kAhead - 1] = fetch(from + kAhead * NW);
+      from += NW;
       return page;
     };
 #pragma unroll 1
@@ -326,7 +372,7 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
     // four keys whose values a lane needs then are q4, q4 + 4, q4 + 8, q4 + 12.
     const int krow = (gid >> 1) + 4 * (gid & 1);
     int st = 0, fill = NS - 1;
-    for (int j = jb + warp; j < je; j += 4) {
+    for (int j = jb + warp; j < je; j += NW) {
       asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
       __syncwarp();                             // landed for every lane; the stage before is used up
       {
@@ -496,7 +542,7 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
     __syncthreads();                            // the rings are used up
     // Every warp leaves its O in rows of HD + 4 floats, then the four states join.
     constexpr int LD = HD + 4;
-    static_assert(4 * R * LD * 4 <= C::kSmem, "the warps' O fit the rings");
+    static_assert(NW * R * LD * 4 <= C::kSmem, "the warps' O fit the rings");
     float *so = reinterpret_cast<float *>(smem);
 #pragma unroll
     for (int t = 0; t < MT; ++t)
@@ -508,14 +554,25 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
               make_float2(o[t][nt][e], o[t][nt][2 + e]);
     __syncthreads();
     const int64_t slot = (2 * (int64_t)blockIdx.x + (first ? 0 : 1)) * R;
-    for (int i = threadIdx.x; i < rows * (HD / 4); i += kDecThreads) {
+    // an output's four columns, divided by the sum
+    auto write = [&](int r, int c, float4 a, float L) {
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const int qi = P.by_G.div(l0 + r);
+      T *dst = reinterpret_cast<T *>(P.out) + (int64_t)(row0 + qi) * P.ld_out +
+               (int64_t)(g * P.G + l0 + r - qi * P.G) * HD + c;
+      if constexpr (F32)
+        *reinterpret_cast<float4 *>(dst) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+      else
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+    };
+    for (int i = threadIdx.x; i < rows * (HD / 4); i += C::kThreads) {
       const int r = i / (HD / 4), c = i % (HD / 4) * 4;
       float M = -INFINITY, L = 0.f;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) M = fmaxf(M, s_ml[k * R + r].x);
+      for (int k = 0; k < NW; ++k) M = fmaxf(M, s_ml[k * R + r].x);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < NW; ++k) {
         const float2 ml = s_ml[k * R + r];
         const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
         const float4 v = *reinterpret_cast<const float4 *>(so + (k * R + r) * LD + c);
@@ -523,21 +580,17 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
         a.x += w * v.x; a.y += w * v.y; a.z += w * v.z; a.w += w * v.w;
       }
       a.x *= P.v_mul; a.y *= P.v_mul; a.z *= P.v_mul; a.w *= P.v_mul;
-      if (!whole) {
+      if constexpr (CL) {
+        *reinterpret_cast<float4 *>(s_part + r * HD + c) = a;
+        if (c == 0) s_pml[r] = make_float2(M, L);
+      } else if (!whole) {
         *reinterpret_cast<float4 *>(P.part_o + (slot + r) * HD + c) = a;
         if (c == 0) P.part_ml[slot + r] = make_float2(M, L);
       } else {
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        const int qi = P.by_G.div(l0 + r);
-        T *dst = reinterpret_cast<T *>(P.out) + (int64_t)(row0 + qi) * P.ld_out +
-                 (int64_t)(g * P.G + l0 + r - qi * P.G) * HD + c;
-        if constexpr (F32)
-          *reinterpret_cast<float4 *>(dst) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-        else
-          *reinterpret_cast<uint2 *>(dst) =
-              make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+        write(r, c, a, L);
       }
     }
+    if constexpr (CL) cluster_join<C::kThreads, HD>(s_part, s_pml, rows, rank, ranks, write);
     __syncthreads();                            // before the next piece fills the rings
   }
 }
@@ -545,6 +598,7 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
 // ------------------------------------------------------------------ plan --
 struct Plan {
   int nt, grid;                         // few-rows kernel: score columns / 8 per tile (0: not launched), blocks
+  int cluster;                          // blocks of a tile's cluster, 0: the line
   int few_hi, rows_lo;                  // which sequences each kernel takes
   ChunkPlan chunk;                      // R 0: not launched
 };
@@ -553,6 +607,21 @@ struct Plan {
 // through the few-rows kernel, longer ones through the chunk kernel; fp32 runs the
 // few-rows kernel alone.
 constexpr int kFewRows = 32;
+
+// Few tiles over few keys: each tile's keys go to one cluster of up to 16 blocks of eight
+// warps, which joins in its shared memory: one launch in place of two.  The warps' rounds
+// over their keys may be one or two more than on the line, which spreads over all SMs.
+static int plan_cluster(const Plan &p, int64_t items, int max_kv, cb_dtype dt) {
+  const int sms = device_sm_count(), nb = (max_kv + kBN - 1) / kBN > 0 ? (max_kv + kBN - 1) / kBN : 1;
+  const int64_t fit = sms * (p.nt == 1 && dt == CB_BF16 ? 2 : 1);
+  int c = 1;
+  while (c < 16 && 8 * c < nb) c <<= 1;
+  while (c > 1 && items * c > fit) c >>= 1;
+  if (items * c > fit) return 0;
+  const int64_t rounds = (nb + 8 * c - 1) / (8 * c), line = (items * nb + 4 * p.grid - 1) / (4 * p.grid);
+  return rounds <= line + 1 ? c : 0;
+}
+
 static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd, cb_dtype dt) {
   Plan p = {};
   const int64_t all = n_rows * G, per_seq = (all + S - 1) / S;
@@ -560,41 +629,58 @@ static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd, cb_d
   p.few_hi = 0x7fffffff;
   if (few || S > 1) p.nt = per_seq <= 8 ? 1 : per_seq <= 16 ? 2 : few || per_seq <= kFewRows ? 4 : 1;
   p.grid = device_sm_count() * (p.nt == 4 || dt == CB_F32 ? 2 : p.nt == 2 ? 3 : 4);
-  if (few) return p;
+  if (few) {
+    p.cluster = plan_cluster(p, tile_bound(n_rows, S, G, 8 * p.nt) * Hkv, max_kv, dt);
+    return p;
+  }
   if (S > 1) p.few_hi = p.rows_lo = kFewRows;
   p.chunk = plan_chunk(n_rows, S, max_kv, G, Hkv, hd);
   return p;
 }
-static int64_t few_partials(const Plan &p) { return p.nt ? 2LL * p.grid * 8 * p.nt : 0; }
+static int64_t few_partials(const Plan &p) { return p.nt && !p.cluster ? 2LL * p.grid * 8 * p.nt : 0; }
 static int64_t chunk_partials(const Plan &p, int Hkv) {
   return p.chunk.R && p.chunk.n_split > 1 ? p.chunk.units * Hkv * p.chunk.n_split * p.chunk.R : 0;
 }
 static size_t plan_bytes(const Plan &p, int Hkv, int hd) {
   const size_t row = hd * sizeof(float) + sizeof(float2);
-  const size_t few = (size_t)few_partials(p) * row + (p.nt ? p.grid * sizeof(Join) : 0);
+  const size_t few = (size_t)few_partials(p) * row + (p.nt && !p.cluster ? p.grid * sizeof(Join) : 0);
   const size_t chunk = (size_t)chunk_partials(p, Hkv) * row;
   return few > chunk ? few : chunk;
 }
 
-template <typename T, int HD, int NT>
-static cudaError_t run(const Params &P, int grid, int *status, cudaStream_t s) {
-  typedef Cfg<HD, NT, std::is_same<T, float>::value> C;
+template <typename T, int HD, int NT, bool CL>
+static cudaError_t run(const Params &P, const Plan &p, int *status, cudaStream_t s) {
+  typedef Cfg<HD, NT, std::is_same<T, float>::value, CL> C;
   static PerDeviceOnce attr;
   cudaError_t e = attr.run([](int) {
-    return cudaFuncSetAttribute(paged4_few_kernel<T, HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    const cudaError_t e = cudaFuncSetAttribute(paged4_few_kernel<T, HD, NT, CL>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    return e != cudaSuccess || !CL
+        ? e : cudaFuncSetAttribute(paged4_few_kernel<T, HD, NT, CL>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   });
   if (e != cudaSuccess) return e;
-  e = launch_pdl(paged4_few_kernel<T, HD, NT>, dim3(grid), dim3(kDecThreads), C::kSmem, s, P, status);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(decode_merge_kernel<T, HD>, dim3(grid, C::kRows / kJoinRows), dim3(kJoinThreads),
-                 grid * kJoinRows * sizeof(float2), s, static_cast<const AttnParams &>(P), C::kRows);
-  return e == cudaSuccess ? launched(2) : e;
+  if constexpr (CL) {
+    const int64_t blocks = tile_bound(P.n_rows, P.kv.n_seq, P.G, C::kRows) * P.Hkv * p.cluster;
+    e = launch_clusters(paged4_few_kernel<T, HD, NT, CL>, dim3((unsigned)blocks), dim3(C::kThreads), p.cluster, C::kSmem, s,
+                        P, status);
+    return e == cudaSuccess ? launched(1) : e;
+  } else {
+    e = launch_pdl(paged4_few_kernel<T, HD, NT, CL>, dim3(p.grid), dim3(kDecThreads), C::kSmem, s, P, status);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(decode_merge_kernel<T, HD>, dim3(p.grid, C::kRows / kJoinRows), dim3(kJoinThreads),
+                   p.grid * kJoinRows * sizeof(float2), s, P, C::kRows);
+    return e == cudaSuccess ? launched(2) : e;
+  }
 }
 
+template <typename T, int HD, int NT>
+static cudaError_t run_form(const Params &P, const Plan &p, int *status, cudaStream_t s) {
+  return p.cluster ? run<T, HD, NT, true>(P, p, status, s) : run<T, HD, NT, false>(P, p, status, s);
+}
 template <typename T, int HD>
 static cudaError_t run_rows(const Params &P, const Plan &p, int *status, cudaStream_t s) {
-  return p.nt == 1 ? run<T, HD, 1>(P, p.grid, status, s)
-         : p.nt == 2 ? run<T, HD, 2>(P, p.grid, status, s) : run<T, HD, 4>(P, p.grid, status, s);
+  return p.nt == 1 ? run_form<T, HD, 1>(P, p, status, s)
+         : p.nt == 2 ? run_form<T, HD, 2>(P, p, status, s) : run_form<T, HD, 4>(P, p, status, s);
 }
 
 }  // namespace paged4
@@ -602,6 +688,12 @@ static cudaError_t run_rows(const Params &P, const Plan &p, int *status, cudaStr
 size_t paged4_attention_ws_bytes(int n_rows, int n_seq, int max_kv, int Hq, int Hkv, int hd, cb_dtype dt) {
   if (n_rows <= 0 || n_seq <= 0) return 0;
   return paged4::plan_bytes(paged4::plan(n_rows, n_seq, max_kv, Hq / Hkv, Hkv, hd, dt), Hkv, hd);
+}
+
+void paged4_attention_plan(int n_rows, int n_seq, int max_kv, int Hq, int Hkv, int hd, cb_dtype dt, int64_t out[6]) {
+  const paged4::Plan p = paged4::plan(n_rows, n_seq, max_kv, Hq / Hkv, Hkv, hd, dt);
+  const int64_t v[6] = {8 * p.nt, p.cluster, p.grid, p.chunk.R, p.chunk.n_split, p.nt ? p.few_hi : 0};
+  for (int i = 0; i < 6; ++i) out[i] = v[i];
 }
 
 cudaError_t launch_paged4_attention(const cb_paged4_kv &kv, const cb_paged_query &a, cb_dtype dt, int *status,

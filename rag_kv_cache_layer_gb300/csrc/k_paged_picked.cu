@@ -21,6 +21,7 @@
 #include "cb_paged_attn.cuh"
 #include "cb_paged_few.cuh"
 #include "cb_paged_line.cuh"
+#include "cb_tc.cuh"
 
 namespace cb {
 namespace picked {
@@ -36,23 +37,33 @@ struct Params : AttnParams {
 
 constexpr int kBlocksPerSm = 2;
 
+// CL: an item's keys in one cluster, eight warps a block.
+template <bool CL> struct Form {
+  static constexpr int kWarps = CL ? 8 : 4, kThreads = 32 * kWarps, kPerSm = CL ? 1 : kBlocksPerSm;
+};
+
 __device__ __forceinline__ int64_t begin_of(const Params &P, int c) { return P.units * c / P.parts; }
 __device__ __forceinline__ int part_of(const Params &P, int64_t u) { return (int)(((u + 1) * P.parts - 1) / P.units); }
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(kDecThreads, kBlocksPerSm)
+template <typename T, int HD, bool CL>
+__global__ void __launch_bounds__(Form<CL>::kThreads, Form<CL>::kPerSm)
 paged_picked_kernel(const __grid_constant__ Params P, int *status) {
+  constexpr int NW = Form<CL>::kWarps, NTH = Form<CL>::kThreads;
   typedef DecCfg<T, HD, 1> C;
   constexpr bool F32 = std::is_same<T, float>::value;
   constexpr int R = 16, ND = HD / 8, KS = F32 ? HD / 8 : HD / 16, BN = C::kBN, NS = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int s_page[CB_MAX_PICKS], s_vis[CB_MAX_PICKS];   // page of the pool, slots that the row sees
-  __shared__ float2 s_ml[4 * R];
+  __shared__ float2 s_ml[NW * R];
   __shared__ int s_seq, s_any;
+  // CL: the block's joined rows, read by the cluster's others
+  __shared__ __align__(16) float s_part[CL ? R * HD : 4];
+  __shared__ float2 s_pml[CL ? R : 1];
   grid_dep_wait();
   grid_dep_launch();
-  Join *const join = P.joins + blockIdx.x;
-  const int64_t u0 = begin_of(P, blockIdx.x), u1 = begin_of(P, blockIdx.x + 1);
+  // CL: block `rank` of an item's cluster; the line's units are not used
+  const int ranks = CL ? tcx::cluster_size() : 1, rank = CL ? (int)(blockIdx.x % ranks) : 0;
+  const int64_t u0 = CL ? 0 : begin_of(P, blockIdx.x), u1 = CL ? 1 : begin_of(P, blockIdx.x + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, q4 = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * NS * C::kStage;
   const int page_size = P.kv.page_size, shift = __ffs(page_size) - 1;
@@ -61,22 +72,23 @@ paged_picked_kernel(const __grid_constant__ Params P, int *status) {
   const int crow = lane / kCols, ccol = lane % kCols;
   const int krow = lane & 7, kcol = lane >> 3, vrow = lane & 15, vcol = lane >> 4;
   const float sl2 = P.scale_log2;
-  if (threadIdx.x == 0) join->rows = 0;
+  if (!CL && threadIdx.x == 0) P.joins[blockIdx.x].rows = 0;
 
   for (int64_t u = u0; u < u1;) {
-    const int64_t item = u / P.blocks;
-    const int jb = (int)(u - item * P.blocks), je = (int)min((int64_t)P.blocks, jb + (u1 - u));
+    const int64_t item = CL ? blockIdx.x / ranks : u / P.blocks;
+    const int jb = CL ? (int)((int64_t)P.blocks * rank / ranks) : (int)(u - item * P.blocks);
+    const int je = CL ? (int)((int64_t)P.blocks * (rank + 1) / ranks) : (int)min((int64_t)P.blocks, jb + (u1 - u));
     const bool whole = je - jb == P.blocks, first = u == u0;
     const int tile = (int)(item % P.tiles), g = (int)(item / P.tiles % P.Hkv), r = (int)(item / P.tiles / P.Hkv);
     const int l0 = tile * R, rows = min(R, P.G - l0);
-    u += je - jb;
+    u = CL ? u1 : u + (je - jb);
     // the row's sequence and position
     if (threadIdx.x == 0) {
       s_seq = 0x7fffffff;
       s_any = 0;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < P.kv.n_seq; i += kDecThreads) {
+    for (int i = threadIdx.x; i < P.kv.n_seq; i += NTH) {
       const int a = __ldg(P.kv.row_offsets + i), b = __ldg(P.kv.row_offsets + i + 1);
       if (a < 0 || b < a || b > P.n_rows) report(status, CB_ERR_DEVICE_INDEX);
       else if (a <= r && r < b) atomicMin(&s_seq, i);
@@ -84,7 +96,7 @@ paged_picked_kernel(const __grid_constant__ Params P, int *status) {
     // the part's picks, while the sequence is found
     const int p0 = jb * BN >> shift, p1 = min(P.n_picks, (je * BN + page_size - 1) >> shift);
     const int32_t *list = P.picks + ((int64_t)r * P.Hkv + g) * P.n_picks;
-    for (int i = p0 + threadIdx.x; i < p1; i += kDecThreads) s_page[i] = __ldg(list + i);
+    for (int i = p0 + threadIdx.x; i < p1; i += NTH) s_page[i] = __ldg(list + i);
     __syncthreads();
     const int s = s_seq;
     if (s == 0x7fffffff) {                      // a row of no sequence is left alone
@@ -100,7 +112,7 @@ paged_picked_kernel(const __grid_constant__ Params P, int *status) {
     const int64_t pos = (int64_t)kv - __ldg(P.kv.row_offsets + s + 1) + r;
     const int32_t *table = P.kv.block_table + (int64_t)s * P.kv.ld_table;
     bool any = false;
-    for (int i = p0 + threadIdx.x; i < p1; i += kDecThreads) {
+    for (int i = p0 + threadIdx.x; i < p1; i += NTH) {
       const int j = s_page[i];
       int page = -1, vis = 0;
       if (j < -1 || j >= P.kv.max_pages) {
@@ -122,8 +134,8 @@ paged_picked_kernel(const __grid_constant__ Params P, int *status) {
       any |= vis > 0;
     }
     if (any) s_any = 1;
-    if (threadIdx.x == 0 && u == u1 && jb == 0 && !whole)     // the last piece: the one that goes on in the next part
-      *join = Join{r, l0, rows, g, part_of(P, (item + 1) * P.blocks - 1), first ? 0 : 1};
+    if (!CL && threadIdx.x == 0 && u == u1 && jb == 0 && !whole)     // the last piece: the one that goes on in the next part
+      P.joins[blockIdx.x] = Join{r, l0, rows, g, part_of(P, (item + 1) * P.blocks - 1), first ? 0 : 1};
     __syncthreads();
     const int end = s_any ? je : jb;            // a piece without a key has nothing to stream
 
@@ -144,7 +156,7 @@ paged_picked_kernel(const __grid_constant__ Params P, int *status) {
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 #pragma unroll 1
     for (int i = 0; i < NS - 1; ++i) {
-      const int j = jb + warp + 4 * i;
+      const int j = jb + warp + NW * i;
       if (j < end) load(j, i);
       commit();
     }
@@ -167,10 +179,10 @@ paged_picked_kernel(const __grid_constant__ Params P, int *status) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
     int st = 0, fill = NS - 1;
-    for (int j = jb + warp; j < end; j += 4) {
+    for (int j = jb + warp; j < end; j += NW) {
       asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
       __syncwarp();                             // landed for every lane; the stage before is used up
-      if (j + 4 * (NS - 1) < end) load(j + 4 * (NS - 1), fill);
+      if (j + NW * (NS - 1) < end) load(j + NW * (NS - 1), fill);
       commit();
       fill = fill + 1 == NS ? 0 : fill + 1;
       const uint32_t ks = ring + st * C::kStage, vs = ks + C::kTile;
@@ -291,7 +303,7 @@ paged_picked_kernel(const __grid_constant__ Params P, int *status) {
     }
     __syncthreads();                            // the rings are used up
     constexpr int LD = HD + 4;
-    static_assert(4 * R * LD * 4 <= C::kSmem, "the warps' O fit the rings");
+    static_assert(R * LD * 4 <= NS * C::kStage, "the warps' O fit the rings");
     float *so = reinterpret_cast<float *>(smem);
 #pragma unroll
     for (int d = 0; d < ND; ++d)
@@ -301,32 +313,39 @@ paged_picked_kernel(const __grid_constant__ Params P, int *status) {
             make_float2(o[d][2 * h], o[d][2 * h + 1]);
     __syncthreads();
     const int64_t slot = (2 * (int64_t)blockIdx.x + (first ? 0 : 1)) * R;
-    for (int i = threadIdx.x; i < rows * (HD / 4); i += kDecThreads) {
+    auto write = [&](int x, int c, float4 a, float L) {
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      T *dst = reinterpret_cast<T *>(P.out) + (int64_t)r * P.ld_out + (int64_t)(g * P.G + l0 + x) * HD + c;
+      if constexpr (F32)
+        *reinterpret_cast<float4 *>(dst) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+      else
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+    };
+    for (int i = threadIdx.x; i < rows * (HD / 4); i += NTH) {
       const int x = i / (HD / 4), c = i % (HD / 4) * 4;
       float M = -INFINITY, L = 0.f;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) M = fmaxf(M, s_ml[k * R + x].x);
+      for (int k = 0; k < NW; ++k) M = fmaxf(M, s_ml[k * R + x].x);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < NW; ++k) {
         const float2 ml = s_ml[k * R + x];
         const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
         const float4 v = *reinterpret_cast<const float4 *>(so + (k * R + x) * LD + c);
         L += w * ml.y;
         a.x += w * v.x; a.y += w * v.y; a.z += w * v.z; a.w += w * v.w;
       }
-      if (!whole) {
+      if constexpr (CL) {
+        *reinterpret_cast<float4 *>(s_part + x * HD + c) = a;
+        if (c == 0) s_pml[x] = make_float2(M, L);
+      } else if (!whole) {
         *reinterpret_cast<float4 *>(P.part_o + (slot + x) * HD + c) = a;
         if (c == 0) P.part_ml[slot + x] = make_float2(M, L);
       } else {
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        T *dst = reinterpret_cast<T *>(P.out) + (int64_t)r * P.ld_out + (int64_t)(g * P.G + l0 + x) * HD + c;
-        if constexpr (F32)
-          *reinterpret_cast<float4 *>(dst) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-        else
-          *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+        write(x, c, a, L);
       }
     }
+    if constexpr (CL) cluster_join<NTH, HD>(s_part, s_pml, rows, rank, ranks, write);
     __syncthreads();                            // before the next piece fills the rings and the list
   }
 }
@@ -335,22 +354,52 @@ static int full_grid() { return kBlocksPerSm * device_sm_count(); }
 
 static size_t partials() { return 2ull * full_grid() * 16; }
 
+// Few items over few keys: each item's keys go to one cluster of up to 8 blocks, which
+// joins in its shared memory (see plan_cluster in k_paged4_attn.cu).  0: the line.  A block
+// fills its SM, and clusters of 16 such blocks do not all find room at once (128 pages of
+// 16 for one row, 32/8 heads of 128: 14.2 us with 16 blocks).
+static int plan_cluster(int64_t items, int64_t blocks) {
+  const int64_t fit = device_sm_count();
+  int c = 1;
+  while (c < 8 && 8 * c < blocks) c <<= 1;
+  while (c > 1 && items * c > fit) c >>= 1;
+  if (items * c > fit) return 0;
+  const int64_t rounds = (blocks + 8 * c - 1) / (8 * c), line = (items * blocks + 4 * full_grid() - 1) / (4 * full_grid());
+  return rounds <= line + 1 ? c : 0;
+}
+
+// Key blocks of an item.
+static int64_t key_blocks(int n_picks, int page_size, int hd, cb_dtype dt) {
+  const int bn = dt == CB_BF16 ? (hd == 128 ? DecCfg<bf16, 128, 1>::kBN : DecCfg<bf16, 64, 1>::kBN)
+                               : (hd == 128 ? DecCfg<float, 128, 1>::kBN : DecCfg<float, 64, 1>::kBN);
+  return ((int64_t)n_picks * page_size + bn - 1) / bn;
+}
+
 template <typename T, int HD>
 static cudaError_t run(Params &P, int page_size, int *status, cudaStream_t s) {
   typedef DecCfg<T, HD, 1> C;
   static PerDeviceOnce attr;
   cudaError_t e = attr.run([](int) {
-    return cudaFuncSetAttribute(paged_picked_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(paged_picked_kernel<T, HD, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         C::kSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(paged_picked_kernel<T, HD, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * C::kSmem);
+    return e;
   });
   if (e != cudaSuccess) return e;
-  P.blocks = (int)(((int64_t)P.n_picks * page_size + C::kBN - 1) / C::kBN);
+  P.blocks = (int)key_blocks(P.n_picks, page_size, HD, std::is_same<T, float>::value ? CB_F32 : CB_BF16);
   const int64_t items = (int64_t)P.n_rows * P.Hkv * P.tiles;
   P.units = items * P.blocks;
+  if (const int c = plan_cluster(items, P.blocks)) {
+    e = launch_clusters(paged_picked_kernel<T, HD, true>, dim3((unsigned)(items * c)), dim3(Form<true>::kThreads), c,
+                        2 * C::kSmem, s, P, status);
+    return e == cudaSuccess ? launched(1) : e;
+  }
   // a part has a block for each warp; few items take the same number of parts each
   const int64_t most = (P.units + 3) / 4;
   P.parts = (int)(most < full_grid() ? most : full_grid());
   if (items < P.parts) P.parts -= (int)(P.parts % items);
-  e = launch_pdl(paged_picked_kernel<T, HD>, dim3(P.parts), dim3(kDecThreads), C::kSmem, s, P, status);
+  e = launch_pdl(paged_picked_kernel<T, HD, false>, dim3(P.parts), dim3(kDecThreads), C::kSmem, s, P, status);
   if (e != cudaSuccess) return e;
   e = launch_pdl(decode_merge_kernel<T, HD>, dim3(P.parts, 16 / kJoinRows), dim3(kJoinThreads),
                  P.parts * kJoinRows * sizeof(float2), s, static_cast<const AttnParams &>(P), 16);
@@ -363,6 +412,13 @@ size_t paged_picked_ws_bytes(int n_rows, int, int, int, int, int hd, cb_dtype) {
   using namespace picked;
   if (n_rows <= 0) return 0;
   return partials() * (hd * sizeof(float) + sizeof(float2)) + full_grid() * sizeof(Join);
+}
+
+void paged_picked_plan(int n_rows, int n_picks, int page_size, int Hq, int Hkv, int hd, cb_dtype dt, int64_t out[3]) {
+  const int64_t items = (int64_t)n_rows * Hkv * ((Hq / Hkv + 15) / 16), blocks = picked::key_blocks(n_picks, page_size, hd, dt);
+  out[0] = picked::plan_cluster(items, blocks);
+  out[1] = items;
+  out[2] = blocks;
 }
 
 cudaError_t launch_paged_picked(const PagedKV &kv, const cb_paged_query &a, const int32_t *picks, int n_picks,
