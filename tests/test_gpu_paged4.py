@@ -11,7 +11,8 @@ power of two: a bf16 q is exact but for elements below 2^-27 of the row's
 largest, off by 2^-39 of it; an fp32 q in two halves is off by 2^-23 of itself:
 A grows by at most 2 F hd and 4 F.  Tensor cores may truncate: twice the sums'
 error.  Probabilities round to fp16, 2^-11 with the half below (their factor of
-2^14 keeps them normal down to 2^-28): + 2^-11 B; in fp32 two halves: 2^-22 B."""
+2^8 keeps them normal down to 2^-22 of the reference and exact to 2^-33 of it
+below): + 2^-11 B; in fp32 two halves: 2^-22 B."""
 import numpy as np
 import pytest
 import torch
@@ -293,6 +294,70 @@ def test_attention_long_loops(dt, heads, page, n):
     rng = np.random.default_rng(n)
     seqs = [(n, int(rng.integers(1200, 3000))) for _ in range(26 if n < 20 else 8)]
     attention_case(rng, dt, heads, page, seqs)
+
+
+def plan(n_rows, seqs, max_kv, heads, dt):
+    import ctypes
+    out = (ctypes.c_int64 * 6)()
+    assert L.lib.cb_debug_paged4_plan(n_rows, seqs, max_kv, *heads, R.dtype_code(dt), out) == L.CB_OK
+    return list(out)
+
+
+@pytest.mark.parametrize("dt", list(HALF))
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("n,tile", [(1, 8), (3, 16), (7, 32)])
+@pytest.mark.parametrize("kv,cluster", [(200, 1), (500, 2), (1000, 4), (2000, 8), (4001, 16)])
+def test_tiles_in_clusters(dt, hd, n, tile, kv, cluster):
+    """Every cluster size and tile of the one-launch form, by the plan that leads to it; lengths
+    that leave some of a cluster's blocks without keys."""
+    heads = (8, 2, hd)
+    assert plan(n, 1, kv, heads, dt)[:2] == [tile, cluster]
+    rng = np.random.default_rng(n + kv)
+    attention_case(rng, dt, heads, 16, [(n, kv)], max_kv_len=kv)
+    attention_case(rng, dt, heads, 8, [(n, 37)], max_kv_len=kv, tail=1)
+    if tile == 8:       # several sequences, one without keys, one without rows
+        seqs = [(1, kv), (1, 0), (0, 9), (1, 33)]
+        assert plan(3, 4, kv, heads, dt)[1] > 0
+        attention_case(rng, dt, heads, 32, seqs, max_kv_len=kv)
+
+
+@pytest.mark.parametrize("dt", list(HALF))
+@pytest.mark.parametrize("n,tile", [(1, 8), (3, 16), (7, 32)])
+def test_tiles_on_the_line(dt, n, tile):
+    """Many tiles, with and without padding behind them, pieces in several parts."""
+    rng = np.random.default_rng(n)
+    for hd, count, kv in ((64, 160, 300), (128, 160, 200), (64, 3, 9000)):
+        heads, seqs = (8, 2, hd), [(n, int(rng.integers(max(n, kv // 3), kv))) for _ in range(count)]
+        bound = 40000 if count == 3 else kv
+        assert plan(n * count, count, bound, heads, dt)[:2] == [tile, 0] or tile == 32 and dt == torch.bfloat16
+        attention_case(rng, dt, heads, 16, seqs, max_kv_len=bound)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("seqs,unit,split", [
+    ([(64, 3200)], 128, True),                  # few tiles over many keys: joined parts
+    ([(300, 900)], 128, True),
+    ([(600, 700), (512, 512), (500, 2000), (900, 1500)], 0, False),
+])
+def test_chunks_by_plan(hd, seqs, unit, split):
+    heads, rows = (16, 4, hd), sum(n for n, _ in seqs)
+    p = plan(rows, len(seqs), max(kv for _, kv in seqs), heads, torch.bfloat16)
+    assert p[3] == unit or (unit == 0 and p[3] in (128, 256))
+    assert (p[4] > 1) or not split
+    rng = np.random.default_rng(rows)
+    attention_case(rng, torch.bfloat16, heads, 16, seqs, max_kv_len=max(kv for _, kv in seqs), exps=(1, -2))
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("page", [8, 32, 256])
+def test_chunks_of_256_rows(hd, page):
+    """Units of 256 rows (two tiles share each block), whole and with one tile alone."""
+    heads, seqs = (32, 8, hd), [(450, 520), (130, 200), (33, 33), (9, 300), (1, 77)]
+    p = plan(4096, 4, 4096, heads, torch.bfloat16)
+    assert p[3] == 256
+    rng = np.random.default_rng(page)
+    # the plan follows bounds: many rows in the call, few of them in sequences
+    attention_case(rng, torch.bfloat16, heads, page, seqs, tail=3500, max_kv_len=4096)
 
 
 @pytest.mark.parametrize("dt", list(HALF))

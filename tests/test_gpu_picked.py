@@ -223,6 +223,21 @@ def test_picked_attention(dt, heads, page, seqs, n):
 
 
 @pytest.mark.parametrize("dt", list(HALF))
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("n,cluster", [(3, 1), (13, 2), (25, 4), (50, 8)])
+def test_items_in_clusters(dt, hd, n, cluster):
+    """Every cluster size of the one-launch form, by the plan that leads to it."""
+    import ctypes
+    heads, page = (24, 4, hd), 8 * {(64, False): 4, (128, False): 2, (64, True): 2, (128, True): 1}[hd, dt == torch.float32]
+    out = (ctypes.c_int64 * 3)()
+    assert L.lib.cb_debug_picked_plan(3, n, page, *heads, R.dtype_code(dt), out) == L.CB_OK
+    assert out[0] == cluster
+    rng = np.random.default_rng(n)
+    picked_case(rng, dt, heads, page, [(1, 40 * page + 3), (1, 0), (1, page)], n)
+    picked_case(rng, dt, (20, 1, hd), page, [(2, 30 * page + 3), (0, 5), (1, 3)], n, tail=1)    # two tiles of heads
+
+
+@pytest.mark.parametrize("dt", list(HALF))
 def test_all_pages_are_the_whole_attention(dt):
     """Every page picked, in any order: cb_paged_attention's rows."""
     rng = np.random.default_rng(12)

@@ -132,7 +132,8 @@ def test_more_attention_refusals():
 
 
 def test_workspaces():
-    for call, need in ((attn4, L.lib.cb_paged4_attention_workspace_size(3, 2, 64, 4, 2, 128, L.CB_BF16)),
+    long4 = lambda **kw: attn4(max_kv_len=100000, **kw)     # (short keys join in a cluster: no workspace)
+    for call, need in ((long4, L.lib.cb_paged4_attention_workspace_size(3, 2, 100000, 4, 2, 128, L.CB_BF16)),
                        (select, L.lib.cb_paged_select_workspace_size(3, 64, 16, 2)),
                        (picked, L.lib.cb_paged_attention_picked_workspace_size(3, 5, 16, 4, 2, 128, L.CB_BF16))):
         assert need >= 256
@@ -183,6 +184,41 @@ def test_null_structures():
     assert L.lib.cb_paged_select(None, page_bounds(), z, L.CB_BF16, None) == INV
     assert L.lib.cb_paged_attention_picked(kv, None, A, 1, L.CB_BF16, None) == INV
     assert L.lib.cb_paged_attention_picked(None, query(), A, 1, L.CB_BF16, None) == INV
+
+
+def test_plan_queries():
+    """What calls of given sizes run (148 SMs are assumed here), and the workspace from that."""
+    def plan(*a):
+        out = (C.c_int64 * 6)(*[-5] * 6)
+        st = L.lib.cb_debug_paged4_plan(*a, out)
+        return list(out) if st == L.CB_OK else st
+
+    def plan_picked(*a):
+        out = (C.c_int64 * 3)(*[-5] * 3)
+        st = L.lib.cb_debug_picked_plan(*a, out)
+        return list(out) if st == L.CB_OK else st
+    bf, f32 = L.CB_BF16, L.CB_F32
+    assert plan(1, 1, 3137, 32, 8, 128, bf)[:2] == [8, 16] and plan(64, 64, 16384, 32, 8, 128, bf)[:2] == [8, 0]
+    assert plan(2048, 2, 16384, 32, 8, 128, bf)[3] == 256 and plan(2048, 2, 16384, 32, 8, 128, f32)[3] == 0
+    size = L.lib.cb_paged4_attention_workspace_size
+    for a in [(1, 1, 100000, 32, 8, 128), (1, 1, 900, 32, 8, 128), (64, 1, 3200, 32, 8, 128), (8192, 4, 8192, 32, 8, 128),
+              (127, 64, 16384, 32, 8, 128), (2000, 1, 30000, 24, 8, 64), (300, 1, 9000, 32, 16, 64)]:
+        for dt in (bf, f32):
+            tile, cluster, grid, unit, parts, limit = plan(*a, dt)
+            assert tile in (0, 8, 16, 32) and unit in (0, 128, 256) and (tile or unit) and cluster in (0, 1, 2, 4, 8, 16)
+            assert not (unit and dt == f32) and limit == (0 if not tile else 32 if unit else 0x7fffffff)
+            hkv, hd = a[4], a[5]
+            few = 2 * grid * tile * (4 * hd + 8) + 24 * grid if tile and not cluster else 0
+            assert size(*a, dt) >= max(256, few) and (unit or size(*a, dt) == max(256, few))
+    assert plan_picked(1, 128, 16, 32, 8, 128, bf) == [8, 8, 128] and plan_picked(64, 64, 32, 32, 8, 128, bf) == [0, 512, 128]
+    assert plan_picked(1, 3, 8, 40, 2, 64, f32) == [1, 4, 2]
+    for bad in [(0, 1, 8, 4, 2, 128, 1), (1, 1025, 8, 4, 2, 128, 1), (1, 1, -1, 4, 2, 128, 1), (1, 1, L.CB_MAX_KV_LEN + 1, 4, 2, 128, 1),
+                (1, 1, 8, 3, 2, 128, 1), (1, 1, 8, 4, 2, 80, 1), (1, 1, 8, 4, 2, 128, 2)]:
+        assert plan(*bad) == INV
+    for bad in [(0, 1, 8, 4, 2, 128, 1), (1, 0, 8, 4, 2, 128, 1), (1, 1025, 8, 4, 2, 128, 1), (1, 1, 12, 4, 2, 128, 1), (1, 1, 8, 4, 2, 128, 7)]:
+        assert plan_picked(*bad) == INV
+    assert L.lib.cb_debug_paged4_plan(1, 1, 8, 4, 2, 128, bf, None) == INV
+    assert L.lib.cb_debug_picked_plan(1, 1, 8, 4, 2, 128, bf, None) == INV
 
 
 STRUCTS = {"cb_paged4_kv": L.Paged4KV, "cb_paged_rows_out": L.PagedRowsOut, "cb_page_bounds": L.PageBounds,
