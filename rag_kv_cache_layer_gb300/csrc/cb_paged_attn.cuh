@@ -68,6 +68,28 @@ ChunkPlan plan_chunk(int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd);
 cudaError_t launch_chunk(const AttnParams &P, int R, int64_t units, int hd, int *status, cudaStream_t s,
                          bool q4 = false);
 
+// Blocks that find room at once in clusters of c, per_sm of them an SM: a cluster lies in
+// one group of SMs, and not all groups are multiples of it (as cudaOccupancyMaxActiveClusters
+// counts them on 152 SMs: 144 of 152 for 4; 120, and 288 of 304, for 8; 112 and 224 for 16).
+inline int64_t cluster_room(int sms, int per_sm, int c) {
+  return (int64_t)sms * per_sm * (c <= 2 ? 100 : c == 4 || (c == 8 && per_sm > 1) ? 94 : c == 8 ? 78 : 73) / 100;
+}
+
+// Blocks of an item's cluster (up to `most`, of eight warps) where each of `items` items has
+// `blocks` key blocks; 0: the line, `parts` blocks of four warps.  The warps' rounds over
+// their keys may be one more than on the line, which costs a launch and more parts to join;
+// lengths below the bound leave a cluster idle and the line not.  Measured, one row each of
+// S requests of one length (32/8 heads of 128), line and cluster: 3000 keys, S = 1 11.2 and
+// 8.8 us, S = 4 13.2 and 10.4, S = 16 21.6 and 17.1; 8000 keys, S = 1 15.5 and 11.1.
+inline int plan_cluster(int64_t items, int64_t blocks, int sms, int per_sm, int parts, int most) {
+  int c = 1;
+  while (c < most && 8 * c < blocks) c <<= 1;
+  while (c > 1 && items * c > cluster_room(sms, per_sm, c)) c >>= 1;
+  if (items * c > cluster_room(sms, per_sm, c)) return 0;
+  const int64_t rounds = (blocks + 8 * c - 1) / (8 * c), line = (items * blocks + 4 * parts - 1) / (4 * parts);
+  return rounds <= line + 1 ? c : 0;
+}
+
 // Tiles of R rows that n_rows rows over S sequences can make at most.
 inline int64_t tile_bound(int64_t n_rows, int S, int G, int R) {
   const int64_t a = (n_rows * G + (int64_t)S * (R - 1)) / R;

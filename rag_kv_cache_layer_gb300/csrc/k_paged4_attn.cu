@@ -608,20 +608,6 @@ struct Plan {
 // few-rows kernel alone.
 constexpr int kFewRows = 32;
 
-// Few tiles over few keys: each tile's keys go to one cluster of up to 16 blocks of eight
-// warps, which joins in its shared memory: one launch in place of two.  The warps' rounds
-// over their keys may be one or two more than on the line, which spreads over all SMs.
-static int plan_cluster(const Plan &p, int64_t items, int max_kv, cb_dtype dt) {
-  const int sms = device_sm_count(), nb = (max_kv + kBN - 1) / kBN > 0 ? (max_kv + kBN - 1) / kBN : 1;
-  const int64_t fit = sms * (p.nt == 1 && dt == CB_BF16 ? 2 : 1);
-  int c = 1;
-  while (c < 16 && 8 * c < nb) c <<= 1;
-  while (c > 1 && items * c > fit) c >>= 1;
-  if (items * c > fit) return 0;
-  const int64_t rounds = (nb + 8 * c - 1) / (8 * c), line = (items * nb + 4 * p.grid - 1) / (4 * p.grid);
-  return rounds <= line + 1 ? c : 0;
-}
-
 static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd, cb_dtype dt) {
   Plan p = {};
   const int64_t all = n_rows * G, per_seq = (all + S - 1) / S;
@@ -630,7 +616,12 @@ static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd, cb_d
   if (few || S > 1) p.nt = per_seq <= 8 ? 1 : per_seq <= 16 ? 2 : few || per_seq <= kFewRows ? 4 : 1;
   p.grid = device_sm_count() * (p.nt == 4 || dt == CB_F32 ? 2 : p.nt == 2 ? 3 : 4);
   if (few) {
-    p.cluster = plan_cluster(p, tile_bound(n_rows, S, G, 8 * p.nt) * Hkv, max_kv, dt);
+    // few tiles over few keys: each tile's keys go to one cluster of up to 16 blocks, which
+    // joins in its shared memory: one launch in place of two (counted is one tile for
+    // every sequence at least; clusters of tiles that there are not leave at once)
+    const int64_t full = (all + 8 * p.nt - 1) / (8 * p.nt), seqs = S < n_rows ? S : n_rows;
+    p.cluster = plan_cluster((full > seqs ? full : seqs) * Hkv, max_kv > 0 ? (max_kv + kBN - 1) / kBN : 1,
+                             device_sm_count(), p.nt == 1 && dt == CB_BF16 ? 2 : 1, p.grid, 16);
     return p;
   }
   if (S > 1) p.few_hi = p.rows_lo = kFewRows;

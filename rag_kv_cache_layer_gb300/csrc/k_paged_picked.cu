@@ -355,17 +355,9 @@ static int full_grid() { return kBlocksPerSm * device_sm_count(); }
 static size_t partials() { return 2ull * full_grid() * 16; }
 
 // Few items over few keys: each item's keys go to one cluster of up to 8 blocks, which
-// joins in its shared memory (see plan_cluster in k_paged4_attn.cu).  0: the line.  A block
-// fills its SM, and clusters of 16 such blocks do not all find room at once (128 pages of
-// 16 for one row, 32/8 heads of 128: 14.2 us with 16 blocks).
-static int plan_cluster(int64_t items, int64_t blocks) {
-  const int64_t fit = device_sm_count();
-  int c = 1;
-  while (c < 8 && 8 * c < blocks) c <<= 1;
-  while (c > 1 && items * c > fit) c >>= 1;
-  if (items * c > fit) return 0;
-  const int64_t rounds = (blocks + 8 * c - 1) / (8 * c), line = (items * blocks + 4 * full_grid() - 1) / (4 * full_grid());
-  return rounds <= line + 1 ? c : 0;
+// joins in its shared memory.  0: the line.
+static int cluster_of(int64_t items, int64_t blocks) {
+  return plan_cluster(items, blocks, device_sm_count(), 1, full_grid(), 8);
 }
 
 // Key blocks of an item.
@@ -390,7 +382,7 @@ static cudaError_t run(Params &P, int page_size, int *status, cudaStream_t s) {
   P.blocks = (int)key_blocks(P.n_picks, page_size, HD, std::is_same<T, float>::value ? CB_F32 : CB_BF16);
   const int64_t items = (int64_t)P.n_rows * P.Hkv * P.tiles;
   P.units = items * P.blocks;
-  if (const int c = plan_cluster(items, P.blocks)) {
+  if (const int c = cluster_of(items, P.blocks)) {
     e = launch_clusters(paged_picked_kernel<T, HD, true>, dim3((unsigned)(items * c)), dim3(Form<true>::kThreads), c,
                         2 * C::kSmem, s, P, status);
     return e == cudaSuccess ? launched(1) : e;
@@ -416,7 +408,7 @@ size_t paged_picked_ws_bytes(int n_rows, int, int, int, int, int hd, cb_dtype) {
 
 void paged_picked_plan(int n_rows, int n_picks, int page_size, int Hq, int Hkv, int hd, cb_dtype dt, int64_t out[3]) {
   const int64_t items = (int64_t)n_rows * Hkv * ((Hq / Hkv + 15) / 16), blocks = picked::key_blocks(n_picks, page_size, hd, dt);
-  out[0] = picked::plan_cluster(items, blocks);
+  out[0] = picked::cluster_of(items, blocks);
   out[1] = items;
   out[2] = blocks;
 }
