@@ -55,7 +55,7 @@ paged_picked_kernel(const __grid_constant__ Params P, int *status) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int s_page[CB_MAX_PICKS], s_vis[CB_MAX_PICKS];   // page of the pool, slots that the row sees
   __shared__ float2 s_ml[NW * R];
-  __shared__ int s_seq, s_any;
+  __shared__ int s_seq, s_last;                 // s_last: picks up to the last one with a slot that the row sees
   // CL: the block's joined rows, read by the cluster's others
   __shared__ __align__(16) float s_part[CL ? R * HD : 4];
   __shared__ float2 s_pml[CL ? R : 1];
@@ -76,16 +76,15 @@ paged_picked_kernel(const __grid_constant__ Params P, int *status) {
 
   for (int64_t u = u0; u < u1;) {
     const int64_t item = CL ? blockIdx.x / ranks : u / P.blocks;
-    const int jb = CL ? (int)((int64_t)P.blocks * rank / ranks) : (int)(u - item * P.blocks);
-    const int je = CL ? (int)((int64_t)P.blocks * (rank + 1) / ranks) : (int)min((int64_t)P.blocks, jb + (u1 - u));
-    const bool whole = je - jb == P.blocks, first = u == u0;
+    int jb = CL ? 0 : (int)(u - item * P.blocks), je = CL ? P.blocks : (int)min((int64_t)P.blocks, jb + (u1 - u));
+    const bool whole = CL || je - jb == P.blocks, first = u == u0;
     const int tile = (int)(item % P.tiles), g = (int)(item / P.tiles % P.Hkv), r = (int)(item / P.tiles / P.Hkv);
     const int l0 = tile * R, rows = min(R, P.G - l0);
     u = CL ? u1 : u + (je - jb);
     // the row's sequence and position
     if (threadIdx.x == 0) {
       s_seq = 0x7fffffff;
-      s_any = 0;
+      s_last = 0;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < P.kv.n_seq; i += NTH) {
@@ -111,7 +110,7 @@ paged_picked_kernel(const __grid_constant__ Params P, int *status) {
     }
     const int64_t pos = (int64_t)kv - __ldg(P.kv.row_offsets + s + 1) + r;
     const int32_t *table = P.kv.block_table + (int64_t)s * P.kv.ld_table;
-    bool any = false;
+    int last = 0;
     for (int i = p0 + threadIdx.x; i < p1; i += NTH) {
       const int j = s_page[i];
       int page = -1, vis = 0;
@@ -131,13 +130,20 @@ paged_picked_kernel(const __grid_constant__ Params P, int *status) {
       }
       s_page[i] = page;
       s_vis[i] = vis;
-      any |= vis > 0;
+      if (vis > 0) last = i + 1;
     }
-    if (any) s_any = 1;
+    if (last > 0) atomicMax(&s_last, last);
     if (!CL && threadIdx.x == 0 && u == u1 && jb == 0 && !whole)     // the last piece: the one that goes on in the next part
       P.joins[blockIdx.x] = Join{r, l0, rows, g, part_of(P, (item + 1) * P.blocks - 1), first ? 0 : 1};
     __syncthreads();
-    const int end = s_any ? je : jb;            // a piece without a key has nothing to stream
+    // nothing is streamed behind the list's last page (short contexts leave lists half
+    // empty); a cluster shares what is in front of it
+    const int full = (int)min((int64_t)je, (((int64_t)s_last << shift) + BN - 1) / BN);
+    if constexpr (CL) {
+      jb = (int)((int64_t)full * rank / ranks);
+      je = (int)((int64_t)full * (rank + 1) / ranks);
+    }
+    const int end = CL ? je : max(full, jb);
 
     const int64_t lane_off = g * HD + ccol * kVec;
     // slots that the row sees of key block j * BN + x's page, from that key on (<= 0: none)
