@@ -221,12 +221,13 @@ paged_score_kernel(const __grid_constant__ SelectParams P, int *status) {
 // pages form one line that the grid shares in equal parts (long and short requests in
 // one batch keep every SM busy); neighbouring warps take neighbouring heads of the same
 // pages, whose bounds lie side by side.
-constexpr int kTStages = 3;              // of each warp
+constexpr int kTStages = 3;              // of each warp: 192 KB of bounds in a block
 
 // The line: tiles of a sequence, each of its rows as many as its last one.
 struct ScoreLine {
   int64_t begin[CB_MAX_SEQS + 1];       // first tile of each sequence
   int tiles[CB_MAX_SEQS];               // tiles of one of its rows
+  int row0[CB_MAX_SEQS + 1], kv[CB_MAX_SEQS];
 };
 
 // (the bound of 384 threads leaves registers for a block of the choice beside this one's)
@@ -261,6 +262,8 @@ paged_score_tc_kernel(const __grid_constant__ SelectParams P, int *status) {
           }
         }
         line.tiles[i] = tiles;
+        line.row0[i] = __ldg(P.kv.row_offsets + i);
+        line.kv[i] = kv;
         n[k] = (int64_t)rows * tiles;
         sum += n[k];
       }
@@ -280,7 +283,10 @@ paged_score_tc_kernel(const __grid_constant__ SelectParams P, int *status) {
       if (k < per && i0 + k < S) line.begin[i0 + k] = first;
       first += n[k];
     }
-    if (threadIdx.x == kSThreads - 1) line.begin[S] = first;
+    if (threadIdx.x == kSThreads - 1) {
+      line.begin[S] = first;
+      line.row0[S] = __ldg(P.kv.row_offsets + S);
+    }
     __syncthreads();
   }
   const int64_t units = line.begin[S] * P.Hkv;
@@ -308,9 +314,9 @@ paged_score_tc_kernel(const __grid_constant__ SelectParams P, int *status) {
         if (line.begin[mid] <= tile) lo = mid; else hi = mid - 1;
       }
       s = lo;
-      row0 = __ldg(P.kv.row_offsets + s);
-      n = __ldg(P.kv.row_offsets + s + 1) - row0;
-      kv = __ldg(P.kv.kv_lens + s);
+      row0 = line.row0[s];
+      n = line.row0[s + 1] - row0;
+      kv = line.kv[s];
     }
     const int64_t local = tile - line.begin[s];
     const int per = line.tiles[s], i = n == 1 ? 0 : (int)(local / per);
@@ -491,7 +497,7 @@ __global__ void __launch_bounds__(kCThreads, 1024 / kCThreads)
 paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
   constexpr int NW = kCThreads / 32;
   __shared__ RowPlace s_row;
-  __shared__ int s_hist[kBins + kBins / 32], s_warp[NW], s_bin, s_in, s_count;
+  __shared__ int s_hist[kBins + kBins / 32], s_warp[NW], s_bin, s_in, s_count, s_sure;
   __shared__ float s_f[4][NW];
   __shared__ unsigned s_mask[kCThreads];
   __shared__ float2 s_pair[kPairs * kPairs];
@@ -612,18 +618,36 @@ paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
     sure = in_pool >= want ? to + 2.f * eps : -3.402823466e38f;
     none = in_pool >= want ? from - 2.f * eps : -INFINITY;
   }
-  // how many are in for certain; exact scores of those between
-  if (tid == 0) s_count = 0;
+  // how many are in for certain (where registers hold all scores, as masks of 32 pages
+  // each); the list of those between
+  const bool masks = hi - lo <= kHeld * kCThreads;
+  if (tid == 0) s_count = s_sure = 0;
   __syncthreads();
-  int in = 0, total;
-  if (want > 0)
-    each([&](int j, float x) {
-      if (x > sure) ++in;
-      else if (x >= none) list[atomicAdd(&s_count, 1)] = j;
-    });
-  block_scan<kCThreads>(in, s_warp, total);
-  const int need = want - total;                            // of the pages between
+  if (want > 0) {
+    int in = 0;
+    if (masks) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        const int j = lo + tid + i * kCThreads;
+        const bool sure_in = j < hi && held[i] > sure;
+        const unsigned mask = __ballot_sync(0xffffffffu, sure_in);
+        if (lane == 0) s_mask[i * NW + warp] = mask;
+        in += __popc(mask);
+        if (j < hi && !sure_in && held[i] >= none) list[atomicAdd(&s_count, 1)] = j;
+      }
+      if (lane == 0) atomicAdd(&s_sure, in);
+    } else {
+      each([&](int j, float x) {
+        if (x > sure) ++in;
+        else if (x >= none) list[atomicAdd(&s_count, 1)] = j;
+      });
+      atomicAdd(&s_sure, in);
+    }
+  } else if (masks) {
+    for (int i = tid; i < kHeld * NW; i += kCThreads) s_mask[i] = 0;
+  }
   __syncthreads();
+  const int need = want - s_sure;                           // of the pages between
   if (s_count > need) {
     // a warp takes a page and, of up to eight heads, one; the largest of a page's heads
     // afterwards
@@ -679,9 +703,25 @@ paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
         better += f.x > e.x || (f.x == e.x && (f.y > e.y || (f.y == e.y && list[k] < j)));
       }
     }
-    a[j].y = better < need ? -1.f : -2.f;
+    if (!masks) a[j].y = better < need ? -1.f : -2.f;
+    else if (better < need) atomicOr(&s_mask[(j - lo) >> 5], 1u << ((j - lo) & 31));
   }
   __syncthreads();
+  if (masks) {
+    // ascending: the first pages, those of the masks, the last pages
+    const int words = kHeld * NW;
+    int n;
+    const int before = block_scan<kCThreads>(tid < words ? __popc(s_mask[tid]) : 0, s_warp, n);
+    s_hist[tid] = P.n_first + before;
+    __syncthreads();
+    for (int k = warp; k < words; k += NW) {
+      const unsigned mask = s_mask[k];
+      if (mask >> lane & 1) out[s_hist[k] + __popc(mask & ((1u << lane) - 1))] = lo + k * 32 + lane;
+    }
+    for (int i = tid; i < P.n_first; i += kCThreads) out[i] = i;
+    for (int i = tid; i < P.n_last; i += kCThreads) out[P.n_picks - P.n_last + i] = hi + i;
+    return;
+  }
   // ascending: a mask for every 32 pages, one scan over the masks of 32 kCThreads pages
   int written = 0;
   for (int j0 = 0; j0 < pages; j0 += 32 * kCThreads) {
