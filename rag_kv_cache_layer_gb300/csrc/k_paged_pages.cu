@@ -537,7 +537,7 @@ paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
       if (lo + tid + i * kCThreads < hi) f(lo + tid + i * kCThreads, held[i]);
-    for (int j = lo + tid + kHeld * kCThreads; j < hi; j += kCThreads) f(j, a[j].x);
+    for (int j = lo + tid + kHeld * kCThreads; j < hi; j += kCThreads) f(j, a[j].x > -INFINITY ? a[j].x : -INFINITY);
   };
   if (want > 0) {
     float v[4] = {-INFINITY, -INFINITY, 0.f, norm};          // largest score, largest negative, |bound|, |q|_1
@@ -554,7 +554,7 @@ paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
     for (int i = 0; i < kHeld; ++i) {
       const int j = lo + tid + i * kCThreads;
       const float2 x = j < hi ? a[j] : make_float2(-INFINITY, 0.f);
-      held[i] = x.x;
+      held[i] = x.x > -INFINITY ? x.x : -INFINITY;          // (a NaN counts as a page outside the pool)
       take(x);
     }
     for (int j = lo + tid + kHeld * kCThreads; j < hi; j += kCThreads) take(a[j]);
@@ -674,7 +674,7 @@ paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
               add_exact(hi, lo, lane & o ? sum.x : x);
               sum = make_float2(hi, lo);
             }
-            const float hi = sum.x + sum.y, lo = sum.y - (hi - sum.x);   // one pair for one sum
+            const float hi = sum.x + sum.y, lo = fabsf(hi) < INFINITY ? sum.y - (hi - sum.x) : 0.f;   // one pair for one sum
             if (hi > best.x || (hi == best.x && lo > best.y)) best = make_float2(hi, lo);
           }
         }
@@ -716,8 +716,11 @@ paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
     __syncthreads();
     for (int k = warp; k < words; k += NW) {
       const unsigned mask = s_mask[k];
-      if (mask >> lane & 1) out[s_hist[k] + __popc(mask & ((1u << lane) - 1))] = lo + k * 32 + lane;
+      const int at = s_hist[k] + __popc(mask & ((1u << lane) - 1));
+      if (mask >> lane & 1 && at < P.n_picks - P.n_last) out[at] = lo + k * 32 + lane;
     }
+    // (scores that are not finite may leave places, or be too many)
+    for (int i = P.n_first + n + tid; i < P.n_picks - P.n_last; i += kCThreads) out[i] = -1;
     for (int i = tid; i < P.n_first; i += kCThreads) out[i] = i;
     for (int i = tid; i < P.n_last; i += kCThreads) out[P.n_picks - P.n_last + i] = hi + i;
     return;
@@ -743,11 +746,13 @@ paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
     __syncthreads();
     for (int k = warp; k < groups; k += NW) {
       const unsigned mask = s_mask[k];
-      if (mask >> lane & 1) out[s_hist[k] + __popc(mask & ((1u << lane) - 1))] = j0 + k * 32 + lane;
+      const int at = s_hist[k] + __popc(mask & ((1u << lane) - 1));
+      if (mask >> lane & 1 && at < P.n_picks) out[at] = j0 + k * 32 + lane;
     }
     written += n;
     __syncthreads();
   }
+  for (int i = written + tid; i < P.n_picks; i += kCThreads) out[i] = -1;
 }
 
 }  // namespace pages

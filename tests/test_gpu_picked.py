@@ -142,6 +142,31 @@ def test_select_scores_of_any_distribution(dt, kind):
     assert np.array_equal(picks.cpu().numpy(), want) and R.device_status() == 0
 
 
+@pytest.mark.parametrize("dt", list(HALF))
+@pytest.mark.parametrize("pages", [60, 9000])
+def test_select_keeps_its_places_where_scores_are_not_finite(dt, pages):
+    """Not promised to be sensible, but n_picks places a row are written and no others, with
+    pages of the row or -1, the forced ones among them."""
+    for what in ("q nan", "q inf", "bounds nan", "bounds inf", "overflow"):
+        bounds = torch.randn(pages, 1, 64, device="cuda").to(dt).repeat(1, 2, 1)
+        q = torch.randn(1, 128, device="cuda").to(dt)
+        if what[0] == "q":
+            q[0, 5] = float(what[2:])
+        elif what == "overflow":
+            bounds, q = bounds * 3e38, q * 3e38
+        else:
+            bounds[::3, 1, 7] = float(what[7:])
+        table = torch.randperm(pages, device="cuda").int()[None]
+        picks = torch.full((3, 1, 20), -5, dtype=torch.int32, device="cuda")
+        R.cb_paged_select(q, ints([0, 1]), ints([8 * pages]), table, bounds, 8, 2, 1, 64, picks[1:2], n_first=2, n_last=3)
+        torch.cuda.synchronize()
+        assert (picks[0] == -5).all() and (picks[2] == -5).all()
+        got = picks[1, 0].tolist()
+        assert got[:2] == [0, 1] and (got[-3:] == list(range(pages - 3, pages)) or -1 in got)
+        assert all(-1 <= j < pages for j in got) and len(set(got) - {-1}) == sum(j >= 0 for j in got)
+    assert R.device_status() == 0
+
+
 def test_select_errors_on_the_device():
     dt, page = torch.bfloat16, 8
     bounds, q = torch.zeros(20, 2, 64, dtype=dt, device="cuda"), torch.ones(3, 64, dtype=dt, device="cuda")
