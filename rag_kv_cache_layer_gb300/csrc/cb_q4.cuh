@@ -39,7 +39,7 @@ __device__ __forceinline__ void decode8(uint32_t w, uint32_t (&h)[4]) {
 // Two scales of 16 bits, the low one first, as fp16.
 __device__ __forceinline__ uint32_t decode_scales(uint32_t two) {
   uint32_t h;
-  asm("{\n\t.reg .b16 s;\n\tcvt.u16.u32 s, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, s;\n\t}" : "=r"(h) : "r"(two));
+  asm("{\n\t.reg .b16 s, t;\n\tmov.b32 {s, t}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, s;\n\t}" : "=r"(h) : "r"(two));
   return h;
 }
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {

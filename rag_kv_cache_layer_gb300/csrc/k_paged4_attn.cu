@@ -89,8 +89,8 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   return v;
 }
 __device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+  uint32_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
 __device__ __forceinline__ uint32_t lds8(uint32_t a) {
@@ -229,41 +229,62 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
     const int sure = base + P.by_G.div(l0);                   // every row sees the keys up to this one
     const int32_t *table = P.kv.block_table + (int64_t)s * P.kv.ld_table;
 
-    auto fetch = [&](int j) -> int {            // page of key j * 32 + lane
-      const int key = j * kBN + lane;
-      return j < je && key < kv ? __ldg(table + (key >> shift)) : -1;
-    };
     const uint8_t *const head = pool + (int64_t)g * P.head_bytes;
     // places of this lane's 16 bytes of a stage's values and scales; a 16-byte column of
     // the values is swizzled by the key's bit 1 (see below)
-    const bool one_page = page_size >= kBN;
     const uint32_t vdst = C::kOffV + (HD == 128 ? (lane & ~3) * 16 + ((lane & 3) ^ ((lane >> 2) & 2)) * 16 : lane * 16);
     constexpr int kHalf = C::kScales / 16;      // lanes that copy the keys' scales
-    const uint32_t sdst = C::kOffKs + lane * 16;
-    const int ssrc = lane < kHalf ? q4::scales_at(page_size, HD, false) + lane * 16
-                                  : q4::scales_at(page_size, HD, true) + (lane - kHalf) * 16;
-    auto load = [&](int j, int st, int page) {
-      const uint32_t dst = ring + st * C::kStage;
-      const int key0 = j * kBN, left = kv - key0;             // keys from key0 on
-      if (lane < left && (page < 0 || page >= P.kv.n_pages)) {
+    const uint8_t *const codes = head + lane * 16, *const scales = head +
+        (lane < kHalf ? q4::scales_at(page_size, HD, false) + lane * 16
+                      : q4::scales_at(page_size, HD, true) + (lane - kHalf) * 16);
+    const int to_v = q4::codes_at(page_size, HD, true);
+    // A block has 1, 2 or 4 pages (page_size >= 32, 16, 8), 2^es.  The warp reads the table
+    // for 32 >> es of its blocks at once: lane i has page i mod 2^es of the (i >> es)-th,
+    // -1 where there is no key or no page of the pool.
+    const bool one_page = page_size >= kBN && P.kv.page_stride >> 32 == 0;
+    const uint32_t stride32 = (uint32_t)P.kv.page_stride;
+    const int es = shift >= 5 ? 0 : 5 - shift, batch = 32 >> es;
+    int from = jb + warp, ahead = from, left_in = batch, pages, next_pages;    // from: the next block to load
+    auto fetch = [&]() -> int {
+      const int key = (ahead + (lane >> es) * NW) * kBN + (lane & ((1 << es) - 1)) * (kBN >> es);
+      const bool there = ahead + (lane >> es) * NW < je && key < kv;
+      ahead += batch * NW;
+      int page = there ? __ldg(table + (key >> shift)) : -1;
+      if (there && (page < 0 || page >= P.kv.n_pages)) {
         report(status, CB_ERR_DEVICE_INDEX);
         page = -1;
       }
+      return page;
+    };
+    pages = fetch();
+    next_pages = -1;                            // (a batch outlasts the prologue)
+    // Loads block `from`, the batch's (batch - left_in)-th, to the stage at dst, and goes on to
+    // the next.
+    auto load = [&](uint32_t dst) {
+      const int j = from, at = (batch - left_in) << es;       // lane of the block's first page
+      const int key0 = j * kBN, left = kv - key0;             // keys from key0 on
+      from += NW;
       // A whole block inside one page: everything lies at fixed distances.
-      if (one_page && left >= kBN) {
-        const int pg = __shfl_sync(0xffffffffu, page, 0), slot = key0 & (page_size - 1);
-        if (pg >= 0) {
-          const uint8_t *src = head + pg * P.kv.page_stride + slot * (HD / 2) + lane * 16;
-          const uint8_t *vsrc = src + q4::codes_at(page_size, HD, true);
-#pragma unroll
-          for (int i = 0; i < C::kCodes / 512; ++i) {
-            copy_all(dst + lane * 16 + i * 512, src + i * 512);
-            copy_all(dst + vdst + i * 512, vsrc + i * 512);
-          }
-          if (HD == 128 || lane < 16) copy_all(dst + sdst, head + pg * P.kv.page_stride + ssrc + slot * (HD / 16));
-          return;
-        }
+      const int pg0 = __shfl_sync(0xffffffffu, pages, at);
+      const int these = pages;
+      if (--left_in == 0) {
+        pages = next_pages;
+        left_in = batch;
+        next_pages = fetch();
       }
+      if (one_page && left >= kBN && pg0 >= 0) {
+        const int slot = key0 & (page_size - 1);
+        const uint64_t off = (uint64_t)(uint32_t)pg0 * stride32;
+        const uint8_t *src = codes + off + slot * (HD / 2), *vsrc = src + to_v;
+#pragma unroll
+        for (int i = 0; i < C::kCodes / 512; ++i) {
+          copy_all(dst + lane * 16 + i * 512, src + i * 512);
+          copy_all(dst + vdst + i * 512, vsrc + i * 512);
+        }
+        if (HD == 128 || lane < 16) copy_all(dst + C::kOffKs + lane * 16, scales + off + slot * (HD / 16));
+        return;
+      }
+      const int page = __shfl_sync(0xffffffffu, these, at + (lane >> (5 - es)));   // of key key0 + lane
       // Codes: a warp copies 512 bytes at once, 1024 / HD keys: a group of eight
       // keys lies in one page (page_size >= 8).  The values' 16-byte columns are
       // swizzled by the key (bit 1) so that the fragments' loads meet all banks.
@@ -293,25 +314,12 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
-    // the table is read kAhead blocks further ahead than the pages
-    constexpr int kAhead = 3;
-    int ahead[kAhead], from = jb + warp;
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) ahead[i] = fetch(from + i * NW);
-    auto next_page = [&]() -> int {
-      const int page = ahead[0];
-#pragma unroll
-      for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
-      ahead[kAhead - 1] = fetch(from + kAhead * NW);
-      from += NW;
-      return page;
-    };
 #pragma unroll 1
     for (int i = 0; i < NS - 1; ++i) {
-      const int j = from, page = next_page();
-      if (j < je) load(j, i, page);
+      if (from < je) load(ring + i * C::kStage);
       commit();
     }
+    next_pages = fetch();
     // q: column gid of tile nt is row nt * 8 + gid; k-step k takes dimensions
     // HD / 4 * q4 + 4 k .. + 3 of it
     uint32_t qh[NT][KS][2], ql[F32 ? NT : 1][F32 ? KS : 1][2];
@@ -368,19 +376,18 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[t][nt][k] = 0.f;
     }
-    // Row i of a score tile of 16 keys is key (i & 8) + (i & 7) / 2 + 4 (i & 1): the
-    // four keys whose values a lane needs then are q4, q4 + 4, q4 + 8, q4 + 12.
-    const int krow = (gid >> 1) + 4 * (gid & 1);
+    // Rows 2 a and 2 a + 1 of a score tile's eight keys are keys a and 4 + (a ^ 1): the keys
+    // whose values a lane needs then are q4 and 4 + (q4 ^ 1) of each eight, and both the
+    // keys' loads (neighbouring rows) and the values' (a lane's four keys) meet all banks.
+    const int krow = gid & 1 ? 4 + ((gid >> 1) ^ 1) : gid >> 1;
+    const int vkey[2] = {q4, 4 + (q4 ^ 1)};
     int st = 0, fill = NS - 1;
     for (int j = jb + warp; j < je; j += NW) {
       asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
       __syncwarp();                             // landed for every lane; the stage before is used up
-      {
-        const int jn = from, page = next_page();
-        if (jn < je) load(jn, fill, page);
-        commit();
-        fill = fill + 1 == NS ? 0 : fill + 1;
-      }
+      if (from < je) load(ring + fill * C::kStage);
+      commit();
+      fill = fill + 1 == NS ? 0 : fill + 1;
       const uint32_t stage = ring + st * C::kStage;
       st = st + 1 == NS ? 0 : st + 1;
       float x[2][NT][4];
@@ -487,22 +494,22 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
             ph[nt][h] = transposed(hi);
             if constexpr (F32) pl[nt][h] = transposed(pack_rest(p[0], p[1], hi));
           }
-        // values of keys q4 + 4 i; pairs (i = 0, 1) and (2, 3)
+        // values of the lane's four keys; pairs (i = 0, 1) and (2, 3)
         uint32_t w[4][VW], sc[2];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int key = mt * 16 + q4 + 4 * i;
+          const int key = mt * 16 + 8 * (i >> 1) + vkey[i & 1];
           const int col = HD == 128 ? ((gid >> 1) ^ (key & 2)) * 16 + (gid & 1) * 8 : gid * 4;
           lds_words<VW>(stage + C::kOffV + key * (HD / 2) + col, w[i]);
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t at = stage + C::kOffVs + (mt * 16 + q4 + 8 * h) * (HD / 16) + gid * HD / 128;
-          sc[h] = q4::decode_scales(__byte_perm(lds8(at), lds8(at + 4 * (HD / 16)), 0x0040));
+          const uint32_t at = stage + C::kOffVs + (mt * 16 + 8 * h) * (HD / 16) + gid * HD / 128;
+          sc[h] = q4::decode_scales(__byte_perm(lds8(at + vkey[0] * (HD / 16)), lds8(at + vkey[1] * (HD / 16)), 0x0040));
         }
 #pragma unroll
         for (int i = 0; i < VW; ++i) {
-          uint32_t even[2][4], odd[2][4];       // (key, key + 4) of dimensions 2 t and 2 t + 1
+          uint32_t even[2][4], odd[2][4];       // pairs of keys, of dimensions 2 t and 2 t + 1
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t a = w[2 * h][i], b = w[2 * h + 1][i];
