@@ -40,6 +40,8 @@ using namespace paged;
 typedef AttnParams Params;
 
 constexpr int kBN = 32;                 // keys per block
+// Blocks that a tile's own cost (its q, the joins) counts as when the line is cut: 64 ragged
+// requests 51 us, without 73, with 24 55; two of 131 k keys 61.6 and 63.4.
 constexpr int kPad = 12;
 constexpr float kPShift = 8.f;          // log2 of P at the reference
 constexpr float kRise = 7.f;            // log2 of what a score may exceed it by: P stays below 2^15
@@ -610,17 +612,21 @@ struct Plan {
   ChunkPlan chunk;                      // R 0: not launched
 };
 
-// bf16: as for the 16-bit cache, sequences of up to kFewRows rows (queries x G) go
-// through the few-rows kernel, longer ones through the chunk kernel; fp32 runs the
-// few-rows kernel alone.
-constexpr int kFewRows = 32;
+// bf16: sequences of up to few_rows rows (queries x G) go through the few-rows kernel,
+// longer ones through the chunk kernel, which is made for 128 rows; fp32 runs the
+// few-rows kernel alone.  A tile of 32 rows reads its keys once, two of them twice: at
+// head_dim 128, 32 rows 64 x over 4096 keys take 203 us as one tile and 266 by the chunk
+// kernel, 48 rows 365 and 271; at 64, where the chunk kernel's softmax has half the
+// products to hide behind, 16 x 36 or 64 rows over 8192 keys take 87 and 88 against 106
+// and 98 (one sequence over 4096 keys alone 20 against 17.5).
+static int few_rows(int hd) { return hd == 64 ? 64 : 32; }
 
 static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd, cb_dtype dt) {
   Plan p = {};
   const int64_t all = n_rows * G, per_seq = (all + S - 1) / S;
-  const bool few = dt == CB_F32 || all <= kFewRows || n_rows <= S;
+  const bool few = dt == CB_F32 || all <= few_rows(hd) || n_rows <= S;
   p.few_hi = 0x7fffffff;
-  if (few || S > 1) p.nt = per_seq <= 8 ? 1 : per_seq <= 16 ? 2 : few || per_seq <= kFewRows ? 4 : 1;
+  if (few || S > 1) p.nt = per_seq <= 8 ? 1 : per_seq <= 16 ? 2 : few || per_seq <= few_rows(hd) ? 4 : 1;
   p.grid = device_sm_count() * (p.nt == 4 || dt == CB_F32 ? 2 : p.nt == 2 ? 3 : 4);
   if (few) {
     // few tiles over few keys: each tile's keys go to one cluster of up to 16 blocks, which
@@ -631,7 +637,7 @@ static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd, cb_d
                              device_sm_count(), p.nt == 1 && dt == CB_BF16 ? 2 : 1, p.grid, 16);
     return p;
   }
-  if (S > 1) p.few_hi = p.rows_lo = kFewRows;
+  if (S > 1) p.few_hi = p.rows_lo = few_rows(hd);
   p.chunk = plan_chunk(n_rows, S, max_kv, G, Hkv, hd);
   return p;
 }
@@ -710,7 +716,7 @@ cudaError_t launch_paged4_attention(const cb_paged4_kv &kv, const cb_paged_query
   P.G = G;
   P.Hkv = a.n_kv_heads;
   P.max_kv = a.max_kv_len;
-  P.pad = 2 * kv.n_seq * a.n_kv_heads >= p.grid ? kPad : 0;
+  P.pad = kPad;
   P.n_split = p.chunk.n_split;
   P.few_hi = p.few_hi;
   P.rows_lo = p.rows_lo;
