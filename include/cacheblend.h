@@ -1004,8 +1004,8 @@ cb_status cb_paged_bounds(const cb_paged_kv *kv, const cb_page_bounds *bounds,
  *   score(j) = max_h sum_d max(q[h][d] min[j][d], q[h][d] max[j][d]).
  * Where the row has more than n_picks pages: the first n_first, the last n_last
  * and of the others those of the largest scores (ties: the lower page), n_picks
- * in all; else all of them.  Where the choice hangs on it, scores are summed in
- * 64 bits.
+ * in all; else all of them.  Where the choice hangs on it, scores are summed to
+ * 2^-40 of their terms' magnitudes.
  * picks: device int32 [n_rows][n_kv_heads][n_picks] contiguous, a sequence's page
  * numbers (indices into its table row) ascending, -1 behind the last one; all -1
  * for a row with a negative position.  Rows of no sequence, or of one with wrong

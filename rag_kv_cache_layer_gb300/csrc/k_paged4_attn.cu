@@ -4,15 +4,18 @@
 // tile is R = 8 NT rows of one sequence and kv head, its keys come in blocks of 32,
 // all blocks of all tiles form one line that the grid's blocks share in equal parts,
 // and decode_merge_kernel joins tiles that several parts hold.  The block's four
-// warps take a tile's key blocks in turn, each with a cp.async ring of its own.
+// warps take a tile's key blocks in turn, each with a cp.async ring of its own.  A call
+// of few tiles over few keys gives each tile to a cluster instead, blocks of eight
+// warps, which join in its shared memory: one launch (see plan_cluster).
 //
 // Mathematics.  A code times its scale is exact in fp16 (cb_q4.cuh), so keys and
 // values meet the tensor cores as fp16 without a rounding.  q is put into fp16 after
 // a power of two per row that brings its largest magnitude to [2^13, 2^14): a bf16 q
 // is then exact down to 2^-27 of that magnitude and off by at most 2^-39 of it
-// below.  P = 2^(x - m + 8), m a reference that scores exceed by 2^7 at most, rounds to
-// fp16 (2^-12 of itself, 2^-33 of the reference's weight at the bottom); both powers of two leave with the softmax scale and the
-// division by the sum.  fp32 rows take q and P as two fp16 halves (hi, lo with
+// below.  P = 2^(x - m + 8), m a reference that the scores x exceed by 7 at most (so that
+// most blocks leave it and O as they are), rounds to fp16 (2^-12 of itself, 2^-33 of the
+// reference's weight at the bottom); both powers of two leave with the softmax scale and
+// the division by the sum.  fp32 rows take q and P as two fp16 halves (hi, lo with
 // 2^-22 and less dropped) and every step of 16 in a fresh accumulator that is added
 // in fp32, since the tensor core truncates its sums.
 //
@@ -24,6 +27,15 @@
 // conversion and one product with the scale for two values; V's pairs are two keys'
 // codes of one dimension, put into a byte by a shift and a select first.  S^T comes
 // out as P^T's operand up to a transposition of 8x8 blocks (movmatrix).
+//
+// Measured, 32/8 heads of 128: 64 ragged requests of up to 16,384 keys 51.2 us (4.2 TB/s
+// of 216 MB), two of 131 k keys 61.5 (4.8 TB/s), one row over 3137 keys 8.3 from a graph.
+// Bound by instructions, not by the cache's bytes: a block of 32 keys costs a warp about
+// 590, of which 250 go to the ALU pipe at half a warp a cycle (the codes' conversions,
+// the maximum, the masks), 220 to the FMA pipes, 30 to the tensor cores (26% busy); a
+// scheduler issues in 0.60 of its cycles with its four warps and waits mostly for the
+// results of the warp's own instructions.  The 16-bit cache's kernel is bound by bytes
+// (122 us for the same requests).
 #include "cb_common.cuh"
 #include "cb_internal.h"
 #include "cb_paged.cuh"
@@ -44,7 +56,9 @@ constexpr int kBN = 32;                 // keys per block
 // requests 51 us, without 73, with 24 55; two of 131 k keys 61.6 and 63.4.
 constexpr int kPad = 12;
 constexpr float kPShift = 8.f;          // log2 of P at the reference
-constexpr float kRise = 7.f;            // log2 of what a score may exceed it by: P stays below 2^15
+// log2 of what a score may exceed it by: P stays below 2^15 (64 ragged requests 51.0 us; 52.4
+// with a reference that follows every rise)
+constexpr float kRise = 7.f;
 
 // CL: a tile's keys in one cluster, eight warps a block.
 template <int HD, int NT, bool F32, bool CL> struct Cfg {

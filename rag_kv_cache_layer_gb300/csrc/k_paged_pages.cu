@@ -19,6 +19,12 @@
 //
 // A generated token reads two bounds for a page in place of its keys: the scores are
 // a stream over the bounds.
+//
+// Measured, bf16, 32/8 heads of 128, the three launches after one another: 64 requests of up
+// to 65,536 keys in pages of 32 48 us (158 MB of bounds), two of 131,072 keys in pages of 16
+// 31 us (66 MB).  Of the first about 33 are the scores (4.8 TB/s, with 6 us of launch, line
+// and first loads in them), 7 the choice, a block of dependent steps for each row and
+// head, and 4.5 the bounds.
 #include "cb_common.cuh"
 #include "cb_internal.h"
 #include <type_traits>
@@ -158,7 +164,8 @@ struct SelectParams {
   bool scored;                          // the launch before the choice is the scores'
 };
 
-constexpr int kSThreads = 256, kSPages = 64;   // pages of a block
+constexpr int kSThreads = 256;
+constexpr int kSPages = 64;             // fp32: pages of a block
 
 // The pages of a row: 0 at a negative position, -1 where the row has no sequence or its
 // length is wrong (recorded).
@@ -171,6 +178,7 @@ __device__ __forceinline__ int pages_of(const SelectParams &P, const RowPlace &a
   return at.pos < 0 ? 0 : at.pos / P.kv.page_size + 1;
 }
 
+// fp32: a warp a page.
 template <typename T, int HD>
 __global__ void __launch_bounds__(kSThreads)
 paged_score_kernel(const __grid_constant__ SelectParams P, int *status) {
@@ -221,7 +229,7 @@ paged_score_kernel(const __grid_constant__ SelectParams P, int *status) {
 // pages form one line that the grid shares in equal parts (long and short requests in
 // one batch keep every SM busy); neighbouring warps take neighbouring heads of the same
 // pages, whose bounds lie side by side.
-constexpr int kTStages = 3;              // of each warp: 192 KB of bounds in a block
+constexpr int kTStages = 3;              // of each warp: 192 KB of bounds in a block (64 requests 47.7 us; two stages 48.1)
 
 // The line: tiles of a sequence, each of its rows as many as its last one.
 struct ScoreLine {
@@ -492,7 +500,8 @@ __device__ __forceinline__ void add_product(float &hi, float &lo, float x, float
   add_exact(hi, lo, p);
 }
 
-// kCThreads: 256 for up to 2048 pages, all in registers, 1024 for more.
+// kCThreads: 256 for up to 2048 pages, all in registers, 1024 for more (512 rows and heads of
+// up to 2048 pages: 48 us with 256, 64 with 1024; 16 of 8192 pages: 31 with 1024, 49 with 256).
 template <typename T, int HD, int kCThreads>
 __global__ void __launch_bounds__(kCThreads, 1024 / kCThreads)
 paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {

@@ -4,7 +4,10 @@
 // its list's pages one after the other, in blocks of BN.  All items count as many
 // blocks as the longest list can have, and that line of units is cut into equal parts
 // for the grid's blocks (two per SM); an item inside a part is written out, one that
-// crosses parts leaves its pieces for decode_merge_kernel (cb_paged_line.cuh).
+// crosses parts leaves its pieces for decode_merge_kernel (cb_paged_line.cuh).  Few items
+// take a cluster each, blocks of eight warps, and join in its shared memory (one row over
+// 128 pages of 16: 9.1 us, on the line 12.1).  Nothing is loaded behind a list's last page
+// (27 requests with 35 pages of 32 each and room for 128: 34 us, 87 with zeros for the rest).
 //
 // A block first turns its part of the list into pages of the pool and the number of
 // slots that the row sees in each (two dependent rounds of loads for all of them, not
@@ -12,7 +15,8 @@
 // paged_decode_kernel: four warps with a cp.async ring each take the key blocks in
 // turn and hold the 16 rows' maximum, sum and O in registers.  The products, their
 // roundings and the fp32 steps are those of that kernel.  Bound by the picked pages'
-// bytes.
+// bytes: 64 requests with 64 pages of 32 each, 32/8 heads of 128, take 96 us, 5.6 TB/s of
+// 538 MB in slices of 256 bytes.
 #include <type_traits>
 
 #include "cb_common.cuh"
