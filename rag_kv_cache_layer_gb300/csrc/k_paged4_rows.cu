@@ -40,6 +40,7 @@ struct Rows4Params {
   int k_units, v_units, q_units;        // threads' shares of a row
   int rows_per_block;
   paged::Divisor by_row;                // units of a row
+  int width;                            // threads side by side on a row, a power of two (all but rotated rows)
   float k_mul, v_mul;                   // 2^-exp (append), 2^exp (gather)
   const float2 *rope;                   // nullptr: keys are taken as they are
 };
@@ -68,13 +69,14 @@ template <typename T> __device__ __forceinline__ void store_group(T *p, const fl
   }
 }
 
-// The places of the block's rows: page (-1: none) and position of each.
+// The places of the block's rows.
 struct Places4 {
   int off[CB_MAX_SEQS + 1], len[CB_MAX_SEQS];
-  int pos[kR4Rows], page[kR4Rows], bad;
-  // byte offsets of the row's page in the pool (-1: none) and of its key and value rows, so
-  // that a unit's addresses take no 64-bit products
-  int64_t base[kR4Rows], k[kR4Rows], v[kR4Rows];
+  int pos[kR4Rows], bad;
+  // byte offsets of the row's slot among its page's first codes (-1: no place) and first
+  // scales in the pool, and of its key and value rows, so that a unit's addresses take no
+  // 64-bit products
+  int64_t codes[kR4Rows], scales[kR4Rows], k[kR4Rows], v[kR4Rows];
 };
 template <typename T>
 __device__ __forceinline__ void find_places(const Rows4Params &P, int row0, int rows, bool rotate, Places4 &s,
@@ -100,9 +102,10 @@ __device__ __forceinline__ void find_places(const Rows4Params &P, int row0, int 
         pos = (int)p;
       }
     }
+    const int slot = pos & (P.kv.page_size - 1);
     s.pos[threadIdx.x] = pos;
-    s.page[threadIdx.x] = page;
-    s.base[threadIdx.x] = page < 0 ? -1 : page * P.kv.page_stride;
+    s.codes[threadIdx.x] = page < 0 ? -1 : page * P.kv.page_stride + slot * (P.hd / 2);
+    s.scales[threadIdx.x] = page * P.kv.page_stride + slot * (P.hd / 16);
     s.k[threadIdx.x] = (row0 + (int64_t)threadIdx.x) * P.ld_k * (int)sizeof(T);
     s.v[threadIdx.x] = (row0 + (int64_t)threadIdx.x) * P.ld_v * (int)sizeof(T);
   };
@@ -123,38 +126,64 @@ paged4_append_kernel(const __grid_constant__ Rows4Params P, int *status) {
   uint8_t *pool = reinterpret_cast<uint8_t *>(P.kv.k_pages) + layer * P.cache_stride;
   const uint8_t *kn = reinterpret_cast<const uint8_t *>(reinterpret_cast<const T *>(P.k) + layer * P.k_layer_stride);
   const uint8_t *vn = reinterpret_cast<const uint8_t *>(reinterpret_cast<const T *>(P.v) + layer * P.v_layer_stride);
-  const int per_row = P.k_units + P.v_units + P.q_units;
-  for (int t = threadIdx.x; t < rows * per_row; t += kR4Threads) {
-    const int lr = P.by_row.div(t);
-    int u = t - lr * per_row;
-    const int64_t base = s_at.base[lr];
-    if (base < 0) continue;
-    const int slot = s_at.pos[lr] & (page - 1);
-    uint8_t *at = pool + base;
-    // codes and scale of group e of head h
-    auto put = [&](float (&x)[16], int h, int e, bool v, float mul) {
-      if (mul != 1.f) {
+  // codes and scale of group e of head h of a row
+  auto put = [&](float (&x)[16], int64_t codes_of, int64_t scales_of, int h, int e, bool v, float mul) {
+    if (mul != 1.f) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] *= mul;
-      }
-      uint2 codes;
-      const uint32_t scale = q4::quantise<T>(x, codes);
-      uint8_t *head = at + h * head_bytes;
-      *reinterpret_cast<uint2 *>(head + q4::codes_at(page, HD, v) + slot * (HD / 2) + e * 8) = codes;
-      head[q4::scales_at(page, HD, v) + slot * kGroups + e] = (uint8_t)scale;
-    };
-    if (u < P.v_units) {
-      float x[16];
-      load_group(reinterpret_cast<const T *>(vn + s_at.v[lr]) + u * 16, x);
-      put(x, u / kGroups, u % kGroups, true, P.v_mul);
-      continue;
+      for (int i = 0; i < 16; ++i) x[i] *= mul;
     }
-    u -= P.v_units;
-    if constexpr (!ROT) {
-      float x[16];
-      load_group(reinterpret_cast<const T *>(kn + s_at.k[lr]) + u * 16, x);
-      put(x, u / kGroups, u % kGroups, false, P.k_mul);
-    } else {
+    uint2 codes;
+    const uint32_t scale = q4::quantise<T>(x, codes);
+    *reinterpret_cast<uint2 *>(pool + codes_of + (h * head_bytes + q4::codes_at(page, HD, v) + e * 8)) = codes;
+    pool[scales_of + (h * head_bytes + q4::scales_at(page, HD, v) + e)] = (uint8_t)scale;
+  };
+  if constexpr (!ROT) {
+    // a thread keeps its group and goes down the rows, kAhead of them under way
+    constexpr int kAhead = sizeof(T) == 2 ? 4 : 1, kLoads = sizeof(T);
+    const int per_row = P.v_units + P.k_units, step = kR4Threads / P.width;
+    for (int t = threadIdx.x & (P.width - 1); t < per_row; t += P.width) {
+      const bool v = t < P.v_units;
+      const int u = v ? t : t - P.v_units, h = u / kGroups, e = u % kGroups;
+      const uint8_t *src = (v ? vn : kn) + u * (16 * (int)sizeof(T));
+      const int64_t *row_at = v ? s_at.v : s_at.k;
+      const float mul = v ? P.v_mul : P.k_mul;
+      for (int lr = threadIdx.x / P.width; lr < rows; lr += kAhead * step) {
+        uint4 raw[kAhead][kLoads];
+        int64_t at[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int l = lr + i * step;
+          at[i] = l < rows ? s_at.codes[l] : -1;
+          if (at[i] >= 0) {
+#pragma unroll
+            for (int c = 0; c < kLoads; ++c) raw[i][c] = ldg16(src + row_at[l] + c * 16);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (at[i] < 0) continue;
+          float x[16];
+          const T *y = reinterpret_cast<const T *>(raw[i]);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) x[k] = to_f(y[k]);
+          put(x, at[i], s_at.scales[lr + i * step], h, e, v, mul);
+        }
+      }
+    }
+  } else {
+    const int per_row = P.k_units + P.v_units + P.q_units;
+    for (int t = threadIdx.x; t < rows * per_row; t += kR4Threads) {
+      const int lr = P.by_row.div(t);
+      int u = t - lr * per_row;
+      const int64_t at = s_at.codes[lr];
+      if (at < 0) continue;
+      if (u < P.v_units) {
+        float x[16];
+        load_group(reinterpret_cast<const T *>(vn + s_at.v[lr]) + u * 16, x);
+        put(x, at, s_at.scales[lr], u / kGroups, u % kGroups, true, P.v_mul);
+        continue;
+      }
+      u -= P.v_units;
       const bool is_q = u >= P.k_units;
       if (is_q) u -= P.k_units;
       constexpr int kPairs = kGroups / 2, kHalf = HD / 2;
@@ -180,8 +209,8 @@ paged4_append_kernel(const __grid_constant__ Rows4Params P, int *status) {
         store_group(dst, x1);
         store_group(dst + kHalf, x2);
       } else {
-        put(x1, h, e, false, P.k_mul);
-        put(x2, h, e + kPairs, false, P.k_mul);
+        put(x1, at, s_at.scales[lr], h, e, false, P.k_mul);
+        put(x2, at, s_at.scales[lr], h, e + kPairs, false, P.k_mul);
       }
     }
   }
@@ -204,29 +233,26 @@ paged4_gather_kernel(const __grid_constant__ Rows4Params P, int *status) {
                    : reinterpret_cast<uint8_t *>(reinterpret_cast<T *>(P.k_out) + blockIdx.y * P.k_layer_stride);
   const int64_t *row_at = v ? s_at.v : s_at.k;
   const float mul = v ? P.v_mul : P.k_mul;
-  // a unit is 8 values (4 bytes of codes), so that neighbours write neighbouring 16 bytes;
-  // a thread's kUnits are under way together
-  constexpr int kUnits = 4, kHead = HD / 8;     // units of a thread, of a head
-  const int per_row = P.k_units, step_row = kR4Threads / per_row, step_unit = kR4Threads % per_row;
-  int lr = P.by_row.div(threadIdx.x), u = threadIdx.x - lr * per_row;
-  while (lr < rows) {
+  // a unit is 8 values (4 bytes of codes), so that neighbours write neighbouring 16 bytes; a
+  // thread keeps its unit of a row and goes down the rows, kUnits of them under way
+  constexpr int kUnits = 4, kHead = HD / 8;     // rows of a thread; units of a head
+  const int step = kR4Threads / P.width;
+  for (int u = threadIdx.x & (P.width - 1); u < P.k_units; u += P.width) {
+  const int h = u / kHead, e = u % kHead;
+  const uint8_t *codes_at = codes_of + (h * head_bytes + e * 4), *scales_at = scales_of + (h * head_bytes + e / 2);
+  uint8_t *to_unit = out + u * (8 * (int)sizeof(T));
+  for (int lr = threadIdx.x / P.width; lr < rows; lr += kUnits * step) {
     uint32_t codes[kUnits], scale[kUnits];
     uint8_t *dst[kUnits];
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
-      const int64_t base = lr < rows ? s_at.base[lr] : -1;
+      const int l = lr + k * step;
+      const int64_t at = l < rows ? s_at.codes[l] : -1;
       dst[k] = nullptr;
-      if (base >= 0) {
-        const int h = u / kHead, e = u % kHead, slot = s_at.pos[lr] & (page - 1), at = h * head_bytes;
-        codes[k] = __ldg(reinterpret_cast<const uint32_t *>(codes_of + base + (at + slot * (HD / 2) + e * 4)));
-        scale[k] = __ldg(scales_of + base + (at + slot * (HD / 16) + e / 2));
-        dst[k] = out + row_at[lr] + u * (8 * (int)sizeof(T));
-      }
-      lr += step_row;
-      u += step_unit;
-      if (u >= per_row) {
-        u -= per_row;
-        ++lr;
+      if (at >= 0) {
+        codes[k] = __ldg(reinterpret_cast<const uint32_t *>(codes_at + at));
+        scale[k] = __ldg(scales_at + s_at.scales[l]);
+        dst[k] = to_unit + row_at[l];
       }
     }
 #pragma unroll
@@ -258,6 +284,7 @@ paged4_gather_kernel(const __grid_constant__ Rows4Params P, int *status) {
       }
     }
   }
+  }
 }
 
 PagedKV paged4_plain_kv(const cb_paged4_kv &kv) {
@@ -280,7 +307,10 @@ PagedKV paged4_plain_kv(const cb_paged4_kv &kv) {
 // of 3136 rows: 237 us with 4 and 8 rows, 202 with 16 and 16).
 static dim3 plan_rows(Rows4Params &P, int n_layers) {
   P.rows_per_block = (int)max((int64_t)1, min((int64_t)kR4Rows, (int64_t)P.n_rows * n_layers / (8 * device_sm_count())));
-  P.by_row = paged::Divisor(P.k_units + P.v_units + P.q_units);
+  const int units = P.k_units + P.v_units + P.q_units;
+  P.by_row = paged::Divisor(units);
+  P.width = 1;
+  while (P.width < units && P.width < kR4Threads) P.width *= 2;
   return dim3((P.n_rows + P.rows_per_block - 1) / P.rows_per_block, n_layers);
 }
 
