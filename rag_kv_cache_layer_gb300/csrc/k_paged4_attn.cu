@@ -164,6 +164,7 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
   grid_dep_launch();
   int64_t u0 = 0, u1 = 1;
   int s = 0, rank = 0, ranks = 1;
+  int at_s = -1, row0 = 0, n = 0, kv = 0;       // of sequence at_s: first row, rows, length
   if constexpr (CL) {
     ranks = tcx::cluster_size();
     rank = blockIdx.x % ranks;
@@ -181,7 +182,7 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
   }
   for (int64_t u = u0; u < u1;) {
     // this piece: rows [l0, l0 + rows) of sequence s and kv head g, key blocks [jb, je)
-    int row0, kv, base, g, l0 = 0, rows, jb, je, seen;
+    int base, g, l0 = 0, rows, jb, je, seen;
     bool whole = true, first = true;
     if constexpr (CL) {
       const PagedTile t = s_tile;
@@ -202,9 +203,12 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
       // (as in paged_decode_kernel)
       const Line &line = s_line;
       while (line.blocks[s] == 0 || (s + 1 < P.kv.n_seq && line.begin[s + 1] <= u)) ++s;
-      row0 = __ldg(P.kv.row_offsets + s);
-      const int n = __ldg(P.kv.row_offsets + s + 1) - row0;
-      kv = __ldg(P.kv.kv_lens + s);
+      if (s != at_s) {                          // (most often the next head of the same sequence)
+        at_s = s;
+        row0 = __ldg(P.kv.row_offsets + s);
+        n = __ldg(P.kv.row_offsets + s + 1) - row0;
+        kv = __ldg(P.kv.kv_lens + s);
+      }
       base = kv - n;
       const int all = n * P.G, tiles = (all - 1) / R + 1;
       int64_t local = u - line.begin[s];
@@ -243,6 +247,18 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
         P.joins[blockIdx.x] = Join{row0, l0, rows, g, part_of(line, item_end - 1), first ? 0 : 1};
     }
     const int sure = base + P.by_G.div(l0);                   // every row sees the keys up to this one
+    // q, on its way while the pages are looked up: column gid of tile nt is row nt * 8 + gid;
+    // k-step k takes dimensions HD / 4 * q4 + 4 k .. + 3 of it
+    constexpr int VEC = 16 / sizeof(T);
+    uint4 raw[NT][HD / 4 / VEC];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + gid, qi = P.by_G.div(l0 + r);
+      const T *src = reinterpret_cast<const T *>(P.q) + (int64_t)(row0 + qi) * P.ld_q +
+                     (int64_t)(g * P.G + l0 + r - qi * P.G) * HD + q4 * (HD / 4);
+#pragma unroll
+      for (int i = 0; i < HD / 4 / VEC; ++i) raw[nt][i] = r < rows ? ldg16(src + i * VEC) : make_uint4(0, 0, 0, 0);
+    }
     const int32_t *table = P.kv.block_table + (int64_t)s * P.kv.ld_table;
 
     const uint8_t *const head = pool + (int64_t)g * P.head_bytes;
@@ -336,26 +352,15 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
       commit();
     }
     next_pages = fetch();
-    // q: column gid of tile nt is row nt * 8 + gid; k-step k takes dimensions
-    // HD / 4 * q4 + 4 k .. + 3 of it
     uint32_t qh[NT][KS][2], ql[F32 ? NT : 1][F32 ? KS : 1][2];
     float sl[NT][2];                            // log2 scale of this lane's two score columns
     int pos[NT][2];                             // their positions, -1: no row
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = nt * 8 + gid, qi = P.by_G.div(l0 + r);
-      const T *src = reinterpret_cast<const T *>(P.q) + (int64_t)(row0 + qi) * P.ld_q +
-                     (int64_t)(g * P.G + l0 + r - qi * P.G) * HD + q4 * (HD / 4);
       float x[HD / 4];
-      constexpr int VEC = 16 / sizeof(T);
+      const T *e = reinterpret_cast<const T *>(raw[nt]);
 #pragma unroll
-      for (int i = 0; i < HD / 4; i += VEC) {
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (r < rows) raw = ldg16(src + i);
-        const T *e = reinterpret_cast<const T *>(&raw);
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) x[i + k] = to_f(e[k]);
-      }
+      for (int i = 0; i < HD / 4; ++i) x[i] = to_f(e[i]);
       float top = 0.f;
 #pragma unroll
       for (int i = 0; i < HD / 4; ++i) top = fmaxf(top, fabsf(x[i]));
