@@ -78,6 +78,9 @@ paged_picked_kernel(const __grid_constant__ Params P, int *status) {
   const float sl2 = P.scale_log2;
   if (!CL && threadIdx.x == 0) P.joins[blockIdx.x].rows = 0;
 
+  int at_r = -1, s = 0;                         // row at_r: its sequence (0x7fffffff: none), position
+  int64_t pos = 0;
+  if (threadIdx.x == 0) s_last = 0;
   for (int64_t u = u0; u < u1;) {
     const int64_t item = CL ? blockIdx.x / ranks : u / P.blocks;
     int jb = CL ? 0 : (int)(u - item * P.blocks), je = CL ? P.blocks : (int)min((int64_t)P.blocks, jb + (u1 - u));
@@ -85,34 +88,38 @@ paged_picked_kernel(const __grid_constant__ Params P, int *status) {
     const int tile = (int)(item % P.tiles), g = (int)(item / P.tiles % P.Hkv), r = (int)(item / P.tiles / P.Hkv);
     const int l0 = tile * R, rows = min(R, P.G - l0);
     u = CL ? u1 : u + (je - jb);
-    // the row's sequence and position
-    if (threadIdx.x == 0) {
-      s_seq = 0x7fffffff;
-      s_last = 0;
+    // the row's sequence and position (kept for the row's next head); the part's picks,
+    // while the sequence is found
+    const bool fresh = r != at_r;
+    if (fresh) {
+      if (threadIdx.x == 0) s_seq = 0x7fffffff;
+      __syncthreads();
+      for (int i = threadIdx.x; i < P.kv.n_seq; i += NTH) {
+        const int a = __ldg(P.kv.row_offsets + i), b = __ldg(P.kv.row_offsets + i + 1);
+        if (a < 0 || b < a || b > P.n_rows) report(status, CB_ERR_DEVICE_INDEX);
+        else if (a <= r && r < b) atomicMin(&s_seq, i);
+      }
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < P.kv.n_seq; i += NTH) {
-      const int a = __ldg(P.kv.row_offsets + i), b = __ldg(P.kv.row_offsets + i + 1);
-      if (a < 0 || b < a || b > P.n_rows) report(status, CB_ERR_DEVICE_INDEX);
-      else if (a <= r && r < b) atomicMin(&s_seq, i);
-    }
-    // the part's picks, while the sequence is found
     const int p0 = jb * BN >> shift, p1 = min(P.n_picks, (je * BN + page_size - 1) >> shift);
     const int32_t *list = P.picks + ((int64_t)r * P.Hkv + g) * P.n_picks;
     for (int i = p0 + threadIdx.x; i < p1; i += NTH) s_page[i] = __ldg(list + i);
-    __syncthreads();
-    const int s = s_seq;
+    if (fresh) {
+      __syncthreads();
+      at_r = r;
+      s = s_seq;
+      if (s != 0x7fffffff) {
+        const int kv = __ldg(P.kv.kv_lens + s);
+        pos = (int64_t)kv - __ldg(P.kv.row_offsets + s + 1) + r;
+        if (kv < 0 || kv > (int64_t)P.kv.max_pages * page_size) {
+          report(status, CB_ERR_DEVICE_INDEX);
+          s = 0x7fffffff;
+        }
+      }
+    }
     if (s == 0x7fffffff) {                      // a row of no sequence is left alone
       __syncthreads();
       continue;
     }
-    const int kv = __ldg(P.kv.kv_lens + s);
-    if (kv < 0 || kv > (int64_t)P.kv.max_pages * page_size) {
-      report(status, CB_ERR_DEVICE_INDEX);
-      __syncthreads();
-      continue;
-    }
-    const int64_t pos = (int64_t)kv - __ldg(P.kv.row_offsets + s + 1) + r;
     const int32_t *table = P.kv.block_table + (int64_t)s * P.kv.ld_table;
     int last = 0;
     for (int i = p0 + threadIdx.x; i < p1; i += NTH) {
@@ -312,6 +319,7 @@ paged_picked_kernel(const __grid_constant__ Params P, int *status) {
       if (q4 == 0) s_ml[warp * R + gid + 8 * h] = make_float2(m[h], l[h]);
     }
     __syncthreads();                            // the rings are used up
+    if (threadIdx.x == 0) s_last = 0;           // (for the next piece)
     constexpr int LD = HD + 4;
     static_assert(R * LD * 4 <= NS * C::kStage, "the warps' O fit the rings");
     float *so = reinterpret_cast<float *>(smem);
