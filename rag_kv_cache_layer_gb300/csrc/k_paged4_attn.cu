@@ -633,11 +633,10 @@ struct Plan {
 
 // bf16: sequences of up to few_rows rows (queries x G) go through the few-rows kernel,
 // longer ones through the chunk kernel, which is made for 128 rows; fp32 runs the
-// few-rows kernel alone.  A tile of 32 rows reads its keys once, two of them twice: at
-// head_dim 128, 32 rows 64 x over 4096 keys take 203 us as one tile and 266 by the chunk
-// kernel, 48 rows 365 and 271; at 64, where the chunk kernel's softmax has half the
-// products to hide behind, 16 x 36 or 64 rows over 8192 keys take 87 and 88 against 106
-// and 98 (one sequence over 4096 keys alone 20 against 17.5).
+// few-rows kernel alone.  At head_dim 128, 64 x 32 rows over 4096 keys take 177 us so and 266
+// by the chunk kernel, 48 rows 365 (in tiles of 32) and 271; at 64, where the chunk kernel's
+// softmax has half the products to hide behind, 16 x 36 or 64 rows over 8192 keys take 84
+// and 87 against 106 and 98 (one sequence of 64 rows over 4096 keys 15 against 17.5).
 static int few_rows(int hd) { return hd == 64 ? 64 : 32; }
 
 static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd, cb_dtype dt) {
@@ -645,7 +644,12 @@ static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd, cb_d
   const int64_t all = n_rows * G, per_seq = (all + S - 1) / S;
   const bool few = dt == CB_F32 || all <= few_rows(hd) || n_rows <= S;
   p.few_hi = 0x7fffffff;
-  if (few || S > 1) p.nt = per_seq <= 8 ? 1 : per_seq <= 16 ? 2 : few || per_seq <= few_rows(hd) ? 4 : 1;
+  // Tiles of 32 rows read the keys less often and leave two blocks an SM: bf16, 64 sequences
+  // of 32 rows over 4096 keys 188 us, 177 with tiles of 16; at head_dim 64, 48 rows 169 and
+  // 163, 64 rows 173 and 207.  In fp32 they do not fit the registers (256 rows over 8192 keys
+  // 387 us, 266 with tiles of 16).
+  if (few || S > 1)
+    p.nt = per_seq <= 8 ? 1 : per_seq <= 48 || dt == CB_F32 ? 2 : few || per_seq <= few_rows(hd) ? 4 : 1;
   p.grid = device_sm_count() * (p.nt == 4 || dt == CB_F32 ? 2 : p.nt == 2 ? 3 : 4);
   if (few) {
     // few tiles over few keys: each tile's keys go to one cluster of up to 16 blocks, which
@@ -702,8 +706,9 @@ static cudaError_t run_form(const Params &P, const Plan &p, int *status, cudaStr
 }
 template <typename T, int HD>
 static cudaError_t run_rows(const Params &P, const Plan &p, int *status, cudaStream_t s) {
-  return p.nt == 1 ? run_form<T, HD, 1>(P, p, status, s)
-         : p.nt == 2 ? run_form<T, HD, 2>(P, p, status, s) : run_form<T, HD, 4>(P, p, status, s);
+  if constexpr (std::is_same<T, bf16>::value)
+    if (p.nt == 4) return run_form<T, HD, 4>(P, p, status, s);
+  return p.nt == 1 ? run_form<T, HD, 1>(P, p, status, s) : run_form<T, HD, 2>(P, p, status, s);
 }
 
 }  // namespace paged4

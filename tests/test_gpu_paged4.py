@@ -305,12 +305,13 @@ def plan(n_rows, seqs, max_kv, heads, dt):
 
 @pytest.mark.parametrize("dt", list(HALF))
 @pytest.mark.parametrize("hd", [64, 128])
-@pytest.mark.parametrize("n,tile", [(1, 8), (3, 16), (7, 32)])
+@pytest.mark.parametrize("n,group,tile", [(1, 4, 8), (3, 4, 16), (7, 4, 16), (1, 64, 32)])
 @pytest.mark.parametrize("kv,cluster", [(200, 1), (500, 2), (1000, 4), (2000, 8), (4001, 16)])
-def test_tiles_in_clusters(dt, hd, n, tile, kv, cluster):
+def test_tiles_in_clusters(dt, hd, n, group, tile, kv, cluster):
     """Every cluster size and tile of the one-launch form, by the plan that leads to it; lengths
     that leave some of a cluster's blocks without keys."""
-    heads = (8, 2, hd)
+    heads = (8, 2, hd) if group == 4 else (group, 1, hd)
+    tile = min(tile, 16 if dt == torch.float32 else 32)
     assert plan(n, 1, kv, heads, dt)[:2] == [tile, cluster]
     rng = np.random.default_rng(n + kv)
     attention_case(rng, dt, heads, 16, [(n, kv)], max_kv_len=kv)
@@ -322,14 +323,15 @@ def test_tiles_in_clusters(dt, hd, n, tile, kv, cluster):
 
 
 @pytest.mark.parametrize("dt", list(HALF))
-@pytest.mark.parametrize("n,tile", [(1, 8), (3, 16), (7, 32)])
-def test_tiles_on_the_line(dt, n, tile):
+@pytest.mark.parametrize("n,group,tile", [(1, 4, 8), (3, 4, 16), (7, 4, 16), (1, 64, 32)])
+def test_tiles_on_the_line(dt, n, group, tile):
     """Many tiles, with and without padding behind them, pieces in several parts."""
     rng = np.random.default_rng(n)
     for hd, count, kv in ((64, 160, 300), (128, 160, 200), (64, 3, 9000)):
-        heads, seqs = (8, 2, hd), [(n, int(rng.integers(max(n, kv // 3), kv))) for _ in range(count)]
+        heads, seqs = (2 * group, 2, hd), [(n, int(rng.integers(max(n, kv // 3), kv))) for _ in range(count)]
         bound = 40000 if count == 3 else kv
-        assert plan(n * count, count, bound, heads, dt)[:2] == [tile, 0] or tile == 32 and dt == torch.bfloat16
+        tile = min(tile, 16 if dt == torch.float32 else 32)
+        assert plan(n * count, count, bound, heads, dt)[:2] == [tile, 0]
         attention_case(rng, dt, heads, 16, seqs, max_kv_len=bound)
 
 
