@@ -28,14 +28,15 @@
 // codes of one dimension, put into a byte by a shift and a select first.  S^T comes
 // out as P^T's operand up to a transposition of 8x8 blocks (movmatrix).
 //
-// Measured, 32/8 heads of 128: 64 ragged requests of up to 16,384 keys 51.2 us (4.2 TB/s
-// of 216 MB), two of 131 k keys 61.5 (4.8 TB/s), one row over 3137 keys 8.3 from a graph.
+// Measured, 32/8 heads of 128: 64 ragged requests of up to 16,384 keys 50.5 us (4.3 TB/s
+// of 216 MB), two of 131 k keys 61 (4.9 TB/s), one row over 3137 keys 8.3 from a graph.
 // Bound by instructions, not by the cache's bytes: a block of 32 keys costs a warp about
 // 590, of which 250 go to the ALU pipe at half a warp a cycle (the codes' conversions,
 // the maximum, the masks), 220 to the FMA pipes, 30 to the tensor cores (26% busy); a
 // scheduler issues in 0.60 of its cycles with its four warps and waits mostly for the
-// results of the warp's own instructions.  The 16-bit cache's kernel is bound by bytes
-// (122 us for the same requests).
+// results of the warp's own instructions.  A piece of a tile costs about 6000 cycles beside
+// (places 1000, pages and q 2000, join and output 2000), the cut of the line 4000.  The
+// 16-bit cache's kernel is bound by bytes (122 us for the same requests).
 #include "cb_common.cuh"
 #include "cb_internal.h"
 #include "cb_paged.cuh"

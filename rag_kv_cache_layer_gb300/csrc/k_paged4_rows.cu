@@ -12,15 +12,14 @@
 // Both are streams: rows are read once and written once, 4.5 bits a value on the
 // cache's side.  Appending, a thread has 16 values (a scale's group, or the two groups that a
 // rotation mixes), whose codes are one 8-byte store; eight neighbours make a head's
-// line; reading, a thread has four times 8 values under way (32 layers of 3136 rows
-// stored and read back: 186 us; with one at a time 207).  The rows' places come as in
-// paged_append_kernel: three dependent rounds of loads in a call of any size.
+// line; a thread keeps its group of a row, so that its addresses are made once, and goes down
+// the rows with four of them under way (32 layers of 3136 rows stored and read back 168 us;
+// two under way 172 appending, 183 reading, one 179 appending).  The rows' places come as
+// in paged_append_kernel: three dependent rounds of loads in a call of any size.
 //
-// Measured, 8 heads of 128: those 32 layers are appended in 89 us (5.9 TB/s of 527 MB) and
-// gathered in 92 (5.7 TB/s), bound by the loads' latency at 64% of the warps (append) and
-// by the conversions' pipe beside it (gather: 0.78 instructions a cycle and scheduler);
-// one rotated row each of 96 sequences and its way back take 6.7 us in a graph, launches
-// and the three rounds.
+// Measured, 8 heads of 128: those 32 layers are appended in 82 us (6.4 TB/s of 527 MB) and
+// gathered in 80 (6.6 TB/s), bound by memory; one rotated row each of 96 sequences and its
+// way back take 6.7 us in a graph, launches and the three rounds.
 #include "cb_common.cuh"
 #include "cb_internal.h"
 #include "cb_paged.cuh"
@@ -304,7 +303,7 @@ PagedKV paged4_plain_kv(const cb_paged4_kv &kv) {
 
 // As many rows a block as leave every SM its eight blocks once: a block's three rounds of
 // lookups are paid for a row where rows are few, and for 32 where they are many (32 layers
-// of 3136 rows: 237 us with 4 and 8 rows, 202 with 16 and 16).
+// of 3136 rows: 168 us; with at most 16 rows 173, with 8 196).
 static dim3 plan_rows(Rows4Params &P, int n_layers) {
   P.rows_per_block = (int)max((int64_t)1, min((int64_t)kR4Rows, (int64_t)P.n_rows * n_layers / (8 * device_sm_count())));
   const int units = P.k_units + P.v_units + P.q_units;
