@@ -544,8 +544,10 @@ paged_choose_kernel(const __grid_constant__ SelectParams P, int *status) {
   static_assert(kCThreads <= kBins, "the masks' places reuse the bins");
   if (!P.scored) grid_dep_wait();
   const int g = blockIdx.x % P.Hkv, r = blockIdx.x / P.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const RowPlace at = find_row<kCThreads>(P.kv, P.n_rows, r, &s_row, nullptr);
-  const int pages = pages_of(P, at, nullptr);
+  // (the scores' kernel records what is wrong, where it runs)
+  int *const record = P.scored ? nullptr : status;
+  const RowPlace at = find_row<kCThreads>(P.kv, P.n_rows, r, &s_row, record);
+  const int pages = pages_of(P, at, record);
   int32_t *out = P.picks + ((int64_t)r * P.Hkv + g) * P.n_picks;
   const int want = P.n_picks - P.n_first - P.n_last;        // of the scored pages are picked, fewer than there are
   const T *q = reinterpret_cast<const T *>(P.q) + r * P.ld_q + (int64_t)g * P.G * HD;
