@@ -46,6 +46,7 @@ struct AttnParams {
   Join *joins;                            // one per block of the few-rows kernel
   // 4-bit cache (kv.k_pages: the pool, kv.page_stride in bytes)
   int head_bytes = 0;                     // of one head's block of a page
+  int scale_exp = 0;                      // scale_log2 is to be multiplied by 2^that
   float v_mul = 1.f;                      // 2^v_exp
   int pad = 0;                            // units that a tile counts beyond its blocks
 };

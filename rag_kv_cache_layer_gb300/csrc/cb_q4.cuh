@@ -188,15 +188,18 @@ __device__ __forceinline__ float turned(float x, float a, float y, float b) {
 
 // The power of two that brings a row's largest magnitude to [2^13, 2^14), as an exponent.
 __device__ __forceinline__ int exponent_up(float top) { return top > 0.f ? 13 - ilogbf(top) : 0; }
-// ... and what is left of the softmax's log2 scale: above 0, so that a masked -inf stays
-// one (with a smaller scale every weight is 1 too).
-__device__ __forceinline__ float scale_down(float scale_log2, int up) {
-  const int down = -up;                     // in two factors: 2^down may leave fp32
-  return fmaxf(scale_log2 * ldexpf(1.f, down / 2) * ldexpf(1.f, down - down / 2), 0x1p-126f);
+// ... and what is left of the softmax's log2 scale, scale_log2 2^scale_exp: above 0, so that a
+// masked -inf stays one (with a smaller scale every weight is 1 too), and finite, so that a
+// score of 0 stays one (with a larger scale the largest score has all the weight too: scores
+// differ by 2^-34 at least before it).  The cache's exponent is in scale_exp, since it may
+// take the scale alone out of fp32 where a score is far inside.
+__device__ __forceinline__ float scale_down(float scale_log2, int scale_exp, int up) {
+  const int down = scale_exp - up;          // in two factors: 2^down may leave fp32
+  return fminf(fmaxf(scale_log2 * ldexpf(1.f, down / 2) * ldexpf(1.f, down - down / 2), 0x1p-126f), 0x1.fffffep127f);
 }
 // A bf16 row (8 values each) to fp16 behind its power of two; the softmax's log2 scale of
 // the row.
-template <int N> __device__ __forceinline__ float scaled_row(uint4 (&v)[N], float scale_log2) {
+template <int N> __device__ __forceinline__ float scaled_row(uint4 (&v)[N], float scale_log2, int scale_exp) {
   __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);
   __nv_bfloat162 *e = reinterpret_cast<__nv_bfloat162 *>(v);
 #pragma unroll
@@ -209,7 +212,7 @@ template <int N> __device__ __forceinline__ float scaled_row(uint4 (&v)[N], floa
     const __half2 h = __floats2half2_rn(x.x * f1 * f2, x.y * f1 * f2);
     e[i] = *reinterpret_cast<const __nv_bfloat162 *>(&h);
   }
-  return scale_down(scale_log2, up);
+  return scale_down(scale_log2, scale_exp, up);
 }
 
 }  // namespace q4

@@ -381,7 +381,7 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int rc = nt * 8 + 2 * q4 + e;
-        sl[nt][e] = q4::scale_down(P.scale_log2, __shfl_sync(0xffffffffu, up, 8 * q4 + 4 * e));
+        sl[nt][e] = q4::scale_down(P.scale_log2, P.scale_exp, __shfl_sync(0xffffffffu, up, 8 * q4 + 4 * e));
         pos[nt][e] = rc < rows ? base + P.by_G.div(l0 + rc) : -1;
       }
     }
@@ -748,7 +748,8 @@ cudaError_t launch_paged4_attention(const cb_paged4_kv &kv, const cb_paged_query
   P.hc = 1;
   P.by_G = Divisor(G);
   P.by_quads = Divisor(a.n_kv_heads);
-  P.scale_log2 = a.scale * 1.4426950408889634f * ldexpf(1.f, kv.k_exp);
+  P.scale_log2 = frexpf(a.scale, &P.scale_exp) * 1.4426950408889634f;
+  P.scale_exp += kv.k_exp;
   P.head_bytes = q4::head_bytes(kv.page_size, a.head_dim);
   P.v_mul = ldexpf(1.f, kv.v_exp);
   // the partials of a launch reuse the workspace of the one before it: each waits for its

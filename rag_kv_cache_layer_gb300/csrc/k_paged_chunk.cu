@@ -409,7 +409,7 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
 #pragma unroll
       for (int c = 0; c < HD / 8; ++c)
         v[c] = r < rows ? *reinterpret_cast<const uint4 *>(q + c * 8) : make_uint4(0, 0, 0, 0);
-      if constexpr (Q4) sl2 = q4::scaled_row(v, sl2);
+      if constexpr (Q4) sl2 = q4::scaled_row(v, sl2, P.scale_exp);
 #pragma unroll
       for (int c = 0; c < HD / 8; ++c)
         *reinterpret_cast<uint4 *>(smem + t * C::kQ + (c >> 3) * C::kAtom + (r & 127) * 128 +

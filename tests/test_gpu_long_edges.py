@@ -6,11 +6,16 @@ import pytest
 import torch
 
 import rag_kv_cache_layer_gb300 as R
+from oracle import paged as OP
+from oracle import paged4 as O4
 from rag_kv_cache_layer_gb300 import _lib as L
-from test_gpu_paged import ints
+from test_gpu_paged import Batch, f64, ints, vals
+from test_gpu_paged4 import dev
 
 pytestmark = pytest.mark.gpu
 DTYPES = [torch.float32, torch.bfloat16]
+F = 2.0 ** -24
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
 
 
 @pytest.fixture(autouse=True)
@@ -70,4 +75,72 @@ def test_select_keeps_the_newest_pages_where_scores_are_not_finite(dt, pages):
         got = [j for j in picks.flatten().tolist() if j >= 0]
         assert {0, 1, *range(pages - 3, pages)} <= set(got) and len(set(got)) == len(got), (what, got)
         assert got == sorted(got) and got[-1] == pages - 1
+    assert R.device_status() == 0
+
+
+def check_attention(out, q, k, v, b, heads, scale, dt):
+    """The bound of test_gpu_paged4.py, whose terms are relative to the weighted values B, and the
+    probabilities' absolute one, which counts where a weight close to 1 meets a value of 0: in fp16
+    a small probability is off by up to 2^-25 (half its least step) where the sum is 2^8 at least
+    (few rows) or 2^6 (chunks of bf16), so each of p + 1 weights by 2^-33 or 2^-31."""
+    hq, hkv, hd = heads
+    want = OP.paged_attention(q, k, v, b.table, b.offsets, b.lens, *heads, scale, np.full((b.rows, hq * hd), 9.0))
+    B = OP.paged_attention(q, k, np.abs(v), b.table, b.offsets, b.lens, *heads, scale, np.zeros(want.shape))
+    lim, u = np.zeros(want.shape), HALF[dt]
+    rel, low = (2.0 ** -11, 2.0 ** -31) if dt == torch.bfloat16 else (2.0 ** -22, 2.0 ** -33)
+    for r, s, p in OP.row_positions(b.offsets, b.lens):
+        j = np.arange(p + 1)
+        at = b.table[s][j // b.page], j % b.page
+        K, V = (np.abs(x[at]).reshape(p + 1, hkv, hd) for x in (k, v))
+        for h in range(hq if p >= 0 else 0):
+            c = slice(h * hd, (h + 1) * hd)
+            A = scale * (K[:, h // (hq // hkv)] @ np.abs(q[r, c].astype(np.float64))).max()
+            d = (2 * hd + 2 * hd + 4) * F * A + 8 * F * (A + 1) + 4 * F
+            lim[r, c] = (2 * d + 2 * (p + 1) * F + rel) * B[r, c] + u * np.abs(want[r, c]) + \
+                low * V[:, h // (hq // hkv)].sum(0)
+    err = np.abs(f64(out) - want)
+    assert np.all(err <= lim), (float((err - lim).max()), np.argwhere(err > lim)[:4].tolist())
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("heads", [(8, 2, 64), (8, 2, 128)])
+@pytest.mark.parametrize("seqs", [[(1, 300), (1, 41)], [(3, 200), (1, 0)], [(70, 130)]])     # clusters and chunks
+@pytest.mark.parametrize("q_std,k_std,k_exp,scale", [
+    (2.0 ** -128, 1.0, 40, 2.0 ** 88),          # scale * 2^k_exp above fp32, the scores about 10
+    (2.0 ** -128, 1.0, 64, 2.0 ** 65),
+    (2.0 ** -100, 1.0, -64, 2.0 ** 126),
+    (2.0 ** 124, 600.0, -64, 1.75 * 2.0 ** -75),    # below fp32's normal numbers
+])
+def test_attention_scales_and_exponents_beyond_fp32_together(dt, heads, seqs, q_std, k_std, k_exp, scale):
+    hq, hkv, hd = heads
+    rng = np.random.default_rng(hd + len(seqs))
+    b = Batch(rng, seqs, 16, dt, hkv, hd, extra_cols=1)
+    pool = O4.Pool(np.zeros((b.n_pages, R.cb_paged4_page_bytes(16, hkv, hd)), np.uint8), 16, hkv, hd)
+    for p in range(b.n_pages):
+        for slot in range(16):
+            pool.put("k", p, slot, vals(rng, (b.kvw,), dt, k_std))
+            pool.put("v", p, slot, vals(rng, (b.kvw,), dt))
+    q = vals(rng, (b.rows, hq * hd), dt, q_std)
+    out = torch.full((b.rows, hq * hd), 9.0, dtype=dt, device="cuda")
+    R.cb_paged4_attention(dev(q, dt), *b.dev(), torch.from_numpy(pool.raw).cuda(), 16, hq, hkv, hd, out, scale=scale, k_exp=k_exp)
+    torch.cuda.synchronize()
+    assert R.device_status() == 0
+    check_attention(out, q, pool.values("k") * 2.0 ** k_exp, pool.values("v"), b, heads, scale, dt)
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+def test_attention_over_keys_of_zero_with_any_scale(dt):
+    """Scores of zero, whatever multiplies them: the values' mean."""
+    heads, rng = (8, 2, 64), np.random.default_rng(3)
+    b = Batch(rng, [(1, 300), (2, 41)], 16, dt, 2, 64, extra_cols=1)
+    pool = O4.Pool(np.zeros((b.n_pages, R.cb_paged4_page_bytes(16, 2, 64)), np.uint8), 16, 2, 64)
+    for p in range(b.n_pages):
+        for slot in range(16):
+            pool.put("k", p, slot, np.zeros(128))
+            pool.put("v", p, slot, vals(rng, (128,), dt))
+    for std, k_exp, scale in ((2.0 ** 100, 64, 2.0 ** 126), (2.0 ** -126, -64, 2.0 ** -126), (1.0, 0, 0.0)):
+        q = vals(rng, (b.rows, 512), dt, std)
+        out = torch.full((b.rows, 512), 9.0, dtype=dt, device="cuda")
+        R.cb_paged4_attention(dev(q, dt), *b.dev(), torch.from_numpy(pool.raw).cuda(), 16, *heads, out, scale=scale, k_exp=k_exp)
+        check_attention(out, q, pool.values("k"), pool.values("v"), b, heads, 0.0, dt)
     assert R.device_status() == 0
