@@ -951,7 +951,8 @@ cb_status cb_paged4_gather(const cb_paged4_kv *kv, const cb_paged_rows_out *rows
 /* cb_paged_attention over a 4-bit cache, with its arguments and errors: q and out
  * are of dtype, the keys and values what their codes stand for, without a further
  * rounding.  Codes past kv_lens are never used; scales up to it must not be NaN
- * (cb_paged4_append writes none).  q, and scale * q . K * log2(e), must be finite. */
+ * (cb_paged4_append writes none).  q, and scale * q . K * log2(e), must be finite; scores
+ * of 2^22 and more after that factor keep their order, their distances only roughly. */
 size_t cb_paged4_attention_workspace_size(int n_rows, int n_seq, int max_kv_len,
                                           int n_q_heads, int n_kv_heads, int head_dim,
                                           cb_dtype dtype);

@@ -60,6 +60,11 @@ constexpr float kPShift = 8.f;          // log2 of P at the reference
 // log2 of what a score may exceed it by: P stays below 2^15 (64 ragged requests 51.0 us; 52.4
 // with a reference that follows every rise)
 constexpr float kRise = 7.f;
+// A row whose reference (log2) is larger than this is scaled down to it: fp32 tells such scores
+// apart by 0.5 at best, and x sl + shift would be off by more than P has room for (the same
+// branch that moves the reference looks: the batch above 50.1 us with and without, one row over
+// 3137 keys 8.7 without and 8.85 with).
+constexpr float kBig = 0x1p22f;
 
 // CL: a tile's keys in one cluster, eight warps a block.
 template <int HD, int NT, bool F32, bool CL> struct Cfg {
@@ -153,6 +158,7 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
   __shared__ typename std::conditional<CL, None, Line>::type s_line;
   __shared__ int64_t s_sums[NW];
   __shared__ float2 s_ml[NW * R];               // (m, l) of each warp's rows
+  __shared__ float s_sl[NW * R];                // their log2 scales, where sl is scaled down
   __shared__ PagedTile s_tile;
   // CL: the block's joined rows, read by the cluster's others
   __shared__ __align__(16) float s_part[CL ? R * HD : 4];
@@ -385,13 +391,17 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
         pos[nt][e] = rc < rows ? base + P.by_G.div(l0 + rc) : -1;
       }
     }
-    float o[MT][NT][4], m[NT][2], l[NT][2], shift[NT][2];     // shift: kPShift - m
+    // P = 2^(x sl + shift), x the products: shift = kPShift - m sl of the reference m (before the
+    // first one large, so that any product sets it)
+    float o[MT][NT][4], m[NT][2], l[NT][2], shift[NT][2];
+    bool scaled = false;                        // sl is less for some row (kBig)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         m[nt][e] = -INFINITY;
-        l[nt][e] = shift[nt][e] = 0.f;
+        l[nt][e] = 0.f;
+        shift[nt][e] = 0x1.fffffep127f;
       }
 #pragma unroll
       for (int t = 0; t < MT; ++t)
@@ -472,25 +482,30 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           mx[nt][e] = fmaxf(max3(x[0][nt][e], x[0][nt][2 + e], x[1][nt][e]), x[1][nt][2 + e]);
-      // The reference m stays until a score of some lane exceeds it by more than 2^kRise:
+      // The reference m stays until P of some lane would exceed its own by more than 2^kRise:
       // most blocks need no exchange between lanes (the scale is positive: the largest
       // score is the largest product).
       bool over = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) over |= mx[nt][e] * sl[nt][e] > m[nt][e] + kRise;
+        for (int e = 0; e < 2; ++e) over |= fmaf(mx[nt][e], sl[nt][e], shift[nt][e]) > kPShift + kRise;
       if (__any_sync(0xffffffffu, over)) {
+        bool far = scaled;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], d));
-            const float mn = fmaxf(m[nt][e], mx[nt][e] * sl[nt][e]);
-            const float corr = mn == m[nt][e] ? 1.f : ex2(m[nt][e] - mn);      // also where both are -inf
+            const float mn = fmaxf(m[nt][e], mx[nt][e]);
+            const float corr = mn == m[nt][e] ? 1.f : ex2((m[nt][e] - mn) * sl[nt][e]);    // also where both are -inf
             m[nt][e] = mn;
-            shift[nt][e] = mn == -INFINITY ? 0.f : kPShift - mn;
+            if (mn != -INFINITY) {
+              const float score = mn * sl[nt][e];
+              shift[nt][e] = kPShift - score;
+              far |= fabsf(score) > kBig;
+            }
             l[nt][e] *= corr;
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
@@ -498,6 +513,21 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
               o[t][nt][2 + e] *= corr;
             }
           }
+        if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float &whole = s_sl[warp * R + nt * 8 + 2 * q4 + e];   // (a lane reads what it wrote)
+              if (!scaled) whole = sl[nt][e];
+              sl[nt][e] = whole;
+              if (m[nt][e] != -INFINITY) {
+                if (fabsf(m[nt][e] * whole) > kBig) sl[nt][e] = __fdividef(kBig, fabsf(m[nt][e]));
+                shift[nt][e] = kPShift - m[nt][e] * sl[nt][e];
+              }
+            }
+          scaled = true;
+        }
       }
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
@@ -566,7 +596,8 @@ paged4_few_kernel(const __grid_constant__ Params P, int *status) {
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
-        if (gid == 0) s_ml[warp * R + nt * 8 + 2 * q4 + e] = make_float2(m[nt][e], l[nt][e]);
+        if (gid == 0) s_ml[warp * R + nt * 8 + 2 * q4 + e] =
+              make_float2(m[nt][e] * (scaled ? s_sl[warp * R + nt * 8 + 2 * q4 + e] : sl[nt][e]), l[nt][e]);
       }
     __syncthreads();                            // the rings are used up
     // Every warp leaves its O in rows of HD + 4 floats, then the four states join.

@@ -424,6 +424,7 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const uint32_t tm = tmem + t * kChTmem + lane_off, obase = tm + kChO;
     float m = -INFINITY, l = 0.f;                // reference max (log2 domain), sum
+    float ref = -INFINITY;                       // Q4: the product that m is of
     bool failed = false;
     auto pv_landed = [&](int j) -> bool {
       const bool bad = !mbar_wait_bounded(smem_u32(&pd[j & 1]), (j >> 1) & 1, kWaitLimitNs, status);
@@ -462,15 +463,15 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
         for (int i = 0; i < kChBN; ++i)
           if (i < n_vis) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
       }
-      const float mloc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), mloc = top * sl2;
       // move the reference only for a large rise; the first visible key
       // always sets it (m = -inf before)
-      const bool move = mloc > m + kChRescale;
+      const bool move = Q4 ? (top - ref) * sl2 > kChRescale : mloc > m + kChRescale;
       const bool rescale = move && m != -INFINITY;   // O and l hold earlier blocks
       if (__any_sync(0xffffffffu, rescale) && j > 0) {
         // O must hold P_{j-1} V_{j-1} first; rows that keep m scale by 1
         if (!pv_landed(j - 1)) { failed = true; break; }
-        const float corr = rescale ? fast_exp2(m - mloc) : 1.f;
+        const float corr = rescale ? fast_exp2(Q4 ? (ref - top) * sl2 : m - mloc) : 1.f;
 #pragma unroll 1
         for (int c = 0; c < HD; c += 32) {
           float y[32];
@@ -481,7 +482,10 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
         }
         l *= corr;
       }
-      if (move) m = mloc;
+      if (move) {
+        m = mloc;
+        ref = top;
+      }
       // P_j for keys c..c+31 -> columns c/2 .. c/2+15; the scale-and-shift and
       // the sums run on packed pairs.  The columns held P_{j-2}: S_j was
       // issued after P_{j-2} V_{j-2} and its commit covers what came before,
@@ -494,7 +498,12 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            const unsigned long long a = fma2(pack2(x[c + i], x[c + i + 1]), s2, nm2);
+            const unsigned long long x2 = pack2(x[c + i], x[c + i + 1]);
+            unsigned long long a;
+            if constexpr (Q4 && decltype(masked)::value)
+              a = fma2(add2(x2, pack2(-ref, -ref)), s2, pack2(kCh4Shift, kCh4Shift));
+            else
+              a = fma2(x2, s2, nm2);
             float p0 = fast_exp2(lo2(a));
             float p1 = fast_exp2(hi2(a));
             if (decltype(masked)::value) {
@@ -514,7 +523,9 @@ paged_chunk_kernel(const __grid_constant__ AttnParams P, int *status) {
         }
       };
       // most blocks lie wholly before every row of the warp: no selects there
-      if (__all_sync(0xffffffffu, n_vis >= kChBN)) exps(std::false_type{});
+      // (Q4: nor where m's rounding counts beside fp16's range, 2^-4 of an exponent from 2^20
+      // on; they take the reference off the products first)
+      if (__all_sync(0xffffffffu, n_vis >= kChBN && (!Q4 || fabsf(m) < 0x1p20f))) exps(std::false_type{});
       else exps(std::true_type{});
       wait_st();
       l += (lo2(ls2[0]) + hi2(ls2[0])) + (lo2(ls2[1]) + hi2(ls2[1]));

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import rag_kv_cache_layer_gb300 as R
+from gpu_common import bf16_values
 from oracle import paged as OP
 from oracle import paged4 as O4
 from rag_kv_cache_layer_gb300 import _lib as L
@@ -110,6 +111,7 @@ def check_attention(out, q, k, v, b, heads, scale, dt):
     (2.0 ** -128, 1.0, 64, 2.0 ** 65),
     (2.0 ** -100, 1.0, -64, 2.0 ** 126),
     (2.0 ** 124, 600.0, -64, 1.75 * 2.0 ** -75),    # below fp32's normal numbers
+    (2.0 ** 100, 1.0, 64, 2.0 ** -126),         # scores of 2^38 and more
 ])
 def test_attention_scales_and_exponents_beyond_fp32_together(dt, heads, seqs, q_std, k_std, k_exp, scale):
     hq, hkv, hd = heads
@@ -144,3 +146,91 @@ def test_attention_over_keys_of_zero_with_any_scale(dt):
         R.cb_paged4_attention(dev(q, dt), *b.dev(), torch.from_numpy(pool.raw).cuda(), 16, *heads, out, scale=scale, k_exp=k_exp)
         check_attention(out, q, pool.values("k"), pool.values("v"), b, heads, 0.0, dt)
     assert R.device_status() == 0
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("n,kv", [(1, 4000), (3, 200), (64, 300), (150, 700)])
+@pytest.mark.parametrize("power", [10, 19, 21, 25, 31, 60, 118])
+def test_attention_with_scores_of_any_size(dt, hd, n, kv, power):
+    """Keys along one dimension, so that every score is exact: multiples of 2^power.  The largest
+    has all the weight (2^-1024 and less are left), two keys that share it a half each."""
+    hq, hkv, page = 4, 2, 16
+    rng = np.random.default_rng(power)
+    b = Batch(rng, [(n, kv), (n, kv)], page, dt, hkv, hd)
+    pool = O4.Pool(np.zeros((b.n_pages, R.cb_paged4_page_bytes(page, hkv, hd)), np.uint8), page, hkv, hd)
+    v = vals(rng, (b.n_pages, page, hkv * hd), dt)
+    k = np.zeros(v.shape)
+    k[..., 1::hd] = 6.0                 # (q is 0 there: makes the group's scale 1)
+    k[..., ::hd] = np.array([0.5, 1, 1.5, 2, 3])[rng.integers(0, 5, (b.n_pages, page, 1))]
+    # one or two of the keys that every row sees are the largest
+    top = rng.choice(kv - n + 1, (2, 2))
+    top[1, 1] = top[1, 0]
+    for s in range(2):
+        for j in top[s]:
+            k[b.table[s][j // page], j % page, ::hd] = 6.0
+    for p in range(b.n_pages):
+        for slot in range(page):
+            pool.put("k", p, slot, k[p, slot])
+            pool.put("v", p, slot, v[p, slot])
+    q = np.zeros((b.rows, hq * hd), np.float32)
+    q[:, ::hd] = 1.0
+    assert np.array_equal(pool.values("k"), k)
+    out = torch.full((b.rows, hq * hd), 9.0, dtype=dt, device="cuda")
+    R.cb_paged4_attention(dev(q, dt), *b.dev(), torch.from_numpy(pool.raw).cuda(), page, hq, hkv, hd, out,
+                          scale=2.0 ** (power + 1 - 20), k_exp=20)
+    torch.cuda.synchronize()
+    V = pool.values("v")
+    for s in range(2):
+        best = [V[b.table[s][j // page], j % page].reshape(hkv, hd) for j in set(top[s].tolist())]
+        want, B = (np.mean(x, 0)[None, :, None] for x in (best, np.abs(best)))
+        got = f64(out)[b.offsets[s]:b.offsets[s + 1]].reshape(n, hkv, hq // hkv, hd)
+        # both probabilities are the same power of two up to the rounding of their exponent, and
+        # round to fp16 (in fp32: to two halves) beside a sum that does not; the sum's reciprocal
+        # and two products, each twice where parts are joined; the result's rounding
+        lim = ((2.0 ** -11 if dt == torch.bfloat16 else 2.0 ** -22) + 8 * F) * B + HALF[dt] * np.abs(want)
+        assert np.all(np.abs(got - want) <= lim)
+    assert R.device_status() == 0
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("n,kv", [(1, 3000), (3, 90), (40, 400)])
+@pytest.mark.parametrize("first", [True, False])
+def test_attention_past_keys_of_very_low_scores(dt, hd, n, kv, first):
+    """Two thirds of the keys, in front of the others or behind them, have scores of -2^24 and less:
+    their weights are zero, and the others' are as without them.  (A key's sums are exact up to
+    roundings of its own terms, so A is the other keys'.)"""
+    hq, hkv, page = 4, 2, 16
+    rng = np.random.default_rng(n)
+    b = Batch(rng, [(n, kv)], page, dt, hkv, hd)
+    low = np.zeros((b.n_pages, page), bool)
+    j = np.arange(2 * kv // 3) if first else np.arange(kv // 3 - n, kv - n)
+    j = j[j < kv - n]
+    low[b.table[0][j // page], j % page] = True
+    k = vals(rng, (b.n_pages, page, hkv * hd), dt, 2.0 ** -8)
+    k[low] = -2688.0
+    v = vals(rng, k.shape, dt)
+    pool = O4.Pool(np.zeros((b.n_pages, R.cb_paged4_page_bytes(page, hkv, hd)), np.uint8), page, hkv, hd)
+    for p in range(b.n_pages):
+        for slot in range(page):
+            pool.put("k", p, slot, k[p, slot])
+            pool.put("v", p, slot, v[p, slot])
+    q = np.abs(vals(rng, (b.rows, hq * hd), dt)) + np.float32(0.5)
+    if dt == torch.bfloat16:
+        q = bf16_values(q)
+    out = torch.full((b.rows, hq * hd), 9.0, dtype=dt, device="cuda")
+    R.cb_paged4_attention(dev(q, dt), *b.dev(), torch.from_numpy(pool.raw).cuda(), page, hq, hkv, hd, out, scale=128.0)
+    torch.cuda.synchronize()
+    assert R.device_status() == 0
+    K, V = pool.values("k"), pool.values("v")
+    args = (b.table, b.offsets, b.lens, hq, hkv, hd, 128.0)
+    want = OP.paged_attention(q, K, V, *args, np.zeros((b.rows, hq * hd)))
+    assert 128.0 * 2688 * np.abs(q.reshape(-1, hd)).sum(1).min() > 2.0 ** 24
+    # the largest |score's terms| of the others, and weights and values as in check_attention
+    A = 128.0 * np.abs(q.astype(np.float64)).reshape(-1, hd).sum(1).max() * np.abs(K[~low]).max()
+    d = (4 * hd + 4) * F * A + 8 * F * (A + 1) + 4 * F
+    rel, few = (2.0 ** -11, 2.0 ** -31) if dt == torch.bfloat16 else (2.0 ** -22, 2.0 ** -33)
+    B = OP.paged_attention(q, K, np.abs(V), *args, np.zeros(want.shape))
+    lim = (2 * d + 2 * kv * F + rel) * B + HALF[dt] * np.abs(want) + few * kv * np.abs(V).max()
+    assert np.all(np.abs(f64(out) - want) <= lim)
