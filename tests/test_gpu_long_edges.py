@@ -234,3 +234,56 @@ def test_attention_past_keys_of_very_low_scores(dt, hd, n, kv, first):
     B = OP.paged_attention(q, K, np.abs(V), *args, np.zeros(want.shape))
     lim = (2 * d + 2 * kv * F + rel) * B + HALF[dt] * np.abs(want) + few * kv * np.abs(V).max()
     assert np.all(np.abs(f64(out) - want) <= lim)
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("pages,n", [(1500, 600), (2040, 64), (5000, 1000), (20000, 7)])
+@pytest.mark.parametrize("kind", ["zero q", "zero bounds", "same bounds", "three bounds", "outlier page", "near", "outside"])
+def test_select_at_borders_among_many_scores(dt, pages, n, kind):
+    """Hundreds and thousands of pages that fp32 scores do not tell apart from the border: equal
+    ones (the lower pages), a page whose bounds widen every page's margin, scores that differ
+    in their last bits, pages outside the pool."""
+    rng = np.random.default_rng(pages)
+    hq, hkv, hd, page = 6, 2, 64, 8
+    b = Batch(rng, [(1, page * pages), (2, page * pages - 3)], page, dt, hkv, hd)
+    x = vals(rng, (b.n_pages, 2, b.kvw), dt)
+    bounds, q = np.sort(x, axis=1), vals(rng, (b.rows, hq * hd), dt)
+    if kind == "zero q":
+        q[0] = 0
+        q[1] = -0.0
+    elif kind == "zero bounds":
+        bounds[:] = 0
+        bounds[::3] = -0.0
+    elif kind == "same bounds":
+        bounds[:] = bounds[:1]
+    elif kind == "three bounds":
+        bounds[:] = bounds[rng.integers(0, 3, len(bounds))]
+    elif kind == "outlier page":
+        bounds[b.table[0][pages // 2]] *= np.float32(2.0 ** 12)
+        bounds[b.table[1][pages // 3]] *= np.float32(2.0 ** 12)
+    elif kind == "near":
+        bounds[:] = 1
+        bounds[:, :, ::hd] = 2.0 ** 20
+        bounds[:, :, 1::hd] = (rng.integers(0, 200, (b.n_pages, 1, 1)) * 2.0 ** -14).astype(np.float32)
+        q = np.ones_like(q)
+    table = b.table.copy()
+    if kind == "outside":           # more than the picks: the lowest of them beside all that are inside
+        table[:, :pages] = np.where(rng.random((2, pages)) < 0.5 * n / pages, table[:, :pages], b.n_pages + 5)
+    picks = torch.full((b.rows, hkv, n), -5, dtype=torch.int32, device="cuda")
+    R.cb_paged_select(dev(q, dt), ints(b.offsets), ints(b.lens), ints(table), dev(bounds, dt), page, hq, hkv, hd, picks,
+                      n_first=1, n_last=2)
+    torch.cuda.synchronize()
+    assert R.device_status() == (L.CB_ERR_DEVICE_INDEX if kind == "outside" else 0)
+    if kind == "outside":
+        gone = np.nextafter(np.float32(-3e38), 0) * np.ones((1, 2, b.kvw))      # the smallest score of any
+        want = np.full(picks.shape, -5)
+        for r, s in ((0, 0), (1, 1), (2, 1)):
+            for g in range(hkv):
+                there = table[s][:pages] < b.n_pages
+                x = O4.page_scores(q[r], np.concatenate([bounds, gone]), np.minimum(table[s], b.n_pages), pages, hq, hkv, hd)[g]
+                x[~there] = -np.inf
+                x[0] = x[-2:] = np.inf
+                want[r, g] = np.sort(np.lexsort((np.arange(pages), -x))[:n])
+    else:
+        want = O4.select(q, bounds, b.table, b.offsets, b.lens, page, hq, hkv, hd, np.full(picks.shape, -5), 1, 2)
+    assert np.array_equal(picks.cpu().numpy(), want)
