@@ -69,7 +69,43 @@ ChunkPlan plan_chunk(int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd);
 cudaError_t launch_chunk(const AttnParams &P, int R, int64_t units, int hd, int *status, cudaStream_t s,
                          bool q4 = false);
 
-// Blocks that find room at once in clusters of c, per_sm of them an SM: a cluster lies in
+// Blocks of a kernel that the current device takes at once in clusters of 1, 2, 4, 8 and 16 (0:
+// no group of its SMs holds one), asked once per device; nullptr without a device.  `prepare`
+// sets the kernel's attributes.
+struct ClusterRoom {
+  PerDeviceOnce once;
+  int blocks[kMaxDevices][5];
+  template <typename Prepare, typename... Params>
+  const int *of(void (*kernel)(Params...), int threads, size_t smem, Prepare &&prepare) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+    const cudaError_t e = once.run([&](int d) {
+      const cudaError_t e = prepare();
+      for (int i = 0; i < 5 && e == cudaSuccess; ++i) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(1 << i);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 1 << i;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+          n = 0;
+          cudaGetLastError();                   // (a size that the device refuses)
+        }
+        blocks[d][i] = n << i;
+      }
+      return e;
+    });
+    return e == cudaSuccess ? blocks[dev] : nullptr;
+  }
+};
+
+// Blocks that a plan counts on at once in clusters of c, per_sm of them an SM: a cluster lies in
 // one group of SMs, and not all groups are multiples of it (as cudaOccupancyMaxActiveClusters
 // counts them on 152 SMs: 144 of 152 for 4; 120, and 288 of 304, for 8; 112 and 224 for 16).
 inline int64_t cluster_room(int sms, int per_sm, int c) {
@@ -82,11 +118,16 @@ inline int64_t cluster_room(int sms, int per_sm, int c) {
 // lengths below the bound leave a cluster idle and the line not.  Measured, one row each of
 // S requests of one length (32/8 heads of 128), line and cluster: 3000 keys, S = 1 11.2 and
 // 8.8 us, S = 4 13.2 and 10.4, S = 16 21.6 and 17.1; 8000 keys, S = 1 15.5 and 11.1.
-inline int plan_cluster(int64_t items, int64_t blocks, int sms, int per_sm, int parts, int most) {
+// room: from ClusterRoom, a device may take fewer clusters than that, or none of a size.
+inline int plan_cluster(int64_t items, int64_t blocks, int sms, int per_sm, int parts, int most, const int *room) {
+  auto fits = [&](int c) {
+    const int i = c == 1 ? 0 : c == 2 ? 1 : c == 4 ? 2 : c == 8 ? 3 : 4;
+    return items * c <= cluster_room(sms, per_sm, c) && (!room || items * c <= room[i]);
+  };
   int c = 1;
   while (c < most && 8 * c < blocks) c <<= 1;
-  while (c > 1 && items * c > cluster_room(sms, per_sm, c)) c >>= 1;
-  if (items * c > cluster_room(sms, per_sm, c)) return 0;
+  while (c > 1 && !fits(c)) c >>= 1;
+  if (!fits(c)) return 0;
   const int64_t rounds = (blocks + 8 * c - 1) / (8 * c), line = (items * blocks + 4 * parts - 1) / (4 * parts);
   return rounds <= line + 1 ? c : 0;
 }

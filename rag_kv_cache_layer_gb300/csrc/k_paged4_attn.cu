@@ -671,6 +671,30 @@ struct Plan {
 // and 87 against 106 and 98 (one sequence of 64 rows over 4096 keys 15 against 17.5).
 static int few_rows(int hd) { return hd == 64 ? 64 : 32; }
 
+// Attributes of a form of the kernel.
+template <typename T, int HD, int NT, bool CL> static cudaError_t set_attributes() {
+  typedef Cfg<HD, NT, std::is_same<T, float>::value, CL> C;
+  const cudaError_t e =
+      cudaFuncSetAttribute(paged4_few_kernel<T, HD, NT, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  return e != cudaSuccess || !CL
+      ? e : cudaFuncSetAttribute(paged4_few_kernel<T, HD, NT, CL>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+}
+
+template <typename T, int HD, int NT> static const int *cluster_room_of() {
+  typedef Cfg<HD, NT, std::is_same<T, float>::value, true> C;
+  static ClusterRoom room;
+  return room.of(paged4_few_kernel<T, HD, NT, true>, C::kThreads, C::kSmem, set_attributes<T, HD, NT, true>);
+}
+static const int *cluster_room_of(int nt, int hd, cb_dtype dt) {
+  if (dt == CB_F32) {
+    if (nt == 1) return hd == 128 ? cluster_room_of<float, 128, 1>() : cluster_room_of<float, 64, 1>();
+    return hd == 128 ? cluster_room_of<float, 128, 2>() : cluster_room_of<float, 64, 2>();
+  }
+  if (nt == 1) return hd == 128 ? cluster_room_of<bf16, 128, 1>() : cluster_room_of<bf16, 64, 1>();
+  if (nt == 2) return hd == 128 ? cluster_room_of<bf16, 128, 2>() : cluster_room_of<bf16, 64, 2>();
+  return hd == 128 ? cluster_room_of<bf16, 128, 4>() : cluster_room_of<bf16, 64, 4>();
+}
+
 static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd, cb_dtype dt) {
   Plan p = {};
   const int64_t all = n_rows * G, per_seq = (all + S - 1) / S;
@@ -689,7 +713,7 @@ static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd, cb_d
     // every sequence at least; clusters of tiles that there are not leave at once)
     const int64_t full = (all + 8 * p.nt - 1) / (8 * p.nt), seqs = S < n_rows ? S : n_rows;
     p.cluster = plan_cluster((full > seqs ? full : seqs) * Hkv, max_kv > 0 ? (max_kv + kBN - 1) / kBN : 1,
-                             device_sm_count(), p.nt == 1 && dt == CB_BF16 ? 2 : 1, p.grid, 16);
+                             device_sm_count(), p.nt == 1 && dt == CB_BF16 ? 2 : 1, p.grid, 16, cluster_room_of(p.nt, hd, dt));
     return p;
   }
   if (S > 1) p.few_hi = p.rows_lo = few_rows(hd);
@@ -711,12 +735,7 @@ template <typename T, int HD, int NT, bool CL>
 static cudaError_t run(const Params &P, const Plan &p, int *status, cudaStream_t s) {
   typedef Cfg<HD, NT, std::is_same<T, float>::value, CL> C;
   static PerDeviceOnce attr;
-  cudaError_t e = attr.run([](int) {
-    const cudaError_t e = cudaFuncSetAttribute(paged4_few_kernel<T, HD, NT, CL>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    return e != cudaSuccess || !CL
-        ? e : cudaFuncSetAttribute(paged4_few_kernel<T, HD, NT, CL>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  });
+  cudaError_t e = attr.run([](int) { return set_attributes<T, HD, NT, CL>(); });
   if (e != cudaSuccess) return e;
   if constexpr (CL) {
     const int64_t blocks = tile_bound(P.n_rows, P.kv.n_seq, P.G, C::kRows) * P.Hkv * p.cluster;

@@ -374,8 +374,17 @@ static size_t partials() { return 2ull * full_grid() * 16; }
 
 // Few items over few keys: each item's keys go to one cluster of up to 8 blocks, which
 // joins in its shared memory.  0: the line.
-static int cluster_of(int64_t items, int64_t blocks) {
-  return plan_cluster(items, blocks, device_sm_count(), 1, full_grid(), 8);
+template <typename T, int HD> static cudaError_t set_attributes() {
+  const cudaError_t e = cudaFuncSetAttribute(paged_picked_kernel<T, HD, false>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, DecCfg<T, HD, 1>::kSmem);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(paged_picked_kernel<T, HD, true>,
+                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * DecCfg<T, HD, 1>::kSmem);
+}
+template <typename T, int HD> static int cluster_of(int64_t items, int64_t blocks) {
+  static ClusterRoom room;
+  return plan_cluster(items, blocks, device_sm_count(), 1, full_grid(), 8,
+                      room.of(paged_picked_kernel<T, HD, true>, Form<true>::kThreads, 2 * DecCfg<T, HD, 1>::kSmem,
+                              set_attributes<T, HD>));
 }
 
 // Key blocks of an item.
@@ -389,18 +398,12 @@ template <typename T, int HD>
 static cudaError_t run(Params &P, int page_size, int *status, cudaStream_t s) {
   typedef DecCfg<T, HD, 1> C;
   static PerDeviceOnce attr;
-  cudaError_t e = attr.run([](int) {
-    cudaError_t e = cudaFuncSetAttribute(paged_picked_kernel<T, HD, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         C::kSmem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(paged_picked_kernel<T, HD, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * C::kSmem);
-    return e;
-  });
+  cudaError_t e = attr.run([](int) { return set_attributes<T, HD>(); });
   if (e != cudaSuccess) return e;
   P.blocks = (int)key_blocks(P.n_picks, page_size, HD, std::is_same<T, float>::value ? CB_F32 : CB_BF16);
   const int64_t items = (int64_t)P.n_rows * P.Hkv * P.tiles;
   P.units = items * P.blocks;
-  if (const int c = cluster_of(items, P.blocks)) {
+  if (const int c = cluster_of<T, HD>(items, P.blocks)) {
     e = launch_clusters(paged_picked_kernel<T, HD, true>, dim3((unsigned)(items * c)), dim3(Form<true>::kThreads), c,
                         2 * C::kSmem, s, P, status);
     return e == cudaSuccess ? launched(1) : e;
@@ -426,7 +429,8 @@ size_t paged_picked_ws_bytes(int n_rows, int, int, int, int, int hd, cb_dtype) {
 
 void paged_picked_plan(int n_rows, int n_picks, int page_size, int Hq, int Hkv, int hd, cb_dtype dt, int64_t out[3]) {
   const int64_t items = (int64_t)n_rows * Hkv * ((Hq / Hkv + 15) / 16), blocks = picked::key_blocks(n_picks, page_size, hd, dt);
-  out[0] = picked::cluster_of(items, blocks);
+  if (dt == CB_BF16) out[0] = hd == 128 ? picked::cluster_of<bf16, 128>(items, blocks) : picked::cluster_of<bf16, 64>(items, blocks);
+  else out[0] = hd == 128 ? picked::cluster_of<float, 128>(items, blocks) : picked::cluster_of<float, 64>(items, blocks);
   out[1] = items;
   out[2] = blocks;
 }

@@ -287,3 +287,41 @@ def test_select_at_borders_among_many_scores(dt, pages, n, kind):
     else:
         want = O4.select(q, bounds, b.table, b.offsets, b.lens, page, hq, hkv, hd, np.full(picks.shape, -5), 1, 2)
     assert np.array_equal(picks.cpu().numpy(), want)
+
+
+FIRST = r"""
+import torch
+import rag_kv_cache_layer_gb300 as R
+ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+dt, hq, hkv, hd, page, kv = torch.bfloat16, 8, 2, 64, 16, 700
+torch.manual_seed(0)
+k, q = (torch.randn(n, w, device="cuda").to(dt) for n, w in ((kv, hkv * hd), (1, hq * hd)))
+off, lens, table = ints([0, 1]), ints([kv]), torch.arange(44, device="cuda").int()[None]
+pool = torch.randint(0, 127, (44, R.cb_paged4_page_bytes(page, hkv, hd)), device="cuda").to(torch.uint8) & 0x77
+kp = torch.randn(44, page, hkv * hd, device="cuda").to(dt)
+picks = torch.arange(40, device="cuda").int().expand(1, hkv, 40).contiguous()
+ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+a, b = torch.zeros_like(q), torch.zeros_like(q)
+
+def step(a, b):
+    R.cb_paged4_attention(q, off, lens, table, pool, page, hq, hkv, hd, a, max_kv_len=kv, ws=ws)
+    R.cb_paged_attention_picked(q, off, lens, table, kp, kp, picks, hq, hkv, hd, b, ws=ws)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step(a, b)
+g.replay()
+c, d = torch.zeros_like(q), torch.zeros_like(q)
+step(c, d)
+torch.cuda.synchronize()
+assert torch.equal(a, c) and torch.equal(b, d) and bool(a.any()) and bool(b.any()) and R.device_status() == 0
+"""
+
+
+def test_the_first_calls_of_a_process_inside_a_capture():
+    """What a call asks the device once may be asked while a graph is recorded."""
+    import subprocess
+    import sys
+    from conftest import ROOT
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
