@@ -13,10 +13,12 @@
 // slots that the row sees in each (two dependent rounds of loads for all of them, not
 // two on every key block's path); from then on the keys stream as in
 // paged_decode_kernel: four warps with a cp.async ring each take the key blocks in
-// turn and hold the 16 rows' maximum, sum and O in registers.  The products, their
-// roundings and the fp32 steps are those of that kernel.  Bound by the picked pages'
-// bytes: 64 requests with 64 pages of 32 each, 32/8 heads of 128, take 95 us, 5.7 TB/s of
-// 538 MB in slices of 256 bytes.
+// turn and hold the 16 rows' maximum, sum and O in registers.  The products and the fp32
+// steps are those of that kernel, but P meets the values as two halves of bf16 (16 bits in
+// place of 8): a group of up to 8 heads leaves the instruction's other 8 rows for the second
+// half, at no cost (one half 95.1 us, two 92.7; in products of their own 100.5, as larger
+// groups have them).  Bound by the picked pages' bytes: 64 requests with 64 pages of 32
+// each, 32/8 heads of 128, take 93 us, 5.8 TB/s of 538 MB in slices of 256 bytes.
 #include <type_traits>
 
 #include "cb_common.cuh"
@@ -49,7 +51,9 @@ template <bool CL> struct Form {
 __device__ __forceinline__ int64_t begin_of(const Params &P, int c) { return P.units * c / P.parts; }
 __device__ __forceinline__ int part_of(const Params &P, int64_t u) { return (int)(((u + 1) * P.parts - 1) / P.units); }
 
-template <typename T, int HD, bool CL>
+// HALF (bf16, groups of up to 8 heads): rows 8 to 15 of the instruction's 16, which have no head,
+// take what P's rounding to bf16 leaves of rows 0 to 7.
+template <typename T, int HD, bool CL, bool HALF>
 __global__ void __launch_bounds__(Form<CL>::kThreads, Form<CL>::kPerSm)
 paged_picked_kernel(const __grid_constant__ Params P, int *status) {
   constexpr int NW = Form<CL>::kWarps, NTH = Form<CL>::kThreads;
@@ -244,14 +248,14 @@ paged_picked_kernel(const __grid_constant__ Params P, int *status) {
         const int key = j * BN + t * 8, pick = key >> shift;
         const int vis = pick < P.n_picks ? s_vis[pick] - (key & (page_size - 1)) : 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[t][k] = q4 * 2 + (k & 1) < vis ? x[t][k] * sl2 : -INFINITY;
+        for (int k = 0; k < (HALF ? 2 : 4); ++k) x[t][k] = q4 * 2 + (k & 1) < vis ? x[t][k] * sl2 : -INFINITY;
         mx = fmaxf(mx, fmaxf(x[t][0], x[t][1]));
-        mx1 = fmaxf(mx1, fmaxf(x[t][2], x[t][3]));
+        if constexpr (!HALF) mx1 = fmaxf(mx1, fmaxf(x[t][2], x[t][3]));
       }
       float mxs[2] = {mx, mx1}, corr[2];
       bool moved = false;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < (HALF ? 1 : 2); ++h) {
         mxs[h] = fmaxf(mxs[h], __shfl_xor_sync(0xffffffffu, mxs[h], 1));
         mxs[h] = fmaxf(mxs[h], __shfl_xor_sync(0xffffffffu, mxs[h], 2));
         const float mn = fmaxf(m[h], mxs[h]);
@@ -264,12 +268,12 @@ paged_picked_kernel(const __grid_constant__ Params P, int *status) {
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o[d][k] *= corr[k >> 1];
+          for (int k = 0; k < 4; ++k) o[d][k] *= corr[HALF ? 0 : k >> 1];
       }
 #pragma unroll
       for (int t = 0; t < BN / 8; ++t)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < (HALF ? 2 : 4); ++k) {
           const float p = x[t][k] == -INFINITY ? 0.f : ex2(x[t][k] - m[k >> 1]);
           x[t][k] = p;
           l[k >> 1] += p;
@@ -297,14 +301,26 @@ paged_picked_kernel(const __grid_constant__ Params P, int *status) {
       } else {
 #pragma unroll
         for (int k2 = 0; k2 < BN / 16; ++k2) {
-          const uint32_t a[4] = {pack_bf16(x[2 * k2][0], x[2 * k2][1]), pack_bf16(x[2 * k2][2], x[2 * k2][3]),
-                                 pack_bf16(x[2 * k2 + 1][0], x[2 * k2 + 1][1]),
-                                 pack_bf16(x[2 * k2 + 1][2], x[2 * k2 + 1][3])};
+          // rows gid and gid + 8 of the keys 0..7, then of 8..15; P as two halves of bf16, so that it
+          // keeps 16 bits
+          uint32_t a[4], rest[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (HALF && (i & 1)) continue;
+            const float p0 = x[2 * k2 + (i >> 1)][2 * (i & 1)], p1 = x[2 * k2 + (i >> 1)][2 * (i & 1) + 1];
+            a[i] = pack_bf16(p0, p1);
+            rest[i] = pack_bf16(p0 - __uint_as_float(a[i] << 16), p1 - __uint_as_float(a[i] & 0xffff0000u));
+            if (HALF) a[i + 1] = rest[i];
+          }
           const uint32_t row = vs + (k2 * 16 + vrow) * C::kRow;
 #pragma unroll
           for (int d2 = 0; d2 < ND / 2; ++d2) {
             uint32_t b[4];
             ldsm_x4_t(row + (((d2 * 2 + vcol) ^ (vrow & 7)) << 4), b);
+            if constexpr (!HALF) {
+              mma16816(o[2 * d2], rest, b[0], b[1]);
+              mma16816(o[2 * d2 + 1], rest, b[2], b[3]);
+            }
             mma16816(o[2 * d2], a, b[0], b[1]);
             mma16816(o[2 * d2 + 1], a, b[2], b[3]);
           }
@@ -326,9 +342,9 @@ paged_picked_kernel(const __grid_constant__ Params P, int *status) {
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < (HALF ? 1 : 2); ++h)
         *reinterpret_cast<float2 *>(so + (warp * R + gid + 8 * h) * LD + d * 8 + q4 * 2) =
-            make_float2(o[d][2 * h], o[d][2 * h + 1]);
+            HALF ? make_float2(o[d][0] + o[d][2], o[d][1] + o[d][3]) : make_float2(o[d][2 * h], o[d][2 * h + 1]);
     __syncthreads();
     const int64_t slot = (2 * (int64_t)blockIdx.x + (first ? 0 : 1)) * R;
     auto write = [&](int x, int c, float4 a, float L) {
@@ -374,17 +390,25 @@ static size_t partials() { return 2ull * full_grid() * 16; }
 
 // Few items over few keys: each item's keys go to one cluster of up to 8 blocks, which
 // joins in its shared memory.  0: the line.
-template <typename T, int HD> static cudaError_t set_attributes() {
-  const cudaError_t e = cudaFuncSetAttribute(paged_picked_kernel<T, HD, false>,
+template <typename T, int HD, bool HALF> static cudaError_t set_attributes() {
+  const cudaError_t e = cudaFuncSetAttribute(paged_picked_kernel<T, HD, false, HALF>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, DecCfg<T, HD, 1>::kSmem);
-  return e != cudaSuccess ? e : cudaFuncSetAttribute(paged_picked_kernel<T, HD, true>,
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(paged_picked_kernel<T, HD, true, HALF>,
                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * DecCfg<T, HD, 1>::kSmem);
 }
-template <typename T, int HD> static int cluster_of(int64_t items, int64_t blocks) {
+template <typename T, int HD, bool HALF> static int cluster_of(int64_t items, int64_t blocks) {
   static ClusterRoom room;
   return plan_cluster(items, blocks, device_sm_count(), 1, full_grid(), 8,
-                      room.of(paged_picked_kernel<T, HD, true>, Form<true>::kThreads, 2 * DecCfg<T, HD, 1>::kSmem,
-                              set_attributes<T, HD>));
+                      room.of(paged_picked_kernel<T, HD, true, HALF>, Form<true>::kThreads, 2 * DecCfg<T, HD, 1>::kSmem,
+                              set_attributes<T, HD, HALF>));
+}
+// f(kernel's type, head_dim, HALF) as values of types, for a call's dtype, head_dim and group.
+template <typename F> static auto with_form(cb_dtype dt, int hd, int G, F &&f) {
+  typedef std::integral_constant<int, 64> D64;
+  typedef std::integral_constant<int, 128> D128;
+  if (dt == CB_F32) return hd == 128 ? f(0.f, D128{}, std::false_type{}) : f(0.f, D64{}, std::false_type{});
+  if (G <= 8) return hd == 128 ? f(bf16{}, D128{}, std::true_type{}) : f(bf16{}, D64{}, std::true_type{});
+  return hd == 128 ? f(bf16{}, D128{}, std::false_type{}) : f(bf16{}, D64{}, std::false_type{});
 }
 
 // Key blocks of an item.
@@ -394,17 +418,17 @@ static int64_t key_blocks(int n_picks, int page_size, int hd, cb_dtype dt) {
   return ((int64_t)n_picks * page_size + bn - 1) / bn;
 }
 
-template <typename T, int HD>
+template <typename T, int HD, bool HALF>
 static cudaError_t run(Params &P, int page_size, int *status, cudaStream_t s) {
   typedef DecCfg<T, HD, 1> C;
   static PerDeviceOnce attr;
-  cudaError_t e = attr.run([](int) { return set_attributes<T, HD>(); });
+  cudaError_t e = attr.run([](int) { return set_attributes<T, HD, HALF>(); });
   if (e != cudaSuccess) return e;
   P.blocks = (int)key_blocks(P.n_picks, page_size, HD, std::is_same<T, float>::value ? CB_F32 : CB_BF16);
   const int64_t items = (int64_t)P.n_rows * P.Hkv * P.tiles;
   P.units = items * P.blocks;
-  if (const int c = cluster_of<T, HD>(items, P.blocks)) {
-    e = launch_clusters(paged_picked_kernel<T, HD, true>, dim3((unsigned)(items * c)), dim3(Form<true>::kThreads), c,
+  if (const int c = cluster_of<T, HD, HALF>(items, P.blocks)) {
+    e = launch_clusters(paged_picked_kernel<T, HD, true, HALF>, dim3((unsigned)(items * c)), dim3(Form<true>::kThreads), c,
                         2 * C::kSmem, s, P, status);
     return e == cudaSuccess ? launched(1) : e;
   }
@@ -412,7 +436,7 @@ static cudaError_t run(Params &P, int page_size, int *status, cudaStream_t s) {
   const int64_t most = (P.units + 3) / 4;
   P.parts = (int)(most < full_grid() ? most : full_grid());
   if (items < P.parts) P.parts -= (int)(P.parts % items);
-  e = launch_pdl(paged_picked_kernel<T, HD, false>, dim3(P.parts), dim3(kDecThreads), C::kSmem, s, P, status);
+  e = launch_pdl(paged_picked_kernel<T, HD, false, HALF>, dim3(P.parts), dim3(kDecThreads), C::kSmem, s, P, status);
   if (e != cudaSuccess) return e;
   e = launch_pdl(decode_merge_kernel<T, HD>, dim3(P.parts, 16 / kJoinRows), dim3(kJoinThreads),
                  P.parts * kJoinRows * sizeof(float2), s, static_cast<const AttnParams &>(P), 16);
@@ -429,8 +453,9 @@ size_t paged_picked_ws_bytes(int n_rows, int, int, int, int, int hd, cb_dtype) {
 
 void paged_picked_plan(int n_rows, int n_picks, int page_size, int Hq, int Hkv, int hd, cb_dtype dt, int64_t out[3]) {
   const int64_t items = (int64_t)n_rows * Hkv * ((Hq / Hkv + 15) / 16), blocks = picked::key_blocks(n_picks, page_size, hd, dt);
-  if (dt == CB_BF16) out[0] = hd == 128 ? picked::cluster_of<bf16, 128>(items, blocks) : picked::cluster_of<bf16, 64>(items, blocks);
-  else out[0] = hd == 128 ? picked::cluster_of<float, 128>(items, blocks) : picked::cluster_of<float, 64>(items, blocks);
+  out[0] = picked::with_form(dt, hd, Hq / Hkv, [&](auto t, auto d, auto half) {
+    return picked::cluster_of<decltype(t), decltype(d)::value, decltype(half)::value>(items, blocks);
+  });
   out[1] = items;
   out[2] = blocks;
 }
@@ -460,9 +485,9 @@ cudaError_t launch_paged_picked(const PagedKV &kv, const cb_paged_query &a, cons
   P.part_o = reinterpret_cast<float *>(a.ws);
   P.part_ml = reinterpret_cast<float2 *>(P.part_o + partials() * a.head_dim);
   P.joins = reinterpret_cast<Join *>(P.part_ml + partials());
-  if (dt == CB_BF16)
-    return a.head_dim == 128 ? run<bf16, 128>(P, kv.page_size, status, s) : run<bf16, 64>(P, kv.page_size, status, s);
-  return a.head_dim == 128 ? run<float, 128>(P, kv.page_size, status, s) : run<float, 64>(P, kv.page_size, status, s);
+  return with_form(dt, a.head_dim, P.G, [&](auto t, auto d, auto half) {
+    return run<decltype(t), decltype(d)::value, decltype(half)::value>(P, kv.page_size, status, s);
+  });
 }
 
 }  // namespace cb

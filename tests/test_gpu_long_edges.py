@@ -12,6 +12,7 @@ from oracle import paged4 as O4
 from rag_kv_cache_layer_gb300 import _lib as L
 from test_gpu_paged import Batch, f64, ints, vals
 from test_gpu_paged4 import dev
+from test_gpu_picked import picked_case
 
 pytestmark = pytest.mark.gpu
 DTYPES = [torch.float32, torch.bfloat16]
@@ -287,6 +288,26 @@ def test_select_at_borders_among_many_scores(dt, pages, n, kind):
     else:
         want = O4.select(q, bounds, b.table, b.offsets, b.lens, page, hq, hkv, hd, np.full(picks.shape, -5), 1, 2)
     assert np.array_equal(picks.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("group", [1, 4, 7, 8, 9, 16, 20, 128])
+@pytest.mark.parametrize("seqs,n", [([(1, 400), (2, 90)], 5), ([(1, 300 + 7 * i) for i in range(40)], 30)])
+def test_picked_probabilities_keep_16_bits(hd, group, seqs, n):
+    """bf16 rows: a probability meets the values as two halves of bf16, off by 2^-8 of 2^-8 of itself;
+    the other terms as in test_gpu_picked.py.  Weights that are much alike: values of both signs
+    nearly cancel, so that the results' own rounding does not hide the weights'."""
+    dt, hkv = torch.bfloat16, 2 if group <= 20 else 1
+    rng = np.random.default_rng(group)
+    heads, scale = (group * hkv, hkv, hd), 0.02
+    b, q, k, v, _, _, picks, out = picked_case(rng, dt, heads, 16, seqs, n, scale=scale, tail=1)
+    args = (picks, b.table, b.offsets, b.lens, *heads, scale)
+    want = O4.picked_attention(q, k, v, *args, np.full(out.shape, 9.0))
+    B = O4.picked_attention(q, k, np.abs(v), *args, np.zeros(out.shape))
+    A = scale * np.abs(q.astype(np.float64)).reshape(b.rows, -1, hd).sum(-1).repeat(hd, -1) * np.abs(k).max()
+    d = 2 * hd * F * A + 8 * F * (A + 1) + 4 * F
+    lim = (2 * d + 2 * n * 16 * F + 2.0 ** -16) * B + 2.0 ** -8 * np.abs(want)
+    assert np.all(np.abs(f64(out) - want) <= lim)
 
 
 FIRST = r"""
