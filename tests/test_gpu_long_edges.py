@@ -12,7 +12,7 @@ from oracle import paged4 as O4
 from rag_kv_cache_layer_gb300 import _lib as L
 from test_gpu_paged import Batch, f64, ints, vals
 from test_gpu_paged4 import dev
-from test_gpu_picked import picked_case
+from test_gpu_picked import picked_case, select_case
 
 pytestmark = pytest.mark.gpu
 DTYPES = [torch.float32, torch.bfloat16]
@@ -288,6 +288,17 @@ def test_select_at_borders_among_many_scores(dt, pages, n, kind):
     else:
         want = O4.select(q, bounds, b.table, b.offsets, b.lens, page, hq, hkv, hd, np.full(picks.shape, -5), 1, 2)
     assert np.array_equal(picks.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("heads,page,seqs,n", [
+    ((8, 2, 64), 8, [(300, 2000), (1, 900), (150, 150)], 20),
+    ((12, 4, 128), 32, [(400, 1500)], 9),
+    ((16, 1, 64), 16, [(700, 700), (33, 5000)], 33),
+])
+def test_select_for_chunks_of_rows(dt, heads, page, seqs, n):
+    """Hundreds of rows of a sequence, which begin before the picks are scarce and end behind."""
+    select_case(np.random.default_rng(n), dt, heads, page, seqs, n, 1, 2, tail=1)
 
 
 @pytest.mark.parametrize("hd", [64, 128])
