@@ -167,23 +167,50 @@ __device__ __forceinline__ uint32_t quantise(float (&x)[kGroup], uint2 &codes) {
   return scale;
 }
 
-// x a - y b (a, b fp32), correctly rounded to T up to 2^-46 of the larger product:
-// products and sum in pairs of floats, and an odd last bit in place of the rest where
-// T has fewer.
+// x a - y b (a, b fp32), correctly rounded to T: products and sum in pairs of floats, and an
+// odd last bit in place of the rest where T has fewer.  The pair's own rounding loses up to
+// 2^-46 of the larger product, which meets no border of bf16's values (8 bits); in fp32 it
+// counts where the pair is close to the middle of two neighbours, as a value of few bits
+// beside a tiny one may bring it: then `near` is set, and turned_near has the result.
 template <typename T>
-__device__ __forceinline__ float turned(float x, float a, float y, float b) {
+__device__ __forceinline__ float turned(float x, float a, float y, float b, bool &near) {
   // (__fmul_rn: a product that a sum took into an fma would not be the rounded one)
   const float h1 = __fmul_rn(x, a), l1 = fmaf(x, a, -h1), h2 = -__fmul_rn(y, b), l2 = fmaf(-y, b, -h2);
   const float s = h1 + h2, t = s - h1;
   const float e = (h1 - (s - t)) + (h2 - t) + (l1 + l2);
   const float hi = s + e, lo = e - (hi - s);
-  if (sizeof(T) == 4) return hi;
   uint32_t bits = __float_as_uint(hi);
+  if (sizeof(T) == 4) {
+    near = fmaf(lo, 1.f + 0x1p-18f, hi) != hi;  // lo is half a step, or nearly
+    return hi;
+  }
   if (lo != 0.f && hi != 0.f) {
     if ((lo < 0.f) != (hi < 0.f)) --bits;
     bits |= 1u;
   }
   return to_f(from_f<bf16>(__uint_as_float(bits)));
+}
+// x + y and what its rounding leaves.
+__device__ __forceinline__ float add_rest(float x, float y, float &rest) {
+  const float s = x + y, t = s - x;
+  rest = (x - (s - t)) + (y - t);
+  return s;
+}
+// x a - y b correctly rounded to fp32: all of the sum's rests, the last one as an odd bit.
+__device__ __forceinline__ float turned_near(float x, float a, float y, float b) {
+  const float h1 = __fmul_rn(x, a), l1 = fmaf(x, a, -h1), h2 = -__fmul_rn(y, b), l2 = fmaf(-y, b, -h2);
+  float d, r1, r2;
+  const float s = add_rest(h1, h2, d), l = add_rest(l1, l2, r1);
+  float e = add_rest(d, l, r2);
+  const float rest = r1 + r2;
+  if (e == 0.f) {
+    e = rest;
+  } else if (rest != 0.f) {
+    uint32_t bits = __float_as_uint(e);
+    if ((rest < 0.f) != (e < 0.f)) --bits;
+    e = __uint_as_float(bits | 1u);
+  }
+  return s + e;
 }
 
 // The power of two that brings a row's largest magnitude to [2^13, 2^14), as an exponent.

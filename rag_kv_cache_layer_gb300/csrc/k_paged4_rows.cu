@@ -193,15 +193,37 @@ paged4_append_kernel(const __grid_constant__ Rows4Params P, int *status) {
       float x1[16], x2[16];
       load_group(src, x1);
       load_group(src + kHalf, x2);
-      const float4 *cs = reinterpret_cast<const float4 *>(P.rope + (int64_t)s_at.pos[lr] * kHalf + e * 16);
+      const float2 *const rope = P.rope + (int64_t)s_at.pos[lr] * kHalf + e * 16;
+      const float4 *cs = reinterpret_cast<const float4 *>(rope);
+      uint32_t near = 0;                        // values that turned_near is to have
+      auto turn = [&](float x, float a, float y, float b, int bit) -> float {
+        bool n = false;
+        const float r = q4::turned<T>(x, a, y, b, n);
+        if (sizeof(T) == 4 && n) near |= 1u << bit;
+        return r;
+      };
 #pragma unroll
       for (int i = 0; i < 16; i += 2) {
         const float4 w = __ldg(cs + i / 2);
         const float a0 = x1[i], b0 = x2[i], a1 = x1[i + 1], b1 = x2[i + 1];
-        x1[i] = q4::turned<T>(a0, w.x, b0, w.y);
-        x2[i] = q4::turned<T>(b0, w.x, -a0, w.y);
-        x1[i + 1] = q4::turned<T>(a1, w.z, b1, w.w);
-        x2[i + 1] = q4::turned<T>(b1, w.z, -a1, w.w);
+        x1[i] = turn(a0, w.x, b0, w.y, i);
+        x2[i] = turn(b0, w.x, -a0, w.y, 16 + i);
+        x1[i + 1] = turn(a1, w.z, b1, w.w, i + 1);
+        x2[i + 1] = turn(b1, w.z, -a1, w.w, 16 + i + 1);
+      }
+      if constexpr (sizeof(T) == 4) {
+        while (near) {                          // (one value in 2^18, of few bits more)
+          const int at_bit = __ffs(near) - 1, i = at_bit & 15;
+          near &= near - 1;
+          const float a = src[i], b = src[kHalf + i];
+          const float2 w = __ldg(rope + i);
+          const float y = at_bit < 16 ? q4::turned_near(a, w.x, b, w.y) : q4::turned_near(b, w.x, -a, w.y);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            x1[k] = k == at_bit ? y : x1[k];
+            x2[k] = k + 16 == at_bit ? y : x2[k];
+          }
+        }
       }
       if (is_q) {
         T *dst = reinterpret_cast<T *>(P.q_out) + r * P.ld_qo + h * HD + e * 16;

@@ -1,6 +1,8 @@
 """Calls of the operators for long contexts that lie beside those of the other files: page
 selections that take every page, errors in each of its kernels, factors at the ends of the
 exponents, borders between many scores."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -357,3 +359,51 @@ def test_the_first_calls_of_a_process_inside_a_capture():
     from conftest import ROOT
     r = subprocess.run([sys.executable, "-c", FIRST], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def nearest(x, dt):
+    """The float of type dt nearest to the fraction x, ties to even."""
+    bits = 24 if dt == torch.float32 else 8
+    if x == 0:
+        return 0.0
+    _, e = np.frexp(float(x))
+    step = Fraction(2) ** (int(e) - bits)
+    n = x / step
+    low = n.numerator // n.denominator
+    up = n - low > Fraction(1, 2) or (n - low == Fraction(1, 2) and low % 2)
+    return float((low + up) * step)
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+def test_rotated_rows_are_rounded_exactly(dt):
+    """Values of few bits beside values far smaller: products and sums in the middle of two
+    neighbours, or beside it by less than float64 shows.  q_out against exact fractions; the keys'
+    codes are those of the same values."""
+    rng = np.random.default_rng(4)
+    hd, heads, rows = 64, 16, 150
+    shape = (rows, heads * hd)
+    few = rng.integers(-48, 49, shape) * 0.125 * np.exp2(rng.integers(-6, 6, shape))
+    tiny = rng.standard_normal(shape) * np.exp2(rng.integers(-50, -10, shape))
+    x = np.where(rng.random(shape) < 0.5, few, tiny).astype(np.float32)
+    if dt == torch.bfloat16:
+        x = bf16_values(x)
+    table = R.cb_rope_table_init(256, hd, 10000.0)
+    cos, sin = np.moveaxis(table.cpu().numpy().reshape(-1, hd // 2, 2), -1, 0)
+    b = Batch(rng, [(rows, rows + 2)], 16, dt, heads, hd)
+    pool = torch.zeros(b.n_pages, R.cb_paged4_page_bytes(16, heads, hd), dtype=torch.uint8, device="cuda")
+    qo = torch.zeros(shape, dtype=dt, device="cuda")
+    R.cb_paged4_append(dev(x, dt), dev(x, dt), *b.dev(), pool, 16, hd, rope_table=table, q=dev(x, dt), q_out=qo)
+    torch.cuda.synchronize()
+    got, want = f64(qo).reshape(rows, heads, 2, -1), np.zeros((rows, heads, 2, hd // 2))
+    for r in range(rows):
+        for h in range(heads):
+            for e in range(hd // 2):
+                u, v = (Fraction(float(x[r, h * hd + i * hd // 2 + e])) for i in (0, 1))
+                c, s = Fraction(float(cos[r + 2, e])), Fraction(float(sin[r + 2, e]))
+                want[r, h, 0, e], want[r, h, 1, e] = nearest(u * c - v * s, dt), nearest(v * c + u * s, dt)
+    assert np.array_equal(got, want)
+    stored = O4.Pool(pool.cpu().numpy(), 16, heads, hd).values("k")
+    for r in range(rows):
+        at = b.table[0][(r + 2) // 16], (r + 2) % 16
+        assert np.array_equal(stored[at], O4.values(*O4.quantise(want[r].reshape(heads, hd))).reshape(-1))
+    assert R.device_status() == 0
