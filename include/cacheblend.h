@@ -1012,7 +1012,9 @@ cb_status cb_paged_bounds(const cb_paged_kv *kv, const cb_page_bounds *bounds,
  * for a row with a negative position.  Rows of no sequence, or of one with wrong
  * offsets or length, keep theirs.
  * kv's k_pages and v_pages are not read (may be NULL).  q, the bounds and the scores
- * (in fp32) must be finite.  The workspace as for cb_paged_attention.
+ * (in fp32) must be finite.  The workspace as for cb_paged_attention; it holds 20 bytes
+ * for every row, kv head and page of max_kv_len.  Time grows with the number of pages
+ * whose scores lie at the border (equal ones, or bounds far larger than the others').
  * Errors: CB_ERR_INVALID_ARG (NULL or misaligned pointers, strides, n_picks outside
  * [1, CB_MAX_PICKS], n_first or n_last negative or their sum above n_picks, head
  * counts not dividing or more than 128 q heads per kv head, head_dim not 64 or

@@ -11,10 +11,12 @@
 // Mathematics.  A code times its scale is exact in fp16 (cb_q4.cuh), so keys and
 // values meet the tensor cores as fp16 without a rounding.  q is put into fp16 after
 // a power of two per row that brings its largest magnitude to [2^13, 2^14): a bf16 q
-// is then exact down to 2^-27 of that magnitude and off by at most 2^-39 of it
+// is then exact down to 2^-27 of that magnitude and off by at most 2^-38 of it
 // below.  P = 2^(x - m + 8), m a reference that the scores x exceed by 7 at most (so that
-// most blocks leave it and O as they are), rounds to fp16 (2^-12 of itself, 2^-33 of the
-// reference's weight at the bottom); both powers of two leave with the softmax scale and
+// most blocks leave it and O as they are), rounds to fp16 (2^-11 of itself, 2^-33 of the
+// reference's weight at the bottom: the results' error is that of their own rounding, 0.0017
+// with P in fp16 and in fp32, and a second half of P would be products on the pipes that bound
+// this kernel); both powers of two leave with the softmax scale and
 // the division by the sum.  fp32 rows take q and P as two fp16 halves (hi, lo with
 // 2^-22 and less dropped) and every step of 16 in a fresh accumulator that is added
 // in fp32, since the tensor core truncates its sums.
@@ -28,15 +30,15 @@
 // codes of one dimension, put into a byte by a shift and a select first.  S^T comes
 // out as P^T's operand up to a transposition of 8x8 blocks (movmatrix).
 //
-// Measured, 32/8 heads of 128: 64 ragged requests of up to 16,384 keys 50.5 us (4.3 TB/s
-// of 216 MB), two of 131 k keys 61 (4.9 TB/s), one row over 3137 keys 8.3 from a graph.
+// Measured, 32/8 heads of 128: 64 ragged requests of up to 16,384 keys 50.1 us (4.3 TB/s
+// of 216 MB), two of 131 k keys 60 (4.9 TB/s), one row over 3137 keys 9.0, from a graph.
 // Bound by instructions, not by the cache's bytes: a block of 32 keys costs a warp about
 // 590, of which 250 go to the ALU pipe at half a warp a cycle (the codes' conversions,
 // the maximum, the masks), 220 to the FMA pipes, 30 to the tensor cores (26% busy); a
 // scheduler issues in 0.60 of its cycles with its four warps and waits mostly for the
 // results of the warp's own instructions.  A piece of a tile costs about 6000 cycles beside
 // (places 1000, pages and q 2000, join and output 2000), the cut of the line 4000.  The
-// 16-bit cache's kernel is bound by bytes (122 us for the same requests).
+// 16-bit cache's kernel is bound by bytes (128 us for the same requests).
 #include "cb_common.cuh"
 #include "cb_internal.h"
 #include "cb_paged.cuh"
@@ -702,7 +704,8 @@ static Plan plan(int64_t n_rows, int S, int max_kv, int G, int Hkv, int hd, cb_d
   p.few_hi = 0x7fffffff;
   // Tiles of 32 rows read the keys less often and leave two blocks an SM: bf16, 64 sequences
   // of 32 rows over 4096 keys 188 us, 177 with tiles of 16; at head_dim 64, 48 rows 169 and
-  // 163, 64 rows 173 and 207.  In fp32 they do not fit the registers (256 rows over 8192 keys
+  // 163, 64 rows 173 and 207 (on the line; in a cluster 64 rows over 4096 keys take 15.4 with
+  // tiles of 32 and 9.9 with 16: the rule does not look).  In fp32 they do not fit the registers (256 rows over 8192 keys
   // 387 us, 266 with tiles of 16).
   if (few || S > 1)
     p.nt = per_seq <= 8 ? 1 : per_seq <= 48 || dt == CB_F32 ? 2 : few || per_seq <= few_rows(hd) ? 4 : 1;

@@ -45,8 +45,10 @@
 //
 // Over a 4-bit cache the producers load codes and scales into registers and store fp16
 // (exact); the rest is the same with fp16 in bf16's place.  Two chunks of 1024 rows over
-// 12,288 and 16,384 keys: 420 to 462 us by the values' spread, 1.12 to 1.23 PFLOP/s, the
-// 16-bit cache 405: the conversion is hidden behind the products.
+// 12,288 and 16,384 keys: 420 to 461 us by the values' spread, 1.12 to 1.23 PFLOP/s, the
+// 16-bit cache 405 to 447; four of 2048 rows over 8192 keys 795 and 763: units of 256 rows hide
+// the conversion but for 4%.  With units of 128 rows, which have one producer warp per operand
+// beside half the products, they do not: 64 rows over 3200 keys 19.3 and 15.9.
 #include <type_traits>
 
 #include "cb_attn_tc.cuh"

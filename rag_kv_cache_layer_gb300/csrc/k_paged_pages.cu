@@ -15,14 +15,15 @@
 // [from, to]; pages above to + 2 eps are in, pages below from - 2 eps are not, and the
 // few between are scored again with exact products in pairs of floats (2^-44 of the
 // terms; an fp64 sum costs twenty times as much here) and ranked (ties: the lower
-// page): the picks are those of the exact scores.
+// page): the picks are those of the exact scores.  How many there are follows the data, since
+// the bound takes the largest |bound| of any page: see kRanked for many.
 //
 // A generated token reads two bounds for a page in place of its keys: the scores are
 // a stream over the bounds.
 //
 // Measured, bf16, 32/8 heads of 128, the three launches after one another: 64 requests of up
-// to 65,536 keys in pages of 32 48 us (158 MB of bounds), two of 131,072 keys in pages of 16
-// 31 us (66 MB).  Of the first about 33 are the scores (4.8 TB/s, with 6 us of launch, line
+// to 65,536 keys in pages of 32 47 us (158 MB of bounds), two of 131,072 keys in pages of 16
+// 31 us (66 MB; 24 where they stay in L2).  Of the first about 33 are the scores (4.8 TB/s, with 6 us of launch, line
 // and first loads in them), 7 the choice, a block of dependent steps for each row and
 // head, and 4.5 the bounds.
 #include "cb_common.cuh"
@@ -195,8 +196,8 @@ template <typename F> __device__ __forceinline__ float reduce8(float (&v)[8], in
 }
 
 // fp32: a warp's eight pages at once, a lane HD / 32 dimensions of them; the selection of 64
-// pages for 64 requests of 30,000 keys in pages of 32, 32/8 heads of 128, takes 136 us (a page
-// and head at a time 219), bf16 56.
+// pages for 64 requests of 30,000 keys in pages of 32, 32/8 heads of 128, takes 136 to 141 us (a
+// page and head at a time 219), bf16 56.
 template <int HD>
 __global__ void __launch_bounds__(kSThreads)
 paged_score_kernel(const __grid_constant__ SelectParams P, int *status) {

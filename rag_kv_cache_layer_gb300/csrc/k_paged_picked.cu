@@ -6,7 +6,7 @@
 // for the grid's blocks (two per SM); an item inside a part is written out, one that
 // crosses parts leaves its pieces for decode_merge_kernel (cb_paged_line.cuh).  Few items
 // take a cluster each, blocks of eight warps, and join in its shared memory (one row over
-// 128 pages of 16: 9.1 us, on the line 12.1).  Nothing is loaded behind a list's last page
+// 128 pages of 16: 9.0 us, on the line 12.1).  Nothing is loaded behind a list's last page
 // (27 requests with 35 pages of 32 each and room for 128: 34 us, 87 with zeros for the rest).
 //
 // A block first turns its part of the list into pages of the pool and the number of
